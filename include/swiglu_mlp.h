@@ -313,6 +313,149 @@ SWG_API int gemm_splitk_noalloc(int transA, int transB, int64_t M, int64_t N,
                                 float beta, void *C, int64_t ldc, int dtype,
                                 int split_k, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Products grouped by expert, with ragged sizes.  (The pages have no
+ * counterpart; the mathematics is the GEMM statement applied to each group.)
+ *
+ * The M rows of A (and C) are sorted by group: group g owns rows
+ * offsets[g] .. offsets[g+1] - 1.  `offsets` is a DEVICE array of G + 1
+ * int32 values, non-decreasing within [0, M]; it is read on the stream, so a
+ * kernel queued earlier may write it, and the host never waits for it.
+ * offsets == NULL with G == 1: one group of all M rows.  Groups may be empty.
+ * Rows outside [offsets[0], offsets[G]) are neither read into a result nor
+ * written.  Offsets that break the rule are clamped to it by the kernels
+ * (nothing is accessed out of bounds), and the device error word becomes
+ * SWG_ERR_INVALID_ARG.  G <= SWG_MAX_GROUPS, else SWG_ERR_UNSUPPORTED.
+ * 16-bit dtypes only (SWG_F16_F32OUT, SWG_BF16, SWG_F16, SWG_BF16_F32OUT);
+ * alignment, size and graph-capture rules are gemm's, for every pointer,
+ * row stride and group stride.
+ */
+#define SWG_MAX_GROUPS 1024
+
+/*
+ * gemm_grouped — C[i,:] = alpha * A[i,:] * op(B_g) + beta * C[i,:] for the
+ * rows i of every group g.  With op = N this is the forward product, with
+ * op = T (the same stored B) the gradient of its input.
+ *   A, lda            M x K.
+ *   B, ldb, strideB   group g at B + g * strideB elements, stored K x N
+ *                     (transB = SWG_OP_N) or N x K (SWG_OP_T).
+ *   C, ldc            M x N; not read when beta == 0.
+ *   K == 0: C = beta * C.
+ */
+SWG_API int gemm_grouped(int transB, int64_t G, int64_t M, int64_t N, int64_t K, float alpha,
+                         const void *A, int64_t lda, const void *B, int64_t ldb,
+                         int64_t strideB, const int32_t *offsets, float beta, void *C,
+                         int64_t ldc, int dtype, void *stream);
+
+/*
+ * gemm_grouped_wgrad — the gradient of each group's weight:
+ * C_g = alpha * A_g^T * D_g + beta * C_g, where A_g and D_g are the group's
+ * rows of A (M x K) and D (M x N).  C_g is K x N at C + g * strideC elements,
+ * row stride ldc.  An empty group gives beta * C_g (0 when beta == 0).
+ */
+SWG_API int gemm_grouped_wgrad(int64_t G, int64_t M, int64_t N, int64_t K, float alpha,
+                               const void *A, int64_t lda, const void *D, int64_t ldd,
+                               const int32_t *offsets, float beta, void *C, int64_t ldc,
+                               int64_t strideC, int dtype, void *stream);
+
+/*
+ * swiglu_grouped — swiglu_mlp with each group's own weight:
+ * Y[i,:] = SiLU(A[i,:] W1_g) (.) (A[i,:] W2_g).
+ *   A        bfloat16, M x K.   W_fused  bfloat16, G x K x 2N (each group's
+ *   weight interleaved as for swiglu_mlp).   Y  bfloat16, M x N.
+ *   All contiguous; K % 8 == 0 and N % 8 == 0, pointers 16-byte aligned.
+ */
+SWG_API int swiglu_grouped(const void *A, const void *W_fused, void *Y, const int32_t *offsets,
+                           int64_t G, int64_t M, int64_t N, int64_t K, void *stream);
+
+/*
+ * swiglu_grouped_grad — the gradient of swiglu_grouped in its pre-activations.
+ * With g = A W1_g, u = A W2_g (computed again; they are never stored) and
+ * s = 1 / (1 + e^-g):
+ *   dH[i][2n]   = dY[i][n] * u * s * (1 + g * (1 - s))      (Gate)
+ *   dH[i][2n+1] = dY[i][n] * g * s                          (Up)
+ * and, when Y is not NULL, Y[i][n] = g * s * u as swiglu_grouped gives it.
+ *   dY, Y    bfloat16, M x N.   dH  bfloat16, M x 2N (interleaved like
+ *   W_fused).  The gradients of A and W_fused follow as
+ *   gemm_grouped(SWG_OP_T) of dH and W_fused, and gemm_grouped_wgrad of A
+ *   and dH.  Other rules as for swiglu_grouped.
+ */
+SWG_API int swiglu_grouped_grad(const void *A, const void *W_fused, const void *dY, void *Y,
+                                void *dH, const int32_t *offsets, int64_t G, int64_t M,
+                                int64_t N, int64_t K, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (no counterpart on the pages).  Values are
+ * E2M1 (1 sign, 2 exponent, 1 fraction bit: 0, .5, 1, 1.5, 2, 3, 4, 6) in
+ * blocks along K that share a scale:
+ *   SWG_MXFP4  blocks of 32; scale 2^e in E8M0 (a byte e + 127), with
+ *              e = floor(log2(max |x|)) - 2, as the OCP microscaling formats
+ *              specification (v1.0) gives its conversion;
+ *   SWG_NVFP4  blocks of 16; scale an unsigned E4M3 value: max |x| / 6
+ *              rounded to nearest even, at least 2^-9, at most 448.
+ * A value x becomes x / scale rounded to the nearest E2M1 value, ties to even
+ * code, magnitudes beyond 6 to 6.  A block that holds a NaN or an infinity
+ * gets the NaN scale (0xFF, 0x7F): it reads back as NaN, and so do the sums
+ * that use it.  A block of zeros gets the smallest scale.
+ *
+ * Storage of an M x K matrix: two codes per byte, column 2j in the low half of
+ * byte j of its row, rows ld BYTES apart (a multiple of 16, at least
+ * 16 * ceil(K / 32)); the codes from column K up to a multiple of 32 are zero.
+ * Scales are kept in tiles of 128 rows x 4 blocks (512 bytes): row r, block b
+ * of a tile at byte 16 * (r % 32) + 4 * (r / 32) + b.  The tiles of 128 rows
+ * across K follow one another, then those of the next 128 rows; each GROUP of
+ * rows begins a new row of tiles, and rows and blocks that do not exist hold 0.
+ * mx4_scale_bytes gives the size that is enough for any offsets.
+ * offsets, G: as above; offsets == NULL: one group (G is then 1).
+ */
+typedef enum { SWG_MXFP4 = 0, SWG_NVFP4 = 1 } swg_mx4;
+typedef enum { SWG_TYPE_F16 = 0, SWG_TYPE_BF16 = 1, SWG_TYPE_F32 = 2 } swg_type;
+
+/* 512 * ceil(K / (4 blocks)) * (floor(M / 128) + G); -1 for bad arguments. */
+SWG_API int64_t mx4_scale_bytes(int format, int64_t G, int64_t M, int64_t K);
+
+/*
+ * mx4_quantize — X (M x K, row stride ldx, of type xtype) times `scale`
+ * (finite, > 0; the product is formed in FP32) to 4 bits: codes to Q, scale
+ * tiles to S.  X, Q, S 16-byte aligned, row strides multiples of 16 bytes.
+ * Its gradient is taken straight through: that of the identity times `scale`.
+ */
+SWG_API int mx4_quantize(int format, int64_t G, int64_t M, int64_t K, const void *X, int64_t ldx,
+                         int xtype, float scale, const int32_t *offsets, void *Q, int64_t ldq,
+                         void *S, void *stream);
+
+/* mx4_dequantize — X = scale * the values of (Q, S), rounded once to xtype. */
+SWG_API int mx4_dequantize(int format, int64_t G, int64_t M, int64_t K, const void *Q,
+                           int64_t ldq, const void *S, float scale, const int32_t *offsets,
+                           void *X, int64_t ldx, int xtype, void *stream);
+
+/*
+ * gemm_mx4 — C[i,:] = alpha * A[i,:] * B_g^T + beta * C[i,:] with A (M x K)
+ * and B_g (N x K each) in 4 bits of the same format, FP32 accumulation, C of
+ * type ctype.  Dense: G = 1, offsets = NULL.
+ *   A, lda, SA       as mx4_quantize writes them with the same offsets.
+ *   B, ldb, strideB  group g's codes at B + g * strideB bytes (a multiple of
+ *                    16), rows ldb bytes apart.
+ *   SB               scale tiles, each group's N rows beginning a new row of
+ *                    tiles (ceil(N / 128) of them per group).
+ *   alpha            also takes the dequantisation scales of both operands.
+ */
+SWG_API int gemm_mx4(int format, int64_t G, int64_t M, int64_t N, int64_t K, float alpha,
+                     const void *A, int64_t lda, const void *SA, const void *B, int64_t ldb,
+                     int64_t strideB, const void *SB, const int32_t *offsets, float beta,
+                     void *C, int64_t ldc, int ctype, void *stream);
+
+/*
+ * swiglu_mx4 — Y[i,:] = SiLU(alpha A[i,:] W1_g) (.) (alpha A[i,:] W2_g) with
+ * 4-bit A and weights: W holds, for each group, 2N rows of K codes, row 2n =
+ * W1 column n (Gate) and row 2n + 1 = W2 column n (Up), as swiglu_mlp_fp8's
+ * W_fused_t.  A's and W's rows are 16 * ceil(K / 32) bytes apart, groups of W
+ * 2N rows apart; Y bfloat16, M x N contiguous, N % 8 == 0.
+ */
+SWG_API int swiglu_mx4(int format, const void *A, const void *SA, const void *W, const void *SW,
+                       void *Y, const int32_t *offsets, int64_t G, int64_t M, int64_t N,
+                       int64_t K, float alpha, void *stream);
+
 /*
  * swg_debug_workspace_guards — diagnostic for tests (no counterpart on the
  * pages).  With the environment variable SWG_TEST_WS_GUARD=1 set before a

@@ -22,10 +22,19 @@ __all__ = [
     "gemm", "gemm_ex", "gemm_splitk_noalloc", "swiglu_mlp", "swiglu_mlp_dual", "swiglu_mlp_forward", "swiglu_interleave", "status_string",
     "get_device_error", "debug_workspace_guards", "launch_count", "shutdown", "gemm_into", "selftest_wait_timeout",
     "swiglu_mlp_into", "interleave_weights", "library_path", "load",
+    "MXFP4", "NVFP4", "TYPE_F16", "TYPE_BF16", "TYPE_F32", "MAX_GROUPS",
+    "gemm_grouped", "gemm_grouped_wgrad", "swiglu_grouped", "swiglu_grouped_grad",
+    "mx4_scale_bytes", "mx4_quantize", "mx4_dequantize", "gemm_mx4", "swiglu_mx4",
+    "gemm_grouped_into", "gemm_grouped_wgrad_into", "swiglu_grouped_into",
+    "swiglu_grouped_grad_into", "mx4_alloc", "mx4_quantize_into", "mx4_dequantize_into",
+    "gemm_mx4_into", "swiglu_mx4_into",
 ]
 
 OP_N, OP_T = 0, 1
 F16_F32OUT, BF16, F16, BF16_F32OUT, E4M3_BF16OUT, E4M3_F32OUT = 0, 1, 2, 3, 4, 5
+MXFP4, NVFP4 = 0, 1
+TYPE_F16, TYPE_BF16, TYPE_F32 = 0, 1, 2
+MAX_GROUPS = 1024
 STATUS = {0: "SWG_OK", 1: "SWG_ERR_INVALID_ARG", 2: "SWG_ERR_MISALIGNED",
           3: "SWG_ERR_UNSUPPORTED", 4: "SWG_ERR_CUDA", 5: "SWG_ERR_NO_MEMORY",
           6: "SWG_ERR_DEVICE_TIMEOUT"}
@@ -99,6 +108,23 @@ def load():
         lib.swg_cuda_error_name.restype = ctypes.c_char_p
         lib.swg_debug_workspace_guards.argtypes = [vp, ctypes.POINTER(i64)]
         lib.swg_debug_workspace_guards.restype = i32
+        lib.gemm_grouped.argtypes = [i32, i64, i64, i64, i64, f32, vp, i64, vp, i64, i64, vp, f32,
+                                     vp, i64, i32, vp]
+        lib.gemm_grouped_wgrad.argtypes = [i64, i64, i64, i64, f32, vp, i64, vp, i64, vp, f32, vp,
+                                           i64, i64, i32, vp]
+        lib.swiglu_grouped.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, vp]
+        lib.swiglu_grouped_grad.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp]
+        lib.mx4_scale_bytes.argtypes = [i32, i64, i64, i64]
+        lib.mx4_scale_bytes.restype = i64
+        lib.mx4_quantize.argtypes = [i32, i64, i64, i64, vp, i64, i32, f32, vp, vp, i64, vp, vp]
+        lib.mx4_dequantize.argtypes = [i32, i64, i64, i64, vp, i64, vp, f32, vp, vp, i64, i32, vp]
+        lib.gemm_mx4.argtypes = [i32, i64, i64, i64, i64, f32, vp, i64, vp, vp, i64, i64, vp, vp,
+                                 f32, vp, i64, i32, vp]
+        lib.swiglu_mx4.argtypes = [i32, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, f32, vp]
+        for name in ("gemm_grouped", "gemm_grouped_wgrad", "swiglu_grouped",
+                     "swiglu_grouped_grad", "mx4_quantize", "mx4_dequantize", "gemm_mx4",
+                     "swiglu_mx4"):
+            getattr(lib, name).restype = i32
         _lib = lib
         return lib
 
@@ -205,6 +231,76 @@ def swiglu_interleave(W1, W2, W_fused, K, N, stream=None):
                                            _stream(stream)), "swiglu_interleave")
 
 
+def gemm_grouped(transB, G, M, N, K, alpha, A, lda, B, ldb, strideB, offsets, beta, C, ldc,
+                 dtype, stream=None):
+    """C = alpha * A op(B_g) + beta * C for the rows of every group (see the C header)."""
+    return _check(load().gemm_grouped(int(transB), int(G), int(M), int(N), int(K), float(alpha),
+                                      _ptr(A), int(lda), _ptr(B), int(ldb), int(strideB),
+                                      _ptr(offsets), float(beta), _ptr(C), int(ldc), int(dtype),
+                                      _stream(stream)), "gemm_grouped")
+
+
+def gemm_grouped_wgrad(G, M, N, K, alpha, A, lda, D, ldd, offsets, beta, C, ldc, strideC, dtype,
+                       stream=None):
+    """C_g = alpha * A_g^T D_g + beta * C_g (see the C header)."""
+    return _check(load().gemm_grouped_wgrad(int(G), int(M), int(N), int(K), float(alpha), _ptr(A),
+                                            int(lda), _ptr(D), int(ldd), _ptr(offsets),
+                                            float(beta), _ptr(C), int(ldc), int(strideC),
+                                            int(dtype), _stream(stream)), "gemm_grouped_wgrad")
+
+
+def swiglu_grouped(A, W_fused, Y, offsets, G, M, N, K, stream=None):
+    """Y = SiLU(A W1_g) (.) (A W2_g) for the rows of every group (see the C header)."""
+    return _check(load().swiglu_grouped(_ptr(A), _ptr(W_fused), _ptr(Y), _ptr(offsets), int(G),
+                                        int(M), int(N), int(K), _stream(stream)),
+                  "swiglu_grouped")
+
+
+def swiglu_grouped_grad(A, W_fused, dY, Y, dH, offsets, G, M, N, K, stream=None):
+    """The gradient of swiglu_grouped in Gate and Up, and Y (see the C header)."""
+    return _check(load().swiglu_grouped_grad(_ptr(A), _ptr(W_fused), _ptr(dY), _ptr(Y), _ptr(dH),
+                                             _ptr(offsets), int(G), int(M), int(N), int(K),
+                                             _stream(stream)), "swiglu_grouped_grad")
+
+
+def mx4_scale_bytes(format, G, M, K) -> int:
+    """Bytes of scale tiles that are enough for any offsets (see the C header)."""
+    n = int(load().mx4_scale_bytes(int(format), int(G), int(M), int(K)))
+    if n < 0:
+        raise SwgError(1, "mx4_scale_bytes")
+    return n
+
+
+def mx4_quantize(format, G, M, K, X, ldx, xtype, scale, offsets, Q, ldq, S, stream=None):
+    """X * scale to 4-bit codes and scale tiles (see the C header)."""
+    return _check(load().mx4_quantize(int(format), int(G), int(M), int(K), _ptr(X), int(ldx),
+                                      int(xtype), float(scale), _ptr(offsets), _ptr(Q), int(ldq),
+                                      _ptr(S), _stream(stream)), "mx4_quantize")
+
+
+def mx4_dequantize(format, G, M, K, Q, ldq, S, scale, offsets, X, ldx, xtype, stream=None):
+    """The values of 4-bit codes and scale tiles, times scale (see the C header)."""
+    return _check(load().mx4_dequantize(int(format), int(G), int(M), int(K), _ptr(Q), int(ldq),
+                                        _ptr(S), float(scale), _ptr(offsets), _ptr(X), int(ldx),
+                                        int(xtype), _stream(stream)), "mx4_dequantize")
+
+
+def gemm_mx4(format, G, M, N, K, alpha, A, lda, SA, B, ldb, strideB, SB, offsets, beta, C, ldc,
+             ctype, stream=None):
+    """C = alpha * A B_g^T + beta * C with 4-bit A and B (see the C header)."""
+    return _check(load().gemm_mx4(int(format), int(G), int(M), int(N), int(K), float(alpha),
+                                  _ptr(A), int(lda), _ptr(SA), _ptr(B), int(ldb), int(strideB),
+                                  _ptr(SB), _ptr(offsets), float(beta), _ptr(C), int(ldc),
+                                  int(ctype), _stream(stream)), "gemm_mx4")
+
+
+def swiglu_mx4(format, A, SA, W, SW, Y, offsets, G, M, N, K, alpha, stream=None):
+    """Y = SiLU(alpha A W1_g) (.) (alpha A W2_g) with 4-bit A and W (see the C header)."""
+    return _check(load().swiglu_mx4(int(format), _ptr(A), _ptr(SA), _ptr(W), _ptr(SW), _ptr(Y),
+                                    _ptr(offsets), int(G), int(M), int(N), int(K), float(alpha),
+                                    _stream(stream)), "swiglu_mx4")
+
+
 def status_string(status: int) -> str:
     return load().swg_status_string(int(status)).decode()
 
@@ -295,3 +391,211 @@ def interleave_weights(W1, W2, stream=None):
     Wf = torch.empty((K, 2 * N), dtype=W1.dtype, device=W1.device)
     swiglu_interleave(W1, W2, Wf, K, N, stream=stream)
     return Wf
+
+
+# ------------------------------------------------- tensor helpers, expert MLP
+
+def _groups(offsets, where):
+    """(device pointer or None, G) of an int32 CUDA offsets tensor, or of none."""
+    if offsets is None:
+        return None, 1
+    import torch
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() \
+            or offsets.numel() < 1:
+        raise SwgError(1, f"{where}: offsets must be a contiguous 1-D int32 tensor of G + 1 values")
+    return offsets, offsets.numel() - 1
+
+
+def _matrices(t, name, where):
+    """(rows, columns, row stride, group stride) of a 3-D [G, rows, columns]
+    tensor, or of a 2-D one (one group)."""
+    if t.dim() not in (2, 3) or t.stride(-1) != 1:
+        raise SwgError(1, f"{where}: {name} must have unit column stride and 2 or 3 dimensions")
+    return t.shape[-2], t.shape[-1], t.stride(-2), t.stride(0) if t.dim() == 3 else 0
+
+
+def _contiguous(where, **tensors):
+    for name, t in tensors.items():
+        if not t.is_contiguous():
+            raise SwgError(1, f"{where}: {name} must be contiguous")
+
+
+def _of_type(where, dtype, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != dtype:
+            raise SwgError(1, f"{where}: {name} must be {dtype}")
+
+
+def _type_code(dtype, where) -> int:
+    import torch
+    table = {torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
+    if dtype not in table:
+        raise SwgError(3, f"{where}: unsupported dtype {dtype}")
+    return table[dtype]
+
+
+def _group_count(where, G, t, name):
+    if (t.shape[0] if t.dim() == 3 else 1) != G:
+        raise SwgError(1, f"{where}: {name} must hold one matrix for each of {G} groups")
+
+
+def gemm_grouped_into(C, A, B, offsets, transB=0, alpha=1.0, beta=0.0, stream=None):
+    """C[M, N] <- alpha * A[M, K] op(B_g) + beta * C for the rows of each group;
+    B is [G, K, N] (transB = 0) or [G, N, K], offsets int32 [G + 1] on the GPU."""
+    w = "gemm_grouped_into"
+    off, G = _groups(offsets, w)
+    _group_count(w, G, B, "B")
+    rows, cols, ldb, stride = _matrices(B, "B", w)
+    N, Kb = (rows, cols) if transB else (cols, rows)
+    M, K = A.shape
+    if Kb != K or tuple(C.shape) != (M, N) or A.dtype != B.dtype:
+        raise SwgError(1, f"{w}: inconsistent shapes or dtypes")
+    gemm_grouped(transB, G, M, N, K, alpha, A, _row_major_ld(A, "A"), B, ldb, stride, off, beta,
+                 C, _row_major_ld(C, "C"), _dtype_code(A.dtype, C.dtype), stream=stream)
+    return C
+
+
+def gemm_grouped_wgrad_into(C, A, D, offsets, alpha=1.0, beta=0.0, stream=None):
+    """C[G, K, N] <- alpha * A_g^T D_g + beta * C_g from A[M, K] and D[M, N]."""
+    w = "gemm_grouped_wgrad_into"
+    off, G = _groups(offsets, w)
+    _group_count(w, G, C, "C")
+    rows, cols, ldc, stride = _matrices(C, "C", w)
+    M, K = A.shape
+    N = D.shape[1]
+    if D.shape[0] != M or (rows, cols) != (K, N) or A.dtype != D.dtype:
+        raise SwgError(1, f"{w}: inconsistent shapes or dtypes")
+    gemm_grouped_wgrad(G, M, N, K, alpha, A, _row_major_ld(A, "A"), D, _row_major_ld(D, "D"), off,
+                       beta, C, ldc, stride, _dtype_code(A.dtype, C.dtype), stream=stream)
+    return C
+
+
+def _swiglu_shapes(w, A, W_fused, G, **outs):
+    import torch
+    _group_count(w, G, W_fused, "W_fused")
+    M, K = A.shape
+    N = W_fused.shape[-1] // 2
+    if W_fused.shape[-2] != K or W_fused.shape[-1] != 2 * N:
+        raise SwgError(1, f"{w}: inconsistent shapes")
+    for name, (t, cols) in outs.items():
+        if tuple(t.shape) != (M, cols * N):
+            raise SwgError(1, f"{w}: inconsistent shapes")
+        _contiguous(w, **{name: t})
+        _of_type(w, torch.bfloat16, **{name: t})
+    _contiguous(w, A=A, W_fused=W_fused)
+    _of_type(w, torch.bfloat16, A=A, W_fused=W_fused)
+    return M, N, K
+
+
+def swiglu_grouped_into(Y, A, W_fused, offsets, stream=None):
+    """Y[M, N] <- SiLU(A W1_g) (.) (A W2_g), W_fused [G, K, 2N] interleaved."""
+    w = "swiglu_grouped_into"
+    off, G = _groups(offsets, w)
+    M, N, K = _swiglu_shapes(w, A, W_fused, G, Y=(Y, 1))
+    swiglu_grouped(A, W_fused, Y, off, G, M, N, K, stream=stream)
+    return Y
+
+
+def swiglu_grouped_grad_into(dH, A, W_fused, dY, offsets, Y=None, stream=None):
+    """dH[M, 2N] <- the gradient of swiglu_grouped in the interleaved Gate and
+    Up, from dY[M, N]; Y, when given, receives swiglu_grouped's result."""
+    w = "swiglu_grouped_grad_into"
+    off, G = _groups(offsets, w)
+    outs = {"dH": (dH, 2), "dY": (dY, 1)}
+    if Y is not None:
+        outs["Y"] = (Y, 1)
+    M, N, K = _swiglu_shapes(w, A, W_fused, G, **outs)
+    swiglu_grouped_grad(A, W_fused, dY, Y, dH, off, G, M, N, K, stream=stream)
+    return dH
+
+
+def mx4_alloc(M, K, format, groups=1, device="cuda"):
+    """(Q, S) for mx4_quantize_into: codes [M, 16 * ceil(K / 32)] and scale tiles."""
+    import torch
+    return (torch.empty((M, -(-K // 32) * 16), dtype=torch.uint8, device=device),
+            torch.empty(mx4_scale_bytes(format, groups, M, K), dtype=torch.uint8, device=device))
+
+
+def _mx4_scales(where, format, G, M, K, **tensors):
+    import torch
+    _contiguous(where, **tensors)
+    _of_type(where, torch.uint8, **tensors)
+    for name, t in tensors.items():
+        if t.numel() < mx4_scale_bytes(format, G, M, K):
+            raise SwgError(1, f"{where}: {name} is smaller than mx4_scale_bytes")
+
+
+def mx4_quantize_into(Q, S, X, format, scale=1.0, offsets=None, stream=None):
+    """Q, S <- X[M, K] * scale in 4 bits (Q uint8 rows of codes, S scale tiles)."""
+    import torch
+    w = "mx4_quantize_into"
+    off, G = _groups(offsets, w)
+    M, K = X.shape
+    _of_type(w, torch.uint8, Q=Q)
+    _mx4_scales(w, format, G, M, K, S=S)
+    if Q.dim() != 2 or Q.shape[0] != M or Q.shape[1] < -(-K // 32) * 16:
+        raise SwgError(1, f"{w}: Q must be M rows of at least 16 * ceil(K / 32) bytes")
+    mx4_quantize(format, G, M, K, X, _row_major_ld(X, "X"), _type_code(X.dtype, w), scale, off, Q,
+                 _row_major_ld(Q, "Q"), S, stream=stream)
+    return Q, S
+
+
+def mx4_dequantize_into(X, Q, S, format, scale=1.0, offsets=None, stream=None):
+    """X[M, K] <- scale * the values of the 4-bit rows (Q, S)."""
+    import torch
+    w = "mx4_dequantize_into"
+    off, G = _groups(offsets, w)
+    M, K = X.shape
+    _of_type(w, torch.uint8, Q=Q)
+    _mx4_scales(w, format, G, M, K, S=S)
+    if Q.dim() != 2 or Q.shape[0] != M or Q.shape[1] < -(-K // 32) * 16:
+        raise SwgError(1, f"{w}: Q must be M rows of at least 16 * ceil(K / 32) bytes")
+    mx4_dequantize(format, G, M, K, Q, _row_major_ld(Q, "Q"), S, scale, off, X,
+                   _row_major_ld(X, "X"), _type_code(X.dtype, w), stream=stream)
+    return X
+
+
+def _mx4_operands(w, format, G, Q, S, W, SW, K):
+    import torch
+    _of_type(w, torch.uint8, Q=Q, W=W)
+    _group_count(w, G, W, "W")
+    N, width, ldb, stride = _matrices(W, "W", w)
+    if Q.dim() != 2 or min(Q.shape[1], width) < -(-K // 32) * 16:
+        raise SwgError(1, f"{w}: rows of codes must have at least 16 * ceil(K / 32) bytes")
+    M = Q.shape[0]
+    _mx4_scales(w, format, G, M, K, S=S)
+    _contiguous(w, SW=SW)
+    _of_type(w, torch.uint8, SW=SW)
+    # one group of N rows fills ceil(N / 128) rows of tiles
+    if SW.numel() < G * mx4_scale_bytes(format, 0, -(-N // 128) * 128, K):
+        raise SwgError(1, f"{w}: SW is smaller than the weights' scale tiles")
+    return M, N, ldb, stride
+
+
+def gemm_mx4_into(C, Q, S, W, SW, K, format, alpha=1.0, beta=0.0, offsets=None, stream=None):
+    """C[M, N] <- alpha * A W_g^T + beta * C with 4-bit A = (Q, S) of K columns
+    and weights (W [N, bytes] or [G, N, bytes], SW)."""
+    w = "gemm_mx4_into"
+    off, G = _groups(offsets, w)
+    M, N, ldb, stride = _mx4_operands(w, format, G, Q, S, W, SW, K)
+    if tuple(C.shape) != (M, N):
+        raise SwgError(1, f"{w}: inconsistent shapes")
+    gemm_mx4(format, G, M, N, K, alpha, Q, _row_major_ld(Q, "Q"), S, W, ldb, stride, SW, off,
+             beta, C, _row_major_ld(C, "C"), _type_code(C.dtype, w), stream=stream)
+    return C
+
+
+def swiglu_mx4_into(Y, Q, S, W, SW, K, format, alpha=1.0, offsets=None, stream=None):
+    """Y[M, N] <- SiLU(alpha A W1_g^T) (.) (alpha A W2_g^T), W [2N, bytes] or
+    [G, 2N, bytes] with Gate in even and Up in odd rows."""
+    import torch
+    w = "swiglu_mx4_into"
+    off, G = _groups(offsets, w)
+    M, N2, _, _ = _mx4_operands(w, format, G, Q, S, W, SW, K)
+    if tuple(Y.shape) != (M, N2 // 2) or N2 % 2 or \
+            Q.shape[1] != W.shape[-1] or Q.shape[1] != -(-K // 32) * 16:
+        raise SwgError(1, f"{w}: inconsistent shapes")
+    _contiguous(w, Y=Y, Q=Q, W=W)
+    _of_type(w, torch.bfloat16, Y=Y)
+    swiglu_mx4(format, Q, S, W, SW, Y, off, G, M, N2 // 2, K, alpha, stream=stream)
+    return Y

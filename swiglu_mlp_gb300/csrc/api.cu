@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "swiglu_mlp.h"
+#include "host.h"
 #include "launch.h"
 
 namespace {
@@ -871,6 +872,69 @@ int grid_for(long long work, int sms)
 }
 
 }  // namespace
+
+// =================================================== helpers of api_experts.cu
+
+namespace swg {
+
+int device_info(DeviceInfo &out)
+{
+    DeviceState *d = nullptr;
+    if (int rc = device_state(d)) return rc;
+    out.sms = d->sms;
+    out.err = d->err;
+    return SWG_OK;
+}
+
+int record_cuda_error() { return cuda_fail(); }
+
+int count_launch(cudaError_t e)
+{
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        t_last_cuda_error = (int)e;
+        return SWG_ERR_CUDA;
+    }
+    g_launches++;
+    return SWG_OK;
+}
+
+int stream_workspace(cudaStream_t s, size_t bytes, float *&out)
+{
+    DeviceState *d = nullptr;
+    if (int rc = device_state(d)) return rc;
+    Workspace *w = nullptr;
+    if (int rc = workspace(d, s, bytes, w)) return rc;
+    out = static_cast<float *>(w->base);
+    return SWG_OK;
+}
+
+bool encode_tiled(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *ptr,
+                  const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
+                  bool swizzle128)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) {
+        t_last_cuda_error = 10000 + (int)CUDA_ERROR_NOT_FOUND;
+        return false;
+    }
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        es[i] = 1u;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    const CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void *>(ptr), d, st, b, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) t_last_cuda_error = 10000 + (int)r;
+    return r == CUDA_SUCCESS;
+}
+
+}  // namespace swg
 
 // =================================================================== C ABI
 

@@ -1,0 +1,322 @@
+// api_experts.cu — the C ABI of the expert-MLP operators: products grouped by
+// expert with ragged sizes, and microscaled 4-bit floating point.  As in
+// api.cu, every argument is validated before any CUDA call.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "swiglu_mlp.h"
+#include "experts_launch.h"
+#include "host.h"
+#include "tc_gemm.cuh"
+
+namespace {
+
+constexpr int64_t kMaxDim = 0x7fffffff;
+
+int64_t ceil_to(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// The 16-bit dtypes of gemm.
+bool io_types(int dtype, swg::GrpKind &in, int &out, int &out_bytes)
+{
+    switch (dtype) {
+    case SWG_F16_F32OUT: in = swg::GRP_F16; out = swg::OUT_F32; out_bytes = 4; return true;
+    case SWG_BF16: in = swg::GRP_BF16; out = swg::OUT_BF16; out_bytes = 2; return true;
+    case SWG_F16: in = swg::GRP_F16; out = swg::OUT_F16; out_bytes = 2; return true;
+    case SWG_BF16_F32OUT: in = swg::GRP_BF16; out = swg::OUT_F32; out_bytes = 4; return true;
+    default: return false;
+    }
+}
+
+bool type_bytes(int type, int &bytes)
+{
+    switch (type) {
+    case SWG_TYPE_F16: case SWG_TYPE_BF16: bytes = 2; return true;
+    case SWG_TYPE_F32: bytes = 4; return true;
+    default: return false;
+    }
+}
+
+// Rules on groups shared by every entry point; *empty: nothing to do.
+int check_groups(const int32_t *offsets, int64_t G)
+{
+    if (G < 0) return SWG_ERR_INVALID_ARG;
+    if (G > SWG_MAX_GROUPS) return SWG_ERR_UNSUPPORTED;
+    if (offsets == nullptr && G > 1) return SWG_ERR_INVALID_ARG;
+    if (offsets != nullptr && (reinterpret_cast<uintptr_t>(offsets) & 3u)) return SWG_ERR_MISALIGNED;
+    return SWG_OK;
+}
+
+bool too_big(std::initializer_list<int64_t> v)
+{
+    for (int64_t x : v)
+        if (x > kMaxDim) return true;
+    return false;
+}
+
+int block_of(int format) { return format == SWG_NVFP4 ? 16 : 32; }
+bool known_format(int format) { return format == SWG_MXFP4 || format == SWG_NVFP4; }
+
+int run_grouped(const swg::GrpArgs &p, swg::GrpKind kind, swg::GrpEpi epi, void *stream)
+{
+    swg::DeviceInfo d;
+    if (int rc = swg::device_info(d)) return rc;
+    return swg::count_launch(
+        swg::launch_grouped(p, kind, epi, d.sms, d.err, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_grouped(int transB, int64_t G, int64_t M, int64_t N, int64_t K, float alpha,
+                 const void *A, int64_t lda, const void *B, int64_t ldb, int64_t strideB,
+                 const int32_t *offsets, float beta, void *C, int64_t ldc, int dtype, void *stream)
+{
+    swg::GrpKind in;
+    int out, out_bytes;
+    if (!io_types(dtype, in, out, out_bytes)) return SWG_ERR_UNSUPPORTED;
+    if (transB != SWG_OP_N && transB != SWG_OP_T) return SWG_ERR_INVALID_ARG;
+    if (M < 0 || N < 0 || K < 0) return SWG_ERR_INVALID_ARG;
+    if (int rc = check_groups(offsets, G)) return rc;
+    if (M == 0 || N == 0 || G == 0) return SWG_OK;
+    const int64_t b_rows = transB ? N : K, b_cols = transB ? K : N;
+    if (C == nullptr || ldc < N) return SWG_ERR_INVALID_ARG;
+    if (K > 0 && (A == nullptr || B == nullptr || lda < K || ldb < b_cols))
+        return SWG_ERR_INVALID_ARG;
+    if (K > 0 && G > 1 && strideB < (b_rows - 1) * ldb + b_cols) return SWG_ERR_INVALID_ARG;
+    if (too_big({M, N, K, lda, ldb, ldc})) return SWG_ERR_UNSUPPORTED;
+    if (!aligned16(C) || (ldc * out_bytes) % 16 != 0) return SWG_ERR_MISALIGNED;
+    if (K > 0 && (!aligned16(A) || !aligned16(B) || lda % 8 != 0 || ldb % 8 != 0 ||
+                  (G > 1 && strideB % 8 != 0)))
+        return SWG_ERR_MISALIGNED;
+    swg::GrpArgs p{};
+    p.groups = {offsets, (int)G, (int)M};
+    p.N = (int)N;
+    p.K = (int)K;
+    p.A = A;
+    p.lda = lda;
+    p.B = B;
+    p.ldb = ldb;
+    p.strideB = G > 1 ? strideB : 0;
+    p.b_kn = transB == SWG_OP_N;
+    p.C = C;
+    p.ldc = ldc;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.out_kind = out;
+    return run_grouped(p, in, swg::GRP_STORE, stream);
+}
+
+int gemm_grouped_wgrad(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, const void *A,
+                       int64_t lda, const void *D, int64_t ldd, const int32_t *offsets, float beta,
+                       void *C, int64_t ldc, int64_t strideC, int dtype, void *stream)
+{
+    swg::GrpKind in;
+    int out, out_bytes;
+    if (!io_types(dtype, in, out, out_bytes)) return SWG_ERR_UNSUPPORTED;
+    if (M < 0 || N < 0 || K < 0) return SWG_ERR_INVALID_ARG;
+    if (int rc = check_groups(offsets, G)) return rc;
+    if (N == 0 || K == 0 || G == 0) return SWG_OK;
+    if (C == nullptr || ldc < N) return SWG_ERR_INVALID_ARG;
+    if (G > 1 && strideC < (K - 1) * ldc + N) return SWG_ERR_INVALID_ARG;
+    if (M > 0 && (A == nullptr || D == nullptr || lda < K || ldd < N)) return SWG_ERR_INVALID_ARG;
+    if (too_big({M, N, K, lda, ldd, ldc})) return SWG_ERR_UNSUPPORTED;
+    if (!aligned16(C) || (ldc * out_bytes) % 16 != 0 || (G > 1 && (strideC * out_bytes) % 16 != 0))
+        return SWG_ERR_MISALIGNED;
+    if (M > 0 && (!aligned16(A) || !aligned16(D) || lda % 8 != 0 || ldd % 8 != 0))
+        return SWG_ERR_MISALIGNED;
+    swg::WgradArgs p{};
+    p.groups = {offsets, (int)G, (int)M};
+    p.N = (int)N;
+    p.K = (int)K;
+    p.A = A;
+    p.lda = lda;
+    p.D = D;
+    p.ldd = ldd;
+    p.C = C;
+    p.ldc = ldc;
+    p.strideC = G > 1 ? strideC : 0;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.in_bf16 = in == swg::GRP_BF16;
+    p.out_kind = out;
+    swg::DeviceInfo d;
+    if (int rc = swg::device_info(d)) return rc;
+    return swg::count_launch(
+        swg::launch_wgrad(p, d.sms, d.err, static_cast<cudaStream_t>(stream)));
+}
+
+static int swiglu_grouped_impl(const void *A, const void *W, const void *dY, void *Y, void *dH,
+                               const int32_t *offsets, int64_t G, int64_t M, int64_t N, int64_t K,
+                               bool grad, void *stream)
+{
+    if (M < 0 || N < 0 || K < 0) return SWG_ERR_INVALID_ARG;
+    if (int rc = check_groups(offsets, G)) return rc;
+    if (M == 0 || N == 0 || G == 0) return SWG_OK;
+    if (grad ? dY == nullptr || dH == nullptr : Y == nullptr) return SWG_ERR_INVALID_ARG;
+    if (K > 0 && (A == nullptr || W == nullptr)) return SWG_ERR_INVALID_ARG;
+    if (too_big({M, 2 * N, K})) return SWG_ERR_UNSUPPORTED;
+    if (!aligned16(Y) || !aligned16(dY) || !aligned16(dH) || N % 8 != 0) return SWG_ERR_MISALIGNED;
+    if (K > 0 && (!aligned16(A) || !aligned16(W) || K % 8 != 0)) return SWG_ERR_MISALIGNED;
+    swg::GrpArgs p{};
+    p.groups = {offsets, (int)G, (int)M};
+    p.N = (int)(2 * N);
+    p.K = (int)K;
+    p.A = A;
+    p.lda = K;
+    p.B = W;
+    p.ldb = 2 * N;
+    p.strideB = G > 1 ? 2 * N * K : 0;
+    p.b_kn = 1;
+    p.C = grad ? dH : Y;
+    p.ldc = grad ? 2 * N : N;
+    p.dY = dY;
+    p.Y = grad ? Y : nullptr;
+    p.alpha = 1.0f;
+    p.out_kind = swg::OUT_BF16;
+    return run_grouped(p, swg::GRP_BF16, grad ? swg::GRP_DSWIGLU : swg::GRP_SWIGLU, stream);
+}
+
+int swiglu_grouped(const void *A, const void *W_fused, void *Y, const int32_t *offsets, int64_t G,
+                   int64_t M, int64_t N, int64_t K, void *stream)
+{
+    return swiglu_grouped_impl(A, W_fused, nullptr, Y, nullptr, offsets, G, M, N, K, false, stream);
+}
+
+int swiglu_grouped_grad(const void *A, const void *W_fused, const void *dY, void *Y, void *dH,
+                        const int32_t *offsets, int64_t G, int64_t M, int64_t N, int64_t K,
+                        void *stream)
+{
+    return swiglu_grouped_impl(A, W_fused, dY, Y, dH, offsets, G, M, N, K, true, stream);
+}
+
+int64_t mx4_scale_bytes(int format, int64_t G, int64_t M, int64_t K)
+{
+    if (!known_format(format) || G < 0 || M < 0 || K < 0 || too_big({G, M, K})) return -1;
+    const int64_t tiles_k = ceil_to(K, 4 * block_of(format)) / (4 * block_of(format));
+    return 512 * tiles_k * (M / 128 + G);
+}
+
+static int mx4_convert(int format, int64_t G, int64_t M, int64_t K, const void *X, int64_t ldx,
+                       int xtype, float scale, const int32_t *offsets, const void *Q, int64_t ldq,
+                       const void *S, bool back, void *stream)
+{
+    int bytes;
+    if (!known_format(format) || !type_bytes(xtype, bytes)) return SWG_ERR_UNSUPPORTED;
+    if (M < 0 || K < 0) return SWG_ERR_INVALID_ARG;
+    if (int rc = check_groups(offsets, G)) return rc;
+    if (M == 0 || K == 0 || G == 0) return SWG_OK;
+    if (X == nullptr || Q == nullptr || S == nullptr || ldx < K || ldq < ceil_to(K, 32) / 2)
+        return SWG_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return SWG_ERR_INVALID_ARG;
+    if (too_big({M, K, ldx, ldq})) return SWG_ERR_UNSUPPORTED;
+    if (!aligned16(X) || !aligned16(Q) || !aligned16(S) || (ldx * bytes) % 16 != 0 || ldq % 16 != 0)
+        return SWG_ERR_MISALIGNED;
+    swg::Mx4Args p{};
+    p.groups = {offsets, (int)G, (int)M};
+    p.K = (int)K;
+    p.format = format;
+    p.X = const_cast<void *>(X);
+    p.ldx = ldx;
+    p.type = xtype;
+    p.scale = scale;
+    p.Q = static_cast<uint8_t *>(const_cast<void *>(Q));
+    p.ldq = ldq;
+    p.S = static_cast<uint8_t *>(const_cast<void *>(S));
+    swg::DeviceInfo d;
+    if (int rc = swg::device_info(d)) return rc;
+    return swg::count_launch(swg::launch_mx4(p, back, (int)(M / 128 + G), d.err,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+int mx4_quantize(int format, int64_t G, int64_t M, int64_t K, const void *X, int64_t ldx,
+                 int xtype, float scale, const int32_t *offsets, void *Q, int64_t ldq, void *S,
+                 void *stream)
+{
+    return mx4_convert(format, G, M, K, X, ldx, xtype, scale, offsets, Q, ldq, S, false, stream);
+}
+
+int mx4_dequantize(int format, int64_t G, int64_t M, int64_t K, const void *Q, int64_t ldq,
+                   const void *S, float scale, const int32_t *offsets, void *X, int64_t ldx,
+                   int xtype, void *stream)
+{
+    return mx4_convert(format, G, M, K, X, ldx, xtype, scale, offsets, Q, ldq, S, true, stream);
+}
+
+int gemm_mx4(int format, int64_t G, int64_t M, int64_t N, int64_t K, float alpha, const void *A,
+             int64_t lda, const void *SA, const void *B, int64_t ldb, int64_t strideB,
+             const void *SB, const int32_t *offsets, float beta, void *C, int64_t ldc, int ctype,
+             void *stream)
+{
+    int bytes;
+    if (!known_format(format) || !type_bytes(ctype, bytes)) return SWG_ERR_UNSUPPORTED;
+    if (M < 0 || N < 0 || K < 0) return SWG_ERR_INVALID_ARG;
+    if (int rc = check_groups(offsets, G)) return rc;
+    if (M == 0 || N == 0 || G == 0) return SWG_OK;
+    const int64_t row = ceil_to(K, 32) / 2;
+    if (C == nullptr || ldc < N) return SWG_ERR_INVALID_ARG;
+    if (K > 0 && (!A || !SA || !B || !SB || lda < row || ldb < row)) return SWG_ERR_INVALID_ARG;
+    if (K > 0 && G > 1 && strideB < (N - 1) * ldb + row) return SWG_ERR_INVALID_ARG;
+    if (too_big({M, N, K, lda, ldb, ldc})) return SWG_ERR_UNSUPPORTED;
+    if (!aligned16(C) || (ldc * bytes) % 16 != 0) return SWG_ERR_MISALIGNED;
+    if (K > 0 && (!aligned16(A) || !aligned16(SA) || !aligned16(B) || !aligned16(SB) ||
+                  lda % 16 != 0 || ldb % 16 != 0 || (G > 1 && strideB % 16 != 0)))
+        return SWG_ERR_MISALIGNED;
+    swg::GrpArgs p{};
+    p.groups = {offsets, (int)G, (int)M};
+    p.N = (int)N;
+    p.K = (int)K;
+    p.A = A;
+    p.lda = lda;
+    p.SA = static_cast<const uint8_t *>(SA);
+    p.B = B;
+    p.ldb = ldb;
+    p.strideB = G > 1 ? strideB : 0;
+    p.SB = static_cast<const uint8_t *>(SB);
+    p.C = C;
+    p.ldc = ldc;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.out_kind = ctype == SWG_TYPE_F32 ? swg::OUT_F32 : ctype == SWG_TYPE_F16 ? swg::OUT_F16
+                                                                              : swg::OUT_BF16;
+    return run_grouped(p, format == SWG_NVFP4 ? swg::GRP_NVFP4 : swg::GRP_MXFP4, swg::GRP_STORE,
+                       stream);
+}
+
+int swiglu_mx4(int format, const void *A, const void *SA, const void *W, const void *SW, void *Y,
+               const int32_t *offsets, int64_t G, int64_t M, int64_t N, int64_t K, float alpha,
+               void *stream)
+{
+    if (!known_format(format)) return SWG_ERR_UNSUPPORTED;
+    if (M < 0 || N < 0 || K < 0) return SWG_ERR_INVALID_ARG;
+    if (int rc = check_groups(offsets, G)) return rc;
+    if (M == 0 || N == 0 || G == 0) return SWG_OK;
+    if (Y == nullptr || (K > 0 && (!A || !SA || !W || !SW))) return SWG_ERR_INVALID_ARG;
+    if (too_big({M, 2 * N, K})) return SWG_ERR_UNSUPPORTED;
+    if (!aligned16(Y) || N % 8 != 0) return SWG_ERR_MISALIGNED;
+    if (K > 0 && (!aligned16(A) || !aligned16(SA) || !aligned16(W) || !aligned16(SW)))
+        return SWG_ERR_MISALIGNED;
+    const int64_t row = ceil_to(K, 32) / 2;
+    swg::GrpArgs p{};
+    p.groups = {offsets, (int)G, (int)M};
+    p.N = (int)(2 * N);
+    p.K = (int)K;
+    p.A = A;
+    p.lda = row;
+    p.SA = static_cast<const uint8_t *>(SA);
+    p.B = W;
+    p.ldb = row;
+    p.strideB = G > 1 ? 2 * N * row : 0;
+    p.SB = static_cast<const uint8_t *>(SW);
+    p.C = Y;
+    p.ldc = N;
+    p.alpha = alpha;
+    p.out_kind = swg::OUT_BF16;
+    return run_grouped(p, format == SWG_NVFP4 ? swg::GRP_NVFP4 : swg::GRP_MXFP4, swg::GRP_SWIGLU,
+                       stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,63 @@
+// experts_launch.h — launches of the expert-MLP kernels, and the decoding of
+// 4-bit values that they share.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "experts.h"
+
+namespace swg {
+
+struct Mx4Args {
+    Groups groups;
+    int K;
+    int format;                // 0 MXFP4, 1 NVFP4
+    void *X;                   // read by quantize, written by dequantize
+    long long ldx;             // elements
+    int type;                  // swg_type
+    float scale;
+    uint8_t *Q;
+    long long ldq;             // bytes
+    uint8_t *S;
+};
+// tile_rows: an upper bound of the rows of scale tiles over all groups.
+cudaError_t launch_mx4(const Mx4Args &p, bool back, int tile_rows, int *err, cudaStream_t s);
+
+cudaError_t launch_grouped(const GrpArgs &p, GrpKind kind, GrpEpi epi, int sms, int *err,
+                           cudaStream_t s);
+
+struct WgradArgs {
+    Groups groups;
+    int N, K;
+    const void *A;
+    long long lda;
+    const void *D;
+    long long ldd;
+    void *C;
+    long long ldc, strideC;
+    float alpha, beta;
+    int in_bf16;
+    int out_kind;
+};
+cudaError_t launch_wgrad(const WgradArgs &p, int sms, int *err, cudaStream_t s);
+
+#ifdef __CUDACC__
+// The value of an E2M1 code (sign in bit 3).
+__device__ __forceinline__ float e2m1_value(uint32_t c)
+{
+    const uint32_t e = (c >> 1) & 3, m = c & 1;
+    const float v = e ? __int_as_float(((126 + e) << 23) | (m << 22)) : 0.5f * m;
+    return (c & 8) ? -v : v;
+}
+
+// The value of a scale byte: E8M0 (0xFF is NaN), or E4M3.
+__device__ __forceinline__ float mx4_scale_value(bool nv, uint32_t c)
+{
+    if (nv) return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3)));
+    return c == 255u ? __int_as_float(0x7fffffff)
+                     : __int_as_float(c > 0 ? c << 23 : 1 << 22);
+}
+#endif
+
+}  // namespace swg
