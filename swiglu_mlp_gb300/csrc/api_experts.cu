@@ -3,13 +3,14 @@
 // api.cu, every argument is validated before any CUDA call.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
 #include "swiglu_mlp.h"
 #include "experts_launch.h"
+#include "grouped.cuh"
 #include "host.h"
-#include "tc_gemm.cuh"
 
 namespace {
 
@@ -59,12 +60,97 @@ bool too_big(std::initializer_list<int64_t> v)
 int block_of(int format) { return format == SWG_NVFP4 ? 16 : 32; }
 bool known_format(int format) { return format == SWG_MXFP4 || format == SWG_NVFP4; }
 
-int run_grouped(const swg::GrpArgs &p, swg::GrpKind kind, swg::GrpEpi epi, void *stream)
+// Tensor maps and parameters of a grouped product, and its launch.
+int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void *stream)
 {
+    using swg::encode_tiled;
     swg::DeviceInfo d;
     if (int rc = swg::device_info(d)) return rc;
-    return swg::count_launch(
-        swg::launch_grouped(p, kind, epi, d.sms, d.err, static_cast<cudaStream_t>(stream)));
+    const bool f4 = kind >= swg::GRP_MXFP4, nv = kind == swg::GRP_NVFP4;
+    const int64_t M = a.groups.M, G = a.groups.G, N = a.N, K = a.K;
+    const int tokens = f4 ? swg::GrpCfg<swg::MATH_MX>::TOKENS : swg::GrpCfg<swg::MATH_16>::TOKENS;
+
+    swg::GrpParams p{};
+    p.groups = a.groups;
+    p.N = a.N;
+    p.K = a.K;
+    p.n_blocks = (int)((N + 255) / 256);
+    p.bk = f4 ? 256 : 64;
+    p.k_blocks = (int)((K + p.bk - 1) / p.bk);
+    p.w_mn = a.b_kn;
+    p.w_tiles = (int)((N + 127) / 128);
+    p.alpha = a.alpha;
+    p.beta = a.beta;
+    p.C = a.C;
+    p.ldc = a.ldc;
+    p.dY = a.dY;
+    p.Y = a.Y;
+    p.out_kind = a.out_kind;
+    p.err = d.err;
+
+    swg::GrpMaps m{};
+    bool ok = true;
+    if (K > 0 && !f4) {
+        // instruction descriptor, kind::f16: FP32 accumulators (bits 4-5 = 1), types (7-9,
+        // 10-12: 1 = bf16), weight MN-major (15), M >> 4 (24-28); N is set per tile (17-22)
+        const uint32_t t = kind == swg::GRP_BF16 ? 1u : 0u;
+        p.idesc = (1u << 4) | (t << 7) | (t << 10) | ((uint32_t)p.w_mn << 15) | (16u << 24);
+        const CUtensorMapDataType type = kind == swg::GRP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        const uint64_t ldb = (uint64_t)a.ldb * 2;
+        const uint64_t sb = G > 1 ? (uint64_t)a.strideB * 2 : ldb * (p.w_mn ? K : N);
+        if (!p.w_mn) {
+            const uint64_t dims[] = {(uint64_t)K, (uint64_t)N, (uint64_t)G}, st[] = {ldb, sb};
+            const uint32_t box[] = {64, 128, 1};
+            ok = encode_tiled(&m.w, type, 3, a.B, dims, st, box, true);
+        } else if (N % 64 == 0) {
+            // 64 columns at a time as their own dimension: one box of 64 x 64 x 2
+            const uint64_t dims[] = {64, (uint64_t)K, (uint64_t)N / 64, (uint64_t)G};
+            const uint64_t st[] = {ldb, 128, sb};
+            const uint32_t box[] = {64, 64, 2, 1};
+            ok = encode_tiled(&m.w, type, 4, a.B, dims, st, box, true);
+            p.w_4d = 1;
+        } else {
+            const uint64_t dims[] = {(uint64_t)N, (uint64_t)K, (uint64_t)G}, st[] = {ldb, sb};
+            const uint32_t box[] = {64, 64, 1};
+            ok = encode_tiled(&m.w, type, 3, a.B, dims, st, box, true);
+        }
+        for (int i = 0; i < swg::TOKEN_BOXES && ok; ++i) {
+            const uint64_t dims[] = {(uint64_t)K, (uint64_t)M}, st[] = {(uint64_t)a.lda * 2};
+            const uint32_t box[] = {64, i == 0 ? tokens / 2u : 128u >> i};
+            ok = encode_tiled(&m.t[i], type, 2, a.A, dims, st, box, true);
+        }
+    } else if (K > 0) {
+        // kind::mxf4 and mxf4nvf4: E2M1 operands (7-9, 10-12: 1), scale type (23: 1 = E8M0,
+        // 0 = E4M3), M >> 4 (24-28); the scales' byte in their column (4-5, 29-30) per instruction
+        p.idesc = (1u << 7) | (1u << 10) | (nv ? 0u : 1u << 23) | (16u << 24);
+        const uint64_t row = (uint64_t)ceil_to(K, 32) / 2;
+        const uint64_t sb = G > 1 ? (uint64_t)a.strideB : (uint64_t)a.ldb * N;
+        const uint64_t wd[] = {row, (uint64_t)N, (uint64_t)G}, wst[] = {(uint64_t)a.ldb, sb};
+        const uint32_t wbox[] = {128, 128, 1};
+        ok = encode_tiled(&m.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.B, wd, wst, wbox, true);
+        for (int i = 0; i < swg::TOKEN_BOXES && ok; ++i) {
+            const uint64_t dims[] = {row, (uint64_t)M}, st[] = {(uint64_t)a.lda};
+            const uint32_t box[] = {128, i == 0 ? tokens / 2u : 128u >> i};
+            ok = encode_tiled(&m.t[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.A, dims, st, box, true);
+        }
+        // Scale tiles as rows of 64-bit elements, one row per 128 rows of the
+        // matrix: a box is one stage's tiles (1 KB or 2 KB) of one row, two for A
+        const int tile_k = nv ? 64 : 128;
+        const uint64_t tiles = (uint64_t)(K + tile_k - 1) / tile_k * 64;
+        const uint64_t sst[] = {tiles * 8};
+        const uint64_t swd[] = {tiles, (uint64_t)(p.w_tiles * G)};
+        const uint64_t std_[] = {tiles, (uint64_t)(M / 128 + G)};
+        const uint32_t per = nv ? 256u : 128u;
+        const uint32_t swbox[] = {per, 1}, stbox[] = {per, 2};
+        ok = ok && encode_tiled(&m.sw, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, a.SB, swd, sst, swbox, false);
+        ok = ok && encode_tiled(&m.st, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, a.SA, std_, sst, stbox, false);
+    }
+    if (!ok) return swg::record_cuda_error();
+    const long long units = (M / tokens + std::min(G, M)) * (long long)p.n_blocks;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return swg::count_launch(f4 ? swg::launch_grouped_f4(nv, epi, m, p, units, d.sms, s)
+                                : swg::launch_grouped_16(epi, m, p, units, d.sms, s));
 }
 
 }  // namespace

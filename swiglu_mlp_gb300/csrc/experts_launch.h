@@ -24,8 +24,13 @@ struct Mx4Args {
 // tile_rows: an upper bound of the rows of scale tiles over all groups.
 cudaError_t launch_mx4(const Mx4Args &p, bool back, int tile_rows, int *err, cudaStream_t s);
 
-cudaError_t launch_grouped(const GrpArgs &p, GrpKind kind, GrpEpi epi, int sms, int *err,
-                           cudaStream_t s);
+struct GrpMaps;
+struct GrpParams;
+// `units`: an upper bound of the tiles over all groups.
+cudaError_t launch_grouped_16(GrpEpi epi, const GrpMaps &m, const GrpParams &p, long long units,
+                              int sms, cudaStream_t s);
+cudaError_t launch_grouped_f4(bool nv, GrpEpi epi, const GrpMaps &m, const GrpParams &p,
+                              long long units, int sms, cudaStream_t s);
 
 struct WgradArgs {
     Groups groups;

@@ -1,0 +1,598 @@
+// grouped.cuh — products grouped by expert on tcgen05: 16-bit operands and
+// microscaled 4-bit ones, with the plain, SwiGLU and SwiGLU-gradient epilogues.
+//
+//   C[i, n] = sum_k A[i, k] * W_g[n, k]      for the rows i of group g
+//
+// The product is computed transposed: the weight is the MMA's 256-row operand
+// (128 rows per CTA of a pair) and the group's rows are its N, which every
+// instruction may choose anew as any multiple of 16 up to TOKENS.  A group
+// of r rows is cut into ceil(r / TOKENS) tiles of nearly equal width, so the
+// padding is below 16 rows a tile, where 256-row tiles of A would pad every
+// group to 256: with 16 experts of about 500 rows a third of the work.
+//
+// Warp 0 loads (TMA), warp 1 issues the MMAs, warps 2..9 empty the finished
+// accumulator while the next tile's main loop runs (two accumulators in tensor
+// memory).  Every CTA finds its tiles itself from the offsets on the device;
+// the host never waits for them.
+//
+// 4-bit operands (kind::mxf4 / kind::mxf4nvf4, K = 64 per instruction): a
+// stage holds 256 elements of K and their scales, which tcgen05.cp copies from
+// the 512-byte scale tiles in shared memory to tensor memory ahead of the
+// stage's MMAs (same issuing thread, so they execute in order).  Both CTAs
+// need the scales of all of the tile's rows of A, and those of their own
+// weight rows.
+#pragma once
+
+#include "experts_launch.h"
+#include "groups.cuh"
+#include "tc_gemm.cuh"
+
+namespace swg {
+
+// ------------------------------------------------------------ PTX wrappers
+
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void *tmap, uint32_t bar,
+                                                 int32_t x, int32_t y, int32_t z, int32_t w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+// Scales of one tile (128 rows x 4 blocks, 512 bytes in shared memory) to four
+// tensor-memory columns, repeated for the four lane quarters, in both CTAs.
+__device__ __forceinline__ void tc_cp_scales_pair(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+}
+
+template <bool NV>
+__device__ __forceinline__ void tc_mma_f4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                               uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                               uint32_t accumulate)
+{
+    if (NV)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
+            " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
+            " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// Descriptor of a scale tile: 8-row x 16-byte core matrices 128 bytes apart, no swizzle.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (8ull << 32) | (1ull << 46);
+}
+
+// ------------------------------------------------------------ configuration
+
+enum GrpMath { MATH_16 = 0, MATH_MX = 1, MATH_NV = 2 };
+
+constexpr int TOKEN_BOXES = 4;           // box heights of A's maps: TOKENS / 2, 64, 32, 16 rows
+
+struct GrpMaps {
+    CUtensorMap w;                       // weights
+    CUtensorMap t[TOKEN_BOXES];          // rows of A
+    CUtensorMap sw, st;                  // scale tiles of both (4-bit)
+};
+
+struct GrpParams {
+    Groups groups;
+    int N, K;
+    int n_blocks, k_blocks;
+    int bk;                              // K elements of a stage: 64 (16-bit) or 256 (4-bit)
+    uint32_t idesc;                      // without N
+    int w_mn;                            // weight MN-major (stored K x N)
+    int w_4d;                            // ... as one 4-D box per stage
+    int w_tiles;                         // rows of scale tiles per group of weights
+    float alpha, beta;
+    void *C;
+    long long ldc;
+    const void *dY;
+    void *Y;
+    int out_kind;
+    int *err;
+};
+
+template <int MATH>
+struct GrpCfg {
+    static constexpr bool F4 = MATH != MATH_16;
+    // Rows of A per tile: two accumulators fill tensor memory at 256; with
+    // scales there they leave room at 192.
+    static constexpr int TOKENS = F4 ? 192 : 256;
+    static constexpr int TILES_PER_STAGE = MATH == MATH_NV ? 4 : 2;   // scale tiles along K
+    static constexpr int SCALE_BYTES = F4 ? 512 * TILES_PER_STAGE : 0;
+    static constexpr int W_BYTES = 128 * 128;
+    static constexpr int T_BYTES = TOKENS / 2 * 128;
+    static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + 3 * SCALE_BYTES;
+    static constexpr int OUT_BYTES = 3072;        // per epilogue warp, see grp_emit
+    static constexpr int TABLE_BYTES = (F4 ? 3 : 2) * 4 * (MAX_GROUPS + 1) + 4;
+    static constexpr int FIXED = 1024 + NUM_EPI_WARPS * OUT_BYTES + TABLE_BYTES + 512;
+    static constexpr int STAGES_RAW = (232448 - FIXED) / STAGE_BYTES;
+    static constexpr int STAGES = STAGES_RAW > 6 ? 6 : STAGES_RAW;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + FIXED;
+    static constexpr int ACC_STRIDE = TOKENS;     // tensor-memory columns per accumulator
+    static constexpr int SCALE_COL = 2 * TOKENS;  // first scale column (two buffers of 64)
+    static_assert(STAGES >= 4, "pipeline too shallow");
+    static_assert(!F4 || 2 * TOKENS + 128 <= 512, "tensor memory");
+};
+
+// Rows of A covered by each tile of a group of `rows` (> 0) rows, but the last.
+template <int MATH>
+__device__ __forceinline__ int tile_step(int rows)
+{
+    using C = GrpCfg<MATH>;
+    const int t = ceil_div(rows, C::TOKENS);
+    // 4-bit: a tile begins at a multiple of 64 rows, two scale columns
+    const int unit = C::F4 ? 64 : 16;
+    return ceil_div(ceil_div(rows, t), unit) * unit;
+}
+
+struct GrpTile {
+    int g, nb;         // group, block of 256 weight rows
+    int row0, rows;    // rows of A
+    int local;         // row0 within the group
+    int width;         // rows rounded up to 16: the MMA's N
+};
+
+// Tile u: groups in order; within a group bands of 8 tiles of A walk the
+// weight blocks together, so that concurrently running pairs share both in L2.
+template <int MATH>
+__device__ __forceinline__ GrpTile grp_tile(const int *start, const int *first, int G,
+                                            int n_blocks, int u)
+{
+    GrpTile t;
+    t.g = group_of(first, G, u / n_blocks);
+    const int tiles = first[t.g + 1] - first[t.g];
+    const int local = u - first[t.g] * n_blocks;
+    const int rows = start[t.g + 1] - start[t.g];
+    int mb;
+    if (tiles == 1) {
+        mb = 0;
+        t.nb = local;
+    } else {
+        const int band = local / (8 * n_blocks);
+        const int in = local - band * 8 * n_blocks;
+        const int bm = min(8, tiles - band * 8);
+        t.nb = in / bm;
+        mb = band * 8 + in - t.nb * bm;
+    }
+    const int step = tile_step<MATH>(rows);
+    t.local = mb * step;
+    t.row0 = start[t.g] + t.local;
+    t.rows = min(step, rows - t.local);
+    t.width = (t.rows + 15) & ~15;
+    return t;
+}
+
+// ------------------------------------------------------------ epilogue
+
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((unsigned short)v) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t to_16(float v, int out_kind)
+{
+    if (out_kind == OUT_F16) return __half_as_ushort(__float2half_rn(v));
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Copies `rows` rows of COLS 16-bit values, staged back to back, to rows of
+// `out` ldo apart, 16 bytes per lane; columns from `limit` on are left out.
+template <int COLS>
+__device__ __forceinline__ void copy_rows(uint32_t src, uint16_t *out, long long ldo, int rows,
+                                          int limit, int lane)
+{
+    constexpr int PER_ROW = COLS / 8, ROWS = 32 / PER_ROW;
+    const int c = (lane % PER_ROW) * 8;
+#pragma unroll
+    for (int r = lane / PER_ROW; r < 32; r += ROWS) {
+        if (r >= rows || c >= limit) continue;
+        const uint4 v = ld_shared_v4(src + (uint32_t)(r * COLS + c) * 2);
+        uint16_t *dst = out + r * ldo + c;
+        if (c + 8 <= limit) {
+            *reinterpret_cast<uint4 *>(dst) = v;
+        } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < limit) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+        }
+    }
+}
+
+// 32 rows of A (from `row`, `rows` of them real) of the 32 accumulator rows
+// (columns n0 + lane of C) that this warp holds: acc[j] is row j's.  16-bit
+// results pass through `buf`, this warp's shared memory, to be stored as 16
+// bytes per lane.
+template <int EPI>
+__device__ __forceinline__ void grp_emit(const GrpParams &p, const uint32_t (&acc)[32],
+                                         const uint32_t (&dy)[16], int row, int rows, int n0,
+                                         uint32_t buf, int lane)
+{
+    if (EPI == GRP_STORE) {
+        const int n = n0 + lane;
+        const bool in = n < p.N;
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(acc[j]);
+        if (p.beta != 0.0f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (in && j < rows)
+                    v[j] += p.beta * load_out(p.C, (row + j) * p.ldc + n, p.out_kind);
+        }
+        if (p.out_kind == OUT_F32) {
+            float *out = reinterpret_cast<float *>(p.C) + row * p.ldc + n;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (in && j < rows) out[j * p.ldc] = v[j];
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            st_shared_u16(buf + (uint32_t)(j * 32 + lane) * 2, to_16(v[j], p.out_kind));
+        __syncwarp();
+        copy_rows<32>(buf, reinterpret_cast<uint16_t *>(p.C) + row * p.ldc + n0, p.ldc, rows,
+                      p.N - n0, lane);
+        __syncwarp();
+        return;
+    }
+    // Lanes 2i and 2i + 1 hold Gate and Up of one output column.  They swap
+    // halves, so that the even lane has both for the even rows and the odd
+    // lane for the odd ones.
+    const int odd = lane & 1;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const uint32_t send = odd ? acc[2 * j] : acc[2 * j + 1];
+        const float got = __uint_as_float(__shfl_xor_sync(0xffffffffu, send, 1));
+        const float g = p.alpha * (odd ? got : __uint_as_float(acc[2 * j]));
+        const float u = p.alpha * (odd ? __uint_as_float(acc[2 * j + 1]) : got);
+        const uint32_t at = (uint32_t)((2 * j + odd) * 16 + lane / 2);
+        if (EPI == GRP_SWIGLU) {
+            st_shared_u16(buf + at * 2, to_16(silu_f32(g) * u, OUT_BF16));
+        } else {
+            const float s = __fdividef(1.0f, 1.0f + __expf(-g));
+            const float d = __uint_as_float(dy[j]);
+            const float gs = g * s;
+            st_shared_u32(buf + at * 4, pack2(d * u * (s + gs * (1.0f - s)), d * gs, OUT_BF16));
+            if (p.Y) st_shared_u16(buf + 2048 + at * 2, to_16(gs * u, OUT_BF16));
+        }
+    }
+    __syncwarp();
+    if (EPI == GRP_SWIGLU) {
+        copy_rows<16>(buf, reinterpret_cast<uint16_t *>(p.C) + row * p.ldc + n0 / 2, p.ldc, rows,
+                      (p.N - n0) / 2, lane);
+    } else {
+        copy_rows<32>(buf, reinterpret_cast<uint16_t *>(p.C) + row * p.ldc + n0, p.ldc, rows,
+                      p.N - n0, lane);
+        if (p.Y)
+            copy_rows<16>(buf + 2048,
+                          reinterpret_cast<uint16_t *>(p.Y) + row * (long long)(p.N / 2) + n0 / 2,
+                          p.N / 2, rows, (p.N - n0) / 2, lane);
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------------------ kernel
+
+template <int MATH, int EPI>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    grouped_kernel(const __grid_constant__ GrpMaps maps, const GrpParams p)
+{
+    using C = GrpCfg<MATH>;
+    constexpr bool F4 = C::F4;
+    constexpr int S = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // stages (W, rows of A, scales), output staging, barriers, group table
+    uint8_t *sW = smem;
+    uint8_t *sT = sW + S * C::W_BYTES;
+    uint8_t *sS = sT + S * C::T_BYTES;
+    uint8_t *sOut = sS + S * 3 * C::SCALE_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sOut + NUM_EPI_WARPS * C::OUT_BYTES);
+    uint64_t *full = bars;
+    uint64_t *empty = bars + S;
+    uint64_t *acc_full = bars + 2 * S;
+    uint64_t *acc_empty = bars + 2 * S + 2;
+    uint64_t *mma_done = bars + 2 * S + 4;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 2 * S + 5);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    int *start = reinterpret_cast<int *>(sOut + NUM_EPI_WARPS * C::OUT_BYTES + 512 - 64);
+    int *first = start + p.groups.G + 1;
+    int *stile = first + p.groups.G + 1;          // rows of scale tiles before each group
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        if (p.k_blocks > 0) tma_prefetch_desc(&maps.w);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&acc_full[b]), 1);
+            mbar_init(smem_u32(&acc_empty[b]), 2 * NUM_EPI_WARPS);
+        }
+        mbar_init(smem_u32(mma_done), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_holder), 512);
+        tmem_relinquish_pair();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 2) {
+        group_table(p.groups, start, first, p.err, [](int rows) { return ceil_div(rows, C::TOKENS); });
+        if (F4) {
+            if (lane == 0) stile[0] = 0;
+            int sum = 0;
+            for (int base = 0; base < p.groups.G; base += 32) {
+                const int i = base + lane;
+                int v = i < p.groups.G ? ceil_div(start[i + 1] - start[i], 128) : 0;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, v, d);
+                    if (lane >= d) v += o;
+                }
+                if (i < p.groups.G) stile[i + 1] = sum + v;
+                sum += __shfl_sync(0xffffffffu, v, 31);
+            }
+        }
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    const int G = p.groups.G;
+    const int units = first[G] * p.n_blocks;
+    const int u0 = (int)(blockIdx.x >> 1), du = (int)(gridDim.x >> 1);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0 && p.k_blocks > 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t armed = 0, armed_parity = 0;
+            bool ok = true;
+            for (int u = u0; u < units && ok; u += du) {
+                const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, u);
+                const int half = t.width / 2;
+                // the lowest box that holds this CTA's rows of A
+                int box = 0;
+                while (box + 1 < TOKEN_BOXES && half <= (64 >> box)) ++box;
+                const int t_row = t.row0 + (int)rank * half;
+                const int n0 = t.nb * 256 + (int)rank * 128;
+                const uint32_t t_bytes = box == 0 ? C::T_BYTES : (128u >> box) * 128u;
+                const uint32_t bytes = C::W_BYTES + t_bytes + 3 * C::SCALE_BYTES;
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    if (!wait_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    // both CTAs' bytes complete on the leader's barrier
+                    const uint32_t fb_local = smem_u32(&full[stage]);
+                    const uint32_t fb = mapa_shared(fb_local, 0);
+                    if (leader) mbar_arrive_expect_tx(fb_local, 2 * bytes);
+                    armed |= 1u << stage;
+                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                    const uint32_t w_dst = smem_u32(sW + stage * C::W_BYTES);
+                    const uint32_t t_dst = smem_u32(sT + stage * C::T_BYTES);
+                    const int k0 = kb * (F4 ? 128 : 64);     // inner coordinate of the boxes
+                    if (!p.w_mn) {
+                        tma_load_3d_pair(w_dst, &maps.w, fb, k0, n0, t.g);
+                    } else if (p.w_4d) {
+                        tma_load_4d_pair(w_dst, &maps.w, fb, 0, k0, n0 / 64, t.g);
+                    } else {
+                        tma_load_3d_pair(w_dst, &maps.w, fb, n0, k0, t.g);
+                        tma_load_3d_pair(w_dst + 8192, &maps.w, fb, n0 + 64, k0, t.g);
+                    }
+                    tma_load_2d_pair(t_dst, &maps.t[box], fb, k0, t_row);
+                    if (F4) {
+                        const uint32_t s_dst = smem_u32(sS + stage * 3 * C::SCALE_BYTES);
+                        const int x = kb * (C::SCALE_BYTES / 8);
+                        tma_load_2d_pair(s_dst, &maps.sw, fb, x,
+                                         t.g * p.w_tiles + t.nb * 2 + (int)rank);
+                        tma_load_2d_pair(s_dst + C::SCALE_BYTES, &maps.st, fb, x,
+                                         stile[t.g] + t.local / 128);
+                    }
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // Never leave with loads in flight into this CTA's shared memory.
+            if (leader) {
+                for (int s = 0; s < S; ++s)
+                    if (armed & (1u << s))
+                        wait_bounded(smem_u32(&full[s]), (armed_parity >> s) & 1, abort_flag,
+                                     p.err, false, DRAIN_LIMIT_NS);
+            } else if (!ok) {
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 200000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0 && leader && p.k_blocks > 0) {
+            const uint32_t w_kstep = p.w_mn ? 2048u : 32u;
+            const uint32_t w_lbo = p.w_mn ? 8192u : 16u;
+            constexpr int MMA_K = F4 ? 64 : 16;
+            const int last_steps = ceil_div(p.K - (p.k_blocks - 1) * p.bk, MMA_K);
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t sbuf = 0;
+            bool ok = true;
+            int n = 0;
+            for (int u = u0; u < units && ok; u += du, ++n) {
+                const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, u);
+                const uint32_t idesc = p.idesc | ((uint32_t)(t.width >> 3) << 17);
+                const int acc = n & 1;
+                if (!wait_bounded(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, p.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc * C::ACC_STRIDE;
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    if (!wait_bounded(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int steps = kb + 1 == p.k_blocks ? last_steps : 4;
+                    const uint32_t w_base = smem_u32(sW + stage * C::W_BYTES);
+                    const uint32_t t_base = smem_u32(sT + stage * C::T_BYTES);
+                    uint32_t sf = 0, sfb = 0;
+                    if (F4) {
+                        // columns: 4 per tile of this CTA's weight rows, then 8
+                        // per tile of A (its rows 0..127 and 128..255)
+                        sf = tmem_base + C::SCALE_COL + sbuf * 64;
+                        sfb = sf + 4 * C::TILES_PER_STAGE;
+                        sbuf ^= 1;
+                        const uint32_t s_base = smem_u32(sS + stage * 3 * C::SCALE_BYTES);
+#pragma unroll
+                        for (int i = 0; i < C::TILES_PER_STAGE; ++i) {
+                            tc_cp_scales_pair(sf + 4 * i, scale_desc(s_base + i * 512));
+                            tc_cp_scales_pair(sfb + 8 * i,
+                                              scale_desc(s_base + C::SCALE_BYTES + i * 512));
+                            tc_cp_scales_pair(sfb + 8 * i + 4,
+                                              scale_desc(s_base + 2 * C::SCALE_BYTES + i * 512));
+                        }
+                        // a tile that begins at the second half of its scale tile
+                        sfb += (t.local & 64) ? 2 : 0;
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk >= steps) break;
+                        const uint64_t wd = smem_desc(w_base + kk * w_kstep, w_lbo, 1024);
+                        const uint64_t td = smem_desc(t_base + kk * 32, 16, 1024);
+                        const uint32_t accum = (kb > 0 || kk > 0) ? 1u : 0u;
+                        if (MATH == MATH_16) {
+                            tc_mma_f16_pair(d_tmem, wd, td, idesc, accum);
+                        } else if (MATH == MATH_NV) {
+                            tc_mma_f4_pair<true>(d_tmem, wd, td, idesc, sf + 4 * kk, sfb + 8 * kk,
+                                                 accum);
+                        } else {
+                            // two blocks of 32 per instruction: bytes 0, 1 or 2, 3 of a tile's four
+                            const uint32_t id = (kk & 1) * 2;
+                            tc_mma_f4_pair<false>(d_tmem, wd, td, idesc | (id << 29) | (id << 4),
+                                                  sf + 4 * (kk >> 1), sfb + 8 * (kk >> 1), accum);
+                        }
+                    }
+                    tc_commit_pair(smem_u32(&empty[stage]));
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                tc_commit_pair(smem_u32(&acc_full[acc]));
+            }
+            // Never free tensor memory under a running MMA.
+            tc_commit_pair_local(smem_u32(mma_done));
+            wait_bounded(smem_u32(mma_done), 0, abort_flag, p.err, false, DRAIN_LIMIT_NS);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;                 // tensor-memory lane quarter of this warp
+        const int h = (warp - EPI_WARP0) / 4;   // takes every second chunk of 32 rows of A
+        const uint32_t buf = smem_u32(sOut + (warp - EPI_WARP0) * C::OUT_BYTES);
+        int n = 0;
+        for (int u = u0; u < units; u += du, ++n) {
+            const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, u);
+            const int acc = n & 1;
+            const int n0 = t.nb * 256 + (int)rank * 128 + q * 32;
+            const bool work = n0 < p.N;
+            const int chunks = ceil_div(t.rows, 32);
+            uint32_t dy[16];
+            auto load_dy = [&](int c) {
+                if (EPI != GRP_DSWIGLU) return;
+                const int col = n0 / 2 + lane / 2;
+                const uint16_t *src = reinterpret_cast<const uint16_t *>(p.dY) +
+                                      (t.row0 + c * 32 + (lane & 1)) * (long long)(p.N / 2) + col;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    dy[j] = 0;
+                    if (2 * col < p.N && c * 32 + 2 * j + (lane & 1) < t.rows)
+                        dy[j] = (uint32_t)src[(long long)j * p.N] << 16;
+                }
+            };
+            if (h < chunks) load_dy(h);
+            if (p.k_blocks > 0) {
+                bool ok = wait_bounded(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, p.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * C::ACC_STRIDE;
+#pragma unroll 1
+            for (int c = h; c < chunks && work; c += 2) {
+                uint32_t r[32];
+                if (p.k_blocks > 0) {
+                    tmem_ld_32cols(t_row + c * 32, r);
+                    tmem_ld_wait(r);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = 0;
+                }
+                grp_emit<EPI>(p, r, dy, t.row0 + c * 32, min(32, t.rows - c * 32), n0, buf, lane);
+                if (c + 2 < chunks) load_dy(c + 2);
+            }
+            if (p.k_blocks > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_tmem(mapa_shared(smem_u32(&acc_empty[acc]), 0));
+            }
+        }
+    }
+
+    // Neither CTA frees its tensor memory or exits while the leader's MMAs or
+    // the peer's arrivals can still reach it.
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+}  // namespace swg

@@ -1,0 +1,55 @@
+// grouped_launch.cuh — launch helper of the grouped kernels' translation units.
+#pragma once
+
+#include <algorithm>
+
+#include "grouped.cuh"
+#include "launch.h"
+
+namespace swg {
+
+// Launches at most `units` pairs of CTAs (clusters of two), no more than can
+// be resident at once.  The kernel may be scheduled early behind the kernel
+// before it on the stream; it waits for that kernel's end before it reads
+// the offsets.
+template <auto KERNEL, class... Args>
+cudaError_t launch_pairs(int smem, long long units, int sms, cudaStream_t s,
+                         const Args &...args)
+{
+    static DeviceOnce configured;
+    static std::atomic<int> resident[DeviceOnce::kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    int pairs = 0;
+    if (configured.needed(dev)) {
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3(2 * (sms / 2));
+        e = cudaOccupancyMaxActiveClusters(&pairs, KERNEL, &cfg);
+        if (e != cudaSuccess) return e;
+        if (pairs < 1) return cudaErrorInvalidConfiguration;
+        if (dev >= 0 && dev < DeviceOnce::kDevices) resident[dev].store(pairs);
+        configured.mark(dev);
+    } else {
+        pairs = resident[dev].load();
+    }
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3((unsigned)(2 * std::min<long long>(units, pairs)));
+    return cudaLaunchKernelEx(&cfg, KERNEL, args...);
+}
+
+}  // namespace swg
