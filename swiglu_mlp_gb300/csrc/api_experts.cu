@@ -231,8 +231,10 @@ int gemm_grouped_wgrad(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, 
     p.out_kind = out;
     swg::DeviceInfo d;
     if (int rc = swg::device_info(d)) return rc;
-    return swg::count_launch(
-        swg::launch_wgrad(p, d.sms, d.err, static_cast<cudaStream_t>(stream)));
+    bool mapped = true;
+    const cudaError_t e =
+        swg::launch_wgrad(p, d.sms, d.err, static_cast<cudaStream_t>(stream), mapped);
+    return mapped ? swg::count_launch(e) : swg::record_cuda_error();
 }
 
 static int swiglu_grouped_impl(const void *A, const void *W, const void *dY, void *Y, void *dH,

@@ -45,7 +45,8 @@ struct WgradArgs {
     int in_bf16;
     int out_kind;
 };
-cudaError_t launch_wgrad(const WgradArgs &p, int sms, int *err, cudaStream_t s);
+// mapped: whether the tensor maps could be encoded (if not, nothing was launched).
+cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, bool &mapped);
 
 #ifdef __CUDACC__
 // The value of an E2M1 code (sign in bit 3).

@@ -4,6 +4,7 @@
 #include <algorithm>
 
 #include "grouped.cuh"
+#include "host.h"
 #include "launch.h"
 
 namespace swg {
