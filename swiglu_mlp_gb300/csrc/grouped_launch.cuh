@@ -13,9 +13,8 @@ namespace swg {
 // be resident at once.  The kernel may be scheduled early behind the kernel
 // before it on the stream; it waits for that kernel's end before it reads
 // the offsets.
-template <auto KERNEL, class... Args>
-cudaError_t launch_pairs(int smem, long long units, int sms, cudaStream_t s,
-                         const Args &...args)
+template <auto KERNEL, int THREADS, class... Args>
+cudaError_t launch_pairs(int smem, long long units, int sms, cudaStream_t s, const Args &...args)
 {
     static DeviceOnce configured;
     static std::atomic<int> resident[DeviceOnce::kDevices];
@@ -23,7 +22,7 @@ cudaError_t launch_pairs(int smem, long long units, int sms, cudaStream_t s,
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];

@@ -37,11 +37,12 @@ struct WgradParams {
     int *err;
 };
 
-constexpr int WG_STAGES = 5;             // a sixth would not leave room for the output staging
+constexpr int WG_STAGES = 6;
+constexpr int FIX_WARP = EPI_WARP0 + NUM_EPI_WARPS;
+constexpr int WG_THREADS = NUM_THREADS + 32;
 constexpr int OP_BYTES = 128 * 128;      // 64 rows x 128 columns of one operand per CTA
-constexpr int OUT_BYTES = 32 * 32 * 4;   // per epilogue warp
-constexpr int SMEM_BYTES = 1024 + WG_STAGES * 2 * OP_BYTES + NUM_EPI_WARPS * OUT_BYTES + 256 +
-                           2 * 4 * (MAX_GROUPS + 1);
+constexpr int BAR_BYTES = 512;
+constexpr int SMEM_BYTES = 1024 + WG_STAGES * 2 * OP_BYTES + BAR_BYTES + 2 * 4 * (MAX_GROUPS + 1);
 static_assert(SMEM_BYTES <= 232448, "beyond the per-CTA shared memory");
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
@@ -50,10 +51,24 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
                  : "memory");
 }
 
-__device__ __forceinline__ void fence_acquire_cluster()
+// Whether the phase has completed, acquiring at cluster scope: what the
+// peer's threads wrote before their arrivals is visible.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
 {
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
+
+// Whether a block with `left` rows of the group from its first on (64 rows and
+// more: all of them) also holds foreign rows in an MMA step that is run.
+__device__ __forceinline__ bool ends_inside(int left) { return left < 64 && (left & 15) != 0; }
 
 struct WgradTile {
     int g, kb, nb, row0, rows;
@@ -75,73 +90,7 @@ __device__ __forceinline__ WgradTile wgrad_tile(const WgradParams &p, const int 
     return t;
 }
 
-// 32 x 32 accumulators of this warp (row `k`: its lane's, columns n ..): to
-// C through `buf`, in which 16-byte chunk j of row r sits at j ^ (r mod 8).
-__device__ __forceinline__ void wgrad_emit(const WgradParams &p, const uint32_t (&acc)[32], int g,
-                                           int k0, int n, uint32_t buf, int lane)
-{
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        st_shared_v4(buf + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4)),
-                     make_uint4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]));
-    __syncwarp();
-    const long long base = (long long)g * p.strideC + n;
-    if (p.out_kind == OUT_F32) {
-        const int j = lane & 7;
-#pragma unroll 4
-        for (int r = lane >> 3; r < 32; r += 4) {
-            const uint4 w = ld_shared_v4(buf + (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)));
-            if (k0 + r >= p.K || n + 4 * j >= p.N) continue;
-            float *dst = reinterpret_cast<float *>(p.C) + base + (k0 + r) * p.ldc + 4 * j;
-            float v[4] = {p.alpha * __uint_as_float(w.x), p.alpha * __uint_as_float(w.y),
-                          p.alpha * __uint_as_float(w.z), p.alpha * __uint_as_float(w.w)};
-            if (n + 4 * j + 4 <= p.N) {
-                if (p.beta != 0.0f) {
-                    const float4 c = *reinterpret_cast<const float4 *>(dst);
-                    v[0] += p.beta * c.x;
-                    v[1] += p.beta * c.y;
-                    v[2] += p.beta * c.z;
-                    v[3] += p.beta * c.w;
-                }
-                *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-            } else {
-                for (int i = 0; i < 4 && n + 4 * j + i < p.N; ++i)
-                    dst[i] = p.beta != 0.0f ? v[i] + p.beta * dst[i] : v[i];
-            }
-        }
-    } else {
-        const int j = (lane & 3) * 2;
-#pragma unroll 4
-        for (int r = lane >> 2; r < 32; r += 8) {
-            const uint4 a = ld_shared_v4(buf + (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)));
-            const uint4 b = ld_shared_v4(buf + (uint32_t)(r * 128 + (((j + 1) ^ (r & 7)) << 4)));
-            if (k0 + r >= p.K || n + 4 * j >= p.N) continue;
-            const long long o = base + (k0 + r) * p.ldc + 4 * j;
-            uint16_t *dst = reinterpret_cast<uint16_t *>(p.C) + o;
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = p.alpha * __uint_as_float(w[i]);
-            if (p.beta != 0.0f) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (n + 4 * j + i < p.N) v[i] += p.beta * load_out(p.C, o + i, p.out_kind);
-            }
-            if (n + 4 * j + 8 <= p.N) {
-                *reinterpret_cast<uint4 *>(dst) =
-                    make_uint4(pack2(v[0], v[1], p.out_kind), pack2(v[2], v[3], p.out_kind),
-                               pack2(v[4], v[5], p.out_kind), pack2(v[6], v[7], p.out_kind));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (n + 4 * j + i < p.N) dst[i] = (uint16_t)to_16(v[i], p.out_kind);
-            }
-        }
-    }
-    __syncwarp();
-}
-
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(WG_THREADS, 1)
     wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -149,17 +98,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *sA = smem;
     uint8_t *sD = sA + WG_STAGES * OP_BYTES;
-    uint8_t *sOut = sD + WG_STAGES * OP_BYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sOut + NUM_EPI_WARPS * OUT_BYTES);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sD + WG_STAGES * OP_BYTES);
     uint64_t *full = bars;
     uint64_t *empty = bars + WG_STAGES;
     uint64_t *acc_full = bars + 2 * WG_STAGES;
     uint64_t *acc_empty = bars + 2 * WG_STAGES + 2;
     uint64_t *mma_done = bars + 2 * WG_STAGES + 4;
     uint64_t *landed = bars + 2 * WG_STAGES + 5;     // a group's last block, in this CTA
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 2 * WG_STAGES + 6);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 3 * WG_STAGES + 5);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    int *start = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + 256);
+    int *start = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + BAR_BYTES);
     int *first = start + MAX_GROUPS + 1;
 
     const int warp = threadIdx.x >> 5;
@@ -170,15 +118,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int s = 0; s < WG_STAGES; ++s) {
-            mbar_init(smem_u32(&full[s]), 2);        // the loading warps of both CTAs
+            mbar_init(smem_u32(&full[s]), 2);        // a thread of each CTA
             mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&landed[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&acc_full[b]), 1);
             mbar_init(smem_u32(&acc_empty[b]), 2 * NUM_EPI_WARPS);
         }
         mbar_init(smem_u32(mma_done), 1);
-        mbar_init(smem_u32(landed), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -197,80 +145,58 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        int stage = 0;
-        uint32_t phase = 0;
-        uint32_t armed = 0, armed_parity = 0;
-        uint32_t landed_phase = 0;
-        bool ok = true;
-        for (int u = u0; u < units && ok; u += du) {
-            const WgradTile t = wgrad_tile(p, start, u);
-            const int ka = t.kb * 256 + (int)rank * 128;
-            const int nd = t.nb * 256 + (int)rank * 128;
-            const int blocks = ceil_div(t.rows, 64);
-            for (int b = 0; b < blocks; ++b) {
-                const int left = t.rows - b * 64;            // rows of the group from here on
-                const bool ends = left < 64 && (left & 15) != 0;
-                bool got = true;
-                const uint32_t full_leader = mapa_shared(smem_u32(&full[stage]), 0);
-                const uint32_t a_dst = smem_u32(sA + stage * OP_BYTES);
-                const uint32_t d_dst = smem_u32(sD + stage * OP_BYTES);
-                if (lane == 0) {
-                    got = wait_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.err);
-                    if (got) {
-                        uint32_t bar = full_leader;
-                        if (ends) {
-                            bar = smem_u32(landed);
-                            mbar_arrive_expect_tx(bar, 2 * OP_BYTES);
-                        } else if (leader) {
-                            mbar_arrive_expect_tx(smem_u32(&full[stage]), 4 * OP_BYTES);
-                        } else {
-                            mbar_arrive_cluster(full_leader);
-                        }
-                        armed |= 1u << stage;
-                        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                        const int row = t.row0 + b * 64;
-                        if (p.a_3d) {
-                            tma_load_3d_pair(a_dst, &maps.a, bar, 0, row, ka / 64);
-                        } else {
-                            tma_load_2d_pair(a_dst, &maps.a, bar, ka, row);
-                            tma_load_2d_pair(a_dst + 8192, &maps.a, bar, ka + 64, row);
-                        }
-                        if (p.d_3d) {
-                            tma_load_3d_pair(d_dst, &maps.d, bar, 0, row, nd / 64);
-                        } else {
-                            tma_load_2d_pair(d_dst, &maps.d, bar, nd, row);
-                            tma_load_2d_pair(d_dst + 8192, &maps.d, bar, nd + 64, row);
-                        }
-                        if (ends) got = wait_bounded(bar, landed_phase, abort_flag, p.err);
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t armed = 0, armed_parity = 0;
+            bool ok = true;
+            for (int u = u0; u < units && ok; u += du) {
+                const WgradTile t = wgrad_tile(p, start, u);
+                const int ka = t.kb * 256 + (int)rank * 128;
+                const int nd = t.nb * 256 + (int)rank * 128;
+                const int blocks = ceil_div(t.rows, 64);
+                for (int b = 0; b < blocks; ++b) {
+                    if (!wait_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.err)) {
+                        ok = false;
+                        break;
                     }
-                }
-                got = __all_sync(0xffffffffu, got);
-                if (!got) {
-                    ok = false;
-                    break;
-                }
-                if (ends) {
-                    landed_phase ^= 1;
-                    // rows [left, left rounded up to 16) of the four 64-column atoms
-                    const uint32_t zero0 = (uint32_t)left * 128, zero1 = (uint32_t)((left + 15) & ~15) * 128;
-                    for (uint32_t o = zero0 + lane * 16; o < zero1; o += 512) {
-                        st_shared_v4(a_dst + o, make_uint4(0, 0, 0, 0));
-                        st_shared_v4(a_dst + 8192 + o, make_uint4(0, 0, 0, 0));
-                        st_shared_v4(d_dst + o, make_uint4(0, 0, 0, 0));
-                        st_shared_v4(d_dst + 8192 + o, make_uint4(0, 0, 0, 0));
+                    // Both CTAs' bytes and one arrival of each complete the
+                    // leader's barrier.  A block in which the group ends lands on
+                    // a barrier of this CTA instead; the fixing warp arrives for it.
+                    const uint32_t fb = smem_u32(&full[stage]);
+                    uint32_t bar = mapa_shared(fb, 0);
+                    if (ends_inside(t.rows - b * 64)) {
+                        bar = smem_u32(&landed[stage]);
+                        mbar_arrive_expect_tx(bar, 2 * OP_BYTES);
+                    } else if (leader) {
+                        mbar_arrive_expect_tx(fb, 4 * OP_BYTES);
+                    } else {
+                        mbar_arrive_remote_tmem(bar);            // nothing to release
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(full_leader);
-                }
-                if (++stage == WG_STAGES) {
-                    stage = 0;
-                    phase ^= 1;
+                    armed |= 1u << stage;
+                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                    const uint32_t a_dst = smem_u32(sA + stage * OP_BYTES);
+                    const uint32_t d_dst = smem_u32(sD + stage * OP_BYTES);
+                    const int row = t.row0 + b * 64;
+                    if (p.a_3d) {
+                        tma_load_3d_pair(a_dst, &maps.a, bar, 0, row, ka / 64);
+                    } else {
+                        tma_load_2d_pair(a_dst, &maps.a, bar, ka, row);
+                        tma_load_2d_pair(a_dst + 8192, &maps.a, bar, ka + 64, row);
+                    }
+                    if (p.d_3d) {
+                        tma_load_3d_pair(d_dst, &maps.d, bar, 0, row, nd / 64);
+                    } else {
+                        tma_load_2d_pair(d_dst, &maps.d, bar, nd, row);
+                        tma_load_2d_pair(d_dst + 8192, &maps.d, bar, nd + 64, row);
+                    }
+                    if (++stage == WG_STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
             }
-        }
-        // Never leave with loads in flight into this CTA's shared memory.
-        if (lane == 0) {
+            // Never leave with loads in flight into this CTA's shared memory.
             if (leader) {
                 for (int s = 0; s < WG_STAGES; ++s)
                     if (armed & (1u << s))
@@ -283,6 +209,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
         }
         __syncwarp();
+    } else if (warp == FIX_WARP) {
+        // ------------------------------------------------------------ foreign rows
+        int stage = 0;
+        uint32_t phases = 0;                             // next parity of each landed[]
+        bool ok = true;
+        for (int u = u0; u < units && ok; u += du) {
+            const WgradTile t = wgrad_tile(p, start, u);
+            const int blocks = ceil_div(t.rows, 64);
+            if (ends_inside(t.rows - (blocks - 1) * 64) && blocks > 0) {
+                const int left = t.rows - (blocks - 1) * 64;
+                const int s = (stage + blocks - 1) % WG_STAGES;
+                ok = wait_bounded(smem_u32(&landed[s]), (phases >> s) & 1, abort_flag, p.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                phases ^= 1u << s;
+                // rows [left, left rounded up to 16) of the four 64-column atoms
+                const uint32_t a_dst = smem_u32(sA + s * OP_BYTES);
+                const uint32_t d_dst = smem_u32(sD + s * OP_BYTES);
+                const uint32_t end = (uint32_t)((left + 15) & ~15) * 128;
+                for (uint32_t o = (uint32_t)left * 128 + lane * 16; o < end; o += 512) {
+                    st_shared_v4(a_dst + o, make_uint4(0, 0, 0, 0));
+                    st_shared_v4(a_dst + 8192 + o, make_uint4(0, 0, 0, 0));
+                    st_shared_v4(d_dst + o, make_uint4(0, 0, 0, 0));
+                    st_shared_v4(d_dst + 8192 + o, make_uint4(0, 0, 0, 0));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
+            }
+            stage = (stage + blocks) % WG_STAGES;
+        }
+        __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0 && leader) {
@@ -290,6 +248,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t phase = 0;
             bool ok = true;
             int n = 0;                                   // tiles with rows so far
+            // K-step kk of a stage is 16 rows (2048 bytes) further in each atom
+            const uint64_t a_desc = smem_desc(smem_u32(sA), 8192, 1024);
+            const uint64_t d_desc = smem_desc(smem_u32(sD), 8192, 1024);
             for (int u = u0; u < units && ok; u += du) {
                 const WgradTile t = wgrad_tile(p, start, u);
                 if (t.rows == 0) continue;
@@ -301,23 +262,41 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 ++n;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * 256;
-                const int blocks = ceil_div(t.rows, 64);
+                const int blocks = t.rows / 64, left = t.rows % 64;
+                uint32_t accum = 0;
+                // Whole blocks first: this loop issues one MMA per 128 cycles
+                // from one thread, and tests in it show in the time.
                 for (int b = 0; b < blocks; ++b) {
                     if (!wait_bounded(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
-                    fence_acquire_cluster();             // the peer's zeros, if any
                     tc_fence_after();
-                    const int steps = min(4, ceil_div(t.rows - b * 64, 16));
-                    const uint32_t a_base = smem_u32(sA + stage * OP_BYTES);
-                    const uint32_t d_base = smem_u32(sD + stage * OP_BYTES);
+                    const uint64_t ad = a_desc + (uint64_t)(stage * (OP_BYTES >> 4));
+                    const uint64_t dd = d_desc + (uint64_t)(stage * (OP_BYTES >> 4));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        if (kk >= steps) break;
-                        tc_mma_f16_pair(d_tmem, smem_desc(a_base + kk * 2048, 8192, 1024),
-                                        smem_desc(d_base + kk * 2048, 8192, 1024), p.idesc,
-                                        (b > 0 || kk > 0) ? 1u : 0u);
+                        tc_mma_f16_pair(d_tmem, ad + kk * 128, dd + kk * 128, p.idesc, accum);
+                        accum = 1;
+                    }
+                    tc_commit_pair(smem_u32(&empty[stage]));
+                    if (++stage == WG_STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (ok && left > 0) {
+                    if (!wait_bounded(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    if (ends_inside(left)) mbar_try_wait_cluster(smem_u32(&full[stage]), phase);
+                    tc_fence_after();
+                    const uint64_t ad = a_desc + (uint64_t)(stage * (OP_BYTES >> 4));
+                    const uint64_t dd = d_desc + (uint64_t)(stage * (OP_BYTES >> 4));
+                    for (int kk = 0; kk < ceil_div(left, 16); ++kk) {
+                        tc_mma_f16_pair(d_tmem, ad + kk * 128, dd + kk * 128, p.idesc, accum);
+                        accum = 1;
                     }
                     tc_commit_pair(smem_u32(&empty[stage]));
                     if (++stage == WG_STAGES) {
@@ -334,9 +313,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue
+        // Each lane holds 32 consecutive columns of its row of C and stores them
+        // itself: the main loop takes most of the shared-memory bandwidth, and
+        // passing the results through it cost a quarter of the time.
         const int q = warp & 3;
         const int h = (warp - EPI_WARP0) / 4;
-        const uint32_t buf = smem_u32(sOut + (warp - EPI_WARP0) * OUT_BYTES);
+        const int row = q * 32 + lane;
+        TileParams tp{};
+        tp.alpha = p.alpha;
+        tp.beta = p.beta;
+        tp.D = p.C;
+        tp.out_kind = p.out_kind;
         int n = 0;
         for (int u = u0; u < units; u += du) {
             const WgradTile t = wgrad_tile(p, start, u);
@@ -348,12 +335,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 tc_fence_after();
             }
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-            const int k0 = t.kb * 256 + (int)rank * 128 + q * 32;
+            const int k = t.kb * 256 + (int)rank * 128 + row;
+            const long long out = (long long)t.g * p.strideC + (long long)k * p.ldc;
+            uint32_t r[32];
 #pragma unroll 1
-            for (int c = h; c < 8; c += 2) {
+            for (int c = h * 4; c < h * 4 + 4; ++c) {
                 const int col = t.nb * 256 + c * 32;
-                if (k0 >= p.K || col >= p.N) break;
-                uint32_t r[32];
+                if (k - lane >= p.K || col >= p.N) break;        // the whole warp
                 if (t.rows > 0) {
                     tmem_ld_32cols(t_row + c * 32, r);
                     tmem_ld_wait(r);
@@ -361,7 +349,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = 0;
                 }
-                wgrad_emit(p, r, t.g, k0, col, buf, lane);
+                if (k < p.K) {
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                    store_row_chunk(tp, out + col, v, min(32, p.N - col));
+                }
             }
             if (t.rows > 0) {
                 ++n;
@@ -417,7 +410,7 @@ cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, 
     mapped = M == 0 || (encode(&m.a, a.A, K, a.lda, p.a_3d) && encode(&m.d, a.D, N, a.ldd, p.d_3d));
     if (!mapped) return cudaErrorInvalidValue;
     const long long units = (long long)a.groups.G * p.k_tiles * p.n_tiles;
-    return launch_pairs<wgrad_kernel>(SMEM_BYTES, units, sms, s, m, p);
+    return launch_pairs<wgrad_kernel, WG_THREADS>(SMEM_BYTES, units, sms, s, m, p);
 }
 
 }  // namespace swg
