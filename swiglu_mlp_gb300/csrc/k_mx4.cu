@@ -1,4 +1,13 @@
 // k_mx4.cu — microscaled 4-bit floating point: to 4 bits and back.
+//
+// Both directions stream: 2 bytes (16-bit x) and 1/2 + 1/32 or 1/16 bytes per
+// element, each once, so memory bounds them.  A CTA takes 128 rows x 256
+// columns -- whole scale tiles -- and a warp one row of that at a time: 8
+// columns per lane, one 16-byte access of x and 4 bytes of codes, eight rows
+// in flight.  A block's largest magnitude meets across its 4 (MXFP4) or 2
+// (NVFP4) lanes.  The scale bytes pass through shared memory, because in
+// memory the tile's rows r, r + 32, r + 64, r + 96 lie side by side; they are
+// stored as one run of 1 or 2 KB.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -6,148 +15,304 @@
 
 #include "experts_launch.h"
 #include "groups.cuh"
+#include "launch.h"
 #include "tc_gemm.cuh"
 
 namespace swg {
 namespace {
 
 constexpr int TILE_ROWS = 128;       // rows of a scale tile
+constexpr int TILE_COLS = 256;       // columns per CTA: 2 (MXFP4) or 4 (NVFP4) scale tiles
 constexpr int THREADS = 256;
+constexpr int ROWS_PER_WARP = TILE_ROWS / (THREADS / 32);
+constexpr int BATCH = 8;             // rows whose loads are in flight together
 
-__device__ __forceinline__ float load_f32(const void *x, long long i, int type)
-{
-    if (type == 2) return static_cast<const float *>(x)[i];
-    if (type == 1) return __bfloat162float(static_cast<const __nv_bfloat16 *>(x)[i]);
-    return __half2float(static_cast<const __half *>(x)[i]);
-}
+template <int TYPE> struct Elem;
+template <> struct Elem<0> { using T = __half; };
+template <> struct Elem<1> { using T = __nv_bfloat16; };
+template <> struct Elem<2> { using T = float; };
 
-__device__ __forceinline__ void store_f32(void *x, long long i, float v, int type)
-{
-    if (type == 2)
-        static_cast<float *>(x)[i] = v;
-    else if (type == 1)
-        static_cast<__nv_bfloat16 *>(x)[i] = __float2bfloat16_rn(v);
-    else
-        static_cast<__half *>(x)[i] = __float2half_rn(v);
-}
+// 8 columns of a row as they are stored; those from `cnt` on are zero and not
+// read.
+template <int TYPE> struct Raw8 {
+    uint4 w[TYPE == 2 ? 2 : 1];
+};
 
-// The scale of a block whose largest magnitude is `top`: its byte and value.
-__device__ __forceinline__ uint32_t block_scale(bool nv, float top, float &scale)
+template <int TYPE>
+__device__ __forceinline__ Raw8<TYPE> load8(const void *x, long long i, int cnt)
 {
-    if (nv) {
-        if (!(top <= 3.402823466e38f)) {                 // NaN or infinity
-            scale = __int_as_float(0x7fffffff);
-            return 0x7fu;
+    using T = typename Elem<TYPE>::T;
+    const T *src = static_cast<const T *>(x) + i;
+    Raw8<TYPE> r;
+    if (cnt == 8) {
+        r.w[0] = reinterpret_cast<const uint4 *>(src)[0];
+        if (TYPE == 2) r.w[TYPE == 2] = reinterpret_cast<const uint4 *>(src)[1];
+    } else {
+        uint32_t u[TYPE == 2 ? 8 : 4] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j >= cnt) continue;
+            if (TYPE == 2)
+                u[j % (TYPE == 2 ? 8 : 4)] = reinterpret_cast<const uint32_t *>(src)[j];
+            else
+                u[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(src)[j] << (16 * (j & 1));
         }
-        const float s = fminf(__fdiv_rn(top, 6.0f), 448.0f);
-        uint32_t code = __nv_cvt_float_to_fp8(s, __NV_SATFINITE, __NV_E4M3);
-        if (code == 0) code = 1;                         // at least 2^-9
-        scale = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
-        return code;
+#pragma unroll
+        for (int h = 0; h < (TYPE == 2 ? 2 : 1); ++h)
+            r.w[h] = make_uint4(u[4 * h], u[4 * h + 1], u[4 * h + 2], u[4 * h + 3]);
     }
-    const int e = (__float_as_int(top) >> 23) & 0xff;    // exponent field of |x|
-    if (e == 255) {
-        scale = __int_as_float(0x7fffffff);
-        return 0xffu;
-    }
-    const uint32_t code = e > 2 ? e - 2 : 0;             // 2^(floor(log2 top) - 2)
-    scale = __int_as_float(code > 0 ? code << 23 : 1 << 22);
-    return code;
+    return r;
 }
 
-// One thread per block of one row.
-__global__ void __launch_bounds__(THREADS)
-    quantize_kernel(Mx4Args p, int *err)
+template <int TYPE>
+__device__ __forceinline__ void to_floats(const Raw8<TYPE> &r, float (&v)[8])
 {
-    extern __shared__ int table[];
-    int *start = table, *first = table + p.groups.G + 1;
-    const bool nv = p.format == 1;
-    const int B = nv ? 16 : 32;
-    const int tiles_k = ceil_div(p.K, 4 * B);
-    if (threadIdx.x < 32)
-        group_table(p.groups, start, first, err,
-                    [](int rows) { return ceil_div(rows, TILE_ROWS); });
-    __syncthreads();
-    const int t = blockIdx.y;
-    if (t >= first[p.groups.G]) return;
-    const int g = group_of(first, p.groups.G, t);
-    const int row0 = start[g] + (t - first[g]) * TILE_ROWS;
-    for (int u = threadIdx.x; u < TILE_ROWS * 4; u += THREADS) {
-        const int r = u >> 2, b = u & 3;
-        const int row = row0 + r;
-        const int k0 = (blockIdx.x * 4 + b) * B;
-        uint32_t code = 0;
-        if (row < start[g + 1] && k0 < p.K) {
-            float top = 0.0f, scale;
-            bool nan = false;
-            for (int i = 0; i < B && k0 + i < p.K; ++i) {
-                const float v = fabsf(p.scale * load_f32(p.X, (long long)row * p.ldx + k0 + i, p.type));
-                nan = nan || v != v;
-                top = fmaxf(top, v);
+#pragma unroll
+    for (int h = 0; h < (TYPE == 2 ? 2 : 1); ++h) {
+        const uint32_t u[4] = {r.w[h].x, r.w[h].y, r.w[h].z, r.w[h].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (TYPE == 2) {
+                v[4 * h + j] = __uint_as_float(u[j]);
+            } else {
+                const float2 f = TYPE == 1
+                                     ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[j]))
+                                     : __half22float2(*reinterpret_cast<const __half2 *>(&u[j]));
+                v[2 * j] = f.x;
+                v[2 * j + 1] = f.y;
             }
-            if (nan) top = __int_as_float(0x7fffffff);
-            code = block_scale(nv, top, scale);
-            uint8_t *q = p.Q + (long long)row * p.ldq + k0 / 2;
-            for (int i = 0; i < B; i += 2) {
-                float v[2];
-                for (int j = 0; j < 2; ++j)
-                    v[j] = k0 + i + j < p.K
-                               ? __fdiv_rn(p.scale * load_f32(p.X, (long long)row * p.ldx + k0 + i + j, p.type), scale)
-                               : 0.0f;
-                q[i / 2] = __nv_cvt_float2_to_fp4x2(make_float2(v[0], v[1]), __NV_E2M1, cudaRoundNearest);
-            }
-            // NVFP4: the codes up to a multiple of 32 columns are zero too
-            if (nv && k0 + 16 >= p.K && (k0 & 31) == 0)
-                for (int i = 8; i < 16; ++i) q[i] = 0;
         }
-        p.S[((long long)t * tiles_k + blockIdx.x) * 512 + 16 * (r & 31) + 4 * (r >> 5) + b] =
-            (uint8_t)code;
     }
 }
 
-__global__ void __launch_bounds__(THREADS)
-    dequantize_kernel(Mx4Args p, int *err)
+template <int TYPE>
+__device__ __forceinline__ void store8(void *x, long long i, int cnt, const float (&v)[8])
 {
-    extern __shared__ int table[];
-    int *start = table, *first = table + p.groups.G + 1;
-    const bool nv = p.format == 1;
-    const int B = nv ? 16 : 32;
-    const int tiles_k = ceil_div(p.K, 4 * B);
+    using T = typename Elem<TYPE>::T;
+    T *dst = static_cast<T *>(x) + i;
+    if (cnt == 8 && TYPE == 2) {
+        reinterpret_cast<float4 *>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else if (cnt == 8) {
+        constexpr int kind = TYPE == 1 ? OUT_BF16 : OUT_F16;
+        *reinterpret_cast<uint4 *>(dst) =
+            make_uint4(pack2(v[0], v[1], kind), pack2(v[2], v[3], kind), pack2(v[4], v[5], kind),
+                       pack2(v[6], v[7], kind));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < cnt) dst[j] = T(v[j]);
+    }
+}
+
+// The larger of two magnitudes; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The scale of a block whose largest magnitude is `top` (NaN if the block has
+// one): its byte; `scale` its value and `inverse` 1 / scale, both NaN for a
+// block with a NaN or an infinity.
+template <bool NV>
+__device__ __forceinline__ uint32_t block_scale(float top, float &scale, float &inverse)
+{
+    const uint32_t bits = __float_as_uint(top) & 0x7fffffffu;
+    const float nan = __uint_as_float(0x7fffffffu);
+    if (NV) {
+        // to nearest even by the conversion, which saturates at 448
+        const uint32_t code = max(
+            (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(top, 6.0f), __NV_SATFINITE, __NV_E4M3), 1u);
+        const bool bad = bits >= 0x7f800000u;
+        scale = bad ? nan
+                    : __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
+        inverse = __frcp_rn(scale);
+        return bad ? 0x7fu : code;
+    }
+    const uint32_t e = bits >> 23;                   // floor(log2 top) + 127
+    const uint32_t code = e > 2 ? e - 2 : 0;
+    const bool bad = e == 255;
+    scale = bad ? nan : __uint_as_float(code > 0 ? code << 23 : 1u << 22);
+    inverse = bad ? nan : __uint_as_float((254u - code) << 23);       // 2^(127 - code), exact
+    return bad ? 0xffu : code;
+}
+
+struct RowTile {
+    int g, row0, end, t;     // group, first row, end of the group, row of scale tiles
+};
+
+// Finds the CTA's rows; false for a CTA beyond the last group's tiles.
+__device__ __forceinline__ bool find_rows(const Groups &gr, int t, int *err, int *table, RowTile &r)
+{
+    int *start = table, *first = table + gr.G + 1;
     if (threadIdx.x < 32)
-        group_table(p.groups, start, first, err,
-                    [](int rows) { return ceil_div(rows, TILE_ROWS); });
+        group_table(gr, start, first, err, [](int rows) { return ceil_div(rows, TILE_ROWS); });
     __syncthreads();
-    const int t = blockIdx.y;
-    if (t >= first[p.groups.G]) return;
-    const int g = group_of(first, p.groups.G, t);
-    const int row0 = start[g] + (t - first[g]) * TILE_ROWS;
-    for (int u = threadIdx.x; u < TILE_ROWS * 4; u += THREADS) {
-        const int r = u >> 2, b = u & 3;
-        const int row = row0 + r;
-        const int k0 = (blockIdx.x * 4 + b) * B;
-        if (row >= start[g + 1] || k0 >= p.K) continue;
-        const uint32_t code =
-            p.S[((long long)t * tiles_k + blockIdx.x) * 512 + 16 * (r & 31) + 4 * (r >> 5) + b];
-        const float s = mx4_scale_value(nv, code);
-        for (int i = 0; i < B && k0 + i < p.K; ++i) {
-            const uint32_t q = p.Q[(long long)row * p.ldq + (k0 + i) / 2] >> (4 * (i & 1));
-            store_f32(p.X, (long long)row * p.ldx + k0 + i, p.scale * (e2m1_value(q & 15) * s), p.type);
+    if (t >= first[gr.G]) return false;
+    r.g = group_of(first, gr.G, t);
+    r.row0 = start[r.g] + (t - first[r.g]) * TILE_ROWS;
+    r.end = start[r.g + 1];
+    r.t = t;
+    return true;
+}
+
+template <int TYPE, bool NV>
+__global__ void __launch_bounds__(THREADS) quantize_kernel(const Mx4Args p, int chunks, int *err)
+{
+    constexpr int LANES = NV ? 2 : 4;                // lanes per block
+    constexpr int TILES = NV ? 4 : 2;                // scale tiles per CTA along K
+    extern __shared__ int table[];
+    __shared__ __align__(16) uint8_t sc[TILES * 512];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int t = blockIdx.x / chunks, chunk = blockIdx.x - t * chunks;
+    RowTile rt;
+    if (!find_rows(p.groups, t, err, table, rt)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int k = chunk * TILE_COLS + lane * 8;
+    const int cnt = min(8, max(0, p.K - k));
+    const bool write = k < ((p.K + 31) & ~31);       // codes up to a multiple of 32 columns
+    const int b = lane / LANES;                      // block within the CTA's columns
+    uint8_t *const my = sc + (b >> 2) * 512 + (b & 3);
+#pragma unroll 1
+    for (int r0 = 0; r0 < ROWS_PER_WARP; r0 += BATCH) {
+        const int first = warp * ROWS_PER_WARP + r0;
+        if (rt.row0 + first >= rt.end) {             // no such rows: their scales are zero
+            if (lane % LANES == 0)
+                for (int i = 0; i < BATCH; ++i) {
+                    const int r = first + i;
+                    my[16 * (r & 31) + 4 * (r >> 5)] = 0;
+                }
+            continue;
+        }
+        Raw8<TYPE> raw[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int row = rt.row0 + first + i;
+            raw[i] = load8<TYPE>(p.X, (long long)row * p.ldx + k, row < rt.end ? cnt : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = first + i;
+            float v[8], top = 0.0f;
+            to_floats<TYPE>(raw[i], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] *= p.scale;
+                top = max_nan(top, fabsf(v[j]));
+            }
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            if (!NV) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            float s, inv;
+            uint32_t code = block_scale<NV>(top, s, inv);
+            uint32_t q = 0;
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                float a = v[j] * inv, c = v[j + 1] * inv;
+                if (NV) {
+                    // One residual correction (Markstein's): a quotient that is
+                    // itself a float -- every tie between two codes is, for
+                    // 16-bit x -- comes out exact, so ties go to even as in the
+                    // definition; a * inv alone may miss them by a rounding.
+                    a = __fmaf_rn(__fmaf_rn(-a, s, v[j]), inv, a);
+                    c = __fmaf_rn(__fmaf_rn(-c, s, v[j + 1]), inv, c);
+                }
+                q |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(a, c), __NV_E2M1, cudaRoundNearest)
+                     << (4 * j);
+            }
+            const int row = rt.row0 + r;
+            if (row < rt.end && write)
+                *reinterpret_cast<uint32_t *>(p.Q + (long long)row * p.ldq + k / 2) = q;
+            if (row >= rt.end || k - (lane % LANES) * 8 >= p.K) code = 0;
+            if (lane % LANES == 0) my[16 * (r & 31) + 4 * (r >> 5)] = (uint8_t)code;
         }
     }
+    __syncthreads();
+    const int tiles_k = ceil_div(p.K, NV ? 64 : 128);
+    const int have = min(TILES, tiles_k - chunk * TILES) * 32;         // 16-byte pieces
+    uint4 *out = reinterpret_cast<uint4 *>(p.S + ((long long)t * tiles_k + chunk * TILES) * 512);
+    for (int i = threadIdx.x; i < have; i += THREADS) out[i] = reinterpret_cast<const uint4 *>(sc)[i];
+}
+
+template <int TYPE, bool NV>
+__global__ void __launch_bounds__(THREADS) dequantize_kernel(const Mx4Args p, int chunks, int *err)
+{
+    constexpr int LANES = NV ? 2 : 4;
+    constexpr int TILES = NV ? 4 : 2;
+    extern __shared__ int table[];
+    __shared__ __align__(16) uint8_t sc[TILES * 512];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int t = blockIdx.x / chunks, chunk = blockIdx.x - t * chunks;
+    RowTile rt;
+    if (!find_rows(p.groups, t, err, table, rt)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int k = chunk * TILE_COLS + lane * 8;
+    const int cnt = min(8, max(0, p.K - k));
+    const int tiles_k = ceil_div(p.K, NV ? 64 : 128);
+    const int have = min(TILES, tiles_k - chunk * TILES) * 32;
+    const uint4 *in = reinterpret_cast<const uint4 *>(p.S + ((long long)t * tiles_k + chunk * TILES) * 512);
+    for (int i = threadIdx.x; i < have; i += THREADS) reinterpret_cast<uint4 *>(sc)[i] = in[i];
+    uint32_t q[ROWS_PER_WARP];
+#pragma unroll
+    for (int i = 0; i < ROWS_PER_WARP; ++i) {
+        const int row = rt.row0 + warp * ROWS_PER_WARP + i;
+        q[i] = 0;
+        if (row < rt.end && cnt > 0)
+            q[i] = *reinterpret_cast<const uint32_t *>(p.Q + (long long)row * p.ldq + k / 2);
+    }
+    __syncthreads();
+    const int b = lane / LANES;
+    const uint8_t *const my = sc + (b >> 2) * 512 + (b & 3);
+#pragma unroll
+    for (int i = 0; i < ROWS_PER_WARP; ++i) {
+        const int r = warp * ROWS_PER_WARP + i;
+        const int row = rt.row0 + r;
+        if (row >= rt.end || cnt == 0) continue;
+        const float s = mx4_scale_value(NV, my[16 * (r & 31) + 4 * (r >> 5)]);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2(
+                (__nv_fp4x2_storage_t)((q[i] >> (4 * j)) & 0xffu), __NV_E2M1));
+            const float2 f = __half22float2(h);
+            v[j] = p.scale * (f.x * s);
+            v[j + 1] = p.scale * (f.y * s);
+        }
+        store8<TYPE>(p.X, (long long)row * p.ldx + k, cnt, v);
+    }
+}
+
+template <int TYPE, bool NV>
+cudaError_t launch(const Mx4Args &p, bool back, int tile_rows, int *err, cudaStream_t s)
+{
+    const int chunks = (p.K + TILE_COLS - 1) / TILE_COLS;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)tile_rows * chunks));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = 2 * sizeof(int) * (p.groups.G + 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return back ? cudaLaunchKernelEx(&cfg, dequantize_kernel<TYPE, NV>, p, chunks, err)
+                : cudaLaunchKernelEx(&cfg, quantize_kernel<TYPE, NV>, p, chunks, err);
 }
 
 }  // namespace
 
 cudaError_t launch_mx4(const Mx4Args &p, bool back, int tile_rows, int *err, cudaStream_t s)
 {
-    const int B = p.format == 1 ? 16 : 32;
-    const dim3 grid((p.K + 4 * B - 1) / (4 * B), tile_rows);
-    const size_t smem = 2 * sizeof(int) * (p.groups.G + 1);
-    if (back)
-        dequantize_kernel<<<grid, THREADS, smem, s>>>(p, err);
-    else
-        quantize_kernel<<<grid, THREADS, smem, s>>>(p, err);
-    return cudaGetLastError();
+    const bool nv = p.format == 1;
+    if (p.type == 0)
+        return nv ? launch<0, true>(p, back, tile_rows, err, s) : launch<0, false>(p, back, tile_rows, err, s);
+    if (p.type == 1)
+        return nv ? launch<1, true>(p, back, tile_rows, err, s) : launch<1, false>(p, back, tile_rows, err, s);
+    return nv ? launch<2, true>(p, back, tile_rows, err, s) : launch<2, false>(p, back, tile_rows, err, s);
 }
 
 }  // namespace swg
