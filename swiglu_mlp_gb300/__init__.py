@@ -335,12 +335,18 @@ def shutdown() -> None:
 
 # ---------------------------------------------------------------- tensor helpers
 
+_dtype_table = None
+
+
 def _dtype_code(in_dtype, out_dtype) -> int:
-    import torch
-    table = {(torch.float16, torch.float32): F16_F32OUT, (torch.bfloat16, torch.bfloat16): BF16,
-             (torch.float16, torch.float16): F16, (torch.bfloat16, torch.float32): BF16_F32OUT}
+    global _dtype_table
+    if _dtype_table is None:
+        import torch
+        _dtype_table = {
+            (torch.float16, torch.float32): F16_F32OUT, (torch.bfloat16, torch.bfloat16): BF16,
+            (torch.float16, torch.float16): F16, (torch.bfloat16, torch.float32): BF16_F32OUT}
     try:
-        return table[(in_dtype, out_dtype)]
+        return _dtype_table[(in_dtype, out_dtype)]
     except KeyError:
         raise SwgError(3, f"gemm_into: unsupported dtypes {in_dtype} -> {out_dtype}") from None
 
@@ -394,105 +400,137 @@ def interleave_weights(W1, W2, stream=None):
 
 
 # ------------------------------------------------- tensor helpers, expert MLP
+#
+# These run once per call of operators that take a few microseconds on the
+# GPU, so each tensor's shape and strides are fetched once and the refusals'
+# messages are only built when one is raised.
+
+_torch = None
+
+
+def _fast():
+    """The library and torch, loaded on the first call."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _lib or load(), _torch
+
+
+def _refuse(where, why, status=1):
+    raise SwgError(status, f"{where}: {why}")
+
 
 def _groups(offsets, where):
-    """(device pointer or None, G) of an int32 CUDA offsets tensor, or of none."""
+    """(device pointer or None, G) of an int32 offsets tensor, or of none."""
     if offsets is None:
         return None, 1
-    import torch
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() \
-            or offsets.numel() < 1:
-        raise SwgError(1, f"{where}: offsets must be a contiguous 1-D int32 tensor of G + 1 values")
-    return offsets, offsets.numel() - 1
+    if offsets.dtype is not _torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 \
+            or not offsets.is_contiguous():
+        _refuse(where, "offsets must be a contiguous 1-D int32 tensor of G + 1 values")
+    return offsets.data_ptr(), offsets.numel() - 1
 
 
-def _matrices(t, name, where):
-    """(rows, columns, row stride, group stride) of a 3-D [G, rows, columns]
-    tensor, or of a 2-D one (one group)."""
-    if t.dim() not in (2, 3) or t.stride(-1) != 1:
-        raise SwgError(1, f"{where}: {name} must have unit column stride and 2 or 3 dimensions")
-    return t.shape[-2], t.shape[-1], t.stride(-2), t.stride(0) if t.dim() == 3 else 0
+def _matrices(t, name, where, G):
+    """(rows, columns, row stride, group stride) of a [G, rows, columns]
+    tensor, or with G = 1 also of a [rows, columns] one."""
+    shape, stride = t.shape, t.stride()
+    n = len(shape)
+    if n not in (2, 3) or stride[-1] != 1 or (shape[0] if n == 3 else 1) != G:
+        _refuse(where, f"{name} must hold one row-major matrix for each of {G} groups")
+    return shape[-2], shape[-1], stride[-2], stride[0] if n == 3 else 0
 
 
-def _contiguous(where, **tensors):
-    for name, t in tensors.items():
-        if not t.is_contiguous():
-            raise SwgError(1, f"{where}: {name} must be contiguous")
-
-
-def _of_type(where, dtype, **tensors):
-    for name, t in tensors.items():
-        if t.dtype != dtype:
-            raise SwgError(1, f"{where}: {name} must be {dtype}")
+def _matrix(t, name, where):
+    """(rows, columns, row stride) of a 2-D row-major tensor."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or stride[1] != 1:
+        _refuse(where, f"{name} must be a 2-D row-major tensor (unit column stride)")
+    return shape[0], shape[1], stride[0]
 
 
 def _type_code(dtype, where) -> int:
-    import torch
-    table = {torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
-    if dtype not in table:
-        raise SwgError(3, f"{where}: unsupported dtype {dtype}")
-    return table[dtype]
+    if dtype is _torch.bfloat16:
+        return TYPE_BF16
+    if dtype is _torch.float16:
+        return TYPE_F16
+    if dtype is _torch.float32:
+        return TYPE_F32
+    _refuse(where, f"unsupported dtype {dtype}", 3)
 
 
-def _group_count(where, G, t, name):
-    if (t.shape[0] if t.dim() == 3 else 1) != G:
-        raise SwgError(1, f"{where}: {name} must hold one matrix for each of {G} groups")
+def _plain(where, dtype, **tensors):
+    """Contiguous tensors of one type."""
+    for name, t in tensors.items():
+        if t.dtype is not dtype or not t.is_contiguous():
+            _refuse(where, f"{name} must be a contiguous {dtype} tensor")
 
 
 def gemm_grouped_into(C, A, B, offsets, transB=0, alpha=1.0, beta=0.0, stream=None):
     """C[M, N] <- alpha * A[M, K] op(B_g) + beta * C for the rows of each group;
     B is [G, K, N] (transB = 0) or [G, N, K], offsets int32 [G + 1] on the GPU."""
     w = "gemm_grouped_into"
+    lib, _ = _fast()
     off, G = _groups(offsets, w)
-    _group_count(w, G, B, "B")
-    rows, cols, ldb, stride = _matrices(B, "B", w)
+    rows, cols, ldb, stride = _matrices(B, "B", w, G)
     N, Kb = (rows, cols) if transB else (cols, rows)
-    M, K = A.shape
-    if Kb != K or tuple(C.shape) != (M, N) or A.dtype != B.dtype:
-        raise SwgError(1, f"{w}: inconsistent shapes or dtypes")
-    gemm_grouped(transB, G, M, N, K, alpha, A, _row_major_ld(A, "A"), B, ldb, stride, off, beta,
-                 C, _row_major_ld(C, "C"), _dtype_code(A.dtype, C.dtype), stream=stream)
+    M, K, lda = _matrix(A, "A", w)
+    Mc, Nc, ldc = _matrix(C, "C", w)
+    if Kb != K or Mc != M or Nc != N or A.dtype is not B.dtype:
+        _refuse(w, "inconsistent shapes or dtypes")
+    rc = lib.gemm_grouped(int(transB), G, M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(), ldb,
+                          stride, off, beta, C.data_ptr(), ldc, _dtype_code(A.dtype, C.dtype),
+                          _stream(stream))
+    if rc:
+        _check(rc, "gemm_grouped")
     return C
 
 
 def gemm_grouped_wgrad_into(C, A, D, offsets, alpha=1.0, beta=0.0, stream=None):
     """C[G, K, N] <- alpha * A_g^T D_g + beta * C_g from A[M, K] and D[M, N]."""
     w = "gemm_grouped_wgrad_into"
+    lib, _ = _fast()
     off, G = _groups(offsets, w)
-    _group_count(w, G, C, "C")
-    rows, cols, ldc, stride = _matrices(C, "C", w)
-    M, K = A.shape
-    N = D.shape[1]
-    if D.shape[0] != M or (rows, cols) != (K, N) or A.dtype != D.dtype:
-        raise SwgError(1, f"{w}: inconsistent shapes or dtypes")
-    gemm_grouped_wgrad(G, M, N, K, alpha, A, _row_major_ld(A, "A"), D, _row_major_ld(D, "D"), off,
-                       beta, C, ldc, stride, _dtype_code(A.dtype, C.dtype), stream=stream)
+    rows, cols, ldc, stride = _matrices(C, "C", w, G)
+    M, K, lda = _matrix(A, "A", w)
+    Md, N, ldd = _matrix(D, "D", w)
+    if Md != M or rows != K or cols != N or A.dtype is not D.dtype:
+        _refuse(w, "inconsistent shapes or dtypes")
+    rc = lib.gemm_grouped_wgrad(G, M, N, K, alpha, A.data_ptr(), lda, D.data_ptr(), ldd, off, beta,
+                                C.data_ptr(), ldc, stride, _dtype_code(A.dtype, C.dtype),
+                                _stream(stream))
+    if rc:
+        _check(rc, "gemm_grouped_wgrad")
     return C
 
 
-def _swiglu_shapes(w, A, W_fused, G, **outs):
-    import torch
-    _group_count(w, G, W_fused, "W_fused")
-    M, K = A.shape
-    N = W_fused.shape[-1] // 2
-    if W_fused.shape[-2] != K or W_fused.shape[-1] != 2 * N:
-        raise SwgError(1, f"{w}: inconsistent shapes")
-    for name, (t, cols) in outs.items():
-        if tuple(t.shape) != (M, cols * N):
-            raise SwgError(1, f"{w}: inconsistent shapes")
-        _contiguous(w, **{name: t})
-        _of_type(w, torch.bfloat16, **{name: t})
-    _contiguous(w, A=A, W_fused=W_fused)
-    _of_type(w, torch.bfloat16, A=A, W_fused=W_fused)
-    return M, N, K
+def _swiglu_shapes(w, A, W_fused, G, torch):
+    rows, cols, ldw, stride = _matrices(W_fused, "W_fused", w, G)
+    M, K, lda = _matrix(A, "A", w)
+    if rows != K or cols % 2:
+        _refuse(w, "inconsistent shapes")
+    _plain(w, torch.bfloat16, A=A, W_fused=W_fused)
+    return M, cols // 2, K
+
+
+def _output(w, name, t, rows, cols, dtype):
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.dtype is not dtype \
+            or not t.is_contiguous():
+        _refuse(w, f"{name} must be a contiguous [{rows}, {cols}] {dtype} tensor")
 
 
 def swiglu_grouped_into(Y, A, W_fused, offsets, stream=None):
     """Y[M, N] <- SiLU(A W1_g) (.) (A W2_g), W_fused [G, K, 2N] interleaved."""
     w = "swiglu_grouped_into"
+    lib, torch = _fast()
     off, G = _groups(offsets, w)
-    M, N, K = _swiglu_shapes(w, A, W_fused, G, Y=(Y, 1))
-    swiglu_grouped(A, W_fused, Y, off, G, M, N, K, stream=stream)
+    M, N, K = _swiglu_shapes(w, A, W_fused, G, torch)
+    _output(w, "Y", Y, M, N, torch.bfloat16)
+    rc = lib.swiglu_grouped(A.data_ptr(), W_fused.data_ptr(), Y.data_ptr(), off, G, M, N, K,
+                            _stream(stream))
+    if rc:
+        _check(rc, "swiglu_grouped")
     return Y
 
 
@@ -500,12 +538,17 @@ def swiglu_grouped_grad_into(dH, A, W_fused, dY, offsets, Y=None, stream=None):
     """dH[M, 2N] <- the gradient of swiglu_grouped in the interleaved Gate and
     Up, from dY[M, N]; Y, when given, receives swiglu_grouped's result."""
     w = "swiglu_grouped_grad_into"
+    lib, torch = _fast()
     off, G = _groups(offsets, w)
-    outs = {"dH": (dH, 2), "dY": (dY, 1)}
+    M, N, K = _swiglu_shapes(w, A, W_fused, G, torch)
+    _output(w, "dH", dH, M, 2 * N, torch.bfloat16)
+    _output(w, "dY", dY, M, N, torch.bfloat16)
     if Y is not None:
-        outs["Y"] = (Y, 1)
-    M, N, K = _swiglu_shapes(w, A, W_fused, G, **outs)
-    swiglu_grouped_grad(A, W_fused, dY, Y, dH, off, G, M, N, K, stream=stream)
+        _output(w, "Y", Y, M, N, torch.bfloat16)
+    rc = lib.swiglu_grouped_grad(A.data_ptr(), W_fused.data_ptr(), dY.data_ptr(), _ptr(Y),
+                                 dH.data_ptr(), off, G, M, N, K, _stream(stream))
+    if rc:
+        _check(rc, "swiglu_grouped_grad")
     return dH
 
 
@@ -516,86 +559,92 @@ def mx4_alloc(M, K, format, groups=1, device="cuda"):
             torch.empty(mx4_scale_bytes(format, groups, M, K), dtype=torch.uint8, device=device))
 
 
-def _mx4_scales(where, format, G, M, K, **tensors):
-    import torch
-    _contiguous(where, **tensors)
-    _of_type(where, torch.uint8, **tensors)
-    for name, t in tensors.items():
-        if t.numel() < mx4_scale_bytes(format, G, M, K):
-            raise SwgError(1, f"{where}: {name} is smaller than mx4_scale_bytes")
+def _mx4_rows(w, Q, S, format, G, M, K, torch):
+    """Row stride of the codes Q of an M x K matrix whose scale tiles are S."""
+    rows, width, ldq = _matrix(Q, "Q", w)
+    if rows != M or width < -(-K // 32) * 16 or Q.dtype is not torch.uint8:
+        _refuse(w, "Q must be M uint8 rows of at least 16 * ceil(K / 32) bytes")
+    block = 64 if format == NVFP4 else 128
+    if S.dtype is not torch.uint8 or not S.is_contiguous() \
+            or S.numel() < 512 * -(-K // block) * (M // 128 + G):
+        _refuse(w, "S must be contiguous uint8 scale tiles of mx4_scale_bytes")
+    return ldq
 
 
 def mx4_quantize_into(Q, S, X, format, scale=1.0, offsets=None, stream=None):
     """Q, S <- X[M, K] * scale in 4 bits (Q uint8 rows of codes, S scale tiles)."""
-    import torch
     w = "mx4_quantize_into"
+    lib, torch = _fast()
     off, G = _groups(offsets, w)
-    M, K = X.shape
-    _of_type(w, torch.uint8, Q=Q)
-    _mx4_scales(w, format, G, M, K, S=S)
-    if Q.dim() != 2 or Q.shape[0] != M or Q.shape[1] < -(-K // 32) * 16:
-        raise SwgError(1, f"{w}: Q must be M rows of at least 16 * ceil(K / 32) bytes")
-    mx4_quantize(format, G, M, K, X, _row_major_ld(X, "X"), _type_code(X.dtype, w), scale, off, Q,
-                 _row_major_ld(Q, "Q"), S, stream=stream)
+    M, K, ldx = _matrix(X, "X", w)
+    ldq = _mx4_rows(w, Q, S, format, G, M, K, torch)
+    rc = lib.mx4_quantize(format, G, M, K, X.data_ptr(), ldx, _type_code(X.dtype, w), scale, off,
+                          Q.data_ptr(), ldq, S.data_ptr(), _stream(stream))
+    if rc:
+        _check(rc, "mx4_quantize")
     return Q, S
 
 
 def mx4_dequantize_into(X, Q, S, format, scale=1.0, offsets=None, stream=None):
     """X[M, K] <- scale * the values of the 4-bit rows (Q, S)."""
-    import torch
     w = "mx4_dequantize_into"
+    lib, torch = _fast()
     off, G = _groups(offsets, w)
-    M, K = X.shape
-    _of_type(w, torch.uint8, Q=Q)
-    _mx4_scales(w, format, G, M, K, S=S)
-    if Q.dim() != 2 or Q.shape[0] != M or Q.shape[1] < -(-K // 32) * 16:
-        raise SwgError(1, f"{w}: Q must be M rows of at least 16 * ceil(K / 32) bytes")
-    mx4_dequantize(format, G, M, K, Q, _row_major_ld(Q, "Q"), S, scale, off, X,
-                   _row_major_ld(X, "X"), _type_code(X.dtype, w), stream=stream)
+    M, K, ldx = _matrix(X, "X", w)
+    ldq = _mx4_rows(w, Q, S, format, G, M, K, torch)
+    rc = lib.mx4_dequantize(format, G, M, K, Q.data_ptr(), ldq, S.data_ptr(), scale, off,
+                            X.data_ptr(), ldx, _type_code(X.dtype, w), _stream(stream))
+    if rc:
+        _check(rc, "mx4_dequantize")
     return X
 
 
-def _mx4_operands(w, format, G, Q, S, W, SW, K):
-    import torch
-    _of_type(w, torch.uint8, Q=Q, W=W)
-    _group_count(w, G, W, "W")
-    N, width, ldb, stride = _matrices(W, "W", w)
-    if Q.dim() != 2 or min(Q.shape[1], width) < -(-K // 32) * 16:
-        raise SwgError(1, f"{w}: rows of codes must have at least 16 * ceil(K / 32) bytes")
-    M = Q.shape[0]
-    _mx4_scales(w, format, G, M, K, S=S)
-    _contiguous(w, SW=SW)
-    _of_type(w, torch.uint8, SW=SW)
-    # one group of N rows fills ceil(N / 128) rows of tiles
-    if SW.numel() < G * mx4_scale_bytes(format, 0, -(-N // 128) * 128, K):
-        raise SwgError(1, f"{w}: SW is smaller than the weights' scale tiles")
-    return M, N, ldb, stride
+def _mx4_weights(w, W, SW, format, G, K, torch):
+    """(N, row stride, group stride) of weights W with scale tiles SW."""
+    N, width, ldb, stride = _matrices(W, "W", w, G)
+    if width < -(-K // 32) * 16 or W.dtype is not torch.uint8:
+        _refuse(w, "W must hold uint8 rows of at least 16 * ceil(K / 32) bytes")
+    block = 64 if format == NVFP4 else 128
+    if SW.dtype is not torch.uint8 or not SW.is_contiguous() \
+            or SW.numel() < 512 * -(-K // block) * -(-N // 128) * G:
+        _refuse(w, "SW must be the weights' contiguous uint8 scale tiles")
+    return N, ldb, stride
 
 
 def gemm_mx4_into(C, Q, S, W, SW, K, format, alpha=1.0, beta=0.0, offsets=None, stream=None):
     """C[M, N] <- alpha * A W_g^T + beta * C with 4-bit A = (Q, S) of K columns
     and weights (W [N, bytes] or [G, N, bytes], SW)."""
     w = "gemm_mx4_into"
+    lib, torch = _fast()
     off, G = _groups(offsets, w)
-    M, N, ldb, stride = _mx4_operands(w, format, G, Q, S, W, SW, K)
-    if tuple(C.shape) != (M, N):
-        raise SwgError(1, f"{w}: inconsistent shapes")
-    gemm_mx4(format, G, M, N, K, alpha, Q, _row_major_ld(Q, "Q"), S, W, ldb, stride, SW, off,
-             beta, C, _row_major_ld(C, "C"), _type_code(C.dtype, w), stream=stream)
+    M, Nc, ldc = _matrix(C, "C", w)
+    lda = _mx4_rows(w, Q, S, format, G, M, K, torch)
+    N, ldb, stride = _mx4_weights(w, W, SW, format, G, K, torch)
+    if Nc != N:
+        _refuse(w, "inconsistent shapes")
+    rc = lib.gemm_mx4(format, G, M, N, K, alpha, Q.data_ptr(), lda, S.data_ptr(), W.data_ptr(),
+                      ldb, stride, SW.data_ptr(), off, beta, C.data_ptr(), ldc,
+                      _type_code(C.dtype, w), _stream(stream))
+    if rc:
+        _check(rc, "gemm_mx4")
     return C
 
 
 def swiglu_mx4_into(Y, Q, S, W, SW, K, format, alpha=1.0, offsets=None, stream=None):
     """Y[M, N] <- SiLU(alpha A W1_g^T) (.) (alpha A W2_g^T), W [2N, bytes] or
     [G, 2N, bytes] with Gate in even and Up in odd rows."""
-    import torch
     w = "swiglu_mx4_into"
+    lib, torch = _fast()
     off, G = _groups(offsets, w)
-    M, N2, _, _ = _mx4_operands(w, format, G, Q, S, W, SW, K)
-    if tuple(Y.shape) != (M, N2 // 2) or N2 % 2 or \
-            Q.shape[1] != W.shape[-1] or Q.shape[1] != -(-K // 32) * 16:
-        raise SwgError(1, f"{w}: inconsistent shapes")
-    _contiguous(w, Y=Y, Q=Q, W=W)
-    _of_type(w, torch.bfloat16, Y=Y)
-    swiglu_mx4(format, Q, S, W, SW, Y, off, G, M, N2 // 2, K, alpha, stream=stream)
+    M = Q.shape[0]
+    lda = _mx4_rows(w, Q, S, format, G, M, K, torch)
+    N2, ldb, stride = _mx4_weights(w, W, SW, format, G, K, torch)
+    row = -(-K // 32) * 16
+    if N2 % 2 or (lda != row and M > 1) or ldb != row or (stride != N2 * row and G > 1):
+        _refuse(w, "Q and W must be contiguous rows of 16 * ceil(K / 32) bytes, W of 2N of them")
+    _output(w, "Y", Y, M, N2 // 2, torch.bfloat16)
+    rc = lib.swiglu_mx4(format, Q.data_ptr(), S.data_ptr(), W.data_ptr(), SW.data_ptr(),
+                        Y.data_ptr(), off, G, M, N2 // 2, K, alpha, _stream(stream))
+    if rc:
+        _check(rc, "swiglu_mx4")
     return Y

@@ -102,23 +102,23 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
         if (!p.w_mn) {
             const uint64_t dims[] = {(uint64_t)K, (uint64_t)N, (uint64_t)G}, st[] = {ldb, sb};
             const uint32_t box[] = {64, 128, 1};
-            ok = encode_tiled(&m.w, type, 3, a.B, dims, st, box, true);
+            ok = encode_tiled(&m.w, type, 3, a.B, dims, st, box, 128);
         } else if (N % 64 == 0) {
             // 64 columns at a time as their own dimension: one box of 64 x 64 x 2
             const uint64_t dims[] = {64, (uint64_t)K, (uint64_t)N / 64, (uint64_t)G};
             const uint64_t st[] = {ldb, 128, sb};
             const uint32_t box[] = {64, 64, 2, 1};
-            ok = encode_tiled(&m.w, type, 4, a.B, dims, st, box, true);
+            ok = encode_tiled(&m.w, type, 4, a.B, dims, st, box, 128);
             p.w_4d = 1;
         } else {
             const uint64_t dims[] = {(uint64_t)N, (uint64_t)K, (uint64_t)G}, st[] = {ldb, sb};
             const uint32_t box[] = {64, 64, 1};
-            ok = encode_tiled(&m.w, type, 3, a.B, dims, st, box, true);
+            ok = encode_tiled(&m.w, type, 3, a.B, dims, st, box, 128);
         }
         for (int i = 0; i < swg::TOKEN_BOXES && ok; ++i) {
             const uint64_t dims[] = {(uint64_t)K, (uint64_t)M}, st[] = {(uint64_t)a.lda * 2};
             const uint32_t box[] = {64, i == 0 ? tokens / 2u : 128u >> i};
-            ok = encode_tiled(&m.t[i], type, 2, a.A, dims, st, box, true);
+            ok = encode_tiled(&m.t[i], type, 2, a.A, dims, st, box, 128);
         }
     } else if (K > 0) {
         // kind::mxf4 and mxf4nvf4: E2M1 operands (7-9, 10-12: 1), scale type (23: 1 = E8M0,
@@ -128,11 +128,11 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
         const uint64_t sb = G > 1 ? (uint64_t)a.strideB : (uint64_t)a.ldb * N;
         const uint64_t wd[] = {row, (uint64_t)N, (uint64_t)G}, wst[] = {(uint64_t)a.ldb, sb};
         const uint32_t wbox[] = {128, 128, 1};
-        ok = encode_tiled(&m.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.B, wd, wst, wbox, true);
+        ok = encode_tiled(&m.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.B, wd, wst, wbox, 128);
         for (int i = 0; i < swg::TOKEN_BOXES && ok; ++i) {
             const uint64_t dims[] = {row, (uint64_t)M}, st[] = {(uint64_t)a.lda};
             const uint32_t box[] = {128, i == 0 ? tokens / 2u : 128u >> i};
-            ok = encode_tiled(&m.t[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.A, dims, st, box, true);
+            ok = encode_tiled(&m.t[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.A, dims, st, box, 128);
         }
         // Scale tiles as rows of 64-bit elements, one row per 128 rows of the
         // matrix: a box is one stage's tiles (1 KB or 2 KB) of one row, two for A
@@ -143,11 +143,28 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
         const uint64_t std_[] = {tiles, (uint64_t)(M / 128 + G)};
         const uint32_t per = nv ? 256u : 128u;
         const uint32_t swbox[] = {per, 1}, stbox[] = {per, 2};
-        ok = ok && encode_tiled(&m.sw, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, a.SB, swd, sst, swbox, false);
-        ok = ok && encode_tiled(&m.st, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, a.SA, std_, sst, stbox, false);
+        ok = ok && encode_tiled(&m.sw, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, a.SB, swd, sst, swbox, 0);
+        ok = ok && encode_tiled(&m.st, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, a.SA, std_, sst, stbox, 0);
+    }
+    // 16-bit outputs in boxes of 32 rows: 64 bytes (or 32, a SwiGLU output) wide.  TMA
+    // clips a row at 16-byte granules, so the columns must end on one.
+    auto out_map = [&](CUtensorMap *map, void *ptr, int64_t cols, int64_t ld, uint32_t width, int sw) {
+        const uint64_t dims[] = {(uint64_t)cols, (uint64_t)M}, st[] = {(uint64_t)ld * 2};
+        const uint32_t box[] = {width, 32};
+        return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, ptr, dims, st, box, sw);
+    };
+    if (epi == swg::GRP_STORE) {
+        p.tma_out = a.out_kind != swg::OUT_F32 && a.beta == 0.0f && N % 8 == 0 && M >= 32;
+        if (p.tma_out) ok = ok && out_map(&m.c, a.C, N, a.ldc, 32, 64);
+    } else {
+        p.tma_out = 1;
+        ok = ok && (epi == swg::GRP_SWIGLU ? out_map(&m.c, a.C, N / 2, a.ldc, 16, 0)
+                                           : out_map(&m.c, a.C, N, a.ldc, 32, 0));
+        if (a.Y) ok = ok && out_map(&m.y, a.Y, N / 2, N / 2, 16, 0);
     }
     if (!ok) return swg::record_cuda_error();
-    const long long units = (M / tokens + std::min(G, M)) * (long long)p.n_blocks;
+    // (tiles of as few as 128 rows may be chosen)
+    const long long units = (M / 128 + std::min(G, M)) * (long long)p.n_blocks;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return swg::count_launch(f4 ? swg::launch_grouped_f4(nv, epi, m, p, units, d.sms, s)
                                 : swg::launch_grouped_16(epi, m, p, units, d.sms, s));

@@ -88,6 +88,7 @@ struct GrpMaps {
     CUtensorMap w;                       // weights
     CUtensorMap t[TOKEN_BOXES];          // rows of A
     CUtensorMap sw, st;                  // scale tiles of both (4-bit)
+    CUtensorMap c, y;                    // 16-bit outputs, in boxes of 32 rows (tma_out)
 };
 
 struct GrpParams {
@@ -105,6 +106,7 @@ struct GrpParams {
     const void *dY;
     void *Y;
     int out_kind;
+    int tma_out;                         // whole chunks of 32 rows leave through TMA stores
     int *err;
 };
 
@@ -119,7 +121,7 @@ struct GrpCfg {
     static constexpr int W_BYTES = 128 * 128;
     static constexpr int T_BYTES = TOKENS / 2 * 128;
     static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + 3 * SCALE_BYTES;
-    static constexpr int OUT_BYTES = 3072;        // per epilogue warp, see grp_emit
+    static constexpr int OUT_BYTES = 3072;        // per epilogue warp, see the epilogue
     static constexpr int TABLE_BYTES = (F4 ? 3 : 2) * 4 * (MAX_GROUPS + 1) + 4;
     static constexpr int FIXED = 1024 + NUM_EPI_WARPS * OUT_BYTES + TABLE_BYTES + 512;
     static constexpr int STAGES_RAW = (232448 - FIXED) / STAGE_BYTES;
@@ -131,15 +133,57 @@ struct GrpCfg {
     static_assert(!F4 || 2 * TOKENS + 128 <= 512, "tensor memory");
 };
 
-// Rows of A covered by each tile of a group of `rows` (> 0) rows, but the last.
+// Rows of A covered by each tile of a group of `rows` (> 0) rows, but the
+// last, when tiles have at most `most` rows.
 template <int MATH>
-__device__ __forceinline__ int tile_step(int rows)
+__device__ __forceinline__ int tile_step(int rows, int most)
+{
+    const int t = ceil_div(rows, most);
+    // 4-bit: a tile begins at a multiple of 64 rows, two scale columns
+    const int unit = GrpCfg<MATH>::F4 ? 64 : 16;
+    return ceil_div(ceil_div(rows, t), unit) * unit;
+}
+
+// The most rows of A that a tile should have, chosen by one whole warp so that
+// the last wave of tiles is not nearly empty: of TOKENS, TOKENS - unit, .. the
+// one with the least  waves * (average rows per tile + 24).  A tile's time is
+// proportional to its rows (the MMA's N) down to about 64, plus a fixed part
+// worth some 24 rows.  994 tiles on 76 pairs are 13.1 waves at 256 rows; the
+// 1064 tiles of at most 240 rows make 14.0 of them and take 7% less.
+template <int MATH>
+__device__ __forceinline__ int choose_rows(const int *start, int G, int n_blocks, int pairs)
 {
     using C = GrpCfg<MATH>;
-    const int t = ceil_div(rows, C::TOKENS);
-    // 4-bit: a tile begins at a multiple of 64 rows, two scale columns
-    const int unit = C::F4 ? 64 : 16;
-    return ceil_div(ceil_div(rows, t), unit) * unit;
+    constexpr int UNIT = C::F4 ? 64 : 16;
+    constexpr int CANDS = C::F4 ? 2 : 8;            // down to 128 rows
+    const int lane = threadIdx.x & 31;
+    const int cand = lane % CANDS;
+    const int most = C::TOKENS - cand * UNIT;
+    int tiles = 0, rows = 0;
+    for (int g = lane / CANDS; g < G; g += 32 / CANDS) {
+        const int r = start[g + 1] - start[g];
+        tiles += ceil_div(r, most);
+        rows += r;
+    }
+#pragma unroll
+    for (int d = CANDS; d < 32; d <<= 1) {
+        tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+        rows += __shfl_xor_sync(0xffffffffu, rows, d);
+    }
+    const long long units = (long long)tiles * n_blocks;
+    const float waves = (float)((units + pairs - 1) / pairs);
+    float cost = tiles > 0 ? waves * (fmaxf((float)rows / (float)tiles, 64.0f) + 24.0f) : 0.0f;
+    int best = cand;
+#pragma unroll
+    for (int d = 1; d < CANDS; d <<= 1) {
+        const float c = __shfl_xor_sync(0xffffffffu, cost, d);
+        const int b = __shfl_xor_sync(0xffffffffu, best, d);
+        if (c < cost || (c == cost && b < best)) {
+            cost = c;
+            best = b;
+        }
+    }
+    return C::TOKENS - best * UNIT;
 }
 
 struct GrpTile {
@@ -153,7 +197,7 @@ struct GrpTile {
 // weight blocks together, so that concurrently running pairs share both in L2.
 template <int MATH>
 __device__ __forceinline__ GrpTile grp_tile(const int *start, const int *first, int G,
-                                            int n_blocks, int u)
+                                            int n_blocks, int most, int u)
 {
     GrpTile t;
     t.g = group_of(first, G, u / n_blocks);
@@ -171,7 +215,7 @@ __device__ __forceinline__ GrpTile grp_tile(const int *start, const int *first, 
         t.nb = in / bm;
         mb = band * 8 + in - t.nb * bm;
     }
-    const int step = tile_step<MATH>(rows);
+    const int step = tile_step<MATH>(rows, most);
     t.local = mb * step;
     t.row0 = start[t.g] + t.local;
     t.rows = min(step, rows - t.local);
@@ -231,46 +275,143 @@ __device__ __forceinline__ void copy_rows(uint32_t src, uint16_t *out, long long
     }
 }
 
-// 32 rows of A (from `row`, `rows` of them real) of the 32 accumulator rows
-// (columns n0 + lane of C) that this warp holds: acc[j] is row j's.  16-bit
-// results pass through `buf`, this warp's shared memory, to be stored as 16
-// bytes per lane.
-template <int EPI>
-__device__ __forceinline__ void grp_emit(const GrpParams &p, const uint32_t (&acc)[32],
-                                         const uint32_t (&dy)[16], int row, int rows, int n0,
-                                         uint32_t buf, int lane)
+// 16 lanes (from taddr's lane on) x 32 columns of the accumulator in fragments:
+// for each 8 columns i, r[4 i] and r[4 i + 1] are row lane / 4, columns
+// 2 (lane % 4) and + 1; r[4 i + 2] and r[4 i + 3] the same of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16])
 {
-    if (EPI == GRP_STORE) {
-        const int n = n0 + lane;
-        const bool in = n < p.N;
-        float v[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Four 8 x 8 matrices of 16-bit values, each stored transposed: matrix m's
+// row j of 16 bytes goes to the address that lane 8 m + j gives.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                  uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// The copy of 32 staged rows of 32 16-bit values in the 64-byte swizzle
+// (16-byte piece j of row r at j ^ (r / 2 mod 4)) to the first `rows` rows of
+// `out`, columns from `limit` on left out.
+__device__ __forceinline__ void copy_rows_swizzled(uint32_t src, uint16_t *out, long long ldo,
+                                                   int rows, int limit, int lane)
+{
+    const int j = lane & 3, c = j * 8;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(acc[j]);
+    for (int r = lane >> 2; r < 32; r += 8) {
+        if (r >= rows || c >= limit) continue;
+        const uint4 v = ld_shared_v4(src + (uint32_t)(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)));
+        uint16_t *dst = out + r * ldo + c;
+        if (c + 8 <= limit) {
+            *reinterpret_cast<uint4 *>(dst) = v;
+        } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < limit) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+        }
+    }
+}
+
+// Before this warp's staging memory is written again: the TMA stores that
+// lane 0 issued from it have read it.
+__device__ __forceinline__ void staging_free(int lane)
+{
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
+}
+
+// One chunk: the 32 columns n0 .. of C (this warp's lanes of the accumulator,
+// at taddr) by 32 rows of A from `row`, of which `rows` exist.  16-bit results
+// pass through `buf`, this warp's shared memory, where they are transposed:
+// whole chunks then leave through a TMA store, others 16 bytes per lane.  (The
+// main loop's operands take most of the shared-memory and L1 bandwidth, so
+// what the epilogue passes through them shows in the time: 2-byte shared and
+// row-wise global stores cost 5% of 8192 x 4096 x 4096.)
+__device__ __forceinline__ void emit_store_16(const GrpParams &p, const CUtensorMap *tm,
+                                              uint32_t taddr, int row, int rows, int n0,
+                                              uint32_t buf, int lane)
+{
+    uint32_t lo[16], hi[16];                        // lanes 0..15 and 16..31
+    tmem_ld_16x32(taddr, lo);
+    tmem_ld_16x32(taddr + (16u << 16), hi);
+    tmem_ld_wait(lo);
+    tmem_ld_wait(hi);
+    staging_free(lane);
+    const int m = lane >> 3, j8 = lane & 7;         // the 16 bytes that this lane addresses
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        auto pk = [&](const uint32_t(&r)[16], int k) {
+            return pack2(p.alpha * __uint_as_float(r[4 * i + k]),
+                         p.alpha * __uint_as_float(r[4 * i + k + 1]), p.out_kind);
+        };
+        const int r = 8 * i + j8;
+        stmatrix_x4_trans(buf + (uint32_t)(r * 64 + ((m ^ ((r >> 1) & 3)) << 4)), pk(lo, 0), pk(lo, 2),
+                          pk(hi, 0), pk(hi, 2));
+    }
+    if (p.tma_out && rows == 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(tm, buf, n0, row);
+            bulk_commit_group();
+        }
+    } else {
+        __syncwarp();
+        copy_rows_swizzled(buf, reinterpret_cast<uint16_t *>(p.C) + row * p.ldc + n0, p.ldc, rows,
+                           p.N - n0, lane);
+        __syncwarp();
+    }
+}
+
+// The same for FP32 results, with beta, and for K = 0 (no accumulator): each
+// lane is a column, its stores (and loads of C) of one row are 64 or 128 bytes
+// a warp.
+__device__ __forceinline__ void emit_store_direct(const GrpParams &p, uint32_t taddr, int row,
+                                                  int rows, int n0, int lane)
+{
+    const int n = n0 + lane;
+#pragma unroll 1
+    for (int j0 = 0; j0 < rows; j0 += 16) {
+        uint32_t acc[16] = {};
+        if (p.k_blocks > 0) {
+            tmem_ld_16cols(taddr + j0, acc);
+            tmem_ld_wait(acc);
+        }
+        if (n >= p.N) continue;
+        const long long o = (row + j0) * p.ldc + n;
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = p.alpha * __uint_as_float(acc[j]);
         if (p.beta != 0.0f) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (in && j < rows)
-                    v[j] += p.beta * load_out(p.C, (row + j) * p.ldc + n, p.out_kind);
-        }
-        if (p.out_kind == OUT_F32) {
-            float *out = reinterpret_cast<float *>(p.C) + row * p.ldc + n;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (in && j < rows) out[j * p.ldc] = v[j];
-            return;
+            for (int j = 0; j < 16; ++j)
+                if (j0 + j < rows) v[j] += p.beta * load_out(p.C, o + j * p.ldc, p.out_kind);
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            st_shared_u16(buf + (uint32_t)(j * 32 + lane) * 2, to_16(v[j], p.out_kind));
-        __syncwarp();
-        copy_rows<32>(buf, reinterpret_cast<uint16_t *>(p.C) + row * p.ldc + n0, p.ldc, rows,
-                      p.N - n0, lane);
-        __syncwarp();
-        return;
+        for (int j = 0; j < 16; ++j)
+            if (j0 + j < rows) store_out(p.C, o + j * p.ldc, v[j], p.out_kind);
     }
-    // Lanes 2i and 2i + 1 hold Gate and Up of one output column.  They swap
-    // halves, so that the even lane has both for the even rows and the odd
-    // lane for the odd ones.
+}
+
+// SwiGLU and its gradient.  Lanes 2i and 2i + 1 hold Gate and Up of one output
+// column.  They swap halves, so that the even lane has both for the even rows
+// and the odd lane for the odd ones.
+template <int EPI>
+__device__ __forceinline__ void emit_swiglu(const GrpParams &p, const GrpMaps &maps,
+                                            const uint32_t (&acc)[32], const uint32_t (&dy)[16],
+                                            int row, int rows, int n0, uint32_t buf, int lane)
+{
+    staging_free(lane);
     const int odd = lane & 1;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -288,6 +429,20 @@ __device__ __forceinline__ void grp_emit(const GrpParams &p, const uint32_t (&ac
             st_shared_u32(buf + at * 4, pack2(d * u * (s + gs * (1.0f - s)), d * gs, OUT_BF16));
             if (p.Y) st_shared_u16(buf + 2048 + at * 2, to_16(gs * u, OUT_BF16));
         }
+    }
+    if (rows == 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (EPI == GRP_SWIGLU) {
+                tma_store_2d(&maps.c, buf, n0 / 2, row);
+            } else {
+                tma_store_2d(&maps.c, buf, n0, row);
+                if (p.Y) tma_store_2d(&maps.y, buf + 2048, n0 / 2, row);
+            }
+            bulk_commit_group();
+        }
+        return;
     }
     __syncwarp();
     if (EPI == GRP_SWIGLU) {
@@ -329,6 +484,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint64_t *mma_done = bars + 2 * S + 4;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 2 * S + 5);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    int *most_rows = reinterpret_cast<int *>(tmem_holder + 2);
     int *start = reinterpret_cast<int *>(sOut + NUM_EPI_WARPS * C::OUT_BYTES + 512 - 64);
     int *first = start + p.groups.G + 1;
     int *stile = first + p.groups.G + 1;          // rows of scale tiles before each group
@@ -359,28 +515,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 2) {
-        group_table(p.groups, start, first, p.err, [](int rows) { return ceil_div(rows, C::TOKENS); });
-        if (F4) {
-            if (lane == 0) stile[0] = 0;
-            int sum = 0;
-            for (int base = 0; base < p.groups.G; base += 32) {
-                const int i = base + lane;
-                int v = i < p.groups.G ? ceil_div(start[i + 1] - start[i], 128) : 0;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, v, d);
-                    if (lane >= d) v += o;
-                }
-                if (i < p.groups.G) stile[i + 1] = sum + v;
-                sum += __shfl_sync(0xffffffffu, v, 31);
-            }
-        }
+        group_starts(p.groups, start, p.err);
+        const int rows = choose_rows<MATH>(start, p.groups.G, p.n_blocks, (int)(gridDim.x >> 1));
+        tile_sums(p.groups.G, start, first, [rows](int n) { return ceil_div(n, rows); });
+        if (lane == 0) *most_rows = rows;
+        if (F4) tile_sums(p.groups.G, start, stile, [](int n) { return ceil_div(n, 128); });
     }
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
     const int G = p.groups.G;
+    const int most = *most_rows;
     const int units = first[G] * p.n_blocks;
     const int u0 = (int)(blockIdx.x >> 1), du = (int)(gridDim.x >> 1);
 
@@ -392,7 +538,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t armed = 0, armed_parity = 0;
             bool ok = true;
             for (int u = u0; u < units && ok; u += du) {
-                const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, u);
+                const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, most, u);
                 const int half = t.width / 2;
                 // the lowest box that holds this CTA's rows of A
                 int box = 0;
@@ -466,7 +612,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             bool ok = true;
             int n = 0;
             for (int u = u0; u < units && ok; u += du, ++n) {
-                const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, u);
+                const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, most, u);
                 const uint32_t idesc = p.idesc | ((uint32_t)(t.width >> 3) << 17);
                 const int acc = n & 1;
                 if (!wait_bounded(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, p.err)) {
@@ -542,7 +688,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t buf = smem_u32(sOut + (warp - EPI_WARP0) * C::OUT_BYTES);
         int n = 0;
         for (int u = u0; u < units; u += du, ++n) {
-            const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, u);
+            const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, most, u);
             const int acc = n & 1;
             const int n0 = t.nb * 256 + (int)rank * 128 + q * 32;
             const bool work = n0 < p.N;
@@ -570,6 +716,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * C::ACC_STRIDE;
 #pragma unroll 1
             for (int c = h; c < chunks && work; c += 2) {
+                const int row = t.row0 + c * 32, rows = min(32, t.rows - c * 32);
+                if (EPI == GRP_STORE) {
+                    if (p.out_kind != OUT_F32 && p.beta == 0.0f && p.k_blocks > 0)
+                        emit_store_16(p, &maps.c, t_row + c * 32, row, rows, n0, buf, lane);
+                    else
+                        emit_store_direct(p, t_row + c * 32, row, rows, n0, lane);
+                    continue;
+                }
                 uint32_t r[32];
                 if (p.k_blocks > 0) {
                     tmem_ld_32cols(t_row + c * 32, r);
@@ -578,7 +732,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = 0;
                 }
-                grp_emit<EPI>(p, r, dy, t.row0 + c * 32, min(32, t.rows - c * 32), n0, buf, lane);
+                emit_swiglu<EPI>(p, maps, r, dy, row, rows, n0, buf, lane);
                 if (c + 2 < chunks) load_dy(c + 2);
             }
             if (p.k_blocks > 0) {
@@ -587,6 +741,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (lane == 0) mbar_arrive_remote_tmem(mapa_shared(smem_u32(&acc_empty[acc]), 0));
             }
         }
+        staging_free(lane);                     // before this CTA's shared memory goes
     }
 
     // Neither CTA frees its tensor memory or exits while the leader's MMAs or

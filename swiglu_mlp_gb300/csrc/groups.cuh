@@ -11,24 +11,18 @@ constexpr int ERR_INVALID = 1;       // == SWG_ERR_INVALID_ARG
 // Run by one whole warp.  start[0..G]: the offsets, clamped to be
 // non-decreasing within [0, M], so that every row a kernel derives from them
 // exists; an offset that had to be clamped is reported in the error word.
-// first[0..G]: how many tiles the groups before g have, a group of `rows`
-// rows having tiles_of(rows).  The host keeps first[G] below 2^31.
-template <class F>
-__device__ __forceinline__ void group_table(const Groups &gr, int *start, int *first, int *err,
-                                            F tiles_of)
+__device__ __forceinline__ void group_starts(const Groups &gr, int *start, int *err)
 {
     const int lane = threadIdx.x & 31;
-    const int G = gr.G;
     if (gr.offsets == nullptr) {         // one group of all rows
         if (lane == 0) {
             start[0] = 0;
             start[1] = gr.M;
-            first[0] = 0;
-            first[1] = tiles_of(gr.M);
         }
         __syncwarp();
         return;
     }
+    const int G = gr.G;
     int top = 0;                         // the largest offset so far
     bool bad = false;
     for (int base = 0; base <= G; base += 32) {
@@ -49,6 +43,14 @@ __device__ __forceinline__ void group_table(const Groups &gr, int *start, int *f
     }
     if (bad) atomicCAS(err, 0, ERR_INVALID);
     __syncwarp();
+}
+
+// Run by one whole warp.  first[0..G]: how many tiles the groups before g
+// have, a group of `rows` rows having tiles_of(rows).
+template <class F>
+__device__ __forceinline__ void tile_sums(int G, const int *start, int *first, F tiles_of)
+{
+    const int lane = threadIdx.x & 31;
     int sum = 0;
     for (int base = 0; base < G; base += 32) {
         const int i = base + lane;

@@ -31,11 +31,10 @@ int count_launch(cudaError_t e);
 // have to allocate while the stream is being captured.
 int stream_workspace(cudaStream_t s, size_t bytes, float *&out);
 
-// cuTensorMapEncodeTiled with the 128-byte swizzle (or none), unit element
-// strides, no interleave and zero fill; false (recorded) when it fails.
-// strides[i] is the byte stride of dimension i + 1.
+// cuTensorMapEncodeTiled with a swizzle of 128, 64 or 0 (none) bytes, unit
+// element strides, no interleave and zero fill; false (recorded) when it
+// fails.  strides[i] is the byte stride of dimension i + 1.
 bool encode_tiled(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *ptr,
-                  const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
-                  bool swizzle128);
+                  const uint64_t *dims, const uint64_t *strides, const uint32_t *box, int swizzle);
 
 }  // namespace swg

@@ -147,8 +147,10 @@ struct RowTile {
 __device__ __forceinline__ bool find_rows(const Groups &gr, int t, int *err, int *table, RowTile &r)
 {
     int *start = table, *first = table + gr.G + 1;
-    if (threadIdx.x < 32)
-        group_table(gr, start, first, err, [](int rows) { return ceil_div(rows, TILE_ROWS); });
+    if (threadIdx.x < 32) {
+        group_starts(gr, start, err);
+        tile_sums(gr.G, start, first, [](int rows) { return ceil_div(rows, TILE_ROWS); });
+    }
     __syncthreads();
     if (t >= first[gr.G]) return false;
     r.g = group_of(first, gr.G, t);

@@ -22,6 +22,7 @@ namespace {
 
 struct WgradMaps {
     CUtensorMap a, d;
+    CUtensorMap c;                       // 16-bit output, in boxes of 32 x 32 (tma_out)
 };
 
 struct WgradParams {
@@ -34,6 +35,8 @@ struct WgradParams {
     void *C;
     long long ldc, strideC;
     int out_kind;
+    int staged;                          // 16-bit output, beta = 0: through shared memory
+    int tma_out;                         // ... and from there with TMA stores
     int *err;
 };
 
@@ -42,7 +45,9 @@ constexpr int FIX_WARP = EPI_WARP0 + NUM_EPI_WARPS;
 constexpr int WG_THREADS = NUM_THREADS + 32;
 constexpr int OP_BYTES = 128 * 128;      // 64 rows x 128 columns of one operand per CTA
 constexpr int BAR_BYTES = 512;
-constexpr int SMEM_BYTES = 1024 + WG_STAGES * 2 * OP_BYTES + BAR_BYTES + 2 * 4 * (MAX_GROUPS + 1);
+constexpr int OUT_BYTES = 2048;          // 32 x 32 16-bit results per epilogue warp
+constexpr int SMEM_BYTES = 1024 + WG_STAGES * 2 * OP_BYTES + NUM_EPI_WARPS * OUT_BYTES + BAR_BYTES +
+                           4 * (MAX_GROUPS + 1);
 static_assert(SMEM_BYTES <= 232448, "beyond the per-CTA shared memory");
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
@@ -98,7 +103,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *sA = smem;
     uint8_t *sD = sA + WG_STAGES * OP_BYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sD + WG_STAGES * OP_BYTES);
+    uint8_t *sOut = sD + WG_STAGES * OP_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sOut + NUM_EPI_WARPS * OUT_BYTES);
     uint64_t *full = bars;
     uint64_t *empty = bars + WG_STAGES;
     uint64_t *acc_full = bars + 2 * WG_STAGES;
@@ -108,7 +114,6 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 3 * WG_STAGES + 5);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *start = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + BAR_BYTES);
-    int *first = start + MAX_GROUPS + 1;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         tmem_relinquish_pair();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == 2) group_table(p.groups, start, first, p.err, [](int) { return 1; });
+    if (warp == 2) group_starts(p.groups, start, p.err);
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
@@ -313,12 +318,15 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue
-        // Each lane holds 32 consecutive columns of its row of C and stores them
-        // itself: the main loop takes most of the shared-memory bandwidth, and
-        // passing the results through it cost a quarter of the time.
+        // Each lane holds 32 consecutive columns of its row of C.  16-bit results
+        // pass through shared memory and leave 32 x 32 at a time with TMA stores
+        // (or, where a row does not end on 16 bytes, as 64-byte pieces of rows):
+        // stored by the lanes themselves they touch 32 lines per instruction, and
+        // the main loop, whose operands use the same memory, took a fifth longer.
         const int q = warp & 3;
         const int h = (warp - EPI_WARP0) / 4;
         const int row = q * 32 + lane;
+        const uint32_t buf = smem_u32(sOut + (warp - EPI_WARP0) * OUT_BYTES);
         TileParams tp{};
         tp.alpha = p.alpha;
         tp.beta = p.beta;
@@ -349,7 +357,34 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = 0;
                 }
-                if (k < p.K) {
+                if (p.staged) {
+                    staging_free(lane);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = pack2(p.alpha * __uint_as_float(r[8 * j + 2 * i]),
+                                         p.alpha * __uint_as_float(r[8 * j + 2 * i + 1]), p.out_kind);
+                        st_shared_v4(buf + (uint32_t)(lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)),
+                                     make_uint4(w[0], w[1], w[2], w[3]));
+                    }
+                    if (p.tma_out) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(&maps.c, buf, col, k, t.g);
+                            bulk_commit_group();
+                        }
+                    } else {
+                        __syncwarp();
+                        copy_rows_swizzled(buf,
+                                           reinterpret_cast<uint16_t *>(p.C) + out -
+                                               lane * p.ldc + col,
+                                           p.ldc, p.K - (k - lane), p.N - col, lane);
+                        __syncwarp();
+                    }
+                } else if (k < p.K) {
                     float v[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
@@ -363,6 +398,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
                 if (lane == 0) mbar_arrive_remote_tmem(mapa_shared(smem_u32(&acc_empty[acc]), 0));
             }
         }
+        staging_free(lane);                     // before this CTA's shared memory goes
     }
 
     tc_fence_before();
@@ -400,14 +436,23 @@ cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, 
             const uint64_t dims[] = {64, (uint64_t)M, (uint64_t)cols / 64}, st[] = {(uint64_t)ld * 2, 128};
             const uint32_t box[] = {64, 64, 2};
             in_3d = 1;
-            return encode_tiled(map, type, 3, ptr, dims, st, box, true);
+            return encode_tiled(map, type, 3, ptr, dims, st, box, 128);
         }
         const uint64_t dims[] = {(uint64_t)cols, (uint64_t)M}, st[] = {(uint64_t)ld * 2};
         const uint32_t box[] = {64, 64};
         in_3d = 0;
-        return encode_tiled(map, type, 2, ptr, dims, st, box, true);
+        return encode_tiled(map, type, 2, ptr, dims, st, box, 128);
     };
     mapped = M == 0 || (encode(&m.a, a.A, K, a.lda, p.a_3d) && encode(&m.d, a.D, N, a.ldd, p.d_3d));
+    p.staged = a.out_kind != OUT_F32 && a.beta == 0.0f;
+    p.tma_out = p.staged && N % 8 == 0;              // TMA clips a row at 16-byte granules
+    if (p.tma_out) {
+        const uint64_t ld = (uint64_t)a.ldc * 2;
+        const uint64_t dims[] = {(uint64_t)N, (uint64_t)K, (uint64_t)a.groups.G};
+        const uint64_t st[] = {ld, a.groups.G > 1 ? (uint64_t)a.strideC * 2 : ld * K};
+        const uint32_t box[] = {32, 32, 1};
+        mapped = mapped && encode_tiled(&m.c, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, a.C, dims, st, box, 64);
+    }
     if (!mapped) return cudaErrorInvalidValue;
     const long long units = (long long)a.groups.G * p.k_tiles * p.n_tiles;
     return launch_pairs<wgrad_kernel, WG_THREADS>(SMEM_BYTES, units, sms, s, m, p);
