@@ -72,6 +72,27 @@ __device__ __forceinline__ void tc_mma_f4_pair(uint32_t d_tmem, uint64_t adesc, 
             : "memory");
 }
 
+// True in one lane of the (converged) warp, the same one every time.  The
+// warps that issue MMAs stay converged and elect a lane only around the
+// tcgen05 instructions, so that descriptors and loop state are uniform.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
+// wait_bounded by every lane of a converged warp.
+__device__ __forceinline__ bool wait_bounded_warp(uint32_t bar, uint32_t parity,
+                                                  volatile int *abort_flag, int *err)
+{
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err));
+}
+
 // Descriptor of a scale tile: 8-row x 16-byte core matrices 128 bytes apart, no swizzle.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr)
 {
@@ -459,6 +480,37 @@ __device__ __forceinline__ void emit_swiglu(const GrpParams &p, const GrpMaps &m
     __syncwarp();
 }
 
+// One stage of 4-bit operands: the scales to tensor memory (from column sf on:
+// 4 columns per tile of this CTA's weight rows, then 8 per tile of A -- its
+// rows 0..127 and 128..255), then four K steps.  Consecutive stages alternate
+// between two sets of columns.
+template <int MATH>
+__device__ __forceinline__ void issue_f4(uint32_t d_tmem, uint64_t w, uint64_t t, uint64_t s,
+                                         uint32_t idesc, uint32_t sf, uint32_t t_shift,
+                                         uint32_t accum)
+{
+    using C = GrpCfg<MATH>;
+    const uint32_t st = sf + 4 * C::TILES_PER_STAGE;
+#pragma unroll
+    for (int i = 0; i < C::TILES_PER_STAGE; ++i) {
+        tc_cp_scales_pair(sf + 4 * i, s + i * 32);
+        tc_cp_scales_pair(st + 8 * i, s + (C::SCALE_BYTES >> 4) + i * 32);
+        tc_cp_scales_pair(st + 8 * i + 4, s + 2 * (C::SCALE_BYTES >> 4) + i * 32);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+        if (MATH == MATH_NV) {
+            tc_mma_f4_pair<true>(d_tmem, w + kk * 2, t + kk * 2, idesc, sf + 4 * kk,
+                                 st + t_shift + 8 * kk, accum | kk);
+        } else {
+            // two blocks of 32 per instruction: bytes 0, 1 or 2, 3 of a tile's four
+            const uint32_t id = (kk & 1) * 2;
+            tc_mma_f4_pair<false>(d_tmem, w + kk * 2, t + kk * 2, idesc | (id << 29) | (id << 4),
+                                  sf + 4 * (kk >> 1), st + t_shift + 8 * (kk >> 1), accum | kk);
+        }
+    }
+}
+
 // ------------------------------------------------------------ kernel
 
 template <int MATH, int EPI>
@@ -524,7 +576,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_holder;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const int G = p.groups.G;
     const int most = *most_rows;
     const int units = first[G] * p.n_blocks;
@@ -599,7 +651,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0 && leader && p.k_blocks > 0) {
+        if (leader && p.k_blocks > 0) {
             // Descriptors of the first stage; stages and K steps are added in
             // units of 16 bytes (shared memory stays below the field's 2^14).
             const uint64_t w_desc = smem_desc(smem_u32(sW), p.w_mn ? 8192u : 16u, 1024);
@@ -608,14 +660,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint32_t w_kstep = p.w_mn ? 128u : 2u;
             int stage = 0;
             uint32_t phase = 0;
-            uint32_t sbuf = 0;
             bool ok = true;
             int n = 0;
             for (int u = u0; u < units && ok; u += du, ++n) {
                 const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, most, u);
-                const uint32_t idesc = p.idesc | ((uint32_t)(t.width >> 3) << 17);
+                const uint32_t idesc =
+                    __shfl_sync(0xffffffffu, p.idesc | ((uint32_t)(t.width >> 3) << 17), 0);
+                // a tile of A that begins at the second half of its scale tile
+                const uint32_t t_shift = __shfl_sync(0xffffffffu, (t.local & 64) ? 2u : 0u, 0);
                 const int acc = n & 1;
-                if (!wait_bounded(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, p.err)) {
+                if (!wait_bounded_warp(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, p.err)) {
                     ok = false;
                     break;
                 }
@@ -623,61 +677,43 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t d_tmem = tmem_base + acc * C::ACC_STRIDE;
                 uint32_t accum = 0;
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!wait_bounded(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
+                    if (!wait_bounded_warp(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t w_stage = w_desc + (uint64_t)(stage * (C::W_BYTES >> 4));
                     const uint64_t t_stage = t_desc + (uint64_t)(stage * (C::T_BYTES >> 4));
-                    uint32_t sf = 0, sfb = 0;
                     // (Always four K steps: behind K the loads give zeros.  Testing
-                    // for the last steps made this thread, not the tensor pipe,
+                    // for the last steps made the issuing, not the tensor pipe,
                     // the bound: 8192 x 4096 x 4096 in 176 us instead of 159.)
-                    if (F4) {
-                        // columns: 4 per tile of this CTA's weight rows, then 8
-                        // per tile of A (its rows 0..127 and 128..255)
-                        sf = tmem_base + C::SCALE_COL + sbuf * 64;
-                        sfb = sf + 4 * C::TILES_PER_STAGE;
-                        sbuf ^= 1;
-                        const uint64_t sd = s_desc + (uint64_t)(stage * 3 * (C::SCALE_BYTES >> 4));
-#pragma unroll
-                        for (int i = 0; i < C::TILES_PER_STAGE; ++i) {
-                            tc_cp_scales_pair(sf + 4 * i, sd + i * 32);
-                            tc_cp_scales_pair(sfb + 8 * i, sd + (C::SCALE_BYTES >> 4) + i * 32);
-                            tc_cp_scales_pair(sfb + 8 * i + 4, sd + 2 * (C::SCALE_BYTES >> 4) + i * 32);
-                        }
-                        // a tile that begins at the second half of its scale tile
-                        sfb += (t.local & 64) ? 2 : 0;
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t wd = w_stage + kk * w_kstep;
-                        const uint64_t td = t_stage + kk * 2;
+                    if (elect_one()) {
                         if (MATH == MATH_16) {
-                            tc_mma_f16_pair(d_tmem, wd, td, idesc, accum);
-                        } else if (MATH == MATH_NV) {
-                            tc_mma_f4_pair<true>(d_tmem, wd, td, idesc, sf + 4 * kk, sfb + 8 * kk,
-                                                 accum);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc_mma_f16_pair(d_tmem, w_stage + kk * w_kstep, t_stage + kk * 2,
+                                                idesc, accum | kk);
                         } else {
-                            // two blocks of 32 per instruction: bytes 0, 1 or 2, 3 of a tile's four
-                            const uint32_t id = (kk & 1) * 2;
-                            tc_mma_f4_pair<false>(d_tmem, wd, td, idesc | (id << 29) | (id << 4),
-                                                  sf + 4 * (kk >> 1), sfb + 8 * (kk >> 1), accum);
+                            const uint64_t sd = s_desc + (uint64_t)(stage * 3 * (C::SCALE_BYTES >> 4));
+                            issue_f4<MATH>(d_tmem, w_stage, t_stage, sd, idesc,
+                                           tmem_base + C::SCALE_COL + (kb & 1) * 64, t_shift, accum);
                         }
-                        accum = 1;
+                        tc_commit_pair(smem_u32(&empty[stage]));
                     }
-                    tc_commit_pair(smem_u32(&empty[stage]));
+                    __syncwarp();
+                    accum = 1;
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
                 if (!ok) break;
-                tc_commit_pair(smem_u32(&acc_full[acc]));
+                if (elect_one()) tc_commit_pair(smem_u32(&acc_full[acc]));
+                __syncwarp();
             }
             // Never free tensor memory under a running MMA.
-            tc_commit_pair_local(smem_u32(mma_done));
+            if (elect_one()) tc_commit_pair_local(smem_u32(mma_done));
+            __syncwarp();
             wait_bounded(smem_u32(mma_done), 0, abort_flag, p.err, false, DRAIN_LIMIT_NS);
         }
         __syncwarp();

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_holder;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const int units = p.groups.G * p.k_tiles * p.n_tiles;
     const int u0 = (int)(blockIdx.x >> 1), du = (int)(gridDim.x >> 1);
 
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0 && leader) {
+        if (leader) {
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -257,62 +257,50 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
             const uint64_t a_desc = smem_desc(smem_u32(sA), 8192, 1024);
             const uint64_t d_desc = smem_desc(smem_u32(sD), 8192, 1024);
             for (int u = u0; u < units && ok; u += du) {
-                const WgradTile t = wgrad_tile(p, start, u);
-                if (t.rows == 0) continue;
+                const int rows = __shfl_sync(0xffffffffu, wgrad_tile(p, start, u).rows, 0);
+                if (rows == 0) continue;
                 const int acc = n & 1;
-                if (!wait_bounded(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, p.err)) {
+                if (!wait_bounded_warp(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, p.err)) {
                     ok = false;
                     break;
                 }
                 ++n;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * 256;
-                const int blocks = t.rows / 64, left = t.rows % 64;
-                uint32_t accum = 0;
-                // Whole blocks first: this loop issues one MMA per 128 cycles
-                // from one thread, and tests in it show in the time.
+                const int blocks = ceil_div(rows, 64);
                 for (int b = 0; b < blocks; ++b) {
-                    if (!wait_bounded(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
+                    if (!wait_bounded_warp(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint64_t ad = a_desc + (uint64_t)(stage * (OP_BYTES >> 4));
-                    const uint64_t dd = d_desc + (uint64_t)(stage * (OP_BYTES >> 4));
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        tc_mma_f16_pair(d_tmem, ad + kk * 128, dd + kk * 128, p.idesc, accum);
-                        accum = 1;
-                    }
-                    tc_commit_pair(smem_u32(&empty[stage]));
-                    if (++stage == WG_STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
-                if (ok && left > 0) {
-                    if (!wait_bounded(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
-                        ok = false;
-                        break;
-                    }
+                    const int left = rows - b * 64;
                     if (ends_inside(left)) mbar_try_wait_cluster(smem_u32(&full[stage]), phase);
                     tc_fence_after();
                     const uint64_t ad = a_desc + (uint64_t)(stage * (OP_BYTES >> 4));
                     const uint64_t dd = d_desc + (uint64_t)(stage * (OP_BYTES >> 4));
-                    for (int kk = 0; kk < ceil_div(left, 16); ++kk) {
-                        tc_mma_f16_pair(d_tmem, ad + kk * 128, dd + kk * 128, p.idesc, accum);
-                        accum = 1;
+                    if (elect_one()) {
+                        if (left > 48) {                 // every block but a group's last
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc_mma_f16_pair(d_tmem, ad + kk * 128, dd + kk * 128, p.idesc, b | kk);
+                        } else {
+                            for (int kk = 0; kk < ceil_div(left, 16); ++kk)
+                                tc_mma_f16_pair(d_tmem, ad + kk * 128, dd + kk * 128, p.idesc, b | kk);
+                        }
+                        tc_commit_pair(smem_u32(&empty[stage]));
                     }
-                    tc_commit_pair(smem_u32(&empty[stage]));
+                    __syncwarp();
                     if (++stage == WG_STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
                 if (!ok) break;
-                tc_commit_pair(smem_u32(&acc_full[acc]));
+                if (elect_one()) tc_commit_pair(smem_u32(&acc_full[acc]));
+                __syncwarp();
             }
-            tc_commit_pair_local(smem_u32(mma_done));
+            if (elect_one()) tc_commit_pair_local(smem_u32(mma_done));
+            __syncwarp();
             wait_bounded(smem_u32(mma_done), 0, abort_flag, p.err, false, DRAIN_LIMIT_NS);
         }
         __syncwarp();
