@@ -584,52 +584,57 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0 && p.k_blocks > 0) {
+        if (p.k_blocks > 0) {
             int stage = 0;
             uint32_t phase = 0;
             uint32_t armed = 0, armed_parity = 0;
             bool ok = true;
             for (int u = u0; u < units && ok; u += du) {
                 const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, most, u);
-                const int half = t.width / 2;
+                const int half = __shfl_sync(0xffffffffu, t.width, 0) / 2;
+                const int g = __shfl_sync(0xffffffffu, t.g, 0);
                 // the lowest box that holds this CTA's rows of A
                 int box = 0;
                 while (box + 1 < TOKEN_BOXES && half <= (64 >> box)) ++box;
-                const int t_row = t.row0 + (int)rank * half;
-                const int n0 = t.nb * 256 + (int)rank * 128;
+                const CUtensorMap *t_map = &maps.t[box];
+                const int t_row = __shfl_sync(0xffffffffu, t.row0, 0) + (int)rank * half;
+                const int n0 = __shfl_sync(0xffffffffu, t.nb, 0) * 256 + (int)rank * 128;
+                const int w_tile = g * p.w_tiles + n0 / 128;
+                const int t_tile = F4 ? __shfl_sync(0xffffffffu, stile[t.g] + t.local / 128, 0) : 0;
                 const uint32_t t_bytes = box == 0 ? C::T_BYTES : (128u >> box) * 128u;
                 const uint32_t bytes = C::W_BYTES + t_bytes + 3 * C::SCALE_BYTES;
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!wait_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.err)) {
+                    if (!wait_bounded_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
-                    // both CTAs' bytes complete on the leader's barrier
-                    const uint32_t fb_local = smem_u32(&full[stage]);
-                    const uint32_t fb = mapa_shared(fb_local, 0);
-                    if (leader) mbar_arrive_expect_tx(fb_local, 2 * bytes);
                     armed |= 1u << stage;
                     armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                    const uint32_t fb_local = smem_u32(&full[stage]);
+                    const uint32_t fb = mapa_shared(fb_local, 0);
                     const uint32_t w_dst = smem_u32(sW + stage * C::W_BYTES);
                     const uint32_t t_dst = smem_u32(sT + stage * C::T_BYTES);
                     const int k0 = kb * (F4 ? 128 : 64);     // inner coordinate of the boxes
-                    if (!p.w_mn) {
-                        tma_load_3d_pair(w_dst, &maps.w, fb, k0, n0, t.g);
-                    } else if (p.w_4d) {
-                        tma_load_4d_pair(w_dst, &maps.w, fb, 0, k0, n0 / 64, t.g);
-                    } else {
-                        tma_load_3d_pair(w_dst, &maps.w, fb, n0, k0, t.g);
-                        tma_load_3d_pair(w_dst + 8192, &maps.w, fb, n0 + 64, k0, t.g);
+                    if (elect_one()) {
+                        // both CTAs' bytes complete on the leader's barrier
+                        if (leader) mbar_arrive_expect_tx(fb_local, 2 * bytes);
+                        if (!p.w_mn) {
+                            tma_load_3d_pair(w_dst, &maps.w, fb, k0, n0, g);
+                        } else if (p.w_4d) {
+                            tma_load_4d_pair(w_dst, &maps.w, fb, 0, k0, n0 / 64, g);
+                        } else {
+                            tma_load_3d_pair(w_dst, &maps.w, fb, n0, k0, g);
+                            tma_load_3d_pair(w_dst + 8192, &maps.w, fb, n0 + 64, k0, g);
+                        }
+                        tma_load_2d_pair(t_dst, t_map, fb, k0, t_row);
+                        if (F4) {
+                            const uint32_t s_dst = smem_u32(sS + stage * 3 * C::SCALE_BYTES);
+                            const int x = kb * (C::SCALE_BYTES / 8);
+                            tma_load_2d_pair(s_dst, &maps.sw, fb, x, w_tile);
+                            tma_load_2d_pair(s_dst + C::SCALE_BYTES, &maps.st, fb, x, t_tile);
+                        }
                     }
-                    tma_load_2d_pair(t_dst, &maps.t[box], fb, k0, t_row);
-                    if (F4) {
-                        const uint32_t s_dst = smem_u32(sS + stage * 3 * C::SCALE_BYTES);
-                        const int x = kb * (C::SCALE_BYTES / 8);
-                        tma_load_2d_pair(s_dst, &maps.sw, fb, x,
-                                         t.g * p.w_tiles + t.nb * 2 + (int)rank);
-                        tma_load_2d_pair(s_dst + C::SCALE_BYTES, &maps.st, fb, x,
-                                         stile[t.g] + t.local / 128);
-                    }
+                    __syncwarp();
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1;

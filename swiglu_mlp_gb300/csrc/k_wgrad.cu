@@ -150,39 +150,40 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            uint32_t armed = 0, armed_parity = 0;
-            bool ok = true;
-            for (int u = u0; u < units && ok; u += du) {
-                const WgradTile t = wgrad_tile(p, start, u);
-                const int ka = t.kb * 256 + (int)rank * 128;
-                const int nd = t.nb * 256 + (int)rank * 128;
-                const int blocks = ceil_div(t.rows, 64);
-                for (int b = 0; b < blocks; ++b) {
-                    if (!wait_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.err)) {
-                        ok = false;
-                        break;
-                    }
-                    // Both CTAs' bytes and one arrival of each complete the
-                    // leader's barrier.  A block in which the group ends lands on
-                    // a barrier of this CTA instead; the fixing warp arrives for it.
-                    const uint32_t fb = smem_u32(&full[stage]);
-                    uint32_t bar = mapa_shared(fb, 0);
-                    if (ends_inside(t.rows - b * 64)) {
-                        bar = smem_u32(&landed[stage]);
+        int stage = 0;
+        uint32_t phase = 0;
+        uint32_t armed = 0, armed_parity = 0;
+        bool ok = true;
+        for (int u = u0; u < units && ok; u += du) {
+            const WgradTile t = wgrad_tile(p, start, u);
+            const int rows = __shfl_sync(0xffffffffu, t.rows, 0);
+            const int row0 = __shfl_sync(0xffffffffu, t.row0, 0);
+            const int ka = t.kb * 256 + (int)rank * 128;
+            const int nd = t.nb * 256 + (int)rank * 128;
+            const int blocks = ceil_div(rows, 64);
+            for (int b = 0; b < blocks; ++b) {
+                if (!wait_bounded_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.err)) {
+                    ok = false;
+                    break;
+                }
+                armed |= 1u << stage;
+                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                const uint32_t a_dst = smem_u32(sA + stage * OP_BYTES);
+                const uint32_t d_dst = smem_u32(sD + stage * OP_BYTES);
+                const int row = row0 + b * 64;
+                const bool ends = ends_inside(rows - b * 64);
+                // Both CTAs' bytes and one arrival of each complete the
+                // leader's barrier.  A block in which the group ends lands on
+                // a barrier of this CTA instead; the fixing warp arrives for it.
+                const uint32_t fb = smem_u32(&full[stage]);
+                const uint32_t bar = ends ? smem_u32(&landed[stage]) : mapa_shared(fb, 0);
+                if (elect_one()) {
+                    if (ends)
                         mbar_arrive_expect_tx(bar, 2 * OP_BYTES);
-                    } else if (leader) {
+                    else if (leader)
                         mbar_arrive_expect_tx(fb, 4 * OP_BYTES);
-                    } else {
+                    else
                         mbar_arrive_remote_tmem(bar);            // nothing to release
-                    }
-                    armed |= 1u << stage;
-                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                    const uint32_t a_dst = smem_u32(sA + stage * OP_BYTES);
-                    const uint32_t d_dst = smem_u32(sD + stage * OP_BYTES);
-                    const int row = t.row0 + b * 64;
                     if (p.a_3d) {
                         tma_load_3d_pair(a_dst, &maps.a, bar, 0, row, ka / 64);
                     } else {
@@ -195,22 +196,23 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
                         tma_load_2d_pair(d_dst, &maps.d, bar, nd, row);
                         tma_load_2d_pair(d_dst + 8192, &maps.d, bar, nd + 64, row);
                     }
-                    if (++stage == WG_STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                if (++stage == WG_STAGES) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-            // Never leave with loads in flight into this CTA's shared memory.
-            if (leader) {
-                for (int s = 0; s < WG_STAGES; ++s)
-                    if (armed & (1u << s))
-                        wait_bounded(smem_u32(&full[s]), (armed_parity >> s) & 1, abort_flag,
-                                     p.err, false, DRAIN_LIMIT_NS);
-            } else if (!ok) {
-                const uint64_t t0 = global_timer_ns();
-                while (global_timer_ns() - t0 < 200000ull) {
-                }
+        }
+        // Never leave with loads in flight into this CTA's shared memory.
+        if (leader) {
+            for (int s = 0; s < WG_STAGES; ++s)
+                if (armed & (1u << s))
+                    wait_bounded(smem_u32(&full[s]), (armed_parity >> s) & 1, abort_flag, p.err,
+                                 false, DRAIN_LIMIT_NS);
+        } else if (!ok) {
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 200000ull) {
             }
         }
         __syncwarp();
