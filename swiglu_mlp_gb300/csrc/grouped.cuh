@@ -137,6 +137,10 @@ struct GrpCfg {
     // Rows of A per tile: two accumulators fill tensor memory at 256; with
     // scales there they leave room at 192.
     static constexpr int TOKENS = F4 ? 192 : 256;
+    // A tile begins at a multiple of UNIT rows of its group (4-bit: 64 rows are
+    // two columns of scales) and may be CANDIDATES widths, see choose_rows.
+    static constexpr int UNIT = F4 ? 64 : 16;
+    static constexpr int CANDIDATES = F4 ? 2 : 8;
     static constexpr int TILES_PER_STAGE = MATH == MATH_NV ? 4 : 2;   // scale tiles along K
     static constexpr int SCALE_BYTES = F4 ? 512 * TILES_PER_STAGE : 0;
     static constexpr int W_BYTES = 128 * 128;
@@ -160,51 +164,49 @@ template <int MATH>
 __device__ __forceinline__ int tile_step(int rows, int most)
 {
     const int t = ceil_div(rows, most);
-    // 4-bit: a tile begins at a multiple of 64 rows, two scale columns
-    const int unit = GrpCfg<MATH>::F4 ? 64 : 16;
-    return ceil_div(ceil_div(rows, t), unit) * unit;
+    constexpr int UNIT = GrpCfg<MATH>::UNIT;
+    return ceil_div(ceil_div(rows, t), UNIT) * UNIT;
 }
 
-// The most rows of A that a tile should have, chosen by one whole warp so that
-// the last wave of tiles is not nearly empty: of TOKENS, TOKENS - unit, .. the
-// one with the least  waves * (average rows per tile + 24).  A tile's time is
-// proportional to its rows (the MMA's N) down to about 64, plus a fixed part
-// worth some 24 rows.  994 tiles on 76 pairs are 13.1 waves at 256 rows; the
-// 1064 tiles of at most 240 rows make 14.0 of them and take 7% less.
+// The most rows of A that a tile should have, chosen so that the last wave of
+// tiles is not nearly empty: of TOKENS, TOKENS - unit, .. the one with the least
+//   waves * (stages * max(rows per tile, 176) + 700),
+// a tile's measured time in units of 1.145 ns: a 16-bit stage takes 292 ns at
+// 256 rows, 228 at 192, 212 at 160 and not less than 195 below (the loading
+// and issuing), and a tile about 0.8 us besides.  994 tiles on 76 pairs are
+// 13.1 waves at 256 rows; 1064 tiles of at most 240 make 14.0 and are 7% faster.
+// Warp w of the first eight computes candidate w's; ends with a barrier.
 template <int MATH>
-__device__ __forceinline__ int choose_rows(const int *start, int G, int n_blocks, int pairs)
+__device__ __forceinline__ int choose_rows(const int *start, int G, int n_blocks, int k_blocks,
+                                           int pairs, float *costs)
 {
     using C = GrpCfg<MATH>;
-    constexpr int UNIT = C::F4 ? 64 : 16;
-    constexpr int CANDS = C::F4 ? 2 : 8;            // down to 128 rows
-    const int lane = threadIdx.x & 31;
-    const int cand = lane % CANDS;
-    const int most = C::TOKENS - cand * UNIT;
-    int tiles = 0, rows = 0;
-    for (int g = lane / CANDS; g < G; g += 32 / CANDS) {
-        const int r = start[g + 1] - start[g];
-        tiles += ceil_div(r, most);
-        rows += r;
-    }
-#pragma unroll
-    for (int d = CANDS; d < 32; d <<= 1) {
-        tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
-        rows += __shfl_xor_sync(0xffffffffu, rows, d);
-    }
-    const long long units = (long long)tiles * n_blocks;
-    const float waves = (float)((units + pairs - 1) / pairs);
-    float cost = tiles > 0 ? waves * (fmaxf((float)rows / (float)tiles, 64.0f) + 24.0f) : 0.0f;
-    int best = cand;
-#pragma unroll
-    for (int d = 1; d < CANDS; d <<= 1) {
-        const float c = __shfl_xor_sync(0xffffffffu, cost, d);
-        const int b = __shfl_xor_sync(0xffffffffu, best, d);
-        if (c < cost || (c == cost && b < best)) {
-            cost = c;
-            best = b;
+    constexpr int CANDS = C::CANDIDATES;
+    const int lane = threadIdx.x & 31, cand = threadIdx.x >> 5;
+    if (cand < CANDS) {
+        const int most = C::TOKENS - cand * C::UNIT;
+        int tiles = 0, rows = 0;
+        for (int g = lane; g < G; g += 32) {
+            const int r = start[g + 1] - start[g];
+            tiles += ceil_div(r, most);
+            rows += r;
         }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+            rows += __shfl_xor_sync(0xffffffffu, rows, d);
+        }
+        const float units = (float)tiles * (float)n_blocks;
+        const float waves = ceilf(units / (float)pairs);
+        const float mean = (float)rows / fmaxf((float)tiles, 1.0f);
+        if (lane == 0) costs[cand] = waves * ((float)k_blocks * fmaxf(mean, 176.0f) + 700.0f);
     }
-    return C::TOKENS - best * UNIT;
+    __syncthreads();
+    int best = 0;
+#pragma unroll
+    for (int c = 1; c < CANDS; ++c)
+        if (costs[c] < costs[best]) best = c;
+    return C::TOKENS - best * C::UNIT;
 }
 
 struct GrpTile {
@@ -221,7 +223,7 @@ __device__ __forceinline__ GrpTile grp_tile(const int *start, const int *first, 
                                             int n_blocks, int most, int u)
 {
     GrpTile t;
-    t.g = group_of(first, G, u / n_blocks);
+    t.g = group_of(first, G, n_blocks, u);
     const int tiles = first[t.g + 1] - first[t.g];
     const int local = u - first[t.g] * n_blocks;
     const int rows = start[t.g + 1] - start[t.g];
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint64_t *mma_done = bars + 2 * S + 4;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 2 * S + 5);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    int *most_rows = reinterpret_cast<int *>(tmem_holder + 2);
+    int *scratch = reinterpret_cast<int *>(tmem_holder + 4);      // 16 ints, 8 floats
     int *start = reinterpret_cast<int *>(sOut + NUM_EPI_WARPS * C::OUT_BYTES + 512 - 64);
     int *first = start + p.groups.G + 1;
     int *stile = first + p.groups.G + 1;          // rows of scale tiles before each group
@@ -565,20 +567,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tmem_alloc_pair(smem_u32(tmem_holder), 512);
         tmem_relinquish_pair();
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == 2) {
-        group_starts(p.groups, start, p.err);
-        const int rows = choose_rows<MATH>(start, p.groups.G, p.n_blocks, (int)(gridDim.x >> 1));
-        tile_sums(p.groups.G, start, first, [rows](int n) { return ceil_div(n, rows); });
-        if (lane == 0) *most_rows = rows;
-        if (F4) tile_sums(p.groups.G, start, stile, [](int n) { return ceil_div(n, 128); });
-    }
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_holder, 0);
+    // Up to here only this pair's own resources; now the offsets may be read.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int G = p.groups.G;
-    const int most = *most_rows;
+    group_starts<NUM_THREADS>(p.groups, start, p.err);
+    // (tiles of one width do for groups that all fit the narrowest)
+    const int most = p.groups.M <= C::TOKENS - (C::CANDIDATES - 1) * C::UNIT
+                         ? C::TOKENS
+                         : choose_rows<MATH>(start, G, p.n_blocks, p.k_blocks, (int)(gridDim.x >> 1),
+                                             reinterpret_cast<float *>(scratch + 16));
+    tile_sums<NUM_THREADS>(G, start, first, scratch, [most](int n) { return ceil_div(n, most); });
+    if (F4)
+        tile_sums<NUM_THREADS>(G, start, stile, scratch, [](int n) { return ceil_div(n, 128); });
     const int units = first[G] * p.n_blocks;
     const int u0 = (int)(blockIdx.x >> 1), du = (int)(gridDim.x >> 1);
 

@@ -1,5 +1,5 @@
-// groups.cuh — the table of row groups that the grouped kernels build in
-// shared memory from the offsets on the device.
+// groups.cuh — the tables of row groups that the grouped kernels build in
+// shared memory from the offsets on the device, with all threads of a CTA.
 #pragma once
 
 #include "experts.h"
@@ -8,80 +8,99 @@ namespace swg {
 
 constexpr int ERR_INVALID = 1;       // == SWG_ERR_INVALID_ARG
 
-// Run by one whole warp.  start[0..G]: the offsets, clamped to be
-// non-decreasing within [0, M], so that every row a kernel derives from them
-// exists; an offset that had to be clamped is reported in the error word.
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// start[0..G]: the offsets, clamped to be non-decreasing within [0, M], so
+// that every row a kernel derives from them exists; offsets that had to be
+// clamped are reported in the error word.  Called by all NT threads; ends
+// with a barrier.
+template <int NT>
 __device__ __forceinline__ void group_starts(const Groups &gr, int *start, int *err)
 {
-    const int lane = threadIdx.x & 31;
+    const int tid = threadIdx.x, G = gr.G;
     if (gr.offsets == nullptr) {         // one group of all rows
-        if (lane == 0) {
+        if (tid == 0) {
             start[0] = 0;
             start[1] = gr.M;
         }
-        __syncwarp();
+        __syncthreads();
         return;
     }
-    const int G = gr.G;
-    int top = 0;                         // the largest offset so far
     bool bad = false;
-    for (int base = 0; base <= G; base += 32) {
-        const int i = base + lane;
-        const int raw = i <= G ? gr.offsets[i] : 0;
-        int v = raw < 0 ? 0 : raw > gr.M ? gr.M : raw;
-        if (lane == 0 && v < top) v = top;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {          // running maximum
-            const int o = __shfl_up_sync(0xffffffffu, v, d);
-            if (lane >= d && o > v) v = o;
-        }
-        if (i <= G) {
-            start[i] = v;
-            bad = bad || v != raw;
-        }
-        top = __shfl_sync(0xffffffffu, v, 31);
+    for (int i = tid; i <= G; i += NT) {
+        const int raw = gr.offsets[i];
+        const int v = raw < 0 ? 0 : raw > gr.M ? gr.M : raw;
+        bad = bad || v != raw;
+        start[i] = v;
     }
-    if (bad) atomicCAS(err, 0, ERR_INVALID);
-    __syncwarp();
+    __syncthreads();
+    for (int i = tid; i < G; i += NT) bad = bad || start[i + 1] < start[i];
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) {
+            atomicCAS(err, 0, ERR_INVALID);
+            for (int i = 0; i < G; ++i)
+                if (start[i + 1] < start[i]) start[i + 1] = start[i];
+        }
+        __syncthreads();
+    }
 }
 
-// Run by one whole warp.  first[0..G]: how many tiles the groups before g
-// have, a group of `rows` rows having tiles_of(rows).
-template <class F>
-__device__ __forceinline__ void tile_sums(int G, const int *start, int *first, F tiles_of)
+// first[0..G]: how many tiles the groups before g have, a group of `rows`
+// rows having tiles_of(rows).  `warp_sums`: NT / 32 ints of shared memory.
+// Called by all NT threads; ends with a barrier.
+template <int NT, class F>
+__device__ __forceinline__ void tile_sums(int G, const int *start, int *first, int *warp_sums,
+                                          F tiles_of)
 {
-    const int lane = threadIdx.x & 31;
-    int sum = 0;
-    for (int base = 0; base < G; base += 32) {
-        const int i = base + lane;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (G == 1) {
+        if (tid == 0) {
+            first[0] = 0;
+            first[1] = tiles_of(start[1] - start[0]);
+        }
+        __syncthreads();
+        return;
+    }
+    int before = 0;                      // tiles of the rounds before this one
+    for (int base = 0; base < G; base += NT) {
+        const int i = base + tid;
         const int n = i < G ? tiles_of(start[i + 1] - start[i]) : 0;
         int v = n;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {          // running sum
+        for (int d = 1; d < 32; d <<= 1) {          // running sum of the warp
             const int o = __shfl_up_sync(0xffffffffu, v, d);
             if (lane >= d) v += o;
         }
-        if (i < G) first[i] = sum + v - n;
-        sum += __shfl_sync(0xffffffffu, v, 31);
+        if (lane == 31) warp_sums[warp] = v;
+        __syncthreads();
+        int lower = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            const int s = warp_sums[w];
+            lower += w < warp ? s : 0;
+            all += s;
+        }
+        if (i < G) first[i] = before + lower + v - n;
+        before += all;
+        __syncthreads();
     }
-    if (lane == 0) first[G] = sum;
-    __syncwarp();
+    if (tid == 0) first[G] = before;
+    __syncthreads();
 }
 
-// The group that tile t (< first[G]) belongs to: the last g with first[g] <= t.
-__device__ __forceinline__ int group_of(const int *first, int G, int t)
+// The group that unit u belongs to, groups having first[g + 1] - first[g]
+// tiles of `per` units each: the last g with first[g] * per <= u.
+__device__ __forceinline__ int group_of(const int *first, int G, int per, int u)
 {
-    int lo = 0, hi = G;                  // first[lo] <= t < first[hi]
+    int lo = 0, hi = G;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (first[mid] <= t)
+        if (first[mid] * per <= u)
             lo = mid;
         else
             hi = mid;
     }
     return lo;
 }
-
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 }  // namespace swg

@@ -1,13 +1,13 @@
 // k_mx4.cu — microscaled 4-bit floating point: to 4 bits and back.
 //
 // Both directions stream: 2 bytes (16-bit x) and 1/2 + 1/32 or 1/16 bytes per
-// element, each once, so memory bounds them.  A CTA takes 128 rows x 256
-// columns -- whole scale tiles -- and a warp one row of that at a time: 8
-// columns per lane, one 16-byte access of x and 4 bytes of codes, eight rows
-// in flight.  A block's largest magnitude meets across its 4 (MXFP4) or 2
-// (NVFP4) lanes.  The scale bytes pass through shared memory, because in
-// memory the tile's rows r, r + 32, r + 64, r + 96 lie side by side; they are
-// stored as one run of 1 or 2 KB.
+// element, each once, so memory bounds them.  A CTA takes 256 columns of 32 of
+// the 128 rows of a row of scale tiles: those with r mod 32 in one eighth, in
+// fours r, r + 32, r + 64, r + 96 a warp, whose scales lie side by side in
+// memory.  A lane has 8 columns of each of its warp's four rows: one 16-byte
+// access of x and 4 bytes of codes per row.  A block's largest magnitude meets
+// across its 4 (MXFP4) or 2 (NVFP4) lanes, and four lanes swap their blocks'
+// scale bytes so that each stores 4 bytes of a tile.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -24,8 +24,8 @@ namespace {
 constexpr int TILE_ROWS = 128;       // rows of a scale tile
 constexpr int TILE_COLS = 256;       // columns per CTA: 2 (MXFP4) or 4 (NVFP4) scale tiles
 constexpr int THREADS = 256;
-constexpr int ROWS_PER_WARP = TILE_ROWS / (THREADS / 32);
-constexpr int BATCH = 8;             // rows whose loads are in flight together
+constexpr int STRIPS = 4;            // CTAs per row of scale tiles
+constexpr int ROWS = 4;              // rows per warp, 32 apart
 
 template <int TYPE> struct Elem;
 template <> struct Elem<0> { using T = __half; };
@@ -139,24 +139,33 @@ __device__ __forceinline__ uint32_t block_scale(float top, float &scale, float &
     return bad ? 0xffu : code;
 }
 
-struct RowTile {
-    int g, row0, end, t;     // group, first row, end of the group, row of scale tiles
+struct Place {
+    int t;                   // row of scale tiles
+    int chunk;               // 256 columns
+    int r32;                 // this warp's rows: r32, r32 + 32, ..
+    int row0, end;           // first row of the tiles, end of their group
 };
 
-// Finds the CTA's rows; false for a CTA beyond the last group's tiles.
-__device__ __forceinline__ bool find_rows(const Groups &gr, int t, int *err, int *table, RowTile &r)
+// This CTA's and warp's place; false for a CTA beyond the last group's tiles.
+__device__ __forceinline__ bool find_place(const Groups &gr, int chunks, int *err, int *table,
+                                           Place &p)
 {
-    int *start = table, *first = table + gr.G + 1;
-    if (threadIdx.x < 32) {
-        group_starts(gr, start, err);
-        tile_sums(gr.G, start, first, [](int rows) { return ceil_div(rows, TILE_ROWS); });
+    const unsigned strip = blockIdx.x / (unsigned)chunks;
+    p.chunk = (int)(blockIdx.x - strip * (unsigned)chunks);
+    p.t = (int)(strip / STRIPS);
+    p.r32 = (int)(strip % STRIPS) * 8 + (threadIdx.x >> 5);
+    if (gr.offsets == nullptr) {
+        p.row0 = p.t * TILE_ROWS;
+        p.end = gr.M;
+        return p.row0 < gr.M;
     }
-    __syncthreads();
-    if (t >= first[gr.G]) return false;
-    r.g = group_of(first, gr.G, t);
-    r.row0 = start[r.g] + (t - first[r.g]) * TILE_ROWS;
-    r.end = start[r.g + 1];
-    r.t = t;
+    int *start = table, *first = table + gr.G + 1, *sums = table + 2 * (gr.G + 1);
+    group_starts<THREADS>(gr, start, err);
+    tile_sums<THREADS>(gr.G, start, first, sums, [](int rows) { return ceil_div(rows, TILE_ROWS); });
+    if (p.t >= first[gr.G]) return false;
+    const int g = group_of(first, gr.G, 1, p.t);
+    p.row0 = start[g] + (p.t - first[g]) * TILE_ROWS;
+    p.end = start[g + 1];
     return true;
 }
 
@@ -166,76 +175,68 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Mx4Args p, int 
     constexpr int LANES = NV ? 2 : 4;                // lanes per block
     constexpr int TILES = NV ? 4 : 2;                // scale tiles per CTA along K
     extern __shared__ int table[];
-    __shared__ __align__(16) uint8_t sc[TILES * 512];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int t = blockIdx.x / chunks, chunk = blockIdx.x - t * chunks;
-    RowTile rt;
-    if (!find_rows(p.groups, t, err, table, rt)) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int k = chunk * TILE_COLS + lane * 8;
+    Place at;
+    if (!find_place(p.groups, chunks, err, table, at)) return;
+    const int lane = threadIdx.x & 31;
+    const int k = at.chunk * TILE_COLS + lane * 8;
     const int cnt = min(8, max(0, p.K - k));
     const bool write = k < ((p.K + 31) & ~31);       // codes up to a multiple of 32 columns
-    const int b = lane / LANES;                      // block within the CTA's columns
-    uint8_t *const my = sc + (b >> 2) * 512 + (b & 3);
-#pragma unroll 1
-    for (int r0 = 0; r0 < ROWS_PER_WARP; r0 += BATCH) {
-        const int first = warp * ROWS_PER_WARP + r0;
-        if (rt.row0 + first >= rt.end) {             // no such rows: their scales are zero
-            if (lane % LANES == 0)
-                for (int i = 0; i < BATCH; ++i) {
-                    const int r = first + i;
-                    my[16 * (r & 31) + 4 * (r >> 5)] = 0;
-                }
-            continue;
-        }
-        Raw8<TYPE> raw[BATCH];
+    const bool block = k - (lane % LANES) * 8 < p.K; // the lane's block has columns
+    Raw8<TYPE> raw[ROWS];
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int row = rt.row0 + first + i;
-            raw[i] = load8<TYPE>(p.X, (long long)row * p.ldx + k, row < rt.end ? cnt : 0);
-        }
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int r = first + i;
-            float v[8], top = 0.0f;
-            to_floats<TYPE>(raw[i], v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] *= p.scale;
-                top = max_nan(top, fabsf(v[j]));
-            }
-            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            if (!NV) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            float s, inv;
-            uint32_t code = block_scale<NV>(top, s, inv);
-            uint32_t q = 0;
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                float a = v[j] * inv, c = v[j + 1] * inv;
-                if (NV) {
-                    // One residual correction (Markstein's): a quotient that is
-                    // itself a float -- every tie between two codes is, for
-                    // 16-bit x -- comes out exact, so ties go to even as in the
-                    // definition; a * inv alone may miss them by a rounding.
-                    a = __fmaf_rn(__fmaf_rn(-a, s, v[j]), inv, a);
-                    c = __fmaf_rn(__fmaf_rn(-c, s, v[j + 1]), inv, c);
-                }
-                q |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(a, c), __NV_E2M1, cudaRoundNearest)
-                     << (4 * j);
-            }
-            const int row = rt.row0 + r;
-            if (row < rt.end && write)
-                *reinterpret_cast<uint32_t *>(p.Q + (long long)row * p.ldq + k / 2) = q;
-            if (row >= rt.end || k - (lane % LANES) * 8 >= p.K) code = 0;
-            if (lane % LANES == 0) my[16 * (r & 31) + 4 * (r >> 5)] = (uint8_t)code;
-        }
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = at.row0 + at.r32 + 32 * i;
+        raw[i] = load8<TYPE>(p.X, (long long)row * p.ldx + k, row < at.end ? cnt : 0);
     }
-    __syncthreads();
+    uint32_t codes = 0;                              // the lane's block's scales, a byte per row
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = at.row0 + at.r32 + 32 * i;
+        float v[8], top = 0.0f;
+        to_floats<TYPE>(raw[i], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] *= p.scale;
+            top = max_nan(top, fabsf(v[j]));
+        }
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        if (!NV) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float s, inv;
+        const uint32_t code = block_scale<NV>(top, s, inv);
+        uint32_t q = 0;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            float a = v[j] * inv, c = v[j + 1] * inv;
+            if (NV) {
+                // One residual correction (Markstein's): a quotient that is
+                // itself a float -- every tie between two codes is, for
+                // 16-bit x -- comes out exact, so ties go to even as in the
+                // definition; a * inv alone may miss them by a rounding.
+                a = __fmaf_rn(__fmaf_rn(-a, s, v[j]), inv, a);
+                c = __fmaf_rn(__fmaf_rn(-c, s, v[j + 1]), inv, c);
+            }
+            q |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(a, c), __NV_E2M1, cudaRoundNearest)
+                 << (4 * j);
+        }
+        if (row < at.end && write)
+            *reinterpret_cast<uint32_t *>(p.Q + (long long)row * p.ldq + k / 2) = q;
+        if (row < at.end && block) codes |= code << (8 * i);
+    }
+    // Lane b of a tile's four blocks takes row b's four bytes and stores them.
+    const int b = lane / LANES % 4, tile = lane / (4 * LANES);
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t c = __shfl_sync(0xffffffffu, codes, tile * 4 * LANES + i * LANES);
+        word |= ((c >> (8 * b)) & 0xffu) << (8 * i);
+    }
     const int tiles_k = ceil_div(p.K, NV ? 64 : 128);
-    const int have = min(TILES, tiles_k - chunk * TILES) * 32;         // 16-byte pieces
-    uint4 *out = reinterpret_cast<uint4 *>(p.S + ((long long)t * tiles_k + chunk * TILES) * 512);
-    for (int i = threadIdx.x; i < have; i += THREADS) out[i] = reinterpret_cast<const uint4 *>(sc)[i];
+    const int kt = at.chunk * TILES + tile;
+    if (lane % LANES == 0 && kt < tiles_k)
+        *reinterpret_cast<uint32_t *>(p.S + ((long long)at.t * tiles_k + kt) * 512 + 16 * at.r32 +
+                                      4 * b) = word;
 }
 
 template <int TYPE, bool NV>
@@ -244,36 +245,30 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const Mx4Args p, in
     constexpr int LANES = NV ? 2 : 4;
     constexpr int TILES = NV ? 4 : 2;
     extern __shared__ int table[];
-    __shared__ __align__(16) uint8_t sc[TILES * 512];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int t = blockIdx.x / chunks, chunk = blockIdx.x - t * chunks;
-    RowTile rt;
-    if (!find_rows(p.groups, t, err, table, rt)) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int k = chunk * TILE_COLS + lane * 8;
+    Place at;
+    if (!find_place(p.groups, chunks, err, table, at)) return;
+    const int lane = threadIdx.x & 31;
+    const int k = at.chunk * TILE_COLS + lane * 8;
     const int cnt = min(8, max(0, p.K - k));
-    const int tiles_k = ceil_div(p.K, NV ? 64 : 128);
-    const int have = min(TILES, tiles_k - chunk * TILES) * 32;
-    const uint4 *in = reinterpret_cast<const uint4 *>(p.S + ((long long)t * tiles_k + chunk * TILES) * 512);
-    for (int i = threadIdx.x; i < have; i += THREADS) reinterpret_cast<uint4 *>(sc)[i] = in[i];
-    uint32_t q[ROWS_PER_WARP];
+    if (cnt == 0) return;
+    uint32_t q[ROWS];
 #pragma unroll
-    for (int i = 0; i < ROWS_PER_WARP; ++i) {
-        const int row = rt.row0 + warp * ROWS_PER_WARP + i;
-        q[i] = 0;
-        if (row < rt.end && cnt > 0)
-            q[i] = *reinterpret_cast<const uint32_t *>(p.Q + (long long)row * p.ldq + k / 2);
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = at.row0 + at.r32 + 32 * i;
+        q[i] = row < at.end ? *reinterpret_cast<const uint32_t *>(p.Q + (long long)row * p.ldq + k / 2) : 0;
     }
-    __syncthreads();
-    const int b = lane / LANES;
-    const uint8_t *const my = sc + (b >> 2) * 512 + (b & 3);
+    // 16 bytes: the four rows' scales of the tile's four blocks
+    const int b = lane / LANES % 4, kt = at.chunk * TILES + lane / (4 * LANES);
+    const uint4 w = *reinterpret_cast<const uint4 *>(
+        p.S + ((long long)at.t * ceil_div(p.K, NV ? 64 : 128) + kt) * 512 + 16 * at.r32);
+    const uint32_t words[ROWS] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < ROWS_PER_WARP; ++i) {
-        const int r = warp * ROWS_PER_WARP + i;
-        const int row = rt.row0 + r;
-        if (row >= rt.end || cnt == 0) continue;
-        const float s = mx4_scale_value(NV, my[16 * (r & 31) + 4 * (r >> 5)]);
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = at.row0 + at.r32 + 32 * i;
+        if (row >= at.end) continue;
+        const float s = mx4_scale_value(NV, (words[i] >> (8 * b)) & 0xffu);
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
@@ -292,9 +287,9 @@ cudaError_t launch(const Mx4Args &p, bool back, int tile_rows, int *err, cudaStr
 {
     const int chunks = (p.K + TILE_COLS - 1) / TILE_COLS;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)tile_rows * chunks));
+    cfg.gridDim = dim3((unsigned)((long long)tile_rows * STRIPS * chunks));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = 2 * sizeof(int) * (p.groups.G + 1);
+    cfg.dynamicSmemBytes = p.groups.offsets ? sizeof(int) * (2 * (p.groups.G + 1) + THREADS / 32) : 0;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

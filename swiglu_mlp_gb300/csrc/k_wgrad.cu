@@ -139,11 +139,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         tmem_alloc_pair(smem_u32(tmem_holder), 512);
         tmem_relinquish_pair();
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == 2) group_starts(p.groups, start, p.err);
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
+    // Up to here only this pair's own resources; now the offsets may be read.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    group_starts<WG_THREADS>(p.groups, start, p.err);
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const int units = p.groups.G * p.k_tiles * p.n_tiles;
     const int u0 = (int)(blockIdx.x >> 1), du = (int)(gridDim.x >> 1);
