@@ -147,7 +147,7 @@ struct GrpCfg {
     static constexpr int T_BYTES = TOKENS / 2 * 128;
     static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + 3 * SCALE_BYTES;
     static constexpr int OUT_BYTES = 3072;        // per epilogue warp, see the epilogue
-    static constexpr int TABLE_BYTES = (F4 ? 3 : 2) * 4 * (MAX_GROUPS + 1) + 4;
+    static constexpr int TABLE_BYTES = (F4 ? 3 : 2) * 4 * (MAX_GROUPS + 1) + MAX_GROUPS;
     static constexpr int FIXED = 1024 + NUM_EPI_WARPS * OUT_BYTES + TABLE_BYTES + 512;
     static constexpr int STAGES_RAW = (232448 - FIXED) / STAGE_BYTES;
     static constexpr int STAGES = STAGES_RAW > 6 ? 6 : STAGES_RAW;
@@ -216,32 +216,41 @@ struct GrpTile {
     int width;         // rows rounded up to 16: the MMA's N
 };
 
+// a / b for a >= 0, b > 0.  Below 2^21 through the fast FP32 division: a + 1/2
+// keeps the quotient 1/(2b) away from the next integer, more than its error of
+// two units in the last place.  (Integer division is a chain of tens of
+// dependent instructions; four of them per tile, before its first load, took
+// 0.4 us.)
+__device__ __forceinline__ int fast_div(int a, int b)
+{
+    if (a < (1 << 21)) return (int)__fdividef((float)a + 0.5f, (float)b);
+    return a / b;
+}
+
 // Tile u: groups in order; within a group bands of 8 tiles of A walk the
 // weight blocks together, so that concurrently running pairs share both in L2.
-template <int MATH>
-__device__ __forceinline__ GrpTile grp_tile(const int *start, const int *first, int G,
-                                            int n_blocks, int most, int u)
+__device__ __forceinline__ GrpTile grp_tile(const int *start, const int *first,
+                                            const uint8_t *steps, int G, int n_blocks, int u)
 {
     GrpTile t;
     t.g = group_of(first, G, n_blocks, u);
     const int tiles = first[t.g + 1] - first[t.g];
     const int local = u - first[t.g] * n_blocks;
-    const int rows = start[t.g + 1] - start[t.g];
     int mb;
     if (tiles == 1) {
         mb = 0;
         t.nb = local;
     } else {
-        const int band = local / (8 * n_blocks);
+        const int band = tiles <= 8 ? 0 : fast_div(local, 8 * n_blocks);
         const int in = local - band * 8 * n_blocks;
         const int bm = min(8, tiles - band * 8);
-        t.nb = in / bm;
+        t.nb = fast_div(in, bm);
         mb = band * 8 + in - t.nb * bm;
     }
-    const int step = tile_step<MATH>(rows, most);
+    const int step = 16 * steps[t.g];
     t.local = mb * step;
     t.row0 = start[t.g] + t.local;
-    t.rows = min(step, rows - t.local);
+    t.rows = min(step, start[t.g + 1] - t.row0);
     t.width = (t.rows + 15) & ~15;
     return t;
 }
@@ -542,6 +551,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int *start = reinterpret_cast<int *>(sOut + NUM_EPI_WARPS * C::OUT_BYTES + 512 - 64);
     int *first = start + p.groups.G + 1;
     int *stile = first + p.groups.G + 1;          // rows of scale tiles before each group
+    // 16 rows of A: a tile of each group covers this many of them
+    uint8_t *steps = reinterpret_cast<uint8_t *>(F4 ? stile + p.groups.G + 1 : stile);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -580,6 +591,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                          ? C::TOKENS
                          : choose_rows<MATH>(start, G, p.n_blocks, p.k_blocks, (int)(gridDim.x >> 1),
                                              reinterpret_cast<float *>(scratch + 16));
+    for (int g = threadIdx.x; g < G; g += NUM_THREADS)
+        steps[g] = (uint8_t)(tile_step<MATH>(max(1, start[g + 1] - start[g]), most) / 16);
     tile_sums<NUM_THREADS>(G, start, first, scratch, [most](int n) { return ceil_div(n, most); });
     if (F4)
         tile_sums<NUM_THREADS>(G, start, stile, scratch, [](int n) { return ceil_div(n, 128); });
@@ -594,7 +607,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t armed = 0, armed_parity = 0;
             bool ok = true;
             for (int u = u0; u < units && ok; u += du) {
-                const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, most, u);
+                const GrpTile t = grp_tile(start, first, steps, G, p.n_blocks, u);
                 const int half = __shfl_sync(0xffffffffu, t.width, 0) / 2;
                 const int g = __shfl_sync(0xffffffffu, t.g, 0);
                 // the lowest box that holds this CTA's rows of A
@@ -672,7 +685,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             bool ok = true;
             int n = 0;
             for (int u = u0; u < units && ok; u += du, ++n) {
-                const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, most, u);
+                const GrpTile t = grp_tile(start, first, steps, G, p.n_blocks, u);
                 const uint32_t idesc =
                     __shfl_sync(0xffffffffu, p.idesc | ((uint32_t)(t.width >> 3) << 17), 0);
                 // a tile of A that begins at the second half of its scale tile
@@ -733,7 +746,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t buf = smem_u32(sOut + (warp - EPI_WARP0) * C::OUT_BYTES);
         int n = 0;
         for (int u = u0; u < units; u += du, ++n) {
-            const GrpTile t = grp_tile<MATH>(start, first, G, p.n_blocks, most, u);
+            const GrpTile t = grp_tile(start, first, steps, G, p.n_blocks, u);
             const int acc = n & 1;
             const int n0 = t.nb * 256 + (int)rank * 128 + q * 32;
             const bool work = n0 < p.N;

@@ -1,13 +1,12 @@
 // k_mx4.cu — microscaled 4-bit floating point: to 4 bits and back.
 //
 // Both directions stream: 2 bytes (16-bit x) and 1/2 + 1/32 or 1/16 bytes per
-// element, each once, so memory bounds them.  A CTA takes 256 columns of 32 of
-// the 128 rows of a row of scale tiles: those with r mod 32 in one eighth, in
-// fours r, r + 32, r + 64, r + 96 a warp, whose scales lie side by side in
-// memory.  A lane has 8 columns of each of its warp's four rows: one 16-byte
-// access of x and 4 bytes of codes per row.  A block's largest magnitude meets
-// across its 4 (MXFP4) or 2 (NVFP4) lanes, and four lanes swap their blocks'
-// scale bytes so that each stores 4 bytes of a tile.
+// element, each once; at 7 or 8 TB/s that leaves about 14 instructions per
+// element and lane, so the arithmetic is kept short too.  To 4 bits a lane has 16
+// columns (a block of NVFP4, half a block of MXFP4) of four rows r, r + 32, r + 64,
+// r + 96 of a row of scale tiles, whose scales lie side by side in memory; a
+// warp has 512 columns.  Lanes swap their blocks' scale bytes so that each
+// stores 4 bytes of a tile.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -22,7 +21,9 @@ namespace swg {
 namespace {
 
 constexpr int TILE_ROWS = 128;       // rows of a scale tile
-constexpr int TILE_COLS = 256;       // columns per CTA: 2 (MXFP4) or 4 (NVFP4) scale tiles
+constexpr int LANE_COLS = 16;        // columns per lane
+constexpr int TILE_COLS = 512;       // columns per CTA: 4 (MXFP4) or 8 (NVFP4) scale tiles
+constexpr int TILE_COLS_BACK = 256;  // ... of the way back, 8 per lane
 constexpr int THREADS = 256;
 constexpr int STRIPS = 4;            // CTAs per row of scale tiles
 constexpr int ROWS = 4;              // rows per warp, 32 apart
@@ -113,42 +114,80 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+// The largest magnitude of 8 stored values, NaN if one is NaN: of 16-bit
+// values two at a time.
+template <int TYPE>
+__device__ __forceinline__ float top8(const Raw8<TYPE> &r)
+{
+    if (TYPE == 2) {
+        float top = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t u[4] = {r.w[h % (TYPE == 2 ? 2 : 1)].x, r.w[h % (TYPE == 2 ? 2 : 1)].y,
+                                   r.w[h % (TYPE == 2 ? 2 : 1)].z, r.w[h % (TYPE == 2 ? 2 : 1)].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = max_nan(top, fabsf(__uint_as_float(u[j])));
+        }
+        return top;
+    }
+    uint32_t m[4] = {r.w[0].x & 0x7fff7fffu, r.w[0].y & 0x7fff7fffu, r.w[0].z & 0x7fff7fffu,
+                     r.w[0].w & 0x7fff7fffu};
+    if (TYPE == 1) {
+        auto h = [](uint32_t a) { return *reinterpret_cast<const __nv_bfloat162 *>(&a); };
+        const float2 f = __bfloat1622float2(
+            __hmax2_nan(__hmax2_nan(h(m[0]), h(m[1])), __hmax2_nan(h(m[2]), h(m[3]))));
+        return max_nan(f.x, f.y);
+    }
+    auto h = [](uint32_t a) { return *reinterpret_cast<const __half2 *>(&a); };
+    const float2 f = __half22float2(
+        __hmax2_nan(__hmax2_nan(h(m[0]), h(m[1])), __hmax2_nan(h(m[2]), h(m[3]))));
+    return max_nan(f.x, f.y);
+}
+
+// x / d from an approximation of 1 / d, with one residual correction
+// (Markstein's): a quotient that is itself a float comes out exact.
+__device__ __forceinline__ float quotient(float x, float d, float inverse)
+{
+    const float q = x * inverse;
+    return __fmaf_rn(__fmaf_rn(-q, d, x), inverse, q);
+}
+
 // The scale of a block whose largest magnitude is `top` (NaN if the block has
-// one): its byte; `scale` its value and `inverse` 1 / scale, both NaN for a
-// block with a NaN or an infinity.
+// one): its byte; `scale` its value and `inverse` about 1 / scale (exactly for
+// MXFP4), both NaN for a block with a NaN or an infinity.
 template <bool NV>
 __device__ __forceinline__ uint32_t block_scale(float top, float &scale, float &inverse)
 {
-    const uint32_t bits = __float_as_uint(top) & 0x7fffffffu;
+    const uint32_t bits = __float_as_uint(top);
     const float nan = __uint_as_float(0x7fffffffu);
     if (NV) {
         // to nearest even by the conversion, which saturates at 448
-        const uint32_t code = max(
-            (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(top, 6.0f), __NV_SATFINITE, __NV_E4M3), 1u);
+        const uint32_t code = max((uint32_t)__nv_cvt_float_to_fp8(quotient(top, 6.0f, 1.0f / 6.0f),
+                                                                  __NV_SATFINITE, __NV_E4M3),
+                                  1u);
         const bool bad = bits >= 0x7f800000u;
         scale = bad ? nan
                     : __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
-        inverse = __frcp_rn(scale);
+        inverse = __fdividef(1.0f, scale);
         return bad ? 0x7fu : code;
     }
     const uint32_t e = bits >> 23;                   // floor(log2 top) + 127
     const uint32_t code = e > 2 ? e - 2 : 0;
-    const bool bad = e == 255;
+    const bool bad = e >= 255;
     scale = bad ? nan : __uint_as_float(code > 0 ? code << 23 : 1u << 22);
-    inverse = bad ? nan : __uint_as_float((254u - code) << 23);       // 2^(127 - code), exact
+    inverse = bad ? nan : __uint_as_float((254u - code) << 23);       // 2^(127 - code)
     return bad ? 0xffu : code;
 }
 
 struct Place {
     int t;                   // row of scale tiles
-    int chunk;               // 256 columns
+    int chunk;               // of the CTA's columns
     int r32;                 // this warp's rows: r32, r32 + 32, ..
     int row0, end;           // first row of the tiles, end of their group
 };
 
 // This CTA's and warp's place; false for a CTA beyond the last group's tiles.
-__device__ __forceinline__ bool find_place(const Groups &gr, int chunks, int *err, int *table,
-                                           Place &p)
+__device__ __forceinline__ bool find_place(const Groups &gr, int chunks, int *err, Place &p)
 {
     const unsigned strip = blockIdx.x / (unsigned)chunks;
     p.chunk = (int)(blockIdx.x - strip * (unsigned)chunks);
@@ -159,70 +198,114 @@ __device__ __forceinline__ bool find_place(const Groups &gr, int chunks, int *er
         p.end = gr.M;
         return p.row0 < gr.M;
     }
-    int *start = table, *first = table + gr.G + 1, *sums = table + 2 * (gr.G + 1);
-    group_starts<THREADS>(gr, start, err);
-    tile_sums<THREADS>(gr.G, start, first, sums, [](int rows) { return ceil_div(rows, TILE_ROWS); });
-    if (p.t >= first[gr.G]) return false;
-    const int g = group_of(first, gr.G, 1, p.t);
-    p.row0 = start[g] + (p.t - first[g]) * TILE_ROWS;
-    p.end = start[g + 1];
-    return true;
+    // Every warp walks the groups itself, 32 at a time: a table for the CTA
+    // would cost it two barriers, and it has little to do.  (Offsets are
+    // clamped as in group_starts.)
+    const int lane = threadIdx.x & 31;
+    int top = 0, before = 0;                         // largest offset, tiles so far
+    bool bad = false;
+    for (int base = 0; base < gr.G; base += 32) {
+        const int g = base + lane;
+        auto offset = [&](int i) {
+            const int raw = gr.offsets[min(i, gr.G)];
+            const int v = raw < 0 ? 0 : raw > gr.M ? gr.M : raw;
+            bad = bad || v != raw;
+            return v;
+        };
+        int lo = max(offset(g), top), hi = offset(g + 1);
+        bad = bad || hi < lo;
+        hi = max(hi, lo);
+        if (__any_sync(0xffffffffu, bad)) {          // running maxima, the slow way
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, hi, d);
+                if (lane >= d) hi = max(hi, o);
+            }
+            const int o = __shfl_up_sync(0xffffffffu, hi, 1);
+            if (lane > 0) lo = max(lo, o);
+            if (lane == 0) atomicCAS(err, 0, ERR_INVALID);
+        }
+        const int n = g < gr.G ? ceil_div(hi - lo, TILE_ROWS) : 0;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        const int first = before + sum - n;
+        const unsigned mine = __ballot_sync(0xffffffffu, p.t >= first && p.t < first + n);
+        if (mine) {
+            const int src = __ffs(mine) - 1;
+            p.row0 = __shfl_sync(0xffffffffu, lo + (p.t - first) * TILE_ROWS, src);
+            p.end = __shfl_sync(0xffffffffu, hi, src);
+            return true;
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+        top = __shfl_sync(0xffffffffu, hi, 31);
+    }
+    return false;
 }
 
 template <int TYPE, bool NV>
 __global__ void __launch_bounds__(THREADS) quantize_kernel(const Mx4Args p, int chunks, int *err)
 {
-    constexpr int LANES = NV ? 2 : 4;                // lanes per block
-    constexpr int TILES = NV ? 4 : 2;                // scale tiles per CTA along K
-    extern __shared__ int table[];
+    constexpr int LANES = NV ? 1 : 2;                // lanes per block
+    constexpr int TILES = NV ? 8 : 4;                // scale tiles per CTA along K
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Place at;
-    if (!find_place(p.groups, chunks, err, table, at)) return;
+    if (!find_place(p.groups, chunks, err, at)) return;
     const int lane = threadIdx.x & 31;
-    const int k = at.chunk * TILE_COLS + lane * 8;
-    const int cnt = min(8, max(0, p.K - k));
-    const bool write = k < ((p.K + 31) & ~31);       // codes up to a multiple of 32 columns
-    const bool block = k - (lane % LANES) * 8 < p.K; // the lane's block has columns
-    Raw8<TYPE> raw[ROWS];
+    const int k = at.chunk * TILE_COLS + lane * LANE_COLS;
+    const int cnt = min(LANE_COLS, max(0, p.K - k));
+    const int width = min(LANE_COLS, max(0, ((p.K + 31) & ~31) - k));  // codes to write
+    const bool block = k - (lane % LANES) * LANE_COLS < p.K;           // the block has columns
+    Raw8<TYPE> raw[ROWS][2];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int row = at.row0 + at.r32 + 32 * i;
-        raw[i] = load8<TYPE>(p.X, (long long)row * p.ldx + k, row < at.end ? cnt : 0);
+        const long long o = (long long)row * p.ldx + k;
+        const int n = row < at.end ? cnt : 0;
+        raw[i][0] = load8<TYPE>(p.X, o, min(n, 8));
+        raw[i][1] = load8<TYPE>(p.X, o + 8, max(n - 8, 0));
     }
     uint32_t codes = 0;                              // the lane's block's scales, a byte per row
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int row = at.row0 + at.r32 + 32 * i;
-        float v[8], top = 0.0f;
-        to_floats<TYPE>(raw[i], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] *= p.scale;
-            top = max_nan(top, fabsf(v[j]));
-        }
-        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        if (!NV) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // (the factor is positive: the largest of the products is its product)
+        float top = p.scale * max_nan(top8<TYPE>(raw[i][0]), top8<TYPE>(raw[i][1]));
+        if (!NV) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
         float s, inv;
         const uint32_t code = block_scale<NV>(top, s, inv);
-        uint32_t q = 0;
+        uint32_t q[2];
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            float a = v[j] * inv, c = v[j + 1] * inv;
-            if (NV) {
-                // One residual correction (Markstein's): a quotient that is
-                // itself a float -- every tie between two codes is, for
-                // 16-bit x -- comes out exact, so ties go to even as in the
-                // definition; a * inv alone may miss them by a rounding.
-                a = __fmaf_rn(__fmaf_rn(-a, s, v[j]), inv, a);
-                c = __fmaf_rn(__fmaf_rn(-c, s, v[j + 1]), inv, c);
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+            to_floats<TYPE>(raw[i][h], v);
+            q[h] = 0;
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                float2 x = make_float2(p.scale * v[j], p.scale * v[j + 1]);
+                if (NV) {
+                    // Every tie between two codes is a quotient that is a float
+                    // (for 16-bit x), so ties go to even as in the definition;
+                    // the product with the inverse alone may miss them.
+                    const float2 inv2 = make_float2(inv, inv);
+                    const float2 y = __fmul2_rn(x, inv2);
+                    x = __ffma2_rn(__ffma2_rn(make_float2(-y.x, -y.y), make_float2(s, s), x), inv2, y);
+                } else {
+                    x = make_float2(x.x * inv, x.y * inv);
+                }
+                q[h] |= (uint32_t)__nv_cvt_float2_to_fp4x2(x, __NV_E2M1, cudaRoundNearest) << (4 * j);
             }
-            q |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(a, c), __NV_E2M1, cudaRoundNearest)
-                 << (4 * j);
         }
-        if (row < at.end && write)
-            *reinterpret_cast<uint32_t *>(p.Q + (long long)row * p.ldq + k / 2) = q;
-        if (row < at.end && block) codes |= code << (8 * i);
+        if (row < at.end) {
+            uint8_t *out = p.Q + (long long)row * p.ldq + k / 2;
+            if (width == 16)
+                *reinterpret_cast<uint2 *>(out) = make_uint2(q[0], q[1]);
+            if (block) codes |= code << (8 * i);
+        }
     }
     // Lane b of a tile's four blocks takes row b's four bytes and stores them.
     const int b = lane / LANES % 4, tile = lane / (4 * LANES);
@@ -239,18 +322,20 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Mx4Args p, int 
                                       4 * b) = word;
 }
 
+// Back: 8 columns per lane, so that a warp's stores of a row are whole lines
+// (with 16, as above, two stores share each 32-byte sector: 33 instead of 24 us
+// for 14336 x 4096 to bf16).
 template <int TYPE, bool NV>
 __global__ void __launch_bounds__(THREADS) dequantize_kernel(const Mx4Args p, int chunks, int *err)
 {
     constexpr int LANES = NV ? 2 : 4;
     constexpr int TILES = NV ? 4 : 2;
-    extern __shared__ int table[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Place at;
-    if (!find_place(p.groups, chunks, err, table, at)) return;
+    if (!find_place(p.groups, chunks, err, at)) return;
     const int lane = threadIdx.x & 31;
-    const int k = at.chunk * TILE_COLS + lane * 8;
+    const int k = at.chunk * TILE_COLS_BACK + lane * 8;
     const int cnt = min(8, max(0, p.K - k));
     if (cnt == 0) return;
     uint32_t q[ROWS];
@@ -272,9 +357,8 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const Mx4Args p, in
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-            const __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2(
-                (__nv_fp4x2_storage_t)((q[i] >> (4 * j)) & 0xffu), __NV_E2M1));
-            const float2 f = __half22float2(h);
+            const float2 f = __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2(
+                (__nv_fp4x2_storage_t)((q[i] >> (4 * j)) & 0xffu), __NV_E2M1)));
             v[j] = p.scale * (f.x * s);
             v[j + 1] = p.scale * (f.y * s);
         }
@@ -285,11 +369,11 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const Mx4Args p, in
 template <int TYPE, bool NV>
 cudaError_t launch(const Mx4Args &p, bool back, int tile_rows, int *err, cudaStream_t s)
 {
-    const int chunks = (p.K + TILE_COLS - 1) / TILE_COLS;
+    const int cols = back ? TILE_COLS_BACK : TILE_COLS;
+    const int chunks = (p.K + cols - 1) / cols;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)tile_rows * STRIPS * chunks));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = p.groups.offsets ? sizeof(int) * (2 * (p.groups.G + 1) + THREADS / 32) : 0;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
