@@ -602,10 +602,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (p.k_blocks > 0) {
+            const uint32_t empty0 = smem_u32(empty), full0 = smem_u32(full);
+            const uint32_t full_leader0 = mapa_shared(full0, 0);
+            const uint32_t w_dst0 = smem_u32(sW), t_dst0 = smem_u32(sT), s_dst0 = smem_u32(sS);
             int stage = 0;
             uint32_t phase = 0;
-            uint32_t armed = 0, armed_parity = 0;
-            bool ok = true;
+            bool ok = true, wrapped = false;
             for (int u = u0; u < units && ok; u += du) {
                 const GrpTile t = grp_tile(start, first, steps, G, p.n_blocks, u);
                 const int half = __shfl_sync(0xffffffffu, t.width, 0) / 2;
@@ -621,20 +623,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t t_bytes = box == 0 ? C::T_BYTES : (128u >> box) * 128u;
                 const uint32_t bytes = C::W_BYTES + t_bytes + 3 * C::SCALE_BYTES;
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!wait_bounded_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.err)) {
+                    if (!wait_bounded_warp(empty0 + 8 * stage, phase ^ 1, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
-                    armed |= 1u << stage;
-                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                    const uint32_t fb_local = smem_u32(&full[stage]);
-                    const uint32_t fb = mapa_shared(fb_local, 0);
-                    const uint32_t w_dst = smem_u32(sW + stage * C::W_BYTES);
-                    const uint32_t t_dst = smem_u32(sT + stage * C::T_BYTES);
+                    const uint32_t fb = full_leader0 + 8 * stage;
+                    const uint32_t w_dst = w_dst0 + stage * C::W_BYTES;
+                    const uint32_t t_dst = t_dst0 + stage * C::T_BYTES;
+                    const uint32_t s_dst = s_dst0 + stage * 3 * C::SCALE_BYTES;
                     const int k0 = kb * (F4 ? 128 : 64);     // inner coordinate of the boxes
+                    const int x = kb * (C::SCALE_BYTES / 8);
                     if (elect_one()) {
                         // both CTAs' bytes complete on the leader's barrier
-                        if (leader) mbar_arrive_expect_tx(fb_local, 2 * bytes);
+                        if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * bytes);
                         if (!p.w_mn) {
                             tma_load_3d_pair(w_dst, &maps.w, fb, k0, n0, g);
                         } else if (p.w_4d) {
@@ -645,24 +646,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         }
                         tma_load_2d_pair(t_dst, t_map, fb, k0, t_row);
                         if (F4) {
-                            const uint32_t s_dst = smem_u32(sS + stage * 3 * C::SCALE_BYTES);
-                            const int x = kb * (C::SCALE_BYTES / 8);
                             tma_load_2d_pair(s_dst, &maps.sw, fb, x, w_tile);
                             tma_load_2d_pair(s_dst + C::SCALE_BYTES, &maps.st, fb, x, t_tile);
                         }
                     }
-                    __syncwarp();
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1;
+                        wrapped = true;
                     }
                 }
             }
             // Never leave with loads in flight into this CTA's shared memory.
             if (leader) {
+                // (stages before `stage` were last used in this round, the others
+                // in the one before)
                 for (int s = 0; s < S; ++s)
-                    if (armed & (1u << s))
-                        wait_bounded(smem_u32(&full[s]), (armed_parity >> s) & 1, abort_flag,
+                    if (s < stage || wrapped)
+                        wait_bounded(full0 + 8 * s, s < stage ? phase : phase ^ 1, abort_flag,
                                      p.err, false, DRAIN_LIMIT_NS);
             } else if (!ok) {
                 const uint64_t t0 = global_timer_ns();
@@ -680,6 +681,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint64_t t_desc = smem_desc(smem_u32(sT), 16, 1024);
             const uint64_t s_desc = scale_desc(smem_u32(sS));
             const uint32_t w_kstep = p.w_mn ? 128u : 2u;
+            const uint32_t empty0 = smem_u32(empty), full0 = smem_u32(full);
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -699,7 +701,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t d_tmem = tmem_base + acc * C::ACC_STRIDE;
                 uint32_t accum = 0;
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!wait_bounded_warp(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
+                    if (!wait_bounded_warp(full0 + 8 * stage, phase, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
@@ -720,9 +722,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             issue_f4<MATH>(d_tmem, w_stage, t_stage, sd, idesc,
                                            tmem_base + C::SCALE_COL + (kb & 1) * 64, t_shift, accum);
                         }
-                        tc_commit_pair(smem_u32(&empty[stage]));
+                        tc_commit_pair(empty0 + 8 * stage);
                     }
-                    __syncwarp();
                     accum = 1;
                     if (++stage == S) {
                         stage = 0;
