@@ -68,7 +68,15 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
     if (int rc = swg::device_info(d)) return rc;
     const bool f4 = kind >= swg::GRP_MXFP4, nv = kind == swg::GRP_NVFP4;
     const int64_t M = a.groups.M, G = a.groups.G, N = a.N, K = a.K;
-    const int tokens = f4 ? swg::GrpCfg<swg::MATH_MX>::TOKENS : swg::GrpCfg<swg::MATH_16>::TOKENS;
+    const bool few = M <= swg::GrpCfg<swg::MATH_16, true>::TOKENS;
+    const int tokens = few  ? swg::GrpCfg<swg::MATH_16, true>::TOKENS
+                       : f4 ? swg::GrpCfg<swg::MATH_MX, false>::TOKENS
+                            : swg::GrpCfg<swg::MATH_16, false>::TOKENS;
+    // Boxes of A's rows: of box i (see GrpMaps) those that tiles of at most
+    // `half` rows per CTA can ask for.
+    const int64_t half = std::min<int64_t>(tokens, ceil_to(M, 16)) / 2;
+    auto box_rows = [&](int i) { return i == 0 ? tokens / 2u : 128u >> i; };
+    auto box_used = [&](int i) { return i + 1 == swg::TOKEN_BOXES || half > (64 >> i); };
 
     swg::GrpParams p{};
     p.groups = a.groups;
@@ -116,8 +124,9 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
             ok = encode_tiled(&m.w, type, 3, a.B, dims, st, box, 128);
         }
         for (int i = 0; i < swg::TOKEN_BOXES && ok; ++i) {
+            if (!box_used(i)) continue;
             const uint64_t dims[] = {(uint64_t)K, (uint64_t)M}, st[] = {(uint64_t)a.lda * 2};
-            const uint32_t box[] = {64, i == 0 ? tokens / 2u : 128u >> i};
+            const uint32_t box[] = {64, box_rows(i)};
             ok = encode_tiled(&m.t[i], type, 2, a.A, dims, st, box, 128);
         }
     } else if (K > 0) {
@@ -130,19 +139,20 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
         const uint32_t wbox[] = {128, 128, 1};
         ok = encode_tiled(&m.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.B, wd, wst, wbox, 128);
         for (int i = 0; i < swg::TOKEN_BOXES && ok; ++i) {
+            if (!box_used(i)) continue;
             const uint64_t dims[] = {row, (uint64_t)M}, st[] = {(uint64_t)a.lda};
-            const uint32_t box[] = {128, i == 0 ? tokens / 2u : 128u >> i};
+            const uint32_t box[] = {128, box_rows(i)};
             ok = encode_tiled(&m.t[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.A, dims, st, box, 128);
         }
         // Scale tiles as rows of 64-bit elements, one row per 128 rows of the
-        // matrix: a box is one stage's tiles (1 KB or 2 KB) of one row, two for A
+        // matrix: a box is one stage's tiles (1 KB or 2 KB) of one row, for A of as many as a tile spans
         const int tile_k = nv ? 64 : 128;
         const uint64_t tiles = (uint64_t)(K + tile_k - 1) / tile_k * 64;
         const uint64_t sst[] = {tiles * 8};
         const uint64_t swd[] = {tiles, (uint64_t)(p.w_tiles * G)};
         const uint64_t std_[] = {tiles, (uint64_t)(M / 128 + G)};
         const uint32_t per = nv ? 256u : 128u;
-        const uint32_t swbox[] = {per, 1}, stbox[] = {per, 2};
+        const uint32_t swbox[] = {per, 1}, stbox[] = {per, few ? 1u : 2u};
         ok = ok && encode_tiled(&m.sw, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, a.SB, swd, sst, swbox, 0);
         ok = ok && encode_tiled(&m.st, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, a.SA, std_, sst, stbox, 0);
     }
@@ -157,17 +167,18 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
         p.tma_out = a.out_kind != swg::OUT_F32 && a.beta == 0.0f && N % 8 == 0 && M >= 32;
         if (p.tma_out) ok = ok && out_map(&m.c, a.C, N, a.ldc, 32, 64);
     } else {
-        p.tma_out = 1;
-        ok = ok && (epi == swg::GRP_SWIGLU ? out_map(&m.c, a.C, N / 2, a.ldc, 16, 0)
+        p.tma_out = M >= 32;
+        if (p.tma_out)
+            ok = ok && (epi == swg::GRP_SWIGLU ? out_map(&m.c, a.C, N / 2, a.ldc, 16, 0)
                                            : out_map(&m.c, a.C, N, a.ldc, 32, 0));
-        if (a.Y) ok = ok && out_map(&m.y, a.Y, N / 2, N / 2, 16, 0);
+        if (a.Y && p.tma_out) ok = ok && out_map(&m.y, a.Y, N / 2, N / 2, 16, 0);
     }
     if (!ok) return swg::record_cuda_error();
     // (tiles of as few as 128 rows may be chosen)
     const long long units = (M / 128 + std::min(G, M)) * (long long)p.n_blocks;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return swg::count_launch(f4 ? swg::launch_grouped_f4(nv, epi, m, p, units, d.sms, s)
-                                : swg::launch_grouped_16(epi, m, p, units, d.sms, s));
+    return swg::count_launch(f4 ? swg::launch_grouped_f4(nv, epi, few, m, p, units, d.sms, s)
+                                : swg::launch_grouped_16(epi, few, m, p, units, d.sms, s));
 }
 
 }  // namespace

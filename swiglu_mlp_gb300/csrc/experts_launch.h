@@ -26,10 +26,11 @@ cudaError_t launch_mx4(const Mx4Args &p, bool back, int tile_rows, int *err, cud
 
 struct GrpMaps;
 struct GrpParams;
-// `units`: an upper bound of the tiles over all groups.
-cudaError_t launch_grouped_16(GrpEpi epi, const GrpMaps &m, const GrpParams &p, long long units,
+// `units`: an upper bound of the tiles over all groups; `few`: the form for few
+// rows of A (GrpCfg).
+cudaError_t launch_grouped_16(GrpEpi epi, bool few, const GrpMaps &m, const GrpParams &p, long long units,
                               int sms, cudaStream_t s);
-cudaError_t launch_grouped_f4(bool nv, GrpEpi epi, const GrpMaps &m, const GrpParams &p,
+cudaError_t launch_grouped_f4(bool nv, GrpEpi epi, bool few, const GrpMaps &m, const GrpParams &p,
                               long long units, int sms, cudaStream_t s);
 
 struct WgradArgs {

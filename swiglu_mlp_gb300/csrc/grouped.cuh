@@ -131,40 +131,52 @@ struct GrpParams {
     int *err;
 };
 
-template <int MATH>
+// FEW: the form for at most 64 rows of A in all, which streams weights from
+// memory.  Its stages hold 64 rows of A instead of 256 (192) and are 8 to 10
+// instead of 5 or 6, so that more of the weight is in flight.  (Two CTAs of
+// half the depth per SM instead were slower: 8 groups of one row, 4096 x 1024
+// each, 21.4 us against 18.2 with 6 stages.)
+template <int MATH, bool FEW>
 struct GrpCfg {
     static constexpr bool F4 = MATH != MATH_16;
     // Rows of A per tile: two accumulators fill tensor memory at 256; with
     // scales there they leave room at 192.
-    static constexpr int TOKENS = F4 ? 192 : 256;
+    static constexpr int TOKENS = FEW ? 64 : F4 ? 192 : 256;
     // A tile begins at a multiple of UNIT rows of its group (4-bit: 64 rows are
     // two columns of scales) and may be CANDIDATES widths, see choose_rows.
     static constexpr int UNIT = F4 ? 64 : 16;
-    static constexpr int CANDIDATES = F4 ? 2 : 8;
+    static constexpr int CANDIDATES = FEW ? 1 : F4 ? 2 : 8;
+    static constexpr int EPI_WARPS = FEW ? 4 : 8;
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int TILES_PER_STAGE = MATH == MATH_NV ? 4 : 2;   // scale tiles along K
+    static constexpr int SCALE_ROWS = FEW ? 1 : 2;                    // rows of tiles of A's scales
     static constexpr int SCALE_BYTES = F4 ? 512 * TILES_PER_STAGE : 0;
+    static constexpr int STAGE_SCALES = (1 + SCALE_ROWS) * SCALE_BYTES;
     static constexpr int W_BYTES = 128 * 128;
     static constexpr int T_BYTES = TOKENS / 2 * 128;
-    static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + 3 * SCALE_BYTES;
-    static constexpr int OUT_BYTES = 3072;        // per epilogue warp, see the epilogue
-    static constexpr int TABLE_BYTES = (F4 ? 3 : 2) * 4 * (MAX_GROUPS + 1) + MAX_GROUPS;
-    static constexpr int FIXED = 1024 + NUM_EPI_WARPS * OUT_BYTES + TABLE_BYTES + 512;
-    static constexpr int STAGES_RAW = (232448 - FIXED) / STAGE_BYTES;
-    static constexpr int STAGES = STAGES_RAW > 6 ? 6 : STAGES_RAW;
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + FIXED;
+    static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + STAGE_SCALES;
+    static constexpr int OUT_BYTES = F4 ? 2048 : 3072;   // per epilogue warp, see the epilogue
+    static constexpr int BAR_BYTES = 512;
+    static constexpr int FIXED = 1024 + EPI_WARPS * OUT_BYTES + BAR_BYTES;
+    static constexpr int table_bytes(int G) { return (F4 ? 3 : 2) * 4 * (G + 1) + G; }
+    static constexpr int LIMIT = 232448 - FIXED - table_bytes(MAX_GROUPS);
+    static constexpr int STAGES_RAW = LIMIT / STAGE_BYTES;
+    static constexpr int STAGES = STAGES_RAW > 6 && !FEW ? 6 : STAGES_RAW;
+    static constexpr int smem_bytes(int G) { return STAGES * STAGE_BYTES + FIXED + table_bytes(G); }
     static constexpr int ACC_STRIDE = TOKENS;     // tensor-memory columns per accumulator
     static constexpr int SCALE_COL = 2 * TOKENS;  // first scale column (two buffers of 64)
-    static_assert(STAGES >= 4, "pipeline too shallow");
-    static_assert(!F4 || 2 * TOKENS + 128 <= 512, "tensor memory");
+    static constexpr int TMEM_COLS = !FEW ? 512 : F4 ? 256 : 128;
+    static_assert(STAGES >= 3, "pipeline too shallow");
+    static_assert(2 * TOKENS + (F4 ? 128 : 0) <= TMEM_COLS, "tensor memory");
 };
 
 // Rows of A covered by each tile of a group of `rows` (> 0) rows, but the
 // last, when tiles have at most `most` rows.
-template <int MATH>
+template <class C>
 __device__ __forceinline__ int tile_step(int rows, int most)
 {
     const int t = ceil_div(rows, most);
-    constexpr int UNIT = GrpCfg<MATH>::UNIT;
+    constexpr int UNIT = C::UNIT;
     return ceil_div(ceil_div(rows, t), UNIT) * UNIT;
 }
 
@@ -176,11 +188,10 @@ __device__ __forceinline__ int tile_step(int rows, int most)
 // and issuing), and a tile about 0.8 us besides.  994 tiles on 76 pairs are
 // 13.1 waves at 256 rows; 1064 tiles of at most 240 make 14.0 and are 7% faster.
 // Warp w of the first eight computes candidate w's; ends with a barrier.
-template <int MATH>
+template <class C>
 __device__ __forceinline__ int choose_rows(const int *start, int G, int n_blocks, int k_blocks,
                                            int pairs, float *costs)
 {
-    using C = GrpCfg<MATH>;
     constexpr int CANDS = C::CANDIDATES;
     const int lane = threadIdx.x & 31, cand = threadIdx.x >> 5;
     if (cand < CANDS) {
@@ -495,18 +506,18 @@ __device__ __forceinline__ void emit_swiglu(const GrpParams &p, const GrpMaps &m
 // 4 columns per tile of this CTA's weight rows, then 8 per tile of A -- its
 // rows 0..127 and 128..255), then four K steps.  Consecutive stages alternate
 // between two sets of columns.
-template <int MATH>
+template <int MATH, class C>
 __device__ __forceinline__ void issue_f4(uint32_t d_tmem, uint64_t w, uint64_t t, uint64_t s,
                                          uint32_t idesc, uint32_t sf, uint32_t t_shift,
                                          uint32_t accum)
 {
-    using C = GrpCfg<MATH>;
     const uint32_t st = sf + 4 * C::TILES_PER_STAGE;
 #pragma unroll
     for (int i = 0; i < C::TILES_PER_STAGE; ++i) {
         tc_cp_scales_pair(sf + 4 * i, s + i * 32);
         tc_cp_scales_pair(st + 8 * i, s + (C::SCALE_BYTES >> 4) + i * 32);
-        tc_cp_scales_pair(st + 8 * i + 4, s + 2 * (C::SCALE_BYTES >> 4) + i * 32);
+        if (C::SCALE_ROWS == 2)
+            tc_cp_scales_pair(st + 8 * i + 4, s + 2 * (C::SCALE_BYTES >> 4) + i * 32);
     }
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
@@ -524,11 +535,11 @@ __device__ __forceinline__ void issue_f4(uint32_t d_tmem, uint64_t w, uint64_t t
 
 // ------------------------------------------------------------ kernel
 
-template <int MATH, int EPI>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+template <int MATH, int EPI, bool FEW>
+__global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
     grouped_kernel(const __grid_constant__ GrpMaps maps, const GrpParams p)
 {
-    using C = GrpCfg<MATH>;
+    using C = GrpCfg<MATH, FEW>;
     constexpr bool F4 = C::F4;
     constexpr int S = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -538,8 +549,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint8_t *sW = smem;
     uint8_t *sT = sW + S * C::W_BYTES;
     uint8_t *sS = sT + S * C::T_BYTES;
-    uint8_t *sOut = sS + S * 3 * C::SCALE_BYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sOut + NUM_EPI_WARPS * C::OUT_BYTES);
+    uint8_t *sOut = sS + S * C::STAGE_SCALES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sOut + C::EPI_WARPS * C::OUT_BYTES);
     uint64_t *full = bars;
     uint64_t *empty = bars + S;
     uint64_t *acc_full = bars + 2 * S;
@@ -548,7 +559,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 2 * S + 5);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *scratch = reinterpret_cast<int *>(tmem_holder + 4);      // 16 ints, 8 floats
-    int *start = reinterpret_cast<int *>(sOut + NUM_EPI_WARPS * C::OUT_BYTES + 512 - 64);
+    int *start = reinterpret_cast<int *>(sOut + C::EPI_WARPS * C::OUT_BYTES + C::BAR_BYTES);
     int *first = start + p.groups.G + 1;
     int *stile = first + p.groups.G + 1;          // rows of scale tiles before each group
     // 16 rows of A: a tile of each group covers this many of them
@@ -568,14 +579,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&acc_full[b]), 1);
-            mbar_init(smem_u32(&acc_empty[b]), 2 * NUM_EPI_WARPS);
+            mbar_init(smem_u32(&acc_empty[b]), 2 * C::EPI_WARPS);
         }
         mbar_init(smem_u32(mma_done), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc_pair(smem_u32(tmem_holder), 512);
+        tmem_alloc_pair(smem_u32(tmem_holder), C::TMEM_COLS);
         tmem_relinquish_pair();
     }
     tc_fence_before();
@@ -585,17 +596,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // Up to here only this pair's own resources; now the offsets may be read.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int G = p.groups.G;
-    group_starts<NUM_THREADS>(p.groups, start, p.err);
+    group_starts<C::THREADS>(p.groups, start, p.err);
     // (tiles of one width do for groups that all fit the narrowest)
     const int most = p.groups.M <= C::TOKENS - (C::CANDIDATES - 1) * C::UNIT
                          ? C::TOKENS
-                         : choose_rows<MATH>(start, G, p.n_blocks, p.k_blocks, (int)(gridDim.x >> 1),
+                         : choose_rows<C>(start, G, p.n_blocks, p.k_blocks, (int)(gridDim.x >> 1),
                                              reinterpret_cast<float *>(scratch + 16));
-    for (int g = threadIdx.x; g < G; g += NUM_THREADS)
-        steps[g] = (uint8_t)(tile_step<MATH>(max(1, start[g + 1] - start[g]), most) / 16);
-    tile_sums<NUM_THREADS>(G, start, first, scratch, [most](int n) { return ceil_div(n, most); });
+    for (int g = threadIdx.x; g < G; g += C::THREADS)
+        steps[g] = (uint8_t)(tile_step<C>(max(1, start[g + 1] - start[g]), most) / 16);
+    tile_sums<C::THREADS>(G, start, first, scratch, [most](int n) { return ceil_div(n, most); });
     if (F4)
-        tile_sums<NUM_THREADS>(G, start, stile, scratch, [](int n) { return ceil_div(n, 128); });
+        tile_sums<C::THREADS>(G, start, stile, scratch, [](int n) { return ceil_div(n, 128); });
     const int units = first[G] * p.n_blocks;
     const int u0 = (int)(blockIdx.x >> 1), du = (int)(gridDim.x >> 1);
 
@@ -621,7 +632,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int w_tile = g * p.w_tiles + n0 / 128;
                 const int t_tile = F4 ? __shfl_sync(0xffffffffu, stile[t.g] + t.local / 128, 0) : 0;
                 const uint32_t t_bytes = box == 0 ? C::T_BYTES : (128u >> box) * 128u;
-                const uint32_t bytes = C::W_BYTES + t_bytes + 3 * C::SCALE_BYTES;
+                const uint32_t bytes = C::W_BYTES + t_bytes + C::STAGE_SCALES;
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
                     if (!wait_bounded_warp(empty0 + 8 * stage, phase ^ 1, abort_flag, p.err)) {
                         ok = false;
@@ -630,7 +641,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const uint32_t fb = full_leader0 + 8 * stage;
                     const uint32_t w_dst = w_dst0 + stage * C::W_BYTES;
                     const uint32_t t_dst = t_dst0 + stage * C::T_BYTES;
-                    const uint32_t s_dst = s_dst0 + stage * 3 * C::SCALE_BYTES;
+                    const uint32_t s_dst = s_dst0 + stage * C::STAGE_SCALES;
                     const int k0 = kb * (F4 ? 128 : 64);     // inner coordinate of the boxes
                     const int x = kb * (C::SCALE_BYTES / 8);
                     if (elect_one()) {
@@ -718,8 +729,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 tc_mma_f16_pair(d_tmem, w_stage + kk * w_kstep, t_stage + kk * 2,
                                                 idesc, accum | kk);
                         } else {
-                            const uint64_t sd = s_desc + (uint64_t)(stage * 3 * (C::SCALE_BYTES >> 4));
-                            issue_f4<MATH>(d_tmem, w_stage, t_stage, sd, idesc,
+                            const uint64_t sd = s_desc + (uint64_t)(stage * (C::STAGE_SCALES >> 4));
+                            issue_f4<MATH, C>(d_tmem, w_stage, t_stage, sd, idesc,
                                            tmem_base + C::SCALE_COL + (kb & 1) * 64, t_shift, accum);
                         }
                         tc_commit_pair(empty0 + 8 * stage);
@@ -743,7 +754,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;                 // tensor-memory lane quarter of this warp
-        const int h = (warp - EPI_WARP0) / 4;   // takes every second chunk of 32 rows of A
+        const int h = (warp - EPI_WARP0) / 4;   // of HALVES warps a quarter: every HALVES-th
+        constexpr int HALVES = C::EPI_WARPS / 4;    // chunk of 32 rows of A
         const uint32_t buf = smem_u32(sOut + (warp - EPI_WARP0) * C::OUT_BYTES);
         int n = 0;
         for (int u = u0; u < units; u += du, ++n) {
@@ -774,7 +786,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * C::ACC_STRIDE;
 #pragma unroll 1
-            for (int c = h; c < chunks && work; c += 2) {
+            for (int c = h; c < chunks && work; c += HALVES) {
                 const int row = t.row0 + c * 32, rows = min(32, t.rows - c * 32);
                 if (EPI == GRP_STORE) {
                     if (p.out_kind != OUT_F32 && p.beta == 0.0f && p.k_blocks > 0)
@@ -792,7 +804,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     for (int j = 0; j < 32; ++j) r[j] = 0;
                 }
                 emit_swiglu<EPI>(p, maps, r, dy, row, rows, n0, buf, lane);
-                if (c + 2 < chunks) load_dy(c + 2);
+                if (c + HALVES < chunks) load_dy(c + HALVES);
             }
             if (p.k_blocks > 0) {
                 tc_fence_before();
@@ -808,7 +820,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+    if (warp == 1) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
 }
 
 }  // namespace swg

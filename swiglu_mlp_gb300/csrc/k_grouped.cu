@@ -3,15 +3,21 @@
 
 namespace swg {
 
-cudaError_t launch_grouped_16(GrpEpi epi, const GrpMaps &m, const GrpParams &p, long long units,
-                              int sms, cudaStream_t s)
+template <bool FEW>
+static cudaError_t launch_16(GrpEpi epi, const GrpMaps &m, const GrpParams &p, long long units,
+                             int sms, cudaStream_t s)
 {
-    constexpr int smem = GrpCfg<MATH_16>::SMEM_BYTES;
     switch (epi) {
-    case GRP_STORE: return launch_pairs<grouped_kernel<MATH_16, GRP_STORE>, NUM_THREADS>(smem, units, sms, s, m, p);
-    case GRP_SWIGLU: return launch_pairs<grouped_kernel<MATH_16, GRP_SWIGLU>, NUM_THREADS>(smem, units, sms, s, m, p);
-    default: return launch_pairs<grouped_kernel<MATH_16, GRP_DSWIGLU>, NUM_THREADS>(smem, units, sms, s, m, p);
+    case GRP_STORE: return launch_grouped_kernel<MATH_16, GRP_STORE, FEW>(m, p, units, sms, s);
+    case GRP_SWIGLU: return launch_grouped_kernel<MATH_16, GRP_SWIGLU, FEW>(m, p, units, sms, s);
+    default: return launch_grouped_kernel<MATH_16, GRP_DSWIGLU, FEW>(m, p, units, sms, s);
     }
+}
+
+cudaError_t launch_grouped_16(GrpEpi epi, bool few, const GrpMaps &m, const GrpParams &p,
+                              long long units, int sms, cudaStream_t s)
+{
+    return few ? launch_16<true>(epi, m, p, units, sms, s) : launch_16<false>(epi, m, p, units, sms, s);
 }
 
 }  // namespace swg

@@ -446,7 +446,7 @@ cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, 
     }
     if (!mapped) return cudaErrorInvalidValue;
     const long long units = (long long)a.groups.G * p.k_tiles * p.n_tiles;
-    return launch_pairs<wgrad_kernel, WG_THREADS>(SMEM_BYTES, units, sms, s, m, p);
+    return launch_pairs<wgrad_kernel, WG_THREADS>(SMEM_BYTES, SMEM_BYTES, units, sms, s, m, p);
 }
 
 }  // namespace swg
