@@ -60,6 +60,17 @@ bool too_big(std::initializer_list<int64_t> v)
 int block_of(int format) { return format == SWG_NVFP4 ? 16 : 32; }
 bool known_format(int format) { return format == SWG_MXFP4 || format == SWG_NVFP4; }
 
+// How many K ranges a product of `tiles` tiles (an upper bound) on `pairs` pairs
+// of CTAs is cut into: as many as there are pairs for, of at least 8 stages
+// each, when that saves a tile at least 14 stages.  (A stage takes 0.2 us, the
+// second kernel and the partials about 2: one row, 4096 x 4096, 17.1 us in one
+// range and 11.6 in four.)
+int pick_splits(int64_t tiles, int k_blocks, int pairs)
+{
+    const int64_t s = std::min<int64_t>({8, pairs / std::max<int64_t>(tiles, 1), k_blocks / 8});
+    return s >= 2 && k_blocks - k_blocks / s >= 14 ? (int)s : 1;
+}
+
 // Tensor maps and parameters of a grouped product, and its launch.
 int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void *stream)
 {
@@ -156,6 +167,47 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
         ok = ok && encode_tiled(&m.sw, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, a.SB, swd, sst, swbox, 0);
         ok = ok && encode_tiled(&m.st, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, a.SA, std_, sst, stbox, 0);
     }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t tiles = (M / tokens + std::min(G, M)) * (int64_t)p.n_blocks;
+    const int splits = pick_splits(tiles, p.k_blocks, d.sms / 2);
+    p.splits = 1;
+    p.split_blocks = p.k_blocks;
+    if (splits > 1) {
+        // Partials of the K ranges to the workspace, then their sum and the epilogue.
+        p.split_blocks = (p.k_blocks + splits - 1) / splits;
+        p.splits = (p.k_blocks + p.split_blocks - 1) / p.split_blocks;
+        swg::ReduceArgs r{};
+        r.ld = ceil_to(N, 8);
+        r.stride = r.ld * M;
+        float *ws = nullptr;
+        if (int rc = swg::stream_workspace(s, sizeof(float) * (size_t)p.splits * (size_t)r.stride, ws))
+            return rc;
+        r.ws = ws;
+        r.splits = p.splits;
+        r.rows = (int)M;
+        r.N = a.N;
+        r.groups = a.groups;
+        r.C = a.C;
+        r.ldc = a.ldc;
+        r.dY = a.dY;
+        r.Y = a.Y;
+        r.alpha = a.alpha;
+        r.beta = a.beta;
+        r.out_kind = a.out_kind;
+        p.C = ws;
+        p.ldc = r.ld;
+        p.split_stride = r.stride;
+        p.alpha = 1.0f;
+        p.beta = 0.0f;
+        p.out_kind = swg::OUT_F32;
+        if (!ok) return swg::record_cuda_error();
+        const long long units = tiles * p.splits;
+        if (int rc = swg::count_launch(
+                f4 ? swg::launch_grouped_f4(nv, swg::GRP_STORE, few, m, p, units, d.sms, s)
+                   : swg::launch_grouped_16(swg::GRP_STORE, few, m, p, units, d.sms, s)))
+            return rc;
+        return swg::count_launch(swg::launch_reduce(r, epi, d.sms, s));
+    }
     // 16-bit outputs in boxes of 32 rows: 64 bytes (or 32, a SwiGLU output) wide.  TMA
     // clips a row at 16-byte granules, so the columns must end on one.
     auto out_map = [&](CUtensorMap *map, void *ptr, int64_t cols, int64_t ld, uint32_t width, int sw) {
@@ -176,7 +228,6 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
     if (!ok) return swg::record_cuda_error();
     // (tiles of as few as 128 rows may be chosen)
     const long long units = (M / 128 + std::min(G, M)) * (long long)p.n_blocks;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     return swg::count_launch(f4 ? swg::launch_grouped_f4(nv, epi, few, m, p, units, d.sms, s)
                                 : swg::launch_grouped_16(epi, few, m, p, units, d.sms, s));
 }
@@ -259,10 +310,42 @@ int gemm_grouped_wgrad(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, 
     p.out_kind = out;
     swg::DeviceInfo d;
     if (int rc = swg::device_info(d)) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // The rows of a group cut into ranges, as pick_splits cuts K; how many rows
+    // a group has is not known here, so their mean decides.
+    const int64_t tiles = G * ((K + 255) / 256) * ((N + 255) / 256);
+    p.splits = pick_splits(tiles, (int)(M / 64 / G), d.sms / 2);
+    swg::ReduceArgs r{};
+    if (p.splits > 1) {
+        r.ld = ceil_to(N, 8);
+        r.stride = r.ld * K * G;
+        float *ws = nullptr;
+        if (int rc = swg::stream_workspace(s, sizeof(float) * (size_t)p.splits * (size_t)r.stride, ws))
+            return rc;
+        r.ws = ws;
+        r.splits = p.splits;
+        r.rows = (int)(K * G);
+        r.N = (int)N;
+        r.per_group = (int)K;
+        r.C = C;
+        r.ldc = ldc;
+        r.strideC = p.strideC;
+        r.alpha = alpha;
+        r.beta = beta;
+        r.out_kind = out;
+        p.C = ws;
+        p.ldc = r.ld;
+        p.strideC = r.ld * K;
+        p.split_stride = r.stride;
+        p.alpha = 1.0f;
+        p.beta = 0.0f;
+        p.out_kind = swg::OUT_F32;
+    }
     bool mapped = true;
-    const cudaError_t e =
-        swg::launch_wgrad(p, d.sms, d.err, static_cast<cudaStream_t>(stream), mapped);
-    return mapped ? swg::count_launch(e) : swg::record_cuda_error();
+    const cudaError_t e = swg::launch_wgrad(p, d.sms, d.err, s, mapped);
+    if (!mapped) return swg::record_cuda_error();
+    if (int rc = swg::count_launch(e)) return rc;
+    return p.splits > 1 ? swg::count_launch(swg::launch_reduce(r, swg::GRP_STORE, d.sms, s)) : SWG_OK;
 }
 
 static int swiglu_grouped_impl(const void *A, const void *W, const void *dY, void *Y, void *dH,

@@ -128,6 +128,10 @@ struct GrpParams {
     void *Y;
     int out_kind;
     int tma_out;                         // whole chunks of 32 rows leave through TMA stores
+    // K cut into `splits` ranges of split_blocks stages: range s of a tile is a
+    // unit of its own and goes to C + s * split_stride (FP32 partials).
+    int splits, split_blocks;
+    long long split_stride;
     int *err;
 };
 
@@ -416,11 +420,12 @@ __device__ __forceinline__ void emit_store_16(const GrpParams &p, const CUtensor
     }
 }
 
-// The same for FP32 results, with beta, and for K = 0 (no accumulator): each
+// The same for FP32 results (and partials of K ranges), with beta, and for K = 0 (no accumulator): each
 // lane is a column, its stores (and loads of C) of one row are 64 or 128 bytes
 // a warp.
-__device__ __forceinline__ void emit_store_direct(const GrpParams &p, uint32_t taddr, int row,
-                                                  int rows, int n0, int lane)
+__device__ __forceinline__ void emit_store_direct(const GrpParams &p, uint32_t taddr,
+                                                  long long offset, int row, int rows, int n0,
+                                                  int lane)
 {
     const int n = n0 + lane;
 #pragma unroll 1
@@ -431,7 +436,7 @@ __device__ __forceinline__ void emit_store_direct(const GrpParams &p, uint32_t t
             tmem_ld_wait(acc);
         }
         if (n >= p.N) continue;
-        const long long o = (row + j0) * p.ldc + n;
+        const long long o = offset + (row + j0) * p.ldc + n;
         float v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = p.alpha * __uint_as_float(acc[j]);
@@ -607,12 +612,20 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
     tile_sums<C::THREADS>(G, start, first, scratch, [most](int n) { return ceil_div(n, most); });
     if (F4)
         tile_sums<C::THREADS>(G, start, stile, scratch, [](int n) { return ceil_div(n, 128); });
-    const int units = first[G] * p.n_blocks;
+    const int units = first[G] * p.n_blocks * p.splits;
     const int u0 = (int)(blockIdx.x >> 1), du = (int)(gridDim.x >> 1);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (p.k_blocks > 0) {
+            if (lane == 0) {                         // fetched from memory on first use
+                tma_prefetch_desc(&maps.t[TOKEN_BOXES - 1]);
+                if (F4) {
+                    tma_prefetch_desc(&maps.sw);
+                    tma_prefetch_desc(&maps.st);
+                }
+            }
+            __syncwarp();
             const uint32_t empty0 = smem_u32(empty), full0 = smem_u32(full);
             const uint32_t full_leader0 = mapa_shared(full0, 0);
             const uint32_t w_dst0 = smem_u32(sW), t_dst0 = smem_u32(sT), s_dst0 = smem_u32(sS);
@@ -620,7 +633,11 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
             uint32_t phase = 0;
             bool ok = true, wrapped = false;
             for (int u = u0; u < units && ok; u += du) {
-                const GrpTile t = grp_tile(start, first, steps, G, p.n_blocks, u);
+                const int split = p.splits == 1 ? 0 : u % p.splits;
+                const GrpTile t = grp_tile(start, first, steps, G, p.n_blocks,
+                                           p.splits == 1 ? u : u / p.splits);
+                const int kb0 = split * p.split_blocks;
+                const int kb1 = min(kb0 + p.split_blocks, p.k_blocks);
                 const int half = __shfl_sync(0xffffffffu, t.width, 0) / 2;
                 const int g = __shfl_sync(0xffffffffu, t.g, 0);
                 // the lowest box that holds this CTA's rows of A
@@ -633,7 +650,7 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
                 const int t_tile = F4 ? __shfl_sync(0xffffffffu, stile[t.g] + t.local / 128, 0) : 0;
                 const uint32_t t_bytes = box == 0 ? C::T_BYTES : (128u >> box) * 128u;
                 const uint32_t bytes = C::W_BYTES + t_bytes + C::STAGE_SCALES;
-                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait_bounded_warp(empty0 + 8 * stage, phase ^ 1, abort_flag, p.err)) {
                         ok = false;
                         break;
@@ -698,7 +715,11 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
             bool ok = true;
             int n = 0;
             for (int u = u0; u < units && ok; u += du, ++n) {
-                const GrpTile t = grp_tile(start, first, steps, G, p.n_blocks, u);
+                const int split = p.splits == 1 ? 0 : u % p.splits;
+                const GrpTile t = grp_tile(start, first, steps, G, p.n_blocks,
+                                           p.splits == 1 ? u : u / p.splits);
+                const int kb0 = split * p.split_blocks;
+                const int kb1 = min(kb0 + p.split_blocks, p.k_blocks);
                 const uint32_t idesc =
                     __shfl_sync(0xffffffffu, p.idesc | ((uint32_t)(t.width >> 3) << 17), 0);
                 // a tile of A that begins at the second half of its scale tile
@@ -711,7 +732,7 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * C::ACC_STRIDE;
                 uint32_t accum = 0;
-                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait_bounded_warp(full0 + 8 * stage, phase, abort_flag, p.err)) {
                         ok = false;
                         break;
@@ -759,7 +780,9 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
         const uint32_t buf = smem_u32(sOut + (warp - EPI_WARP0) * C::OUT_BYTES);
         int n = 0;
         for (int u = u0; u < units; u += du, ++n) {
-            const GrpTile t = grp_tile(start, first, steps, G, p.n_blocks, u);
+            const int split = p.splits == 1 ? 0 : u % p.splits;
+            const GrpTile t = grp_tile(start, first, steps, G, p.n_blocks,
+                                       p.splits == 1 ? u : u / p.splits);
             const int acc = n & 1;
             const int n0 = t.nb * 256 + (int)rank * 128 + q * 32;
             const bool work = n0 < p.N;
@@ -792,7 +815,7 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
                     if (p.out_kind != OUT_F32 && p.beta == 0.0f && p.k_blocks > 0)
                         emit_store_16(p, &maps.c, t_row + c * 32, row, rows, n0, buf, lane);
                     else
-                        emit_store_direct(p, t_row + c * 32, row, rows, n0, lane);
+                        emit_store_direct(p, t_row + c * 32, split * p.split_stride, row, rows, n0, lane);
                     continue;
                 }
                 uint32_t r[32];

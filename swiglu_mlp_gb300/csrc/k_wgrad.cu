@@ -37,6 +37,8 @@ struct WgradParams {
     int out_kind;
     int staged;                          // 16-bit output, beta = 0: through shared memory
     int tma_out;                         // ... and from there with TMA stores
+    int splits;                          // ranges of a group's rows, each a unit
+    long long split_stride;
     int *err;
 };
 
@@ -76,22 +78,34 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 __device__ __forceinline__ bool ends_inside(int left) { return left < 64 && (left & 15) != 0; }
 
 struct WgradTile {
-    int g, kb, nb, row0, rows;
+    int g, kb, nb, split, row0, rows;
 };
 
 __device__ __forceinline__ WgradTile wgrad_tile(const WgradParams &p, const int *start, int u)
 {
-    const int per = p.k_tiles * p.n_tiles;
     WgradTile t;
-    t.g = u / per;
+    t.split = 0;
+    if (p.splits > 1) {
+        const int tile = fast_div(u, p.splits);
+        t.split = u - tile * p.splits;
+        u = tile;
+    }
+    const int per = p.k_tiles * p.n_tiles;
+    t.g = fast_div(u, per);
     const int local = u - t.g * per;
-    const int band = local / (8 * p.n_tiles);
+    const int band = p.k_tiles <= 8 ? 0 : fast_div(local, 8 * p.n_tiles);
     const int in = local - band * 8 * p.n_tiles;
     const int bm = min(8, p.k_tiles - band * 8);
-    t.nb = in / bm;
+    t.nb = fast_div(in, bm);
     t.kb = band * 8 + in - t.nb * bm;
     t.row0 = start[t.g];
     t.rows = start[t.g + 1] - t.row0;
+    if (p.splits > 1) {                  // whole blocks of 64 rows
+        const int range = ceil_div(ceil_div(t.rows, 64), p.splits) * 64;
+        const int from = min(t.rows, t.split * range);
+        t.row0 += from;
+        t.rows = min(range, t.rows - from);
+    }
     return t;
 }
 
@@ -146,7 +160,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     group_starts<WG_THREADS>(p.groups, start, p.err);
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_holder, 0);
-    const int units = p.groups.G * p.k_tiles * p.n_tiles;
+    const int units = p.groups.G * p.k_tiles * p.n_tiles * p.splits;
     const int u0 = (int)(blockIdx.x >> 1), du = (int)(gridDim.x >> 1);
 
     if (warp == 0) {
@@ -335,7 +349,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
             }
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
             const int k = t.kb * 256 + (int)rank * 128 + row;
-            const long long out = (long long)t.g * p.strideC + (long long)k * p.ldc;
+            const long long out = (long long)t.g * p.strideC + (long long)k * p.ldc +
+                                  t.split * p.split_stride;
             uint32_t r[32];
 #pragma unroll 1
             for (int c = h * 4; c < h * 4 + 4; ++c) {
@@ -435,6 +450,8 @@ cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, 
         return encode_tiled(map, type, 2, ptr, dims, st, box, 128);
     };
     mapped = M == 0 || (encode(&m.a, a.A, K, a.lda, p.a_3d) && encode(&m.d, a.D, N, a.ldd, p.d_3d));
+    p.splits = a.splits;
+    p.split_stride = a.split_stride;
     p.staged = a.out_kind != OUT_F32 && a.beta == 0.0f;
     p.tma_out = p.staged && N % 8 == 0;              // TMA clips a row at 16-byte granules
     if (p.tma_out) {
@@ -445,7 +462,7 @@ cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, 
         mapped = mapped && encode_tiled(&m.c, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, a.C, dims, st, box, 64);
     }
     if (!mapped) return cudaErrorInvalidValue;
-    const long long units = (long long)a.groups.G * p.k_tiles * p.n_tiles;
+    const long long units = (long long)a.groups.G * p.k_tiles * p.n_tiles * p.splits;
     return launch_pairs<wgrad_kernel, WG_THREADS>(SMEM_BYTES, SMEM_BYTES, units, sms, s, m, p);
 }
 

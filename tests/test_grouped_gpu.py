@@ -352,3 +352,69 @@ def test_graph_capture_and_repeatability():
         torch.cuda.synchronize()
         assert torch.equal(c, C) and torch.equal(w, W)
     assert swg.get_device_error() == 0
+
+
+# Few tiles and a long contraction: cut into ranges whose FP32 partials a second
+# kernel adds in order.  (Exact for beta, alpha, every epilogue and odd columns.)
+@pytest.mark.parametrize("rows,N,K,types,beta", [([1], 264, 4096, ("bf16", "bf16"), 0.0),
+                                                 ([3, 0, 20], 33, 2048, ("f16", "f32"), 0.5),
+                                                 ([200], 72, 3001, ("f16", "f16"), 1.0),
+                                                 ([0, 300, 1], 520, 1536, ("bf16", "bf16"), 0.0)])
+@pytest.mark.parametrize("transB", [0, 1])
+def test_long_contractions(rows, N, K, types, beta, transB):
+    run_gemm(rows, N, K, types, transB, alpha=0.5, beta=beta, before=3, after=4)
+
+
+@pytest.mark.parametrize("rows", [[1], [2, 0, 5], [100, 90]])
+def test_swiglu_long_contractions(rows):
+    N, K = 40, 4096
+    g = synth.generator(sum(rows))
+    off = offsets_of(rows)
+    M = int(off[-1])
+    A, W, dY = synth.normal((M, K), g), weights(len(rows), K, N, g), synth.normal((M, N), g)
+    Y, Y2 = (Guarded(M, N, torch.bfloat16, fill=9.0, ld=N) for _ in range(2))
+    dH = Guarded(M, 2 * N, torch.bfloat16, fill=9.0, ld=2 * N)
+    o = torch.from_numpy(off).cuda()
+    swg.swiglu_grouped_into(Y.view, A.cuda(), W.cuda(), o)
+    swg.swiglu_grouped_grad_into(dH.view, A.cuda(), W.cuda(), dY.cuda(), o, Y=Y2.view)
+    assert swg.get_device_error() == 0
+    want, tol = plain.swiglu(plain.f64(A), plain.f64(W), off)
+    check(Y.cpu("Y"), want, tol, "Y")
+    check(Y2.cpu("Y"), want, tol, "Y of the gradient")
+    want, tol = plain.swiglu_grad(plain.f64(A), plain.f64(W), plain.f64(dY), off)
+    check(dH.cpu("dH"), want, tol, "dH")
+
+
+@pytest.mark.parametrize("rows,N,K,types,beta", [([3000], 72, 264, ("bf16", "bf16"), 0.0),
+                                                 ([2500, 0, 5000], 33, 77, ("f16", "f32"), 0.5),
+                                                 ([1, 4001], 8, 16, ("f16", "f16"), 1.0)])
+def test_wgrad_long_groups(rows, N, K, types, beta):
+    run_wgrad(rows, N, K, types, alpha=0.5, beta=beta, before=5, after=70, poison=True)
+
+
+def test_split_calls_in_a_graph_need_their_workspace_first():
+    """A call that would allocate while its stream is captured is refused and
+    launches nothing; after the same call outside, it is captured."""
+    g = synth.generator(1)
+    A, B = padded(2, 4096, g, torch.bfloat16), padded(4096, 520, g, torch.bfloat16)
+    C = torch.zeros((2, 520), dtype=torch.bfloat16, device="cuda")
+    o = torch.tensor([0, 2], dtype=torch.int32).cuda()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        C.add_(0)
+        with pytest.raises(swg.SwgError) as e:
+            swg.gemm_grouped_into(C, A, B.unsqueeze(0), o)
+        assert e.value.status == 3
+    with torch.cuda.stream(s):
+        swg.gemm_grouped_into(C, A, B.unsqueeze(0), o)
+    s.synchronize()
+    first = C.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        swg.gemm_grouped_into(C, A, B.unsqueeze(0), o)
+    C.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(C, first) and swg.get_device_error() == 0

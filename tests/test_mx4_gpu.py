@@ -168,7 +168,8 @@ def run_product(rows, N, K, fmt, out="bf16", alpha=1.0, beta=0.0, seed=1, dense=
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 @pytest.mark.parametrize("M,N,K", [(1, 128, 256), (1, 300, 4096), (16, 64, 64), (33, 257, 1000), (128, 128, 32),
-                                   (200, 520, 136), (257, 96, 520), (5, 7, 1), (400, 300, 17)])
+                                   (200, 520, 136), (257, 96, 520), (5, 7, 1), (400, 300, 17),
+                                   (2, 264, 8192), (130, 40, 6001)])
 def test_dense_product(fmt, M, N, K):
     run_product([M], N, K, fmt, dense=True, seed=M + N + K)
 
