@@ -369,6 +369,23 @@ __device__ __forceinline__ void copy_rows_swizzled(uint32_t src, uint16_t *out, 
     }
 }
 
+// The columns from `from` to `limit` - 1 (at most 7 of the 32, which a TMA store
+// leaves out: it clips rows at 16-byte granules) of the same staged rows, a row
+// per lane.
+__device__ __forceinline__ void copy_last_columns(uint32_t src, uint16_t *out, long long ldo,
+                                                  int rows, int from, int limit, int lane)
+{
+    if (lane >= rows) return;
+    for (int c = from; c < limit; ++c) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=h"(v)
+                     : "r"(src + (uint32_t)(lane * 64 + (((c >> 3) ^ ((lane >> 1) & 3)) << 4) + (c & 7) * 2))
+                     : "memory");
+        out[lane * ldo + c] = v;
+    }
+}
+
 // Before this warp's staging memory is written again: the TMA stores that
 // lane 0 issued from it have read it.
 __device__ __forceinline__ void staging_free(int lane)
@@ -408,9 +425,15 @@ __device__ __forceinline__ void emit_store_16(const GrpParams &p, const CUtensor
     if (p.tma_out && rows == 32) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        const int whole = p.N & ~7;
+        if (lane == 0 && n0 < whole) {
             tma_store_2d(tm, buf, n0, row);
             bulk_commit_group();
+        }
+        if (p.N != whole && n0 + 32 > whole) {
+            copy_last_columns(buf, reinterpret_cast<uint16_t *>(p.C) + row * p.ldc + n0, p.ldc, 32,
+                              whole - n0, p.N - n0, lane);
+            __syncwarp();
         }
     } else {
         __syncwarp();

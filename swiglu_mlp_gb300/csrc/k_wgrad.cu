@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         // ------------------------------------------------------------ epilogue
         // Each lane holds 32 consecutive columns of its row of C.  16-bit results
         // pass through shared memory and leave 32 x 32 at a time with TMA stores
-        // (or, where a row does not end on 16 bytes, as 64-byte pieces of rows):
+        // (but the last columns of rows that do not end on 16 bytes):
         // stored by the lanes themselves they touch 32 lines per instruction, and
         // the main loop, whose operands use the same memory, took a fifth longer.
         const int q = warp & 3;
@@ -378,9 +378,17 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
                     if (p.tma_out) {
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
+                        const int whole = p.N & ~7;
+                        if (lane == 0 && col < whole) {
                             tma_store_3d(&maps.c, buf, col, k, t.g);
                             bulk_commit_group();
+                        }
+                        if (p.N != whole && col + 32 > whole) {
+                            copy_last_columns(buf,
+                                              reinterpret_cast<uint16_t *>(p.C) + out -
+                                                  lane * p.ldc + col,
+                                              p.ldc, p.K - (k - lane), whole - col, p.N - col, lane);
+                            __syncwarp();
                         }
                     } else {
                         __syncwarp();
@@ -453,10 +461,10 @@ cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, 
     p.splits = a.splits;
     p.split_stride = a.split_stride;
     p.staged = a.out_kind != OUT_F32 && a.beta == 0.0f;
-    p.tma_out = p.staged && N % 8 == 0;              // TMA clips a row at 16-byte granules
+    p.tma_out = p.staged && N >= 8;
     if (p.tma_out) {
         const uint64_t ld = (uint64_t)a.ldc * 2;
-        const uint64_t dims[] = {(uint64_t)N, (uint64_t)K, (uint64_t)a.groups.G};
+        const uint64_t dims[] = {(uint64_t)(N & ~7), (uint64_t)K, (uint64_t)a.groups.G};
         const uint64_t st[] = {ld, a.groups.G > 1 ? (uint64_t)a.strideC * 2 : ld * K};
         const uint32_t box[] = {32, 32, 1};
         mapped = mapped && encode_tiled(&m.c, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, a.C, dims, st, box, 64);
