@@ -15,13 +15,16 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "grouped_launch.cuh"
 
 namespace swg {
 namespace {
 
 struct WgradMaps {
-    CUtensorMap a, d;
+    CUtensorMap a, d;                    // boxes of 64 rows
+    CUtensorMap a16, d16;                // boxes of 16 rows
     CUtensorMap c;                       // 16-bit output, in boxes of 32 x 32 (tma_out)
 };
 
@@ -42,13 +45,16 @@ struct WgradParams {
     int *err;
 };
 
-constexpr int WG_STAGES = 6;
+constexpr int WG_STAGES = 6;             // the ring
+constexpr int LAST = WG_STAGES;          // a slot for a group's last rows, see Blocks
+constexpr int LAST_FROM = 256;           // rows from which on it is used
+constexpr int LAST_BYTES = 16 * 256;     // 16 rows x 128 columns of one operand
 constexpr int FIX_WARP = EPI_WARP0 + NUM_EPI_WARPS;
 constexpr int WG_THREADS = NUM_THREADS + 32;
 constexpr int OP_BYTES = 128 * 128;      // 64 rows x 128 columns of one operand per CTA
 constexpr int BAR_BYTES = 512;
 constexpr int OUT_BYTES = 2048;          // 32 x 32 16-bit results per epilogue warp
-constexpr int SMEM_BYTES = 1024 + WG_STAGES * 2 * OP_BYTES + NUM_EPI_WARPS * OUT_BYTES + BAR_BYTES +
+constexpr int SMEM_BYTES = 1024 + WG_STAGES * 2 * OP_BYTES + 2 * LAST_BYTES + NUM_EPI_WARPS * OUT_BYTES + BAR_BYTES +
                            4 * (MAX_GROUPS + 1);
 static_assert(SMEM_BYTES <= 232448, "beyond the per-CTA shared memory");
 
@@ -76,6 +82,25 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 // Whether a block with `left` rows of the group from its first on (64 rows and
 // more: all of them) also holds foreign rows in an MMA step that is run.
 __device__ __forceinline__ bool ends_inside(int left) { return left < 64 && (left & 15) != 0; }
+
+// A group's last block, where it ends inside an MMA step, is ready later than
+// others: it lands, the fixing warp overwrites the foreign rows, and only then
+// may the MMAs read it.  In the ring that held every tile up by 0.8 us.  So
+// longer groups load the 16 rows of that step apart from the ring, after the
+// first WG_STAGES blocks (by when the tile before has been done with the slot),
+// and multiply them last (16 groups of 1000 rows, 1792 x 4096: 159 -> 138 us).
+struct Blocks {
+    int ring;        // blocks of 64 rows that go through the ring
+    int rows;        // rows of the group in them
+    bool apart;      // and the rest, fewer than 16, apart
+};
+
+__device__ __forceinline__ Blocks blocks_of(int rows)
+{
+    const bool apart = (rows & 15) != 0 && rows >= LAST_FROM;
+    const int in_ring = apart ? rows & ~15 : rows;
+    return {ceil_div(in_ring, 64), in_ring, apart};
+}
 
 struct WgradTile {
     int g, kb, nb, split, row0, rows;
@@ -117,15 +142,17 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *sA = smem;
     uint8_t *sD = sA + WG_STAGES * OP_BYTES;
-    uint8_t *sOut = sD + WG_STAGES * OP_BYTES;
+    uint8_t *sLast = sD + WG_STAGES * OP_BYTES;       // A's last rows, then D's
+    uint8_t *sOut = sLast + 2 * LAST_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sOut + NUM_EPI_WARPS * OUT_BYTES);
+    constexpr int SLOTS = WG_STAGES + 1;
     uint64_t *full = bars;
-    uint64_t *empty = bars + WG_STAGES;
-    uint64_t *acc_full = bars + 2 * WG_STAGES;
-    uint64_t *acc_empty = bars + 2 * WG_STAGES + 2;
-    uint64_t *mma_done = bars + 2 * WG_STAGES + 4;
-    uint64_t *landed = bars + 2 * WG_STAGES + 5;     // a group's last block, in this CTA
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 3 * WG_STAGES + 5);
+    uint64_t *empty = bars + SLOTS;
+    uint64_t *landed = bars + 2 * SLOTS;             // a group's last block, in this CTA
+    uint64_t *acc_full = bars + 3 * SLOTS;
+    uint64_t *acc_empty = bars + 3 * SLOTS + 2;
+    uint64_t *mma_done = bars + 3 * SLOTS + 4;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 3 * SLOTS + 5);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *start = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + BAR_BYTES);
 
@@ -136,7 +163,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
-        for (int s = 0; s < WG_STAGES; ++s) {
+        for (int s = 0; s < SLOTS; ++s) {
             mbar_init(smem_u32(&full[s]), 2);        // a thread of each CTA
             mbar_init(smem_u32(&empty[s]), 1);
             mbar_init(smem_u32(&landed[s]), 1);
@@ -166,8 +193,11 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         int stage = 0;
-        uint32_t phase = 0;
+        uint32_t phase = 0, last_phase = 0;
         uint32_t armed = 0, armed_parity = 0;
+        const uint32_t empty0 = smem_u32(empty), full0 = smem_u32(full), landed0 = smem_u32(landed);
+        const uint32_t full_leader0 = mapa_shared(full0, 0);
+        const uint32_t a0 = smem_u32(sA), d0 = smem_u32(sD), last0 = smem_u32(sLast);
         bool ok = true;
         for (int u = u0; u < units && ok; u += du) {
             const WgradTile t = wgrad_tile(p, start, u);
@@ -175,44 +205,56 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
             const int row0 = __shfl_sync(0xffffffffu, t.row0, 0);
             const int ka = t.kb * 256 + (int)rank * 128;
             const int nd = t.nb * 256 + (int)rank * 128;
-            const int blocks = ceil_div(rows, 64);
-            for (int b = 0; b < blocks; ++b) {
-                if (!wait_bounded_warp(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.err)) {
-                    ok = false;
-                    break;
-                }
-                armed |= 1u << stage;
-                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                const uint32_t a_dst = smem_u32(sA + stage * OP_BYTES);
-                const uint32_t d_dst = smem_u32(sD + stage * OP_BYTES);
-                const int row = row0 + b * 64;
-                const bool ends = ends_inside(rows - b * 64);
-                // Both CTAs' bytes and one arrival of each complete the
-                // leader's barrier.  A block in which the group ends lands on
-                // a barrier of this CTA instead; the fixing warp arrives for it.
-                const uint32_t fb = smem_u32(&full[stage]);
-                const uint32_t bar = ends ? smem_u32(&landed[stage]) : mapa_shared(fb, 0);
+            const Blocks blocks = blocks_of(rows);
+            // Loads 64 rows (`last`: the 16 of a last step) from `row` on into slot
+            // s, whose barriers are in phase ph.  Both CTAs' bytes and one arrival
+            // of each complete the leader's barrier.  Where foreign rows must go,
+            // the rows land on a barrier of this CTA instead, and the fixing warp
+            // arrives for it.
+            auto load = [&](auto last, int s, uint32_t ph, int row, bool ends) {
+                constexpr bool rows16 = decltype(last)::value;
+                if (!wait_bounded_warp(empty0 + 8 * s, ph ^ 1, abort_flag, p.err)) return false;
+                armed |= 1u << s;
+                armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
+                constexpr uint32_t bytes = rows16 ? LAST_BYTES : OP_BYTES;
+                const uint32_t a_dst = rows16 ? last0 : a0 + s * OP_BYTES;
+                const uint32_t d_dst = rows16 ? last0 + LAST_BYTES : d0 + s * OP_BYTES;
+                const CUtensorMap *ma = rows16 ? &maps.a16 : &maps.a;
+                const CUtensorMap *md = rows16 ? &maps.d16 : &maps.d;
+                const uint32_t fb = full0 + 8 * s;
+                const uint32_t bar = ends ? landed0 + 8 * s : full_leader0 + 8 * s;
                 if (elect_one()) {
                     if (ends)
-                        mbar_arrive_expect_tx(bar, 2 * OP_BYTES);
+                        mbar_arrive_expect_tx(bar, 2 * bytes);
                     else if (leader)
-                        mbar_arrive_expect_tx(fb, 4 * OP_BYTES);
+                        mbar_arrive_expect_tx(fb, 4 * bytes);
                     else
                         mbar_arrive_remote_tmem(bar);            // nothing to release
                     if (p.a_3d) {
-                        tma_load_3d_pair(a_dst, &maps.a, bar, 0, row, ka / 64);
+                        tma_load_3d_pair(a_dst, ma, bar, 0, row, ka / 64);
                     } else {
-                        tma_load_2d_pair(a_dst, &maps.a, bar, ka, row);
-                        tma_load_2d_pair(a_dst + 8192, &maps.a, bar, ka + 64, row);
+                        tma_load_2d_pair(a_dst, ma, bar, ka, row);
+                        tma_load_2d_pair(a_dst + bytes / 2, ma, bar, ka + 64, row);
                     }
                     if (p.d_3d) {
-                        tma_load_3d_pair(d_dst, &maps.d, bar, 0, row, nd / 64);
+                        tma_load_3d_pair(d_dst, md, bar, 0, row, nd / 64);
                     } else {
-                        tma_load_2d_pair(d_dst, &maps.d, bar, nd, row);
-                        tma_load_2d_pair(d_dst + 8192, &maps.d, bar, nd + 64, row);
+                        tma_load_2d_pair(d_dst, md, bar, nd, row);
+                        tma_load_2d_pair(d_dst + bytes / 2, md, bar, nd + 64, row);
                     }
                 }
                 __syncwarp();
+                return true;
+            };
+            const int ahead = blocks.apart ? min(blocks.ring, WG_STAGES) : -1;
+            for (int b = 0; b <= blocks.ring && ok; ++b) {
+                if (b == ahead) {
+                    ok = load(std::true_type{}, LAST, last_phase, row0 + blocks.rows, true);
+                    last_phase ^= 1;
+                }
+                if (b == blocks.ring || !ok) break;
+                ok = load(std::false_type{}, stage, phase, row0 + b * 64,
+                          ends_inside(blocks.rows - b * 64));
                 if (++stage == WG_STAGES) {
                     stage = 0;
                     phase ^= 1;
@@ -221,7 +263,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         }
         // Never leave with loads in flight into this CTA's shared memory.
         if (leader) {
-            for (int s = 0; s < WG_STAGES; ++s)
+            for (int s = 0; s < SLOTS; ++s)
                 if (armed & (1u << s))
                     wait_bounded(smem_u32(&full[s]), (armed_parity >> s) & 1, abort_flag, p.err,
                                  false, DRAIN_LIMIT_NS);
@@ -238,41 +280,43 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         bool ok = true;
         for (int u = u0; u < units && ok; u += du) {
             const WgradTile t = wgrad_tile(p, start, u);
-            const int blocks = ceil_div(t.rows, 64);
-            if (ends_inside(t.rows - (blocks - 1) * 64) && blocks > 0) {
-                const int left = t.rows - (blocks - 1) * 64;
-                const int s = (stage + blocks - 1) % WG_STAGES;
+            const Blocks blocks = blocks_of(t.rows);
+            if (t.rows & 15) {
+                const int s = blocks.apart ? LAST : (stage + blocks.ring - 1) % WG_STAGES;
                 ok = wait_bounded(smem_u32(&landed[s]), (phases >> s) & 1, abort_flag, p.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 phases ^= 1u << s;
-                // rows [left, left rounded up to 16) of the four 64-column atoms
-                const uint32_t a_dst = smem_u32(sA + s * OP_BYTES);
-                const uint32_t d_dst = smem_u32(sD + s * OP_BYTES);
+                // from the group's end to a multiple of 16 rows, in the four 64-column atoms
+                const int left = blocks.apart ? t.rows & 15 : t.rows & 63;
+                const uint32_t atom = blocks.apart ? LAST_BYTES / 2 : OP_BYTES / 2;
+                const uint32_t a_dst = smem_u32(blocks.apart ? sLast : sA + s * OP_BYTES);
+                const uint32_t d_dst = smem_u32(blocks.apart ? sLast + LAST_BYTES : sD + s * OP_BYTES);
                 const uint32_t end = (uint32_t)((left + 15) & ~15) * 128;
                 for (uint32_t o = (uint32_t)left * 128 + lane * 16; o < end; o += 512) {
                     st_shared_v4(a_dst + o, make_uint4(0, 0, 0, 0));
-                    st_shared_v4(a_dst + 8192 + o, make_uint4(0, 0, 0, 0));
+                    st_shared_v4(a_dst + atom + o, make_uint4(0, 0, 0, 0));
                     st_shared_v4(d_dst + o, make_uint4(0, 0, 0, 0));
-                    st_shared_v4(d_dst + 8192 + o, make_uint4(0, 0, 0, 0));
+                    st_shared_v4(d_dst + atom + o, make_uint4(0, 0, 0, 0));
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
             }
-            stage = (stage + blocks) % WG_STAGES;
+            stage = (stage + blocks.ring) % WG_STAGES;
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (leader) {
             int stage = 0;
-            uint32_t phase = 0;
+            uint32_t phase = 0, last_phase = 0;
             bool ok = true;
             int n = 0;                                   // tiles with rows so far
             // K-step kk of a stage is 16 rows (2048 bytes) further in each atom
             const uint64_t a_desc = smem_desc(smem_u32(sA), 8192, 1024);
             const uint64_t d_desc = smem_desc(smem_u32(sD), 8192, 1024);
+            const uint64_t last_desc = smem_desc(smem_u32(sLast), LAST_BYTES / 2, 1024);
             for (int u = u0; u < units && ok; u += du) {
                 const int rows = __shfl_sync(0xffffffffu, wgrad_tile(p, start, u).rows, 0);
                 if (rows == 0) continue;
@@ -284,17 +328,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
                 ++n;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * 256;
-                const int blocks = ceil_div(rows, 64);
-                for (int b = 0; b < blocks; ++b) {
-                    if (!wait_bounded_warp(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
-                        ok = false;
-                        break;
-                    }
-                    const int left = rows - b * 64;
-                    if (ends_inside(left)) mbar_try_wait_cluster(smem_u32(&full[stage]), phase);
+                const Blocks blocks = blocks_of(rows);
+                // Block b of the tile, with `left` rows of it from its first on.
+                auto multiply = [&](int b, int left, int s, uint32_t ph) {
+                    if (!wait_bounded_warp(smem_u32(&full[s]), ph, abort_flag, p.err)) return false;
+                    if (ends_inside(left)) mbar_try_wait_cluster(smem_u32(&full[s]), ph);
                     tc_fence_after();
-                    const uint64_t ad = a_desc + (uint64_t)(stage * (OP_BYTES >> 4));
-                    const uint64_t dd = d_desc + (uint64_t)(stage * (OP_BYTES >> 4));
+                    const uint64_t ad = a_desc + (uint64_t)(s * (OP_BYTES >> 4));
+                    const uint64_t dd = d_desc + (uint64_t)(s * (OP_BYTES >> 4));
                     if (elect_one()) {
                         if (left > 48) {                 // every block but a group's last
 #pragma unroll
@@ -304,13 +345,30 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
                             for (int kk = 0; kk < ceil_div(left, 16); ++kk)
                                 tc_mma_f16_pair(d_tmem, ad + kk * 128, dd + kk * 128, p.idesc, b | kk);
                         }
-                        tc_commit_pair(smem_u32(&empty[stage]));
+                        tc_commit_pair(smem_u32(&empty[s]));
                     }
                     __syncwarp();
+                    return true;
+                };
+                for (int b = 0; b < blocks.ring && ok; ++b) {
+                    ok = multiply(b, blocks.rows - b * 64, stage, phase);
                     if (++stage == WG_STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
+                }
+                if (ok && blocks.apart) {
+                    const uint32_t bar = smem_u32(&full[LAST]);
+                    ok = wait_bounded_warp(bar, last_phase, abort_flag, p.err);
+                    if (!ok) break;
+                    mbar_try_wait_cluster(bar, last_phase);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        tc_mma_f16_pair(d_tmem, last_desc, last_desc + (LAST_BYTES >> 4), p.idesc, 1u);
+                        tc_commit_pair(smem_u32(&empty[LAST]));
+                    }
+                    __syncwarp();
+                    last_phase ^= 1;
                 }
                 if (!ok) break;
                 if (elect_one()) tc_commit_pair(smem_u32(&acc_full[acc]));
@@ -443,21 +501,25 @@ cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, 
     p.strideC = a.strideC;
     p.out_kind = a.out_kind;
     p.err = err;
-    auto encode = [&](CUtensorMap *map, const void *ptr, int64_t cols, int64_t ld, int &in_3d) {
+    auto encode = [&](CUtensorMap *map, const void *ptr, int64_t cols, int64_t ld, uint32_t rows,
+                      int &in_3d) {
         const CUtensorMapDataType type =
             a.in_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
         if (cols % 64 == 0) {
             const uint64_t dims[] = {64, (uint64_t)M, (uint64_t)cols / 64}, st[] = {(uint64_t)ld * 2, 128};
-            const uint32_t box[] = {64, 64, 2};
+            const uint32_t box[] = {64, rows, 2};
             in_3d = 1;
             return encode_tiled(map, type, 3, ptr, dims, st, box, 128);
         }
         const uint64_t dims[] = {(uint64_t)cols, (uint64_t)M}, st[] = {(uint64_t)ld * 2};
-        const uint32_t box[] = {64, 64};
+        const uint32_t box[] = {64, rows};
         in_3d = 0;
         return encode_tiled(map, type, 2, ptr, dims, st, box, 128);
     };
-    mapped = M == 0 || (encode(&m.a, a.A, K, a.lda, p.a_3d) && encode(&m.d, a.D, N, a.ldd, p.d_3d));
+    mapped = M == 0 || (encode(&m.a, a.A, K, a.lda, 64, p.a_3d) && encode(&m.d, a.D, N, a.ldd, 64, p.d_3d));
+    if (M >= LAST_FROM)
+        mapped = mapped && encode(&m.a16, a.A, K, a.lda, 16, p.a_3d) &&
+                 encode(&m.d16, a.D, N, a.ldd, 16, p.d_3d);
     p.splits = a.splits;
     p.split_stride = a.split_stride;
     p.staged = a.out_kind != OUT_F32 && a.beta == 0.0f;
