@@ -138,6 +138,7 @@ def _ptr(x):
 
 
 _raw_stream = None    # torch's accessor of the current raw stream handle, once found
+_device = None        # torch's accessor of the current device, once CUDA is initialised
 
 
 def _current_stream():
@@ -145,15 +146,17 @@ def _current_stream():
     raw handle (None without CUDA).  torch's raw accessor is used when it has
     one: building a torch.cuda.Stream object per call costs several
     microseconds of host time."""
-    global _raw_stream
-    import torch
-    if _raw_stream is None:
+    global _raw_stream, _device
+    if _device is None:
+        import torch
         if not torch.cuda.is_available():
             return None
         get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _raw_stream = get if get is not None else (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-    return _raw_stream(torch.cuda.current_device())
+        torch.cuda.current_device()       # initialises CUDA; the accessor alone does not
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _raw_stream(_device())
 
 
 def _stream(s):
@@ -409,12 +412,12 @@ _torch = None
 
 
 def _fast():
-    """The library and torch, loaded on the first call."""
+    """torch, loaded with the library on the first call."""
     global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _lib or load(), _torch
+    load()
+    import torch
+    _torch = torch
+    return torch
 
 
 def _refuse(where, why, status=1):
@@ -425,20 +428,27 @@ def _groups(offsets, where):
     """(device pointer or None, G) of an int32 offsets tensor, or of none."""
     if offsets is None:
         return None, 1
-    if offsets.dtype is not _torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 \
+    n = offsets.numel()
+    if n < 1 or offsets.dtype is not _torch.int32 or offsets.dim() != 1 \
             or not offsets.is_contiguous():
         _refuse(where, "offsets must be a contiguous 1-D int32 tensor of G + 1 values")
-    return offsets.data_ptr(), offsets.numel() - 1
+    return offsets.data_ptr(), n - 1
 
 
 def _matrices(t, name, where, G):
     """(rows, columns, row stride, group stride) of a [G, rows, columns]
     tensor, or with G = 1 also of a [rows, columns] one."""
     shape, stride = t.shape, t.stride()
-    n = len(shape)
-    if n not in (2, 3) or stride[-1] != 1 or (shape[0] if n == 3 else 1) != G:
+    if len(shape) == 3:
+        g, rows, cols = shape
+        sg, sr, sc = stride
+    elif len(shape) == 2:
+        (rows, cols), (sr, sc), g, sg = shape, stride, 1, 0
+    else:
+        g = sg = sr = sc = rows = cols = -1
+    if sc != 1 or g != G:
         _refuse(where, f"{name} must hold one row-major matrix for each of {G} groups")
-    return shape[-2], shape[-1], stride[-2], stride[0] if n == 3 else 0
+    return rows, cols, sr, sg
 
 
 def _matrix(t, name, where):
@@ -446,7 +456,8 @@ def _matrix(t, name, where):
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or stride[1] != 1:
         _refuse(where, f"{name} must be a 2-D row-major tensor (unit column stride)")
-    return shape[0], shape[1], stride[0]
+    rows, cols = shape
+    return rows, cols, stride[0]
 
 
 def _type_code(dtype, where) -> int:
@@ -459,18 +470,19 @@ def _type_code(dtype, where) -> int:
     _refuse(where, f"unsupported dtype {dtype}", 3)
 
 
-def _plain(where, dtype, **tensors):
-    """Contiguous tensors of one type."""
-    for name, t in tensors.items():
-        if t.dtype is not dtype or not t.is_contiguous():
-            _refuse(where, f"{name} must be a contiguous {dtype} tensor")
+def _output(w, name, t, rows, cols, dtype):
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 2 or shape[0] != rows or shape[1] != cols \
+            or not t.is_contiguous():
+        _refuse(w, f"{name} must be a contiguous [{rows}, {cols}] {dtype} tensor")
 
 
 def gemm_grouped_into(C, A, B, offsets, transB=0, alpha=1.0, beta=0.0, stream=None):
     """C[M, N] <- alpha * A[M, K] op(B_g) + beta * C for the rows of each group;
     B is [G, K, N] (transB = 0) or [G, N, K], offsets int32 [G + 1] on the GPU."""
     w = "gemm_grouped_into"
-    lib, _ = _fast()
+    _torch or _fast()
+    lib = _lib
     off, G = _groups(offsets, w)
     rows, cols, ldb, stride = _matrices(B, "B", w, G)
     N, Kb = (rows, cols) if transB else (cols, rows)
@@ -489,7 +501,8 @@ def gemm_grouped_into(C, A, B, offsets, transB=0, alpha=1.0, beta=0.0, stream=No
 def gemm_grouped_wgrad_into(C, A, D, offsets, alpha=1.0, beta=0.0, stream=None):
     """C[G, K, N] <- alpha * A_g^T D_g + beta * C_g from A[M, K] and D[M, N]."""
     w = "gemm_grouped_wgrad_into"
-    lib, _ = _fast()
+    _torch or _fast()
+    lib = _lib
     off, G = _groups(offsets, w)
     rows, cols, ldc, stride = _matrices(C, "C", w, G)
     M, K, lda = _matrix(A, "A", w)
@@ -504,28 +517,22 @@ def gemm_grouped_wgrad_into(C, A, D, offsets, alpha=1.0, beta=0.0, stream=None):
     return C
 
 
-def _swiglu_shapes(w, A, W_fused, G, torch):
-    rows, cols, ldw, stride = _matrices(W_fused, "W_fused", w, G)
-    M, K, lda = _matrix(A, "A", w)
-    if rows != K or cols % 2:
-        _refuse(w, "inconsistent shapes")
-    _plain(w, torch.bfloat16, A=A, W_fused=W_fused)
+def _swiglu_shapes(w, A, W_fused, G, bf16):
+    rows, cols, _, _ = _matrices(W_fused, "W_fused", w, G)
+    M, K, _ = _matrix(A, "A", w)
+    if rows != K or cols % 2 or A.dtype is not bf16 or W_fused.dtype is not bf16 \
+            or not A.is_contiguous() or not W_fused.is_contiguous():
+        _refuse(w, "A [M, K] and W_fused [G, K, 2N] must be contiguous bfloat16")
     return M, cols // 2, K
-
-
-def _output(w, name, t, rows, cols, dtype):
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.dtype is not dtype \
-            or not t.is_contiguous():
-        _refuse(w, f"{name} must be a contiguous [{rows}, {cols}] {dtype} tensor")
 
 
 def swiglu_grouped_into(Y, A, W_fused, offsets, stream=None):
     """Y[M, N] <- SiLU(A W1_g) (.) (A W2_g), W_fused [G, K, 2N] interleaved."""
     w = "swiglu_grouped_into"
-    lib, torch = _fast()
+    torch = _torch or _fast()
+    lib = _lib
     off, G = _groups(offsets, w)
-    M, N, K = _swiglu_shapes(w, A, W_fused, G, torch)
+    M, N, K = _swiglu_shapes(w, A, W_fused, G, torch.bfloat16)
     _output(w, "Y", Y, M, N, torch.bfloat16)
     rc = lib.swiglu_grouped(A.data_ptr(), W_fused.data_ptr(), Y.data_ptr(), off, G, M, N, K,
                             _stream(stream))
@@ -538,9 +545,10 @@ def swiglu_grouped_grad_into(dH, A, W_fused, dY, offsets, Y=None, stream=None):
     """dH[M, 2N] <- the gradient of swiglu_grouped in the interleaved Gate and
     Up, from dY[M, N]; Y, when given, receives swiglu_grouped's result."""
     w = "swiglu_grouped_grad_into"
-    lib, torch = _fast()
+    torch = _torch or _fast()
+    lib = _lib
     off, G = _groups(offsets, w)
-    M, N, K = _swiglu_shapes(w, A, W_fused, G, torch)
+    M, N, K = _swiglu_shapes(w, A, W_fused, G, torch.bfloat16)
     _output(w, "dH", dH, M, 2 * N, torch.bfloat16)
     _output(w, "dY", dY, M, N, torch.bfloat16)
     if Y is not None:
@@ -574,7 +582,8 @@ def _mx4_rows(w, Q, S, format, G, M, K, torch):
 def mx4_quantize_into(Q, S, X, format, scale=1.0, offsets=None, stream=None):
     """Q, S <- X[M, K] * scale in 4 bits (Q uint8 rows of codes, S scale tiles)."""
     w = "mx4_quantize_into"
-    lib, torch = _fast()
+    torch = _torch or _fast()
+    lib = _lib
     off, G = _groups(offsets, w)
     M, K, ldx = _matrix(X, "X", w)
     ldq = _mx4_rows(w, Q, S, format, G, M, K, torch)
@@ -588,7 +597,8 @@ def mx4_quantize_into(Q, S, X, format, scale=1.0, offsets=None, stream=None):
 def mx4_dequantize_into(X, Q, S, format, scale=1.0, offsets=None, stream=None):
     """X[M, K] <- scale * the values of the 4-bit rows (Q, S)."""
     w = "mx4_dequantize_into"
-    lib, torch = _fast()
+    torch = _torch or _fast()
+    lib = _lib
     off, G = _groups(offsets, w)
     M, K, ldx = _matrix(X, "X", w)
     ldq = _mx4_rows(w, Q, S, format, G, M, K, torch)
@@ -615,7 +625,8 @@ def gemm_mx4_into(C, Q, S, W, SW, K, format, alpha=1.0, beta=0.0, offsets=None, 
     """C[M, N] <- alpha * A W_g^T + beta * C with 4-bit A = (Q, S) of K columns
     and weights (W [N, bytes] or [G, N, bytes], SW)."""
     w = "gemm_mx4_into"
-    lib, torch = _fast()
+    torch = _torch or _fast()
+    lib = _lib
     off, G = _groups(offsets, w)
     M, Nc, ldc = _matrix(C, "C", w)
     lda = _mx4_rows(w, Q, S, format, G, M, K, torch)
@@ -634,7 +645,8 @@ def swiglu_mx4_into(Y, Q, S, W, SW, K, format, alpha=1.0, offsets=None, stream=N
     """Y[M, N] <- SiLU(alpha A W1_g^T) (.) (alpha A W2_g^T), W [2N, bytes] or
     [G, 2N, bytes] with Gate in even and Up in odd rows."""
     w = "swiglu_mx4_into"
-    lib, torch = _fast()
+    torch = _torch or _fast()
+    lib = _lib
     off, G = _groups(offsets, w)
     M = Q.shape[0]
     lda = _mx4_rows(w, Q, S, format, G, M, K, torch)
