@@ -32,6 +32,7 @@ struct WgradParams {
     Groups groups;
     int N, K;
     int k_tiles, n_tiles;
+    int n_step;                          // columns per tile, a multiple of 64
     int a_3d, d_3d;                      // 64-column atoms of an operand as one 3-D box
     uint32_t idesc;
     float alpha, beta;
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
             const int rows = __shfl_sync(0xffffffffu, t.rows, 0);
             const int row0 = __shfl_sync(0xffffffffu, t.row0, 0);
             const int ka = t.kb * 256 + (int)rank * 128;
-            const int nd = t.nb * 256 + (int)rank * 128;
+            const int nd = t.nb * p.n_step + (int)rank * (p.n_step / 2);
             const Blocks blocks = blocks_of(rows);
             // Loads 64 rows (`last`: the 16 of a last step) from `row` on into slot
             // s, whose barriers are in phase ph.  Both CTAs' bytes and one arrival
@@ -390,6 +391,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         const int h = (warp - EPI_WARP0) / 4;
         const int row = q * 32 + lane;
         const uint32_t buf = smem_u32(sOut + (warp - EPI_WARP0) * OUT_BYTES);
+        const int per_half = p.n_step / 64;     // chunks of 32 columns
         TileParams tp{};
         tp.alpha = p.alpha;
         tp.beta = p.beta;
@@ -411,8 +413,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
                                   t.split * p.split_stride;
             uint32_t r[32];
 #pragma unroll 1
-            for (int c = h * 4; c < h * 4 + 4; ++c) {
-                const int col = t.nb * 256 + c * 32;
+            for (int c = h * per_half; c < (h + 1) * per_half; ++c) {
+                const int col = t.nb * p.n_step + c * 32;
                 if (k - lane >= p.K || col >= p.N) break;        // the whole warp
                 if (t.rows > 0) {
                     tmem_ld_32cols(t_row + c * 32, r);
@@ -490,10 +492,13 @@ cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, 
     p.N = a.N;
     p.K = a.K;
     p.k_tiles = (int)((K + 255) / 256);
+    // Tiles of nearly equal width: 521 columns are 3 x 192, not 256, 256 and 9
     p.n_tiles = (int)((N + 255) / 256);
+    p.n_step = (int)((N + 64 * p.n_tiles - 1) / (64 * p.n_tiles) * 64);
     const uint32_t t = a.in_bf16 ? 1u : 0u;
-    // kind::f16, FP32 accumulators, both operands MN-major, 256 x 256
-    p.idesc = (1u << 4) | (t << 7) | (t << 10) | (1u << 15) | (1u << 16) | (32u << 17) | (16u << 24);
+    // kind::f16, FP32 accumulators, both operands MN-major, 256 x n_step
+    p.idesc = (1u << 4) | (t << 7) | (t << 10) | (1u << 15) | (1u << 16) |
+              ((uint32_t)(p.n_step >> 3) << 17) | (16u << 24);
     p.alpha = a.alpha;
     p.beta = a.beta;
     p.C = a.C;
@@ -501,11 +506,13 @@ cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, 
     p.strideC = a.strideC;
     p.out_kind = a.out_kind;
     p.err = err;
+    // (3-D: 64 columns at a time as their own dimension, where a CTA's columns
+    // begin at multiples of 64)
     auto encode = [&](CUtensorMap *map, const void *ptr, int64_t cols, int64_t ld, uint32_t rows,
-                      int &in_3d) {
+                      bool whole, int &in_3d) {
         const CUtensorMapDataType type =
             a.in_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-        if (cols % 64 == 0) {
+        if (whole && cols % 64 == 0) {
             const uint64_t dims[] = {64, (uint64_t)M, (uint64_t)cols / 64}, st[] = {(uint64_t)ld * 2, 128};
             const uint32_t box[] = {64, rows, 2};
             in_3d = 1;
@@ -516,10 +523,11 @@ cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, 
         in_3d = 0;
         return encode_tiled(map, type, 2, ptr, dims, st, box, 128);
     };
-    mapped = M == 0 || (encode(&m.a, a.A, K, a.lda, 64, p.a_3d) && encode(&m.d, a.D, N, a.ldd, 64, p.d_3d));
+    mapped = M == 0 || (encode(&m.a, a.A, K, a.lda, 64, true, p.a_3d) &&
+                        encode(&m.d, a.D, N, a.ldd, 64, p.n_step % 128 == 0, p.d_3d));
     if (M >= LAST_FROM)
-        mapped = mapped && encode(&m.a16, a.A, K, a.lda, 16, p.a_3d) &&
-                 encode(&m.d16, a.D, N, a.ldd, 16, p.d_3d);
+        mapped = mapped && encode(&m.a16, a.A, K, a.lda, 16, true, p.a_3d) &&
+                 encode(&m.d16, a.D, N, a.ldd, 16, p.n_step % 128 == 0, p.d_3d);
     p.splits = a.splits;
     p.split_stride = a.split_stride;
     p.staged = a.out_kind != OUT_F32 && a.beta == 0.0f;
