@@ -22,10 +22,8 @@ __global__ void __launch_bounds__(THREADS) reduce_kernel(const ReduceArgs p)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int begin = 0, end = p.rows;
     if (p.groups.offsets != nullptr) {
-        begin = min(max(p.groups.offsets[0], 0), p.groups.M);
-        end = begin;                 // the largest offset ends the last group
-        for (int g = 1; g <= p.groups.G; ++g)
-            end = max(end, min(p.groups.offsets[g], p.groups.M));
+        begin = max(p.groups.offsets[0], 0);
+        end = min(p.groups.offsets[p.groups.G], p.groups.M);
     }
     const int per_row = (p.N + COLS - 1) / COLS;
     const long long total = (long long)p.rows * per_row;
