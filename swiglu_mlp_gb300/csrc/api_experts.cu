@@ -208,22 +208,19 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
             return rc;
         return swg::count_launch(swg::launch_reduce(r, epi, d.sms, s));
     }
-    // 16-bit outputs in boxes of 32 rows: 64 bytes (or 32, a SwiGLU output) wide.  TMA
-    // clips a row at 16-byte granules: the last N % 8 columns are not the map's.
-    auto out_map = [&](CUtensorMap *map, void *ptr, int64_t cols, int64_t ld, uint32_t width, int sw) {
+    // 16-bit outputs in boxes of 64 columns x 32 rows.  TMA clips a row at 16-byte
+    // granules: the last N % 8 columns are not the map's.
+    auto out_map = [&](CUtensorMap *map, void *ptr, int64_t cols, int64_t ld) {
         const uint64_t dims[] = {(uint64_t)cols, (uint64_t)M}, st[] = {(uint64_t)ld * 2};
-        const uint32_t box[] = {width, 32};
-        return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, ptr, dims, st, box, sw);
+        const uint32_t box[] = {64, 32};
+        return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, ptr, dims, st, box, 128);
     };
-    if (epi == swg::GRP_STORE) {
-        p.tma_out = a.out_kind != swg::OUT_F32 && a.beta == 0.0f && N >= 8 && M >= 32;
-        if (p.tma_out) ok = ok && out_map(&m.c, a.C, N & ~7, a.ldc, 32, 64);
-    } else {
-        p.tma_out = M >= 32;
-        if (p.tma_out)
-            ok = ok && (epi == swg::GRP_SWIGLU ? out_map(&m.c, a.C, N / 2, a.ldc, 16, 0)
-                                           : out_map(&m.c, a.C, N, a.ldc, 32, 0));
-        if (a.Y && p.tma_out) ok = ok && out_map(&m.y, a.Y, N / 2, N / 2, 16, 0);
+    p.tma_out = M >= 32;
+    if (epi == swg::GRP_STORE)
+        p.tma_out = p.tma_out && a.out_kind != swg::OUT_F32 && a.beta == 0.0f && N >= 8;
+    if (p.tma_out) {
+        ok = ok && out_map(&m.c, a.C, epi == swg::GRP_SWIGLU ? N / 2 : N & ~7, a.ldc);
+        if (a.Y) ok = ok && out_map(&m.y, a.Y, N / 2, N / 2);
     }
     if (!ok) return swg::record_cuda_error();
     // (tiles of as few as 128 rows may be chosen)

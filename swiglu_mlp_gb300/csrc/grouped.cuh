@@ -109,7 +109,7 @@ struct GrpMaps {
     CUtensorMap w;                       // weights
     CUtensorMap t[TOKEN_BOXES];          // rows of A
     CUtensorMap sw, st;                  // scale tiles of both (4-bit)
-    CUtensorMap c, y;                    // 16-bit outputs, in boxes of 32 rows (tma_out)
+    CUtensorMap c, y;                    // 16-bit outputs, boxes of 64 columns x 32 rows (tma_out)
 };
 
 struct GrpParams {
@@ -298,30 +298,6 @@ __device__ __forceinline__ uint32_t to_16(float v, int out_kind)
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// Copies `rows` rows of COLS 16-bit values, staged back to back, to rows of
-// `out` ldo apart, 16 bytes per lane; columns from `limit` on are left out.
-template <int COLS>
-__device__ __forceinline__ void copy_rows(uint32_t src, uint16_t *out, long long ldo, int rows,
-                                          int limit, int lane)
-{
-    constexpr int PER_ROW = COLS / 8, ROWS = 32 / PER_ROW;
-    const int c = (lane % PER_ROW) * 8;
-#pragma unroll
-    for (int r = lane / PER_ROW; r < 32; r += ROWS) {
-        if (r >= rows || c >= limit) continue;
-        const uint4 v = ld_shared_v4(src + (uint32_t)(r * COLS + c) * 2);
-        uint16_t *dst = out + r * ldo + c;
-        if (c + 8 <= limit) {
-            *reinterpret_cast<uint4 *>(dst) = v;
-        } else {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (c + i < limit) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-        }
-    }
-}
-
 // 16 lanes (from taddr's lane on) x 32 columns of the accumulator in fragments:
 // for each 8 columns i, r[4 i] and r[4 i + 1] are row lane / 4, columns
 // 2 (lane % 4) and + 1; r[4 i + 2] and r[4 i + 3] the same of row lane / 4 + 8.
@@ -346,17 +322,40 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                  : "memory");
 }
 
-// The copy of 32 staged rows of 32 16-bit values in the 64-byte swizzle
-// (16-byte piece j of row r at j ^ (r / 2 mod 4)) to the first `rows` rows of
-// `out`, columns from `limit` on left out.
-__device__ __forceinline__ void copy_rows_swizzled(uint32_t src, uint16_t *out, long long ldo,
-                                                   int rows, int limit, int lane)
+// A tile store from shared memory whose lines leave L2 first: results would
+// push out the operands that other tiles still read (8192 x 14336 x 4096 in
+// NVFP4: 161.8 -> 159.3 us).
+__device__ __forceinline__ void tma_store_2d_first_out(const void *tmap, uint32_t src, int32_t x,
+                                                       int32_t y)
 {
-    const int j = lane & 3, c = j * 8;
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group.L2::cache_hint"
+        " [%0, {%2, %3}], [%1], %4;" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+        "r"(src), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+}
+
+// Staging of 16-bit results: boxes of 32 rows x 64 columns (128 bytes a row) in
+// the 128-byte swizzle, 16-byte piece j of row r at j ^ (r mod 8).
+__device__ __forceinline__ uint32_t staged_at(uint32_t box, int r, int j)
+{
+    return box + (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4));
+}
+
+// Pieces j0 .. j0 + PIECES - 1 of the first `rows` (of 32) rows of a staged box
+// to rows of `out` ldo apart (out: the column of piece j0), 16 bytes per lane;
+// columns from `limit` on are left out.
+template <int PIECES>
+__device__ __forceinline__ void copy_staged(uint32_t box, int j0, uint16_t *out, long long ldo,
+                                            int rows, int limit, int lane)
+{
+    const int j = lane % PIECES, c = j * 8;
 #pragma unroll
-    for (int r = lane >> 2; r < 32; r += 8) {
+    for (int r = lane / PIECES; r < 32; r += 32 / PIECES) {
         if (r >= rows || c >= limit) continue;
-        const uint4 v = ld_shared_v4(src + (uint32_t)(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)));
+        const uint4 v = ld_shared_v4(staged_at(box, r, j0 + j));
         uint16_t *dst = out + r * ldo + c;
         if (c + 8 <= limit) {
             *reinterpret_cast<uint4 *>(dst) = v;
@@ -369,10 +368,10 @@ __device__ __forceinline__ void copy_rows_swizzled(uint32_t src, uint16_t *out, 
     }
 }
 
-// The columns from `from` to `limit` - 1 (at most 7 of the 32, which a TMA store
-// leaves out: it clips rows at 16-byte granules) of the same staged rows, a row
+// Columns `from` .. `limit` - 1 (counted from piece j0; at most 7, which a TMA
+// store leaves out: it clips rows at 16-byte granules) of the same rows, a row
 // per lane.
-__device__ __forceinline__ void copy_last_columns(uint32_t src, uint16_t *out, long long ldo,
+__device__ __forceinline__ void copy_last_columns(uint32_t box, int j0, uint16_t *out, long long ldo,
                                                   int rows, int from, int limit, int lane)
 {
     if (lane >= rows) return;
@@ -380,72 +379,87 @@ __device__ __forceinline__ void copy_last_columns(uint32_t src, uint16_t *out, l
         uint16_t v;
         asm volatile("ld.shared.u16 %0, [%1];"
                      : "=h"(v)
-                     : "r"(src + (uint32_t)(lane * 64 + (((c >> 3) ^ ((lane >> 1) & 3)) << 4) + (c & 7) * 2))
+                     : "r"(staged_at(box, lane, j0 + (c >> 3)) + (uint32_t)(c & 7) * 2)
                      : "memory");
         out[lane * ldo + c] = v;
     }
 }
 
-// Before this warp's staging memory is written again: the TMA stores that
-// lane 0 issued from it have read it.
-__device__ __forceinline__ void staging_free(int lane)
+// One chunk of the epilogue: 32 rows of A (from `row`; `rows` of them exist) by
+// the CTA's 128 accumulator rows, 32 per warp of a group of four, which stage
+// their results together so that they leave as whole 128-byte lines: as
+// 32-byte pieces of each warp's own, or 64-byte ones, the stores slowed the
+// main loop's loads by a sixth.  (Staged at all because the results come out
+// transposed, and because the operands take most of the L1 and shared-memory
+// bandwidth: 2-byte shared and row-wise global stores cost 5% of 8192 x 4096 x
+// 4096.)
+struct Chunk {
+    int row, rows;
+    int cta_n0, n0;          // first accumulator column (of C) of the CTA, of this warp
+    int q;                   // warp of the group
+    uint32_t buf;            // the group's staging: boxes of 4 KB
+    int bar;                 // its named barrier
+    int lane;
+};
+constexpr int GROUP_THREADS = 128;
+
+// The group's staging may be written again: what its first warp's TMA stores
+// were to read, they have, and every warp has copied what it copies itself.
+__device__ __forceinline__ void staging_free(const Chunk &c)
 {
-    if (lane == 0) bulk_wait_read_all();
-    __syncwarp();
+    if (c.q == 0 && c.lane == 0) bulk_wait_read_all();
+    named_bar_sync(c.bar, GROUP_THREADS);
 }
 
-// One chunk: the 32 columns n0 .. of C (this warp's lanes of the accumulator,
-// at taddr) by 32 rows of A from `row`, of which `rows` exist.  16-bit results
-// pass through `buf`, this warp's shared memory, where they are transposed:
-// whole chunks then leave through a TMA store, others 16 bytes per lane.  (The
-// main loop's operands take most of the shared-memory and L1 bandwidth, so
-// what the epilogue passes through them shows in the time: 2-byte shared and
-// row-wise global stores cost 5% of 8192 x 4096 x 4096.)
+// What the group has staged is visible to the TMA; true in the thread that
+// issues its stores.
+__device__ __forceinline__ bool staging_done(const Chunk &c)
+{
+    fence_proxy_async_smem();
+    named_bar_sync(c.bar, GROUP_THREADS);
+    return c.q == 0 && c.lane == 0;
+}
+
+// 16-bit results of the plain product.
 __device__ __forceinline__ void emit_store_16(const GrpParams &p, const CUtensorMap *tm,
-                                              uint32_t taddr, int row, int rows, int n0,
-                                              uint32_t buf, int lane)
+                                              uint32_t taddr, const Chunk &c)
 {
     uint32_t lo[16], hi[16];                        // lanes 0..15 and 16..31
     tmem_ld_16x32(taddr, lo);
     tmem_ld_16x32(taddr + (16u << 16), hi);
     tmem_ld_wait(lo);
     tmem_ld_wait(hi);
-    staging_free(lane);
-    const int m = lane >> 3, j8 = lane & 7;         // the 16 bytes that this lane addresses
+    staging_free(c);
+    const uint32_t box = c.buf + (uint32_t)(c.q >> 1) * 4096;
+    const int j0 = (c.q & 1) * 4;                   // this warp's pieces of its rows
+    const int m = c.lane >> 3, j8 = c.lane & 7;     // the 16 bytes that this lane addresses
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         auto pk = [&](const uint32_t(&r)[16], int k) {
             return pack2(p.alpha * __uint_as_float(r[4 * i + k]),
                          p.alpha * __uint_as_float(r[4 * i + k + 1]), p.out_kind);
         };
-        const int r = 8 * i + j8;
-        stmatrix_x4_trans(buf + (uint32_t)(r * 64 + ((m ^ ((r >> 1) & 3)) << 4)), pk(lo, 0), pk(lo, 2),
-                          pk(hi, 0), pk(hi, 2));
+        stmatrix_x4_trans(staged_at(box, 8 * i + j8, j0 + m), pk(lo, 0), pk(lo, 2), pk(hi, 0), pk(hi, 2));
     }
-    if (p.tma_out && rows == 32) {
-        fence_proxy_async_smem();
-        __syncwarp();
+    uint16_t *out = reinterpret_cast<uint16_t *>(p.C) + c.row * p.ldc + c.n0;
+    if (p.tma_out && c.rows == 32) {
         const int whole = p.N & ~7;
-        if (lane == 0 && n0 < whole) {
-            tma_store_2d(tm, buf, n0, row);
+        if (staging_done(c)) {
+            tma_store_2d_first_out(tm, c.buf, c.cta_n0, c.row);
+            if (c.cta_n0 + 64 < whole) tma_store_2d_first_out(tm, c.buf + 4096, c.cta_n0 + 64, c.row);
             bulk_commit_group();
         }
-        if (p.N != whole && n0 + 32 > whole) {
-            copy_last_columns(buf, reinterpret_cast<uint16_t *>(p.C) + row * p.ldc + n0, p.ldc, 32,
-                              whole - n0, p.N - n0, lane);
-            __syncwarp();
-        }
+        if (p.N != whole && c.n0 < p.N && c.n0 + 32 > whole)
+            copy_last_columns(box, j0, out, p.ldc, 32, whole - c.n0, p.N - c.n0, c.lane);
     } else {
         __syncwarp();
-        copy_rows_swizzled(buf, reinterpret_cast<uint16_t *>(p.C) + row * p.ldc + n0, p.ldc, rows,
-                           p.N - n0, lane);
-        __syncwarp();
+        copy_staged<4>(box, j0, out, p.ldc, c.rows, p.N - c.n0, c.lane);
     }
 }
 
-// The same for FP32 results (and partials of K ranges), with beta, and for K = 0 (no accumulator): each
-// lane is a column, its stores (and loads of C) of one row are 64 or 128 bytes
-// a warp.
+// FP32 results (and partials of K ranges), beta, and K = 0 (no accumulator):
+// each lane is a column, its stores (and loads of C) of one row are 64 or 128
+// bytes a warp.
 __device__ __forceinline__ void emit_store_direct(const GrpParams &p, uint32_t taddr,
                                                   long long offset, int row, int rows, int n0,
                                                   int lane)
@@ -480,36 +494,43 @@ __device__ __forceinline__ void emit_store_direct(const GrpParams &p, uint32_t t
 template <int EPI>
 __device__ __forceinline__ void emit_swiglu(const GrpParams &p, const GrpMaps &maps,
                                             const uint32_t (&acc)[32], const uint32_t (&dy)[16],
-                                            int row, int rows, int n0, uint32_t buf, int lane)
+                                            const Chunk &c)
 {
-    staging_free(lane);
-    const int odd = lane & 1;
+    staging_free(c);
+    const int odd = c.lane & 1;
+    // where this lane's results go: of the 64 output columns, and of the 128 of dH
+    const uint32_t y_box = c.buf + (EPI == GRP_SWIGLU ? 0 : 8192);
+    const int y_j0 = c.q * 2;
+    const uint32_t h_box = c.buf + (uint32_t)(c.q >> 1) * 4096;
+    const int h_j0 = (c.q & 1) * 4;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         const uint32_t send = odd ? acc[2 * j] : acc[2 * j + 1];
         const float got = __uint_as_float(__shfl_xor_sync(0xffffffffu, send, 1));
         const float g = p.alpha * (odd ? got : __uint_as_float(acc[2 * j]));
         const float u = p.alpha * (odd ? __uint_as_float(acc[2 * j + 1]) : got);
-        const uint32_t at = (uint32_t)((2 * j + odd) * 16 + lane / 2);
+        const int r = 2 * j + odd;
+        const uint32_t y_at = staged_at(y_box, r, y_j0 + (c.lane >> 4)) + (uint32_t)((c.lane >> 1) & 7) * 2;
         if (EPI == GRP_SWIGLU) {
-            st_shared_u16(buf + at * 2, to_16(silu_f32(g) * u, OUT_BF16));
+            st_shared_u16(y_at, to_16(silu_f32(g) * u, OUT_BF16));
         } else {
             const float s = __fdividef(1.0f, 1.0f + __expf(-g));
             const float d = __uint_as_float(dy[j]);
             const float gs = g * s;
-            st_shared_u32(buf + at * 4, pack2(d * u * (s + gs * (1.0f - s)), d * gs, OUT_BF16));
-            if (p.Y) st_shared_u16(buf + 2048 + at * 2, to_16(gs * u, OUT_BF16));
+            st_shared_u32(staged_at(h_box, r, h_j0 + (c.lane >> 3)) + (uint32_t)((c.lane >> 1) & 3) * 4,
+                          pack2(d * u * (s + gs * (1.0f - s)), d * gs, OUT_BF16));
+            if (p.Y) st_shared_u16(y_at, to_16(gs * u, OUT_BF16));
         }
     }
-    if (rows == 32) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
+    if (c.rows == 32) {
+        if (staging_done(c)) {
             if (EPI == GRP_SWIGLU) {
-                tma_store_2d(&maps.c, buf, n0 / 2, row);
+                tma_store_2d_first_out(&maps.c, y_box, c.cta_n0 / 2, c.row);
             } else {
-                tma_store_2d(&maps.c, buf, n0, row);
-                if (p.Y) tma_store_2d(&maps.y, buf + 2048, n0 / 2, row);
+                tma_store_2d_first_out(&maps.c, c.buf, c.cta_n0, c.row);
+                if (c.cta_n0 + 64 < p.N)
+                    tma_store_2d_first_out(&maps.c, c.buf + 4096, c.cta_n0 + 64, c.row);
+                if (p.Y) tma_store_2d_first_out(&maps.y, y_box, c.cta_n0 / 2, c.row);
             }
             bulk_commit_group();
         }
@@ -517,17 +538,16 @@ __device__ __forceinline__ void emit_swiglu(const GrpParams &p, const GrpMaps &m
     }
     __syncwarp();
     if (EPI == GRP_SWIGLU) {
-        copy_rows<16>(buf, reinterpret_cast<uint16_t *>(p.C) + row * p.ldc + n0 / 2, p.ldc, rows,
-                      (p.N - n0) / 2, lane);
+        copy_staged<2>(y_box, y_j0, reinterpret_cast<uint16_t *>(p.C) + c.row * p.ldc + c.n0 / 2, p.ldc,
+                       c.rows, (p.N - c.n0) / 2, c.lane);
     } else {
-        copy_rows<32>(buf, reinterpret_cast<uint16_t *>(p.C) + row * p.ldc + n0, p.ldc, rows,
-                      p.N - n0, lane);
+        copy_staged<4>(h_box, h_j0, reinterpret_cast<uint16_t *>(p.C) + c.row * p.ldc + c.n0, p.ldc,
+                       c.rows, p.N - c.n0, c.lane);
         if (p.Y)
-            copy_rows<16>(buf + 2048,
-                          reinterpret_cast<uint16_t *>(p.Y) + row * (long long)(p.N / 2) + n0 / 2,
-                          p.N / 2, rows, (p.N - n0) / 2, lane);
+            copy_staged<2>(y_box, y_j0,
+                           reinterpret_cast<uint16_t *>(p.Y) + c.row * (long long)(p.N / 2) + c.n0 / 2,
+                           p.N / 2, c.rows, (p.N - c.n0) / 2, c.lane);
     }
-    __syncwarp();
 }
 
 // One stage of 4-bit operands: the scales to tensor memory (from column sf on:
@@ -800,15 +820,21 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
         const int q = warp & 3;                 // tensor-memory lane quarter of this warp
         const int h = (warp - EPI_WARP0) / 4;   // of HALVES warps a quarter: every HALVES-th
         constexpr int HALVES = C::EPI_WARPS / 4;    // chunk of 32 rows of A
-        const uint32_t buf = smem_u32(sOut + (warp - EPI_WARP0) * C::OUT_BYTES);
+        Chunk ch;
+        ch.q = q;
+        ch.buf = smem_u32(sOut + h * 4 * C::OUT_BYTES);
+        ch.bar = 1 + h;
+        ch.lane = lane;
         int n = 0;
         for (int u = u0; u < units; u += du, ++n) {
             const int split = p.splits == 1 ? 0 : u % p.splits;
             const GrpTile t = grp_tile(start, first, steps, G, p.n_blocks,
                                        p.splits == 1 ? u : u / p.splits);
             const int acc = n & 1;
-            const int n0 = t.nb * 256 + (int)rank * 128 + q * 32;
-            const bool work = n0 < p.N;
+            ch.cta_n0 = t.nb * 256 + (int)rank * 128;
+            ch.n0 = ch.cta_n0 + q * 32;
+            const int n0 = ch.n0;
+            const bool work = ch.cta_n0 < p.N;      // (the same for the whole group)
             const int chunks = ceil_div(t.rows, 32);
             uint32_t dy[16];
             auto load_dy = [&](int c) {
@@ -825,20 +851,22 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
             };
             if (h < chunks) load_dy(h);
             if (p.k_blocks > 0) {
-                bool ok = wait_bounded(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, p.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                const bool ok = wait_bounded(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, p.err);
+                // the whole group leaves, or none of it
+                if (!named_bar_and(ch.bar, GROUP_THREADS, ok)) break;
                 tc_fence_after();
             }
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * C::ACC_STRIDE;
 #pragma unroll 1
             for (int c = h; c < chunks && work; c += HALVES) {
-                const int row = t.row0 + c * 32, rows = min(32, t.rows - c * 32);
+                ch.row = t.row0 + c * 32;
+                ch.rows = min(32, t.rows - c * 32);
                 if (EPI == GRP_STORE) {
                     if (p.out_kind != OUT_F32 && p.beta == 0.0f && p.k_blocks > 0)
-                        emit_store_16(p, &maps.c, t_row + c * 32, row, rows, n0, buf, lane);
+                        emit_store_16(p, &maps.c, t_row + c * 32, ch);
                     else
-                        emit_store_direct(p, t_row + c * 32, split * p.split_stride, row, rows, n0, lane);
+                        emit_store_direct(p, t_row + c * 32, split * p.split_stride, ch.row, ch.rows, n0,
+                                          lane);
                     continue;
                 }
                 uint32_t r[32];
@@ -849,7 +877,7 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = 0;
                 }
-                emit_swiglu<EPI>(p, maps, r, dy, row, rows, n0, buf, lane);
+                emit_swiglu<EPI>(p, maps, r, dy, ch);
                 if (c + HALVES < chunks) load_dy(c + HALVES);
             }
             if (p.k_blocks > 0) {
@@ -858,7 +886,7 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
                 if (lane == 0) mbar_arrive_remote_tmem(mapa_shared(smem_u32(&acc_empty[acc]), 0));
             }
         }
-        staging_free(lane);                     // before this CTA's shared memory goes
+        if (q == 0 && lane == 0) bulk_wait_read_all();      // before this CTA's shared memory goes
     }
 
     // Neither CTA frees its tensor memory or exits while the leader's MMAs or

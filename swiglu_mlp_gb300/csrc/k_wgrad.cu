@@ -25,7 +25,7 @@ namespace {
 struct WgradMaps {
     CUtensorMap a, d;                    // boxes of 64 rows
     CUtensorMap a16, d16;                // boxes of 16 rows
-    CUtensorMap c;                       // 16-bit output, in boxes of 32 x 32 (tma_out)
+    CUtensorMap c;                       // 16-bit output, boxes of 64 columns x 32 rows (tma_out)
 };
 
 struct WgradParams {
@@ -383,15 +383,18 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     } else {
         // ------------------------------------------------------------ epilogue
         // Each lane holds 32 consecutive columns of its row of C.  16-bit results
-        // pass through shared memory and leave 32 x 32 at a time with TMA stores
-        // (but the last columns of rows that do not end on 16 bytes):
-        // stored by the lanes themselves they touch 32 lines per instruction, and
-        // the main loop, whose operands use the same memory, took a fifth longer.
+        // pass through shared memory: the two warps of a lane quarter stage 32
+        // rows x 64 columns, whole 128-byte lines, which leave with a TMA store
+        // (but the last columns of rows that do not end on 16 bytes).  Stored by
+        // the lanes themselves they touch 32 lines per instruction, and the main
+        // loop, whose operands use the same memory, took a fifth longer.
         const int q = warp & 3;
         const int h = (warp - EPI_WARP0) / 4;
         const int row = q * 32 + lane;
-        const uint32_t buf = smem_u32(sOut + (warp - EPI_WARP0) * OUT_BYTES);
-        const int per_half = p.n_step / 64;     // chunks of 32 columns
+        const uint32_t box = smem_u32(sOut + q * 2 * OUT_BYTES);
+        const int bar = 1 + q;
+        constexpr int PAIR_THREADS = 64;
+        const bool issuer = h == 0 && lane == 0;
         TileParams tp{};
         tp.alpha = p.alpha;
         tp.beta = p.beta;
@@ -402,9 +405,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
             const WgradTile t = wgrad_tile(p, start, u);
             const int acc = n & 1;
             if (t.rows > 0) {
-                bool ok = wait_bounded(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, p.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                const bool ok = wait_bounded(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, p.err);
+                if (!named_bar_and(bar, PAIR_THREADS, ok)) break;    // both warps leave, or none
                 tc_fence_after();
             }
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
@@ -413,18 +415,20 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
                                   t.split * p.split_stride;
             uint32_t r[32];
 #pragma unroll 1
-            for (int c = h * per_half; c < (h + 1) * per_half; ++c) {
-                const int col = t.nb * p.n_step + c * 32;
-                if (k - lane >= p.K || col >= p.N) break;        // the whole warp
+            for (int c = 0; c < p.n_step / 64; ++c) {
+                const int col0 = t.nb * p.n_step + c * 64;
+                if (k - lane >= p.K || col0 >= p.N) break;       // (the same for both warps)
+                const int col = col0 + h * 32;
                 if (t.rows > 0) {
-                    tmem_ld_32cols(t_row + c * 32, r);
+                    tmem_ld_32cols(t_row + c * 64 + h * 32, r);
                     tmem_ld_wait(r);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = 0;
                 }
                 if (p.staged) {
-                    staging_free(lane);
+                    if (issuer) bulk_wait_read_all();
+                    named_bar_sync(bar, PAIR_THREADS);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t w[4];
@@ -432,33 +436,25 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
                         for (int i = 0; i < 4; ++i)
                             w[i] = pack2(p.alpha * __uint_as_float(r[8 * j + 2 * i]),
                                          p.alpha * __uint_as_float(r[8 * j + 2 * i + 1]), p.out_kind);
-                        st_shared_v4(buf + (uint32_t)(lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)),
-                                     make_uint4(w[0], w[1], w[2], w[3]));
+                        st_shared_v4(staged_at(box, lane, h * 4 + j), make_uint4(w[0], w[1], w[2], w[3]));
                     }
+                    uint16_t *dst = reinterpret_cast<uint16_t *>(p.C) + out - lane * p.ldc + col;
+                    const int rows = p.K - (k - lane);
                     if (p.tma_out) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
                         const int whole = p.N & ~7;
-                        if (lane == 0 && col < whole) {
-                            tma_store_3d(&maps.c, buf, col, k, t.g);
+                        fence_proxy_async_smem();
+                        named_bar_sync(bar, PAIR_THREADS);
+                        if (issuer && col0 < whole) {
+                            tma_store_3d(&maps.c, box, col0, k, t.g);
                             bulk_commit_group();
                         }
-                        if (p.N != whole && col + 32 > whole) {
-                            copy_last_columns(buf,
-                                              reinterpret_cast<uint16_t *>(p.C) + out -
-                                                  lane * p.ldc + col,
-                                              p.ldc, p.K - (k - lane), whole - col, p.N - col, lane);
-                            __syncwarp();
-                        }
+                        if (p.N != whole && col < p.N && col + 32 > whole)
+                            copy_last_columns(box, h * 4, dst, p.ldc, rows, whole - col, p.N - col, lane);
                     } else {
                         __syncwarp();
-                        copy_rows_swizzled(buf,
-                                           reinterpret_cast<uint16_t *>(p.C) + out -
-                                               lane * p.ldc + col,
-                                           p.ldc, p.K - (k - lane), p.N - col, lane);
-                        __syncwarp();
+                        copy_staged<4>(box, h * 4, dst, p.ldc, rows, p.N - col, lane);
                     }
-                } else if (k < p.K) {
+                } else if (k < p.K && col < p.N) {
                     float v[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
@@ -472,7 +468,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
                 if (lane == 0) mbar_arrive_remote_tmem(mapa_shared(smem_u32(&acc_empty[acc]), 0));
             }
         }
-        staging_free(lane);                     // before this CTA's shared memory goes
+        if (issuer) bulk_wait_read_all();           // before this CTA's shared memory goes
     }
 
     tc_fence_before();
@@ -536,8 +532,8 @@ cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, 
         const uint64_t ld = (uint64_t)a.ldc * 2;
         const uint64_t dims[] = {(uint64_t)(N & ~7), (uint64_t)K, (uint64_t)a.groups.G};
         const uint64_t st[] = {ld, a.groups.G > 1 ? (uint64_t)a.strideC * 2 : ld * K};
-        const uint32_t box[] = {32, 32, 1};
-        mapped = mapped && encode_tiled(&m.c, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, a.C, dims, st, box, 64);
+        const uint32_t box[] = {64, 32, 1};
+        mapped = mapped && encode_tiled(&m.c, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, a.C, dims, st, box, 128);
     }
     if (!mapped) return cudaErrorInvalidValue;
     const long long units = (long long)a.groups.G * p.k_tiles * p.n_tiles * p.splits;
