@@ -522,7 +522,7 @@ __device__ __forceinline__ void emit_swiglu(const GrpParams &p, const GrpMaps &m
             if (p.Y) st_shared_u16(y_at, to_16(gs * u, OUT_BF16));
         }
     }
-    if (c.rows == 32) {
+    if (p.tma_out && c.rows == 32) {
         if (staging_done(c)) {
             if (EPI == GRP_SWIGLU) {
                 tma_store_2d_first_out(&maps.c, y_box, c.cta_n0 / 2, c.row);
