@@ -445,7 +445,7 @@ __device__ __forceinline__ void emit_store_16(const GrpParams &p, const CUtensor
     if (p.tma_out && c.rows == 32) {
         const int whole = p.N & ~7;
         if (staging_done(c)) {
-            tma_store_2d_first_out(tm, c.buf, c.cta_n0, c.row);
+            if (c.cta_n0 < whole) tma_store_2d_first_out(tm, c.buf, c.cta_n0, c.row);
             if (c.cta_n0 + 64 < whole) tma_store_2d_first_out(tm, c.buf + 4096, c.cta_n0 + 64, c.row);
             bulk_commit_group();
         }
