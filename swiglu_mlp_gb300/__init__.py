@@ -2,7 +2,9 @@
 
 Argument marshalling only: every step of the computation runs in the
 library's CUDA kernels.  There is no fallback of any kind; if the shared
-library has not been built this module raises on first use.
+library has not been built this module raises on first use.  (ctypes, but for
+the ``*_into`` helpers of the expert MLP, which go through the CPython module
+``_binding``.)
 
 Functions with the C names take the C arguments (pointers may be given as
 ints or as tensors, whose ``data_ptr()`` is used; ``stream`` may be a
@@ -409,13 +411,17 @@ def interleave_weights(W1, W2, stream=None):
 # messages are only built when one is raised.
 
 _torch = None
+_bound = None         # the CPython module of the C functions these helpers call
 
 
 def _fast():
-    """torch, loaded with the library on the first call."""
-    global _torch
+    """torch, loaded with the library and its binding on the first call."""
+    global _torch, _bound
     load()
+    import importlib
+
     import torch
+    _bound = importlib.import_module("._binding", __name__)
     _torch = torch
     return torch
 
@@ -482,7 +488,7 @@ def gemm_grouped_into(C, A, B, offsets, transB=0, alpha=1.0, beta=0.0, stream=No
     B is [G, K, N] (transB = 0) or [G, N, K], offsets int32 [G + 1] on the GPU."""
     w = "gemm_grouped_into"
     _torch or _fast()
-    lib = _lib
+    lib = _bound
     off, G = _groups(offsets, w)
     rows, cols, ldb, stride = _matrices(B, "B", w, G)
     N, Kb = (rows, cols) if transB else (cols, rows)
@@ -502,7 +508,7 @@ def gemm_grouped_wgrad_into(C, A, D, offsets, alpha=1.0, beta=0.0, stream=None):
     """C[G, K, N] <- alpha * A_g^T D_g + beta * C_g from A[M, K] and D[M, N]."""
     w = "gemm_grouped_wgrad_into"
     _torch or _fast()
-    lib = _lib
+    lib = _bound
     off, G = _groups(offsets, w)
     rows, cols, ldc, stride = _matrices(C, "C", w, G)
     M, K, lda = _matrix(A, "A", w)
@@ -530,7 +536,7 @@ def swiglu_grouped_into(Y, A, W_fused, offsets, stream=None):
     """Y[M, N] <- SiLU(A W1_g) (.) (A W2_g), W_fused [G, K, 2N] interleaved."""
     w = "swiglu_grouped_into"
     torch = _torch or _fast()
-    lib = _lib
+    lib = _bound
     off, G = _groups(offsets, w)
     M, N, K = _swiglu_shapes(w, A, W_fused, G, torch.bfloat16)
     _output(w, "Y", Y, M, N, torch.bfloat16)
@@ -546,7 +552,7 @@ def swiglu_grouped_grad_into(dH, A, W_fused, dY, offsets, Y=None, stream=None):
     Up, from dY[M, N]; Y, when given, receives swiglu_grouped's result."""
     w = "swiglu_grouped_grad_into"
     torch = _torch or _fast()
-    lib = _lib
+    lib = _bound
     off, G = _groups(offsets, w)
     M, N, K = _swiglu_shapes(w, A, W_fused, G, torch.bfloat16)
     _output(w, "dH", dH, M, 2 * N, torch.bfloat16)
@@ -583,7 +589,7 @@ def mx4_quantize_into(Q, S, X, format, scale=1.0, offsets=None, stream=None):
     """Q, S <- X[M, K] * scale in 4 bits (Q uint8 rows of codes, S scale tiles)."""
     w = "mx4_quantize_into"
     torch = _torch or _fast()
-    lib = _lib
+    lib = _bound
     off, G = _groups(offsets, w)
     M, K, ldx = _matrix(X, "X", w)
     ldq = _mx4_rows(w, Q, S, format, G, M, K, torch)
@@ -598,7 +604,7 @@ def mx4_dequantize_into(X, Q, S, format, scale=1.0, offsets=None, stream=None):
     """X[M, K] <- scale * the values of the 4-bit rows (Q, S)."""
     w = "mx4_dequantize_into"
     torch = _torch or _fast()
-    lib = _lib
+    lib = _bound
     off, G = _groups(offsets, w)
     M, K, ldx = _matrix(X, "X", w)
     ldq = _mx4_rows(w, Q, S, format, G, M, K, torch)
@@ -626,7 +632,7 @@ def gemm_mx4_into(C, Q, S, W, SW, K, format, alpha=1.0, beta=0.0, offsets=None, 
     and weights (W [N, bytes] or [G, N, bytes], SW)."""
     w = "gemm_mx4_into"
     torch = _torch or _fast()
-    lib = _lib
+    lib = _bound
     off, G = _groups(offsets, w)
     M, Nc, ldc = _matrix(C, "C", w)
     lda = _mx4_rows(w, Q, S, format, G, M, K, torch)
@@ -646,7 +652,7 @@ def swiglu_mx4_into(Y, Q, S, W, SW, K, format, alpha=1.0, offsets=None, stream=N
     [G, 2N, bytes] with Gate in even and Up in odd rows."""
     w = "swiglu_mx4_into"
     torch = _torch or _fast()
-    lib = _lib
+    lib = _bound
     off, G = _groups(offsets, w)
     M = Q.shape[0]
     lda = _mx4_rows(w, Q, S, format, G, M, K, torch)

@@ -2,7 +2,8 @@
 
 Each translation unit is compiled in parallel to ``_build/*.o`` and the objects
 are linked into one shared library (CUDA runtime linked statically).  Objects
-are rebuilt only when a source or header is newer than them.
+are rebuilt only when a source or header is newer than them.  The CPython module
+``_binding`` (plain C, gcc) is linked against that library beside it.
 """
 from __future__ import annotations
 
@@ -10,12 +11,14 @@ import concurrent.futures as cf
 import glob
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libswiglu_mlp.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["api.cu", "api_experts.cu", "k_grouped.cu", "k_grouped_mx4.cu", "k_wgrad.cu", "k_mx4.cu", "k_reduce.cu", "k_store.cu", "k_swiglu.cu", "k_splitk.cu", "k_fp8.cu", "k_gemv.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -70,6 +73,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    src = os.path.join(CSRC, "binding.c")
+    if force or _stale(BINDING, [src] + hdrs):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        run(["gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", INCLUDE,
+             "-I", sysconfig.get_paths()["include"], src, "-o", tmp,
+             "-L", HERE, "-lswiglu_mlp", "-Wl,-rpath,$ORIGIN"])
+        os.replace(tmp, BINDING)
     return LIB
 
 
