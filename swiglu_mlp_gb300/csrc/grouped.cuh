@@ -620,7 +620,14 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
-        if (p.k_blocks > 0) tma_prefetch_desc(&maps.w);
+        if (p.k_blocks > 0) {                        // fetched from memory on first use
+            tma_prefetch_desc(&maps.w);
+            tma_prefetch_desc(&maps.t[TOKEN_BOXES - 1]);
+            if (F4) {
+                tma_prefetch_desc(&maps.sw);
+                tma_prefetch_desc(&maps.st);
+            }
+        }
         for (int s = 0; s < S; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
@@ -644,31 +651,37 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
     // Up to here only this pair's own resources; now the offsets may be read.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int G = p.groups.G;
-    group_starts<C::THREADS>(p.groups, start, p.err);
-    // (tiles of one width do for groups that all fit the narrowest)
-    const int most = p.groups.M <= C::TOKENS - (C::CANDIDATES - 1) * C::UNIT
-                         ? C::TOKENS
-                         : choose_rows<C>(start, G, p.n_blocks, p.k_blocks, (int)(gridDim.x >> 1),
-                                             reinterpret_cast<float *>(scratch + 16));
-    for (int g = threadIdx.x; g < G; g += C::THREADS)
-        steps[g] = (uint8_t)(tile_step<C>(max(1, start[g + 1] - start[g]), most) / 16);
-    tile_sums<C::THREADS>(G, start, first, scratch, [most](int n) { return ceil_div(n, most); });
-    if (F4)
-        tile_sums<C::THREADS>(G, start, stile, scratch, [](int n) { return ceil_div(n, 128); });
+    // so few rows that a group has at most one tile, and one of the narrowest width
+    const bool narrow = p.groups.M <= C::TOKENS - (C::CANDIDATES - 1) * C::UNIT;
+    if (narrow && G < 32 * WARP_ROUNDS) {
+        static_assert(!F4 || C::TOKENS - (C::CANDIDATES - 1) * C::UNIT <= 128, "one scale tile");
+        if (warp == 0)
+            warp_tables(p.groups, p.err, [&](int i, int s, int rows, int tile) {
+                start[i] = s;
+                first[i] = tile;
+                if (F4) stile[i] = tile;
+                if (i < G) steps[i] = (uint8_t)(ceil_div(max(1, rows), C::UNIT) * (C::UNIT / 16));
+            });
+        __syncthreads();
+    } else {
+        group_starts<C::THREADS>(p.groups, start, p.err);
+        const int most = narrow ? C::TOKENS
+                                : choose_rows<C>(start, G, p.n_blocks, p.k_blocks,
+                                                 (int)(gridDim.x >> 1),
+                                                 reinterpret_cast<float *>(scratch + 16));
+        for (int g = threadIdx.x; g < G; g += C::THREADS)
+            steps[g] = (uint8_t)(tile_step<C>(max(1, start[g + 1] - start[g]), most) / 16);
+        tile_sums<C::THREADS>(G, start, first, scratch,
+                              [most](int n) { return ceil_div(n, most); });
+        if (F4)
+            tile_sums<C::THREADS>(G, start, stile, scratch, [](int n) { return ceil_div(n, 128); });
+    }
     const int units = first[G] * p.n_blocks * p.splits;
     const int u0 = (int)(blockIdx.x >> 1), du = (int)(gridDim.x >> 1);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (p.k_blocks > 0) {
-            if (lane == 0) {                         // fetched from memory on first use
-                tma_prefetch_desc(&maps.t[TOKEN_BOXES - 1]);
-                if (F4) {
-                    tma_prefetch_desc(&maps.sw);
-                    tma_prefetch_desc(&maps.st);
-                }
-            }
-            __syncwarp();
             const uint32_t empty0 = smem_u32(empty), full0 = smem_u32(full);
             const uint32_t full_leader0 = mapa_shared(full0, 0);
             const uint32_t w_dst0 = smem_u32(sW), t_dst0 = smem_u32(sT), s_dst0 = smem_u32(sS);

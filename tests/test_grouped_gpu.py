@@ -418,3 +418,34 @@ def test_split_calls_in_a_graph_need_their_workspace_first():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(C, first) and swg.get_device_error() == 0
+
+
+@pytest.mark.parametrize("M", [1, 64, 65, 144, 145])
+@pytest.mark.parametrize("G", [1, 2, 31, 32, 33, 96, 127, 128, 129, 600])
+def test_few_rows_over_many_groups(M, G):
+    """Most groups empty, the rows anywhere among them, the outer groups too."""
+    r = np.random.default_rng(G * 1000 + M)
+    rows = np.bincount(r.integers(0, G, M - M // 2), minlength=G) + \
+        np.bincount(r.choice([0, G // 2, G - 1], M // 2), minlength=G)
+    run_gemm([int(n) for n in rows], 40, 72, ("bf16", "bf16"), G % 2, seed=G)
+
+
+@pytest.mark.parametrize("M", [50, 140, 200])
+@pytest.mark.parametrize("G", [5, 40, 127, 130])
+def test_bad_offsets_run_the_clamped_groups(M, G):
+    """What runs is the groups that the documented clamping leaves."""
+    r = np.random.default_rng(G * 1000 + M)
+    off = np.sort(r.integers(0, M + 1, G + 1))
+    off[[0, -1]] = 0, M
+    at = r.choice(G + 1, 4)
+    off[at] = [off[at[0]] - 30, -7, M + 9, off[at[3]] // 2]
+    off[1] = max(off[1], 1)
+    off[2] = 0                                        # at least one is out of order
+    clamped = np.maximum.accumulate(np.clip(off, 0, M))
+    g = synth.generator(G)
+    A, B = padded(M, 72, g, torch.bfloat16), padded(G * 72, 40, g, torch.bfloat16).unflatten(0, (G, 72))
+    C = Guarded(M, 40, torch.bfloat16, init=torch.zeros((M, 40), dtype=torch.bfloat16))
+    swg.gemm_grouped_into(C.view, A, B, torch.from_numpy(off.astype(np.int32)).cuda())
+    assert swg.get_device_error() == 1
+    want, tol = plain.product(plain.f64(A), plain.f64(B), clamped, 0, 1.0, 0.0, np.zeros((M, 40)), "bf16")
+    check(C.cpu("clamped groups"), want, tol, f"clamped groups {M} {G}")
