@@ -80,14 +80,13 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
     const bool f4 = kind >= swg::GRP_MXFP4, nv = kind == swg::GRP_NVFP4;
     const int64_t M = a.groups.M, G = a.groups.G, N = a.N, K = a.K;
     const bool few = M <= swg::GrpCfg<swg::MATH_16, true>::TOKENS;
-    const int tokens = few  ? swg::GrpCfg<swg::MATH_16, true>::TOKENS
-                       : f4 ? swg::GrpCfg<swg::MATH_MX, false>::TOKENS
-                            : swg::GrpCfg<swg::MATH_16, false>::TOKENS;
+    const int tokens = few ? swg::GrpCfg<swg::MATH_16, true>::TOKENS
+                           : swg::GrpCfg<swg::MATH_16, false>::TOKENS;
     // Boxes of A's rows: of box i (see GrpMaps) those that tiles of at most
     // `half` rows per CTA can ask for.
     const int64_t half = std::min<int64_t>(tokens, ceil_to(M, 16)) / 2;
-    auto box_rows = [&](int i) { return i == 0 ? tokens / 2u : 128u >> i; };
-    auto box_used = [&](int i) { return i + 1 == swg::TOKEN_BOXES || half > (64 >> i); };
+    auto box_rows = [&](int i) { return (uint32_t)swg::token_box(i); };
+    auto box_used = [&](int i) { return i + 1 == swg::TOKEN_BOXES || half > swg::token_box(i + 1); };
 
     swg::GrpParams p{};
     p.groups = a.groups;

@@ -103,7 +103,9 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr)
 
 enum GrpMath { MATH_16 = 0, MATH_MX = 1, MATH_NV = 2 };
 
-constexpr int TOKEN_BOXES = 4;           // box heights of A's maps: TOKENS / 2, 64, 32, 16 rows
+// A's maps: boxes of 128, 96, 64, 32 and 16 rows.
+constexpr int TOKEN_BOXES = 5;
+__host__ __device__ constexpr int token_box(int i) { return i == 0 ? 128 : i == 1 ? 96 : 128 >> (i - 1); }
 
 struct GrpMaps {
     CUtensorMap w;                       // weights
@@ -136,20 +138,19 @@ struct GrpParams {
 };
 
 // FEW: the form for at most 64 rows of A in all, which streams weights from
-// memory.  Its stages hold 64 rows of A instead of 256 (192) and are 8 to 10
+// memory.  Its stages hold 64 rows of A instead of 256 and are 8 to 10
 // instead of 5 or 6, so that more of the weight is in flight.  (Two CTAs of
 // half the depth per SM instead were slower: 8 groups of one row, 4096 x 1024
 // each, 21.4 us against 18.2 with 6 stages.)
 template <int MATH, bool FEW>
 struct GrpCfg {
     static constexpr bool F4 = MATH != MATH_16;
-    // Rows of A per tile: two accumulators fill tensor memory at 256; with
-    // scales there they leave room at 192.
-    static constexpr int TOKENS = FEW ? 64 : F4 ? 192 : 256;
+    // Rows of A per tile: two accumulators fill tensor memory at 256.
+    static constexpr int TOKENS = FEW ? 64 : 256;
     // A tile begins at a multiple of UNIT rows of its group (4-bit: 64 rows are
     // two columns of scales) and may be CANDIDATES widths, see choose_rows.
     static constexpr int UNIT = F4 ? 64 : 16;
-    static constexpr int CANDIDATES = FEW ? 1 : F4 ? 2 : 8;
+    static constexpr int CANDIDATES = FEW ? 1 : F4 ? 3 : 8;
     static constexpr int EPI_WARPS = FEW ? 4 : 8;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int TILES_PER_STAGE = MATH == MATH_NV ? 4 : 2;   // scale tiles along K
@@ -166,12 +167,30 @@ struct GrpCfg {
     static constexpr int LIMIT = 232448 - FIXED - table_bytes(MAX_GROUPS);
     static constexpr int STAGES_RAW = LIMIT / STAGE_BYTES;
     static constexpr int STAGES = STAGES_RAW > 6 && !FEW ? 6 : STAGES_RAW;
-    static constexpr int smem_bytes(int G) { return STAGES * STAGE_BYTES + FIXED + table_bytes(G); }
-    static constexpr int ACC_STRIDE = TOKENS;     // tensor-memory columns per accumulator
-    static constexpr int SCALE_COL = 2 * TOKENS;  // first scale column (two buffers of 64)
+    // A launch whose tiles have at most 192 rows lays out stages of that many
+    // (MXFP4: 6 instead of 5; 4096 x 4096 x 14336 70 us against 74).
+    static constexpr int T_NARROW = F4 && !FEW ? 192 / 2 * 128 : T_BYTES;
+    static constexpr int NARROW_BYTES = W_BYTES + T_NARROW + STAGE_SCALES;
+    static constexpr int STAGES_NARROW = F4 && !FEW ? LIMIT / NARROW_BYTES : STAGES;
+    static constexpr int RING_BYTES = STAGES * STAGE_BYTES > STAGES_NARROW * NARROW_BYTES
+                                          ? STAGES * STAGE_BYTES : STAGES_NARROW * NARROW_BYTES;
+    static constexpr int smem_bytes(int G) { return RING_BYTES + FIXED + table_bytes(G); }
     static constexpr int TMEM_COLS = !FEW ? 512 : F4 ? 256 : 128;
-    static_assert(STAGES >= 3, "pipeline too shallow");
-    static_assert(2 * TOKENS + (F4 ? 128 : 0) <= TMEM_COLS, "tensor memory");
+    // Two buffers of a stage's scales at the end of tensor memory.  What they
+    // take of it the two accumulators share: the second begins ACC_STRIDE
+    // columns behind the first, and the columns that are in both are emptied
+    // first (OVERLAP, see the epilogue).  With two apart, tiles have 192 rows
+    // at most and the bound is what an SM gets from L2, 64 bytes a cycle: 34 KB
+    // a stage in 290 ns for 200 ns of MMAs (8192 x 14336 x 4096 in NVFP4 156 us
+    // against 143, MXFP4 144 against 139; 16 groups of 512 rows, 4096 x 4096,
+    // 65 against 60 and 61 against 55).
+    static constexpr int SCALE_COLS = F4 ? 12 * TILES_PER_STAGE : 0;
+    static constexpr int SCALE_COL = TMEM_COLS - 2 * SCALE_COLS;
+    static constexpr bool OVERLAP = 2 * TOKENS > SCALE_COL;
+    static constexpr int ACC_STRIDE = OVERLAP ? (SCALE_COL - TOKENS) / 32 * 32 : TOKENS;
+    static constexpr bool TWO_SHARED = OVERLAP && TOKENS - ACC_STRIDE > 64;
+    static_assert(STAGES >= 3 && RING_BYTES % 1024 == 0, "ring");
+    static_assert(ACC_STRIDE + TOKENS <= SCALE_COL && 2 * ACC_STRIDE >= TOKENS, "tensor memory");
 };
 
 // Rows of A covered by each tile of a group of `rows` (> 0) rows, but the
@@ -191,6 +210,10 @@ __device__ __forceinline__ int tile_step(int rows, int most)
 // 256 rows, 228 at 192, 212 at 160 and not less than 195 below (the loading
 // and issuing), and a tile about 0.8 us besides.  994 tiles on 76 pairs are
 // 13.1 waves at 256 rows; 1064 tiles of at most 240 make 14.0 and are 7% faster.
+// In 4 bits, in cycles: a stage takes what its loads do (22 KB and 64 bytes a
+// row, at 64 bytes a cycle) or its MMAs (2.8 a row in NVFP4, 2.55 in MXFP4), and
+// a tile not less than its epilogue (21 a row).  1536 x 4096 x 8192: 22.3 us at
+// the 192 rows that this gives, 26.7 at 256.
 // Warp w of the first eight computes candidate w's; ends with a barrier.
 template <class C>
 __device__ __forceinline__ int choose_rows(const int *start, int G, int n_blocks, int k_blocks,
@@ -214,7 +237,10 @@ __device__ __forceinline__ int choose_rows(const int *start, int G, int n_blocks
         const float units = (float)tiles * (float)n_blocks;
         const float waves = ceilf(units / (float)pairs);
         const float mean = (float)rows / fmaxf((float)tiles, 1.0f);
-        if (lane == 0) costs[cand] = waves * ((float)k_blocks * fmaxf(mean, 176.0f) + 700.0f);
+        const float k = (float)k_blocks;
+        const float tile = C::F4 ? fmaxf(k * fmaxf(330.0f + mean, 2.7f * mean), 21.0f * mean) + 500.0f
+                                 : k * fmaxf(mean, 176.0f) + 700.0f;
+        if (lane == 0) costs[cand] = waves * tile;
     }
     __syncthreads();
     int best = 0;
@@ -298,18 +324,27 @@ __device__ __forceinline__ uint32_t to_16(float v, int out_kind)
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// 16 lanes (from taddr's lane on) x 32 columns of the accumulator in fragments:
-// for each 8 columns i, r[4 i] and r[4 i + 1] are row lane / 4, columns
-// 2 (lane % 4) and + 1; r[4 i + 2] and r[4 i + 3] the same of row lane / 4 + 8.
-__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16])
+// A warp's 32 lanes x 32 columns of the accumulator in fragments: for each 8
+// columns i, r[4 i] and r[4 i + 1] are row lane / 4, columns 2 (lane % 4) and
+// + 1; r[4 i + 2] and r[4 i + 3] the same of row lane / 4 + 8; r[16 + 4 i] ..
+// those of rows + 16.
+template <int FROM>
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[32])
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32"
         " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=r"(r[FROM + 0]), "=r"(r[FROM + 1]), "=r"(r[FROM + 2]), "=r"(r[FROM + 3]),
+          "=r"(r[FROM + 4]), "=r"(r[FROM + 5]), "=r"(r[FROM + 6]), "=r"(r[FROM + 7]),
+          "=r"(r[FROM + 8]), "=r"(r[FROM + 9]), "=r"(r[FROM + 10]), "=r"(r[FROM + 11]),
+          "=r"(r[FROM + 12]), "=r"(r[FROM + 13]), "=r"(r[FROM + 14]), "=r"(r[FROM + 15])
         : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, uint32_t (&r)[32])
+{
+    tmem_ld_16x32<0>(taddr, r);
+    tmem_ld_16x32<16>(taddr + (16u << 16), r);
 }
 
 // Four 8 x 8 matrices of 16-bit values, each stored transposed: matrix m's
@@ -421,25 +456,21 @@ __device__ __forceinline__ bool staging_done(const Chunk &c)
 }
 
 // 16-bit results of the plain product.
+template <int KIND>
 __device__ __forceinline__ void emit_store_16(const GrpParams &p, const CUtensorMap *tm,
-                                              uint32_t taddr, const Chunk &c)
+                                              const uint32_t (&r)[32], const Chunk &c)
 {
-    uint32_t lo[16], hi[16];                        // lanes 0..15 and 16..31
-    tmem_ld_16x32(taddr, lo);
-    tmem_ld_16x32(taddr + (16u << 16), hi);
-    tmem_ld_wait(lo);
-    tmem_ld_wait(hi);
     staging_free(c);
     const uint32_t box = c.buf + (uint32_t)(c.q >> 1) * 4096;
     const int j0 = (c.q & 1) * 4;                   // this warp's pieces of its rows
     const int m = c.lane >> 3, j8 = c.lane & 7;     // the 16 bytes that this lane addresses
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        auto pk = [&](const uint32_t(&r)[16], int k) {
+        auto pk = [&](int k) {
             return pack2(p.alpha * __uint_as_float(r[4 * i + k]),
-                         p.alpha * __uint_as_float(r[4 * i + k + 1]), p.out_kind);
+                         p.alpha * __uint_as_float(r[4 * i + k + 1]), KIND);
         };
-        stmatrix_x4_trans(staged_at(box, 8 * i + j8, j0 + m), pk(lo, 0), pk(lo, 2), pk(hi, 0), pk(hi, 2));
+        stmatrix_x4_trans(staged_at(box, 8 * i + j8, j0 + m), pk(0), pk(2), pk(16), pk(18));
     }
     uint16_t *out = reinterpret_cast<uint16_t *>(p.C) + c.row * p.ldc + c.n0;
     if (p.tma_out && c.rows == 32) {
@@ -457,9 +488,15 @@ __device__ __forceinline__ void emit_store_16(const GrpParams &p, const CUtensor
     }
 }
 
+template <int KIND>
+struct Kind {
+    static constexpr int value = KIND;
+};
+
 // FP32 results (and partials of K ranges), beta, and K = 0 (no accumulator):
 // each lane is a column, its stores (and loads of C) of one row are 64 or 128
 // bytes a warp.
+template <int KIND>
 __device__ __forceinline__ void emit_store_direct(const GrpParams &p, uint32_t taddr,
                                                   long long offset, int row, int rows, int n0,
                                                   int lane)
@@ -480,11 +517,11 @@ __device__ __forceinline__ void emit_store_direct(const GrpParams &p, uint32_t t
         if (p.beta != 0.0f) {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                if (j0 + j < rows) v[j] += p.beta * load_out(p.C, o + j * p.ldc, p.out_kind);
+                if (j0 + j < rows) v[j] += p.beta * load_out(p.C, o + j * p.ldc, KIND);
         }
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            if (j0 + j < rows) store_out(p.C, o + j * p.ldc, v[j], p.out_kind);
+            if (j0 + j < rows) store_out(p.C, o + j * p.ldc, v[j], KIND);
     }
 }
 
@@ -589,22 +626,20 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
 {
     using C = GrpCfg<MATH, FEW>;
     constexpr bool F4 = C::F4;
-    constexpr int S = C::STAGES;
+    constexpr int RING = C::STAGES_NARROW;           // barriers
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     // stages (W, rows of A, scales), output staging, barriers, group table
     uint8_t *sW = smem;
-    uint8_t *sT = sW + S * C::W_BYTES;
-    uint8_t *sS = sT + S * C::T_BYTES;
-    uint8_t *sOut = sS + S * C::STAGE_SCALES;
+    uint8_t *sOut = smem + C::RING_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sOut + C::EPI_WARPS * C::OUT_BYTES);
     uint64_t *full = bars;
-    uint64_t *empty = bars + S;
-    uint64_t *acc_full = bars + 2 * S;
-    uint64_t *acc_empty = bars + 2 * S + 2;
-    uint64_t *mma_done = bars + 2 * S + 4;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 2 * S + 5);
+    uint64_t *empty = bars + RING;
+    uint64_t *acc_full = bars + 2 * RING;
+    uint64_t *acc_empty = bars + 2 * RING + 2;
+    uint64_t *mma_done = bars + 2 * RING + 4;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 2 * RING + 5);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *scratch = reinterpret_cast<int *>(tmem_holder + 4);      // 16 ints, 8 floats
     int *start = reinterpret_cast<int *>(sOut + C::EPI_WARPS * C::OUT_BYTES + C::BAR_BYTES);
@@ -628,13 +663,13 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
                 tma_prefetch_desc(&maps.st);
             }
         }
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < RING; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&acc_full[b]), 1);
-            mbar_init(smem_u32(&acc_empty[b]), 2 * C::EPI_WARPS);
+            mbar_init(smem_u32(&acc_empty[b]), 2 * C::EPI_WARPS);   // (one with OVERLAP)
         }
         mbar_init(smem_u32(mma_done), 1);
         *abort_flag = 0;
@@ -652,6 +687,7 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int G = p.groups.G;
     // so few rows that a group has at most one tile, and one of the narrowest width
+    int most = C::TOKENS;
     const bool narrow = p.groups.M <= C::TOKENS - (C::CANDIDATES - 1) * C::UNIT;
     if (narrow && G < 32 * WARP_ROUNDS) {
         static_assert(!F4 || C::TOKENS - (C::CANDIDATES - 1) * C::UNIT <= 128, "one scale tile");
@@ -665,10 +701,9 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
         __syncthreads();
     } else {
         group_starts<C::THREADS>(p.groups, start, p.err);
-        const int most = narrow ? C::TOKENS
-                                : choose_rows<C>(start, G, p.n_blocks, p.k_blocks,
-                                                 (int)(gridDim.x >> 1),
-                                                 reinterpret_cast<float *>(scratch + 16));
+        if (!narrow)
+            most = choose_rows<C>(start, G, p.n_blocks, p.k_blocks, (int)(gridDim.x >> 1),
+                                  reinterpret_cast<float *>(scratch + 16));
         for (int g = threadIdx.x; g < G; g += C::THREADS)
             steps[g] = (uint8_t)(tile_step<C>(max(1, start[g + 1] - start[g]), most) / 16);
         tile_sums<C::THREADS>(G, start, first, scratch,
@@ -676,6 +711,12 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
         if (F4)
             tile_sums<C::THREADS>(G, start, stile, scratch, [](int n) { return ceil_div(n, 128); });
     }
+    // the ring
+    const bool more = C::STAGES_NARROW > C::STAGES && (narrow || most <= 192);
+    const int S = more ? C::STAGES_NARROW : C::STAGES;
+    const uint32_t t_size = more ? C::T_NARROW : C::T_BYTES;
+    uint8_t *sT = sW + S * C::W_BYTES;
+    uint8_t *sS = sT + S * t_size;
     const int units = first[G] * p.n_blocks * p.splits;
     const int u0 = (int)(blockIdx.x >> 1), du = (int)(gridDim.x >> 1);
 
@@ -698,13 +739,13 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
                 const int g = __shfl_sync(0xffffffffu, t.g, 0);
                 // the lowest box that holds this CTA's rows of A
                 int box = 0;
-                while (box + 1 < TOKEN_BOXES && half <= (64 >> box)) ++box;
+                while (box + 1 < TOKEN_BOXES && half <= token_box(box + 1)) ++box;
                 const CUtensorMap *t_map = &maps.t[box];
                 const int t_row = __shfl_sync(0xffffffffu, t.row0, 0) + (int)rank * half;
                 const int n0 = __shfl_sync(0xffffffffu, t.nb, 0) * 256 + (int)rank * 128;
                 const int w_tile = g * p.w_tiles + n0 / 128;
                 const int t_tile = F4 ? __shfl_sync(0xffffffffu, stile[t.g] + t.local / 128, 0) : 0;
-                const uint32_t t_bytes = box == 0 ? C::T_BYTES : (128u >> box) * 128u;
+                const uint32_t t_bytes = (uint32_t)token_box(box) * 128u;
                 const uint32_t bytes = C::W_BYTES + t_bytes + C::STAGE_SCALES;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait_bounded_warp(empty0 + 8 * stage, phase ^ 1, abort_flag, p.err)) {
@@ -713,7 +754,7 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
                     }
                     const uint32_t fb = full_leader0 + 8 * stage;
                     const uint32_t w_dst = w_dst0 + stage * C::W_BYTES;
-                    const uint32_t t_dst = t_dst0 + stage * C::T_BYTES;
+                    const uint32_t t_dst = t_dst0 + stage * t_size;
                     const uint32_t s_dst = s_dst0 + stage * C::STAGE_SCALES;
                     const int k0 = kb * (F4 ? 128 : 64);     // inner coordinate of the boxes
                     const int x = kb * (C::SCALE_BYTES / 8);
@@ -781,7 +822,9 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
                 // a tile of A that begins at the second half of its scale tile
                 const uint32_t t_shift = __shfl_sync(0xffffffffu, (t.local & 64) ? 2u : 0u, 0);
                 const int acc = n & 1;
-                if (!wait_bounded_warp(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, p.err)) {
+                // the accumulator, or what it shares with the last tile's, is empty
+                if (!wait_bounded_warp(smem_u32(&acc_empty[C::OVERLAP ? 0 : acc]),
+                                       ((C::OVERLAP ? n : n >> 1) & 1) ^ 1, abort_flag, p.err)) {
                     ok = false;
                     break;
                 }
@@ -795,7 +838,7 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
                     }
                     tc_fence_after();
                     const uint64_t w_stage = w_desc + (uint64_t)(stage * (C::W_BYTES >> 4));
-                    const uint64_t t_stage = t_desc + (uint64_t)(stage * (C::T_BYTES >> 4));
+                    const uint64_t t_stage = t_desc + (uint64_t)(stage * (t_size >> 4));
                     // (Always four K steps: behind K the loads give zeros.  Testing
                     // for the last steps made the issuing, not the tensor pipe,
                     // the bound: 8192 x 4096 x 4096 in 176 us instead of 159.)
@@ -808,7 +851,8 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
                         } else {
                             const uint64_t sd = s_desc + (uint64_t)(stage * (C::STAGE_SCALES >> 4));
                             issue_f4<MATH, C>(d_tmem, w_stage, t_stage, sd, idesc,
-                                           tmem_base + C::SCALE_COL + (kb & 1) * 64, t_shift, accum);
+                                           tmem_base + C::SCALE_COL + (kb & 1) * C::SCALE_COLS, t_shift,
+                                              accum);
                         }
                         tc_commit_pair(empty0 + 8 * stage);
                     }
@@ -862,41 +906,99 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
                         dy[j] = (uint32_t)src[(long long)j * p.N] << 16;
                 }
             };
-            if (h < chunks) load_dy(h);
+            // This group's chunks, of HALVES groups': h, h + HALVES, ..  With OVERLAP
+            // the first accumulator's from the last on, so that the columns that
+            // it shares with the second come first, and `keep` is the number of
+            // the group's chunks that have none: at that many left, the next tile
+            // may be accumulated.
+            const int mine = work ? (chunks - h + HALVES - 1) / HALVES : 0;
+            const bool down = C::OVERLAP && acc == 0;
+            auto chunk_at = [&](int i) { return h + HALVES * (down ? mine - 1 - i : i); };
+            int keep = 0;
+            if (C::OVERLAP) {
+                constexpr int SHARED = (C::TOKENS - C::ACC_STRIDE) / 32, OWN = C::ACC_STRIDE / 32;
+                keep = down ? min(mine, (OWN - h + HALVES - 1) / HALVES)
+                            : max(0, mine - (SHARED - h + HALVES - 1) / HALVES);
+            }
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_remote_tmem(mapa_shared(smem_u32(&acc_empty[C::OVERLAP ? 0 : acc]), 0));
+            };
+            if (mine > 0) load_dy(chunk_at(0));
             if (p.k_blocks > 0) {
                 const bool ok = wait_bounded(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, p.err);
                 // the whole group leaves, or none of it
                 if (!named_bar_and(ch.bar, GROUP_THREADS, ok)) break;
                 tc_fence_after();
+                if (keep == mine) release();
             }
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * C::ACC_STRIDE;
-#pragma unroll 1
-            for (int c = h; c < chunks && work; c += HALVES) {
-                ch.row = t.row0 + c * 32;
-                ch.rows = min(32, t.rows - c * 32);
+            const bool direct = EPI == GRP_STORE &&
+                                (p.out_kind == OUT_F32 || p.beta != 0.0f || p.k_blocks == 0);
+            auto load = [&](int i, uint32_t(&r)[32]) {
                 if (EPI == GRP_STORE) {
-                    if (p.out_kind != OUT_F32 && p.beta == 0.0f && p.k_blocks > 0)
-                        emit_store_16(p, &maps.c, t_row + c * 32, ch);
-                    else
-                        emit_store_direct(p, t_row + c * 32, split * p.split_stride, ch.row, ch.rows, n0,
-                                          lane);
-                    continue;
-                }
-                uint32_t r[32];
-                if (p.k_blocks > 0) {
-                    tmem_ld_32cols(t_row + c * 32, r);
-                    tmem_ld_wait(r);
+                    tmem_ld_fragments(t_row + chunk_at(i) * 32, r);
+                } else if (p.k_blocks > 0) {
+                    tmem_ld_32cols(t_row + chunk_at(i) * 32, r);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = 0;
                 }
-                emit_swiglu<EPI>(p, maps, r, dy, ch);
-                if (c + HALVES < chunks) load_dy(c + HALVES);
+            };
+            auto emit = [&](int i, const uint32_t(&r)[32]) {
+                const int c = chunk_at(i);
+                ch.row = t.row0 + c * 32;
+                ch.rows = min(32, t.rows - c * 32);
+                if (EPI == GRP_STORE) {
+                    if (p.out_kind == OUT_F16)
+                        emit_store_16<OUT_F16>(p, &maps.c, r, ch);
+                    else
+                        emit_store_16<OUT_BF16>(p, &maps.c, r, ch);
+                } else {
+                    emit_swiglu<EPI>(p, maps, r, dy, ch);
+                    if (i + 1 < mine) load_dy(chunk_at(i + 1));
+                }
+            };
+            int i = 0;
+            if (C::TWO_SHARED && !direct && mine - keep == 2) {
+                // both are read before the first is written out: the next
+                // tile's MMAs wait for them (8192 x 14336 x 4096 151 -> 143 us)
+                uint32_t r[32], second[32];
+                load(0, r);
+                load(1, second);
+                tmem_ld_wait(r);
+                tmem_ld_wait(second);
+                release();
+                emit(0, r);
+                emit(1, second);
+                i = 2;
             }
-            if (p.k_blocks > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote_tmem(mapa_shared(smem_u32(&acc_empty[acc]), 0));
+#pragma unroll 1
+            for (; i < mine; ++i) {
+                const bool last = p.k_blocks > 0 && mine - i == keep + 1;
+                if (direct) {
+                    const int c = chunk_at(i);
+                    auto store = [&](auto kind) {
+                        emit_store_direct<decltype(kind)::value>(
+                            p, t_row + c * 32, split * p.split_stride, t.row0 + c * 32,
+                            min(32, t.rows - c * 32), n0, lane);
+                    };
+                    if (p.out_kind == OUT_F32)
+                        store(Kind<OUT_F32>());
+                    else if (p.out_kind == OUT_F16)
+                        store(Kind<OUT_F16>());
+                    else
+                        store(Kind<OUT_BF16>());
+                    if (last) release();
+                    continue;
+                }
+                uint32_t r[32];
+                load(i, r);
+                tmem_ld_wait(r);
+                if (last) release();
+                emit(i, r);
             }
         }
         if (q == 0 && lane == 0) bulk_wait_read_all();      // before this CTA's shared memory goes

@@ -449,3 +449,19 @@ def test_bad_offsets_run_the_clamped_groups(M, G):
     assert swg.get_device_error() == 1
     want, tol = plain.product(plain.f64(A), plain.f64(B), clamped, 0, 1.0, 0.0, np.zeros((M, 40)), "bf16")
     check(C.cpu("clamped groups"), want, tol, f"clamped groups {M} {G}")
+
+
+# Several tiles for every pair of CTAs, of all widths.
+MANY_TILES = [0, 300, 256, 161, 1000, 193, 0, 33, 900, 160]
+
+
+@pytest.mark.parametrize("types,beta", [(("bf16", "bf16"), 0.0), (("f16", "f32"), 0.5)])
+@pytest.mark.parametrize("N,K", [(5000, 40), (4600, 328)])
+def test_many_tiles(types, beta, N, K):
+    run_gemm(MANY_TILES, N, K, types, 1, 1.0, beta, seed=K)
+
+
+@pytest.mark.parametrize("N,K", [(2504, 40), (2312, 328)])
+def test_swiglu_many_tiles(N, K):
+    test_swiglu_grouped(MANY_TILES, N, K)
+    test_swiglu_grouped_grad(MANY_TILES, N, K, True)

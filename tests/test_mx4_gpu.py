@@ -250,3 +250,26 @@ def test_products_repeat_bit_for_bit_and_in_graphs(fmt):
         torch.cuda.synchronize()
         assert torch.equal(C, first)
     assert swg.get_device_error() == 0
+
+
+# Several tiles for every pair of CTAs, of all widths and in both accumulators.
+MANY_TILES = [0, 300, 256, 161, 1000, 193, 0, 33, 900, 160]
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("out,beta", [("bf16", 0.0), ("f32", 0.5)])
+@pytest.mark.parametrize("N,K", [(5000, 40), (4600, 584)])
+def test_many_tiles(fmt, out, beta, N, K):
+    run_product(MANY_TILES, N, K, fmt, out, 1.0, beta, seed=K)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("N,K", [(2504, 40), (2312, 584)])
+def test_swiglu_many_tiles(fmt, N, K):
+    test_swiglu(fmt, MANY_TILES, False, N, K)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("M,N,K", [(2500, 2600, 72), (1500, 4104, 520), (770, 7700, 264)])
+def test_dense_many_tiles(fmt, M, N, K):
+    run_product([M], N, K, fmt, dense=True, seed=M)
