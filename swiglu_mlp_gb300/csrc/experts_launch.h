@@ -70,14 +70,6 @@ struct WgradArgs {
 cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, bool &mapped);
 
 #ifdef __CUDACC__
-// The value of an E2M1 code (sign in bit 3).
-__device__ __forceinline__ float e2m1_value(uint32_t c)
-{
-    const uint32_t e = (c >> 1) & 3, m = c & 1;
-    const float v = e ? __int_as_float(((126 + e) << 23) | (m << 22)) : 0.5f * m;
-    return (c & 8) ? -v : v;
-}
-
 // The value of a scale byte: E8M0 (0xFF is NaN), or E4M3.
 __device__ __forceinline__ float mx4_scale_value(bool nv, uint32_t c)
 {

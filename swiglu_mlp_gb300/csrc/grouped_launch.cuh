@@ -41,7 +41,7 @@ cudaError_t launch_pairs(int smem, int smem_most, long long units, int sms, cuda
         if (e != cudaSuccess) return e;
         cfg.numAttrs = 1;
         cfg.dynamicSmemBytes = smem_most;
-        cfg.gridDim = dim3(4 * (sms / 2));           // (up to two CTAs per SM)
+        cfg.gridDim = dim3(2 * (sms / 2));           // a CTA per SM
         e = cudaOccupancyMaxActiveClusters(&pairs, KERNEL, &cfg);
         if (e != cudaSuccess) return e;
         if (pairs < 1) return cudaErrorInvalidConfiguration;

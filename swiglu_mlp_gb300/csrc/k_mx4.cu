@@ -7,6 +7,12 @@
 // r + 96 of a row of scale tiles, whose scales lie side by side in memory; a
 // warp has 512 columns.  Lanes swap their blocks' scale bytes so that each
 // stores 4 bytes of a tile.
+//
+// Measured, to 4 bits from bf16: 57344 x 4096 in 96 us (MXFP4) and 100 us
+// (NVFP4), 6.2 and 6.0 TB/s of traffic; 8192 x 4096 in 13.7 and 15.3 us; 1024 x
+// 4096 in 4.0 and 4.5 us; 1 x 4096 in 2.2 us, a launch.  Back to bf16: 14336 x
+// 4096 in 24 us, 6.2 TB/s, most of it written (a plain fill of the result takes
+// 30).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>

@@ -12,6 +12,13 @@
 // Tiles are 256 (k) x 256 (n) per CTA pair with two accumulators, as in
 // grouped.cuh.  A group without rows runs no main loop: its tiles store
 // beta * C_g, or zeros.
+//
+// What bounds it: for long groups the tensor pipe at the clock that the power
+// limit leaves (16 groups of about 1024 rows, 1792 x 4096, bf16: 147 us, 1640
+// TFLOP/s; 75% of the pipe's cycles); for short ones writing C (64 groups of 16
+// rows, 2048 x 1024: 63 us for 268 MB, 4.3 TB/s; 64 of 3, 1024 x 1024: 36 us, 3.8;
+// a plain fill reaches 4.1), and 4 us that any call takes (48 groups of about 4
+// rows, 896 x 521 with rows 1072 bytes apart: 19 to 24 us for 45 MB).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
