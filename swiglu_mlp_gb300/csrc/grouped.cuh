@@ -28,13 +28,13 @@
 //     1800 TFLOP/s; gradient of half as many rows, 8 groups: 150 us, 1600.
 //   many rows, 4 bits: MMAs and the copies of their scales, one behind the other
 //     in the tensor pipe, which is 71% busy.  8192 x 14336 x 4096: NVFP4 143 us,
-//     6.7 PFLOP/s; MXFP4 139 us, 6.9.
+//     6.7 PFLOP/s; MXFP4 135 us, 7.1.
 //   few rows: the weights' way from memory and about 3.3 us that any call takes
 //     (set-up, offsets, first load, last store).  8 groups of one row, 4096 x
 //     9728 in 16 bits: 94 us, 6.8 TB/s; 16 rows, 229376 x 4096 in MXFP4: 78 us,
 //     6.4 TB/s; 2 rows of 8 groups, 896 x 9728: 8.3 us, 4.2 TB/s.
 //   between: the latency of loads that miss L2, 1.3 to 2.3 us for a ring of 5 or
-//     6 stages.  32 groups of 128 rows, 2048 x 2432 in MXFP4: 25 us, 3.4 TB/s.
+//     6 stages.  32 groups of 128 rows, 2048 x 2432 in MXFP4: 24 us, 3.5 TB/s.
 #pragma once
 
 #include "experts_launch.h"
@@ -119,6 +119,7 @@ enum GrpMath { MATH_16 = 0, MATH_MX = 1, MATH_NV = 2 };
 
 // A's maps: boxes of 128, 96, 64, 32 and 16 rows.
 constexpr int TOKEN_BOXES = 5;
+constexpr int SMEM_MOST = 232448;        // bytes of shared memory that a CTA can have
 __host__ __device__ constexpr int token_box(int i) { return i == 0 ? 128 : i == 1 ? 96 : 128 >> (i - 1); }
 
 struct GrpMaps {
@@ -148,6 +149,8 @@ struct GrpParams {
     // unit of its own and goes to C + s * split_stride (FP32 partials).
     int splits, split_blocks;
     long long split_stride;
+    int stages, stages_narrow;           // of the ring, see GrpCfg (4-bit)
+    int ring_bytes;
     int *err;
 };
 
@@ -176,19 +179,28 @@ struct GrpCfg {
     static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + STAGE_SCALES;
     static constexpr int OUT_BYTES = F4 ? 2048 : 3072;   // per epilogue warp, see the epilogue
     static constexpr int BAR_BYTES = 512;
-    static constexpr int FIXED = 1024 + EPI_WARPS * OUT_BYTES + BAR_BYTES;
-    static constexpr int table_bytes(int G) { return (F4 ? 3 : 2) * 4 * (G + 1) + G; }
-    static constexpr int LIMIT = 232448 - FIXED - table_bytes(MAX_GROUPS);
-    static constexpr int STAGES_RAW = LIMIT / STAGE_BYTES;
-    static constexpr int STAGES = STAGES_RAW > 6 && !FEW ? 6 : STAGES_RAW;
-    // A launch whose tiles have at most 192 rows lays out stages of that many
-    // (MXFP4: 6 instead of 5; 4096 x 4096 x 14336 70 us against 74).
+    static constexpr int FIXED = EPI_WARPS * OUT_BYTES + BAR_BYTES;
+    __host__ __device__ static constexpr int table_bytes(int G) { return (F4 ? 3 : 2) * 4 * (G + 1) + G; }
+    // The ring has as many stages as the table of G groups leaves room for, at
+    // most 6 unless weights are streamed; a launch whose tiles have at most 192
+    // rows lays out stages of that many.  (For 32 groups 6 instead of 5: MXFP4
+    // 8192 x 14336 x 4096 133 us against 138, with 192 rows 4096 x 4096 x 14336
+    // 70 against 74, in NVFP4 73 against 77.)
     static constexpr int T_NARROW = F4 && !FEW ? 192 / 2 * 128 : T_BYTES;
     static constexpr int NARROW_BYTES = W_BYTES + T_NARROW + STAGE_SCALES;
-    static constexpr int STAGES_NARROW = F4 && !FEW ? LIMIT / NARROW_BYTES : STAGES;
-    static constexpr int RING_BYTES = STAGES * STAGE_BYTES > STAGES_NARROW * NARROW_BYTES
-                                          ? STAGES * STAGE_BYTES : STAGES_NARROW * NARROW_BYTES;
-    static constexpr int smem_bytes(int G) { return RING_BYTES + FIXED + table_bytes(G); }
+    static constexpr int RING = FEW ? 12 : 6;        // barriers for that many
+    __host__ __device__ static constexpr int stages_of(int bytes, int G)
+    {
+        const int n = (SMEM_MOST - FIXED - table_bytes(G)) / bytes;
+        return n < RING ? n : RING;
+    }
+    __host__ __device__ static constexpr int ring_bytes(int G)
+    {
+        const int wide = stages_of(STAGE_BYTES, G) * STAGE_BYTES;
+        const int narrow = stages_of(NARROW_BYTES, G) * NARROW_BYTES;
+        return wide > narrow ? wide : narrow;
+    }
+    static constexpr int smem_bytes(int G) { return ring_bytes(G) + FIXED + table_bytes(G); }
     static constexpr int TMEM_COLS = !FEW ? 512 : F4 ? 256 : 128;
     // Two buffers of a stage's scales at the end of tensor memory.  What they
     // take of it the two accumulators share: the second begins ACC_STRIDE
@@ -203,7 +215,8 @@ struct GrpCfg {
     static constexpr bool OVERLAP = 2 * TOKENS > SCALE_COL;
     static constexpr int ACC_STRIDE = OVERLAP ? (SCALE_COL - TOKENS) / 32 * 32 : TOKENS;
     static constexpr bool TWO_SHARED = OVERLAP && TOKENS - ACC_STRIDE > 64;
-    static_assert(STAGES >= 3 && RING_BYTES % 1024 == 0, "ring");
+    static_assert(stages_of(STAGE_BYTES, MAX_GROUPS) >= 5, "pipeline too shallow");
+    static_assert(STAGE_BYTES % 1024 == 0 && NARROW_BYTES % 1024 == 0, "swizzled tiles");
     static_assert(ACC_STRIDE + TOKENS <= SCALE_COL && 2 * ACC_STRIDE >= TOKENS, "tensor memory");
 };
 
@@ -640,13 +653,14 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
 {
     using C = GrpCfg<MATH, FEW>;
     constexpr bool F4 = C::F4;
-    constexpr int RING = C::STAGES_NARROW;           // barriers
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    constexpr int RING = C::RING;
+    constexpr int RING_16 = C::ring_bytes(MAX_GROUPS);   // of 16-bit operands, for any G
+    constexpr int STAGES_16 = C::stages_of(C::STAGE_BYTES, MAX_GROUPS);
+    static_assert(F4 || C::ring_bytes(1) == RING_16);
+    extern __shared__ __align__(1024) uint8_t grouped_smem[];
     // stages (W, rows of A, scales), output staging, barriers, group table
-    uint8_t *sW = smem;
-    uint8_t *sOut = smem + C::RING_BYTES;
+    uint8_t *sW = grouped_smem;
+    uint8_t *sOut = grouped_smem + (F4 ? p.ring_bytes : RING_16);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sOut + C::EPI_WARPS * C::OUT_BYTES);
     uint64_t *full = bars;
     uint64_t *empty = bars + RING;
@@ -726,9 +740,9 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
             tile_sums<C::THREADS>(G, start, stile, scratch, [](int n) { return ceil_div(n, 128); });
     }
     // the ring
-    const bool more = C::STAGES_NARROW > C::STAGES && (narrow || most <= 192);
-    const int S = more ? C::STAGES_NARROW : C::STAGES;
-    const uint32_t t_size = more ? C::T_NARROW : C::T_BYTES;
+    const bool small = C::T_NARROW < C::T_BYTES && (narrow || most <= 192);
+    const int S = !F4 ? STAGES_16 : small ? p.stages_narrow : p.stages;
+    const uint32_t t_size = small ? C::T_NARROW : C::T_BYTES;
     uint8_t *sT = sW + S * C::W_BYTES;
     uint8_t *sS = sT + S * t_size;
     const int units = first[G] * p.n_blocks * p.splits;

@@ -57,12 +57,22 @@ cudaError_t launch_pairs(int smem, int smem_most, long long units, int sms, cuda
 }
 
 template <int MATH, int EPI, bool FEW>
-cudaError_t launch_grouped_kernel(const GrpMaps &m, const GrpParams &p, long long units, int sms,
+cudaError_t launch_grouped_kernel(const GrpMaps &m, GrpParams p, long long units, int sms,
                                   cudaStream_t s)
 {
     using C = GrpCfg<MATH, FEW>;
-    return launch_pairs<grouped_kernel<MATH, EPI, FEW>, C::THREADS>(
-        C::smem_bytes(p.groups.G), C::smem_bytes(MAX_GROUPS), units, sms, s, m, p);
+    const int G = p.groups.G;
+    p.stages = C::stages_of(C::STAGE_BYTES, G);
+    // Tiles of whole width that are done in a few stages are bound by their
+    // results; loads further ahead slow those (MXFP4, 8192 x 8192: K = 1024 49.4
+    // us with 6 stages, 47.4 with 5; K = 4096 the other way round, 133 and 138 us
+    // for 8192 x 14336; 32 groups of 128 rows, K = 2048: 23.7 and 24.5).
+    if (!FEW && p.k_blocks <= 8 && p.groups.M / std::max(G, 1) >= C::TOKENS)
+        p.stages = std::min(p.stages, 5);
+    p.stages_narrow = C::stages_of(C::NARROW_BYTES, G);
+    p.ring_bytes = C::ring_bytes(G);
+    return launch_pairs<grouped_kernel<MATH, EPI, FEW>, C::THREADS>(C::smem_bytes(G), SMEM_MOST, units,
+                                                                    sms, s, m, p);
 }
 
 }  // namespace swg

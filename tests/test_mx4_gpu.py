@@ -273,3 +273,14 @@ def test_swiglu_many_tiles(fmt, N, K):
 @pytest.mark.parametrize("M,N,K", [(2500, 2600, 72), (1500, 4104, 520), (770, 7700, 264)])
 def test_dense_many_tiles(fmt, M, N, K):
     run_product([M], N, K, fmt, dense=True, seed=M)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("G", [36, 37, 38, 39, 40, 128, 505, 512, 1024])
+@pytest.mark.parametrize("M", [40, 700])
+def test_many_groups(fmt, G, M):
+    """What the table of groups takes of shared memory the ring does without."""
+    r = np.random.default_rng(G + M)
+    rows = np.bincount(r.integers(0, G, M), minlength=G)
+    rows[G // 3] += M
+    run_product([int(n) for n in rows], 40, 600, fmt, seed=G)
