@@ -220,70 +220,6 @@ struct GrpCfg {
     static_assert(ACC_STRIDE + TOKENS <= SCALE_COL && 2 * ACC_STRIDE >= TOKENS, "tensor memory");
 };
 
-// Rows of A covered by each tile of a group of `rows` (> 0) rows, but the
-// last, when tiles have at most `most` rows.
-template <class C>
-__device__ __forceinline__ int tile_step(int rows, int most)
-{
-    const int t = ceil_div(rows, most);
-    constexpr int UNIT = C::UNIT;
-    return ceil_div(ceil_div(rows, t), UNIT) * UNIT;
-}
-
-// The most rows of A that a tile should have, chosen so that the last wave of
-// tiles is not nearly empty: of TOKENS, TOKENS - unit, .. the one with the least
-//   waves * (stages * max(rows per tile, 176) + 700),
-// a tile's measured time in units of 1.145 ns: a 16-bit stage takes 292 ns at
-// 256 rows, 228 at 192, 212 at 160 and not less than 195 below (the loading
-// and issuing), and a tile about 0.8 us besides.  994 tiles on 76 pairs are
-// 13.1 waves at 256 rows; 1064 tiles of at most 240 make 14.0 and are 7% faster.
-// In 4 bits, in cycles: a stage takes what its loads do (22 KB and 64 bytes a
-// row, at 64 bytes a cycle) or its MMAs (2.8 a row in NVFP4, 2.55 in MXFP4), and
-// a tile not less than its epilogue (21 a row).  1536 x 4096 x 8192: 22.3 us at
-// the 192 rows that this gives, 26.7 at 256.
-// Warp w of the first eight computes candidate w's; ends with a barrier.
-template <class C>
-__device__ __forceinline__ int choose_rows(const int *start, int G, int n_blocks, int k_blocks,
-                                           int pairs, float *costs)
-{
-    constexpr int CANDS = C::CANDIDATES;
-    const int lane = threadIdx.x & 31, cand = threadIdx.x >> 5;
-    if (cand < CANDS) {
-        const int most = C::TOKENS - cand * C::UNIT;
-        int tiles = 0, rows = 0;
-        for (int g = lane; g < G; g += 32) {
-            const int r = start[g + 1] - start[g];
-            tiles += ceil_div(r, most);
-            rows += r;
-        }
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
-            rows += __shfl_xor_sync(0xffffffffu, rows, d);
-        }
-        const float units = (float)tiles * (float)n_blocks;
-        const float waves = ceilf(units / (float)pairs);
-        const float mean = (float)rows / fmaxf((float)tiles, 1.0f);
-        const float k = (float)k_blocks;
-        const float tile = C::F4 ? fmaxf(k * fmaxf(330.0f + mean, 2.7f * mean), 21.0f * mean) + 500.0f
-                                 : k * fmaxf(mean, 176.0f) + 700.0f;
-        if (lane == 0) costs[cand] = waves * tile;
-    }
-    __syncthreads();
-    int best = 0;
-#pragma unroll
-    for (int c = 1; c < CANDS; ++c)
-        if (costs[c] < costs[best]) best = c;
-    return C::TOKENS - best * C::UNIT;
-}
-
-struct GrpTile {
-    int g, nb;         // group, block of 256 weight rows
-    int row0, rows;    // rows of A
-    int local;         // row0 within the group
-    int width;         // rows rounded up to 16: the MMA's N
-};
-
 // a / b for a >= 0, b > 0.  Below 2^21 through the fast FP32 division: a + 1/2
 // keeps the quotient 1/(2b) away from the next integer, more than its error of
 // two units in the last place.  (Integer division is a chain of tens of
@@ -294,6 +230,85 @@ __device__ __forceinline__ int fast_div(int a, int b)
     if (a < (1 << 21)) return (int)__fdividef((float)a + 0.5f, (float)b);
     return a / b;
 }
+
+// Tiles of a group of `rows` rows, when they have at most `most`.
+template <class C>
+__device__ __forceinline__ int tiles_of(int rows, int most)
+{
+    return C::CANDIDATES == 1 ? ceil_div(rows, C::TOKENS) : fast_div(rows + most - 1, most);
+}
+
+// Rows of A covered by each tile of a group of `rows` (> 0) rows, but the
+// last, when tiles have at most `most` rows.
+template <class C>
+__device__ __forceinline__ int tile_step(int rows, int most)
+{
+    const int t = tiles_of<C>(rows, most);
+    constexpr int UNIT = C::UNIT;
+    return ceil_div(fast_div(rows + t - 1, t), UNIT) * UNIT;
+}
+
+// The most rows of A that a tile should have, chosen so that the last wave of
+// tiles is not nearly empty: of TOKENS, TOKENS - unit, .. the one with the least
+//   waves * (stages * max(rows of a tile, 176) + 700),
+// a tile's measured time in units of 1.145 ns: a 16-bit stage takes 292 ns at
+// 256 rows, 228 at 192, 212 at 160 and not less than 195 below (the loading
+// and issuing), and a tile about 0.8 us besides.  994 tiles on 76 pairs are
+// 13.1 waves at 256 rows; 1064 tiles of at most 240 make 14.0 and are 7% faster.
+// In 4 bits, in cycles: a stage takes what its loads do (22 KB and 64 bytes a
+// row, at 64 bytes a cycle) or its MMAs (2.8 a row in NVFP4, 2.55 in MXFP4), and
+// a tile not less than its epilogue (21 a row).  1536 x 4096 x 8192: 22.3 us at
+// the 192 rows that this gives, 26.7 at 256.
+// A tile's rows are their mean over many waves; in few, the widest tiles hold
+// the others up.  Among equals the narrowest.  (3000 rows in 16 groups, 2048 x
+// 2048: 34.8 us; by the mean alone, and the widest of equals, 39.9.  5003 in 12,
+// 2051 x 1003: 31.4 us against 33.7.)  The three 4-bit widths are told apart by
+// the mean as well.
+// Warp w of the first eight computes candidate w's; ends with a barrier.
+template <class C>
+__device__ __forceinline__ int choose_rows(const int *start, int G, int n_blocks, int k_blocks,
+                                           int pairs, float *costs)
+{
+    constexpr int CANDS = C::CANDIDATES;
+    const int lane = threadIdx.x & 31, cand = threadIdx.x >> 5;
+    if (cand < CANDS) {
+        const int most = C::TOKENS - cand * C::UNIT;
+        int tiles = 0, rows = 0, widest = 0;
+        for (int g = lane; g < G; g += 32) {
+            const int r = start[g + 1] - start[g];
+            tiles += tiles_of<C>(r, most);
+            rows += r;
+            if (!C::F4 && r > 0) widest = max(widest, tile_step<C>(r, most));
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+            rows += __shfl_xor_sync(0xffffffffu, rows, d);
+            if (!C::F4) widest = max(widest, __shfl_xor_sync(0xffffffffu, widest, d));
+        }
+        const float units = (float)tiles * (float)n_blocks;
+        const float waves = ceilf(units / (float)pairs);
+        const float mean = (float)rows / fmaxf((float)tiles, 1.0f);
+        const float r = C::F4 ? mean : mean + ((float)widest - mean) / fmaxf(waves, 1.0f);
+        const float k = (float)k_blocks;
+        const float tile = C::F4 ? fmaxf(k * fmaxf(330.0f + r, 2.7f * r), 21.0f * r) + 500.0f
+                                 : k * fmaxf(r, 176.0f) + 700.0f;
+        if (lane == 0) costs[cand] = waves * tile;
+    }
+    __syncthreads();
+    int best = 0;
+#pragma unroll
+    for (int c = 1; c < CANDS; ++c)
+        if (C::F4 ? costs[c] < costs[best] : costs[c] <= costs[best]) best = c;
+    return C::TOKENS - best * C::UNIT;
+}
+
+struct GrpTile {
+    int g, nb;         // group, block of 256 weight rows
+    int row0, rows;    // rows of A
+    int local;         // row0 within the group
+    int width;         // rows rounded up to 16: the MMA's N
+};
 
 // Tile u: groups in order; within a group bands of 8 tiles of A walk the
 // weight blocks together, so that concurrently running pairs share both in L2.
@@ -735,7 +750,7 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
         for (int g = threadIdx.x; g < G; g += C::THREADS)
             steps[g] = (uint8_t)(tile_step<C>(max(1, start[g + 1] - start[g]), most) / 16);
         tile_sums<C::THREADS>(G, start, first, scratch,
-                              [most](int n) { return ceil_div(n, most); });
+                              [most](int n) { return tiles_of<C>(n, most); });
         if (F4)
             tile_sums<C::THREADS>(G, start, stile, scratch, [](int n) { return ceil_div(n, 128); });
     }
