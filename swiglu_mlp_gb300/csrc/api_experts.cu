@@ -423,8 +423,7 @@ static int mx4_convert(int format, int64_t G, int64_t M, int64_t K, const void *
     p.S = static_cast<uint8_t *>(const_cast<void *>(S));
     swg::DeviceInfo d;
     if (int rc = swg::device_info(d)) return rc;
-    return swg::count_launch(swg::launch_mx4(p, back, (int)(M / 128 + G), d.err,
-                                             static_cast<cudaStream_t>(stream)));
+    return swg::count_launch(swg::launch_mx4(p, back, d.err, static_cast<cudaStream_t>(stream)));
 }
 
 int mx4_quantize(int format, int64_t G, int64_t M, int64_t K, const void *X, int64_t ldx,

@@ -21,8 +21,7 @@ struct Mx4Args {
     long long ldq;             // bytes
     uint8_t *S;
 };
-// tile_rows: an upper bound of the rows of scale tiles over all groups.
-cudaError_t launch_mx4(const Mx4Args &p, bool back, int tile_rows, int *err, cudaStream_t s);
+cudaError_t launch_mx4(const Mx4Args &p, bool back, int *err, cudaStream_t s);
 
 struct GrpMaps;
 struct GrpParams;

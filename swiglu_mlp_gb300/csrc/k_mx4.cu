@@ -12,7 +12,9 @@
 // (NVFP4), 6.2 and 6.0 TB/s of traffic; 8192 x 4096 in 13.7 and 15.3 us; 1024 x
 // 4096 in 4.0 and 4.5 us; 1 x 4096 in 2.2 us, a launch.  Back to bf16: 14336 x
 // 4096 in 24 us, 6.2 TB/s, most of it written (a plain fill of the result takes
-// 30).
+// 30).  256 groups of 8 rows, K = 2048: 7 us each way.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -187,80 +189,122 @@ __device__ __forceinline__ uint32_t block_scale(float top, float &scale, float &
 
 struct Place {
     int t;                   // row of scale tiles
-    int chunk;               // of the CTA's columns
-    int r32;                 // this warp's rows: r32, r32 + 32, ..
+    int chunk;               // of columns
+    int r;                   // this warp's first row in them; the others are 32 apart, or next to it
     int row0, end;           // first row of the tiles, end of their group
 };
 
-// This CTA's and warp's place; false for a CTA beyond the last group's tiles.
-__device__ __forceinline__ bool find_place(const Groups &gr, int chunks, int *err, Place &p)
+// The unit'th row of scale tiles (PER = 128) or four rows of one (PER = 4); false
+// beyond the last group's.  Every warp walks the groups itself, 32 at a time or,
+// where there may be hundreds, 128, whose offsets it loads together: a table
+// for the CTA would cost it two barriers, and it has little to do.  (Offsets are
+// clamped as in group_starts.)
+template <int PER>
+__device__ __forceinline__ bool find_rows(const Groups &gr, int unit, int *err, Place &p)
 {
-    const unsigned strip = blockIdx.x / (unsigned)chunks;
-    p.chunk = (int)(blockIdx.x - strip * (unsigned)chunks);
-    p.t = (int)(strip / STRIPS);
-    p.r32 = (int)(strip % STRIPS) * 8 + (threadIdx.x >> 5);
-    if (gr.offsets == nullptr) {
-        p.row0 = p.t * TILE_ROWS;
-        p.end = gr.M;
-        return p.row0 < gr.M;
-    }
-    // Every warp walks the groups itself, 32 at a time: a table for the CTA
-    // would cost it two barriers, and it has little to do.  (Offsets are
-    // clamped as in group_starts.)
     const int lane = threadIdx.x & 31;
-    int top = 0, before = 0;                         // largest offset, tiles so far
+    auto found = [&](int lo, int hi, int tiles, int i) {             // unit i of rows lo .. hi - 1
+        const int tile = i * PER / TILE_ROWS;
+        p.t = tiles + tile;
+        p.r = i * PER % TILE_ROWS;
+        p.row0 = lo + tile * TILE_ROWS;
+        p.end = hi;
+    };
+    if (gr.offsets == nullptr) {
+        found(0, gr.M, 0, unit);
+        return p.row0 + p.r < gr.M;
+    }
+    constexpr int BATCH = PER == TILE_ROWS ? 1 : 4;
+    int top = 0, before = 0, tiles = 0;              // largest offset, units and tiles so far
     bool bad = false;
-    for (int base = 0; base < gr.G; base += 32) {
-        const int g = base + lane;
-        auto offset = [&](int i) {
-            const int raw = gr.offsets[min(i, gr.G)];
-            const int v = raw < 0 ? 0 : raw > gr.M ? gr.M : raw;
-            bad = bad || v != raw;
-            return v;
-        };
-        int lo = max(offset(g), top), hi = offset(g + 1);
-        bad = bad || hi < lo;
-        hi = max(hi, lo);
-        if (__any_sync(0xffffffffu, bad)) {          // running maxima, the slow way
+    for (int base = 0; base < gr.G; base += 32 * BATCH) {
+        int v[BATCH + 1];                            // the last: what follows them
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, hi, d);
-                if (lane >= d) hi = max(hi, o);
+        for (int r = 0; r <= BATCH; ++r) {
+            const int raw = gr.offsets[min(base + 32 * r + (r < BATCH ? lane : 0), gr.G)];
+            v[r] = raw < 0 ? 0 : raw > gr.M ? gr.M : raw;
+            bad = bad || v[r] != raw;
+        }
+#pragma unroll
+        for (int r = 0; r < BATCH; ++r) {
+            if (base + 32 * r >= gr.G) break;
+            const int next = __shfl_down_sync(0xffffffffu, v[r], 1);
+            const int wrap = __shfl_sync(0xffffffffu, v[r + 1], 0);
+            int lo = max(v[r], top), hi = lane < 31 ? next : wrap;
+            bad = bad || hi < lo;
+            hi = max(hi, lo);
+            if (__any_sync(0xffffffffu, bad)) {      // running maxima, the slow way
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, hi, d);
+                    if (lane >= d) hi = max(hi, o);
+                }
+                const int o = __shfl_up_sync(0xffffffffu, hi, 1);
+                if (lane > 0) lo = max(lo, o);
+                if (lane == 0) atomicCAS(err, 0, ERR_INVALID);
             }
-            const int o = __shfl_up_sync(0xffffffffu, hi, 1);
-            if (lane > 0) lo = max(lo, o);
-            if (lane == 0) atomicCAS(err, 0, ERR_INVALID);
-        }
-        const int n = g < gr.G ? ceil_div(hi - lo, TILE_ROWS) : 0;
-        int sum = n;
+            const int here = base + 32 * r + lane < gr.G ? hi - lo : 0;
+            const int n = ceil_div(here, PER), own = ceil_div(here, TILE_ROWS);
+            const int all = __reduce_add_sync(0xffffffffu, n);
+            if (unit < before + all) {
+                int sum = n, own_sum = own;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += o;
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, sum, d);
+                    if (lane >= d) sum += o;
+                    if (PER < TILE_ROWS) {
+                        const int q = __shfl_up_sync(0xffffffffu, own_sum, d);
+                        if (lane >= d) own_sum += q;
+                    }
+                }
+                if (PER == TILE_ROWS) own_sum = sum;
+                const int first = before + sum - n;
+                const int src = __ffs(__ballot_sync(0xffffffffu, unit >= first && unit < first + n)) - 1;
+                found(__shfl_sync(0xffffffffu, lo, src), __shfl_sync(0xffffffffu, hi, src),
+                      tiles + __shfl_sync(0xffffffffu, own_sum - own, src),
+                      unit - __shfl_sync(0xffffffffu, first, src));
+                return true;
+            }
+            before += all;
+            tiles += PER == TILE_ROWS ? all : __reduce_add_sync(0xffffffffu, own);
+            top = __shfl_sync(0xffffffffu, hi, 31);
         }
-        const int first = before + sum - n;
-        const unsigned mine = __ballot_sync(0xffffffffu, p.t >= first && p.t < first + n);
-        if (mine) {
-            const int src = __ffs(mine) - 1;
-            p.row0 = __shfl_sync(0xffffffffu, lo + (p.t - first) * TILE_ROWS, src);
-            p.end = __shfl_sync(0xffffffffu, hi, src);
-            return true;
-        }
-        before += __shfl_sync(0xffffffffu, sum, 31);
-        top = __shfl_sync(0xffffffffu, hi, 31);
     }
     return false;
 }
 
-template <int TYPE, bool NV>
+// This warp's place; false beyond the last group's rows.  FEW = false: a CTA has
+// eight neighbouring rows of each 32, of one chunk, whose scales lie side by
+// side.  FEW: a warp has four neighbouring rows of a group, and the last of a
+// tile's writes the scales, zeros, of the rows that do not exist.  In the other
+// form a group of few rows has the warps of a whole tile, nearly all of which
+// do only that.
+template <bool FEW>
+__device__ __forceinline__ bool find_place(const Groups &gr, int chunks, int *err, Place &p)
+{
+    const unsigned warp = threadIdx.x >> 5;
+    if (FEW) {
+        const unsigned unit = blockIdx.x * (THREADS / 32) + warp, rows = unit / (unsigned)chunks;
+        p.chunk = (int)(unit - rows * (unsigned)chunks);
+        return find_rows<ROWS>(gr, (int)rows, err, p);
+    }
+    const unsigned strip = blockIdx.x / (unsigned)chunks;
+    p.chunk = (int)(blockIdx.x - strip * (unsigned)chunks);
+    const bool is = find_rows<TILE_ROWS>(gr, (int)(strip / STRIPS), err, p);
+    p.r = (int)(strip % STRIPS * 8 + warp);
+    return is;
+}
+
+template <int TYPE, bool NV, bool FEW>
 __global__ void __launch_bounds__(THREADS) quantize_kernel(const Mx4Args p, int chunks, int *err)
 {
     constexpr int LANES = NV ? 1 : 2;                // lanes per block
-    constexpr int TILES = NV ? 8 : 4;                // scale tiles per CTA along K
+    constexpr int TILES = NV ? 8 : 4;                // scale tiles per chunk along K
+    constexpr int APART = FEW ? 1 : 32;              // a warp's four rows
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Place at;
-    if (!find_place(p.groups, chunks, err, at)) return;
+    if (!find_place<FEW>(p.groups, chunks, err, at)) return;
     const int lane = threadIdx.x & 31;
     const int k = at.chunk * TILE_COLS + lane * LANE_COLS;
     const int cnt = min(LANE_COLS, max(0, p.K - k));
@@ -269,7 +313,7 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Mx4Args p, int 
     Raw8<TYPE> raw[ROWS][2];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const int row = at.row0 + at.r32 + 32 * i;
+        const int row = at.row0 + at.r + APART * i;
         const long long o = (long long)row * p.ldx + k;
         const int n = row < at.end ? cnt : 0;
         raw[i][0] = load8<TYPE>(p.X, o, min(n, 8));
@@ -278,7 +322,7 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Mx4Args p, int 
     uint32_t codes = 0;                              // the lane's block's scales, a byte per row
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const int row = at.row0 + at.r32 + 32 * i;
+        const int row = at.row0 + at.r + APART * i;
         // (the factor is positive: the largest of the products is its product)
         float top = p.scale * max_nan(top8<TYPE>(raw[i][0]), top8<TYPE>(raw[i][1]));
         if (!NV) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -322,24 +366,39 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Mx4Args p, int 
         word |= ((c >> (8 * b)) & 0xffu) << (8 * i);
     }
     const int tiles_k = ceil_div(p.K, NV ? 64 : 128);
-    const int kt = at.chunk * TILES + tile;
-    if (lane % LANES == 0 && kt < tiles_k)
-        *reinterpret_cast<uint32_t *>(p.S + ((long long)at.t * tiles_k + kt) * 512 + 16 * at.r32 +
-                                      4 * b) = word;
+    const int kt = at.chunk * TILES;
+    uint8_t *scales = p.S + ((long long)at.t * tiles_k + kt) * 512;
+    const int rows = at.end - at.row0, r = at.r + APART * b;
+    if (lane % LANES == 0 && kt + tile < tiles_k && (!FEW || r < rows))
+        *reinterpret_cast<uint32_t *>(scales + tile * 512 + 16 * (r % 32) + 4 * (r / 32)) = word;
+    if (FEW && at.r + ROWS >= min(rows, TILE_ROWS)) {
+        // The tile's last rows: those behind them do not exist, their scales are zero.
+        for (int t = 0; t < TILES && kt + t < tiles_k; ++t) {
+            uint32_t *of_lane = reinterpret_cast<uint32_t *>(scales + t * 512 + 16 * lane);
+            if (lane >= rows) {
+                *reinterpret_cast<uint4 *>(of_lane) = make_uint4(0, 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int i = 1; i < 4; ++i)
+                    if (lane + 32 * i >= rows) of_lane[i] = 0;
+            }
+        }
+    }
 }
 
 // Back: 8 columns per lane, so that a warp's stores of a row are whole lines
 // (with 16, as above, two stores share each 32-byte sector: 33 instead of 24 us
 // for 14336 x 4096 to bf16).
-template <int TYPE, bool NV>
+template <int TYPE, bool NV, bool FEW>
 __global__ void __launch_bounds__(THREADS) dequantize_kernel(const Mx4Args p, int chunks, int *err)
 {
     constexpr int LANES = NV ? 2 : 4;
     constexpr int TILES = NV ? 4 : 2;
+    constexpr int APART = FEW ? 1 : 32;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Place at;
-    if (!find_place(p.groups, chunks, err, at)) return;
+    if (!find_place<FEW>(p.groups, chunks, err, at)) return;
     const int lane = threadIdx.x & 31;
     const int k = at.chunk * TILE_COLS_BACK + lane * 8;
     const int cnt = min(8, max(0, p.K - k));
@@ -347,17 +406,24 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const Mx4Args p, in
     uint32_t q[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const int row = at.row0 + at.r32 + 32 * i;
+        const int row = at.row0 + at.r + APART * i;
         q[i] = row < at.end ? *reinterpret_cast<const uint32_t *>(p.Q + (long long)row * p.ldq + k / 2) : 0;
     }
     // 16 bytes: the four rows' scales of the tile's four blocks
     const int b = lane / LANES % 4, kt = at.chunk * TILES + lane / (4 * LANES);
-    const uint4 w = *reinterpret_cast<const uint4 *>(
-        p.S + ((long long)at.t * ceil_div(p.K, NV ? 64 : 128) + kt) * 512 + 16 * at.r32);
-    const uint32_t words[ROWS] = {w.x, w.y, w.z, w.w};
+    const uint8_t *scales = p.S + ((long long)at.t * ceil_div(p.K, NV ? 64 : 128) + kt) * 512;
+    uint32_t words[ROWS];
+    if (FEW) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            words[i] = *reinterpret_cast<const uint32_t *>(scales + 16 * ((at.r + i) % 32) + 4 * (at.r / 32));
+    } else {
+        const uint4 w = *reinterpret_cast<const uint4 *>(scales + 16 * at.r);
+        words[0] = w.x, words[1] = w.y, words[2] = w.z, words[3] = w.w;
+    }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const int row = at.row0 + at.r32 + 32 * i;
+        const int row = at.row0 + at.r + APART * i;
         if (row >= at.end) continue;
         const float s = mx4_scale_value(NV, (words[i] >> (8 * b)) & 0xffu);
         float v[8];
@@ -372,13 +438,15 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const Mx4Args p, in
     }
 }
 
-template <int TYPE, bool NV>
-cudaError_t launch(const Mx4Args &p, bool back, int tile_rows, int *err, cudaStream_t s)
+template <int TYPE, bool NV, bool FEW>
+cudaError_t launch(const Mx4Args &p, bool back, int *err, cudaStream_t s)
 {
-    const int cols = back ? TILE_COLS_BACK : TILE_COLS;
+    const int cols = back ? TILE_COLS_BACK : TILE_COLS, G = p.groups.G, M = p.groups.M;
     const int chunks = (p.K + cols - 1) / cols;
+    // upper bounds of the units over all groups
+    const long long units = FEW ? M / ROWS + std::min(G, M) : (M / TILE_ROWS + std::min(G, M)) * 32ll;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)tile_rows * STRIPS * chunks));
+    cfg.gridDim = dim3((unsigned)((units * chunks + THREADS / 32 - 1) / (THREADS / 32)));
     cfg.blockDim = dim3(THREADS);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -386,20 +454,31 @@ cudaError_t launch(const Mx4Args &p, bool back, int tile_rows, int *err, cudaStr
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return back ? cudaLaunchKernelEx(&cfg, dequantize_kernel<TYPE, NV>, p, chunks, err)
-                : cudaLaunchKernelEx(&cfg, quantize_kernel<TYPE, NV>, p, chunks, err);
+    return back ? cudaLaunchKernelEx(&cfg, dequantize_kernel<TYPE, NV, FEW>, p, chunks, err)
+                : cudaLaunchKernelEx(&cfg, quantize_kernel<TYPE, NV, FEW>, p, chunks, err);
+}
+
+template <int TYPE, bool NV>
+cudaError_t launch_form(const Mx4Args &p, bool back, int *err, cudaStream_t s)
+{
+    // FEW for groups of few rows on average, unless they are few themselves:
+    // 256 groups of one row, K = 8192, 6.8 us against 112; 32 of 64, 9.4 against
+    // 13.3; 32 of 96, 13.6 against 14.7 (K = 2048: 5.7 against 5.3); but 8 of 4,
+    // K = 512, 3.3 against 2.7, for its longer way to a warp's rows.
+    const int cols = back ? TILE_COLS_BACK : TILE_COLS, G = p.groups.G, M = p.groups.M;
+    const long long tiles = (long long)(M / TILE_ROWS + std::min(G, M)) * ((p.K + cols - 1) / cols);
+    const bool few = G > 1 && M / G <= 64 && tiles > 40;
+    return few ? launch<TYPE, NV, true>(p, back, err, s) : launch<TYPE, NV, false>(p, back, err, s);
 }
 
 }  // namespace
 
-cudaError_t launch_mx4(const Mx4Args &p, bool back, int tile_rows, int *err, cudaStream_t s)
+cudaError_t launch_mx4(const Mx4Args &p, bool back, int *err, cudaStream_t s)
 {
     const bool nv = p.format == 1;
-    if (p.type == 0)
-        return nv ? launch<0, true>(p, back, tile_rows, err, s) : launch<0, false>(p, back, tile_rows, err, s);
-    if (p.type == 1)
-        return nv ? launch<1, true>(p, back, tile_rows, err, s) : launch<1, false>(p, back, tile_rows, err, s);
-    return nv ? launch<2, true>(p, back, tile_rows, err, s) : launch<2, false>(p, back, tile_rows, err, s);
+    if (p.type == 0) return nv ? launch_form<0, true>(p, back, err, s) : launch_form<0, false>(p, back, err, s);
+    if (p.type == 1) return nv ? launch_form<1, true>(p, back, err, s) : launch_form<1, false>(p, back, err, s);
+    return nv ? launch_form<2, true>(p, back, err, s) : launch_form<2, false>(p, back, err, s);
 }
 
 }  // namespace swg

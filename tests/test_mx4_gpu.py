@@ -284,3 +284,40 @@ def test_many_groups(fmt, G, M):
     rows = np.bincount(r.integers(0, G, M), minlength=G)
     rows[G // 3] += M
     run_product([int(n) for n in rows], 40, 600, fmt, seed=G)
+
+
+# many groups of few rows, and among them some of several tiles
+SKEWED = {
+    "few": [0, 1, 5, 2, 0, 4, 31, 32, 33, 3, 0, 64, 1, 8, 0, 0, 7, 12],
+    "one large": [0] * 40 + [300] + [1, 0, 2] * 20 + [129],
+    "300 groups": [int(n) for n in np.random.default_rng(5).integers(0, 4, 300)],
+    "1024 groups": [int(n) for n in np.random.default_rng(6).integers(0, 3, 1023)] + [260],
+}
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("rows", SKEWED)
+def test_scale_tiles_of_few_rows(fmt, rows):
+    test_grouped_scale_tiles(fmt, SKEWED[rows])
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("G,M", [(5, 700), (60, 200), (300, 500)])
+def test_bad_offsets_of_a_conversion(fmt, G, M):
+    """The rows of the clamped groups are converted and no others, and the
+    error word says so."""
+    r = np.random.default_rng(G)
+    off = np.sort(r.integers(0, M + 1, G + 1))
+    off[[0, -1]] = 0, M
+    off[G // 2], off[1], off[2] = M + 5, max(int(off[1]), 1), -3
+    x = outliers(M, 200, synth.generator(M), torch.bfloat16)
+    clamped = np.maximum.accumulate(np.clip(off, 0, M))
+    rows = [int(n) for n in np.diff(clamped)]
+    q, s = swg.mx4_alloc(M, 200, FMT[fmt], groups=G)
+    swg.mx4_quantize_into(q, s, x.cuda(), FMT[fmt], offsets=torch.from_numpy(off.astype(np.int32)).cuda())
+    assert swg.get_device_error() == 1
+    x64 = plain.f64(x)
+    v = plain.quantised(x64, fmt)
+    want_q, want_s = plain.pack(np.copysign(v, x64), fmt, plain.block_scales(x64, fmt), rows)
+    assert np.array_equal(q.cpu().numpy(), want_q)
+    assert np.array_equal(s.cpu().numpy()[:want_s.size], want_s)
