@@ -64,10 +64,13 @@ bool known_format(int format) { return format == SWG_MXFP4 || format == SWG_NVFP
 // of CTAs is cut into: as many as there are pairs for, of at least 8 stages
 // each, when that saves a tile at least 14 stages.  (A stage takes 0.2 us, the
 // second kernel and the partials about 2: one row, 4096 x 4096, 17.1 us in one
-// range and 11.6 in four.)
+// range and 11.6 in four.)  More than 8, up to 16, only of at least 16 stages
+// (200 rows, 16384 x 256: 18.0 us in 16, 21.9 in 8; 16 rows, 8192 x 1024: 10.3
+// and 9.8; in 32 both are slower).
 int pick_splits(int64_t tiles, int k_blocks, int pairs)
 {
-    const int64_t s = std::min<int64_t>({8, pairs / std::max<int64_t>(tiles, 1), k_blocks / 8});
+    const int64_t most = std::max(8, std::min(16, k_blocks / 16));
+    const int64_t s = std::min<int64_t>({most, pairs / std::max<int64_t>(tiles, 1), k_blocks / 8});
     return s >= 2 && k_blocks - k_blocks / s >= 14 ? (int)s : 1;
 }
 

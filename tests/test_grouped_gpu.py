@@ -465,3 +465,12 @@ def test_many_tiles(types, beta, N, K):
 def test_swiglu_many_tiles(N, K):
     test_swiglu_grouped(MANY_TILES, N, K)
     test_swiglu_grouped_grad(MANY_TILES, N, K, True)
+
+
+@pytest.mark.parametrize("rows", [[1], [200]])
+def test_sixteen_ranges(rows):
+    run_gemm(rows, 136, 16384, ("bf16", "bf16"), 1)
+
+
+def test_wgrad_sixteen_ranges():
+    run_wgrad([20011], 72, 136, ("f16", "f32"))
