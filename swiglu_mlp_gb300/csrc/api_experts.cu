@@ -60,18 +60,30 @@ bool too_big(std::initializer_list<int64_t> v)
 int block_of(int format) { return format == SWG_NVFP4 ? 16 : 32; }
 bool known_format(int format) { return format == SWG_MXFP4 || format == SWG_NVFP4; }
 
-// How many K ranges a product of `tiles` tiles (an upper bound) on `pairs` pairs
-// of CTAs is cut into: as many as there are pairs for, of at least 8 stages
-// each, when that saves a tile at least 14 stages.  (A stage takes 0.2 us, the
-// second kernel and the partials about 2: one row, 4096 x 4096, 17.1 us in one
-// range and 11.6 in four.)  More than 8, up to 16, only of at least 16 stages
-// (200 rows, 16384 x 256: 18.0 us in 16, 21.9 in 8; 16 rows, 8192 x 1024: 10.3
-// and 9.8; in 32 both are slower).
-int pick_splits(int64_t tiles, int k_blocks, int pairs)
+// The most tiles of at most `rows` rows that M > 0 rows of G groups can have: a
+// row in every group, and the others in whole tiles of one.
+int64_t most_tiles(int64_t M, int64_t G, int64_t rows)
+{
+    const int64_t g = std::min(G, M);
+    return (M - g) / rows + g;
+}
+
+// How many K ranges a product of `results` results in `tiles` tiles (an upper
+// bound) on `pairs` pairs of CTAs is cut into: as many as there are pairs for, of
+// at least 8 stages each, when that saves a tile more than the second kernel
+// and the FP32 partials, written and read, cost: a stage takes 0.2 us, the kernel
+// and what goes with it 2.8, 8 bytes of partials a result and range the rest.
+// (One row, 4096 x 4096: 17.1 us in one range and 11.6 in four; 64 rows, 8192 x
+// 8192 in 4 bits: 11.0 in one and 12.3 in two.)  More than 8, up to 16, only of at
+// least 16 stages (64 rows, 16384 x 256: 12.1 us in 16, 13.3 in 8; 16 rows, 8192
+// x 1024: 10.3 and 9.8; in 32 both are slower).
+int pick_splits(int64_t tiles, int k_blocks, int64_t results, int pairs)
 {
     const int64_t most = std::max(8, std::min(16, k_blocks / 16));
     const int64_t s = std::min<int64_t>({most, pairs / std::max<int64_t>(tiles, 1), k_blocks / 8});
-    return s >= 2 && k_blocks - k_blocks / s >= 14 ? (int)s : 1;
+    if (s < 2) return 1;
+    const double cost = 14 + 6e-6 * (double)s * (double)results;
+    return k_blocks - k_blocks / s >= cost ? (int)s : 1;
 }
 
 // Tensor maps and parameters of a grouped product, and its launch.
@@ -85,6 +97,9 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
     const bool few = M <= swg::GrpCfg<swg::MATH_16, true>::TOKENS;
     const int tokens = few ? swg::GrpCfg<swg::MATH_16, true>::TOKENS
                            : swg::GrpCfg<swg::MATH_16, false>::TOKENS;
+    const int narrowest = few  ? tokens
+                          : f4 ? swg::GrpCfg<swg::MATH_MX, false>::NARROWEST
+                               : swg::GrpCfg<swg::MATH_16, false>::NARROWEST;
     // Boxes of A's rows: of box i (see GrpMaps) those that tiles of at most
     // `half` rows per CTA can ask for.
     const int64_t half = std::min<int64_t>(tokens, ceil_to(M, 16)) / 2;
@@ -170,8 +185,10 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
         ok = ok && encode_tiled(&m.st, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, a.SA, std_, sst, stbox, 0);
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t tiles = (M / tokens + std::min(G, M)) * (int64_t)p.n_blocks;
-    const int splits = pick_splits(tiles, p.k_blocks, d.sms / 2);
+    // (Where tiles may be narrower, that comes before ranges of K: 256 rows, 8192 x
+    // 8192: 37 us in two tiles, 45 in two ranges.)
+    const int64_t tiles = most_tiles(M, G, narrowest) * (int64_t)p.n_blocks;
+    const int splits = pick_splits(tiles, p.k_blocks, M * N, d.sms / 2);
     p.splits = 1;
     p.split_blocks = p.k_blocks;
     if (splits > 1) {
@@ -225,10 +242,8 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
         if (a.Y) ok = ok && out_map(&m.y, a.Y, N / 2, N / 2);
     }
     if (!ok) return swg::record_cuda_error();
-    // (tiles of as few as 128 rows may be chosen)
-    const long long units = (M / 128 + std::min(G, M)) * (long long)p.n_blocks;
-    return swg::count_launch(f4 ? swg::launch_grouped_f4(nv, epi, few, m, p, units, d.sms, s)
-                                : swg::launch_grouped_16(epi, few, m, p, units, d.sms, s));
+    return swg::count_launch(f4 ? swg::launch_grouped_f4(nv, epi, few, m, p, tiles, d.sms, s)
+                                : swg::launch_grouped_16(epi, few, m, p, tiles, d.sms, s));
 }
 
 }  // namespace
@@ -313,7 +328,7 @@ int gemm_grouped_wgrad(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, 
     // The rows of a group cut into ranges, as pick_splits cuts K; how many rows
     // a group has is not known here, so their mean decides.
     const int64_t tiles = G * ((K + 255) / 256) * ((N + 255) / 256);
-    p.splits = pick_splits(tiles, (int)(M / 64 / G), d.sms / 2);
+    p.splits = pick_splits(tiles, (int)(M / 64 / G), G * K * N, d.sms / 2);
     swg::ReduceArgs r{};
     if (p.splits > 1) {
         r.ld = ceil_to(N, 8);

@@ -168,6 +168,7 @@ struct GrpCfg {
     // two columns of scales) and may be CANDIDATES widths, see choose_rows.
     static constexpr int UNIT = F4 ? 64 : 16;
     static constexpr int CANDIDATES = FEW ? 1 : F4 ? 3 : 8;
+    static constexpr int NARROWEST = TOKENS - (CANDIDATES - 1) * UNIT;
     static constexpr int EPI_WARPS = FEW ? 4 : 8;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int TILES_PER_STAGE = MATH == MATH_NV ? 4 : 2;   // scale tiles along K
@@ -731,9 +732,9 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
     const int G = p.groups.G;
     // so few rows that a group has at most one tile, and one of the narrowest width
     int most = C::TOKENS;
-    const bool narrow = p.groups.M <= C::TOKENS - (C::CANDIDATES - 1) * C::UNIT;
+    const bool narrow = p.groups.M <= C::NARROWEST;
     if (narrow && G < 32 * WARP_ROUNDS) {
-        static_assert(!F4 || C::TOKENS - (C::CANDIDATES - 1) * C::UNIT <= 128, "one scale tile");
+        static_assert(!F4 || C::NARROWEST <= 128, "one scale tile");
         if (warp == 0)
             warp_tables(p.groups, p.err, [&](int i, int s, int rows, int tile) {
                 start[i] = s;
@@ -745,7 +746,7 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
     } else {
         group_starts<C::THREADS>(p.groups, start, p.err);
         if (!narrow)
-            most = choose_rows<C>(start, G, p.n_blocks, p.k_blocks, (int)(gridDim.x >> 1),
+            most = choose_rows<C>(start, G, p.n_blocks * p.splits, p.split_blocks, (int)(gridDim.x >> 1),
                                   reinterpret_cast<float *>(scratch + 16));
         for (int g = threadIdx.x; g < G; g += C::THREADS)
             steps[g] = (uint8_t)(tile_step<C>(max(1, start[g + 1] - start[g]), most) / 16);
