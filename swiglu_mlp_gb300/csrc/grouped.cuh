@@ -265,41 +265,37 @@ __device__ __forceinline__ int tile_step(int rows, int most)
 // 2048: 34.8 us; by the mean alone, and the widest of equals, 39.9.  5003 in 12,
 // 2051 x 1003: 31.4 us against 33.7.)  The three 4-bit widths are told apart by
 // the mean as well.
-// Warp w of the first eight computes candidate w's; ends with a barrier.
+// cost_of_rows: that of tiles of at most `most` rows, given what the calling
+// warp's lanes have of the groups' tiles and rows, and the widest tile.
 template <class C>
-__device__ __forceinline__ int choose_rows(const int *start, int G, int n_blocks, int k_blocks,
-                                           int pairs, float *costs)
+__device__ __forceinline__ float cost_of_rows(int tiles, int rows, int widest, int n_blocks,
+                                              int k_blocks, int pairs)
 {
-    constexpr int CANDS = C::CANDIDATES;
-    const int lane = threadIdx.x & 31, cand = threadIdx.x >> 5;
-    if (cand < CANDS) {
-        const int most = C::TOKENS - cand * C::UNIT;
-        int tiles = 0, rows = 0, widest = 0;
-        for (int g = lane; g < G; g += 32) {
-            const int r = start[g + 1] - start[g];
-            tiles += tiles_of<C>(r, most);
-            rows += r;
-            if (!C::F4 && r > 0) widest = max(widest, tile_step<C>(r, most));
-        }
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
-            rows += __shfl_xor_sync(0xffffffffu, rows, d);
-            if (!C::F4) widest = max(widest, __shfl_xor_sync(0xffffffffu, widest, d));
-        }
-        const float units = (float)tiles * (float)n_blocks;
-        const float waves = ceilf(units / (float)pairs);
-        const float mean = (float)rows / fmaxf((float)tiles, 1.0f);
-        const float r = C::F4 ? mean : mean + ((float)widest - mean) / fmaxf(waves, 1.0f);
-        const float k = (float)k_blocks;
-        const float tile = C::F4 ? fmaxf(k * fmaxf(330.0f + r, 2.7f * r), 21.0f * r) + 500.0f
-                                 : k * fmaxf(r, 176.0f) + 700.0f;
-        if (lane == 0) costs[cand] = waves * tile;
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    rows = __reduce_add_sync(0xffffffffu, rows);
+    const float waves = (float)fast_div(tiles * n_blocks + pairs - 1, pairs);
+    const float mean = __fdividef((float)rows, fmaxf((float)tiles, 1.0f));
+    float r = mean;
+    if (!C::F4) {
+        widest = __reduce_max_sync(0xffffffffu, widest);
+        r += __fdividef((float)widest - mean, fmaxf(waves, 1.0f));
     }
+    const float k = (float)k_blocks;
+    const float tile = C::F4 ? fmaxf(k * fmaxf(330.0f + r, 2.7f * r), 21.0f * r) + 500.0f
+                             : k * fmaxf(r, 176.0f) + 700.0f;
+    return waves * tile;
+}
+
+// Warp w of the first eight has candidate w's cost; called by all threads, ends
+// with a barrier.
+template <class C>
+__device__ __forceinline__ int choose_rows(float cost, float *costs)
+{
+    if ((threadIdx.x & 31) == 0 && (threadIdx.x >> 5) < C::CANDIDATES) costs[threadIdx.x >> 5] = cost;
     __syncthreads();
     int best = 0;
 #pragma unroll
-    for (int c = 1; c < CANDS; ++c)
+    for (int c = 1; c < C::CANDIDATES; ++c)
         if (C::F4 ? costs[c] < costs[best] : costs[c] <= costs[best]) best = c;
     return C::TOKENS - best * C::UNIT;
 }
@@ -751,24 +747,73 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
     // Up to here only this pair's own resources; now the offsets may be read.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int G = p.groups.G;
-    // so few rows that a group has at most one tile, and one of the narrowest width
+    // So few rows that a group has at most one tile, and one of the narrowest width?
+    const bool narrow = FEW || p.groups.M <= C::NARROWEST;
+    static_assert(!F4 || C::NARROWEST <= 128, "one scale tile");
     int most = C::TOKENS;
-    const bool narrow = p.groups.M <= C::NARROWEST;
+    const int n_blocks = p.n_blocks * p.splits, pairs = (int)(gridDim.x >> 1);
+    const int candidate = C::TOKENS - min(warp, C::CANDIDATES - 1) * C::UNIT;
+    float *costs = reinterpret_cast<float *>(scratch + 16);
     if (narrow && G < 32 * WARP_ROUNDS) {
-        static_assert(!F4 || C::NARROWEST <= 128, "one scale tile");
-        if (warp == 0)
-            warp_tables(p.groups, p.err, [&](int i, int s, int rows, int tile) {
-                start[i] = s;
-                first[i] = tile;
-                if (F4) stile[i] = tile;
-                if (i < G) steps[i] = (uint8_t)(ceil_div(max(1, rows), C::UNIT) * (C::UNIT / 16));
-            });
+        if (warp == 0) {
+            const WarpGroups w = warp_groups(p.groups, p.err, true);
+            int before = 0;                          // groups with rows: they have a tile
+#pragma unroll
+            for (int r = 0; r < WARP_ROUNDS; ++r) {
+                const int i = 32 * r + lane, rows = w.rows(r);
+                const unsigned has = __ballot_sync(0xffffffffu, rows > 0);
+                const int tile = before + __popc(has & ((1u << lane) - 1));
+                if (i <= G) {
+                    start[i] = w.start[r];
+                    first[i] = tile;
+                    if (F4) stile[i] = tile;
+                    if (i < G) steps[i] = (uint8_t)(ceil_div(max(1, rows), C::UNIT) * (C::UNIT / 16));
+                }
+                before += __popc(has);
+            }
+        }
+        __syncthreads();
+    } else if (!FEW && G < (F4 ? 128 : 64)) {
+        // Every warp reads the groups; the first eight find the widths' costs, the
+        // first two write the tables.  (16 bits, 100 groups of 20 rows: 12.7 us so,
+        // 12.3 through shared memory; 8 of 512: 8.5 and 9.1.)
+        const WarpGroups w = warp_groups(p.groups, p.err, warp == 0);
+        int tiles = 0, rows = 0, widest = 0;
+#pragma unroll
+        for (int r = 0; r < WARP_ROUNDS; ++r) {
+            if (32 * r >= G) break;
+            const int n = w.rows(r);
+            tiles += tiles_of<C>(n, candidate);
+            rows += n;
+            if (!C::F4 && n > 0) widest = max(widest, tile_step<C>(n, candidate));
+        }
+        most = choose_rows<C>(
+            cost_of_rows<C>(tiles, rows, widest, n_blocks, p.split_blocks, pairs), costs);
+        if (warp == 0) {
+#pragma unroll
+            for (int r = 0; r < WARP_ROUNDS; ++r) {
+                const int i = 32 * r + lane;
+                if (i <= G) start[i] = w.start[r];
+                if (i < G) steps[i] = (uint8_t)(tile_step<C>(max(1, w.rows(r)), most) / 16);
+            }
+            warp_tile_sums(w, first, [most](int n) { return tiles_of<C>(n, most); });
+        } else if (F4 && warp == 1) {
+            warp_tile_sums(w, stile, [](int n) { return ceil_div(n, 128); });
+        }
         __syncthreads();
     } else {
         group_starts<C::THREADS>(p.groups, start, p.err);
-        if (!narrow)
-            most = choose_rows<C>(start, G, p.n_blocks * p.splits, p.split_blocks, (int)(gridDim.x >> 1),
-                                  reinterpret_cast<float *>(scratch + 16));
+        if (!narrow) {
+            int tiles = 0, rows = 0, widest = 0;
+            for (int g = lane; g < G; g += 32) {
+                const int n = start[g + 1] - start[g];
+                tiles += tiles_of<C>(n, candidate);
+                rows += n;
+                if (!C::F4 && n > 0) widest = max(widest, tile_step<C>(n, candidate));
+            }
+            most = choose_rows<C>(
+                cost_of_rows<C>(tiles, rows, widest, n_blocks, p.split_blocks, pairs), costs);
+        }
         for (int g = threadIdx.x; g < G; g += C::THREADS)
             steps[g] = (uint8_t)(tile_step<C>(max(1, start[g + 1] - start[g]), most) / 16);
         tile_sums<C::THREADS>(G, start, first, scratch,

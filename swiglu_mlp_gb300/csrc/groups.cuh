@@ -88,17 +88,27 @@ __device__ __forceinline__ void tile_sums(int G, const int *start, int *first, i
     __syncthreads();
 }
 
-// The tables for groups that have at most one tile each, by one warp: the
-// offsets stay in registers, and a group's first tile is the count of groups
-// with rows before it.  put(i, start, rows, first) is called for i = 0..G, G <
-// 32 * WARP_ROUNDS; a barrier of the CTA has to follow.  (Through group_starts
-// and tile_sums, with five barriers between them, a call of 8 or 64 groups of
-// few rows took 0.7 or 0.6 us longer.)
+// Fewer than 32 * WARP_ROUNDS groups fit in the registers of a warp: lane l of
+// round r has group 32 r + l.  Through shared memory, by group_starts and
+// tile_sums with the barriers between them, calls of 8 or 64 groups of few rows
+// took 0.7 or 0.6 us longer, of more rows (8192 x 512 x 512) 0.5.
 constexpr int WARP_ROUNDS = 4;
-template <class F>
-__device__ __forceinline__ void warp_tables(const Groups &gr, int *err, F put)
+
+struct WarpGroups {
+    int start[WARP_ROUNDS], next[WARP_ROUNDS];       // offsets of the group and of the next
+    int G;
+    __device__ __forceinline__ int rows(int r) const
+    {
+        return 32 * r + (int)(threadIdx.x & 31) < G ? next[r] - start[r] : 0;
+    }
+};
+
+// The offsets, clamped as in group_starts (and reported, if `report`).
+__device__ __forceinline__ WarpGroups warp_groups(const Groups &gr, int *err, bool report)
 {
     const int lane = threadIdx.x & 31, G = gr.G;
+    WarpGroups w;
+    w.G = G;
     int v[WARP_ROUNDS + 1];
     bool bad = false;
 #pragma unroll
@@ -109,21 +119,20 @@ __device__ __forceinline__ void warp_tables(const Groups &gr, int *err, F put)
         bad = bad || v[r] != raw;
     }
     v[WARP_ROUNDS] = v[WARP_ROUNDS - 1];
-    int next[WARP_ROUNDS];
     auto neighbours = [&] {
 #pragma unroll
         for (int r = 0; r < WARP_ROUNDS; ++r) {
             const int down = __shfl_down_sync(0xffffffffu, v[r], 1);
             const int wrap = __shfl_sync(0xffffffffu, v[r + 1], 0);
-            next[r] = lane < 31 ? down : wrap;
+            w.start[r] = v[r];
+            w.next[r] = lane < 31 ? down : wrap;
         }
     };
     neighbours();
 #pragma unroll
-    for (int r = 0; r < WARP_ROUNDS; ++r)
-        bad = bad || (r * 32 + lane < G && next[r] < v[r]);
+    for (int r = 0; r < WARP_ROUNDS; ++r) bad = bad || w.rows(r) < 0;
     if (__any_sync(0xffffffffu, bad)) {              // clamp: the running maximum
-        if (lane == 0) atomicCAS(err, 0, ERR_INVALID);
+        if (report && lane == 0) atomicCAS(err, 0, ERR_INVALID);
         int top = 0;
 #pragma unroll
         for (int r = 0; r < WARP_ROUNDS; ++r) {
@@ -138,14 +147,33 @@ __device__ __forceinline__ void warp_tables(const Groups &gr, int *err, F put)
         v[WARP_ROUNDS] = top;
         neighbours();
     }
+    return w;
+}
+
+// first[0..G]: how many tiles the groups before g have, a group of `rows` rows
+// having tiles_of(rows).  By one warp; a barrier of the CTA has to follow.
+template <class F>
+__device__ __forceinline__ void warp_tile_sums(const WarpGroups &w, int *first, F tiles_of)
+{
+    const int lane = threadIdx.x & 31;
     int before = 0;
 #pragma unroll
     for (int r = 0; r < WARP_ROUNDS; ++r) {
-        const int i = r * 32 + lane;
-        const int rows = i < G ? next[r] - v[r] : 0;
-        const unsigned has = __ballot_sync(0xffffffffu, rows > 0);
-        if (i <= G) put(i, v[r], rows, before + __popc(has & ((1u << lane) - 1)));
-        before += __popc(has);
+        if (32 * r > w.G) break;
+        const int n = tiles_of(w.rows(r));
+        if (w.G == 1) {
+            const int all = __shfl_sync(0xffffffffu, n, 0);
+            if (lane < 2) first[lane] = lane * all;
+            return;
+        }
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        if (32 * r + lane <= w.G) first[32 * r + lane] = before + sum - n;
+        before += __shfl_sync(0xffffffffu, sum, 31);
     }
 }
 
