@@ -25,9 +25,9 @@
 // What bounds it, and what it measured on one GB300:
 //   many rows, 16 bits: the tensor pipe at the clock that the power limit
 //     leaves.  SwiGLU, 16384 rows of 16 groups, K = 4096, N = 2 x 1792: 267 us,
-//     1800 TFLOP/s; gradient of half as many rows, 8 groups: 150 us, 1600.
+//     1800 TFLOP/s; gradient of half as many rows, 8 groups: 146 us, 1650.
 //   many rows, 4 bits: MMAs and the copies of their scales, one behind the other
-//     in the tensor pipe, which is 71% busy.  8192 x 14336 x 4096: NVFP4 143 us,
+//     in the tensor pipe, which is 70% busy.  8192 x 14336 x 4096: NVFP4 143 us,
 //     6.7 PFLOP/s; MXFP4 135 us, 7.1.
 //   few rows: the weights' way from memory and about 3.3 us that any call takes
 //     (set-up, offsets, first load, last store).  8 groups of one row, 4096 x
