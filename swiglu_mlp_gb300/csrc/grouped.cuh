@@ -894,7 +894,7 @@ __global__ void __launch_bounds__(GrpCfg<MATH, FEW>::THREADS, 1)
             }
             // Never leave with loads in flight into this CTA's shared memory.
             if (leader) {
-                // (stages before `stage` were last used in this round, the others
+                // (stages before `stage` were last used in this lap of the ring, the others
                 // in the one before)
                 for (int s = 0; s < S; ++s)
                     if (s < stage || wrapped)
