@@ -118,6 +118,8 @@ typedef enum {
  *                   allocated (queued work or a captured graph may still use
  *                   them) until swg_shutdown() frees them all.  Two kernels are
  *                   launched: the GEMM and a dependent reduction.
+ *                   Threads that share a stream queue the two together, each
+ *                   call's before the next's.
  *   One or two rows M <= 2 with 16-bit or e4m3 A and B (decode of one or two
  *                   tokens), K <= 8 * 8192 / M and N <= 2^30: one kernel on the FP32 pipes
  *                   instead ("GEMM o Coração Matemático", §14: the product
@@ -303,6 +305,8 @@ SWG_API int swiglu_interleave(const void *W1, const void *W2, void *W_fused,
  *                the last call's contents (each call writes every partial it
  *                reads, so nothing needs clearing).  Calls that overlap on the
  *                GPU race with each other: order them, e.g. on one stream.
+ *                (Threads may share that stream: a call's kernels are queued
+ *                together.)
  *   Reset        call swg_shutdown() before cudaDeviceReset(): it makes the
  *                next call look the address up again.
  */

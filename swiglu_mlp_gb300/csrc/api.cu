@@ -111,6 +111,9 @@ struct Workspace {
     // already queued, or a CUDA graph captured earlier, may still address
     // them, so they are freed only by swg_shutdown.
     std::vector<void *> retired;
+    // Held by a split call from its lookup until the kernel that reads the
+    // partials is queued too.
+    std::mutex mu;
 };
 
 // Test switch SWG_TEST_WS_GUARD=1: every split-K workspace (and the fixed
@@ -154,13 +157,22 @@ int device_state(DeviceState *&out)
     return SWG_OK;
 }
 
-// Grow-only split-K workspace for (device, stream).  Only the stream that
-// owns it uses it, so stream order keeps calls from overlapping.
-int workspace(DeviceState *d, cudaStream_t s, size_t bytes, Workspace *&out)
+// Grow-only split-K workspace for (device, stream).  A split call queues two
+// kernels, one that writes the partials and one that reads them; stream order
+// keeps the calls apart only if no other thread queues its own on the same
+// stream between the two, so the caller keeps `held` until both are queued.
+// (g_mu is released first: nothing is locked while the workspace is waited for.)
+int workspace(DeviceState *d, cudaStream_t s, size_t bytes, Workspace *&out,
+              std::unique_lock<std::mutex> &held)
 {
     if (std::getenv("SWG_TEST_FAIL_ALLOC")) return SWG_ERR_NO_MEMORY;
-    std::lock_guard<std::mutex> lk(g_mu);
-    Workspace &w = d->ws[s];
+    Workspace *found = nullptr;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        found = &d->ws[s];
+    }
+    Workspace &w = *found;
+    held = std::unique_lock<std::mutex>(w.mu);
     if (w.base == nullptr || w.bytes < bytes) {
         // No allocation while the stream is being captured into a graph:
         // the caller runs the call once before capturing.
@@ -195,21 +207,25 @@ int workspace(DeviceState *d, cudaStream_t s, size_t bytes, Workspace *&out)
 // Where a split-K call's FP32 partials go: the (device, stream) workspace
 // above, or -- for gemm_splitk_noalloc -- a fixed array of `bytes` bytes at
 // `base` that belongs to the library's device image.
+// `mu` serves it as Workspace::mu does the others.
 struct FixedScratch {
     float *base;
     size_t bytes;
+    std::mutex *mu;
 };
 
+// `held`: keep it until the call's last kernel is queued.
 int split_workspace(DeviceState *d, cudaStream_t s, size_t bytes, const FixedScratch *fx,
-                    float *&out)
+                    float *&out, std::unique_lock<std::mutex> &held)
 {
     if (fx) {
         if (bytes > fx->bytes) return SWG_ERR_UNSUPPORTED;   // partials would not fit
+        held = std::unique_lock<std::mutex>(*fx->mu);
         out = fx->base;
         return SWG_OK;
     }
     Workspace *w = nullptr;
-    if (int rc = workspace(d, s, bytes, w)) return rc;
+    if (int rc = workspace(d, s, bytes, w, held)) return rc;
     out = static_cast<float *>(w->base);
     return SWG_OK;
 }
@@ -602,8 +618,9 @@ int splitk_swapped(DeviceState *d, const TypeInfo &ti, int transA, int transB, i
 
     const int64_t ld_ws = cdiv(N, 4) * 4;
     float *ws = nullptr;
+    std::unique_lock<std::mutex> held;
     if (int rc = split_workspace(d, s, sizeof(float) * (size_t)splits * (size_t)M * (size_t)ld_ws,
-                                 fx, ws))
+                                 fx, ws, held))
         return rc;
 
     p.splits = splits;
@@ -899,12 +916,12 @@ int count_launch(cudaError_t e)
     return SWG_OK;
 }
 
-int stream_workspace(cudaStream_t s, size_t bytes, float *&out)
+int stream_workspace(cudaStream_t s, size_t bytes, float *&out, std::unique_lock<std::mutex> &held)
 {
     DeviceState *d = nullptr;
     if (int rc = device_state(d)) return rc;
     Workspace *w = nullptr;
-    if (int rc = workspace(d, s, bytes, w)) return rc;
+    if (int rc = workspace(d, s, bytes, w, held)) return rc;
     out = static_cast<float *>(w->base);
     return SWG_OK;
 }
@@ -1222,9 +1239,10 @@ static int gemm_impl(int transA, int transB, int64_t M, int64_t N, int64_t K, fl
         const int units = (int)std::min<int64_t>(p.units, slots);
         const int64_t ld_ws = cdiv(N, 4) * 4;
         float *ws = nullptr;
+        std::unique_lock<std::mutex> held;
         if (int rc = split_workspace(d, s,
                                      sizeof(float) * (size_t)splits * (size_t)M * (size_t)ld_ws,
-                                     fx, ws))
+                                     fx, ws, held))
             return rc;
         p.ws = ws;
         p.ld_ws = ld_ws;
@@ -1669,6 +1687,7 @@ static __device__ __align__(256) float
 
 constexpr int kNoallocMaxDevices = 64;
 std::mutex g_noalloc_mu;
+std::mutex g_noalloc_use;                   // a split call's two kernels, see FixedScratch
 bool g_noalloc_ready[kNoallocMaxDevices];
 bool g_noalloc_guarded[kNoallocMaxDevices];
 float *g_noalloc_ptr[kNoallocMaxDevices];   // device address of g_noalloc_scratch
@@ -1716,6 +1735,7 @@ int noalloc_scratch(cudaStream_t s, FixedScratch &out)
     if (int rc = noalloc_setup(dev, s)) return rc;
     out.base = g_noalloc_ptr[dev] + kNoallocGuardFloats;
     out.bytes = SWG_NOALLOC_SCRATCH_BYTES;
+    out.mu = &g_noalloc_use;
     return SWG_OK;
 }
 
@@ -1748,7 +1768,8 @@ int swg_debug_workspace_guards(void *stream, int64_t *bad_bytes)
         auto it = g_dev.find(dev);
         if (it != g_dev.end()) {
             for (auto &kv : it->second.ws) {
-                const Workspace &w = kv.second;
+                Workspace &w = kv.second;
+                std::lock_guard<std::mutex> lw(w.mu);
                 if (!w.raw || w.raw == w.base) continue;          // allocated without guards
                 const uint8_t *lo = static_cast<const uint8_t *>(w.raw);
                 const int64_t a = guard_damage(lo, kGuardBytes);

@@ -199,7 +199,8 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
         r.ld = ceil_to(N, 8);
         r.stride = r.ld * M;
         float *ws = nullptr;
-        if (int rc = swg::stream_workspace(s, sizeof(float) * (size_t)p.splits * (size_t)r.stride, ws))
+        std::unique_lock<std::mutex> held;           // until the sum of the partials is queued
+        if (int rc = swg::stream_workspace(s, sizeof(float) * (size_t)p.splits * (size_t)r.stride, ws, held))
             return rc;
         r.ws = ws;
         r.splits = p.splits;
@@ -330,11 +331,12 @@ int gemm_grouped_wgrad(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, 
     const int64_t tiles = G * ((K + 255) / 256) * ((N + 255) / 256);
     p.splits = pick_splits(tiles, (int)(M / 64 / G), G * K * N, d.sms / 2);
     swg::ReduceArgs r{};
+    std::unique_lock<std::mutex> held;               // until the sum of the partials is queued
     if (p.splits > 1) {
         r.ld = ceil_to(N, 8);
         r.stride = r.ld * K * G;
         float *ws = nullptr;
-        if (int rc = swg::stream_workspace(s, sizeof(float) * (size_t)p.splits * (size_t)r.stride, ws))
+        if (int rc = swg::stream_workspace(s, sizeof(float) * (size_t)p.splits * (size_t)r.stride, ws, held))
             return rc;
         r.ws = ws;
         r.splits = p.splits;

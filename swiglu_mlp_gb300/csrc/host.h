@@ -8,6 +8,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 namespace swg {
 
@@ -28,8 +29,9 @@ int count_launch(cudaError_t e);
 
 // FP32 partials of a split call on (current device, stream): grow-only,
 // library-owned, freed by swg_shutdown; SWG_ERR_UNSUPPORTED when it would
-// have to allocate while the stream is being captured.
-int stream_workspace(cudaStream_t s, size_t bytes, float *&out);
+// have to allocate while the stream is being captured.  They are this call's
+// as long as it keeps `held`: until its last kernel is queued.
+int stream_workspace(cudaStream_t s, size_t bytes, float *&out, std::unique_lock<std::mutex> &held);
 
 // cuTensorMapEncodeTiled with a swizzle of 128, 64 or 0 (none) bytes, unit
 // element strides, no interleave and zero fill; false (recorded) when it
