@@ -119,7 +119,8 @@ typedef enum {
  *                   them) until swg_shutdown() frees them all.  Two kernels are
  *                   launched: the GEMM and a dependent reduction.
  *                   Threads that share a stream queue the two together, each
- *                   call's before the next's.
+ *                   call's before the next's; cudaStreamPerThread is a stream
+ *                   of its own in every thread.
  *   One or two rows M <= 2 with 16-bit or e4m3 A and B (decode of one or two
  *                   tokens), K <= 8 * 8192 / M and N <= 2^30: one kernel on the FP32 pipes
  *                   instead ("GEMM o Coração Matemático", §14: the product

@@ -15,6 +15,7 @@
 #include <cstdlib>
 #include <map>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include "swiglu_mlp.h"
@@ -116,6 +117,19 @@ struct Workspace {
     std::mutex mu;
 };
 
+// Whose workspace: a stream's.  cudaStreamPerThread is one handle for a stream
+// of its own in every thread, so there the thread counts too (0 elsewhere).
+// Other handles (NULL and cudaStreamLegacy) are the same stream in every thread.
+using StreamKey = std::pair<cudaStream_t, uint64_t>;
+
+StreamKey stream_key(cudaStream_t s)
+{
+    if (s != cudaStreamPerThread) return {s, 0};
+    static std::atomic<uint64_t> threads{0};
+    thread_local const uint64_t self = ++threads;
+    return {s, self};
+}
+
 // Test switch SWG_TEST_WS_GUARD=1: every split-K workspace (and the fixed
 // array of gemm_splitk_noalloc) gets kGuardBytes of kGuardByte before and
 // after it, which swg_debug_workspace_guards checks.  A kernel that wrote
@@ -133,7 +147,7 @@ struct DeviceState {
     bool ready = false;
     int sms = 0;
     int *err = nullptr;                          // address of g_err_word
-    std::map<cudaStream_t, Workspace> ws;
+    std::map<StreamKey, Workspace> ws;
     std::map<int, int> max_pairs;                // (kind, bn) -> resident CTA pairs
 };
 
@@ -169,7 +183,7 @@ int workspace(DeviceState *d, cudaStream_t s, size_t bytes, Workspace *&out,
     Workspace *found = nullptr;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        found = &d->ws[s];
+        found = &d->ws[stream_key(s)];
     }
     Workspace &w = *found;
     held = std::unique_lock<std::mutex>(w.mu);

@@ -109,3 +109,28 @@ def test_threads_sharing_one_stream():
     torch.cuda.synchronize()
     assert swg.get_device_error() == 0
     assert [c.bad.tolist() for c in calls] == [[0] * 5] * 4
+
+
+def test_default_stream_of_each_thread():
+    """cudaStreamPerThread: one handle, in every thread another stream."""
+    per_thread = 2
+    calls = [Calls(20 + i) for i in range(4)]
+    for c in calls:
+        c.alone()
+    first = threading.Barrier(len(calls))
+    bad = [0] * len(calls)
+
+    def work(i):
+        def f():
+            c = calls[i]
+            c.run(per_thread, noalloc=False)
+            first.wait(60)
+            for _ in range(40):
+                for _ in range(5):
+                    c.run(per_thread, noalloc=False)
+                assert swg.get_device_error(per_thread) == 0     # synchronises this thread's
+                bad[i] += sum(not torch.equal(t, w) for t, w in zip(c.outs[:4], c.want))
+        return f
+
+    in_threads([work(i) for i in range(len(calls))])
+    assert bad == [0] * len(calls)
