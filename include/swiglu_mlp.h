@@ -115,8 +115,8 @@ typedef enum {
  *                   in a library-owned workspace, allocated (cudaMalloc) on
  *                   first use per (device, stream) and replaced by a larger
  *                   one when a larger split needs it; replaced workspaces stay
- *                   allocated (queued work or a captured graph may still use
- *                   them) until swg_shutdown() frees them all.  Two kernels are
+ *                   allocated (queued work may still use them) until
+ *                   swg_shutdown() frees them all.  Two kernels are
  *                   launched: the GEMM and a dependent reduction.
  *                   Threads that share a stream queue the two together, each
  *                   call's before the next's; cudaStreamPerThread is a stream
@@ -134,7 +134,13 @@ typedef enum {
  *                   to allocate while its stream is capturing returns
  *                   SWG_ERR_UNSUPPORTED and launches nothing.  Calls of the
  *                   one-or-two-rows kernel and of the cluster-reduced split
- *                   need no earlier run.
+ *                   need no earlier run.  A graph keeps its partials in a
+ *                   workspace of its own, allocated (cudaMalloc, no part of
+ *                   the graph) during the capture and reused by later
+ *                   captures once the graph and what was instantiated from
+ *                   it are destroyed.  So it may run on any stream, beside
+ *                   other graphs and calls; only two executable graphs
+ *                   instantiated from one capture must not run at once.
  */
 SWG_API int gemm(int transA, int transB, int64_t M, int64_t N, int64_t K, float alpha,
          const void *A, int64_t lda, const void *B, int64_t ldb, float beta,
@@ -514,7 +520,7 @@ SWG_API uint64_t swg_launch_count(void);
  * occupancy, kernel attributes), so it is also the call to make before
  * cudaDeviceReset().  Safe to call twice; later calls allocate and look up
  * afresh.  Call only when no library work is in flight and no captured graph
- * that used the workspaces will be replayed. */
+ * with a split call in it will be replayed. */
 SWG_API void swg_shutdown(void);
 
 #ifdef __cplusplus

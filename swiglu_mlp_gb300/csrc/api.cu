@@ -109,8 +109,8 @@ struct Workspace {
     size_t bytes = 0;
     void *raw = nullptr;    // the allocation: base, or base - kGuardBytes with guards
     // Smaller workspaces this one replaced (their raw allocations).  Work
-    // already queued, or a CUDA graph captured earlier, may still address
-    // them, so they are freed only by swg_shutdown.
+    // already queued may still address them, so they are freed only by
+    // swg_shutdown.
     std::vector<void *> retired;
     // Held by a split call from its lookup until the kernel that reads the
     // partials is queued too.
@@ -171,12 +171,139 @@ int device_state(DeviceState *&out)
     return SWG_OK;
 }
 
-// Grow-only split-K workspace for (device, stream).  A split call queues two
+// Partials of captured split calls.  A graph may run on any stream, beside
+// another one captured on the same stream and beside calls on that stream, so
+// what it captures has buffers of its own: one for each stream of a capture,
+// in which the calls follow one another.  They belong to the graph and to what
+// is instantiated from it; when the last of those is gone (and has run), CUDA
+// calls graph_gone and later captures take them over.
+struct GraphScratch {
+    int dev;
+    unsigned long long capture;
+    StreamKey stream;
+    struct Buffer {
+        void *base;
+        size_t bytes;
+    };
+    std::vector<Buffer> buffers;      // the last is the largest
+};
+
+// (Never destroyed: CUDA may still call graph_gone while the process exits.)
+struct GraphBuffers {
+    std::mutex mu;
+    std::map<std::pair<unsigned long long, StreamKey>, GraphScratch *> live;
+    std::map<int, std::vector<GraphScratch::Buffer>> idle;    // by device
+};
+
+GraphBuffers &graph_buffers()
+{
+    static GraphBuffers *const all = new GraphBuffers;
+    return *all;
+}
+
+// On a thread of CUDA's, which may make no CUDA calls.
+void CUDART_CB graph_gone(void *scratch)
+{
+    GraphScratch *const g = static_cast<GraphScratch *>(scratch);
+    GraphBuffers &all = graph_buffers();
+    {
+        std::lock_guard<std::mutex> lk(all.mu);
+        auto &idle = all.idle[g->dev];
+        idle.insert(idle.end(), g->buffers.begin(), g->buffers.end());
+        const auto it = all.live.find({g->capture, g->stream});
+        if (it != all.live.end() && it->second == g) all.live.erase(it);
+    }
+    delete g;
+}
+
+// The buffer of the graph that stream s is being captured into (capture `id`).
+// The caller holds the stream's workspace, so that no other thread has to do
+// with this stream's entry; `mu` is not held in CUDA calls, which may wait for
+// the thread of graph_gone.
+int graph_workspace(int dev, StreamKey s, unsigned long long id, cudaGraph_t graph, size_t bytes,
+                    float *&out)
+{
+    GraphBuffers &all = graph_buffers();
+    GraphScratch *g = nullptr;
+    {
+        std::lock_guard<std::mutex> lk(all.mu);
+        const auto it = all.live.find({id, s});
+        if (it != all.live.end()) g = it->second;
+    }
+    if (g == nullptr) {
+        g = new GraphScratch{dev, id, s, {}};
+        cudaUserObject_t object = nullptr;
+        if (cudaUserObjectCreate(&object, g, graph_gone, 1, cudaUserObjectNoDestructorSync) !=
+            cudaSuccess) {
+            delete g;
+            return cuda_fail();
+        }
+        if (cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) != cudaSuccess) {
+            const int rc = cuda_fail();
+            cudaUserObjectRelease(object, 1);        // (graph_gone deletes g)
+            return rc;
+        }
+        std::lock_guard<std::mutex> lk(all.mu);
+        all.live[{id, s}] = g;
+    }
+    if (g->buffers.empty() || g->buffers.back().bytes < bytes) {
+        GraphScratch::Buffer b{nullptr, bytes};
+        {
+            // the smallest idle buffer that is large enough
+            std::lock_guard<std::mutex> lk(all.mu);
+            auto &idle = all.idle[dev];
+            auto best = idle.end();
+            for (auto it = idle.begin(); it != idle.end(); ++it)
+                if (it->bytes >= bytes && (best == idle.end() || it->bytes < best->bytes)) best = it;
+            if (best != idle.end()) {
+                b = *best;
+                idle.erase(best);
+            }
+        }
+        if (b.base == nullptr) {
+            // no part of the graph; relaxed mode permits it during a capture
+            cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+            if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return cuda_fail();
+            const cudaError_t e = cudaMalloc(&b.base, bytes);
+            cudaThreadExchangeStreamCaptureMode(&mode);
+            if (e != cudaSuccess) {
+                cudaGetLastError();
+                return SWG_ERR_NO_MEMORY;
+            }
+        }
+        g->buffers.push_back(b);
+    }
+    out = static_cast<float *>(g->buffers.back().base);
+    return SWG_OK;
+}
+
+// swg_shutdown: no graph that used them will run again.
+void free_graph_buffers()
+{
+    std::map<int, std::vector<GraphScratch::Buffer>> idle;
+    {
+        GraphBuffers &all = graph_buffers();
+        std::lock_guard<std::mutex> lk(all.mu);
+        idle.swap(all.idle);
+        for (auto &kv : all.live) {
+            auto &to = idle[kv.second->dev];
+            to.insert(to.end(), kv.second->buffers.begin(), kv.second->buffers.end());
+            kv.second->buffers.clear();              // (graph_gone deletes the rest)
+        }
+        all.live.clear();
+    }
+    for (auto &kv : idle)
+        if (!kv.second.empty() && cudaSetDevice(kv.first) == cudaSuccess)
+            for (auto &b : kv.second) cudaFree(b.base);
+}
+
+// Grow-only split-K workspace for (device, stream), and for captured calls a
+// buffer of their graph's.  A split call queues two
 // kernels, one that writes the partials and one that reads them; stream order
 // keeps the calls apart only if no other thread queues its own on the same
 // stream between the two, so the caller keeps `held` until both are queued.
 // (g_mu is released first: nothing is locked while the workspace is waited for.)
-int workspace(DeviceState *d, cudaStream_t s, size_t bytes, Workspace *&out,
+int workspace(DeviceState *d, cudaStream_t s, size_t bytes, float *&out,
               std::unique_lock<std::mutex> &held)
 {
     if (std::getenv("SWG_TEST_FAIL_ALLOC")) return SWG_ERR_NO_MEMORY;
@@ -187,11 +314,10 @@ int workspace(DeviceState *d, cudaStream_t s, size_t bytes, Workspace *&out,
     }
     Workspace &w = *found;
     held = std::unique_lock<std::mutex>(w.mu);
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return cuda_fail();
     if (w.base == nullptr || w.bytes < bytes) {
-        // No allocation while the stream is being captured into a graph:
-        // the caller runs the call once before capturing.
-        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-        if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return cuda_fail();
+        // The caller runs the call once on the stream before capturing it.
         if (cs != cudaStreamCaptureStatusNone) return SWG_ERR_UNSUPPORTED;
         const bool guards = ws_guards_enabled();
         const size_t extra = guards ? 2 * kGuardBytes : 0;
@@ -214,7 +340,16 @@ int workspace(DeviceState *d, cudaStream_t s, size_t bytes, Workspace *&out,
         w.base = static_cast<uint8_t *>(p) + (guards ? kGuardBytes : 0);
         w.bytes = bytes;
     }
-    out = &w;
+    if (cs == cudaStreamCaptureStatusActive) {
+        unsigned long long id = 0;
+        cudaGraph_t graph = nullptr;
+        int dev = 0;
+        if (cudaStreamGetCaptureInfo(s, &cs, &id, &graph) != cudaSuccess ||
+            cudaGetDevice(&dev) != cudaSuccess)
+            return cuda_fail();
+        return graph_workspace(dev, stream_key(s), id, graph, bytes, out);
+    }
+    out = static_cast<float *>(w.base);
     return SWG_OK;
 }
 
@@ -238,10 +373,7 @@ int split_workspace(DeviceState *d, cudaStream_t s, size_t bytes, const FixedScr
         out = fx->base;
         return SWG_OK;
     }
-    Workspace *w = nullptr;
-    if (int rc = workspace(d, s, bytes, w, held)) return rc;
-    out = static_cast<float *>(w->base);
-    return SWG_OK;
+    return workspace(d, s, bytes, out, held);
 }
 
 // The fixed array of gemm_splitk_noalloc on the current device (defined at
@@ -934,10 +1066,7 @@ int stream_workspace(cudaStream_t s, size_t bytes, float *&out, std::unique_lock
 {
     DeviceState *d = nullptr;
     if (int rc = device_state(d)) return rc;
-    Workspace *w = nullptr;
-    if (int rc = workspace(d, s, bytes, w, held)) return rc;
-    out = static_cast<float *>(w->base);
-    return SWG_OK;
+    return workspace(d, s, bytes, out, held);
 }
 
 bool encode_tiled(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *ptr,
@@ -1666,6 +1795,7 @@ void swg_shutdown(void)
             dv.second.ready = false;
             dv.second.max_pairs.clear();
         }
+        free_graph_buffers();
         if (have_cur) cudaSetDevice(cur);
         swg::g_setup_epoch.fetch_add(1);
     }
