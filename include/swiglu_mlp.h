@@ -339,7 +339,8 @@ SWG_API int gemm_splitk_noalloc(int transA, int transB, int64_t M, int64_t N,
  * SWG_ERR_INVALID_ARG.  G <= SWG_MAX_GROUPS, else SWG_ERR_UNSUPPORTED.
  * 16-bit dtypes only (SWG_F16_F32OUT, SWG_BF16, SWG_F16, SWG_BF16_F32OUT);
  * alignment, size and graph-capture rules are gemm's, for every pointer,
- * row stride and group stride.
+ * row stride and group stride, but M, N, K (and 2N of the SwiGLU calls) are at
+ * most 2^31 - 1024, here and in the 4-bit calls below.
  */
 #define SWG_MAX_GROUPS 1024
 

@@ -14,7 +14,10 @@
 
 namespace {
 
-constexpr int64_t kMaxDim = 0x7fffffff;
+constexpr int64_t kMaxStride = 0x7fffffff;
+// The kernels number rows and columns in 32 bits and round them up to whole
+// tiles, up to 511 beyond the last.
+constexpr int64_t kMaxDim = 0x80000000ll - 1024;
 
 int64_t ceil_to(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -50,10 +53,12 @@ int check_groups(const int32_t *offsets, int64_t G)
     return SWG_OK;
 }
 
-bool too_big(std::initializer_list<int64_t> v)
+bool too_big(std::initializer_list<int64_t> dims, std::initializer_list<int64_t> strides = {})
 {
-    for (int64_t x : v)
+    for (int64_t x : dims)
         if (x > kMaxDim) return true;
+    for (int64_t x : strides)
+        if (x > kMaxStride) return true;
     return false;
 }
 
@@ -267,7 +272,7 @@ int gemm_grouped(int transB, int64_t G, int64_t M, int64_t N, int64_t K, float a
     if (K > 0 && (A == nullptr || B == nullptr || lda < K || ldb < b_cols))
         return SWG_ERR_INVALID_ARG;
     if (K > 0 && G > 1 && strideB < (b_rows - 1) * ldb + b_cols) return SWG_ERR_INVALID_ARG;
-    if (too_big({M, N, K, lda, ldb, ldc})) return SWG_ERR_UNSUPPORTED;
+    if (too_big({M, N, K}, {lda, ldb, ldc})) return SWG_ERR_UNSUPPORTED;
     if (!aligned16(C) || (ldc * out_bytes) % 16 != 0) return SWG_ERR_MISALIGNED;
     if (K > 0 && (!aligned16(A) || !aligned16(B) || lda % 8 != 0 || ldb % 8 != 0 ||
                   (G > 1 && strideB % 8 != 0)))
@@ -303,7 +308,7 @@ int gemm_grouped_wgrad(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, 
     if (C == nullptr || ldc < N) return SWG_ERR_INVALID_ARG;
     if (G > 1 && strideC < (K - 1) * ldc + N) return SWG_ERR_INVALID_ARG;
     if (M > 0 && (A == nullptr || D == nullptr || lda < K || ldd < N)) return SWG_ERR_INVALID_ARG;
-    if (too_big({M, N, K, lda, ldd, ldc})) return SWG_ERR_UNSUPPORTED;
+    if (too_big({M, N, K}, {lda, ldd, ldc})) return SWG_ERR_UNSUPPORTED;
     if (!aligned16(C) || (ldc * out_bytes) % 16 != 0 || (G > 1 && (strideC * out_bytes) % 16 != 0))
         return SWG_ERR_MISALIGNED;
     if (M > 0 && (!aligned16(A) || !aligned16(D) || lda % 8 != 0 || ldd % 8 != 0))
@@ -427,7 +432,7 @@ static int mx4_convert(int format, int64_t G, int64_t M, int64_t K, const void *
     if (X == nullptr || Q == nullptr || S == nullptr || ldx < K || ldq < ceil_to(K, 32) / 2)
         return SWG_ERR_INVALID_ARG;
     if (!(scale > 0.0f) || !std::isfinite(scale)) return SWG_ERR_INVALID_ARG;
-    if (too_big({M, K, ldx, ldq})) return SWG_ERR_UNSUPPORTED;
+    if (too_big({M, K}, {ldx, ldq})) return SWG_ERR_UNSUPPORTED;
     if (!aligned16(X) || !aligned16(Q) || !aligned16(S) || (ldx * bytes) % 16 != 0 || ldq % 16 != 0)
         return SWG_ERR_MISALIGNED;
     swg::Mx4Args p{};
@@ -474,7 +479,7 @@ int gemm_mx4(int format, int64_t G, int64_t M, int64_t N, int64_t K, float alpha
     if (C == nullptr || ldc < N) return SWG_ERR_INVALID_ARG;
     if (K > 0 && (!A || !SA || !B || !SB || lda < row || ldb < row)) return SWG_ERR_INVALID_ARG;
     if (K > 0 && G > 1 && strideB < (N - 1) * ldb + row) return SWG_ERR_INVALID_ARG;
-    if (too_big({M, N, K, lda, ldb, ldc})) return SWG_ERR_UNSUPPORTED;
+    if (too_big({M, N, K}, {lda, ldb, ldc})) return SWG_ERR_UNSUPPORTED;
     if (!aligned16(C) || (ldc * bytes) % 16 != 0) return SWG_ERR_MISALIGNED;
     if (K > 0 && (!aligned16(A) || !aligned16(SA) || !aligned16(B) || !aligned16(SB) ||
                   lda % 16 != 0 || ldb % 16 != 0 || (G > 1 && strideB % 16 != 0)))

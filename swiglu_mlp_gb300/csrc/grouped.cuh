@@ -240,13 +240,13 @@ __device__ __forceinline__ int tiles_of(int rows, int most)
 }
 
 // Rows of A covered by each tile of a group of `rows` (> 0) rows, but the
-// last, when tiles have at most `most` rows.
+// last, when tiles have at most `most` rows.  (rows + t - 1 may pass 2^31.)
 template <class C>
 __device__ __forceinline__ int tile_step(int rows, int most)
 {
     const int t = tiles_of<C>(rows, most);
     constexpr int UNIT = C::UNIT;
-    return ceil_div(fast_div(rows + t - 1, t), UNIT) * UNIT;
+    return ceil_div(fast_div(rows - 1, t) + 1, UNIT) * UNIT;
 }
 
 // The most rows of A that a tile should have, chosen so that the last wave of

@@ -153,3 +153,25 @@ def test_tensor_helpers_refuse():
     for f in bad:
         with pytest.raises(swg.SwgError):
             f()
+
+
+def test_sizes_that_round_up_past_32_bits(lib):
+    """Rows and columns are rounded up to whole tiles in 32 bits, so sizes end
+    1023 before 2^31."""
+    top = 2 ** 31 - 1023
+    ld = 2 ** 31 - 8                                   # strides may be larger
+    d = dict(t=0, G=1, M=128, N=64, K=72, alpha=1.0, A=P, lda=ld, B=P, ldb=ld, sB=0, off=P, beta=0.0, C=P,
+             ldc=ld, dt=1, D=P, ldd=ld, sC=0, fmt=0, X=P, ldx=ld, type=1, scale=1.0, Q=P, ldq=2 ** 31 - 16, S=P,
+             SA=P, SB=P, W=P, SW=P, Y=P, dY=P, dH=P)
+    for f, names, sizes in (
+            (lib.gemm_grouped, "t G M N K alpha A lda B ldb sB off beta C ldc dt", "MNK"),
+            (lib.gemm_grouped_wgrad, "G M N K alpha A lda D ldd off beta C ldc sC dt", "MNK"),
+            (lib.swiglu_grouped, "A W Y off G M N K", "MK"),
+            (lib.swiglu_grouped_grad, "A W dY Y dH off G M N K", "MK"),
+            (lib.mx4_quantize, "fmt G M K X ldx type scale off Q ldq S", "MK"),
+            (lib.mx4_dequantize, "fmt G M K Q ldq S scale off X ldx type", "MK"),
+            (lib.gemm_mx4, "fmt G M N K alpha A lda SA B ldb sB SB off beta C ldc type", "MNK"),
+            (lib.swiglu_mx4, "fmt A SA W SW Y off G M N K alpha", "MK")):
+        for name in sizes:
+            assert call(f, names, d, **{name: top}) == UNSUPPORTED, (f, name)
+    assert call(lib.swiglu_grouped, "A W Y off G M N K", d, N=(top + 7) // 2) == UNSUPPORTED

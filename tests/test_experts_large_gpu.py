@@ -142,3 +142,45 @@ def test_streams_and_threads(threads):
     for w, b in zip(want, bufs):
         for x, y in zip(w, b[:3]):
             assert torch.equal(x, y)
+
+
+# The last rows that 32 bits can number: 2^31 - 1024 of them, more than the
+# tiles of a group could be counted in when rows and tiles were added up.
+MOST = 2 ** 31 - 1024
+
+
+def _last_rows(x, rows):
+    g = synth.generator(77)
+    part = synth.normal((rows, x.shape[1]), g).cuda()
+    x[-rows:] = part
+    return part
+
+
+def test_grouped_product_of_the_most_rows():
+    A = torch.zeros((MOST, 8), dtype=torch.bfloat16, device="cuda")
+    last = _last_rows(A, 700)
+    B = synth.normal((2, 8, 8), synth.generator(78)).cuda()
+    C = torch.full((MOST, 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    swg.gemm_grouped_into(C, A, B, torch.tensor([0, 5, MOST], dtype=torch.int32).cuda())
+    assert swg.get_device_error() == 0
+    want = plain.f64(last) @ plain.f64(B[1])
+    tol = plain.fp32_sum_bound(8, np.abs(plain.f64(last)) @ np.abs(plain.f64(B[1]))) \
+        + plain.ROUND["bf16"] * np.abs(want)
+    assert (np.abs(plain.f64(C[-700:]) - want) <= tol).all()
+    for i in range(0, MOST - 700, 2 ** 28):
+        assert not C[i:min(i + 2 ** 28, MOST - 700)].any()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_conversion_of_the_most_rows(fmt):
+    X = torch.zeros((MOST, 8), dtype=torch.bfloat16, device="cuda")
+    last = _last_rows(X, 700)
+    off = torch.tensor([0, MOST - 100, MOST], dtype=torch.int32).cuda()
+    Q, S = swg.mx4_alloc(MOST, 8, FMT[fmt], groups=2)
+    swg.mx4_quantize_into(Q, S, X, FMT[fmt], offsets=off)
+    X.fill_(7.0)
+    swg.mx4_dequantize_into(X, Q, S, FMT[fmt], offsets=off)
+    assert swg.get_device_error() == 0
+    assert np.array_equal(plain.f64(X[-700:]), plain.quantised(plain.f64(last), fmt))
+    for i in range(0, MOST - 700, 2 ** 28):
+        assert not X[i:min(i + 2 ** 28, MOST - 700)].any()
