@@ -1438,7 +1438,7 @@ int swiglu_mlp(const void *A, const void *W_fused, void *Y, int64_t M, int64_t N
     if (M == 0 || N == 0) return SWG_OK;
     if (Y == nullptr || (K > 0 && (A == nullptr || W_fused == nullptr)))
         return SWG_ERR_INVALID_ARG;
-    if (M > kMaxDim || 2 * N > kMaxDim || K > kMaxDim) return SWG_ERR_UNSUPPORTED;
+    if (M > kMaxDim || N > kMaxDim / 2 || K > kMaxDim) return SWG_ERR_UNSUPPORTED;
     if (!aligned16(Y) || N % 8 != 0) return SWG_ERR_MISALIGNED;
     if (K > 0 && (!aligned16(A) || !aligned16(W_fused) || K % 8 != 0)) return SWG_ERR_MISALIGNED;
 
@@ -1571,7 +1571,7 @@ int swiglu_mlp_fp8(const void *A, const void *W_fused_t, void *Y, int64_t M, int
     if (M == 0 || N == 0) return SWG_OK;
     if (Y == nullptr || (K > 0 && (A == nullptr || W_fused_t == nullptr)))
         return SWG_ERR_INVALID_ARG;
-    if (M > kMaxDim || 2 * N > kMaxDim || K > kMaxDim) return SWG_ERR_UNSUPPORTED;
+    if (M > kMaxDim || N > kMaxDim / 2 || K > kMaxDim) return SWG_ERR_UNSUPPORTED;
     if (!aligned16(Y) || N % 8 != 0) return SWG_ERR_MISALIGNED;
     if (K > 0 && (!aligned16(A) || !aligned16(W_fused_t) || K % 16 != 0))
         return SWG_ERR_MISALIGNED;
@@ -1641,7 +1641,7 @@ int swiglu_mlp_dual(const void *A, const void *W1, const void *W2, void *Y, int6
     if (M == 0 || N == 0) return SWG_OK;
     if (Y == nullptr || (K > 0 && (A == nullptr || W1 == nullptr || W2 == nullptr)))
         return SWG_ERR_INVALID_ARG;
-    if (M > kMaxDim || 2 * N > kMaxDim || K > kMaxDim) return SWG_ERR_UNSUPPORTED;
+    if (M > kMaxDim || N > kMaxDim / 2 || K > kMaxDim) return SWG_ERR_UNSUPPORTED;
     if (!aligned16(Y) || N % 8 != 0) return SWG_ERR_MISALIGNED;
     if (K > 0 && (!aligned16(A) || !aligned16(W1) || !aligned16(W2) || K % 8 != 0))
         return SWG_ERR_MISALIGNED;
@@ -1721,7 +1721,7 @@ int swiglu_mlp_forward(const void *A, const void *W_fused, const void *W_down, v
     if (M == 0 || K == 0) return SWG_OK;          // Out is M x K
     if (Out == nullptr || A == nullptr || W_fused == nullptr) return SWG_ERR_INVALID_ARG;
     if (N > 0 && (Y == nullptr || W_down == nullptr)) return SWG_ERR_INVALID_ARG;
-    if (M > kMaxDim || 2 * N > kMaxDim || K > kMaxDim) return SWG_ERR_UNSUPPORTED;
+    if (M > kMaxDim || N > kMaxDim / 2 || K > kMaxDim) return SWG_ERR_UNSUPPORTED;
     if (!aligned16(Out) || !aligned16(A) || !aligned16(W_fused) || K % 8 != 0)
         return SWG_ERR_MISALIGNED;
     if (N > 0 && (!aligned16(Y) || !aligned16(W_down) || N % 8 != 0)) return SWG_ERR_MISALIGNED;
@@ -1738,7 +1738,7 @@ int swiglu_interleave(const void *W1, const void *W2, void *W_fused, int64_t K, 
     if (K < 0 || N < 0) return SWG_ERR_INVALID_ARG;
     if (K == 0 || N == 0) return SWG_OK;
     if (!W1 || !W2 || !W_fused) return SWG_ERR_INVALID_ARG;
-    if (K > kMaxDim || 2 * N > kMaxDim) return SWG_ERR_UNSUPPORTED;
+    if (K > kMaxDim || N > kMaxDim / 2) return SWG_ERR_UNSUPPORTED;
     if (!aligned16(W1) || !aligned16(W2) || !aligned16(W_fused) || N % 4 != 0)
         return SWG_ERR_MISALIGNED;
     DeviceState *d = nullptr;

@@ -271,8 +271,8 @@ int gemm_grouped(int transB, int64_t G, int64_t M, int64_t N, int64_t K, float a
     if (C == nullptr || ldc < N) return SWG_ERR_INVALID_ARG;
     if (K > 0 && (A == nullptr || B == nullptr || lda < K || ldb < b_cols))
         return SWG_ERR_INVALID_ARG;
-    if (K > 0 && G > 1 && strideB < (b_rows - 1) * ldb + b_cols) return SWG_ERR_INVALID_ARG;
     if (too_big({M, N, K}, {lda, ldb, ldc})) return SWG_ERR_UNSUPPORTED;
+    if (K > 0 && G > 1 && strideB < (b_rows - 1) * ldb + b_cols) return SWG_ERR_INVALID_ARG;
     if (!aligned16(C) || (ldc * out_bytes) % 16 != 0) return SWG_ERR_MISALIGNED;
     if (K > 0 && (!aligned16(A) || !aligned16(B) || lda % 8 != 0 || ldb % 8 != 0 ||
                   (G > 1 && strideB % 8 != 0)))
@@ -306,9 +306,9 @@ int gemm_grouped_wgrad(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, 
     if (int rc = check_groups(offsets, G)) return rc;
     if (N == 0 || K == 0 || G == 0) return SWG_OK;
     if (C == nullptr || ldc < N) return SWG_ERR_INVALID_ARG;
-    if (G > 1 && strideC < (K - 1) * ldc + N) return SWG_ERR_INVALID_ARG;
     if (M > 0 && (A == nullptr || D == nullptr || lda < K || ldd < N)) return SWG_ERR_INVALID_ARG;
     if (too_big({M, N, K}, {lda, ldd, ldc})) return SWG_ERR_UNSUPPORTED;
+    if (G > 1 && strideC < (K - 1) * ldc + N) return SWG_ERR_INVALID_ARG;
     if (!aligned16(C) || (ldc * out_bytes) % 16 != 0 || (G > 1 && (strideC * out_bytes) % 16 != 0))
         return SWG_ERR_MISALIGNED;
     if (M > 0 && (!aligned16(A) || !aligned16(D) || lda % 8 != 0 || ldd % 8 != 0))
@@ -378,7 +378,7 @@ static int swiglu_grouped_impl(const void *A, const void *W, const void *dY, voi
     if (M == 0 || N == 0 || G == 0) return SWG_OK;
     if (grad ? dY == nullptr || dH == nullptr : Y == nullptr) return SWG_ERR_INVALID_ARG;
     if (K > 0 && (A == nullptr || W == nullptr)) return SWG_ERR_INVALID_ARG;
-    if (too_big({M, 2 * N, K})) return SWG_ERR_UNSUPPORTED;
+    if (too_big({M, N, K}) || too_big({2 * N})) return SWG_ERR_UNSUPPORTED;
     if (!aligned16(Y) || !aligned16(dY) || !aligned16(dH) || N % 8 != 0) return SWG_ERR_MISALIGNED;
     if (K > 0 && (!aligned16(A) || !aligned16(W) || K % 8 != 0)) return SWG_ERR_MISALIGNED;
     swg::GrpArgs p{};
@@ -429,10 +429,10 @@ static int mx4_convert(int format, int64_t G, int64_t M, int64_t K, const void *
     if (M < 0 || K < 0) return SWG_ERR_INVALID_ARG;
     if (int rc = check_groups(offsets, G)) return rc;
     if (M == 0 || K == 0 || G == 0) return SWG_OK;
-    if (X == nullptr || Q == nullptr || S == nullptr || ldx < K || ldq < ceil_to(K, 32) / 2)
-        return SWG_ERR_INVALID_ARG;
+    if (X == nullptr || Q == nullptr || S == nullptr || ldx < K) return SWG_ERR_INVALID_ARG;
     if (!(scale > 0.0f) || !std::isfinite(scale)) return SWG_ERR_INVALID_ARG;
     if (too_big({M, K}, {ldx, ldq})) return SWG_ERR_UNSUPPORTED;
+    if (ldq < ceil_to(K, 32) / 2) return SWG_ERR_INVALID_ARG;
     if (!aligned16(X) || !aligned16(Q) || !aligned16(S) || (ldx * bytes) % 16 != 0 || ldq % 16 != 0)
         return SWG_ERR_MISALIGNED;
     swg::Mx4Args p{};
@@ -475,11 +475,12 @@ int gemm_mx4(int format, int64_t G, int64_t M, int64_t N, int64_t K, float alpha
     if (M < 0 || N < 0 || K < 0) return SWG_ERR_INVALID_ARG;
     if (int rc = check_groups(offsets, G)) return rc;
     if (M == 0 || N == 0 || G == 0) return SWG_OK;
-    const int64_t row = ceil_to(K, 32) / 2;
     if (C == nullptr || ldc < N) return SWG_ERR_INVALID_ARG;
-    if (K > 0 && (!A || !SA || !B || !SB || lda < row || ldb < row)) return SWG_ERR_INVALID_ARG;
-    if (K > 0 && G > 1 && strideB < (N - 1) * ldb + row) return SWG_ERR_INVALID_ARG;
+    if (K > 0 && (!A || !SA || !B || !SB)) return SWG_ERR_INVALID_ARG;
     if (too_big({M, N, K}, {lda, ldb, ldc})) return SWG_ERR_UNSUPPORTED;
+    const int64_t row = ceil_to(K, 32) / 2;
+    if (K > 0 && (lda < row || ldb < row)) return SWG_ERR_INVALID_ARG;
+    if (K > 0 && G > 1 && strideB < (N - 1) * ldb + row) return SWG_ERR_INVALID_ARG;
     if (!aligned16(C) || (ldc * bytes) % 16 != 0) return SWG_ERR_MISALIGNED;
     if (K > 0 && (!aligned16(A) || !aligned16(SA) || !aligned16(B) || !aligned16(SB) ||
                   lda % 16 != 0 || ldb % 16 != 0 || (G > 1 && strideB % 16 != 0)))
@@ -514,7 +515,7 @@ int swiglu_mx4(int format, const void *A, const void *SA, const void *W, const v
     if (int rc = check_groups(offsets, G)) return rc;
     if (M == 0 || N == 0 || G == 0) return SWG_OK;
     if (Y == nullptr || (K > 0 && (!A || !SA || !W || !SW))) return SWG_ERR_INVALID_ARG;
-    if (too_big({M, 2 * N, K})) return SWG_ERR_UNSUPPORTED;
+    if (too_big({M, N, K}) || too_big({2 * N})) return SWG_ERR_UNSUPPORTED;
     if (!aligned16(Y) || N % 8 != 0) return SWG_ERR_MISALIGNED;
     if (K > 0 && (!aligned16(A) || !aligned16(SA) || !aligned16(W) || !aligned16(SW)))
         return SWG_ERR_MISALIGNED;

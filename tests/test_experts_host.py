@@ -175,3 +175,28 @@ def test_sizes_that_round_up_past_32_bits(lib):
         for name in sizes:
             assert call(f, names, d, **{name: top}) == UNSUPPORTED, (f, name)
     assert call(lib.swiglu_grouped, "A W Y off G M N K", d, N=(top + 7) // 2) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("extra", [8, 64])
+def test_sizes_whose_products_pass_64_bits(lib, extra):
+    """2N of a SwiGLU, or a group stride, may pass 2^63: refused all the same."""
+    big = 2 ** 62 + extra
+    d = dict(A=P, W=P, Y=P, dY=P, dH=P, SA=P, SW=P, off=P, G=2, M=128, N=big, K=72, fmt=0, alpha=1.0)
+    assert call(lib.swiglu_grouped, "A W Y off G M N K", d) == UNSUPPORTED
+    assert call(lib.swiglu_grouped_grad, "A W dY Y dH off G M N K", d) == UNSUPPORTED
+    assert call(lib.swiglu_mx4, "fmt A SA W SW Y off G M N K alpha", d) == UNSUPPORTED
+    d = dict(t=0, G=2, M=128, N=64, K=big, alpha=1.0, A=P, lda=big, B=P, ldb=64, sB=2 ** 62, off=P, beta=0.0,
+             C=P, ldc=64, dt=1, D=P, ldd=64, sC=2 ** 62, fmt=0, SA=P, SB=P, type=1)
+    assert call(lib.gemm_grouped, "t G M N K alpha A lda B ldb sB off beta C ldc dt", d) == UNSUPPORTED
+    assert call(lib.gemm_grouped_wgrad, "G M N K alpha A lda D ldd off beta C ldc sC dt", d) == UNSUPPORTED
+    assert call(lib.gemm_mx4, "fmt G M N K alpha A lda SA B ldb sB SB off beta C ldc type", d) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("extra", [8, 64])
+def test_dense_swiglu_widths_that_pass_64_bits(lib, extra):
+    big = 2 ** 62 + extra
+    assert lib.swiglu_mlp(P, P, P, 128, big, 72, None) == UNSUPPORTED
+    assert lib.swiglu_mlp_fp8(P, P, P, 128, big, 128, 1.0, None) == UNSUPPORTED
+    assert lib.swiglu_mlp_dual(P, P, P, P, 128, big, 72, None) == UNSUPPORTED
+    assert lib.swiglu_mlp_forward(P, P, P, P, P, 128, big, 72, 0.0, None) == UNSUPPORTED
+    assert lib.swiglu_interleave(P, P, P, 72, big, None) == UNSUPPORTED
