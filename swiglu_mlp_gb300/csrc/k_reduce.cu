@@ -23,8 +23,12 @@ __global__ void __launch_bounds__(THREADS) reduce_kernel(const ReduceArgs p)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int begin = 0, end = p.rows;
     if (p.groups.offsets != nullptr) {
+        // the rows of the groups as the products clamp them (groups.cuh): from
+        // the first offset to the largest
+        int top = 0;
+        for (int i = threadIdx.x & 31; i <= p.groups.G; i += 32) top = max(top, p.groups.offsets[i]);
         begin = max(p.groups.offsets[0], 0);
-        end = min(p.groups.offsets[p.groups.G], p.groups.M);
+        end = min(__reduce_max_sync(0xffffffffu, top), p.groups.M);
     }
     const int per_row = (p.N + COLS - 1) / COLS;
     const long long total = (long long)p.rows * per_row;

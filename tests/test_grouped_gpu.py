@@ -474,3 +474,31 @@ def test_sixteen_ranges(rows):
 
 def test_wgrad_sixteen_ranges():
     run_wgrad([20011], 72, 136, ("f16", "f32"))
+
+
+@pytest.mark.parametrize("off", [[0, 50, 30], [20, 70, 41, 3], [-5, 30, 12, 50, 49]])
+def test_bad_offsets_of_long_contractions(off):
+    """Cut into ranges of K or not, what runs is the groups that the clamping
+    leaves: up to the largest offset, not to the last."""
+    M, N, K, G = 50, 72, 4096, len(off) - 1
+    off = np.array(off)
+    clamped = np.maximum.accumulate(np.clip(off, 0, M))
+    g = synth.generator(G)
+    A, B = padded(M, K, g, torch.bfloat16), padded(G * K, N, g, torch.bfloat16, K ** -0.5).unflatten(0, (G, K))
+    C0 = synth.normal((M, N), g)
+    C = Guarded(M, N, torch.bfloat16, init=C0)
+    o = torch.from_numpy(off.astype(np.int32)).cuda()
+    before = swg.launch_count()
+    swg.gemm_grouped_into(C.view, A, B, o)
+    assert swg.launch_count() == before + 2              # a product and a sum
+    assert swg.get_device_error() == 1
+    want, tol = plain.product(plain.f64(A), plain.f64(B), clamped, 0, 1.0, 0.0, plain.f64(C0), "bf16")
+    check(C.cpu("clamped groups"), want, tol, f"clamped groups {off}")
+    Y = torch.full((M, N // 2 // 8 * 8), 9.0, dtype=torch.bfloat16, device="cuda")
+    W = B[:, :, :2 * Y.shape[1]].contiguous()
+    swg.swiglu_grouped_into(Y, A.contiguous(), W, o)
+    assert swg.get_device_error() == 1
+    want, tol = plain.swiglu(plain.f64(A), plain.f64(W), clamped)
+    rows = slice(clamped[0], clamped[-1])
+    check(Y.cpu()[rows], want[rows], tol[rows], f"clamped groups {off}")
+    assert (Y[:clamped[0]] == 9.0).all() and (Y[clamped[-1]:] == 9.0).all()
