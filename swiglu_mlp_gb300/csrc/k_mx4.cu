@@ -443,8 +443,12 @@ cudaError_t launch(const Mx4Args &p, bool back, int *err, cudaStream_t s)
 {
     const int cols = back ? TILE_COLS_BACK : TILE_COLS, G = p.groups.G, M = p.groups.M;
     const int chunks = (p.K + cols - 1) / cols;
-    // upper bounds of the units over all groups
-    const long long units = FEW ? M / ROWS + std::min(G, M) : (M / TILE_ROWS + std::min(G, M)) * 32ll;
+    // Upper bounds of the units over all groups, and with offsets one more, whose
+    // warps find nothing: on the way they look at every offset, also at those
+    // behind the last row, and report what they have to clamp.
+    const int more = p.groups.offsets != nullptr;
+    const long long units = FEW ? M / ROWS + std::min(G, M) + more
+                                : (M / TILE_ROWS + std::min(G, M) + more) * 32ll;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((units * chunks + THREADS / 32 - 1) / (THREADS / 32)));
     cfg.blockDim = dim3(THREADS);

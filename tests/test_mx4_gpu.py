@@ -321,3 +321,18 @@ def test_bad_offsets_of_a_conversion(fmt, G, M):
     want_q, want_s = plain.pack(np.copysign(v, x64), fmt, plain.block_scales(x64, fmt), rows)
     assert np.array_equal(q.cpu().numpy(), want_q)
     assert np.array_equal(s.cpu().numpy()[:want_s.size], want_s)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("M,G,K", [(20, 64, 200), (3, 300, 8192)])
+def test_bad_offsets_behind_the_rows(fmt, M, G, K):
+    """An offset out of order among the empty groups behind all rows is reported too."""
+    off = np.minimum(np.arange(G + 1), M)
+    off[G * 2 // 3] = 1
+    x = outliers(M, K, synth.generator(M), torch.bfloat16).cuda()
+    o = torch.from_numpy(off.astype(np.int32)).cuda()
+    q, s = swg.mx4_alloc(M, K, FMT[fmt], groups=G)
+    swg.mx4_quantize_into(q, s, x, FMT[fmt], offsets=o)
+    assert swg.get_device_error() == 1
+    swg.mx4_dequantize_into(x, q, s, FMT[fmt], offsets=o)
+    assert swg.get_device_error() == 1
