@@ -658,7 +658,7 @@ def swiglu_mx4_into(Y, Q, S, W, SW, K, format, alpha=1.0, offsets=None, stream=N
     lda = _mx4_rows(w, Q, S, format, G, M, K, torch)
     N2, ldb, stride = _mx4_weights(w, W, SW, format, G, K, torch)
     row = -(-K // 32) * 16
-    if N2 % 2 or (lda != row and M > 1) or ldb != row or (stride != N2 * row and G > 1):
+    if N2 % 2 or K > 0 and ((lda != row and M > 1) or ldb != row or (stride != N2 * row and G > 1)):
         _refuse(w, "Q and W must be contiguous rows of 16 * ceil(K / 32) bytes, W of 2N of them")
     _output(w, "Y", Y, M, N2 // 2, torch.bfloat16)
     rc = lib.swiglu_mx4(format, Q.data_ptr(), S.data_ptr(), W.data_ptr(), SW.data_ptr(),

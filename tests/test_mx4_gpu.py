@@ -336,3 +336,19 @@ def test_bad_offsets_behind_the_rows(fmt, M, G, K):
     assert swg.get_device_error() == 1
     swg.mx4_dequantize_into(x, q, s, FMT[fmt], offsets=o)
     assert swg.get_device_error() == 1
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("rows", [[1], [5, 0, 3]])
+def test_products_over_no_columns(fmt, rows):
+    M, G, N = sum(rows), len(rows), 16
+    off = torch.from_numpy(offsets_of(rows)).cuda()
+    q, s = swg.mx4_alloc(M, 0, FMT[fmt], groups=G)
+    w, sw = swg.mx4_alloc(G * 2 * N, 0, FMT[fmt], groups=G)
+    swg.mx4_quantize_into(q, s, torch.empty((M, 0), dtype=torch.bfloat16, device="cuda"), FMT[fmt], offsets=off)
+    Y = torch.full((M, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    swg.swiglu_mx4_into(Y, q, s, w.view(G, 2 * N, 0), sw, 0, FMT[fmt], offsets=off)
+    assert not Y.any()
+    C = torch.full((M, 2 * N), 9.0, dtype=torch.bfloat16, device="cuda")
+    swg.gemm_mx4_into(C, q, s, w.view(G, 2 * N, 0), sw, 0, FMT[fmt], beta=0.5, offsets=off)
+    assert (C == 4.5).all() and swg.get_device_error() == 0
