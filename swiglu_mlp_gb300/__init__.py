@@ -430,15 +430,30 @@ def _refuse(where, why, status=1):
     raise SwgError(status, f"{where}: {why}")
 
 
+def _place(stream):
+    """The handle of the call's stream, and the device that its tensors have to
+    be on: the current one (-2, that of no tensor, without CUDA)."""
+    if _device is None:
+        _current_stream()
+    dev = _device() if _device is not None else -2
+    return (_raw_stream(dev) if stream is None and dev >= 0 else _stream(stream)), dev
+
+
+def _failed(rc, where, name):
+    if rc < 0:            # the binding's: nothing was called
+        _refuse(where, "every tensor must be on the current CUDA device")
+    _check(rc, name)
+
+
 def _groups(offsets, where):
-    """(device pointer or None, G) of an int32 offsets tensor, or of none."""
+    """G of an int32 offsets tensor, or of none."""
     if offsets is None:
-        return None, 1
-    n = offsets.numel()
-    if n < 1 or offsets.dtype is not _torch.int32 or offsets.dim() != 1 \
+        return 1
+    shape = offsets.shape
+    if len(shape) != 1 or shape[0] < 1 or offsets.dtype is not _torch.int32 \
             or not offsets.is_contiguous():
         _refuse(where, "offsets must be a contiguous 1-D int32 tensor of G + 1 values")
-    return offsets.data_ptr(), n - 1
+    return shape[0] - 1
 
 
 def _matrices(t, name, where, G):
@@ -459,11 +474,13 @@ def _matrices(t, name, where, G):
 
 def _matrix(t, name, where):
     """(rows, columns, row stride) of a 2-D row-major tensor."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or stride[1] != 1:
+    try:
+        (rows, cols), (ld, unit) = t.shape, t.stride()
+    except ValueError:
+        unit = 0
+    if unit != 1:
         _refuse(where, f"{name} must be a 2-D row-major tensor (unit column stride)")
-    rows, cols = shape
-    return rows, cols, stride[0]
+    return rows, cols, ld
 
 
 def _type_code(dtype, where) -> int:
@@ -489,18 +506,18 @@ def gemm_grouped_into(C, A, B, offsets, transB=0, alpha=1.0, beta=0.0, stream=No
     w = "gemm_grouped_into"
     _torch or _fast()
     lib = _bound
-    off, G = _groups(offsets, w)
+    G = _groups(offsets, w)
     rows, cols, ldb, stride = _matrices(B, "B", w, G)
     N, Kb = (rows, cols) if transB else (cols, rows)
     M, K, lda = _matrix(A, "A", w)
     Mc, Nc, ldc = _matrix(C, "C", w)
     if Kb != K or Mc != M or Nc != N or A.dtype is not B.dtype:
         _refuse(w, "inconsistent shapes or dtypes")
-    rc = lib.gemm_grouped(int(transB), G, M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(), ldb,
-                          stride, off, beta, C.data_ptr(), ldc, _dtype_code(A.dtype, C.dtype),
-                          _stream(stream))
+    s, dev = _place(stream)
+    rc = lib.gemm_grouped(int(transB), G, M, N, K, alpha, A, lda, B, ldb, stride, offsets, beta, C,
+                          ldc, _dtype_code(A.dtype, C.dtype), s, dev)
     if rc:
-        _check(rc, "gemm_grouped")
+        _failed(rc, w, "gemm_grouped")
     return C
 
 
@@ -509,17 +526,17 @@ def gemm_grouped_wgrad_into(C, A, D, offsets, alpha=1.0, beta=0.0, stream=None):
     w = "gemm_grouped_wgrad_into"
     _torch or _fast()
     lib = _bound
-    off, G = _groups(offsets, w)
+    G = _groups(offsets, w)
     rows, cols, ldc, stride = _matrices(C, "C", w, G)
     M, K, lda = _matrix(A, "A", w)
     Md, N, ldd = _matrix(D, "D", w)
     if Md != M or rows != K or cols != N or A.dtype is not D.dtype:
         _refuse(w, "inconsistent shapes or dtypes")
-    rc = lib.gemm_grouped_wgrad(G, M, N, K, alpha, A.data_ptr(), lda, D.data_ptr(), ldd, off, beta,
-                                C.data_ptr(), ldc, stride, _dtype_code(A.dtype, C.dtype),
-                                _stream(stream))
+    s, dev = _place(stream)
+    rc = lib.gemm_grouped_wgrad(G, M, N, K, alpha, A, lda, D, ldd, offsets, beta, C, ldc, stride,
+                                _dtype_code(A.dtype, C.dtype), s, dev)
     if rc:
-        _check(rc, "gemm_grouped_wgrad")
+        _failed(rc, w, "gemm_grouped_wgrad")
     return C
 
 
@@ -537,13 +554,13 @@ def swiglu_grouped_into(Y, A, W_fused, offsets, stream=None):
     w = "swiglu_grouped_into"
     torch = _torch or _fast()
     lib = _bound
-    off, G = _groups(offsets, w)
+    G = _groups(offsets, w)
     M, N, K = _swiglu_shapes(w, A, W_fused, G, torch.bfloat16)
     _output(w, "Y", Y, M, N, torch.bfloat16)
-    rc = lib.swiglu_grouped(A.data_ptr(), W_fused.data_ptr(), Y.data_ptr(), off, G, M, N, K,
-                            _stream(stream))
+    s, dev = _place(stream)
+    rc = lib.swiglu_grouped(A, W_fused, Y, offsets, G, M, N, K, s, dev)
     if rc:
-        _check(rc, "swiglu_grouped")
+        _failed(rc, w, "swiglu_grouped")
     return Y
 
 
@@ -553,16 +570,16 @@ def swiglu_grouped_grad_into(dH, A, W_fused, dY, offsets, Y=None, stream=None):
     w = "swiglu_grouped_grad_into"
     torch = _torch or _fast()
     lib = _bound
-    off, G = _groups(offsets, w)
+    G = _groups(offsets, w)
     M, N, K = _swiglu_shapes(w, A, W_fused, G, torch.bfloat16)
     _output(w, "dH", dH, M, 2 * N, torch.bfloat16)
     _output(w, "dY", dY, M, N, torch.bfloat16)
     if Y is not None:
         _output(w, "Y", Y, M, N, torch.bfloat16)
-    rc = lib.swiglu_grouped_grad(A.data_ptr(), W_fused.data_ptr(), dY.data_ptr(), _ptr(Y),
-                                 dH.data_ptr(), off, G, M, N, K, _stream(stream))
+    s, dev = _place(stream)
+    rc = lib.swiglu_grouped_grad(A, W_fused, dY, Y, dH, offsets, G, M, N, K, s, dev)
     if rc:
-        _check(rc, "swiglu_grouped_grad")
+        _failed(rc, w, "swiglu_grouped_grad")
     return dH
 
 
@@ -590,13 +607,14 @@ def mx4_quantize_into(Q, S, X, format, scale=1.0, offsets=None, stream=None):
     w = "mx4_quantize_into"
     torch = _torch or _fast()
     lib = _bound
-    off, G = _groups(offsets, w)
+    G = _groups(offsets, w)
     M, K, ldx = _matrix(X, "X", w)
     ldq = _mx4_rows(w, Q, S, format, G, M, K, torch)
-    rc = lib.mx4_quantize(format, G, M, K, X.data_ptr(), ldx, _type_code(X.dtype, w), scale, off,
-                          Q.data_ptr(), ldq, S.data_ptr(), _stream(stream))
+    s, dev = _place(stream)
+    rc = lib.mx4_quantize(format, G, M, K, X, ldx, _type_code(X.dtype, w), scale, offsets, Q, ldq,
+                          S, s, dev)
     if rc:
-        _check(rc, "mx4_quantize")
+        _failed(rc, w, "mx4_quantize")
     return Q, S
 
 
@@ -605,13 +623,14 @@ def mx4_dequantize_into(X, Q, S, format, scale=1.0, offsets=None, stream=None):
     w = "mx4_dequantize_into"
     torch = _torch or _fast()
     lib = _bound
-    off, G = _groups(offsets, w)
+    G = _groups(offsets, w)
     M, K, ldx = _matrix(X, "X", w)
     ldq = _mx4_rows(w, Q, S, format, G, M, K, torch)
-    rc = lib.mx4_dequantize(format, G, M, K, Q.data_ptr(), ldq, S.data_ptr(), scale, off,
-                            X.data_ptr(), ldx, _type_code(X.dtype, w), _stream(stream))
+    s, dev = _place(stream)
+    rc = lib.mx4_dequantize(format, G, M, K, Q, ldq, S, scale, offsets, X, ldx,
+                            _type_code(X.dtype, w), s, dev)
     if rc:
-        _check(rc, "mx4_dequantize")
+        _failed(rc, w, "mx4_dequantize")
     return X
 
 
@@ -633,17 +652,17 @@ def gemm_mx4_into(C, Q, S, W, SW, K, format, alpha=1.0, beta=0.0, offsets=None, 
     w = "gemm_mx4_into"
     torch = _torch or _fast()
     lib = _bound
-    off, G = _groups(offsets, w)
+    G = _groups(offsets, w)
     M, Nc, ldc = _matrix(C, "C", w)
     lda = _mx4_rows(w, Q, S, format, G, M, K, torch)
     N, ldb, stride = _mx4_weights(w, W, SW, format, G, K, torch)
     if Nc != N:
         _refuse(w, "inconsistent shapes")
-    rc = lib.gemm_mx4(format, G, M, N, K, alpha, Q.data_ptr(), lda, S.data_ptr(), W.data_ptr(),
-                      ldb, stride, SW.data_ptr(), off, beta, C.data_ptr(), ldc,
-                      _type_code(C.dtype, w), _stream(stream))
+    s, dev = _place(stream)
+    rc = lib.gemm_mx4(format, G, M, N, K, alpha, Q, lda, S, W, ldb, stride, SW, offsets, beta, C,
+                      ldc, _type_code(C.dtype, w), s, dev)
     if rc:
-        _check(rc, "gemm_mx4")
+        _failed(rc, w, "gemm_mx4")
     return C
 
 
@@ -653,7 +672,7 @@ def swiglu_mx4_into(Y, Q, S, W, SW, K, format, alpha=1.0, offsets=None, stream=N
     w = "swiglu_mx4_into"
     torch = _torch or _fast()
     lib = _bound
-    off, G = _groups(offsets, w)
+    G = _groups(offsets, w)
     M = Q.shape[0]
     lda = _mx4_rows(w, Q, S, format, G, M, K, torch)
     N2, ldb, stride = _mx4_weights(w, W, SW, format, G, K, torch)
@@ -661,8 +680,8 @@ def swiglu_mx4_into(Y, Q, S, W, SW, K, format, alpha=1.0, offsets=None, stream=N
     if N2 % 2 or K > 0 and ((lda != row and M > 1) or ldb != row or (stride != N2 * row and G > 1)):
         _refuse(w, "Q and W must be contiguous rows of 16 * ceil(K / 32) bytes, W of 2N of them")
     _output(w, "Y", Y, M, N2 // 2, torch.bfloat16)
-    rc = lib.swiglu_mx4(format, Q.data_ptr(), S.data_ptr(), W.data_ptr(), SW.data_ptr(),
-                        Y.data_ptr(), off, G, M, N2 // 2, K, alpha, _stream(stream))
+    s, dev = _place(stream)
+    rc = lib.swiglu_mx4(format, Q, S, W, SW, Y, offsets, G, M, N2 // 2, K, alpha, s, dev)
     if rc:
-        _check(rc, "swiglu_mx4")
+        _failed(rc, w, "swiglu_mx4")
     return Y

@@ -3,33 +3,55 @@
  * The operators take a few microseconds on the GPU and up to nineteen
  * arguments; converting those through ctypes takes 1.7 us a call, through
  * this module 0.3.  Arguments are marshalled and nothing else: pointers come
- * as ints (None is NULL), the result is the status.  The interpreter lock is
+ * as tensors, ints or None (NULL), the result is the status.  The last argument
+ * is the device whose memory the call works on: where a tensor is on another,
+ * or on the host, the C function is not called and the result is -1.  (The
+ * check takes 0.1 to 0.2 us of a call's 3.8 to 5.6.)  The interpreter lock is
  * released around the call, as ctypes does. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include "swiglu_mlp.h"
 
-static void *pointer(PyObject *o) { return o == Py_None ? NULL : PyLong_AsVoidPtr(o); }
+static PyObject *get_device, *data_ptr;       /* names of a tensor's methods */
+
+static void *pointer(PyObject *o, long device, int *elsewhere)
+{
+    if (o == Py_None) return NULL;
+    if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) return NULL;         /* an argument before this one */
+    PyObject *on = PyObject_CallMethodObjArgs(o, get_device, NULL);
+    if (on == NULL) return NULL;
+    if (PyLong_AsLong(on) != device) *elsewhere = 1;
+    Py_DECREF(on);
+    PyObject *at = PyObject_CallMethodObjArgs(o, data_ptr, NULL);
+    if (at == NULL) return NULL;
+    void *p = PyLong_AsVoidPtr(at);
+    Py_DECREF(at);
+    return p;
+}
 static int64_t whole(PyObject *o) { return PyLong_AsLongLong(o); }
 static float real(PyObject *o) { return (float)PyFloat_AsDouble(o); }
 
-#define P(i) pointer(a[i])
+#define P(i) pointer(a[i], device, &elsewhere)
 #define I(i) whole(a[i])
 #define F(i) real(a[i])
 
-/* A Python function `name` of `count` arguments: ENTRY, their conversion into
- * locals, then CALL of the C function with those. */
+/* A Python function `name` of `count` arguments and the device: ENTRY, their
+ * conversion into locals, then CALL of the C function with those. */
 #define ENTRY(name, count)                                                                       \
     static PyObject *py_##name(PyObject *self, PyObject *const *a, Py_ssize_t n)                 \
     {                                                                                            \
         (void)self;                                                                              \
-        if (n != count) {                                                                        \
-            PyErr_SetString(PyExc_TypeError, #name " takes " #count " arguments");               \
+        if (n != count + 1) {                                                                    \
+            PyErr_SetString(PyExc_TypeError, #name " takes " #count " arguments and the device"); \
             return NULL;                                                                         \
-        }
+        }                                                                                        \
+        const long device = PyLong_AsLong(a[count]);                                             \
+        int elsewhere = 0;
 #define CALL(...)                                                                                \
         if (PyErr_Occurred()) return NULL;                                                       \
+        if (elsewhere) return PyLong_FromLong(-1);                                               \
         int rc;                                                                                  \
         Py_BEGIN_ALLOW_THREADS;                                                                  \
         rc = __VA_ARGS__;                                                                        \
@@ -94,4 +116,9 @@ static PyMethodDef methods[] = {
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};
 
-PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding(void)
+{
+    get_device = PyUnicode_InternFromString("get_device");
+    data_ptr = PyUnicode_InternFromString("data_ptr");
+    return get_device != NULL && data_ptr != NULL ? PyModule_Create(&module) : NULL;
+}

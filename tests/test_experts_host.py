@@ -200,3 +200,30 @@ def test_dense_swiglu_widths_that_pass_64_bits(lib, extra):
     assert lib.swiglu_mlp_dual(P, P, P, P, 128, big, 72, None) == UNSUPPORTED
     assert lib.swiglu_mlp_forward(P, P, P, P, P, 128, big, 72, 0.0, None) == UNSUPPORTED
     assert lib.swiglu_interleave(P, P, P, 72, big, None) == UNSUPPORTED
+
+
+def expert_calls():
+    """Each *_into helper with arguments that fit, as (function, tensors, the rest)."""
+    off = torch.tensor([0, 3, 8], dtype=torch.int32)
+    z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t)  # noqa: E731
+    q, s = z(8, 16, t=torch.uint8), z(1024, t=torch.uint8)
+    w, sw = z(2, 32, 16, t=torch.uint8), z(1024, t=torch.uint8)
+    return [
+        (swg.gemm_grouped_into, dict(C=z(8, 24), A=z(8, 16), B=z(2, 16, 24), offsets=off), {}),
+        (swg.gemm_grouped_wgrad_into, dict(C=z(2, 16, 24), A=z(8, 16), D=z(8, 24), offsets=off), {}),
+        (swg.swiglu_grouped_into, dict(Y=z(8, 16), A=z(8, 16), W_fused=z(2, 16, 32), offsets=off), {}),
+        (swg.swiglu_grouped_grad_into, dict(dH=z(8, 32), A=z(8, 16), W_fused=z(2, 16, 32), dY=z(8, 16),
+                                            offsets=off, Y=z(8, 16)), {}),
+        (swg.mx4_quantize_into, dict(Q=q, S=s, X=z(8, 32), offsets=off), dict(format=swg.MXFP4)),
+        (swg.mx4_dequantize_into, dict(Q=q, S=s, X=z(8, 32), offsets=off), dict(format=swg.MXFP4)),
+        (swg.gemm_mx4_into, dict(C=z(8, 32), Q=q, S=s, W=w, SW=sw, offsets=off), dict(K=32, format=swg.MXFP4)),
+        (swg.swiglu_mx4_into, dict(Y=z(8, 16), Q=q, S=s, W=w, SW=sw, offsets=off), dict(K=32, format=swg.MXFP4)),
+    ]
+
+
+@pytest.mark.parametrize("i", range(8))
+def test_tensors_on_the_host_are_refused(i):
+    f, tensors, rest = expert_calls()[i]
+    with pytest.raises(swg.SwgError, match="current CUDA device") as e:
+        f(**tensors, **rest)
+    assert e.value.status == INVALID

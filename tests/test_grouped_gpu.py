@@ -9,6 +9,7 @@ import experts_plain as plain
 import swiglu_mlp_gb300 as swg
 import synth
 from helpers import Guarded
+from test_experts_host import expert_calls
 
 pytestmark = pytest.mark.gpu
 
@@ -502,3 +503,16 @@ def test_bad_offsets_of_long_contractions(off):
     rows = slice(clamped[0], clamped[-1])
     check(Y.cpu()[rows], want[rows], tol[rows], f"clamped groups {off}")
     assert (Y[:clamped[0]] == 9.0).all() and (Y[clamped[-1]:] == 9.0).all()
+
+
+@pytest.mark.parametrize("i", range(8))
+def test_each_tensor_has_to_be_on_the_gpu(i):
+    f, tensors, rest = expert_calls()[i]
+    there = {n: t.cuda() for n, t in tensors.items()}
+    f(**there, **rest)
+    assert swg.get_device_error() == 0
+    before = swg.launch_count()
+    for n, t in tensors.items():
+        with pytest.raises(swg.SwgError, match="current CUDA device"):
+            f(**dict(there, **{n: t}), **rest)
+    assert swg.launch_count() == before
