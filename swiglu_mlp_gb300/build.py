@@ -3,7 +3,9 @@
 Each translation unit is compiled in parallel to ``_build/*.o`` and the objects
 are linked into one shared library (CUDA runtime linked statically).  Objects
 are rebuilt only when a source or header is newer than them.  The CPython module
-``_binding`` (plain C, gcc) is linked against that library beside it.
+``_binding`` (plain C, gcc) is linked against that library beside it, after it:
+the library's C users need no Python headers.  It keeps to the stable ABI of
+CPython 3.10, so that any later interpreter may load it.
 """
 from __future__ import annotations
 
@@ -18,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libswiglu_mlp.so")
-BINDING = os.path.join(HERE, "_binding.so")
+BINDING = os.path.join(HERE, "_binding.abi3.so")
 SOURCES = ["api.cu", "api_experts.cu", "k_grouped.cu", "k_grouped_mx4.cu", "k_wgrad.cu", "k_mx4.cu", "k_reduce.cu", "k_store.cu", "k_swiglu.cu", "k_splitk.cu", "k_fp8.cu", "k_gemv.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -62,7 +64,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed ({' '.join(cmd)}):\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({' '.join(cmd)}):\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr, flush=True)
 
@@ -76,7 +78,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     src = os.path.join(CSRC, "binding.c")
     if force or _stale(BINDING, [src] + hdrs):
         tmp = BINDING + f".tmp{os.getpid()}"
-        run(["gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", INCLUDE,
+        run(["gcc", "-O2", "-shared", "-fPIC", "-Wall", "-DPy_LIMITED_API=0x030A0000", "-I", INCLUDE,
              "-I", sysconfig.get_paths()["include"], src, "-o", tmp,
              "-L", HERE, "-lswiglu_mlp", "-Wl,-rpath,$ORIGIN"])
         os.replace(tmp, BINDING)

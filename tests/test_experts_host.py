@@ -1,5 +1,8 @@
 """Refusals of the expert-MLP entry points: every bad argument is answered
 before any CUDA call, so these run without a GPU."""
+import os
+import subprocess
+
 import pytest
 import torch
 
@@ -227,3 +230,24 @@ def test_tensors_on_the_host_are_refused(i):
     with pytest.raises(swg.SwgError, match="current CUDA device") as e:
         f(**tensors, **rest)
     assert e.value.status == INVALID
+
+
+def test_binding_keeps_to_the_stable_abi(lib):
+    """Another interpreter than the one that built it may find it and load it."""
+    import importlib
+    module = importlib.import_module("swiglu_mlp_gb300._binding")
+    assert os.path.samefile(module.__file__, swg_build.BINDING) and module.__file__.endswith(".abi3.so")
+    needed = subprocess.run(["nm", "-D", "--undefined-only", module.__file__], capture_output=True, text=True).stdout
+    names = [line.split()[-1].split("@")[0] for line in needed.splitlines()]
+    assert any(n.startswith("Py") for n in names)
+    # private names are in no stable ABI, but for these
+    assert {n for n in names if n.startswith("_Py")} <= {"_Py_Dealloc", "_Py_IncRef", "_Py_DecRef", "_Py_NoneStruct"}
+
+
+def test_build_without_python_headers(lib, monkeypatch, tmp_path):
+    """The library is there and the error names the compiler that failed."""
+    monkeypatch.setattr(swg_build, "BINDING", str(tmp_path / "_binding.abi3.so"))
+    monkeypatch.setattr(swg_build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    with pytest.raises(RuntimeError, match="^gcc failed"):
+        swg_build.build()
+    assert os.path.exists(swg_build.LIB)
