@@ -338,9 +338,11 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Mx4Args p, int 
             for (int j = 0; j < 8; j += 2) {
                 float2 x = make_float2(p.scale * v[j], p.scale * v[j + 1]);
                 if (NV) {
-                    // Every tie between two codes is a quotient that is a float
-                    // (for 16-bit x), so ties go to even as in the definition;
-                    // the product with the inverse alone may miss them.
+                    // A tie between two codes is a quotient that is a float, and x
+                    // next to one has a quotient at least 8/15 of a float's unit
+                    // from it (the scale has 4 bits), so that the corrected
+                    // quotient rounds as the exact one does, for any FP32 x; the
+                    // product with the inverse alone may miss ties.
                     const float2 inv2 = make_float2(inv, inv);
                     const float2 y = __fmul2_rn(x, inv2);
                     x = __ffma2_rn(__ffma2_rn(make_float2(-y.x, -y.y), make_float2(s, s), x), inv2, y);

@@ -352,3 +352,45 @@ def test_products_over_no_columns(fmt, rows):
     C = torch.full((M, 2 * N), 9.0, dtype=torch.bfloat16, device="cuda")
     swg.gemm_mx4_into(C, q, s, w.view(G, 2 * N, 0), sw, 0, FMT[fmt], beta=0.5, offsets=off)
     assert (C == 4.5).all() and swg.get_device_error() == 0
+
+
+def e4m3_scales():
+    """Every scale of NVFP4: 2^-9 to 448."""
+    return np.array([m * 2.0 ** -9 for m in range(1, 8)] +
+                    [(8 + m) * 2.0 ** (e - 10) for e in range(1, 16) for m in range(8)][:-1])
+
+
+@pytest.mark.parametrize("factor", [1.0, 0.3, 1.7e-3])
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_f32_ties_and_their_neighbours(fmt, factor):
+    """FP32 values at, just below and just above what lies halfway between two
+    codes or two scales, for every scale, are rounded as the definition says:
+    the FP32 product with the factor, divided exactly, ties to even."""
+    b = plain.BLOCK[fmt]
+    scales = e4m3_scales() if fmt == "nv" else 2.0 ** np.arange(-90, 91, 6)
+    ties = np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    f = np.float32(factor)
+    blocks = []
+
+    def around(v):
+        """FP32 numbers whose product with the factor is v, or the nearest, and their neighbours."""
+        x = np.float32(v / np.float64(f))
+        return [x, np.nextafter(x, np.float32(np.inf)), np.nextafter(x, np.float32(0))]
+
+    for i, s in enumerate(scales):
+        near = np.array([n for t in ties for n in around(t * s)], dtype=np.float32)
+        near[1::2] *= -1
+        for part in (near[:b - 1], near[b - 1:]):
+            block = np.zeros(b, np.float32)
+            block[0] = around(6 * s)[0]
+            block[1:1 + len(part)] = part
+            blocks.append(block)
+        if i + 1 < len(scales):             # halfway between two scales
+            for x in around(6 * (s + scales[i + 1]) / 2):
+                blocks.append(np.r_[x, (near / 1.1)[:b - 1], np.zeros(b)][:b].astype(np.float32))
+    x = np.stack(blocks)
+    q, s = quantise(torch.from_numpy(x), fmt, scale=factor)
+    out = torch.empty(x.shape, dtype=torch.float32, device="cuda")
+    swg.mx4_dequantize_into(out, q, s, FMT[fmt])
+    assert swg.get_device_error() == 0
+    assert np.array_equal(plain.f64(out), plain.quantised((x * f).astype(np.float64), fmt))
