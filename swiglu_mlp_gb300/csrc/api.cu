@@ -1087,9 +1087,8 @@ bool encode_tiled(CUtensorMap *m, CUtensorMapDataType type, int rank, const void
     }
     const CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void *>(ptr), d, st, b, es,
                           CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                          : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                          : CU_TENSOR_MAP_SWIZZLE_NONE,
+                          swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                         : CU_TENSOR_MAP_SWIZZLE_NONE,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) t_last_cuda_error = 10000 + (int)r;
     return r == CUDA_SUCCESS;

@@ -114,10 +114,9 @@ int run_grouped(const swg::GrpArgs &a, swg::GrpKind kind, swg::GrpEpi epi, void 
     swg::GrpParams p{};
     p.groups = a.groups;
     p.N = a.N;
-    p.K = a.K;
     p.n_blocks = (int)((N + 255) / 256);
-    p.bk = f4 ? 256 : 64;
-    p.k_blocks = (int)((K + p.bk - 1) / p.bk);
+    const int bk = f4 ? 256 : 64;
+    p.k_blocks = (int)((K + bk - 1) / bk);
     p.w_mn = a.b_kn;
     p.w_tiles = (int)((N + 127) / 128);
     p.alpha = a.alpha;

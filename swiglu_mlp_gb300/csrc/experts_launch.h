@@ -1,9 +1,5 @@
-// experts_launch.h — launches of the expert-MLP kernels, and the decoding of
-// 4-bit values that they share.
+// experts_launch.h — launches of the expert-MLP kernels.
 #pragma once
-
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "experts.h"
 
@@ -67,15 +63,5 @@ struct WgradArgs {
 };
 // mapped: whether the tensor maps could be encoded (if not, nothing was launched).
 cudaError_t launch_wgrad(const WgradArgs &a, int sms, int *err, cudaStream_t s, bool &mapped);
-
-#ifdef __CUDACC__
-// The value of a scale byte: E8M0 (0xFF is NaN), or E4M3.
-__device__ __forceinline__ float mx4_scale_value(bool nv, uint32_t c)
-{
-    if (nv) return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3)));
-    return c == 255u ? __int_as_float(0x7fffffff)
-                     : __int_as_float(c > 0 ? c << 23 : 1 << 22);
-}
-#endif
 
 }  // namespace swg

@@ -131,9 +131,8 @@ struct GrpMaps {
 
 struct GrpParams {
     Groups groups;
-    int N, K;
-    int n_blocks, k_blocks;
-    int bk;                              // K elements of a stage: 64 (16-bit) or 256 (4-bit)
+    int N;
+    int n_blocks, k_blocks;              // 256 columns; stages of 64 (16-bit) or 256 (4-bit) of K
     uint32_t idesc;                      // without N
     int w_mn;                            // weight MN-major (stored K x N)
     int w_4d;                            // ... as one 4-D box per stage

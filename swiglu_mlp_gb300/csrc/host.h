@@ -33,7 +33,7 @@ int count_launch(cudaError_t e);
 // as long as it keeps `held`: until its last kernel is queued.
 int stream_workspace(cudaStream_t s, size_t bytes, float *&out, std::unique_lock<std::mutex> &held);
 
-// cuTensorMapEncodeTiled with a swizzle of 128, 64 or 0 (none) bytes, unit
+// cuTensorMapEncodeTiled with a swizzle of 128 or 0 (none) bytes, unit
 // element strides, no interleave and zero fill; false (recorded) when it
 // fails.  strides[i] is the byte stride of dimension i + 1.
 bool encode_tiled(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *ptr,

@@ -187,6 +187,14 @@ __device__ __forceinline__ uint32_t block_scale(float top, float &scale, float &
     return bad ? 0xffu : code;
 }
 
+// The value of a scale byte: E8M0 (0xFF is NaN), or E4M3.
+__device__ __forceinline__ float scale_value(bool nv, uint32_t c)
+{
+    if (nv) return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3)));
+    return c == 255u ? __int_as_float(0x7fffffff)
+                     : __int_as_float(c > 0 ? c << 23 : 1 << 22);
+}
+
 struct Place {
     int t;                   // row of scale tiles
     int chunk;               // of columns
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const Mx4Args p, in
     for (int i = 0; i < ROWS; ++i) {
         const int row = at.row0 + at.r + APART * i;
         if (row >= at.end) continue;
-        const float s = mx4_scale_value(NV, (words[i] >> (8 * b)) & 0xffu);
+        const float s = scale_value(NV, (words[i] >> (8 * b)) & 0xffu);
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
