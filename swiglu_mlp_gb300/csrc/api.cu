@@ -15,6 +15,7 @@
 #include <cstdlib>
 #include <map>
 #include <mutex>
+#include <new>
 #include <utility>
 #include <vector>
 
@@ -208,10 +209,13 @@ void CUDART_CB graph_gone(void *scratch)
     GraphBuffers &all = graph_buffers();
     {
         std::lock_guard<std::mutex> lk(all.mu);
-        auto &idle = all.idle[g->dev];
-        idle.insert(idle.end(), g->buffers.begin(), g->buffers.end());
         const auto it = all.live.find({g->capture, g->stream});
         if (it != all.live.end() && it->second == g) all.live.erase(it);
+        try {
+            auto &idle = all.idle[g->dev];
+            idle.insert(idle.end(), g->buffers.begin(), g->buffers.end());
+        } catch (const std::bad_alloc &) {           // no host memory to remember them in
+        }
     }
     delete g;
 }
@@ -366,7 +370,7 @@ struct FixedScratch {
 // `held`: keep it until the call's last kernel is queued.
 int split_workspace(DeviceState *d, cudaStream_t s, size_t bytes, const FixedScratch *fx,
                     float *&out, std::unique_lock<std::mutex> &held)
-{
+try {
     if (fx) {
         if (bytes > fx->bytes) return SWG_ERR_UNSUPPORTED;   // partials would not fit
         held = std::unique_lock<std::mutex>(*fx->mu);
@@ -374,6 +378,8 @@ int split_workspace(DeviceState *d, cudaStream_t s, size_t bytes, const FixedScr
         return SWG_OK;
     }
     return workspace(d, s, bytes, out, held);
+} catch (const std::bad_alloc &) {                   // of host memory: no exception leaves a C entry
+    return SWG_ERR_NO_MEMORY;
 }
 
 // The fixed array of gemm_splitk_noalloc on the current device (defined at
@@ -1066,7 +1072,7 @@ int stream_workspace(cudaStream_t s, size_t bytes, float *&out, std::unique_lock
 {
     DeviceState *d = nullptr;
     if (int rc = device_state(d)) return rc;
-    return workspace(d, s, bytes, out, held);
+    return split_workspace(d, s, bytes, nullptr, out, held);
 }
 
 bool encode_tiled(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *ptr,

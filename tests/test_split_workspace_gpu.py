@@ -183,3 +183,23 @@ def test_destroyed_graphs_leave_their_buffers_to_others():
     # 140 MB (0.35 MB of partials for each graph), if none were reused
     assert free - torch.cuda.mem_get_info()[0] < 16 << 20
     assert swg.get_device_error() == 0
+
+
+def test_graphs_that_outlive_a_shutdown():
+    """swg_shutdown frees what graphs held; destroying them later is harmless,
+    and later captures get buffers of their own."""
+    c = Calls(41)
+    c.alone()
+    s = torch.cuda.Stream()
+    old = captured(c, s)
+    torch.cuda.synchronize()
+    swg.shutdown()
+    new = captured(c, s)
+    old.reset()
+    for t in c.outs:
+        t.zero_()
+    torch.cuda.synchronize()
+    new.replay()
+    torch.cuda.synchronize()
+    assert swg.get_device_error() == 0
+    assert all(torch.equal(t, w) for t, w in zip(c.outs, c.want))
