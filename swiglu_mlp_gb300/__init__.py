@@ -456,6 +456,12 @@ def _groups(offsets, where):
     return shape[0] - 1
 
 
+def _one_row(cols):
+    """The row stride of a matrix of one row, which torch leaves open (it may be
+    less than a row): one that every rule of alignment allows."""
+    return (cols + 15) & ~15
+
+
 def _matrices(t, name, where, G):
     """(rows, columns, row stride, group stride) of a [G, rows, columns]
     tensor, or with G = 1 also of a [rows, columns] one."""
@@ -469,7 +475,7 @@ def _matrices(t, name, where, G):
         g = sg = sr = sc = rows = cols = -1
     if sc != 1 or g != G:
         _refuse(where, f"{name} must hold one row-major matrix for each of {G} groups")
-    return rows, cols, sr, sg
+    return rows, cols, sr if rows > 1 else _one_row(cols), sg
 
 
 def _matrix(t, name, where):
@@ -480,7 +486,7 @@ def _matrix(t, name, where):
         unit = 0
     if unit != 1:
         _refuse(where, f"{name} must be a 2-D row-major tensor (unit column stride)")
-    return rows, cols, ld
+    return rows, cols, ld if rows > 1 else _one_row(cols)
 
 
 def _type_code(dtype, where) -> int:

@@ -516,3 +516,21 @@ def test_each_tensor_has_to_be_on_the_gpu(i):
         with pytest.raises(swg.SwgError, match="current CUDA device"):
             f(**dict(there, **{n: t}), **rest)
     assert swg.launch_count() == before
+
+
+@pytest.mark.parametrize("rows", [[1], [3, 0, 70]])
+@pytest.mark.parametrize("types", DTYPES)
+def test_matrices_of_one_row(rows, types):
+    """Contractions of length one, and single columns of a transposed weight and
+    of a gradient: torch gives a lone row any stride."""
+    run_gemm(rows, 21, 1, types, 0, beta=0.5, seed=1)
+    run_gemm(rows, 1, 21, types, 1, seed=2)
+    run_wgrad(rows, 21, 1, types, beta=0.5, seed=3)
+    g = synth.generator(4)
+    A, B = synth.normal((40, 1), g).cuda().t(), synth.normal((1, 40, 24), g).cuda()
+    assert A.stride() == (1, 1)
+    C = torch.empty((24, 1), dtype=torch.bfloat16, device="cuda").t()
+    swg.gemm_grouped_into(C, A, B, torch.tensor([0, 1], dtype=torch.int32).cuda())
+    assert swg.get_device_error() == 0
+    want, tol = plain.product(plain.f64(A), plain.f64(B), [0, 1], 0, 1.0, 0.0, np.zeros((1, 24)), "bf16")
+    check(C.cpu(), want, tol, "one row")
