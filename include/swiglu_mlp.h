@@ -436,7 +436,8 @@ SWG_API int mx4_quantize(int format, int64_t G, int64_t M, int64_t K, const void
                          int xtype, float scale, const int32_t *offsets, void *Q, int64_t ldq,
                          void *S, void *stream);
 
-/* mx4_dequantize — X = scale * the values of (Q, S), rounded once to xtype. */
+/* mx4_dequantize — X = scale * the values of (Q, S), the product formed in FP32
+ * and rounded to xtype. */
 SWG_API int mx4_dequantize(int format, int64_t G, int64_t M, int64_t K, const void *Q,
                            int64_t ldq, const void *S, float scale, const int32_t *offsets,
                            void *X, int64_t ldx, int xtype, void *stream);

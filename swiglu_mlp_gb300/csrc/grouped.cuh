@@ -25,16 +25,19 @@
 // What bounds it, and what it measured on one GB300:
 //   many rows, 16 bits: the tensor pipe at the clock that the power limit
 //     leaves.  SwiGLU, 16384 rows of 16 groups, K = 4096, N = 2 x 1792: 267 us,
-//     1800 TFLOP/s; gradient of half as many rows, 8 groups: 146 us, 1650.
+//     1800 TFLOP/s, in a burst and 310 us, 1550, in a long run; gradient of half
+//     as many rows, 8 groups: 146 us, 1650, and 167 us, 1440.
 //   many rows, 4 bits: MMAs and the copies of their scales, one behind the other
-//     in the tensor pipe, which is 70% busy.  8192 x 14336 x 4096: NVFP4 143 us,
-//     6.7 PFLOP/s; MXFP4 135 us, 7.1.
+//     in the tensor pipe, which is 70% busy.  8192 x 14336 x 4096, in a burst:
+//     NVFP4 143 us, 6.7 PFLOP/s; MXFP4 135 us, 7.1.
 //   few rows: the weights' way from memory and about 3.3 us that any call takes
 //     (set-up, offsets, first load, last store).  8 groups of one row, 4096 x
 //     9728 in 16 bits: 94 us, 6.8 TB/s; 16 rows, 229376 x 4096 in MXFP4: 78 us,
 //     6.4 TB/s; 2 rows of 8 groups, 896 x 9728: 8.3 us, 4.2 TB/s.
-//   between: the latency of loads that miss L2, 1.3 to 2.3 us for a ring of 5 or
-//     6 stages.  32 groups of 128 rows, 2048 x 2432 in MXFP4: 24 us, 3.5 TB/s.
+//   between: not accounted for.  32 groups of 128 rows, 2048 x 2432 in MXFP4: 24
+//     us, 3.5 TB/s, of which the latency of loads that miss L2 (1.3 to 2.3 us) is
+//     a part at most: the weights of 6 stages on every SM are 15 MB in flight,
+//     6.5 TB/s at 2.3 us.
 #pragma once
 
 #include "experts_launch.h"

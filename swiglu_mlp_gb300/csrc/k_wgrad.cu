@@ -15,7 +15,8 @@
 //
 // What bounds it: for long groups the tensor pipe at the clock that the power
 // limit leaves (16 groups of about 1024 rows, 1792 x 4096, bf16: 147 us, 1640
-// TFLOP/s; 75% of the pipe's cycles); for short ones writing C (64 groups of 16
+// TFLOP/s, in a burst and 168 us, 1430, in a long run; 75% of the pipe's cycles);
+// for short ones writing C (64 groups of 16
 // rows, 2048 x 1024: 63 us for 268 MB, 4.3 TB/s; 64 of 3, 1024 x 1024: 36 us, 3.8;
 // a plain fill reaches 4.1), and 4 us that any call takes (48 groups of about 4
 // rows, 896 x 521 with rows 1072 bytes apart: 19 to 24 us for 45 MB).
@@ -96,7 +97,7 @@ __device__ __forceinline__ bool ends_inside(int left) { return left < 64 && (lef
 // may the MMAs read it.  In the ring that held every tile up by 0.8 us.  So
 // longer groups load the 16 rows of that step apart from the ring, after the
 // first WG_STAGES blocks (by when the tile before has been done with the slot),
-// and multiply them last (16 groups of 1000 rows, 1792 x 4096: 159 -> 138 us).
+// and multiply them last (16 groups of 1000 rows, 1792 x 4096: 156 -> 144 us).
 struct Blocks {
     int ring;        // blocks of 64 rows that go through the ring
     int rows;        // rows of the group in them
