@@ -534,3 +534,30 @@ def test_matrices_of_one_row(rows, types):
     assert swg.get_device_error() == 0
     want, tol = plain.product(plain.f64(A), plain.f64(B), [0, 1], 0, 1.0, 0.0, np.zeros((1, 24)), "bf16")
     check(C.cpu(), want, tol, "one row")
+
+
+@pytest.mark.parametrize("N", [1, 7, 21, 40, 257])
+@pytest.mark.parametrize("K", [40, 4096])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_a_lone_row_ends_where_its_columns_do(N, K, out):
+    """The result of one row, in storage of N elements: nothing behind them is
+    written, whatever row stride it is taken with."""
+    g = synth.generator(N)
+    A, B = padded(1, K, g, torch.bfloat16), padded(K, N, g, torch.bfloat16, K ** -0.5)
+    D = padded(1, N, g, torch.bfloat16)
+    o = torch.tensor([0, 1], dtype=torch.int32).cuda()
+    store = torch.full((N + 64,), 7.0, dtype=TYPE[out], device="cuda")
+    C = store[:N].view(1, N)
+    swg.gemm_grouped_into(C, A, B.unsqueeze(0), o)
+    want, tol = plain.product(plain.f64(A), plain.f64(B)[None], [0, 1], 0, 1.0, 0.0, np.zeros((1, N)), out)
+    check(C.cpu(), want, tol, "lone row")
+    assert (store[N:] == 7.0).all()
+    swg.gemm_grouped_wgrad_into(C, A[:, :1], D, o)
+    want, tol = plain.wgrad(plain.f64(A)[:, :1], plain.f64(D), [0, 1], 1.0, 0.0, np.zeros((1, 1, N)), out)
+    check(C.cpu()[None], want, tol, "lone row of a gradient")
+    assert (store[N:] == 7.0).all()
+    Q, S = swg.mx4_alloc(1, N, swg.NVFP4)
+    swg.mx4_quantize_into(Q, S, D, swg.NVFP4)
+    swg.mx4_dequantize_into(C, Q, S, swg.NVFP4)
+    assert np.array_equal(plain.f64(C), plain.quantised(plain.f64(D), "nv"))
+    assert (store[N:] == 7.0).all() and swg.get_device_error() == 0
