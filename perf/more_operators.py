@@ -316,10 +316,11 @@ def quantise(x, g, zero, dtype):
     x = torch.nn.functional.pad(x.float(), (0, pad_to(K, g) - K)).view(rows, -1, g)
     if zero:
         lo, hi = x.amin(-1).clamp(max=0.0), x.amax(-1).clamp(min=0.0)
-        s = ((hi - lo) / 15.0).to(dtype).float()
+        s = ((hi - lo) / torch.full_like(hi, 15.0)).to(dtype).float()  # (divided by a number, torch multiplies by its inverse)
         z = torch.where(s > 0, torch.round(-lo / s), 0.0).clamp(0, 15)
     else:
-        s = (x.abs().amax(-1) / 7.0).to(dtype).float()
+        top = x.abs().amax(-1)
+        s = (top / torch.full_like(top, 7.0)).to(dtype).float()
         z = torch.full_like(s, 8.0)
     q = torch.where(s[..., None] > 0, torch.round(x / s[..., None]), 0.0) + z[..., None]
     return q.clamp(0, 15).view(rows, -1)[:, :K].to(torch.uint8), s.to(dtype), z.to(torch.uint8)
@@ -608,10 +609,10 @@ def rounded_64(X, case):
         x = X[:, k:k + case["g"]].double()
         if case["zero"]:
             lo, hi = x.amin(1, keepdim=True).clamp(max=0), x.amax(1, keepdim=True).clamp(min=0)
-            s = ((hi - lo).float() / 15.0).to(X.dtype).double()
+            s = ((hi - lo).float().double() / 15.0).float().to(X.dtype).double()
             z = torch.round(-lo / s).clamp(0, 15)
         else:
-            s = (x.abs().amax(1, keepdim=True).float() / 7.0).to(X.dtype).double()
+            s = (x.abs().amax(1, keepdim=True) / 7.0).float().to(X.dtype).double()
             z = torch.full_like(s, 8.0)
         out[:, k:k + case["g"]] = s * ((torch.round(x / s) + z).clamp(0, 15) - z)
     return out
