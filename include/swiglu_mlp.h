@@ -469,6 +469,166 @@ SWG_API int swiglu_mx4(int format, const void *A, const void *SA, const void *W,
                        void *Y, const int32_t *offsets, int64_t G, int64_t M, int64_t N,
                        int64_t K, float alpha, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Routing: which experts a token goes to, and its rows there and back (no
+ * counterpart on the pages).  A slot is one of the `top` places of a token:
+ * slot t * top + j is token t's j'th.  Arrays of slots are contiguous
+ * (T x top).  T * top, R and D are at most 2^31 - 1024, the experts at most
+ * SWG_MAX_EXPERTS, top at most SWG_MAX_TOP, else SWG_ERR_UNSUPPORTED.
+ * X, rows, out and their gradients share one swg_type; they are 16-byte aligned,
+ * row strides multiples of 16 bytes.  Logits need only their type's alignment.
+ * None of the outputs may overlap an input, but out of expert_combine, which is
+ * read for beta != 0.
+ */
+typedef enum { SWG_SOFTMAX = 0, SWG_SIGMOID = 1 } swg_score;
+#define SWG_MAX_EXPERTS 1024
+#define SWG_MAX_TOP 32
+#define SWG_MAX_EXPERT_GROUPS 32
+
+/*
+ * expert_route — the experts of each token and their weights, and, unless
+ * offsets is NULL, the plan of rows that expert_sort gives.
+ *   logits, ldl   T x E of swg_type `type`.
+ *   score         s = softmax(logits) over the token's E experts, or the sigmoid of
+ *                 each.
+ *   bias          E floats or NULL.  Experts are chosen by c = s + bias, compared
+ *                 as FP64 has them (without a bias in the order of the
+ *                 logits); equal ones by the lowest index.  The weights are those of s.
+ *   groups        >= 1, dividing E: experts e with equal e / (E / groups) are a
+ *                 group, of which the top_groups best are chosen first.  A group is
+ *                 worth its largest c (group_sum = 1) or the sum of its two
+ *                 largest (2).  groups <= SWG_MAX_EXPERT_GROUPS.
+ *   top           experts per token, at most E / groups * top_groups.
+ *   normalise     non-zero: weights are scale * s_j / (the sum of the chosen s);
+ *                 zero: scale * s_j.  (scale finite.)
+ *   experts, weights   T x top: largest c first.
+ * An expert whose logit or bias is -inf is not chosen; a slot that none is left for
+ * gets expert -1 and weight 0.  A token with a NaN among its c (a NaN logit or
+ * bias; for softmax also a logit of +inf) goes to experts 0 .. top - 1 with
+ * weights of NaN.
+ * Calls with a plan of more than 64 tokens keep counts in the stream's workspace:
+ * what gemm says of split calls and graph capture holds for them.
+ */
+SWG_API int expert_route(int score, int64_t T, int64_t E, int64_t top, const void *logits, int64_t ldl,
+                         int type, const float *bias, int64_t groups, int64_t top_groups,
+                         int group_sum, int normalise, float scale, int32_t *experts, float *weights,
+                         int32_t *offsets, int32_t *source, int32_t *position, void *stream);
+
+/*
+ * expert_sort — the plan of rows sorted by expert, for experts [T x top] as
+ * expert_route gives them (or any numbers from -1 to E - 1).
+ *   offsets    E + 1: where each expert's rows begin; offsets[E] rows in all.
+ *              The offsets of the grouped products.
+ *   source     T * top: the slot that row r is of; an expert's rows are in the order
+ *              of their slots.  -1 behind the last row.
+ *   position   T x top: the row of each slot, -1 where it has no expert.
+ * Experts beyond the rule count as -1, and the device error word becomes
+ * SWG_ERR_INVALID_ARG.  T == 0: offsets of 0.  More than 4096 slots: workspace as
+ * for expert_route.
+ */
+SWG_API int expert_sort(int64_t T, int64_t E, int64_t top, const int32_t *experts, int32_t *offsets,
+                        int32_t *source, int32_t *position, void *stream);
+
+/*
+ * expert_route_grad — d_logits (T x E of `type`, all written) from d_weights
+ * (T x top floats), the experts taken as given:
+ *   normalised, p_j = s_j / sum s:  softmax dl_j = scale p_j (d_j - sum p d),
+ *                                   sigmoid that times (1 - s_j);
+ *   not normalised:                 softmax dl_e = s_e (g_e - sum g s), g_e the sum of
+ *                                   scale * d over the slots with expert e,
+ *                                   sigmoid dl_j = scale s_j (1 - s_j) d_j.
+ * Slots of expert -1 count for nothing; other numbers beyond [0, E) neither, and
+ * they are reported.  The bias has no gradient.
+ */
+SWG_API int expert_route_grad(int score, int64_t T, int64_t E, int64_t top, const void *logits,
+                              int64_t ldl, int type, const int32_t *experts, int normalise, float scale,
+                              const float *d_weights, void *d_logits, int64_t ldd, void *stream);
+
+/*
+ * expert_dispatch — rows[position[t][j],:] = X[t,:] for every slot with a row: X
+ * T x D, rows R x D.  Other rows keep their values.  Positions beyond [0, R) have no
+ * row; those other than -1 are reported (device error word).  Its gradient is
+ * expert_combine without weights.
+ */
+SWG_API int expert_dispatch(int64_t T, int64_t R, int64_t D, int64_t top, const void *X, int64_t ldx,
+                            int type, const int32_t *position, void *rows, int64_t ldr, void *stream);
+
+/*
+ * expert_combine — out[t,:] = sum_j weights[t][j] * rows[position[t][j],:] + beta *
+ * out[t,:] over the slots with a row, in FP32 and in the order of the slots, rounded
+ * once.  weights NULL: ones.  out is not read when beta == 0.
+ */
+SWG_API int expert_combine(int64_t T, int64_t R, int64_t D, int64_t top, const void *rows, int64_t ldr,
+                           int type, const int32_t *position, const float *weights, float beta,
+                           void *out, int64_t ldo, void *stream);
+
+/*
+ * expert_combine_grad — the gradients of that:
+ *   d_rows[position[t][j],:] = weights[t][j] * d_out[t,:]      (other rows keep theirs)
+ *   d_weights[t][j] = <rows[position[t][j],:], d_out[t,:]>     (0 without a row)
+ * weights NULL: ones.  d_weights NULL: not computed, and rows is not read.  The
+ * positions have to differ (as expert_sort's do): a row of several slots gets the
+ * gradient of one of them.
+ */
+SWG_API int expert_combine_grad(int64_t T, int64_t R, int64_t D, int64_t top, const void *d_out,
+                                int64_t ldd, const void *rows, int64_t ldr, int type,
+                                const int32_t *position, const float *weights, void *d_rows,
+                                int64_t lddr, float *d_weights, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Weights of 4 bits with group scales, rows of A in 16 bits (no counterpart on
+ * the pages): for decoding, where the weights' bytes are the time.
+ *   w[n][k] = S[k / group][n] * (q[n][k] - Z[k / group][n]),  q and Z from 0 to 15;
+ *   Z NULL: 8 everywhere.  group: 32, 64 or 128 columns (else SWG_ERR_UNSUPPORTED).
+ * Storage of an expert's N x K weight; the G experts' follow one another:
+ *   Q   N rows of 16 * ceil(K / 32) bytes.  Eight columns of a row are a 32-bit
+ *       word (little-endian): columns 0, 2, 4, 6 in bits 0, 4, 8, 12 and columns 1,
+ *       3, 5, 7 in bits 16, 20, 24, 28.
+ *   S   ceil(K / group) rows of lds elements, binary16 or bfloat16; lds >= N, a
+ *       multiple of 16.
+ *   Z   the same of bytes (the lower 4 bits count).
+ * Pointers 16-byte aligned, row strides of X, A, C, Y multiples of 16 bytes.  Sizes
+ * as for the grouped products; K of the conversions at most 256 * 65535.
+ */
+
+/*
+ * w4_quantize — X (G * N rows of K, swg_type xtype) to 4 bits.  With m the largest
+ * magnitude of a group of columns in a row, and lo <= 0 <= hi its range:
+ *   Z NULL:  S = m / 7,           q = round(x / S) + 8;
+ *   else:    S = (hi - lo) / 15,  Z = round(-lo / S),  q = round(x / S) + Z;
+ * quotients in FP32, S rounded to stype (the largest finite value at most) before
+ * it is used, ties to even, q and Z clamped to 0 .. 15, x / S = 0 where S is 0.  A
+ * group of columns with a NaN or an infinity gets a NaN S and reads back as NaN.
+ * Codes from column K up to a multiple of 32 are 0.
+ */
+SWG_API int w4_quantize(int64_t G, int64_t N, int64_t K, const void *X, int64_t ldx, int xtype,
+                        int64_t group, void *Q, void *S, void *Z, int64_t lds, int stype, void *stream);
+
+/* w4_dequantize — X = the values, formed in FP32 and rounded to xtype. */
+SWG_API int w4_dequantize(int64_t G, int64_t N, int64_t K, const void *Q, const void *S, const void *Z,
+                          int64_t lds, int stype, int64_t group, void *X, int64_t ldx, int xtype,
+                          void *stream);
+
+/*
+ * gemm_w4 — C[i,:] = alpha * A[i,:] * W_g^T + beta * C[i,:] for the rows i of every
+ * group g (offsets, G: as for gemm_grouped; NULL and 1: dense), FP32 accumulation.
+ *   A, S   of swg_type `type` (16 bits).   C   of ctype.
+ * Meant for few rows of each expert; for many, w4_dequantize and gemm_grouped.
+ */
+SWG_API int gemm_w4(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, const void *A, int64_t lda,
+                    const void *Q, const void *S, const void *Z, int64_t lds, int64_t group,
+                    const int32_t *offsets, float beta, void *C, int64_t ldc, int type, int ctype,
+                    void *stream);
+
+/*
+ * swiglu_w4 — Y[i,:] = SiLU(alpha A[i,:] W1_g^T) (.) (alpha A[i,:] W2_g^T), M x N of
+ * `type`.  W has 2N rows for each group: row 2n = W1's n'th (Gate), row 2n + 1 = W2's
+ * (Up); lds >= 2N.
+ */
+SWG_API int swiglu_w4(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, const void *A, int64_t lda,
+                      const void *Q, const void *S, const void *Z, int64_t lds, int64_t group,
+                      const int32_t *offsets, void *Y, int64_t ldy, int type, void *stream);
+
 /*
  * swg_debug_workspace_guards — diagnostic for tests (no counterpart on the
  * pages).  With the environment variable SWG_TEST_WS_GUARD=1 set before a

@@ -30,6 +30,12 @@ __all__ = [
     "gemm_grouped_into", "gemm_grouped_wgrad_into", "swiglu_grouped_into",
     "swiglu_grouped_grad_into", "mx4_alloc", "mx4_quantize_into", "mx4_dequantize_into",
     "gemm_mx4_into", "swiglu_mx4_into",
+    "SOFTMAX", "SIGMOID", "MAX_EXPERTS", "MAX_TOP", "MAX_EXPERT_GROUPS",
+    "expert_route", "expert_sort", "expert_route_grad", "expert_dispatch", "expert_combine",
+    "expert_combine_grad", "w4_quantize", "w4_dequantize", "gemm_w4", "swiglu_w4",
+    "expert_plan_alloc", "expert_route_into", "expert_sort_into", "expert_route_grad_into",
+    "expert_dispatch_into", "expert_combine_into", "expert_combine_grad_into", "w4_alloc",
+    "w4_quantize_into", "w4_dequantize_into", "gemm_w4_into", "swiglu_w4_into",
 ]
 
 OP_N, OP_T = 0, 1
@@ -37,6 +43,8 @@ F16_F32OUT, BF16, F16, BF16_F32OUT, E4M3_BF16OUT, E4M3_F32OUT = 0, 1, 2, 3, 4, 5
 MXFP4, NVFP4 = 0, 1
 TYPE_F16, TYPE_BF16, TYPE_F32 = 0, 1, 2
 MAX_GROUPS = 1024
+SOFTMAX, SIGMOID = 0, 1
+MAX_EXPERTS, MAX_TOP, MAX_EXPERT_GROUPS = 1024, 32, 32
 STATUS = {0: "SWG_OK", 1: "SWG_ERR_INVALID_ARG", 2: "SWG_ERR_MISALIGNED",
           3: "SWG_ERR_UNSUPPORTED", 4: "SWG_ERR_CUDA", 5: "SWG_ERR_NO_MEMORY",
           6: "SWG_ERR_DEVICE_TIMEOUT"}
@@ -123,9 +131,26 @@ def load():
         lib.gemm_mx4.argtypes = [i32, i64, i64, i64, i64, f32, vp, i64, vp, vp, i64, i64, vp, vp,
                                  f32, vp, i64, i32, vp]
         lib.swiglu_mx4.argtypes = [i32, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, f32, vp]
+        lib.expert_route.argtypes = [i32, i64, i64, i64, vp, i64, i32, vp, i64, i64, i32, i32, f32,
+                                     vp, vp, vp, vp, vp, vp]
+        lib.expert_sort.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp]
+        lib.expert_route_grad.argtypes = [i32, i64, i64, i64, vp, i64, i32, vp, i32, f32, vp, vp,
+                                          i64, vp]
+        lib.expert_dispatch.argtypes = [i64, i64, i64, i64, vp, i64, i32, vp, vp, i64, vp]
+        lib.expert_combine.argtypes = [i64, i64, i64, i64, vp, i64, i32, vp, vp, f32, vp, i64, vp]
+        lib.expert_combine_grad.argtypes = [i64, i64, i64, i64, vp, i64, vp, i64, i32, vp, vp, vp,
+                                            i64, vp, vp]
+        lib.w4_quantize.argtypes = [i64, i64, i64, vp, i64, i32, i64, vp, vp, vp, i64, i32, vp]
+        lib.w4_dequantize.argtypes = [i64, i64, i64, vp, vp, vp, i64, i32, i64, vp, i64, i32, vp]
+        lib.gemm_w4.argtypes = [i64, i64, i64, i64, f32, vp, i64, vp, vp, vp, i64, i64, vp, f32, vp,
+                                i64, i32, i32, vp]
+        lib.swiglu_w4.argtypes = [i64, i64, i64, i64, f32, vp, i64, vp, vp, vp, i64, i64, vp, vp,
+                                  i64, i32, vp]
         for name in ("gemm_grouped", "gemm_grouped_wgrad", "swiglu_grouped",
                      "swiglu_grouped_grad", "mx4_quantize", "mx4_dequantize", "gemm_mx4",
-                     "swiglu_mx4"):
+                     "swiglu_mx4", "expert_route", "expert_sort", "expert_route_grad",
+                     "expert_dispatch", "expert_combine", "expert_combine_grad", "w4_quantize",
+                     "w4_dequantize", "gemm_w4", "swiglu_w4"):
             getattr(lib, name).restype = i32
         _lib = lib
         return lib
@@ -304,6 +329,85 @@ def swiglu_mx4(format, A, SA, W, SW, Y, offsets, G, M, N, K, alpha, stream=None)
     return _check(load().swiglu_mx4(int(format), _ptr(A), _ptr(SA), _ptr(W), _ptr(SW), _ptr(Y),
                                     _ptr(offsets), int(G), int(M), int(N), int(K), float(alpha),
                                     _stream(stream)), "swiglu_mx4")
+
+
+def expert_route(score, T, E, top, logits, ldl, type, bias, groups, top_groups, group_sum, normalise,
+                 scale, experts, weights, offsets, source, position, stream=None):
+    """The experts of each token, their weights and the plan of rows (see the C header)."""
+    return _check(load().expert_route(int(score), int(T), int(E), int(top), _ptr(logits), int(ldl),
+                                      int(type), _ptr(bias), int(groups), int(top_groups),
+                                      int(group_sum), int(normalise), float(scale), _ptr(experts),
+                                      _ptr(weights), _ptr(offsets), _ptr(source), _ptr(position),
+                                      _stream(stream)), "expert_route")
+
+
+def expert_sort(T, E, top, experts, offsets, source, position, stream=None):
+    """The plan of rows sorted by expert (see the C header)."""
+    return _check(load().expert_sort(int(T), int(E), int(top), _ptr(experts), _ptr(offsets),
+                                     _ptr(source), _ptr(position), _stream(stream)), "expert_sort")
+
+
+def expert_route_grad(score, T, E, top, logits, ldl, type, experts, normalise, scale, d_weights,
+                      d_logits, ldd, stream=None):
+    """The gradient of the logits from that of the weights (see the C header)."""
+    return _check(load().expert_route_grad(int(score), int(T), int(E), int(top), _ptr(logits),
+                                           int(ldl), int(type), _ptr(experts), int(normalise),
+                                           float(scale), _ptr(d_weights), _ptr(d_logits), int(ldd),
+                                           _stream(stream)), "expert_route_grad")
+
+
+def expert_dispatch(T, R, D, top, X, ldx, type, position, rows, ldr, stream=None):
+    """rows[position[t, j]] = X[t] (see the C header)."""
+    return _check(load().expert_dispatch(int(T), int(R), int(D), int(top), _ptr(X), int(ldx),
+                                         int(type), _ptr(position), _ptr(rows), int(ldr),
+                                         _stream(stream)), "expert_dispatch")
+
+
+def expert_combine(T, R, D, top, rows, ldr, type, position, weights, beta, out, ldo, stream=None):
+    """out[t] = sum_j weights[t, j] rows[position[t, j]] + beta out[t] (see the C header)."""
+    return _check(load().expert_combine(int(T), int(R), int(D), int(top), _ptr(rows), int(ldr),
+                                        int(type), _ptr(position), _ptr(weights), float(beta),
+                                        _ptr(out), int(ldo), _stream(stream)), "expert_combine")
+
+
+def expert_combine_grad(T, R, D, top, d_out, ldd, rows, ldr, type, position, weights, d_rows, lddr,
+                        d_weights, stream=None):
+    """The gradients of expert_combine in rows and weights (see the C header)."""
+    return _check(load().expert_combine_grad(int(T), int(R), int(D), int(top), _ptr(d_out), int(ldd),
+                                             _ptr(rows), int(ldr), int(type), _ptr(position),
+                                             _ptr(weights), _ptr(d_rows), int(lddr),
+                                             _ptr(d_weights), _stream(stream)),
+                  "expert_combine_grad")
+
+
+def w4_quantize(G, N, K, X, ldx, xtype, group, Q, S, Z, lds, stype, stream=None):
+    """X to 4-bit codes, group scales and zero points (see the C header)."""
+    return _check(load().w4_quantize(int(G), int(N), int(K), _ptr(X), int(ldx), int(xtype),
+                                     int(group), _ptr(Q), _ptr(S), _ptr(Z), int(lds), int(stype),
+                                     _stream(stream)), "w4_quantize")
+
+
+def w4_dequantize(G, N, K, Q, S, Z, lds, stype, group, X, ldx, xtype, stream=None):
+    """The values of 4-bit weights (see the C header)."""
+    return _check(load().w4_dequantize(int(G), int(N), int(K), _ptr(Q), _ptr(S), _ptr(Z), int(lds),
+                                       int(stype), int(group), _ptr(X), int(ldx), int(xtype),
+                                       _stream(stream)), "w4_dequantize")
+
+
+def gemm_w4(G, M, N, K, alpha, A, lda, Q, S, Z, lds, group, offsets, beta, C, ldc, type, ctype,
+            stream=None):
+    """C = alpha * A W_g^T + beta * C with weights of 4 bits (see the C header)."""
+    return _check(load().gemm_w4(int(G), int(M), int(N), int(K), float(alpha), _ptr(A), int(lda),
+                                 _ptr(Q), _ptr(S), _ptr(Z), int(lds), int(group), _ptr(offsets),
+                                 float(beta), _ptr(C), int(ldc), int(type), int(ctype),
+                                 _stream(stream)), "gemm_w4")
+
+
+def swiglu_w4(G, M, N, K, alpha, A, lda, Q, S, Z, lds, group, offsets, Y, ldy, type, stream=None):
+    """Y = SiLU(alpha A W1_g^T) (.) (alpha A W2_g^T), weights of 4 bits (see the C header)."""
+    return _check(load().swiglu_w4(int(G), int(M), int(N), int(K), float(alpha), _ptr(A), int(lda),
+                                   _ptr(Q), _ptr(S), _ptr(Z), int(lds), int(group), _ptr(offsets),
+                                   _ptr(Y), int(ldy), int(type), _stream(stream)), "swiglu_w4")
 
 
 def status_string(status: int) -> str:
@@ -690,4 +794,303 @@ def swiglu_mx4_into(Y, Q, S, W, SW, K, format, alpha=1.0, offsets=None, stream=N
     rc = lib.swiglu_mx4(format, Q, S, W, SW, Y, offsets, G, M, N2 // 2, K, alpha, s, dev)
     if rc:
         _failed(rc, w, "swiglu_mx4")
+    return Y
+
+
+# ------------------------------------------------------ tensor helpers, routing
+
+def expert_plan_alloc(T, E, top, device="cuda"):
+    """(offsets, source, position) for expert_route_into and expert_sort_into."""
+    import torch
+    return tuple(torch.empty(n, dtype=torch.int32, device=device) for n in (E + 1, T * top, (T, top)))
+
+
+def _slots(w, name, t, T, top, dtype):
+    """A contiguous [T, top] tensor of slots."""
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 2 or shape[0] != T or shape[1] != top \
+            or not t.is_contiguous():
+        _refuse(w, f"{name} must be a contiguous [{T}, {top}] {dtype} tensor")
+
+
+def _plan(w, plan, T, E, top, int32):
+    offsets, source, position = plan
+    if offsets.dtype is not int32 or len(offsets.shape) != 1 or not offsets.is_contiguous() \
+            or (offsets.shape[0] != E + 1 if E is not None else offsets.shape[0] < 2):
+        _refuse(w, "offsets must be a contiguous 1-D int32 tensor of E + 1 values")
+    if source.dtype is not int32 or len(source.shape) != 1 or source.shape[0] != T * top \
+            or not source.is_contiguous():
+        _refuse(w, f"source must be a contiguous [{T * top}] int32 tensor")
+    _slots(w, "position", position, T, top, int32)
+    return offsets, source, position
+
+
+def _pair(w, name, t):
+    """(T, top) of a tensor of slots."""
+    shape = t.shape
+    if len(shape) != 2:
+        _refuse(w, f"{name} must be a [T, top] tensor")
+    return shape[0], shape[1]
+
+
+def expert_route_into(experts, weights, logits, score=SOFTMAX, bias=None, groups=1, top_groups=None,
+                      group_sum=1, normalise=True, scale=1.0, plan=None, stream=None):
+    """experts int32 [T, top], weights float32 [T, top] <- the router's choice for
+    logits [T, E], best first (-1 and 0 where a slot has no expert); plan, when
+    given (expert_plan_alloc), receives the rows sorted by expert.  top_groups:
+    all of them by default."""
+    w = "expert_route_into"
+    torch = _torch or _fast()
+    lib = _bound
+    T, E, ld = _matrix(logits, "logits", w)
+    Te, top = _pair(w, "experts", experts)
+    _slots(w, "experts", experts, T, top, torch.int32)
+    _slots(w, "weights", weights, T, top, torch.float32)
+    if bias is not None and (bias.dtype is not torch.float32 or bias.dim() != 1 or bias.shape[0] != E
+                             or not bias.is_contiguous()):
+        _refuse(w, f"bias must be a contiguous [{E}] float32 tensor")
+    offsets = source = position = None
+    if plan is not None:
+        offsets, source, position = _plan(w, plan, T, E, top, torch.int32)
+    s, dev = _place(stream)
+    rc = lib.expert_route(score, T, E, top, logits, ld, _type_code(logits.dtype, w), bias, groups,
+                          groups if top_groups is None else top_groups, group_sum, bool(normalise),
+                          scale, experts, weights, offsets, source, position, s, dev)
+    if rc:
+        _failed(rc, w, "expert_route")
+    return experts, weights
+
+
+def expert_sort_into(plan, experts, stream=None):
+    """plan (expert_plan_alloc) <- rows sorted by expert, for experts int32 [T, top]."""
+    w = "expert_sort_into"
+    torch = _torch or _fast()
+    lib = _bound
+    T, top = _pair(w, "experts", experts)
+    _slots(w, "experts", experts, T, top, torch.int32)
+    offsets, source, position = _plan(w, plan, T, None, top, torch.int32)
+    s, dev = _place(stream)
+    rc = lib.expert_sort(T, offsets.shape[0] - 1, top, experts, offsets, source, position, s, dev)
+    if rc:
+        _failed(rc, w, "expert_sort")
+    return plan
+
+
+def expert_route_grad_into(d_logits, d_weights, logits, experts, score=SOFTMAX, normalise=True,
+                           scale=1.0, stream=None):
+    """d_logits [T, E] <- the gradient of expert_route_into's weights in the logits,
+    from d_weights float32 [T, top]."""
+    w = "expert_route_grad_into"
+    torch = _torch or _fast()
+    lib = _bound
+    T, E, ld = _matrix(logits, "logits", w)
+    Td, Ed, ldd = _matrix(d_logits, "d_logits", w)
+    Te, top = _pair(w, "experts", experts)
+    _slots(w, "experts", experts, T, top, torch.int32)
+    _slots(w, "d_weights", d_weights, T, top, torch.float32)
+    if Td != T or Ed != E or d_logits.dtype is not logits.dtype:
+        _refuse(w, "d_logits must have the shape and type of logits")
+    s, dev = _place(stream)
+    rc = lib.expert_route_grad(score, T, E, top, logits, ld, _type_code(logits.dtype, w), experts,
+                               bool(normalise), scale, d_weights, d_logits, ldd, s, dev)
+    if rc:
+        _failed(rc, w, "expert_route_grad")
+    return d_logits
+
+
+def _weights_of(w, weights, T, top, float32):
+    if weights is not None:
+        _slots(w, "weights", weights, T, top, float32)
+
+
+def expert_dispatch_into(rows, X, position, stream=None):
+    """rows[position[t, j]] <- X[t] for every slot with a row (position int32
+    [T, top], -1 where a slot has none); other rows keep their values."""
+    w = "expert_dispatch_into"
+    torch = _torch or _fast()
+    lib = _bound
+    T, D, ldx = _matrix(X, "X", w)
+    R, Dr, ldr = _matrix(rows, "rows", w)
+    Tp, top = _pair(w, "position", position)
+    _slots(w, "position", position, T, top, torch.int32)
+    if Dr != D or rows.dtype is not X.dtype:
+        _refuse(w, "inconsistent shapes or dtypes")
+    s, dev = _place(stream)
+    rc = lib.expert_dispatch(T, R, D, top, X, ldx, _type_code(X.dtype, w), position, rows, ldr, s, dev)
+    if rc:
+        _failed(rc, w, "expert_dispatch")
+    return rows
+
+
+def expert_combine_into(out, rows, position, weights=None, beta=0.0, stream=None):
+    """out[t] <- sum_j weights[t, j] * rows[position[t, j]] + beta * out[t] (weights
+    float32 [T, top]; None: ones)."""
+    w = "expert_combine_into"
+    torch = _torch or _fast()
+    lib = _bound
+    T, D, ldo = _matrix(out, "out", w)
+    R, Dr, ldr = _matrix(rows, "rows", w)
+    Tp, top = _pair(w, "position", position)
+    _slots(w, "position", position, T, top, torch.int32)
+    _weights_of(w, weights, T, top, torch.float32)
+    if Dr != D or rows.dtype is not out.dtype:
+        _refuse(w, "inconsistent shapes or dtypes")
+    s, dev = _place(stream)
+    rc = lib.expert_combine(T, R, D, top, rows, ldr, _type_code(out.dtype, w), position, weights,
+                            beta, out, ldo, s, dev)
+    if rc:
+        _failed(rc, w, "expert_combine")
+    return out
+
+
+def expert_combine_grad_into(d_rows, d_weights, d_out, rows, position, weights=None, stream=None):
+    """d_rows[position[t, j]] <- weights[t, j] * d_out[t] and d_weights[t, j] <-
+    <rows[position[t, j]], d_out[t]> (d_weights None: neither computed, and rows
+    may be None)."""
+    w = "expert_combine_grad_into"
+    torch = _torch or _fast()
+    lib = _bound
+    T, D, ldd = _matrix(d_out, "d_out", w)
+    R, Dr, lddr = _matrix(d_rows, "d_rows", w)
+    Tp, top = _pair(w, "position", position)
+    _slots(w, "position", position, T, top, torch.int32)
+    _weights_of(w, weights, T, top, torch.float32)
+    ldr = 0
+    if d_weights is not None:
+        _slots(w, "d_weights", d_weights, T, top, torch.float32)
+        Rr, Dx, ldr = _matrix(rows, "rows", w)
+        if Rr != R or Dx != D or rows.dtype is not d_out.dtype:
+            _refuse(w, "inconsistent shapes or dtypes")
+    else:
+        rows = None
+    if Dr != D or d_rows.dtype is not d_out.dtype:
+        _refuse(w, "inconsistent shapes or dtypes")
+    s, dev = _place(stream)
+    rc = lib.expert_combine_grad(T, R, D, top, d_out, ldd, rows, ldr, _type_code(d_out.dtype, w),
+                                 position, weights, d_rows, lddr, d_weights, s, dev)
+    if rc:
+        _failed(rc, w, "expert_combine_grad")
+    return d_rows, d_weights
+
+
+# ------------------------- tensor helpers, 4-bit weights with group scales
+
+def w4_alloc(N, K, group, dtype, zeros=False, experts=None, device="cuda"):
+    """(Q, S, Z) of a weight [N, K], or of [experts, N, K]: codes, scales of dtype
+    (float16 or bfloat16) and zero points (None without `zeros`)."""
+    import torch
+    lead = () if experts is None else (experts,)
+    shape = lead + (-(-K // group), -(-N // 16) * 16)
+    return (torch.empty(lead + (N, -(-K // 32) * 16), dtype=torch.uint8, device=device),
+            torch.empty(shape, dtype=dtype, device=device),
+            torch.empty(shape, dtype=torch.uint8, device=device) if zeros else None)
+
+
+def _w4_weight(w, Q, S, Z, group, G, K, torch):
+    """(rows of each weight, the scales' row length)."""
+    shape = Q.shape
+    if len(shape) == 2:
+        shape = (1, *shape)
+    if len(shape) != 3 or shape[0] != G or shape[2] != -(-K // 32) * 16 or Q.dtype is not torch.uint8 \
+            or not Q.is_contiguous():
+        _refuse(w, f"Q must be contiguous uint8 [{G}, N, {-(-K // 32) * 16}]")
+    if group not in (32, 64, 128):
+        _refuse(w, "scales are kept for 32, 64 or 128 columns", 3)
+    blocks = -(-K // group)
+    for name, t, dtype in (("S", S, None), ("Z", Z, torch.uint8)):
+        if t is None and dtype is not None:
+            continue
+        of = t.shape
+        if len(of) == 2:
+            of = (1, *of)
+        if len(of) != 3 or of[0] != G or of[1] != blocks or of[2] < shape[1] or of[2] % 16 \
+                or of[2] != S.shape[-1] or not t.is_contiguous() \
+                or (t.dtype is not dtype if dtype else t.dtype not in (torch.float16, torch.bfloat16)):
+            _refuse(w, f"{name} must be contiguous [{G}, {blocks}, at least N, a multiple of 16], S of "
+                       "float16 or bfloat16, Z of uint8")
+    return shape[1], S.shape[-1]
+
+
+def _w4_matrix(w, X):
+    """(G, rows, columns, row stride) of [rows, columns] or [G, rows, columns], whose
+    rows follow one another at one stride."""
+    shape, stride = X.shape, X.stride()
+    if len(shape) == 2:
+        rows, cols, ld = _matrix(X, "W", w)
+        return 1, rows, cols, ld
+    if len(shape) != 3 or stride[2] != 1:
+        _refuse(w, "W must hold row-major matrices")
+    G, rows, cols = shape
+    ld = stride[1] if rows > 1 else stride[0] if G > 1 else _one_row(cols)
+    if G > 1 and rows > 1 and stride[0] != rows * ld:
+        _refuse(w, "the matrices of W must follow one another")
+    return G, rows, cols, ld
+
+
+def _w4_convert(w, W, Q, S, Z, group):
+    torch = _torch or _fast()
+    G, N, K, ld = _w4_matrix(w, W)
+    rows, lds = _w4_weight(w, Q, S, Z, group, G, K, torch)
+    if rows != N:
+        _refuse(w, "inconsistent shapes")
+    return G, N, K, ld, _type_code(W.dtype, w), lds, _type_code(S.dtype, w)
+
+
+def w4_quantize_into(Q, S, Z, W, group, stream=None):
+    """Q, S, Z (w4_alloc; Z None: symmetric) <- W [N, K] or [G, N, K] in 4 bits."""
+    w = "w4_quantize_into"
+    G, N, K, ld, xtype, lds, stype = _w4_convert(w, W, Q, S, Z, group)
+    s, dev = _place(stream)
+    rc = _bound.w4_quantize(G, N, K, W, ld, xtype, group, Q, S, Z, lds, stype, s, dev)
+    if rc:
+        _failed(rc, w, "w4_quantize")
+    return Q, S, Z
+
+
+def w4_dequantize_into(W, Q, S, Z, group, stream=None):
+    """W [N, K] or [G, N, K] <- the values of the 4-bit weight (Q, S, Z)."""
+    w = "w4_dequantize_into"
+    G, N, K, ld, xtype, lds, stype = _w4_convert(w, W, Q, S, Z, group)
+    s, dev = _place(stream)
+    rc = _bound.w4_dequantize(G, N, K, Q, S, Z, lds, stype, group, W, ld, xtype, s, dev)
+    if rc:
+        _failed(rc, w, "w4_dequantize")
+    return W
+
+
+def gemm_w4_into(C, A, Q, S, Z, group, alpha=1.0, beta=0.0, offsets=None, stream=None):
+    """C[M, N] <- alpha * A[M, K] W_g^T + beta * C with a 4-bit weight (Q, S, Z) of
+    A's type, [N, K] or [G, N, K]; offsets int32 [G + 1] on the GPU, or None."""
+    w = "gemm_w4_into"
+    torch = _torch or _fast()
+    G = _groups(offsets, w)
+    M, K, lda = _matrix(A, "A", w)
+    Mc, Nc, ldc = _matrix(C, "C", w)
+    N, lds = _w4_weight(w, Q, S, Z, group, G, K, torch)
+    if Mc != M or Nc != N or S.dtype is not A.dtype:
+        _refuse(w, "inconsistent shapes or dtypes")
+    s, dev = _place(stream)
+    rc = _bound.gemm_w4(G, M, N, K, alpha, A, lda, Q, S, Z, lds, group, offsets, beta, C, ldc,
+                        _type_code(A.dtype, w), _type_code(C.dtype, w), s, dev)
+    if rc:
+        _failed(rc, w, "gemm_w4")
+    return C
+
+
+def swiglu_w4_into(Y, A, Q, S, Z, group, alpha=1.0, offsets=None, stream=None):
+    """Y[M, N] <- SiLU(alpha A W1_g^T) (.) (alpha A W2_g^T), the weight's 2N rows W1's
+    and W2's in turn; Y and A of one type."""
+    w = "swiglu_w4_into"
+    torch = _torch or _fast()
+    G = _groups(offsets, w)
+    M, K, lda = _matrix(A, "A", w)
+    My, N, ldy = _matrix(Y, "Y", w)
+    rows, lds = _w4_weight(w, Q, S, Z, group, G, K, torch)
+    if My != M or rows != 2 * N or S.dtype is not A.dtype or Y.dtype is not A.dtype:
+        _refuse(w, "inconsistent shapes or dtypes")
+    s, dev = _place(stream)
+    rc = _bound.swiglu_w4(G, M, N, K, alpha, A, lda, Q, S, Z, lds, group, offsets, Y, ldy,
+                          _type_code(A.dtype, w), s, dev)
+    if rc:
+        _failed(rc, w, "swiglu_w4")
     return Y

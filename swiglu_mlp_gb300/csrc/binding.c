@@ -107,11 +107,74 @@ ENTRY(swiglu_mx4, 13)
     int64_t G = I(7), M = I(8), N = I(9), K = I(10); float alpha = F(11); void *st = P(12);
     CALL(swiglu_mx4(f, A, SA, W, SW, Y, off, G, M, N, K, alpha, st))
 
+ENTRY(expert_route, 19)
+    int sc = (int)I(0); int64_t T = I(1), E = I(2), top = I(3); void *L = P(4); int64_t ldl = I(5);
+    int type = (int)I(6); void *bias = P(7); int64_t gr = I(8), tg = I(9); int gs = (int)I(10);
+    int norm = (int)I(11); float scale = F(12); void *ex = P(13), *we = P(14), *off = P(15);
+    void *src = P(16), *pos = P(17), *st = P(18);
+    CALL(expert_route(sc, T, E, top, L, ldl, type, bias, gr, tg, gs, norm, scale, ex, we, off, src,
+                      pos, st))
+
+ENTRY(expert_sort, 8)
+    int64_t T = I(0), E = I(1), top = I(2); void *ex = P(3), *off = P(4), *src = P(5), *pos = P(6);
+    void *st = P(7);
+    CALL(expert_sort(T, E, top, ex, off, src, pos, st))
+
+ENTRY(expert_route_grad, 14)
+    int sc = (int)I(0); int64_t T = I(1), E = I(2), top = I(3); void *L = P(4); int64_t ldl = I(5);
+    int type = (int)I(6); void *ex = P(7); int norm = (int)I(8); float scale = F(9);
+    void *dw = P(10), *dl = P(11); int64_t ldd = I(12); void *st = P(13);
+    CALL(expert_route_grad(sc, T, E, top, L, ldl, type, ex, norm, scale, dw, dl, ldd, st))
+
+ENTRY(expert_dispatch, 11)
+    int64_t T = I(0), R = I(1), D = I(2), top = I(3); void *X = P(4); int64_t ldx = I(5);
+    int type = (int)I(6); void *pos = P(7), *rows = P(8); int64_t ldr = I(9); void *st = P(10);
+    CALL(expert_dispatch(T, R, D, top, X, ldx, type, pos, rows, ldr, st))
+
+ENTRY(expert_combine, 13)
+    int64_t T = I(0), R = I(1), D = I(2), top = I(3); void *rows = P(4); int64_t ldr = I(5);
+    int type = (int)I(6); void *pos = P(7), *we = P(8); float beta = F(9); void *out = P(10);
+    int64_t ldo = I(11); void *st = P(12);
+    CALL(expert_combine(T, R, D, top, rows, ldr, type, pos, we, beta, out, ldo, st))
+
+ENTRY(expert_combine_grad, 15)
+    int64_t T = I(0), R = I(1), D = I(2), top = I(3); void *d = P(4); int64_t ldd = I(5);
+    void *rows = P(6); int64_t ldr = I(7); int type = (int)I(8); void *pos = P(9), *we = P(10);
+    void *dr = P(11); int64_t lddr = I(12); void *dw = P(13), *st = P(14);
+    CALL(expert_combine_grad(T, R, D, top, d, ldd, rows, ldr, type, pos, we, dr, lddr, dw, st))
+
+ENTRY(w4_quantize, 13)
+    int64_t G = I(0), N = I(1), K = I(2); void *X = P(3); int64_t ldx = I(4); int type = (int)I(5);
+    int64_t g = I(6); void *Q = P(7), *S = P(8), *Z = P(9); int64_t lds = I(10);
+    int stype = (int)I(11); void *st = P(12);
+    CALL(w4_quantize(G, N, K, X, ldx, type, g, Q, S, Z, lds, stype, st))
+
+ENTRY(w4_dequantize, 13)
+    int64_t G = I(0), N = I(1), K = I(2); void *Q = P(3), *S = P(4), *Z = P(5); int64_t lds = I(6);
+    int stype = (int)I(7); int64_t g = I(8); void *X = P(9); int64_t ldx = I(10);
+    int type = (int)I(11); void *st = P(12);
+    CALL(w4_dequantize(G, N, K, Q, S, Z, lds, stype, g, X, ldx, type, st))
+
+ENTRY(gemm_w4, 19)
+    int64_t G = I(0), M = I(1), N = I(2), K = I(3); float alpha = F(4); void *A = P(5);
+    int64_t lda = I(6); void *Q = P(7), *S = P(8), *Z = P(9); int64_t lds = I(10), g = I(11);
+    void *off = P(12); float beta = F(13); void *C = P(14); int64_t ldc = I(15);
+    int type = (int)I(16), ctype = (int)I(17); void *st = P(18);
+    CALL(gemm_w4(G, M, N, K, alpha, A, lda, Q, S, Z, lds, g, off, beta, C, ldc, type, ctype, st))
+
+ENTRY(swiglu_w4, 17)
+    int64_t G = I(0), M = I(1), N = I(2), K = I(3); float alpha = F(4); void *A = P(5);
+    int64_t lda = I(6); void *Q = P(7), *S = P(8), *Z = P(9); int64_t lds = I(10), g = I(11);
+    void *off = P(12), *Y = P(13); int64_t ldy = I(14); int type = (int)I(15); void *st = P(16);
+    CALL(swiglu_w4(G, M, N, K, alpha, A, lda, Q, S, Z, lds, g, off, Y, ldy, type, st))
+
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {
     METHOD(gemm_grouped), METHOD(gemm_grouped_wgrad), METHOD(swiglu_grouped),
     METHOD(swiglu_grouped_grad), METHOD(mx4_quantize), METHOD(mx4_dequantize), METHOD(gemm_mx4),
-    METHOD(swiglu_mx4), {NULL, NULL, 0, NULL}};
+    METHOD(swiglu_mx4), METHOD(expert_route), METHOD(expert_sort), METHOD(expert_route_grad),
+    METHOD(expert_dispatch), METHOD(expert_combine), METHOD(expert_combine_grad),
+    METHOD(w4_quantize), METHOD(w4_dequantize), METHOD(gemm_w4), METHOD(swiglu_w4), {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};

@@ -195,4 +195,58 @@ __device__ __forceinline__ int group_of(const int *first, int G, int per, int u)
     return lo;
 }
 
+// The unit'th chunk of at most PER rows over all groups: its group, first row and
+// rows; false beyond the last.  By whole warps, without shared memory; offsets are
+// clamped as in group_starts.
+template <int PER>
+__device__ __forceinline__ bool find_chunk(const Groups &gr, int unit, int *err, int &g, int &row0,
+                                           int &rows)
+{
+    const int lane = threadIdx.x & 31;
+    if (gr.offsets == nullptr) {
+        g = 0;
+        row0 = unit * PER;
+        rows = min(PER, gr.M - row0);
+        return rows > 0;
+    }
+    int top = 0, before = 0;                         // largest offset and chunks so far
+    bool bad = false;
+    for (int base = 0; base < gr.G; base += 32) {
+        const int a = gr.offsets[min(base + lane, gr.G)], b = gr.offsets[min(base + lane + 1, gr.G)];
+        int lo = a < 0 ? 0 : a > gr.M ? gr.M : a, hi = b < 0 ? 0 : b > gr.M ? gr.M : b;
+        bad = bad || lo != a || hi != b || hi < lo;
+        lo = max(lo, top);
+        hi = max(hi, lo);
+        if (__any_sync(0xffffffffu, bad)) {          // running maxima, the slow way
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, hi, d);
+                if (lane >= d) hi = max(hi, o);
+            }
+            const int o = __shfl_up_sync(0xffffffffu, hi, 1);
+            if (lane > 0) lo = max(lo, o);
+            if (lane == 0) atomicCAS(err, 0, ERR_INVALID);
+        }
+        const int n = base + lane < gr.G ? ceil_div(hi - lo, PER) : 0;
+        const int all = __reduce_add_sync(0xffffffffu, n);
+        if (unit < before + all) {
+            int sum = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += o;
+            }
+            const int first = before + sum - n;
+            const int src = __ffs(__ballot_sync(0xffffffffu, unit >= first && unit < first + n)) - 1;
+            g = base + src;
+            row0 = __shfl_sync(0xffffffffu, lo, src) + (unit - __shfl_sync(0xffffffffu, first, src)) * PER;
+            rows = min(PER, __shfl_sync(0xffffffffu, hi, src) - row0);
+            return true;
+        }
+        before += all;
+        top = __shfl_sync(0xffffffffu, hi, 31);
+    }
+    return false;
+}
+
 }  // namespace swg

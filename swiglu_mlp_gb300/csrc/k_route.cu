@@ -1,0 +1,742 @@
+// k_route.cu — the router: the experts of each token with their weights, rows
+// sorted by expert, and the gradient of the logits.
+//
+// A warp has a token, lane l the experts l, l + 32, ..; the best of them are
+// taken one after the other by a maximum over the warp, the lowest index of
+// equals.  Without a bias the order of the scores is that of the logits, which
+// compare exactly.  With one, or where groups are valued by a sum, the choices
+// (score + bias) are formed in FP32 and compared with a bound of their error;
+// where two are nearer than that, and not the same logit and bias, the token is
+// decided once more in FP64.  So the choice is that of the definition, whatever
+// the rounding of the exponential.
+//
+// Sorting is counting: every chunk of tokens counts its experts in shared memory,
+// and the second kernel adds up the chunks before its own and ranks its slots
+// in order.  (One chunk: the same CTA goes on, without a second kernel.)
+#include <algorithm>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "groups.cuh"
+#include "launch.h"
+#include "routing.h"
+
+namespace swg {
+namespace {
+
+constexpr unsigned ALL = 0xffffffffu;
+constexpr int RANK_WARPS = 8;          // warps that rank a chunk's slots
+constexpr int SORT_THREADS = 512;
+
+__device__ __forceinline__ float load_any(const void *x, long long i, int type)
+{
+    if (type == 2) return static_cast<const float *>(x)[i];
+    if (type == 1) return __bfloat162float(static_cast<const __nv_bfloat16 *>(x)[i]);
+    return __half2float(static_cast<const __half *>(x)[i]);
+}
+
+__device__ __forceinline__ void store_any(void *x, long long i, float v, int type)
+{
+    if (type == 2)
+        static_cast<float *>(x)[i] = v;
+    else if (type == 1)
+        static_cast<__nv_bfloat16 *>(x)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half *>(x)[i] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ float minus_inf() { return __int_as_float(0xff800000); }
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(ALL, v, d);
+    return v;
+}
+__device__ __forceinline__ double warp_sum(double v)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(ALL, v, d);
+    return v;
+}
+
+// Unsigned numbers in the order of the values (not NaN), equal zeros equal; more than 0.
+__device__ __forceinline__ uint32_t ordered(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.0f);      // (-0 becomes 0)
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t ordered(double x)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
+    return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ float value_of(uint32_t k)
+{
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(ALL, k); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t k)
+{
+    const uint32_t hi = __reduce_max_sync(ALL, (uint32_t)(k >> 32));
+    const uint32_t lo = __reduce_max_sync(ALL, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+    return (uint64_t)hi << 32 | lo;
+}
+
+__device__ __forceinline__ float max_of_row(float m)
+{
+    return value_of(warp_max(ordered(m)));
+}
+
+// Takes the largest key (lane l, place i: expert l + 32 i) out, the lowest expert of
+// equals; -1 when none is left.
+template <int V>
+__device__ __forceinline__ int take_best(uint32_t (&key)[V], uint32_t &best)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t k = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+        if (key[i] > k) {
+            k = key[i];
+            at = i;
+        }
+    best = warp_max(k);
+    if (best == 0) return -1;
+    const int e = (int)__reduce_min_sync(ALL, k == best ? (unsigned)(lane + 32 * at) : 0xffffffffu);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (lane + 32 * i == e) key[i] = 0;
+    return e;
+}
+
+// Place of expert e's choice in a warp's scratch: one value further for every
+// 32, so that groups of 32 do not share banks.
+__device__ __forceinline__ int at_scratch(int e) { return e + (e >> 5); }
+
+// The best groups as a bit mask, from the choices in the warp's scratch (-inf
+// where masked).  `tol` > 0: `sure` becomes false where the values of two groups
+// that decide are nearer than it.
+template <class F>
+__device__ unsigned best_groups(const RouteArgs &p, const F *scratch, F tol, bool &sure)
+{
+    const int lane = threadIdx.x & 31, size = p.E / p.groups;
+    int log_lanes = 0;                               // lanes per group, a power of two
+    while ((p.groups << (log_lanes + 1)) <= 32) ++log_lanes;
+    const int lanes = 1 << log_lanes, g = lane >> log_lanes;
+    const F low = (F)minus_inf();
+    F a = low, b = low;                              // the two largest
+    if (g < p.groups)
+        for (int i = lane & (lanes - 1); i < size; i += lanes) {
+            const F v = scratch[at_scratch(g * size + i)];
+            if (v > a) {
+                b = a;
+                a = v;
+            } else if (v > b) {
+                b = v;
+            }
+        }
+    for (int d = 1; d < lanes; d <<= 1) {
+        const F a2 = __shfl_xor_sync(ALL, a, d), b2 = __shfl_xor_sync(ALL, b, d);
+        b = a2 > a ? (a > b2 ? a : b2) : (a2 > b ? a2 : b);
+        a = a2 > a ? a2 : a;
+    }
+    const F value = p.group_sum == 2 && b > low ? a + b : a;
+    auto key = ordered(value);
+    if (!(a > low) || (lane & (lanes - 1)) != 0) key = 0;
+    unsigned keep = 0;
+    F before = (F)0;
+    for (int j = 0; j <= p.top_groups; ++j) {
+        const auto best = warp_max(key);
+        if (best == 0) break;
+        const int who = (int)__reduce_min_sync(ALL, key == best ? (unsigned)lane : 32u);
+        const F now = __shfl_sync(ALL, value, who);
+        if (tol > (F)0 && j > 0 && !(before - now > tol)) sure = false;
+        before = now;
+        if (j < p.top_groups) keep |= 1u << (who >> log_lanes);
+        if (lane == who) key = 0;
+    }
+    return keep;
+}
+
+// The token's experts in FP64: lane j's is the j'th.  Seldom called: its arrays
+// are in local memory, so that it takes no registers from the rest.
+template <int V>
+__device__ __noinline__ int choose_exactly(const RouteArgs &p, long long row, double *scratch)
+{
+    const int lane = threadIdx.x & 31, size = p.E / p.groups;
+    const double low = (double)minus_inf();
+    double c[V];
+    uint64_t key[V];
+    double m = low;
+#pragma unroll 1
+    for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        c[i] = e < p.E ? (double)load_any(p.logits, row + e, p.type) : low;
+        m = c[i] > m ? c[i] : m;
+    }
+    for (int d = 16; d > 0; d >>= 1) {
+        const double o = __shfl_xor_sync(ALL, m, d);
+        m = o > m ? o : m;
+    }
+    double z = 0.0;
+    uint32_t masked = 0;
+#pragma unroll 1
+    for (int i = 0; i < V; ++i) {
+        if (c[i] == low) masked |= 1u << i;
+        if (p.score == SCORE_SOFTMAX) {
+            c[i] = c[i] == low ? 0.0 : exp(c[i] - m);
+            z += c[i];
+        } else {
+            c[i] = 1.0 / (1.0 + exp(-c[i]));
+        }
+    }
+    z = p.score == SCORE_SOFTMAX ? warp_sum(z) : 1.0;
+#pragma unroll 1
+    for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        c[i] /= z;
+        if (p.bias != nullptr && e < p.E) c[i] += (double)p.bias[e];
+        if (c[i] == low) masked |= 1u << i;
+        key[i] = masked >> i & 1 ? 0 : ordered(c[i]);
+    }
+    if (p.groups > 1) {
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            if (e < p.E) scratch[at_scratch(e)] = masked >> i & 1 ? low : c[i];
+        }
+        __syncwarp();
+        bool sure = true;
+        const unsigned keep = best_groups<double>(p, scratch, 0.0, sure);
+#pragma unroll 1
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            if (e >= p.E || !(keep >> (e / size) & 1)) key[i] = 0;
+        }
+    }
+    int mine = -1;
+    for (int j = 0; j < p.top; ++j) {
+        uint64_t k = 0;
+        int at = 0;
+#pragma unroll 1
+        for (int i = 0; i < V; ++i)
+            if (key[i] > k) {
+                k = key[i];
+                at = i;
+            }
+        const uint64_t best = warp_max(k);
+        if (best == 0) break;
+        const int e = (int)__reduce_min_sync(ALL, k == best ? (unsigned)(lane + 32 * at) : 0xffffffffu);
+        if (lane == e % 32) key[e / 32] = 0;
+        if (lane == j) mine = e;
+    }
+    return mine;
+}
+
+// The experts of a token, lane j's the j'th (-1: none), and lane j's weight.
+template <int V>
+__device__ __forceinline__ int choose(const RouteArgs &p, int t, void *scratch, float &weight)
+{
+    const int lane = threadIdx.x & 31;
+    const long long row = t * p.ld;
+    const bool grouped = p.groups > 1;
+    const bool by_score = p.bias != nullptr || (grouped && p.group_sum == 2);
+    const bool softmax = p.score == SCORE_SOFTMAX;
+    float l[V];
+    float m = minus_inf();
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        l[i] = e < p.E ? load_any(p.logits, row + e, p.type) : minus_inf();
+        nan = nan || l[i] != l[i];
+        m = fmaxf(m, l[i]);
+    }
+    if (softmax || by_score) m = max_of_row(m);
+    nan = nan || (softmax && m == -minus_inf());
+    float z = 1.0f;
+    uint32_t key[V];
+    bool sure = true;
+    float tol = 0.0f;
+    if (by_score) {
+        float s[V];
+        if (softmax) {
+            // summed as a tree of four, which keeps its error below the bound used here
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s[i] = l[i] == minus_inf() ? 0.0f : expf(l[i] - m);
+                sum[i % 4] += s[i];
+            }
+            z = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+            if (z == 0.0f) z = 1.0f;                 // all masked
+        }
+        // A score is off by at most: its exponential's 2 units and argument's
+        // rounding (0.37 of a unit of the largest score), the sum's 15 additions,
+        // the division: below 2^-19.5 of the largest score; a sigmoid by 4 units.
+        // Two of them, and the addition of the bias to each.
+        const float largest = softmax ? 1.0f / z : 1.0f / (1.0f + expf(-m));
+        tol = largest * (softmax ? 0x1p-18f : 0x1p-20f);
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            s[i] = softmax ? s[i] / z : 1.0f / (1.0f + expf(-l[i]));
+            if (p.bias != nullptr && e < p.E) s[i] += p.bias[e];
+            nan = nan || s[i] != s[i];
+            const bool masked = l[i] == minus_inf() || s[i] == minus_inf();
+            if (!masked) most = fmaxf(most, fabsf(s[i]));
+            key[i] = masked ? 0u : p.bias != nullptr ? ordered(s[i]) : ordered(l[i]);
+            if (grouped && e < p.E)
+                static_cast<float *>(scratch)[at_scratch(e)] = masked ? minus_inf() : s[i];
+        }
+        // (2^-120: scores that FP32 has no digits left for)
+        tol += 0x1p-22f * max_of_row(most) + 0x1p-120f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            key[i] = l[i] == minus_inf() ? 0u : ordered(l[i]);
+            if (grouped && e < p.E) static_cast<float *>(scratch)[at_scratch(e)] = l[i];
+        }
+    }
+    if (__any_sync(ALL, nan)) {
+        weight = __int_as_float(0x7fffffff);
+        return lane < p.top ? lane : -1;
+    }
+    if (grouped) {
+        __syncwarp();
+        const unsigned keep = best_groups<float>(p, static_cast<float *>(scratch), 2.0f * tol, sure);
+        __syncwarp();
+        // e / size by a product: exact for e, size <= 1024
+        const unsigned size = p.E / p.groups, inverse = ((1u << 22) + size - 1) / size;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const unsigned e = lane + 32 * i;
+            if ((int)e >= p.E || !(keep >> (e * inverse >> 22) & 1)) key[i] = 0;
+        }
+    }
+    int mine = -1;
+    if (p.bias == nullptr) {
+        for (int j = 0; j < p.top && sure; ++j) {
+            uint32_t best;
+            const int e = take_best<V>(key, best);
+            if (e < 0) break;
+            if (lane == j) mine = e;
+        }
+    } else {
+        int last = -1;
+        float before = 0.0f;
+        for (int j = 0; sure; ++j) {                 // on to the first that is surely behind the last chosen
+            uint32_t best;
+            const int e = take_best<V>(key, best);
+            if (e < 0) break;
+            const float now = value_of(best);
+            const bool apart = j == 0 || before - now > tol;
+            if (!apart) {
+                const float x = load_any(p.logits, row + e, p.type), y = load_any(p.logits, row + last, p.type);
+                sure = x == y && p.bias[e] == p.bias[last];
+            }
+            if (j >= p.top && apart) break;
+            if (j < p.top && lane == j) mine = e;
+            before = now;
+            last = e;
+        }
+    }
+    if (!sure) mine = choose_exactly<V>(p, row, static_cast<double *>(scratch));
+
+    // Weights: scores of the chosen, from their logits.
+    const bool on = mine >= 0;
+    const float x = on ? load_any(p.logits, row + mine, p.type) : minus_inf();
+    float s;
+    if (!p.normalise) {
+        if (softmax) {
+            if (!by_score) {
+                z = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) z += l[i] == minus_inf() ? 0.0f : expf(l[i] - m);
+                z = warp_sum(z);
+            }
+            s = on ? expf(x - m) / z : 0.0f;
+        } else {
+            s = 1.0f / (1.0f + expf(-x));
+        }
+        weight = on ? p.scale * s : 0.0f;
+    } else {
+        // What the scores have in common cancels: the chosen experts' own
+        // softmax; of sigmoids too where all are so small that 1 + e^x is 1,
+        // and their sum may be 0 in FP32.
+        const float top = max_of_row(x);
+        if (softmax || top < -40.0f)
+            s = on ? expf(x - top) : 0.0f;
+        else
+            s = on ? 1.0f / (1.0f + expf(-x)) : 0.0f;
+        const float sum = warp_sum(s);
+        weight = on ? p.scale * (s / sum) : 0.0f;
+    }
+    return mine;
+}
+
+// ------------------------------------------------------------------- plan
+
+__host__ __device__ constexpr int sort_ints(int E) { return 2 * (E + 1) + 64 + RANK_WARPS * E; }
+
+// The slots lo .. hi - 1 into the plan.  total[e], before[e] (shared): how many
+// slots have expert e in all, and before lo.  NT threads, all of them; `room`:
+// RANK_WARPS * E + 64 more ints.
+template <int NT>
+__device__ void rank_slots(const int32_t *experts, int lo, int hi, int slots, int E, const Plan &plan,
+                           int *total, const int *before, int *room)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *sums = room, *start = room + 64;            // start[w][e]: the next place of warp w's slots of e
+    const int per = ((hi - lo + RANK_WARPS - 1) / RANK_WARPS + 31) & ~31;
+    const int from = min(lo + warp * per, hi), to = warp < RANK_WARPS ? min(from + per, hi) : from;
+    for (int i = tid; i < RANK_WARPS * E; i += NT) start[i] = 0;
+    __syncthreads();
+    if (warp < RANK_WARPS)
+        for (int i = from + lane; i < to; i += 32) {
+            const int e = experts[i];
+            if ((unsigned)e < (unsigned)E) atomicAdd(&start[warp * E + e], 1);
+        }
+    // total becomes its running sum: where each expert begins
+    int carried = 0;
+    for (int base = 0; base < E; base += NT) {
+        const int e = base + tid, n = e < E ? total[e] : 0;
+        int v = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(ALL, v, d);
+            if (lane >= d) v += o;
+        }
+        if (lane == 31) sums[warp] = v;
+        __syncthreads();
+        int lower = 0, all = 0;
+        for (int w = 0; w < NT / 32; ++w) {
+            const int o = sums[w];
+            lower += w < warp ? o : 0;
+            all += o;
+        }
+        if (e < E) total[e] = carried + lower + v - n;
+        carried += all;
+        __syncthreads();
+    }
+    for (int e = tid; e < E; e += NT) {
+        int next = total[e] + before[e];
+        if (blockIdx.x == 0) plan.offsets[e] = total[e];
+#pragma unroll
+        for (int w = 0; w < RANK_WARPS; ++w) {
+            const int n = start[w * E + e];
+            start[w * E + e] = next;
+            next += n;
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0) plan.offsets[E] = carried;
+    __syncthreads();
+    if (warp < RANK_WARPS)
+        for (int i = from; i < to; i += 32) {
+            const int slot = i + lane;
+            const int e = slot < to ? experts[slot] : -1;
+            const bool on = (unsigned)e < (unsigned)E;
+            const unsigned peers = __match_any_sync(ALL, on ? e : -1);
+            int place = -1;
+            if (on) place = start[warp * E + e] + __popc(peers & ((1u << lane) - 1));
+            __syncwarp();
+            if (on && (peers >> lane) == 1u) start[warp * E + e] = place + 1;   // the last of its peers
+            __syncwarp();
+            if (slot < to) plan.position[slot] = place;
+            if (on) plan.source[place] = slot;
+        }
+    for (int r = carried + blockIdx.x * NT + tid; r < slots; r += gridDim.x * NT) plan.source[r] = -1;
+}
+
+// The tokens of chunk c of n.
+__device__ __forceinline__ void chunk_of(int T, int n, int c, int &from, int &to)
+{
+    const int per = (T + n - 1) / n;
+    from = min((long long)c * per, (long long)T);
+    to = min(from + per, T);
+}
+
+template <int V, int NT>
+__global__ void __launch_bounds__(NT) route_kernel(const RouteArgs p, int scratch_bytes, int32_t *counts)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    extern __shared__ __align__(16) unsigned char shared[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned char *scratch = shared + warp * scratch_bytes;
+    int *count = reinterpret_cast<int *>(shared + (NT / 32) * scratch_bytes);
+    const bool planned = p.plan.offsets != nullptr;
+    if (planned) {
+        for (int e = tid; e < 2 * p.E; e += NT) count[e] = 0;       // and, of one chunk, those before it: none
+        __syncthreads();
+    }
+    int from, to;
+    chunk_of(p.T, gridDim.x, blockIdx.x, from, to);
+    for (int t = from + warp; t < to; t += NT / 32) {
+        float weight;
+        const int e = choose<V>(p, t, scratch, weight);
+        if (lane < p.top) {
+            p.experts[(long long)t * p.top + lane] = e;
+            p.weights[(long long)t * p.top + lane] = weight;
+            if (planned && e >= 0) atomicAdd(&count[e], 1);
+        }
+        __syncwarp();
+    }
+    if (!planned) return;
+    __syncthreads();
+    if (gridDim.x > 1) {
+        for (int e = tid; e < p.E; e += NT) counts[(long long)blockIdx.x * p.E + e] = count[e];
+        return;
+    }
+    rank_slots<NT>(p.experts, 0, p.T * p.top, p.T * p.top, p.E, p.plan, count, count + p.E, count + 2 * p.E);
+}
+
+__global__ void __launch_bounds__(SORT_THREADS)
+    count_kernel(int T, int E, int top, const int32_t *experts, int32_t *counts)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    extern __shared__ __align__(16) unsigned char shared[];
+    int *count = reinterpret_cast<int *>(shared);
+    for (int e = threadIdx.x; e < E; e += SORT_THREADS) count[e] = 0;
+    __syncthreads();
+    int from, to;
+    chunk_of(T, gridDim.x, blockIdx.x, from, to);
+    for (int i = from * top + threadIdx.x; i < to * top; i += SORT_THREADS) {
+        const int e = experts[i];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += SORT_THREADS) counts[(long long)blockIdx.x * E + e] = count[e];
+}
+
+// counts == nullptr: one chunk, counted here.
+__global__ void __launch_bounds__(SORT_THREADS)
+    sort_kernel(int T, int E, int top, const int32_t *experts, Plan plan, const int32_t *counts, int *err)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    extern __shared__ __align__(16) unsigned char shared[];
+    int *total = reinterpret_cast<int *>(shared), *before = total + E;
+    const int tid = threadIdx.x;
+    for (int e = tid; e < 2 * E; e += SORT_THREADS) total[e] = 0;
+    __syncthreads();
+    int from, to;
+    chunk_of(T, gridDim.x, blockIdx.x, from, to);
+    from *= top;
+    to *= top;
+    bool bad = false;
+    if (counts == nullptr) {
+        for (int i = from + tid; i < to; i += SORT_THREADS) {
+            const int e = experts[i];
+            if ((unsigned)e < (unsigned)E) atomicAdd(&total[e], 1);
+        }
+    } else {
+        // a row of counts per chunk: several threads per column, a part of the rows each
+        const int parts = max(SORT_THREADS / E, 1), part = tid / E;
+        if (part < parts)
+            for (int e = tid - part * E; e < E; e += SORT_THREADS) {
+                int all = 0, lower = 0;
+#pragma unroll 8
+                for (int c = part; c < (int)gridDim.x; c += parts) {
+                    const int n = counts[(long long)c * E + e];
+                    all += n;
+                    lower += c < (int)blockIdx.x ? n : 0;
+                }
+                atomicAdd(&total[e], all);
+                atomicAdd(&before[e], lower);
+            }
+    }
+    if (err != nullptr)
+        for (int i = from + tid; i < to; i += SORT_THREADS) bad = bad || experts[i] < -1 || experts[i] >= E;
+    if (__syncthreads_or(bad) && tid == 0) atomicCAS(err, 0, ERR_INVALID);
+    rank_slots<SORT_THREADS>(experts, from, to, T * top, E, plan, total, before, before + E);
+}
+
+// --------------------------------------------------------------- gradient
+
+// Of the weights scale * p_j (p the scores of the chosen, normalised or not) in
+// the logits.  Normalised: softmax p_j (d_j - sum p d), sigmoid that times 1 - s_j,
+// zero for experts that were not chosen.  Not: softmax s_e (g_e - sum g s) with
+// g_e the d of e's slots, sigmoid s_j (1 - s_j) d_j.  One pass over the logits, a
+// warp per token.
+template <int V>
+__global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradArgs p, int *err)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    const bool softmax = p.score == SCORE_SOFTMAX;
+    const long long row = t * p.ld, out = t * p.ldd, slot = (long long)t * p.top + lane;
+    int mine = lane < p.top ? p.experts[slot] : -1;
+    const bool wrong = mine < -1 || mine >= p.E;
+    if (__any_sync(ALL, wrong) && lane == 0) atomicCAS(err, 0, ERR_INVALID);
+    if (wrong) mine = -1;
+    const bool on = mine >= 0;
+    const float d = on ? p.scale * p.d_weights[slot] : 0.0f;
+    const float x = on ? load_any(p.logits, row + mine, p.type) : minus_inf();
+    float l[V];
+    float g = d;                                     // what the slot gives its expert's logit
+    float sum = 0.0f, z = 1.0f, m = 0.0f;
+    bool full = softmax && !p.normalise;             // every logit has a gradient
+    if (p.normalise) {
+        const float top = max_of_row(x);
+        float s = 0.0f;
+        if (on) s = softmax || top < -40.0f ? expf(x - top) : 1.0f / (1.0f + expf(-x));
+        const float all = warp_sum(s);
+        const float share = on ? s / all : 0.0f;
+        const float mean = warp_sum(share * d);
+        g = on ? share * (d - mean) : 0.0f;
+        if (!softmax && on) g *= 1.0f / (1.0f + expf(x));
+    } else if (!softmax) {
+        const float s = 1.0f / (1.0f + expf(-x));
+        g = on ? d * s * (1.0f / (1.0f + expf(x))) : 0.0f;
+    }
+    if (full) {
+        m = minus_inf();
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            l[i] = e < p.E ? load_any(p.logits, row + e, p.type) : minus_inf();
+            m = fmaxf(m, l[i]);
+        }
+        m = max_of_row(m);
+        z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            l[i] = l[i] == minus_inf() ? 0.0f : expf(l[i] - m);
+            z += l[i];
+        }
+        z = warp_sum(z);
+        sum = warp_sum(on ? d * (expf(x - m) / z) : 0.0f);
+    }
+    float a[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = 0.0f;
+    for (int j = 0; j < p.top; ++j) {                // in order: an expert may be in several slots
+        const int e = __shfl_sync(ALL, mine, j);
+        const float v = __shfl_sync(ALL, g, j);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane + 32 * i == e) a[i] += v;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        if (e >= p.E) continue;
+        float v = a[i];
+        if (full) v = l[i] == 0.0f ? 0.0f : l[i] / z * (v - sum);
+        store_any(p.d_logits, out + e, v, p.type);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+template <class K, class... A>
+cudaError_t go(K kernel, DeviceOnce &once, int ctas, int threads, size_t shared, cudaStream_t s, A... args)
+{
+    if (shared > 48 * 1024) {
+        int dev = 0;
+        if (cudaError_t e = cudaGetDevice(&dev)) return e;
+        if (once.needed(dev)) {
+            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024))
+                return e;
+            once.mark(dev);
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int V, int NT>
+cudaError_t route_form(const RouteArgs &p, int ctas, int32_t *counts, cudaStream_t s)
+{
+    // choices in FP32, or in FP64 where sums or a bias make that needed
+    const int wide = p.bias != nullptr || p.group_sum == 2 ? 8 : 4;
+    const int scratch = p.groups > 1 ? ((p.E + p.E / 32 + 1) * wide + 15) & ~15 : 0;
+    const size_t shared = (size_t)scratch * (NT / 32) + (p.plan.offsets ? 4 * sort_ints(p.E) : 0);
+    static DeviceOnce once;
+    return go(route_kernel<V, NT>, once, ctas, NT, shared, s, p, scratch, counts);
+}
+
+int values_per_lane(int E) { return (E + 31) / 32; }
+
+}  // namespace
+
+// One chunk (and one kernel) for few tokens; else a CTA per SM at most, with a
+// warp for each of its tokens as far as that goes.
+int plan_chunks(int T, int top, bool route, int sms)
+{
+    if (route) return T <= 64 ? 1 : std::min((T + 31) / 32, sms);
+    return (long long)T * top <= 4096 ? 1 : (int)std::min<long long>(((long long)T * top + 1023) / 1024, sms);
+}
+
+cudaError_t launch_route(const RouteArgs &p, int chunks, int32_t *counts, cudaStream_t s)
+{
+    const int v = values_per_lane(p.E);
+    const int ctas = p.plan.offsets ? chunks : 0;
+#define FORM(V, NT) return route_form<V, NT>(p, ctas ? ctas : (p.T + NT / 32 - 1) / (NT / 32), counts, s)
+    if (ctas) {
+        if (v <= 1) FORM(1, 1024);
+        if (v <= 2) FORM(2, 1024);
+        if (v <= 4) FORM(4, 1024);
+        if (v <= 8) FORM(8, 1024);
+        if (v <= 16) FORM(16, 512);
+        FORM(32, 512);
+    }
+    if (v <= 1) FORM(1, 256);
+    if (v <= 2) FORM(2, 256);
+    if (v <= 4) FORM(4, 256);
+    if (v <= 8) FORM(8, 256);
+    if (v <= 16) FORM(16, 256);
+    FORM(32, 256);
+#undef FORM
+}
+
+cudaError_t launch_count(int T, int E, int top, const int32_t *experts, int chunks, int32_t *counts,
+                         cudaStream_t s)
+{
+    static DeviceOnce once;
+    return go(count_kernel, once, chunks, SORT_THREADS, 4 * (size_t)E, s, T, E, top, experts, counts);
+}
+
+cudaError_t launch_sort(int T, int E, int top, const int32_t *experts, const Plan &plan, int chunks,
+                        int32_t *counts, int *err, cudaStream_t s)
+{
+    static DeviceOnce once;
+    return go(sort_kernel, once, chunks, SORT_THREADS, 4 * (size_t)sort_ints(E), s, T, E, top, experts, plan,
+              (const int32_t *)(chunks > 1 ? counts : nullptr), err);
+}
+
+cudaError_t launch_route_grad(const RouteGradArgs &p, int *err, cudaStream_t s)
+{
+    const int v = values_per_lane(p.E), ctas = (p.T + 7) / 8;
+    static DeviceOnce once;
+    auto with = [&](auto kernel) { return go(kernel, once, ctas, 256, 0, s, p, err); };
+    if (v <= 1) return with(route_grad_kernel<1>);
+    if (v <= 2) return with(route_grad_kernel<2>);
+    if (v <= 4) return with(route_grad_kernel<4>);
+    if (v <= 8) return with(route_grad_kernel<8>);
+    if (v <= 16) return with(route_grad_kernel<16>);
+    return with(route_grad_kernel<32>);
+}
+
+}  // namespace swg
