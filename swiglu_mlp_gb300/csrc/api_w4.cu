@@ -112,7 +112,9 @@ int product(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, const void 
     if (!swg::w4_fits(p)) return SWG_ERR_UNSUPPORTED;
     swg::DeviceInfo d;
     if (int rc = swg::device_info(d)) return rc;
-    return swg::count_launch(swg::launch_w4(p, d.sms, d.err, static_cast<cudaStream_t>(stream)));
+    bool mapped = true;
+    const cudaError_t e = swg::launch_w4(p, d.sms, d.err, static_cast<cudaStream_t>(stream), mapped);
+    return mapped ? swg::count_launch(e) : swg::record_cuda_error();
 }
 
 }  // namespace

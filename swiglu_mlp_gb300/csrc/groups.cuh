@@ -195,20 +195,20 @@ __device__ __forceinline__ int group_of(const int *first, int G, int per, int u)
     return lo;
 }
 
-// The unit'th chunk of at most PER rows over all groups: its group, first row and
-// rows; false beyond the last.  By whole warps, without shared memory; offsets are
-// clamped as in group_starts.
-template <int PER>
-__device__ __forceinline__ bool find_chunk(const Groups &gr, int unit, int *err, int &g, int &row0,
+// The unit'th chunk of at most `per` rows, a power of two, over all groups: its group,
+// first row and rows; false beyond the last.  By whole warps, without shared
+// memory; offsets are clamped as in group_starts.
+__device__ __forceinline__ bool find_chunk(const Groups &gr, int per, int unit, int *err, int &g, int &row0,
                                            int &rows)
 {
     const int lane = threadIdx.x & 31;
     if (gr.offsets == nullptr) {
         g = 0;
-        row0 = unit * PER;
-        rows = min(PER, gr.M - row0);
+        row0 = unit * per;
+        rows = min(per, gr.M - row0);
         return rows > 0;
     }
+    const int shift = __ffs(per) - 1;
     int top = 0, before = 0;                         // largest offset and chunks so far
     bool bad = false;
     for (int base = 0; base < gr.G; base += 32) {
@@ -227,7 +227,7 @@ __device__ __forceinline__ bool find_chunk(const Groups &gr, int unit, int *err,
             if (lane > 0) lo = max(lo, o);
             if (lane == 0) atomicCAS(err, 0, ERR_INVALID);
         }
-        const int n = base + lane < gr.G ? ceil_div(hi - lo, PER) : 0;
+        const int n = base + lane < gr.G ? (hi - lo + per - 1) >> shift : 0;
         const int all = __reduce_add_sync(0xffffffffu, n);
         if (unit < before + all) {
             int sum = n;
@@ -239,8 +239,8 @@ __device__ __forceinline__ bool find_chunk(const Groups &gr, int unit, int *err,
             const int first = before + sum - n;
             const int src = __ffs(__ballot_sync(0xffffffffu, unit >= first && unit < first + n)) - 1;
             g = base + src;
-            row0 = __shfl_sync(0xffffffffu, lo, src) + (unit - __shfl_sync(0xffffffffu, first, src)) * PER;
-            rows = min(PER, __shfl_sync(0xffffffffu, hi, src) - row0);
+            row0 = __shfl_sync(0xffffffffu, lo, src) + (unit - __shfl_sync(0xffffffffu, first, src)) * per;
+            rows = min(per, __shfl_sync(0xffffffffu, hi, src) - row0);
             return true;
         }
         before += all;

@@ -2,8 +2,10 @@
 // C = alpha A W^T + beta C, and SwiGLU over alternating rows of W, dense or by
 // expert.
 //
-// For few rows the weights' bytes are what the operator cannot do without, so the
-// kernel streams them once and keeps the arithmetic behind that.  The rows of
+// For few rows the weights' bytes are what the operator cannot do without; the
+// kernel streams them once, and what bounds it is the decoding: seven shifts and masks
+// for eight codes, on a pipe that takes one every two cycles (4096 x 14336: 3.7 us of
+// it, 4.5 of memory).  The rows of
 // W are the 16 rows of an mma.sync m16n8k16 (FP32 accumulators), up to eight rows
 // of A its columns: at one row of A 7/8 of the instruction's work is for nothing,
 // but it is free, and the rows of W arrive in fragments as they lie in memory:
@@ -14,73 +16,50 @@
 // are scaled in FP32 as a whole, so that no product with a scale is ever rounded to
 // 16 bits.
 //
-// A CTA has 16 MT rows of W and one chunk of rows of A; its eight warps take steps
-// of 128 columns in turn, so that a row's 512 bytes are asked for together.
-// Each warp has a ring of its own in shared memory, filled by cp.async a few
-// steps ahead (codes, scales, zero points and A: no barrier but the warp's), and
-// the warps' sums are added at the end, in order.
+// A CTA has one chunk of at most eight rows of A; its four warps are teams of
+// `team` along K, and each team has 64 rows of W.  A team's warps take steps of 256
+// columns in turn.  Each warp has a ring of its own that TMA fills: a lane asks
+// for a step's codes (64 rows of 128 bytes), scales, zero points and columns of A
+// with an instruction or four each, which leaves the issue slots to the decoding;
+// cp.async by all lanes, with its addresses and edges, took as many instructions
+// again.  A team's sums are added at the end, in order.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "groups.cuh"
+#include "host.h"
 #include "launch.h"
 #include "w4.h"
 
 namespace swg {
 namespace {
 
-constexpr int WARPS = 8;
+constexpr int WARPS = 4;
+constexpr int MT = 4;                    // tiles of 16 rows of W per warp
+constexpr int ROWS = 16 * MT;
 constexpr int TOKENS = 8;                // rows of A per chunk
-constexpr int STEP = 128;                // columns per warp and step
-constexpr int ROW_PITCH = 80;            // bytes of a row's 128 codes in the ring: eight rows' 16-byte
-                                         // pieces, read four bytes a lane, fall on all banks
+constexpr int STEP = 256;                // columns per warp and step
+constexpr int CODES = ROWS * STEP / 2;   // bytes of a step
+constexpr int SUMS = ROWS + 2;           // floats of a row of A's sums, padded
+constexpr int STAGES = 2;
 
-// Copies 16 bytes, of which those from `bytes` on are zero and not read.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint32_t ld_shared(uint32_t a)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-
-// d += a b, a 16 x 16 (row fragments), b 16 x 8.
-template <bool BF16>
+// d = a b (FIRST) or d += a b, a 16 x 16 (row fragments), b 16 x 8.
+template <bool BF16, bool FIRST>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1)
 {
+    const float c[4] = {FIRST ? 0.0f : d[0], FIRST ? 0.0f : d[1], FIRST ? 0.0f : d[2], FIRST ? 0.0f : d[3]};
     if (BF16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
     else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 // A number whose units' place takes a code: 128 in bfloat16 (7 fraction bits),
@@ -88,10 +67,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 template <bool BF16> constexpr uint32_t UNITS = BF16 ? 0x43004300u : 0x64006400u;
 
 // Codes 2 i and 2 i + 1 of a word, less the zero point (given as UNITS + z).
+// `units` is UNITS kept in a register: an instruction takes only one of mask and
+// units as a constant, and would become two.
 template <bool BF16>
-__device__ __forceinline__ uint32_t decode(uint32_t word, int i, uint32_t zero)
+__device__ __forceinline__ uint32_t decode(uint32_t word, int i, uint32_t units, uint32_t zero)
 {
-    const uint32_t q = ((word >> (4 * i)) & 0x000f000fu) | UNITS<BF16>;
+    uint32_t q;
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(q) : "r"(word >> (4 * i)), "r"(units));   // (a & b) | c
     if (BF16) {
         const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&q),
                                          *reinterpret_cast<const __nv_bfloat162 *>(&zero));
@@ -108,222 +90,325 @@ __device__ __forceinline__ float2 scale_pair(uint32_t s)
                 : __half22float2(*reinterpret_cast<const __half2 *>(&s));
 }
 
-// Bytes of a stage of a warp's ring.
-__host__ __device__ constexpr int codes_bytes(int mt) { return mt * 16 * ROW_PITCH; }
-__host__ __device__ constexpr int scales_bytes(int mt, int per) { return STEP / (32 * per) * mt * 16 * 2; }
-__host__ __device__ constexpr int stage_bytes(int mt, int per, int tokens)
+__device__ __forceinline__ void tma_load_3d_cta(uint32_t dst, const void *map, uint32_t bar, int x, int y, int z)
 {
-    return codes_bytes(mt) + scales_bytes(mt, per) * 3 / 2 + tokens * STEP * 2;
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 
-// PER: a scale's columns in units of 32.  `tokens`: rows of A that a chunk can
-// have, at most TOKENS.
-template <bool BF16, int MT, int PER, int STAGES>
-__global__ void __launch_bounds__(32 * WARPS) w4_kernel(const W4Args p, int tiles, int tokens, int *err)
+struct W4Maps {
+    CUtensorMap q, s, z, a;
+};
+
+// Shared memory: rings of codes, of A, of scales and zero points, barriers; then the
+// teams' sums in its place.
+__host__ __device__ constexpr int scales_bytes(int per) { return STEP / (32 * per) * ROWS * 2; }
+__host__ __device__ constexpr int params_bytes(int per, bool zero) { return scales_bytes(per) * (zero ? 3 : 2) / 2; }
+__host__ __device__ constexpr int params_pitch(int per, bool zero) { return (params_bytes(per, zero) + 127) / 128 * 128; }  // (TMA's rule)
+__host__ __device__ constexpr int a_bytes(int tokens) { return STEP * 2 * tokens; }
+__host__ __device__ constexpr int shared_bytes(int per, bool zero, int tokens)
+{
+    return WARPS * STAGES * (CODES + a_bytes(tokens) + params_pitch(per, zero)) + 256;
+}
+static_assert(WARPS * STAGES * 8 + 8 <= 256, "barriers and the abort flag");
+
+// PER: a scale's columns in units of 32.  `tokens`: rows of A of a chunk, 1, 2, 4 or
+// 8.  `team`: a power of two.
+//
+// Of a row's 128 bytes TMA puts 16-byte piece c to place c ^ (row % 8), the row being that
+// of shared memory.  Lane (quad, t) computes with two neighbouring rows of each 16, a
+// Gate and its Up, as rows quad and quad + 8 of the instruction; which, is chosen so
+// that reads of 4, 8 or 16 bytes a lane meet no bank twice: rows 2 pi and 2 pi + 1, pi
+// the quad with its lower bits swapped, the odd one first in quads 4 to 7.  Word j of
+// the eight that lane t has of a row is columns 32 PER (j / PER) + 8 PER t + 8 (j % PER)
+// .. + 7: the words of a place in all four lanes of a row share a scale.
+template <bool BF16, int PER, bool ZERO>
+__global__ void __launch_bounds__(32 * WARPS, 3)
+    w4_kernel(const __grid_constant__ W4Maps maps, const W4Args p, int tiles, int tokens, int team, int *err)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    extern __shared__ __align__(16) unsigned char shared[];
-    constexpr int ROWS = 16 * MT, BLOCKS = STEP / (32 * PER);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int unit = blockIdx.x / tiles, n0 = (blockIdx.x - unit * tiles) * ROWS;
-    int g, row0, rows;
-    if (!find_chunk<TOKENS>(p.groups, unit, err, g, row0, rows)) return;
-
-    const int stage = stage_bytes(MT, PER, tokens);
-    const uint32_t ring = smem_u32(shared) + warp * STAGES * stage;
-    const int steps = (p.w.K + STEP - 1) / STEP, row_bytes = p.w.row_bytes(), blocks = p.w.blocks();
-    const uint8_t *codes = p.w.Q + (long long)g * p.w.N * row_bytes;
-    const long long first_block = (long long)g * blocks;
-
-    auto load = [&](int step, int slot) {
-        const uint32_t at = ring + slot * stage;
-        // codes: row r of a 16 in place r / 2 + 8 (r % 2), so that a lane's two rows
-        // are neighbours in W (a Gate and its Up)
+    extern __shared__ __align__(1024) unsigned char shared[];
+    constexpr int BLOCKS = STEP / (32 * PER), PARAMS = params_pitch(PER, ZERO);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wk = warp & (team - 1), quad = lane >> 2, t = lane & 3;
+    const int of_a = a_bytes(tokens);
+    unsigned char *const codes = shared + warp * STAGES * CODES;
+    unsigned char *const a = shared + WARPS * STAGES * CODES + warp * STAGES * of_a;
+    unsigned char *const params = shared + WARPS * STAGES * (CODES + of_a) + warp * STAGES * PARAMS;
+    unsigned char *const at_bars = shared + WARPS * STAGES * (CODES + of_a + PARAMS);
+    const uint32_t bars = smem_u32(at_bars) + warp * STAGES * 8;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(at_bars + WARPS * STAGES * 8);
+    if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-            const int r = i * 8 + (lane >> 2), n = n0 + r, c = step * 64 + (lane & 3) * 16;
-            const int place = (r & ~15) + ((r & 15) >> 1) + 8 * (r & 1);
-            const bool in = n < p.w.N && c < row_bytes;
-            copy16(at + place * ROW_PITCH + (lane & 3) * 16, codes + (in ? (long long)n * row_bytes + c : 0),
-                   in ? 16 : 0);
+        for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 1);
+        fence_barrier_init();
+        if (warp == 0) *abort_flag = 0;
+    }
+    const int chunk = blockIdx.x / tiles, tile = blockIdx.x - chunk * tiles;
+    const int n0 = (tile * (WARPS / team) + warp / team) * ROWS;
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int g, row0, rows;
+    if (!find_chunk(p.groups, tokens, chunk, err, g, row0, rows)) return;
+
+    const int steps = n0 < p.w.N ? (p.w.K + STEP - 1) / STEP : 0;
+    auto load = [&](int step, int slot) {            // by the first four lanes
+        const uint32_t bar = bars + 8 * slot;
+        if (lane == 0) {
+            const uint32_t to = smem_u32(params) + slot * PARAMS;
+            mbar_arrive_expect_tx(bar, CODES + params_bytes(PER, ZERO) + a_bytes(tokens));
+            tma_load_3d_cta(smem_u32(codes) + slot * CODES, &maps.q, bar, step * (STEP / 2), n0, g);
+            tma_load_3d_cta(to, &maps.s, bar, n0, step * BLOCKS, g);
+            if (ZERO) tma_load_3d_cta(to + scales_bytes(PER), &maps.z, bar, n0, step * BLOCKS, g);
         }
-        const uint32_t scales = at + codes_bytes(MT);
-        if (lane < BLOCKS * MT * 2) {
-            const int b = lane / (MT * 2), part = lane % (MT * 2), block = step * BLOCKS + b;
-            const bool in = block < blocks && n0 + part * 8 < p.w.lds;
-            copy16(scales + lane * 16,
-                   static_cast<const uint16_t *>(p.w.S) + (in ? (first_block + block) * p.w.lds + n0 + part * 8 : 0),
-                   in ? 16 : 0);
+        if (lane < 4) tma_load_2d(smem_u32(a) + slot * of_a + lane * tokens * 128, &maps.a, bar, step * STEP + lane * 64, row0);
+    };
+#pragma unroll 1
+    for (int i = 0; i < STAGES; ++i)
+        if (wk + i * team < steps) load(wk + i * team, i);
+
+    const int pi = (quad & 4) | (quad & 1) << 1 | (quad >> 1 & 1), odd = quad >> 2;
+    uint32_t units;
+    asm volatile("mov.b32 %0, %1;" : "=r"(units) : "n"(UNITS<BF16>));
+    const uint32_t order = odd ? 0x1032u : 0x3210u;  // of the rows' scales
+    const int swap0 = (2 * pi + odd) & 7, swap1 = (2 * pi + 1 - odd) & 7;
+    const uint32_t scale0 = odd ? 0x3244u : 0x1044u, scale1 = odd ? 0x1044u : 0x3244u;
+    const int row_at0 = (2 * pi + odd) * (STEP / 2), row_at1 = (2 * pi + 1 - odd) * (STEP / 2);
+    // (lanes of rows of A that do not exist compute with another, for nothing)
+    const int token = min(quad, tokens - 1);
+    float acc[MT][4] = {};
+    bool stopped = false;
+    int step = wk, slot = 0;
+    uint32_t parity = 0;
+    for (; step < steps; step += team) {
+        if (!__all_sync(0xffffffffu, wait_bounded(bars + 8 * slot, parity, abort_flag, err))) {
+            stopped = true;
+            break;
         }
-        if (p.w.Z != nullptr && lane < BLOCKS * MT) {
-            const int b = lane / MT, part = lane % MT, block = step * BLOCKS + b;
-            const bool in = block < blocks && n0 + part * 16 < p.w.lds;
-            copy16(scales + scales_bytes(MT, PER) + lane * 16,
-                   p.w.Z + (in ? (first_block + block) * p.w.lds + n0 + part * 16 : 0), in ? 16 : 0);
-        }
-        // A: lane (row, t) has columns 32 j + 8 t .. + 7 of the step, as it will read them
-        const uint32_t a = scales + scales_bytes(MT, PER) * 3 / 2;
-        if ((lane >> 2) < rows) {
-            const char *row = static_cast<const char *>(p.A) + (long long)(row0 + (lane >> 2)) * p.lda * 2;
+        const unsigned char *row = codes + slot * CODES, *par = params + slot * PARAMS;
+        const int x_line = ((int)(a - shared) + slot * of_a) / 128 + token;      // in shared memory
+        const uint32_t *scale = reinterpret_cast<const uint32_t *>(par) + pi;
+        const uint16_t *zero = reinterpret_cast<const uint16_t *>(par + scales_bytes(PER)) + pi;
+        float part[MT][4];
+        uint32_t z0[MT], z1[MT];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (half == 1 && step * STEP + STEP / 2 >= p.w.K) break;
+            uint32_t w[2 * MT][4];                   // both rows of each 16
+#pragma unroll
+            for (int r = 0; r < 2 * MT; ++r) {
+                const unsigned char *at = row + (r % 2 ? row_at1 : row_at0) + r / 2 * 16 * (STEP / 2);
+                const int swap = r % 2 ? swap1 : swap0;
+                if (PER == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(at + ((4 * half + t) ^ swap) * 16);
+                    w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+                } else if (PER == 2) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(at + ((4 * half + 2 * h + (t >> 1)) ^ swap) * 16 + (t & 1) * 8);
+                        w[r][2 * h] = v.x, w[r][2 * h + 1] = v.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[r][j] = *reinterpret_cast<const uint32_t *>(at + ((4 * half + j) ^ swap) * 16 + t * 4);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int k = step * STEP + j * 32 + (lane & 3) * 8;
-                const int left = min(max(p.w.K - k, 0), 8) * 2;
-                copy16(a + (j * tokens * 4 + lane) * 16, row + (left > 0 ? (long long)k * 2 : 0), left);
-            }
-        }
-    };
-
-    float acc[MT][4] = {};
-    const int mine = steps > warp ? (steps - warp + WARPS - 1) / WARPS : 0;
+                // columns in units of 8: block of 64, piece of it
+                const int c = (4 * half + j) / PER * (4 * PER) + PER * t + j % PER, line = (c >> 3) * tokens + x_line;
+                const uint4 x = *reinterpret_cast<const uint4 *>(shared + line * 128 + ((c ^ line) & 7) * 16);
+                const int b = (4 * half + j) / PER;  // the scale's place among the step's
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) {
-        if (i < mine) load(warp + i * WARPS, i);
-        copies_commit();
-    }
-    int slot = 0;
-    for (int i = 0; i < mine; ++i) {
-        copies_wait<STAGES - 2>();
-        __syncwarp();
-        const uint32_t at = ring + slot * stage, scales = at + codes_bytes(MT);
-        const uint32_t a = scales + scales_bytes(MT, PER) * 3 / 2;
-        float part[MT][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if ((lane >> 2) < rows) x = ld_shared_v4(a + (j * tokens * 4 + lane) * 16);
-            const int b = j / PER;                   // the scale's place among the step's
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (j % PER == 0) part[m][0] = part[m][1] = part[m][2] = part[m][3] = 0.0f;
-                const uint32_t row = at + (m * 16 + (lane >> 2)) * ROW_PITCH + j * 16 + (lane & 3) * 4;
-                const uint32_t w0 = ld_shared(row), w1 = ld_shared(row + 8 * ROW_PITCH);
-                const int pair = b * MT * 8 + m * 8 + (lane >> 2);
-                uint32_t z0 = UNITS<BF16> + 0x00080008u, z1 = z0;
-                if (p.w.Z != nullptr) {
-                    const uint32_t z = ld_shared_u16(scales + scales_bytes(MT, PER) + pair * 2);
-                    z0 = UNITS<BF16> + (z & 15u) * 0x00010001u;
-                    z1 = UNITS<BF16> + (z >> 8 & 15u) * 0x00010001u;
-                }
-                mma16816<BF16>(part[m], decode<BF16>(w0, 0, z0), decode<BF16>(w1, 0, z1), decode<BF16>(w0, 1, z0),
-                               decode<BF16>(w1, 1, z1), x.x, x.y);
-                mma16816<BF16>(part[m], decode<BF16>(w0, 2, z0), decode<BF16>(w1, 2, z1), decode<BF16>(w0, 3, z0),
-                               decode<BF16>(w1, 3, z1), x.z, x.w);
-                if (j % PER == PER - 1) {
-                    const float2 s = scale_pair<BF16>(ld_shared(scales + pair * 4));
-                    acc[m][0] = fmaf(s.x, part[m][0], acc[m][0]);
-                    acc[m][1] = fmaf(s.x, part[m][1], acc[m][1]);
-                    acc[m][2] = fmaf(s.y, part[m][2], acc[m][2]);
-                    acc[m][3] = fmaf(s.y, part[m][3], acc[m][3]);
+                for (int m = 0; m < MT; ++m) {
+                    if (j % PER == 0) {
+                        z0[m] = z1[m] = UNITS<BF16> + 0x00080008u;
+                        if (ZERO) {
+                            const uint32_t z = __byte_perm(zero[(b * MT + m) * 8], 0, odd ? 0x4401 : 0x4410);
+                            z0[m] = UNITS<BF16> + (z & 15u) * 0x00010001u;
+                            z1[m] = UNITS<BF16> + (z >> 8 & 15u) * 0x00010001u;
+                        }
+                    }
+                    const uint32_t w0 = w[2 * m][j], w1 = w[2 * m + 1][j];
+                    auto two = [&](int h, uint32_t b0, uint32_t b1, auto f) {
+                        mma16816<BF16, decltype(f)::value>(
+                            part[m], decode<BF16>(w0, h, units, z0[m]), decode<BF16>(w1, h, units, z1[m]),
+                            decode<BF16>(w0, h + 1, units, z0[m]), decode<BF16>(w1, h + 1, units, z1[m]), b0, b1);
+                    };
+                    if (j % PER == 0)
+                        two(0, x.x, x.y, std::true_type{});
+                    else
+                        two(0, x.x, x.y, std::false_type{});
+                    two(2, x.z, x.w, std::false_type{});
+                    if (j % PER == PER - 1) {
+                        float2 s;
+                        if (BF16)                    // (a bfloat16 is the upper half of its FP32)
+                            s = make_float2(__uint_as_float(__byte_perm(scale[(b * MT + m) * 8], 0, scale0)),
+                                            __uint_as_float(__byte_perm(scale[(b * MT + m) * 8], 0, scale1)));
+                        else
+                            s = scale_pair<BF16>(__byte_perm(scale[(b * MT + m) * 8], 0, order));
+                        acc[m][0] = fmaf(s.x, part[m][0], acc[m][0]);
+                        acc[m][1] = fmaf(s.x, part[m][1], acc[m][1]);
+                        acc[m][2] = fmaf(s.y, part[m][2], acc[m][2]);
+                        acc[m][3] = fmaf(s.y, part[m][3], acc[m][3]);
+                    }
                 }
             }
         }
         __syncwarp();
-        const int next = i + STAGES - 1;
-        if (next < mine) load(warp + next * WARPS, slot == 0 ? STAGES - 1 : slot - 1);
-        copies_commit();
+        if (step + STAGES * team < steps) load(step + STAGES * team, slot);
         slot = slot + 1 == STAGES ? 0 : slot + 1;
+        parity ^= slot == 0;
     }
-    copies_wait<0>();
-    __syncthreads();
+    if (stopped)                                     // what is still on its way lands before the CTA ends
+        for (int i = 0; i < STAGES; ++i, step += team) {
+            if (step < steps) wait_bounded(bars + 8 * slot, parity, abort_flag, err, false, DRAIN_LIMIT_NS);
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+            parity ^= slot == 0;
+        }
 
-    // The warps' sums, in order: [warp][token][row], rows padded by 2.
-    constexpr int PITCH = ROWS + 2;
-    float *sums = reinterpret_cast<float *>(shared);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int token = 2 * (lane & 3) + h, row = m * 16 + 2 * (lane >> 2);
-            if (token < rows)
-                *reinterpret_cast<float2 *>(sums + (warp * tokens + token) * PITCH + row) =
-                    make_float2(acc[m][h], acc[m][2 + h]);
-        }
-    __syncthreads();
-    constexpr int PAIRS = ROWS / 2;
-    for (int i = threadIdx.x; i < rows * PAIRS; i += 32 * WARPS) {
-        const int token = i / PAIRS, n = n0 + 2 * (i - token * PAIRS);
-        if (n >= p.w.N) continue;
-        float x = 0.0f, y = 0.0f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            const float2 v = *reinterpret_cast<const float2 *>(sums + (w * tokens + token) * PITCH + n - n0);
-            x += v.x;
-            y += v.y;
-        }
-        const long long o = (row0 + token) * p.ldc;
-        if (p.swiglu) {
-            store_out(p.C, o + n / 2, silu_f32(p.alpha * x) * (p.alpha * y), p.out_kind);
-            continue;
-        }
+    auto store = [&](int row, int n, float x, float y) {             // columns n, n + 1 of a row of A
+        if (n >= p.w.N) return;
+        const long long o = row * p.ldc;
         x *= p.alpha;
         y *= p.alpha;
+        if (p.swiglu) {
+            store_out(p.C, o + n / 2, silu_f32(x) * y, p.out_kind);
+            return;
+        }
         if (p.beta != 0.0f) x += p.beta * load_out(p.C, o + n, p.out_kind);
         store_out(p.C, o + n, x, p.out_kind);
         if (n + 1 < p.w.N) {
             if (p.beta != 0.0f) y += p.beta * load_out(p.C, o + n + 1, p.out_kind);
             store_out(p.C, o + n + 1, y, p.out_kind);
         }
+    };
+    // Rows 2 pi and 2 pi + 1 for rows 2 t + h of A.
+    auto first = [&](int m, int h) { return odd ? acc[m][2 + h] : acc[m][h]; };
+    auto second = [&](int m, int h) { return odd ? acc[m][h] : acc[m][2 + h]; };
+    if (team == 1) {
+        if (stopped) return;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (2 * t + h < rows) store(row0 + 2 * t + h, n0 + m * 16 + 2 * pi, first(m, h), second(m, h));
+        return;
+    }
+    // [warp][row of A][row of W]
+    float *sums = reinterpret_cast<float *>(shared);
+    __syncthreads();
+    if (*abort_flag) return;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (2 * t + h < rows)
+                *reinterpret_cast<float2 *>(sums + (warp * tokens + 2 * t + h) * SUMS + m * 16 + 2 * pi) =
+                    make_float2(first(m, h), second(m, h));
+    __syncthreads();
+    const float *of_team = sums + (warp & ~(team - 1)) * tokens * SUMS;
+    for (int o = wk * 32 + lane; o < rows * (ROWS / 2); o += team * 32) {
+        const int row = o / (ROWS / 2), pair = o % (ROWS / 2);
+        float x = 0.0f, y = 0.0f;
+        for (int w = 0; w < team; ++w) {
+            const float2 v = *reinterpret_cast<const float2 *>(of_team + (w * tokens + row) * SUMS + 2 * pair);
+            x += v.x;
+            y += v.y;
+        }
+        store(row0 + row, n0 + 2 * pair, x, y);
     }
 }
 
 // An upper bound of the chunks over all groups, and with offsets one more, whose
 // CTAs find nothing: on the way they look at every offset and report what they
 // have to clamp.
-long long chunks_of(const Groups &g)
+long long chunks_of(const Groups &g, int tokens)
 {
-    return g.offsets == nullptr ? (g.M + TOKENS - 1) / TOKENS : g.M / TOKENS + std::min(g.G, g.M) + 1;
+    return g.offsets == nullptr ? (g.M + tokens - 1) / tokens : g.M / tokens + std::min(g.G, g.M) + 1;
 }
 
-template <bool BF16, int MT, int PER>
-cudaError_t launch(const W4Args &p, int *err, cudaStream_t s)
+// Rows of A per chunk: of groups four times their mean, since another chunk reads and
+// decodes the weights again (64 rows of 64 experts: 25.6 us with chunks of 1, 21.2
+// with 2, 19.2 with 4, 19.8 with 8).
+int chunk_rows(const Groups &g)
 {
-    constexpr int STAGES = 4;
-    const int tokens = std::min(p.groups.M, TOKENS), tiles = (p.w.N + 16 * MT - 1) / (16 * MT);
-    const size_t ring = (size_t)WARPS * STAGES * stage_bytes(MT, PER, tokens);
-    const size_t sums = (size_t)WARPS * tokens * (16 * MT + 2) * 4;
-    const size_t bytes = std::max(ring, sums);
-    auto kernel = w4_kernel<BF16, MT, PER, STAGES>;
+    const int want = g.offsets == nullptr ? g.M : (int)std::min<long long>(g.M, (4ll * g.M + g.G - 1) / g.G);
+    return want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : TOKENS;
+}
+
+template <bool BF16, int PER, bool ZERO>
+cudaError_t launch(const W4Args &p, const W4Maps &maps, int tokens, int sms, int *err, cudaStream_t s)
+{
+    // As small teams as leave 12 warps for each SM, as many as are resident: one row,
+    // 4096 x 14336, 10.8 us with teams of 4 and 21.2 without; 64 rows of 64 experts, 896 x
+    // 2432, 19.2 without and 23.9 with.
+    const int steps = (p.w.K + STEP - 1) / STEP;
+    const long long items = (p.groups.offsets ? std::min(p.groups.G, p.groups.M) : chunks_of(p.groups, tokens)) * ((p.w.N + ROWS - 1ll) / ROWS);
+    int team = 1;
+    while (team < WARPS && team < steps && items * team < 12ll * sms) team *= 2;
+    const size_t sums = (size_t)WARPS * tokens * SUMS * 4;
+    auto kernel = w4_kernel<BF16, PER, ZERO>;
     static DeviceOnce once;
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     if (once.needed(dev)) {
-        if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 WARPS * STAGES * stage_bytes(MT, PER, TOKENS)))
-            return e;
+        if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared_bytes(PER, ZERO, TOKENS))) return e;
         once.mark(dev);
     }
+    const int per_cta = ROWS * (WARPS / team), tiles = (p.w.N + per_cta - 1) / per_cta;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(chunks_of(p.groups) * tiles));
+    cfg.gridDim = dim3((unsigned)(chunks_of(p.groups, tokens) * tiles));
     cfg.blockDim = dim3(32 * WARPS);
-    cfg.dynamicSmemBytes = bytes;
+    cfg.dynamicSmemBytes = std::max((size_t)shared_bytes(PER, ZERO, tokens), sums);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, tiles, tokens, err);
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p, tiles, tokens, team, err);
 }
 
-template <bool BF16, int MT>
-cudaError_t launch_group(const W4Args &p, int *err, cudaStream_t s)
+template <bool BF16, int PER>
+cudaError_t launch_zero(const W4Args &p, const W4Maps &maps, int tokens, int sms, int *err, cudaStream_t s)
 {
-    return p.w.group == 32   ? launch<BF16, MT, 1>(p, err, s)
-           : p.w.group == 64 ? launch<BF16, MT, 2>(p, err, s)
-                             : launch<BF16, MT, 4>(p, err, s);
+    return p.w.Z != nullptr ? launch<BF16, PER, true>(p, maps, tokens, sms, err, s) : launch<BF16, PER, false>(p, maps, tokens, sms, err, s);
+}
+
+template <bool BF16>
+cudaError_t launch_group(const W4Args &p, const W4Maps &maps, int tokens, int sms, int *err, cudaStream_t s)
+{
+    return p.w.group == 32   ? launch_zero<BF16, 1>(p, maps, tokens, sms, err, s)
+           : p.w.group == 64 ? launch_zero<BF16, 2>(p, maps, tokens, sms, err, s)
+                             : launch_zero<BF16, 4>(p, maps, tokens, sms, err, s);
 }
 
 }  // namespace
 
-bool w4_fits(const W4Args &p) { return chunks_of(p.groups) * ((p.w.N + 15ll) / 16) <= 0x7fffffff; }
+bool w4_fits(const W4Args &p) { return chunks_of(p.groups, 1) * ((p.w.N + 31ll) / 32) <= 0x7fffffff; }
 
-cudaError_t launch_w4(const W4Args &p, int sms, int *err, cudaStream_t s)
+cudaError_t launch_w4(const W4Args &p, int sms, int *err, cudaStream_t s, bool &mapped)
 {
-    const bool wide = (long long)std::min(p.groups.G, p.groups.M) * p.w.N >= 64ll * sms;
-    if (p.bf16) return wide ? launch_group<true, 2>(p, err, s) : launch_group<true, 1>(p, err, s);
-    return wide ? launch_group<false, 2>(p, err, s) : launch_group<false, 1>(p, err, s);
+    W4Maps maps{};
+    const int tokens = chunk_rows(p.groups);
+    mapped = true;
+    if (p.w.K > 0) {
+        const uint64_t N = p.w.N, G = p.groups.G, blocks = p.w.blocks(), row = p.w.row_bytes(), lds = p.w.lds;
+        const uint32_t per_step = STEP / p.w.group;
+        const uint64_t qd[] = {row, N, G}, qs[] = {row, G > 1 ? row * N : row};
+        const uint32_t qb[] = {STEP / 2, ROWS, 1}, sb[] = {ROWS, per_step, 1};
+        const uint64_t sd[] = {lds, blocks, G}, ss[] = {lds * 2, G > 1 ? lds * 2 * blocks : lds * 2}, zs[] = {lds, G > 1 ? lds * blocks : lds};
+        const uint64_t ad[] = {(uint64_t)p.w.K, (uint64_t)p.groups.M}, as[] = {(uint64_t)p.lda * 2};
+        const uint32_t ab[] = {64, (uint32_t)tokens};
+        mapped = encode_tiled(&maps.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.w.Q, qd, qs, qb, 128) &&
+                 encode_tiled(&maps.s, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, p.w.S, sd, ss, sb, 0) &&
+                 (p.w.Z == nullptr || encode_tiled(&maps.z, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.w.Z, sd, zs, sb, 0)) &&
+                 encode_tiled(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, p.A, ad, as, ab, 128);
+        if (!mapped) return cudaErrorInvalidValue;
+    }
+    return p.bf16 ? launch_group<true>(p, maps, tokens, sms, err, s) : launch_group<false>(p, maps, tokens, sms, err, s);
 }
 
 }  // namespace swg

@@ -36,7 +36,8 @@ struct W4Args {
 };
 // The number of CTAs has to fit 32 bits.
 bool w4_fits(const W4Args &p);
-cudaError_t launch_w4(const W4Args &p, int sms, int *err, cudaStream_t s);
+// mapped: whether the tensor maps could be encoded (if not, nothing was launched).
+cudaError_t launch_w4(const W4Args &p, int sms, int *err, cudaStream_t s, bool &mapped);
 
 struct W4Convert {
     int G;
