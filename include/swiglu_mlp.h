@@ -475,8 +475,8 @@ SWG_API int swiglu_mx4(int format, const void *A, const void *SA, const void *W,
  * slot t * top + j is token t's j'th.  Arrays of slots are contiguous
  * (T x top).  T * top, R and D are at most 2^31 - 1024, the experts at most
  * SWG_MAX_EXPERTS, top at most SWG_MAX_TOP, else SWG_ERR_UNSUPPORTED.
- * X, rows, out and their gradients share one swg_type; they are 16-byte aligned,
- * row strides multiples of 16 bytes.  Logits need only their type's alignment.
+ * X, rows, out and their gradients share one swg_type (but for FP32 rows, see
+ * expert_combine); they are 16-byte aligned, row strides multiples of 16 bytes.  Logits need only their type's alignment.
  * None of the outputs may overlap an input, but out of expert_combine, which is
  * read for beta != 0.
  */
@@ -503,9 +503,9 @@ typedef enum { SWG_SOFTMAX = 0, SWG_SIGMOID = 1 } swg_score;
  *                 zero: scale * s_j.  (scale finite.)
  *   experts, weights   T x top: largest c first.
  * An expert whose logit or bias is -inf is not chosen; a slot that none is left for
- * gets expert -1 and weight 0.  A token with a NaN among its c (a NaN logit or
- * bias; for softmax also a logit of +inf) goes to experts 0 .. top - 1 with
- * weights of NaN.
+ * gets expert -1 and weight 0.  A token with a NaN logit, or a NaN among the c of
+ * experts that are not masked (for softmax also by a logit of +inf), goes to experts
+ * 0 .. top - 1 with weights of NaN.
  * Calls with a plan of more than 64 tokens keep counts in the stream's workspace:
  * what gemm says of split calls and graph capture holds for them.
  */
@@ -556,11 +556,12 @@ SWG_API int expert_dispatch(int64_t T, int64_t R, int64_t D, int64_t top, const 
 /*
  * expert_combine — out[t,:] = sum_j weights[t][j] * rows[position[t][j],:] + beta *
  * out[t,:] over the slots with a row, in FP32 and in the order of the slots, rounded
- * once.  weights NULL: ones.  out is not read when beta == 0.
+ * once to otype: the rows' type, or any of the three where they are FP32.  weights
+ * NULL: ones.  out is not read when beta == 0.
  */
 SWG_API int expert_combine(int64_t T, int64_t R, int64_t D, int64_t top, const void *rows, int64_t ldr,
                            int type, const int32_t *position, const float *weights, float beta,
-                           void *out, int64_t ldo, void *stream);
+                           void *out, int64_t ldo, int otype, void *stream);
 
 /*
  * expert_combine_grad — the gradients of that:

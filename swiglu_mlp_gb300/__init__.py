@@ -137,7 +137,8 @@ def load():
         lib.expert_route_grad.argtypes = [i32, i64, i64, i64, vp, i64, i32, vp, i32, f32, vp, vp,
                                           i64, vp]
         lib.expert_dispatch.argtypes = [i64, i64, i64, i64, vp, i64, i32, vp, vp, i64, vp]
-        lib.expert_combine.argtypes = [i64, i64, i64, i64, vp, i64, i32, vp, vp, f32, vp, i64, vp]
+        lib.expert_combine.argtypes = [i64, i64, i64, i64, vp, i64, i32, vp, vp, f32, vp, i64, i32,
+                                       vp]
         lib.expert_combine_grad.argtypes = [i64, i64, i64, i64, vp, i64, vp, i64, i32, vp, vp, vp,
                                             i64, vp, vp]
         lib.w4_quantize.argtypes = [i64, i64, i64, vp, i64, i32, i64, vp, vp, vp, i64, i32, vp]
@@ -363,11 +364,13 @@ def expert_dispatch(T, R, D, top, X, ldx, type, position, rows, ldr, stream=None
                                          _stream(stream)), "expert_dispatch")
 
 
-def expert_combine(T, R, D, top, rows, ldr, type, position, weights, beta, out, ldo, stream=None):
+def expert_combine(T, R, D, top, rows, ldr, type, position, weights, beta, out, ldo, otype,
+                   stream=None):
     """out[t] = sum_j weights[t, j] rows[position[t, j]] + beta out[t] (see the C header)."""
     return _check(load().expert_combine(int(T), int(R), int(D), int(top), _ptr(rows), int(ldr),
                                         int(type), _ptr(position), _ptr(weights), float(beta),
-                                        _ptr(out), int(ldo), _stream(stream)), "expert_combine")
+                                        _ptr(out), int(ldo), int(otype), _stream(stream)),
+                  "expert_combine")
 
 
 def expert_combine_grad(T, R, D, top, d_out, ldd, rows, ldr, type, position, weights, d_rows, lddr,
@@ -924,7 +927,8 @@ def expert_dispatch_into(rows, X, position, stream=None):
 
 def expert_combine_into(out, rows, position, weights=None, beta=0.0, stream=None):
     """out[t] <- sum_j weights[t, j] * rows[position[t, j]] + beta * out[t] (weights
-    float32 [T, top]; None: ones)."""
+    float32 [T, top]; None: ones).  out is of the rows' type; of float32 rows also
+    16-bit."""
     w = "expert_combine_into"
     torch = _torch or _fast()
     lib = _bound
@@ -933,11 +937,11 @@ def expert_combine_into(out, rows, position, weights=None, beta=0.0, stream=None
     Tp, top = _pair(w, "position", position)
     _slots(w, "position", position, T, top, torch.int32)
     _weights_of(w, weights, T, top, torch.float32)
-    if Dr != D or rows.dtype is not out.dtype:
+    if Dr != D or (rows.dtype is not out.dtype and rows.dtype is not torch.float32):
         _refuse(w, "inconsistent shapes or dtypes")
     s, dev = _place(stream)
-    rc = lib.expert_combine(T, R, D, top, rows, ldr, _type_code(out.dtype, w), position, weights,
-                            beta, out, ldo, s, dev)
+    rc = lib.expert_combine(T, R, D, top, rows, ldr, _type_code(rows.dtype, w), position, weights,
+                            beta, out, ldo, _type_code(out.dtype, w), s, dev)
     if rc:
         _failed(rc, w, "expert_combine")
     return out

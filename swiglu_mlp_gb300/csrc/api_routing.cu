@@ -238,20 +238,22 @@ int expert_dispatch(int64_t T, int64_t R, int64_t D, int64_t top, const void *X,
 
 int expert_combine(int64_t T, int64_t R, int64_t D, int64_t top, const void *rows, int64_t ldr, int type,
                    const int32_t *position, const float *weights, float beta, void *out, int64_t ldo,
-                   void *stream)
+                   int otype, void *stream)
 {
-    int bytes;
+    int bytes, obytes;
     swg::RowsArgs p{};
+    if (!type_bytes(otype, obytes) || (otype != type && type != SWG_TYPE_F32)) return SWG_ERR_UNSUPPORTED;
     if (int rc = rows_args(T, R, D, top, type, position, weights, bytes, p)) return rc;
     if (T == 0 || D == 0) return SWG_OK;
     if (R > 0)
         if (int rc = check_rows(rows, ldr, D, bytes)) return rc;
-    if (int rc = check_rows(out, ldo, D, bytes)) return rc;
+    if (int rc = check_rows(out, ldo, D, obytes)) return rc;
     p.rows = const_cast<void *>(rows);
     p.ldr = ldr;
     p.out = out;
     p.ldo = ldo;
     p.beta = beta;
+    p.out_type = otype;
     swg::DeviceInfo d;
     if (int rc = swg::device_info(d)) return rc;
     return swg::count_launch(swg::launch_combine(p, d.sms, d.err, static_cast<cudaStream_t>(stream)));

@@ -131,11 +131,11 @@ ENTRY(expert_dispatch, 11)
     int type = (int)I(6); void *pos = P(7), *rows = P(8); int64_t ldr = I(9); void *st = P(10);
     CALL(expert_dispatch(T, R, D, top, X, ldx, type, pos, rows, ldr, st))
 
-ENTRY(expert_combine, 13)
+ENTRY(expert_combine, 14)
     int64_t T = I(0), R = I(1), D = I(2), top = I(3); void *rows = P(4); int64_t ldr = I(5);
     int type = (int)I(6); void *pos = P(7), *we = P(8); float beta = F(9); void *out = P(10);
-    int64_t ldo = I(11); void *st = P(12);
-    CALL(expert_combine(T, R, D, top, rows, ldr, type, pos, we, beta, out, ldo, st))
+    int64_t ldo = I(11); int otype = (int)I(12); void *st = P(13);
+    CALL(expert_combine(T, R, D, top, rows, ldr, type, pos, we, beta, out, ldo, otype, st))
 
 ENTRY(expert_combine_grad, 15)
     int64_t T = I(0), R = I(1), D = I(2), top = I(3); void *d = P(4); int64_t ldd = I(5);

@@ -1,9 +1,11 @@
 // k_route.cu — the router: the experts of each token with their weights, rows
 // sorted by expert, and the gradient of the logits.
 //
-// A warp has a token, lane l the experts l, l + 32, ..; the best of them are
-// taken one after the other by a maximum over the warp, the lowest index of
-// equals.  Without a bias the order of the scores is that of the logits, which
+// A warp has a token, lane l the experts l, l + 32, ...  As many lanes' largest as
+// experts are wanted give a bound that few others pass; those are ranked by
+// comparing all with all, the lowest index of equals first.  (One after the other by
+// a maximum over the warp, eight of 256 took four times the instructions.)  Without a
+// bias the order of the scores is that of the logits, which
 // compare exactly.  With one, or where groups are valued by a sum, the choices
 // (score + bias) are formed in FP32 and compared with a bound of their error;
 // where two are nearer than that, and not the same logit and bias, the token is
@@ -26,8 +28,7 @@ namespace swg {
 namespace {
 
 constexpr unsigned ALL = 0xffffffffu;
-constexpr int RANK_WARPS = 8;          // warps that rank a chunk's slots
-constexpr int SORT_THREADS = 512;
+constexpr int SORT_THREADS = 1024;
 
 __device__ __forceinline__ float load_any(const void *x, long long i, int type)
 {
@@ -85,18 +86,21 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k)
     return (uint64_t)hi << 32 | lo;
 }
 
-__device__ __forceinline__ float max_of_row(float m)
+// The largest over the warp (of no NaN).
+__device__ __forceinline__ float warp_max(float m)
 {
-    return value_of(warp_max(ordered(m)));
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
+    return r;
 }
 
 // Takes the largest key (lane l, place i: expert l + 32 i) out, the lowest expert of
-// equals; -1 when none is left.
+// equals; -1 when only -inf is left.
 template <int V>
-__device__ __forceinline__ int take_best(uint32_t (&key)[V], uint32_t &best)
+__device__ __forceinline__ int take_best(float (&key)[V], float &best)
 {
     const int lane = threadIdx.x & 31;
-    uint32_t k = key[0];
+    float k = key[0];
     int at = 0;
 #pragma unroll
     for (int i = 1; i < V; ++i)
@@ -105,11 +109,11 @@ __device__ __forceinline__ int take_best(uint32_t (&key)[V], uint32_t &best)
             at = i;
         }
     best = warp_max(k);
-    if (best == 0) return -1;
+    if (best == minus_inf()) return -1;
     const int e = (int)__reduce_min_sync(ALL, k == best ? (unsigned)(lane + 32 * at) : 0xffffffffu);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        if (lane + 32 * i == e) key[i] = 0;
+        if (lane + 32 * i == e) key[i] = minus_inf();
     return e;
 }
 
@@ -117,49 +121,48 @@ __device__ __forceinline__ int take_best(uint32_t (&key)[V], uint32_t &best)
 // 32, so that groups of 32 do not share banks.
 __device__ __forceinline__ int at_scratch(int e) { return e + (e >> 5); }
 
-// The best groups as a bit mask, from the choices in the warp's scratch (-inf
-// where masked).  `tol` > 0: `sure` becomes false where the values of two groups
-// that decide are nearer than it.
+// Lanes that look at a group together: as many as there are for each, a power of two.
+__device__ __forceinline__ int log_group_lanes(int groups) { return 31 - __clz(32 / groups); }
+
+// The best groups as a bit mask, group g's bit g << log_group_lanes, from the choices
+// in the warp's scratch (-inf where masked).  `tol` > 0: `sure` becomes false where
+// the worst of them is nearer than it to the best of the others.
 template <class F>
-__device__ unsigned best_groups(const RouteArgs &p, const F *scratch, F tol, bool &sure)
+__device__ __forceinline__ unsigned best_groups(const RouteArgs &p, const F *scratch, F tol, bool &sure)
 {
     const int lane = threadIdx.x & 31, size = p.E / p.groups;
-    int log_lanes = 0;                               // lanes per group, a power of two
-    while ((p.groups << (log_lanes + 1)) <= 32) ++log_lanes;
-    const int lanes = 1 << log_lanes, g = lane >> log_lanes;
+    const int log_lanes = log_group_lanes(p.groups), lanes = 1 << log_lanes, g = lane >> log_lanes;
     const F low = (F)minus_inf();
     F a = low, b = low;                              // the two largest
     if (g < p.groups)
         for (int i = lane & (lanes - 1); i < size; i += lanes) {
             const F v = scratch[at_scratch(g * size + i)];
-            if (v > a) {
-                b = a;
-                a = v;
-            } else if (v > b) {
-                b = v;
-            }
+            const F less = v < a ? v : a;
+            a = v > a ? v : a;
+            b = less > b ? less : b;
         }
     for (int d = 1; d < lanes; d <<= 1) {
         const F a2 = __shfl_xor_sync(ALL, a, d), b2 = __shfl_xor_sync(ALL, b, d);
-        b = a2 > a ? (a > b2 ? a : b2) : (a2 > b ? a2 : b);
+        const F less = a2 < a ? a2 : a, more = b2 > b ? b2 : b;
         a = a2 > a ? a2 : a;
+        b = less > more ? less : more;
     }
     const F value = p.group_sum == 2 && b > low ? a + b : a;
     auto key = ordered(value);
     if (!(a > low) || (lane & (lanes - 1)) != 0) key = 0;
-    unsigned keep = 0;
-    F before = (F)0;
-    for (int j = 0; j <= p.top_groups; ++j) {
-        const auto best = warp_max(key);
-        if (best == 0) break;
-        const int who = (int)__reduce_min_sync(ALL, key == best ? (unsigned)lane : 32u);
-        const F now = __shfl_sync(ALL, value, who);
-        if (tol > (F)0 && j > 0 && !(before - now > tol)) sure = false;
-        before = now;
-        if (j < p.top_groups) keep |= 1u << (who >> log_lanes);
-        if (lane == who) key = 0;
+    int rank = 0;
+    for (int h = 0; h < p.groups; ++h) {
+        const auto other = __shfl_sync(ALL, key, h << log_lanes);
+        rank += other > key || (other == key && h < g);
     }
-    return keep;
+    const bool kept = key > 0 && rank < p.top_groups;
+    if constexpr (sizeof(F) == 4)
+        if (tol > (F)0) {
+            const uint32_t worst = __reduce_min_sync(ALL, kept ? key : 0xffffffffu);
+            const uint32_t rest = __reduce_max_sync(ALL, kept ? 0u : key);
+            if (rest > 0 && !(value_of(worst) - value_of(rest) > tol)) sure = false;
+        }
+    return __ballot_sync(ALL, kept);
 }
 
 // The token's experts in FP64: lane j's is the j'th.  Seldom called: its arrays
@@ -201,7 +204,9 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &p, long long row, do
         c[i] /= z;
         if (p.bias != nullptr && e < p.E) c[i] += (double)p.bias[e];
         if (c[i] == low) masked |= 1u << i;
-        key[i] = masked >> i & 1 ? 0 : ordered(c[i]);
+        // (without a bias the order is that of the logits, groups apart)
+        const double by = p.bias != nullptr || e >= p.E ? c[i] : (double)load_any(p.logits, row + e, p.type);
+        key[i] = masked >> i & 1 ? 0 : ordered(by);
     }
     if (p.groups > 1) {
         __syncwarp();
@@ -213,10 +218,11 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &p, long long row, do
         __syncwarp();
         bool sure = true;
         const unsigned keep = best_groups<double>(p, scratch, 0.0, sure);
+        const int log_lanes = log_group_lanes(p.groups);
 #pragma unroll 1
         for (int i = 0; i < V; ++i) {
             const int e = lane + 32 * i;
-            if (e >= p.E || !(keep >> (e / size) & 1)) key[i] = 0;
+            if (e >= p.E || !(keep >> (e / size << log_lanes) & 1)) key[i] = 0;
         }
     }
     int mine = -1;
@@ -238,106 +244,164 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &p, long long row, do
     return mine;
 }
 
-// The experts of a token, lane j's the j'th (-1: none), and lane j's weight.
+// A candidate for a token's experts.
+struct Candidate {
+    float key;
+    int expert;
+};
+constexpr int SCRATCH = 32 * sizeof(Candidate);      // bytes of a warp's, before its choices
+
+// What a warp keeps from token to token.
 template <int V>
-__device__ __forceinline__ int choose(const RouteArgs &p, int t, void *scratch, float &weight)
+struct Experts {
+    float bias[V];                                   // of this lane's, 0 without
+    float most;                                      // the largest magnitude among all biases
+    uint8_t bit[V];                                  // of their groups' in best_groups
+};
+
+// The experts of a token, lane j's the j'th (-1: none), and lane j's weight, from
+// logits l (lane l's those of experts l, l + 32, ..; -inf behind the last).
+template <int V>
+__device__ __forceinline__ int choose(const RouteArgs &p, long long row, const float (&l)[V], const Experts<V> &of,
+                                      unsigned char *scratch, float &weight)
 {
     const int lane = threadIdx.x & 31;
-    const long long row = t * p.ld;
-    const bool grouped = p.groups > 1;
-    const bool by_score = p.bias != nullptr || (grouped && p.group_sum == 2);
+    const bool grouped = p.groups > 1, biased = p.bias != nullptr;
+    const bool by_score = biased || (grouped && p.group_sum == 2);
     const bool softmax = p.score == SCORE_SOFTMAX;
-    float l[V];
-    float m = minus_inf();
-    bool nan = false;
+    float *choices = reinterpret_cast<float *>(scratch + SCRATCH);
+    float m = l[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = e < p.E ? load_any(p.logits, row + e, p.type) : minus_inf();
-        nan = nan || l[i] != l[i];
-        m = fmaxf(m, l[i]);
-    }
-    if (softmax || by_score) m = max_of_row(m);
-    nan = nan || (softmax && m == -minus_inf());
-    float z = 1.0f;
-    uint32_t key[V];
+    for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+    bool nan = false;
+    float key[V];                                    // -inf where masked
     bool sure = true;
     float tol = 0.0f;
     if (by_score) {
+        // Scores by the fast exponential, which is off by at most 2 + 1.2 |x| units,
+        // and division (2 units).  Softmax: x = l - m, and |x| e^x is at most 0.4: 3 units
+        // of the largest score for the exponential, as much for the sum's terms, 8 for
+        // its 15 additions in a tree, 1 more: two choices, 2^-18 of it and a half.
+        // Sigmoid: s (1 - s) (2 + 1.2 |x|) + 2 s, of the largest score 6 units, where all
+        // logits are negative 1.2 |m| more.
+        m = warp_max(m == m ? m : minus_inf());
         float s[V];
+        float largest;
         if (softmax) {
-            // summed as a tree of four, which keeps its error below the bound used here
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                s[i] = l[i] == minus_inf() ? 0.0f : expf(l[i] - m);
+                s[i] = __expf(l[i] - m);
                 sum[i % 4] += s[i];
             }
-            z = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
-            if (z == 0.0f) z = 1.0f;                 // all masked
-        }
-        // A score is off by at most: its exponential's 2 units and argument's
-        // rounding (0.37 of a unit of the largest score), the sum's 15 additions,
-        // the division: below 2^-19.5 of the largest score; a sigmoid by 4 units.
-        // Two of them, and the addition of the bias to each.
-        const float largest = softmax ? 1.0f / z : 1.0f / (1.0f + expf(-m));
-        tol = largest * (softmax ? 0x1p-18f : 0x1p-20f);
-        float most = 0.0f;
+            largest = __fdividef(1.0f, warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3])));
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            s[i] = softmax ? s[i] / z : 1.0f / (1.0f + expf(-l[i]));
-            if (p.bias != nullptr && e < p.E) s[i] += p.bias[e];
-            nan = nan || s[i] != s[i];
-            const bool masked = l[i] == minus_inf() || s[i] == minus_inf();
-            if (!masked) most = fmaxf(most, fabsf(s[i]));
-            key[i] = masked ? 0u : p.bias != nullptr ? ordered(s[i]) : ordered(l[i]);
-            if (grouped && e < p.E)
-                static_cast<float *>(scratch)[at_scratch(e)] = masked ? minus_inf() : s[i];
+            for (int i = 0; i < V; ++i) s[i] *= largest;
+            tol = largest * 0x1.8p-18f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] = __fdividef(1.0f, 1.0f + __expf(-l[i]));
+            largest = m < -80.0f ? 0.0f : __fdividef(1.0f, 1.0f + __expf(-m));
+            tol = largest * (12.0f + 2.4f * fmaxf(-m, 0.0f)) * 0x1p-23f;
         }
         // (2^-120: scores that FP32 has no digits left for)
-        tol += 0x1p-22f * max_of_row(most) + 0x1p-120f;
+        tol += 0x1p-22f * (largest + of.most) + 0x1p-120f;
+        sure = tol < 1.0f;                           // (not with a bias of +inf, or of NaN)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s[i] += of.bias[i];
+            if (l[i] == minus_inf()) s[i] = minus_inf();
+            nan = nan || s[i] != s[i];
+            key[i] = biased || s[i] == minus_inf() ? s[i] : l[i];
+            if (grouped && lane + 32 * i < p.E) choices[at_scratch(lane + 32 * i)] = s[i];
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            key[i] = l[i] == minus_inf() ? 0u : ordered(l[i]);
-            if (grouped && e < p.E) static_cast<float *>(scratch)[at_scratch(e)] = l[i];
+            key[i] = l[i];
+            nan = nan || l[i] != l[i];
+            if (grouped && lane + 32 * i < p.E) choices[at_scratch(lane + 32 * i)] = l[i];
         }
+        if (softmax && !p.normalise) m = warp_max(m == m ? m : minus_inf());
     }
+    // A padding token: no logit is left.  (A NaN anywhere, or for softmax +inf, is
+    // found before that.)
+    const bool some = m > minus_inf();
+    nan = nan || (softmax && m == -minus_inf());
     if (__any_sync(ALL, nan)) {
         weight = __int_as_float(0x7fffffff);
         return lane < p.top ? lane : -1;
     }
+    if (!__any_sync(ALL, some)) {
+        weight = 0.0f;
+        return -1;
+    }
     if (grouped) {
         __syncwarp();
-        const unsigned keep = best_groups<float>(p, static_cast<float *>(scratch), 2.0f * tol, sure);
-        __syncwarp();
-        // e / size by a product: exact for e, size <= 1024
-        const unsigned size = p.E / p.groups, inverse = ((1u << 22) + size - 1) / size;
+        const unsigned keep = best_groups<float>(p, choices, 2.0f * tol, sure);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const unsigned e = lane + 32 * i;
-            if ((int)e >= p.E || !(keep >> (e * inverse >> 22) & 1)) key[i] = 0;
-        }
+        for (int i = 0; i < V; ++i)
+            if (!(keep >> of.bit[i] & 1)) key[i] = minus_inf();
+    }
+
+    // The bound: the wanted number of lanes have a key that is not below it.
+    float k = key[0], bound = minus_inf();
+#pragma unroll
+    for (int i = 1; i < V; ++i) k = fmaxf(k, key[i]);
+    for (int left = p.top + biased; left > 0;) {     // (with a bias the next best has to be looked at too)
+        bound = warp_max(k);
+        if (bound == minus_inf()) break;
+        const bool is = k == bound;
+        left -= __popc(__ballot_sync(ALL, is));
+        if (is) k = minus_inf();
+    }
+    if (biased) bound -= 1.01f * tol;
+    Candidate *buffer = reinterpret_cast<Candidate *>(scratch);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const bool in = key[i] >= bound && key[i] > minus_inf();
+        const unsigned all = __ballot_sync(ALL, in);
+        const int at = n + __popc(all & ((1u << lane) - 1));
+        if (in && at < 32) buffer[at] = {key[i], lane + 32 * i};
+        n += __popc(all);
     }
     int mine = -1;
-    if (p.bias == nullptr) {
-        for (int j = 0; j < p.top && sure; ++j) {
-            uint32_t best;
-            const int e = take_best<V>(key, best);
-            if (e < 0) break;
-            if (lane == j) mine = e;
+    if (n <= 32) {
+        // ranked: candidates lie in the order of their experts
+        __syncwarp();
+        Candidate c = {minus_inf(), -1};
+        if (lane < n) c = buffer[lane];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) {
+            const float other = __shfl_sync(ALL, c.key, j);
+            rank += other > c.key || (other == c.key && j < lane);
+        }
+        __syncwarp();
+        if (lane < n) buffer[rank] = c;
+        __syncwarp();
+        if (lane < n) c = buffer[lane];
+        if (lane < min(n, p.top)) mine = c.expert;
+        if (biased) {
+            // Neighbours that are nearer than the error, and not the same logit and bias,
+            // make the order unsure: down to the first behind the last chosen, or
+            // behind those that are equal to it.
+            const float last = __shfl_sync(ALL, c.key, p.top - 1), before = __shfl_up_sync(ALL, c.key, 1);
+            const int expert = __shfl_up_sync(ALL, c.expert, 1);
+            bool wrong = false;
+            if (lane > 0 && lane < n && (lane <= p.top || before == last) && !(before - c.key > tol))
+                wrong = load_any(p.logits, row + expert, p.type) != load_any(p.logits, row + c.expert, p.type) ||
+                        p.bias[expert] != p.bias[c.expert];
+            sure = sure && !__any_sync(ALL, wrong);
         }
     } else {
         int last = -1;
         float before = 0.0f;
-        for (int j = 0; sure; ++j) {                 // on to the first that is surely behind the last chosen
-            uint32_t best;
-            const int e = take_best<V>(key, best);
+        for (int j = 0; sure; ++j) {                 // one after the other, as far as that
+            float now;
+            const int e = take_best<V>(key, now);
             if (e < 0) break;
-            const float now = value_of(best);
-            const bool apart = j == 0 || before - now > tol;
+            const bool apart = !biased || j == 0 || before - now > tol;
             if (!apart) {
                 const float x = load_any(p.logits, row + e, p.type), y = load_any(p.logits, row + last, p.type);
                 sure = x == y && p.bias[e] == p.bias[last];
@@ -348,62 +412,66 @@ __device__ __forceinline__ int choose(const RouteArgs &p, int t, void *scratch, 
             last = e;
         }
     }
-    if (!sure) mine = choose_exactly<V>(p, row, static_cast<double *>(scratch));
+    if (!sure) mine = choose_exactly<V>(p, row, reinterpret_cast<double *>(scratch + SCRATCH));
 
-    // Weights: scores of the chosen, from their logits.
+    // Weights: scores of the chosen, from their logits.  (The fast division is off by 2
+    // units; its divisors are far from where it ends.)
     const bool on = mine >= 0;
     const float x = on ? load_any(p.logits, row + mine, p.type) : minus_inf();
     float s;
     if (!p.normalise) {
         if (softmax) {
-            if (!by_score) {
-                z = 0.0f;
+            float z = 0.0f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) z += l[i] == minus_inf() ? 0.0f : expf(l[i] - m);
-                z = warp_sum(z);
-            }
-            s = on ? expf(x - m) / z : 0.0f;
+            for (int i = 0; i < V; ++i) z += expf(l[i] - m);
+            s = __fdividef(expf(x - m), warp_sum(z));
         } else {
-            s = 1.0f / (1.0f + expf(-x));
+            s = __fdividef(1.0f, 1.0f + expf(-x));
         }
         weight = on ? p.scale * s : 0.0f;
     } else {
         // What the scores have in common cancels: the chosen experts' own
         // softmax; of sigmoids too where all are so small that 1 + e^x is 1,
         // and their sum may be 0 in FP32.
-        const float top = max_of_row(x);
+        const float top = warp_max(x);
         if (softmax || top < -40.0f)
             s = on ? expf(x - top) : 0.0f;
         else
-            s = on ? 1.0f / (1.0f + expf(-x)) : 0.0f;
+            s = on ? __fdividef(1.0f, 1.0f + expf(-x)) : 0.0f;
         const float sum = warp_sum(s);
-        weight = on ? p.scale * (s / sum) : 0.0f;
+        weight = on ? p.scale * __fdividef(s, sum) : 0.0f;
     }
     return mine;
 }
 
 // ------------------------------------------------------------------- plan
 
-__host__ __device__ constexpr int sort_ints(int E) { return 2 * (E + 1) + 64 + RANK_WARPS * E; }
+// Warps that rank a chunk's slots, each with counts of its own: as many as 32 KB hold.
+__host__ __device__ constexpr int rank_warps(int E, int most)
+{
+    return E * most <= 8192 ? most : E * 16 <= 8192 && most >= 16 ? 16 : 8;
+}
+__host__ __device__ constexpr int sort_ints(int E, int most) { return 2 * E + 64 + rank_warps(E, most) * E; }
 
 // The slots lo .. hi - 1 into the plan.  total[e], before[e] (shared): how many
-// slots have expert e in all, and before lo.  NT threads, all of them; `room`:
-// RANK_WARPS * E + 64 more ints.
+// slots have expert e in all, and before lo.  NT threads, all of them; `room`: the
+// rest of sort_ints.
 template <int NT>
 __device__ void rank_slots(const int32_t *experts, int lo, int hi, int slots, int E, const Plan &plan,
                            int *total, const int *before, int *room)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ranking = rank_warps(E, NT / 32);
     int *sums = room, *start = room + 64;            // start[w][e]: the next place of warp w's slots of e
-    const int per = ((hi - lo + RANK_WARPS - 1) / RANK_WARPS + 31) & ~31;
-    const int from = min(lo + warp * per, hi), to = warp < RANK_WARPS ? min(from + per, hi) : from;
-    for (int i = tid; i < RANK_WARPS * E; i += NT) start[i] = 0;
+    const int per = ((hi - lo + ranking - 1) / ranking + 31) & ~31;
+    const int from = min(lo + warp * per, hi), to = warp < ranking ? min(from + per, hi) : from;
+    // (the first slots of each lane, which are all there are of most chunks, are asked for once)
+    const int early = from + lane < to ? experts[from + lane] : -1;
+    for (int i = tid; i < ranking * E; i += NT) start[i] = 0;
     __syncthreads();
-    if (warp < RANK_WARPS)
-        for (int i = from + lane; i < to; i += 32) {
-            const int e = experts[i];
-            if ((unsigned)e < (unsigned)E) atomicAdd(&start[warp * E + e], 1);
-        }
+    for (int i = from + lane; i < to; i += 32) {
+        const int e = i == from + lane ? early : experts[i];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&start[warp * E + e], 1);
+    }
     // total becomes its running sum: where each expert begins
     int carried = 0;
     for (int base = 0; base < E; base += NT) {
@@ -416,12 +484,8 @@ __device__ void rank_slots(const int32_t *experts, int lo, int hi, int slots, in
         }
         if (lane == 31) sums[warp] = v;
         __syncthreads();
-        int lower = 0, all = 0;
-        for (int w = 0; w < NT / 32; ++w) {
-            const int o = sums[w];
-            lower += w < warp ? o : 0;
-            all += o;
-        }
+        int s = lane < NT / 32 ? sums[lane] : 0;
+        const int all = __reduce_add_sync(ALL, s), lower = __reduce_add_sync(ALL, lane < warp ? s : 0);
         if (e < E) total[e] = carried + lower + v - n;
         carried += all;
         __syncthreads();
@@ -429,8 +493,8 @@ __device__ void rank_slots(const int32_t *experts, int lo, int hi, int slots, in
     for (int e = tid; e < E; e += NT) {
         int next = total[e] + before[e];
         if (blockIdx.x == 0) plan.offsets[e] = total[e];
-#pragma unroll
-        for (int w = 0; w < RANK_WARPS; ++w) {
+#pragma unroll 8
+        for (int w = 0; w < ranking; ++w) {
             const int n = start[w * E + e];
             start[w * E + e] = next;
             next += n;
@@ -438,20 +502,19 @@ __device__ void rank_slots(const int32_t *experts, int lo, int hi, int slots, in
     }
     if (blockIdx.x == 0 && tid == 0) plan.offsets[E] = carried;
     __syncthreads();
-    if (warp < RANK_WARPS)
-        for (int i = from; i < to; i += 32) {
-            const int slot = i + lane;
-            const int e = slot < to ? experts[slot] : -1;
-            const bool on = (unsigned)e < (unsigned)E;
-            const unsigned peers = __match_any_sync(ALL, on ? e : -1);
-            int place = -1;
-            if (on) place = start[warp * E + e] + __popc(peers & ((1u << lane) - 1));
-            __syncwarp();
-            if (on && (peers >> lane) == 1u) start[warp * E + e] = place + 1;   // the last of its peers
-            __syncwarp();
-            if (slot < to) plan.position[slot] = place;
-            if (on) plan.source[place] = slot;
-        }
+    for (int i = from; i < to; i += 32) {
+        const int slot = i + lane;
+        const int e = i == from ? early : slot < to ? experts[slot] : -1;
+        const bool on = (unsigned)e < (unsigned)E;
+        const unsigned peers = __match_any_sync(ALL, on ? e : -1);
+        int place = -1;
+        if (on) place = start[warp * E + e] + __popc(peers & ((1u << lane) - 1));
+        __syncwarp();
+        if (on && (peers >> lane) == 1u) start[warp * E + e] = place + 1;       // the last of its peers
+        __syncwarp();
+        if (slot < to) plan.position[slot] = place;
+        if (on) plan.source[place] = slot;
+    }
     for (int r = carried + blockIdx.x * NT + tid; r < slots; r += gridDim.x * NT) plan.source[r] = -1;
 }
 
@@ -479,9 +542,39 @@ __global__ void __launch_bounds__(NT) route_kernel(const RouteArgs p, int scratc
     }
     int from, to;
     chunk_of(p.T, gridDim.x, blockIdx.x, from, to);
+    Experts<V> of;
+    of.most = 0.0f;
+    const int log_lanes = log_group_lanes(p.groups);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        of.bias[i] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.0f;
+        // (a bias of -inf masks its expert; behind the last, the logits do)
+        if (of.bias[i] != minus_inf()) of.most = of.bias[i] == of.bias[i] ? fmaxf(of.most, fabsf(of.bias[i])) : -minus_inf();
+        of.bit[i] = (uint8_t)(min(e, p.E - 1) / (p.E / p.groups) << log_lanes);
+    }
+    of.most = warp_max(of.most);
+    float l[V], next[V];
+    auto load = [&](int t) {
+        const long long row = t * p.ld + lane;
+        if (p.type == 2) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) next[i] = lane + 32 * i < p.E ? load_any(p.logits, row + 32 * i, 2) : minus_inf();
+        } else if (p.type == 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) next[i] = lane + 32 * i < p.E ? load_any(p.logits, row + 32 * i, 1) : minus_inf();
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) next[i] = lane + 32 * i < p.E ? load_any(p.logits, row + 32 * i, 0) : minus_inf();
+        }
+    };
+    if (from + warp < to) load(from + warp);
     for (int t = from + warp; t < to; t += NT / 32) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) l[i] = next[i];
+        if (t + NT / 32 < to) load(t + NT / 32);
         float weight;
-        const int e = choose<V>(p, t, scratch, weight);
+        const int e = choose<V>(p, t * p.ld, l, of, scratch, weight);
         if (lane < p.top) {
             p.experts[(long long)t * p.top + lane] = e;
             p.weights[(long long)t * p.top + lane] = weight;
@@ -544,7 +637,7 @@ __global__ void __launch_bounds__(SORT_THREADS)
         if (part < parts)
             for (int e = tid - part * E; e < E; e += SORT_THREADS) {
                 int all = 0, lower = 0;
-#pragma unroll 8
+#pragma unroll 16
                 for (int c = part; c < (int)gridDim.x; c += parts) {
                     const int n = counts[(long long)c * E + e];
                     all += n;
@@ -589,7 +682,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradArgs p, 
     float sum = 0.0f, z = 1.0f, m = 0.0f;
     bool full = softmax && !p.normalise;             // every logit has a gradient
     if (p.normalise) {
-        const float top = max_of_row(x);
+        const float top = warp_max(x);
         float s = 0.0f;
         if (on) s = softmax || top < -40.0f ? expf(x - top) : 1.0f / (1.0f + expf(-x));
         const float all = warp_sum(s);
@@ -609,7 +702,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradArgs p, 
             l[i] = e < p.E ? load_any(p.logits, row + e, p.type) : minus_inf();
             m = fmaxf(m, l[i]);
         }
-        m = max_of_row(m);
+        m = warp_max(m);
         z = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -671,8 +764,8 @@ cudaError_t route_form(const RouteArgs &p, int ctas, int32_t *counts, cudaStream
 {
     // choices in FP32, or in FP64 where sums or a bias make that needed
     const int wide = p.bias != nullptr || p.group_sum == 2 ? 8 : 4;
-    const int scratch = p.groups > 1 ? ((p.E + p.E / 32 + 1) * wide + 15) & ~15 : 0;
-    const size_t shared = (size_t)scratch * (NT / 32) + (p.plan.offsets ? 4 * sort_ints(p.E) : 0);
+    const int scratch = SCRATCH + (p.groups > 1 ? ((p.E + p.E / 32 + 1) * wide + 15) & ~15 : 0);
+    const size_t shared = (size_t)scratch * (NT / 32) + (p.plan.offsets ? 4 * sort_ints(p.E, NT / 32) : 0);
     static DeviceOnce once;
     return go(route_kernel<V, NT>, once, ctas, NT, shared, s, p, scratch, counts);
 }
@@ -722,7 +815,7 @@ cudaError_t launch_sort(int T, int E, int top, const int32_t *experts, const Pla
                         int32_t *counts, int *err, cudaStream_t s)
 {
     static DeviceOnce once;
-    return go(sort_kernel, once, chunks, SORT_THREADS, 4 * (size_t)sort_ints(E), s, T, E, top, experts, plan,
+    return go(sort_kernel, once, chunks, SORT_THREADS, 4 * (size_t)sort_ints(E, SORT_THREADS / 32), s, T, E, top, experts, plan,
               (const int32_t *)(chunks > 1 ? counts : nullptr), err);
 }
 

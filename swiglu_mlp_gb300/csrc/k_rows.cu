@@ -115,123 +115,150 @@ __device__ __forceinline__ int slot_row(const RowsArgs &p, int t, int *err)
     return at;
 }
 
-// The token and the first column of this warp's unit: `pieces` pieces per lane.
-template <int TYPE, int U>
-__device__ __forceinline__ bool find_unit(const RowsArgs &p, int chunks, int &t, int &col)
+// A warp has a span of a token's pieces: the token, and its first and last column.
+// Spans are `per` pieces, the last one of a token what is left.
+template <int TYPE>
+__device__ __forceinline__ bool find_span(const RowsArgs &p, int spans, int per, int &t, int &from, int &to)
 {
     const long long unit = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);
-    t = (int)(unit / chunks);
-    col = ((int)(unit - (long long)t * chunks) * 32 * U + (int)(threadIdx.x & 31)) * PIECE<TYPE>;
+    t = (int)(unit / spans);
+    const int i = (int)(unit - (long long)t * spans);
+    from = i * per * PIECE<TYPE>;
+    to = i == spans - 1 ? p.D : from + per * PIECE<TYPE>;
     return t < p.T;
 }
 
+// Columns of a piece that begins at col, of those before `to`.
 template <int TYPE>
-__device__ __forceinline__ int columns(int D, int col)
+__device__ __forceinline__ int columns(int to, long long col)
 {
-    return min(max(D - col, 0), PIECE<TYPE>);
+    return (int)min(max(to - col, 0ll), (long long)PIECE<TYPE>);
 }
 
 template <int TYPE, int U>
-__global__ void __launch_bounds__(32 * WARPS) dispatch_kernel(const RowsArgs p, int chunks, int *err)
+__global__ void __launch_bounds__(32 * WARPS) dispatch_kernel(const RowsArgs p, int spans, int per, int *err)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int t, col;
-    if (!find_unit<TYPE, U>(p, chunks, t, col)) return;
+    int t, from, to;
+    if (!find_span<TYPE>(p, spans, per, t, from, to)) return;
     const int at = slot_row(p, t, err);
-    uint4 x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int c = col + u * 32 * PIECE<TYPE>;
-        x[u] = load_piece<TYPE>(p.X, t * p.ldx + c, columns<TYPE>(p.D, c));
-    }
-    for (int j = 0; j < p.top; ++j) {
-        const int r = __shfl_sync(ALL, at, j);
-        if (r < 0) continue;
+    for (long long col = from + (threadIdx.x & 31) * PIECE<TYPE>; __any_sync(ALL, col < to); col += U * 32 * PIECE<TYPE>) {
+        uint4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = col + u * 32 * PIECE<TYPE>;
-            store_piece<TYPE>(p.rows, r * p.ldr + c, columns<TYPE>(p.D, c), x[u]);
+            const long long c = col + u * 32 * PIECE<TYPE>;
+            x[u] = load_piece<TYPE>(p.X, t * p.ldx + c, columns<TYPE>(to, c));
         }
-    }
-}
-
-template <int TYPE, int U>
-__global__ void __launch_bounds__(32 * WARPS) combine_kernel(const RowsArgs p, int chunks, int *err)
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    int t, col;
-    if (!find_unit<TYPE, U>(p, chunks, t, col)) return;
-    const int lane = threadIdx.x & 31;
-    const int at = slot_row(p, t, err);
-    const float w = p.weights != nullptr && lane < p.top ? p.weights[(long long)t * p.top + lane] : 1.0f;
-    int cnt[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) cnt[u] = columns<TYPE>(p.D, col + u * 32 * PIECE<TYPE>);
-    float sum[U][PIECE<TYPE>] = {};
-    for (int j = 0; j < p.top; j += BATCH) {
-        uint4 x[BATCH][U];
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            const int r = __shfl_sync(ALL, at, (j + b) & 31);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (j + b < p.top && r >= 0)
-                    x[b][u] = load_piece<TYPE>(p.rows, r * p.ldr + col + u * 32 * PIECE<TYPE>, cnt[u]);
-        }
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            const int r = __shfl_sync(ALL, at, (j + b) & 31);
-            const float f = __shfl_sync(ALL, w, (j + b) & 31);
-            if (j + b >= p.top || r < 0) continue;
+        for (int j = 0; j < p.top; ++j) {
+            const int r = __shfl_sync(ALL, at, j);
+            if (r < 0) continue;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                float v[PIECE<TYPE>];
-                to_floats<TYPE>(x[b][u], v);
-#pragma unroll
-                for (int i = 0; i < PIECE<TYPE>; ++i) sum[u][i] = fmaf(f, v[i], sum[u][i]);
+                const long long c = col + u * 32 * PIECE<TYPE>;
+                store_piece<TYPE>(p.rows, r * p.ldr + c, columns<TYPE>(to, c), x[u]);
             }
         }
     }
+}
+
+// Columns from col on in the type of the sum: as many as a piece of a row has.
+template <int TYPE, int OUT>
+__device__ __forceinline__ void store_sum(void *out, long long i, int cnt, const float (&v)[PIECE<TYPE>])
+{
+    if constexpr (TYPE == OUT) {
+        store_piece<OUT>(out, i, cnt, from_floats<OUT>(v));
+    } else {                                         // four FP32 columns to 16 bits
+        static_assert(TYPE == 2, "only sums of FP32 rows change their type");
+        typename Elem<OUT>::T *dst = static_cast<typename Elem<OUT>::T *>(out) + i;
+        if (cnt == 4) {
+            constexpr int kind = OUT == 1 ? OUT_BF16 : OUT_F16;
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(v[0], v[1], kind), pack2(v[2], v[3], kind));
+        } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const long long o = t * p.ldo + col + u * 32 * PIECE<TYPE>;
-        if (cnt[u] == 0) continue;
-        if (p.beta != 0.0f) {
-            const typename Elem<TYPE>::T *old = static_cast<const typename Elem<TYPE>::T *>(p.out) + o;
-#pragma unroll
-            for (int i = 0; i < PIECE<TYPE>; ++i)
-                if (i < cnt[u]) sum[u][i] = fmaf(p.beta, (float)old[i], sum[u][i]);
+            for (int j = 0; j < 4; ++j)
+                if (j < cnt) dst[j] = (typename Elem<OUT>::T)v[j];
         }
-        store_piece<TYPE>(p.out, o, cnt[u], from_floats<TYPE>(sum[u]));
     }
 }
 
-// A CTA per token, U pieces of its row per thread and round.
+template <int TYPE, int OUT, int U>
+__global__ void __launch_bounds__(32 * WARPS, 4) combine_kernel(const RowsArgs p, int spans, int per, int *err)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int t, from, to;
+    if (!find_span<TYPE>(p, spans, per, t, from, to)) return;
+    const int lane = threadIdx.x & 31;
+    const int at = slot_row(p, t, err);
+    const float w = p.weights != nullptr && lane < p.top ? p.weights[(long long)t * p.top + lane] : 1.0f;
+    for (long long col = from + lane * PIECE<TYPE>; __any_sync(ALL, col < to); col += U * 32 * PIECE<TYPE>) {
+        int cnt[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) cnt[u] = columns<TYPE>(to, col + u * 32 * PIECE<TYPE>);
+        float sum[U][PIECE<TYPE>] = {};
+        for (int j = 0; j < p.top; j += BATCH) {
+            uint4 x[BATCH][U];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int r = __shfl_sync(ALL, at, (j + b) & 31);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (j + b < p.top && r >= 0)
+                        x[b][u] = load_piece<TYPE>(p.rows, r * p.ldr + col + u * 32 * PIECE<TYPE>, cnt[u]);
+            }
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int r = __shfl_sync(ALL, at, (j + b) & 31);
+                const float f = __shfl_sync(ALL, w, (j + b) & 31);
+                if (j + b >= p.top || r < 0) continue;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float v[PIECE<TYPE>];
+                    to_floats<TYPE>(x[b][u], v);
+#pragma unroll
+                    for (int i = 0; i < PIECE<TYPE>; ++i) sum[u][i] = fmaf(f, v[i], sum[u][i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (cnt[u] == 0) continue;
+            const long long o = t * p.ldo + col + u * 32 * PIECE<TYPE>;
+            if (p.beta != 0.0f) {
+                const typename Elem<OUT>::T *old = static_cast<const typename Elem<OUT>::T *>(p.out) + o;
+#pragma unroll
+                for (int i = 0; i < PIECE<TYPE>; ++i)
+                    if (i < cnt[u]) sum[u][i] = fmaf(p.beta, (float)old[i], sum[u][i]);
+            }
+            store_sum<TYPE, OUT>(p.out, o, cnt[u], sum[u]);
+        }
+    }
+}
+
+// A CTA per token, its warps side by side along the row, U pieces per lane and round.
 template <int TYPE, int U>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const RowsArgs p, int *err)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float part[MAX_TOP][8];               // each warp's part of the products with d_out
-    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int at = slot_row(p, t, err);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int t = blockIdx.x, at = slot_row(p, t, err);
     const float w = p.weights != nullptr && lane < p.top ? p.weights[(long long)t * p.top + lane] : 1.0f;
     const bool products = p.d_weights != nullptr;
-    const int step = blockDim.x * PIECE<TYPE>;
-    long long first = 0;
-    do {                                             // (once for no columns: the products are 0)
-        uint4 d[U];
-        int cnt[U];
-        const int col = (int)first + threadIdx.x * PIECE<TYPE>;
+    const int step = warps * 32 * PIECE<TYPE>;
+    float mine = 0.0f;                               // lane j: slot j's product
+    for (int j = 0; j < p.top; j += BATCH) {
+        float dot[BATCH] = {};
+        for (long long col = (warp * 32 + lane) * PIECE<TYPE>; __any_sync(ALL, col < p.D); col += U * step) {
+            uint4 d[U], x[BATCH][U];
+            int cnt[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            cnt[u] = columns<TYPE>(p.D, col + u * step);
-            d[u] = load_piece<TYPE>(p.X, t * p.ldx + col + u * step, cnt[u]);
-        }
-        for (int j = 0; j < p.top; j += BATCH) {
-            uint4 x[BATCH][U];
+            for (int u = 0; u < U; ++u) {
+                cnt[u] = columns<TYPE>(p.D, col + u * step);
+                d[u] = load_piece<TYPE>(p.X, t * p.ldx + col + u * step, cnt[u]);
+            }
 #pragma unroll
             for (int b = 0; b < BATCH; ++b) {
                 const int r = __shfl_sync(ALL, at, (j + b) & 31);
@@ -244,38 +271,40 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RowsArgs p, int
             for (int b = 0; b < BATCH; ++b) {
                 const int r = __shfl_sync(ALL, at, (j + b) & 31);
                 const float f = __shfl_sync(ALL, w, (j + b) & 31);
-                if (j + b >= p.top) continue;
-                float dot = 0.0f;
-                if (r >= 0) {
+                if (j + b >= p.top || r < 0) continue;
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        float dv[PIECE<TYPE>], v[PIECE<TYPE>];
-                        to_floats<TYPE>(d[u], dv);
-                        if (products) {
-                            to_floats<TYPE>(x[b][u], v);
+                for (int u = 0; u < U; ++u) {
+                    float dv[PIECE<TYPE>], v[PIECE<TYPE>];
+                    to_floats<TYPE>(d[u], dv);
+                    if (products) {
+                        to_floats<TYPE>(x[b][u], v);
 #pragma unroll
-                            for (int i = 0; i < PIECE<TYPE>; ++i) dot = fmaf(dv[i], v[i], dot);
-                        }
-#pragma unroll
-                        for (int i = 0; i < PIECE<TYPE>; ++i) v[i] = f * dv[i];
-                        store_piece<TYPE>(p.out, r * p.ldo + col + u * step, cnt[u], from_floats<TYPE>(v));
+                        for (int i = 0; i < PIECE<TYPE>; ++i) dot[b] = fmaf(dv[i], v[i], dot[b]);
                     }
-                }
-                if (!products) continue;
 #pragma unroll
-                for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(ALL, dot, s);
-                if (lane == 0) part[j + b][warp] = first == 0 ? dot : part[j + b][warp] + dot;
+                    for (int i = 0; i < PIECE<TYPE>; ++i) v[i] = f * dv[i];
+                    store_piece<TYPE>(p.out, r * p.ldo + col + u * step, cnt[u], from_floats<TYPE>(v));
+                }
             }
         }
-        first += U * step;
-    } while (first < p.D);
-    if (!products) return;
-    __syncthreads();
-    if (threadIdx.x < p.top) {
-        float sum = 0.0f;
-        for (int i = 0; i < (int)blockDim.x / 32; ++i) sum += part[threadIdx.x][i];
-        p.d_weights[(long long)t * p.top + threadIdx.x] = sum;
+        if (!products) continue;
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) dot[b] += __shfl_xor_sync(ALL, dot[b], s);
+            if (lane == j + b) mine = dot[b];
+        }
     }
+    if (!products) return;
+    if (warps > 1) {
+        if (lane < p.top) part[lane][warp] = mine;
+        __syncthreads();
+        if (warp > 0) return;
+        mine = 0.0f;
+        if (lane < p.top)
+            for (int i = 0; i < warps; ++i) mine += part[lane][i];
+    }
+    if (lane < p.top) p.d_weights[(long long)t * p.top + lane] = mine;
 }
 
 template <class K, class... A>
@@ -293,32 +322,57 @@ cudaError_t go(K kernel, long long ctas, int threads, cudaStream_t s, A... args)
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-int ceil_to_units(int n, int per) { return (n + per - 1) / per; }
+long long ceil_div(long long n, long long per) { return (n + per - 1) / per; }
+
+// Spans that a token's row is cut into, of 32 `lane` pieces: as many as give the SMs
+// several waves of warps; of a row's remainder only more than a quarter is its own.
+struct Spans {
+    int count, per;
+    long long ctas;
+};
+template <int TYPE>
+Spans spans_of(const RowsArgs &p, int lane)
+{
+    const int per = 32 * lane;
+    const long long pieces = ceil_div(p.D, PIECE<TYPE>);
+    const int count = (int)std::max((pieces + per - 1 - per / 4) / per, 1ll);
+    return {count, per, ceil_div((long long)p.T * count, WARPS)};
+}
 
 template <int TYPE>
 cudaError_t dispatch(const RowsArgs &p, int sms, int *err, cudaStream_t s)
 {
     // Four pieces per lane, unless that leaves SMs without work.
-    const int wide = ceil_to_units(p.D, 32 * 4 * PIECE<TYPE>), narrow = ceil_to_units(p.D, 32 * PIECE<TYPE>);
-    if ((long long)p.T * wide >= 4ll * WARPS * sms)
-        return go(dispatch_kernel<TYPE, 4>, ((long long)p.T * wide + WARPS - 1) / WARPS, 32 * WARPS, s, p, wide, err);
-    return go(dispatch_kernel<TYPE, 1>, ((long long)p.T * narrow + WARPS - 1) / WARPS, 32 * WARPS, s, p, narrow, err);
+    Spans of = spans_of<TYPE>(p, 4);
+    if (of.ctas >= 4ll * sms) return go(dispatch_kernel<TYPE, 4>, of.ctas, 32 * WARPS, s, p, of.count, of.per, err);
+    of = spans_of<TYPE>(p, 1);
+    return go(dispatch_kernel<TYPE, 1>, of.ctas, 32 * WARPS, s, p, of.count, of.per, err);
 }
 
-template <int TYPE>
+template <int TYPE, int OUT>
 cudaError_t combine(const RowsArgs &p, int sms, int *err, cudaStream_t s)
 {
-    const int wide = ceil_to_units(p.D, 32 * 2 * PIECE<TYPE>), narrow = ceil_to_units(p.D, 32 * PIECE<TYPE>);
-    if ((long long)p.T * wide >= 4ll * WARPS * sms)
-        return go(combine_kernel<TYPE, 2>, ((long long)p.T * wide + WARPS - 1) / WARPS, 32 * WARPS, s, p, wide, err);
-    return go(combine_kernel<TYPE, 1>, ((long long)p.T * narrow + WARPS - 1) / WARPS, 32 * WARPS, s, p, narrow, err);
+    Spans of = spans_of<TYPE>(p, 2);
+    if (of.ctas >= 4ll * sms) return go(combine_kernel<TYPE, OUT, 2>, of.ctas, 32 * WARPS, s, p, of.count, of.per, err);
+    of = spans_of<TYPE>(p, 1);
+    return go(combine_kernel<TYPE, OUT, 1>, of.ctas, 32 * WARPS, s, p, of.count, of.per, err);
 }
 
 template <int TYPE>
 cudaError_t combine_grad(const RowsArgs &p, int *err, cudaStream_t s)
 {
-    const int warps = std::max(std::min(ceil_to_units(p.D, 32 * 2 * PIECE<TYPE>), 8), 1);
-    return go(combine_grad_kernel<TYPE, 2>, p.T, 32 * warps, s, p, err);
+    // The warps that leave the fewest lanes without a piece, the most of equals.
+    const long long pieces = ceil_div(p.D, PIECE<TYPE>);
+    int warps = 1;
+    long long least = ceil_div(pieces, 32);
+    for (int w = 2; w <= 8; ++w) {
+        const long long rounds = w * ceil_div(pieces, 32ll * w);
+        if (rounds <= least) {
+            least = rounds;
+            warps = w;
+        }
+    }
+    return go(combine_grad_kernel<TYPE, 1>, p.T, 32 * warps, s, p, err);
 }
 
 }  // namespace
@@ -330,7 +384,10 @@ cudaError_t launch_dispatch(const RowsArgs &p, int sms, int *err, cudaStream_t s
 
 cudaError_t launch_combine(const RowsArgs &p, int sms, int *err, cudaStream_t s)
 {
-    return p.type == 2 ? combine<2>(p, sms, err, s) : p.type == 1 ? combine<1>(p, sms, err, s) : combine<0>(p, sms, err, s);
+    if (p.type != 2) return p.type == 1 ? combine<1, 1>(p, sms, err, s) : combine<0, 0>(p, sms, err, s);
+    return p.out_type == 2   ? combine<2, 2>(p, sms, err, s)
+           : p.out_type == 1 ? combine<2, 1>(p, sms, err, s)
+                             : combine<2, 0>(p, sms, err, s);
 }
 
 cudaError_t launch_combine_grad(const RowsArgs &p, int *err, cudaStream_t s)

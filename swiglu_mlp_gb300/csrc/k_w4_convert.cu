@@ -1,9 +1,13 @@
 // k_w4_convert.cu — weights to 4 bits with group scales, and back.
 //
-// Both directions stream: 2 bytes (16-bit x) and half a byte per element. A lane
+// Both directions stream: 2 bytes (16-bit x) and half a byte per element, which
+// leaves about ten instructions per element and lane; so a code costs a product with
+// two corrections, two bounds, an addition that rounds and one that packs.  A lane
 // has eight columns, a word of codes; a warp 256 columns of four rows; a CTA 32
 // rows, whose scales (which lie side by side for the rows of a group of columns)
 // pass through shared memory, so that they are stored 64 bytes at a time.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -17,6 +21,8 @@ constexpr unsigned ALL = 0xffffffffu;
 constexpr int THREADS = 256;
 constexpr int ROWS = 4;              // per warp
 constexpr int CTA_ROWS = 32;
+constexpr int ROWS_BACK = 8;         // ... of the way back, to have as much to read on the way
+constexpr int CTA_ROWS_BACK = 64;
 constexpr int COLS = 256;            // per CTA
 constexpr int BLOCKS = COLS / 32;    // most groups of columns in them
 
@@ -87,6 +93,20 @@ __device__ __forceinline__ void store8(void *x, long long i, int cnt, const floa
 // half, 1, 3, 5, 7 in the upper, so that one mask takes a pair of neighbours.
 __device__ __forceinline__ constexpr int code_bit(int j) { return 16 * (j & 1) + 4 * (j >> 1); }
 
+// The larger, or smaller, of two; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // A scale in FP32 to its type: to nearest even; beyond the type's largest value
 // that value.
 __device__ __forceinline__ uint16_t scale_bits(float s, bool bf16)
@@ -96,6 +116,18 @@ __device__ __forceinline__ uint16_t scale_bits(float s, bool bf16)
         return b == 0x7f80 ? 0x7f7f : b;
     }
     return __half_as_ushort(__float2half_rn(fminf(s, 65504.0f)));
+}
+
+// x / s from the product with the inverse and one residual correction
+// (Markstein's), which rounds as the division does where that decides: a tie
+// between two codes times the scale has at most 16 bits, so that an x next to it has
+// a quotient more than half of a float's unit from the tie.  Scales below TINY, and
+// what they divide, are made LARGER first, or the inverse might have no FP32 value.
+constexpr float TINY = 0x1p-100f, LARGER = 0x1p100f;
+__device__ __forceinline__ float quotient(float x, float s, float inverse)
+{
+    const float q = x * inverse;
+    return fmaf(fmaf(-q, s, x), inverse, q);
 }
 
 template <int TYPE, bool ZERO>
@@ -116,51 +148,85 @@ __global__ void __launch_bounds__(THREADS) w4_quantize_kernel(const W4Convert p,
         const int n = n0 + warp * ROWS + r;
         load8<TYPE>(p.X, ((long long)g * p.w.N + n) * p.ldx + k, n < p.w.N ? cnt : 0, v[r]);
     }
+    // where this lane's codes end (those of columns that do not exist are 0)
+    uint32_t keep = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < cnt) keep |= 15u << code_bit(j);
+    // The ranges of the rows' groups of columns.  (max.NaN: a NaN anywhere shows.)
+    float lo[ROWS], hi[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        lo[r] = hi[r] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (ZERO) lo[r] = min_nan(lo[r], v[r][j]);
+            hi[r] = max_nan(hi[r], ZERO ? v[r][j] : fabsf(v[r][j]));
+        }
+        for (int d = 1; d < lanes; d <<= 1) {
+            hi[r] = max_nan(hi[r], __shfl_xor_sync(ALL, hi[r], d));
+            if (ZERO) lo[r] = min_nan(lo[r], __shfl_xor_sync(ALL, lo[r], d));
+        }
+    }
+    // Four lanes of a group of columns compute a row's scale each: its bits (0x7fff, a
+    // NaN, where the group holds a NaN or an infinity), inverse and zero point.
+    static_assert(ROWS == 4, "a row for each of a group's four first lanes");
+    uint32_t my_bits;
+    float my_inverse, my_zero = 8.0f;
+    {
+        const int r = lane & 3;
+        const float h = r == 0 ? hi[0] : r == 1 ? hi[1] : r == 2 ? hi[2] : hi[3];
+        const float l = !ZERO ? 0.0f : r == 0 ? lo[0] : r == 1 ? lo[1] : r == 2 ? lo[2] : lo[3];
+        const float inf = __int_as_float(0x7f800000);
+        my_bits = scale_bits(ZERO ? (h - l) / 15.0f : h / 7.0f, bf16);
+        const float s = half_value((uint16_t)my_bits, bf16);
+        // (the inverse of a very small scale may have no FP32 value: see below)
+        my_inverse = s > 0.0f ? 1.0f / (s < TINY ? s * LARGER : s) : 0.0f;
+        if (ZERO) {
+            const float larger = s < TINY ? LARGER : 1.0f;
+            my_zero = fminf(fmaxf(rintf(quotient(-l * larger, s * larger, my_inverse)), 0.0f), 15.0f);
+        }
+        if (!(h < inf) || !(l > -inf)) {
+            my_bits = 0x7fff;
+            my_zero = 0.0f;
+        }
+    }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const int row = warp * ROWS + r, n = n0 + row;
-        float lo = 0.0f, hi = 0.0f;
-        bool finite = true;
+        const int from = (lane & ~3) + r;
+        const uint32_t bits = __shfl_sync(ALL, my_bits, from);
+        const float inverse = __shfl_sync(ALL, my_inverse, from);
+        const float z = ZERO ? __shfl_sync(ALL, my_zero, from) : 8.0f;
+        const bool bad = bits == 0x7fffu;
+        const float s = half_value((uint16_t)bits, bf16);
+        const bool tiny = s < TINY;
+        const float scale = tiny ? s * LARGER : s;
+        if (__any_sync(ALL, tiny)) {                 // seldom: all of these rows' numbers are made larger
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            lo = fminf(lo, v[r][j]);
-            hi = fmaxf(hi, v[r][j]);
-            finite = finite && fabsf(v[r][j]) < __int_as_float(0x7f800000);
+            for (int j = 0; j < 8; ++j) v[r][j] = tiny ? v[r][j] * LARGER : v[r][j];
         }
-        if (!finite) hi = __int_as_float(0x7f800000);    // (a NaN may not show in either)
-        for (int d = 1; d < lanes; d <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(ALL, lo, d));
-            hi = fmaxf(hi, __shfl_xor_sync(ALL, hi, d));
-        }
-        const bool bad = !(hi < __int_as_float(0x7f800000) && lo > -__int_as_float(0x7f800000));
-        const uint16_t bits = scale_bits(ZERO ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f, bf16);
-        const float s = half_value(bits, bf16);
-        const float inverse = s > 0.0f ? 1.0f / s : 0.0f;
-        // x / s with one residual correction (Markstein's), which rounds as the
-        // division does where that decides: a tie between two codes times the
-        // scale has at most 16 bits, so that an x next to it has a quotient more
-        // than half of a float's unit from the tie.  (The inverse of a very small
-        // scale may have no FP32 value: divided.)
-        const bool plain = s < 0x1p-100f;
-        auto quotient = [&](float x) {
-            if (plain) return s > 0.0f ? x / s : 0.0f;
-            const float q = x * inverse;
-            return fmaf(fmaf(-q, s, x), inverse, q);
-        };
-        const float z = ZERO ? fminf(fmaxf(rintf(quotient(-lo)), 0.0f), 15.0f) : 8.0f;
+        // 2^23 + 2^22 takes the units' place: the sum is rounded to a whole number,
+        // ties to even, and its lowest bits are that number's.
+        constexpr float UNITS = 12582912.0f;
         uint32_t word = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float q = fminf(fmaxf(rintf(quotient(v[r][j])) + z, 0.0f), 15.0f);
-            word |= (uint32_t)(j < cnt ? (int)q : 0) << code_bit(j);
+            const float q = fminf(fmaxf(quotient(v[r][j], scale, inverse), -z), 15.0f - z) + UNITS;
+            word += __float_as_uint(q) << code_bit(j);
         }
-        if (bad) word = 0;
+        // less the units, plus the zero point, in every code's place
+        uint32_t places = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) places += 1u << code_bit(j);
+        word += places * ((uint32_t)(int)z - __float_as_uint(UNITS));
+        word = bad ? 0 : word & keep;
         if (n < p.w.N && k < (p.w.K + 31) / 32 * 32)
             *reinterpret_cast<uint32_t *>(const_cast<uint8_t *>(p.w.Q) +
                                           ((long long)g * p.w.N + n) * p.w.row_bytes() + k / 2) = word;
         if (lane % lanes == 0) {
-            scales[lane / lanes][row] = bad ? 0x7fff : bits;
-            if (ZERO) zeros[lane / lanes][row] = bad ? 0 : (uint8_t)z;
+            scales[lane / lanes][row] = (uint16_t)bits;
+            if (ZERO) zeros[lane / lanes][row] = (uint8_t)z;
         }
     }
     __syncthreads();
@@ -180,15 +246,45 @@ __global__ void __launch_bounds__(THREADS) w4_dequantize_kernel(const W4Convert 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = blockIdx.x / row_tiles, n0 = (blockIdx.x - g * row_tiles) * CTA_ROWS + warp * ROWS;
+    const int g = blockIdx.x / row_tiles, n0 = (blockIdx.x - g * row_tiles) * CTA_ROWS_BACK + warp * ROWS_BACK;
     const int k = blockIdx.y * COLS + lane * 8;
     const int cnt = min(max(p.w.K - k, 0), 8);
     if (cnt == 0) return;
     const long long at = ((long long)g * p.w.blocks() + k / p.w.group) * p.w.lds + n0;
-    uint32_t word[ROWS];
-    float s[ROWS], z[ROWS];
+    if (TYPE == p.stype && cnt == 8) {
+        // To the scales' own type two at a time: a code less its zero point is exact
+        // there, and its product with the scale is rounded once.
+        using T2 = std::conditional_t<TYPE == 1, __nv_bfloat162, __half2>;
+        constexpr uint32_t UNITS = TYPE == 1 ? 0x43004300u : 0x64006400u;    // 128 or 1024: a code in the units' place
+        uint32_t codes[ROWS_BACK], scale[ROWS_BACK], zero[ROWS_BACK];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
+        for (int r = 0; r < ROWS_BACK; ++r) {
+            const int n = min(n0 + r, p.w.N - 1) - n0;           // (n0 may be behind the last row)
+            codes[r] = *reinterpret_cast<const uint32_t *>(p.w.Q + ((long long)g * p.w.N + n0 + n) * p.w.row_bytes() + k / 2);
+            scale[r] = static_cast<const uint16_t *>(p.w.S)[at + n];
+            zero[r] = ZERO ? p.w.Z[at + n] & 15u : 8u;
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS_BACK; ++r) {
+            if (n0 + r >= p.w.N) continue;
+            const uint32_t w = codes[r], zz = UNITS + zero[r] * 0x00010001u, ss = scale[r] * 0x00010001u;
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t q = ((w >> (4 * i)) & 0x000f000fu) | UNITS;
+                const T2 d = __hmul2(__hsub2(*reinterpret_cast<const T2 *>(&q), *reinterpret_cast<const T2 *>(&zz)),
+                                     *reinterpret_cast<const T2 *>(&ss));
+                u[i] = *reinterpret_cast<const uint32_t *>(&d);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.X) + ((long long)g * p.w.N + n0 + r) * p.ldx + k) =
+                make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        return;
+    }
+    uint32_t word[ROWS_BACK];
+    float s[ROWS_BACK], z[ROWS_BACK];
+#pragma unroll
+    for (int r = 0; r < ROWS_BACK; ++r) {
         if (n0 + r >= p.w.N) continue;
         word[r] = *reinterpret_cast<const uint32_t *>(
             p.w.Q + ((long long)g * p.w.N + n0 + r) * p.w.row_bytes() + k / 2);
@@ -196,7 +292,7 @@ __global__ void __launch_bounds__(THREADS) w4_dequantize_kernel(const W4Convert 
         z[r] = ZERO ? (float)(p.w.Z[at + r] & 15) : 8.0f;
     }
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
+    for (int r = 0; r < ROWS_BACK; ++r) {
         if (n0 + r >= p.w.N) continue;
         float v[8];
 #pragma unroll
@@ -208,7 +304,7 @@ __global__ void __launch_bounds__(THREADS) w4_dequantize_kernel(const W4Convert 
 template <int TYPE, bool ZERO>
 cudaError_t launch(const W4Convert &p, bool back, cudaStream_t s)
 {
-    const int row_tiles = (p.w.N + CTA_ROWS - 1) / CTA_ROWS;
+    const int rows = back ? CTA_ROWS_BACK : CTA_ROWS, row_tiles = (p.w.N + rows - 1) / rows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)p.G * row_tiles), (unsigned)((p.w.K + COLS - 1) / COLS));
     cfg.blockDim = dim3(THREADS);

@@ -63,7 +63,8 @@ cudaError_t launch_route_grad(const RouteGradArgs &p, int *err, cudaStream_t s);
 struct RowsArgs {
     int T, D, top;
     int R;                             // rows that `rows` and `d_rows` have
-    int type;                          // swg_type of X, rows, out, d_out, d_rows
+    int type;                          // swg_type of X, rows, d_out, d_rows
+    int out_type;                      // combine: of out, `type` or any for FP32 rows
     const int32_t *position;           // T x top
     const float *weights;              // T x top or nullptr: ones
     const void *X;                     // dispatch: T x D; combine_grad: d_out

@@ -32,10 +32,10 @@ def route(l, bias, top, score="softmax", groups=1, top_groups=None, group_sum=1,
     experts, weights = np.full((T, top), -1, np.int64), np.zeros((T, top))
     for t in range(T):
         c = l[t] if bias is None and group_sum == 1 else s[t] if bias is None else s[t] + bias
-        if np.isnan(c).any() or np.isnan(s[t]).any():
+        left = ~np.isneginf(l[t]) & ~np.isneginf(c)
+        if np.isnan(c[left]).any() or np.isnan(s[t]).any():
             experts[t], weights[t] = np.arange(top), np.nan
             continue
-        left = ~np.isneginf(l[t]) & ~np.isneginf(c)
         if top_groups < groups:
             size = E // groups
             value = []
@@ -44,7 +44,8 @@ def route(l, bias, top, score="softmax", groups=1, top_groups=None, group_sum=1,
                 value.append(own[:group_sum].sum() if len(own) else -np.inf)
             best = sorted((g for g in range(groups) if value[g] > -np.inf), key=lambda g: (-value[g], g))[:top_groups]
             left &= np.isin(np.arange(E) // size, best)
-        order = sorted(np.flatnonzero(left), key=lambda e: (-c[e], e))[:top]
+        by = l[t] if bias is None else c                 # (groups are chosen by their scores all the same)
+        order = sorted(np.flatnonzero(left), key=lambda e: (-by[e], e))[:top]
         experts[t, :len(order)] = order
         w = s[t, order]
         if normalise and len(order):

@@ -320,7 +320,8 @@ def padded(rows, cols, dtype, seed, std=1.0):
 
 
 SHAPES = [(1, 1, 1, 1), (1, 4096, 8, 8), (5, 8, 4, 2), (33, 129, 16, 4), (64, 2051, 48, 6), (7, 8200, 9, 3), (300, 520, 8, 32),
-          (2000, 264, 64, 2), (700, 4100, 4, 1), (3, 64, 2, 5)]
+          (2000, 264, 64, 2), (700, 4100, 4, 1), (3, 64, 2, 5),
+          (2600, 1030, 64, 5), (5000, 20, 8, 2)]
 
 
 @pytest.mark.parametrize("T,D,E,top", SHAPES)
@@ -343,11 +344,11 @@ def test_dispatch(T, D, E, top, dtype):
 
 
 @pytest.mark.parametrize("T,D,E,top", SHAPES)
-@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("source,dtype", [("bf16", "bf16"), ("f16", "f16"), ("f32", "f32"), ("f32", "bf16"), ("f32", "f16")])
 @pytest.mark.parametrize("weighted,beta", [(True, 0.0), (False, 1.0), (True, -0.5)])
-def test_combine(T, D, E, top, dtype, weighted, beta):
+def test_combine(T, D, E, top, source, dtype, weighted, beta):
     pos = a_plan(T, E, top, T + D)
-    rows = padded(T * top, D, dtype, 2)
+    rows = padded(T * top, D, source, 2)
     used = pos[pos >= 0]
     idle = np.setdiff1d(np.arange(T * top), used)
     rows[torch.from_numpy(idle).cuda()] = float("nan")   # rows of no slot

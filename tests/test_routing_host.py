@@ -69,10 +69,10 @@ def test_expert_route_grad(lib):
 
 
 def test_moving_rows(lib):
-    d = dict(T=128, R=512, D=64, top=4, X=P, ldx=64, type=1, pos=P, rows=P, ldr=64, we=P, beta=0.0, out=P, ldo=64,
+    d = dict(T=128, R=512, D=64, top=4, X=P, ldx=64, type=1, pos=P, rows=P, ldr=64, we=P, beta=0.0, out=P, ldo=64, otype=1,
              dr=P, lddr=64, dw=P)
     calls = [(lib.expert_dispatch, "T R D top X ldx type pos rows ldr", ("X", "rows"), ("ldx", "ldr")),
-             (lib.expert_combine, "T R D top rows ldr type pos we beta out ldo", ("rows", "out"), ("ldr", "ldo")),
+             (lib.expert_combine, "T R D top rows ldr type pos we beta out ldo otype", ("rows", "out"), ("ldr", "ldo")),
              (lib.expert_combine_grad, "T R D top X ldx rows ldr type pos we dr lddr dw", ("X", "rows", "dr"),
               ("ldx", "ldr", "lddr"))]
     for fn, names, pointers, strides in calls:
@@ -89,6 +89,10 @@ def test_moving_rows(lib):
             assert f(**{name: 2 ** 31}) == UNSUPPORTED
         assert f(T=0) == OK
     assert call(lib.expert_combine, calls[1][1], d, we=P + 2) == MISALIGNED
+    for bad in (0, 2, 3):                               # bfloat16 rows give bfloat16
+        assert call(lib.expert_combine, calls[1][1], d, otype=bad) == UNSUPPORTED
+    assert call(lib.expert_combine, calls[1][1], d, type=2, otype=3) == UNSUPPORTED
+    assert call(lib.expert_combine, calls[1][1], d, type=2, otype=0, ldo=68) == MISALIGNED
     assert call(lib.expert_combine_grad, calls[2][1], d, dw=P + 2) == MISALIGNED
 
 
