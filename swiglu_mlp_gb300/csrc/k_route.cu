@@ -121,20 +121,18 @@ __device__ __forceinline__ int take_best(float (&key)[V], float &best)
 // 32, so that groups of 32 do not share banks.
 __device__ __forceinline__ int at_scratch(int e) { return e + (e >> 5); }
 
-// Lanes that look at a group together: as many as there are for each, a power of two.
+// Lanes that look at a group in the scratch together: as many as there are for each,
+// a power of two.  (A group's home is the first of them.)
 __device__ __forceinline__ int log_group_lanes(int groups) { return 31 - __clz(32 / groups); }
 
-// The best groups as a bit mask, group g's bit g << log_group_lanes, from the choices
-// in the warp's scratch (-inf where masked).  `tol` > 0: `sure` becomes false where
-// the worst of them is nearer than it to the best of the others.
+// The group's two largest choices, at its home, from those in the warp's scratch (-inf
+// where masked).
 template <class F>
-__device__ __forceinline__ unsigned best_groups(const RouteArgs &p, const F *scratch, F tol, bool &sure)
+__device__ __forceinline__ void largest_two(int groups, int size, int log_lanes, const F *scratch, F &a, F &b)
 {
-    const int lane = threadIdx.x & 31, size = p.E / p.groups;
-    const int log_lanes = log_group_lanes(p.groups), lanes = 1 << log_lanes, g = lane >> log_lanes;
-    const F low = (F)minus_inf();
-    F a = low, b = low;                              // the two largest
-    if (g < p.groups)
+    const int lane = threadIdx.x & 31, lanes = 1 << log_lanes, g = lane >> log_lanes;
+    a = b = (F)minus_inf();
+    if (g < groups)
         for (int i = lane & (lanes - 1); i < size; i += lanes) {
             const F v = scratch[at_scratch(g * size + i)];
             const F less = v < a ? v : a;
@@ -147,61 +145,78 @@ __device__ __forceinline__ unsigned best_groups(const RouteArgs &p, const F *scr
         a = a2 > a ? a2 : a;
         b = less > more ? less : more;
     }
-    const F value = p.group_sum == 2 && b > low ? a + b : a;
-    auto key = ordered(value);
-    if (!(a > low) || (lane & (lanes - 1)) != 0) key = 0;
-    int rank = 0;
-    for (int h = 0; h < p.groups; ++h) {
-        const auto other = __shfl_sync(ALL, key, h << log_lanes);
-        rank += other > key || (other == key && h < g);
-    }
-    const bool kept = key > 0 && rank < p.top_groups;
-    if constexpr (sizeof(F) == 4)
-        if (tol > (F)0) {
-            const uint32_t worst = __reduce_min_sync(ALL, kept ? key : 0xffffffffu);
-            const uint32_t rest = __reduce_max_sync(ALL, kept ? 0u : key);
-            if (rest > 0 && !(value_of(worst) - value_of(rest) > tol)) sure = false;
-        }
-    return __ballot_sync(ALL, kept);
 }
 
-// The token's experts in FP64: lane j's is the j'th.  Seldom called: its arrays
-// are in local memory, so that it takes no registers from the rest.
+// The best groups as a bit mask over their homes, from the two largest choices there
+// (a > -inf only there).  Where the worst of them is not further than `tol` > 0 above the best of the
+// others, `near` are those that may change places, and `last` is, at a group's home,
+// the smallest choice in its value.
+template <class F>
+__device__ __forceinline__ unsigned best_groups(const RouteArgs &p, F a, F b, F tol, unsigned &near, F &last)
+{
+    const int lane = threadIdx.x & 31;
+    const F low = (F)minus_inf();
+    const bool both = p.group_sum == 2 && b > low;
+    const F value = both ? a + b : a;
+    last = both ? b : a;
+    auto key = ordered(value);
+    if (!(a > low)) key = 0;
+    const auto own = key;
+    unsigned keep = 0;
+    auto best = key;
+    for (int j = 0; j < p.top_groups; ++j) {
+        best = warp_max(key);
+        if (best == 0) break;
+        const int home = __ffs(__ballot_sync(ALL, key == best)) - 1;
+        keep |= 1u << home;
+        if (lane == home) key = 0;
+    }
+    near = 0;
+    if constexpr (sizeof(F) == 4)
+        if (tol > (F)0 && best != 0) {
+            const uint32_t rest = warp_max(key);
+            const float w = value_of(best), r = value_of(rest);
+            if (rest != 0 && !(w - r > tol))
+                near = __ballot_sync(ALL, own != 0 && (keep >> lane & 1 ? value - r <= tol : w - value <= tol));
+        }
+    return keep;
+}
+
+// The token's experts in FP64: lane j's is the j'th.  For what the candidates alone do
+// not decide (many equal choices, biases of +inf).
 template <int V>
 __device__ __noinline__ int choose_exactly(const RouteArgs &p, long long row, double *scratch)
 {
-    const int lane = threadIdx.x & 31, size = p.E / p.groups;
+    constexpr int TOGETHER = V < 8 ? V : 8;
+    const int lane = threadIdx.x & 31;
     const double low = (double)minus_inf();
     double c[V];
     uint64_t key[V];
-    double m = low;
-#pragma unroll 1
+    double m = low, z = 0.0;
+    uint32_t masked = 0;
+#pragma unroll TOGETHER
     for (int i = 0; i < V; ++i) {
         const int e = lane + 32 * i;
         c[i] = e < p.E ? (double)load_any(p.logits, row + e, p.type) : low;
+        if (c[i] == low) masked |= 1u << i;
         m = c[i] > m ? c[i] : m;
     }
     for (int d = 16; d > 0; d >>= 1) {
         const double o = __shfl_xor_sync(ALL, m, d);
         m = o > m ? o : m;
     }
-    double z = 0.0;
-    uint32_t masked = 0;
-#pragma unroll 1
+    const bool softmax = p.score == SCORE_SOFTMAX;
+#pragma unroll TOGETHER
     for (int i = 0; i < V; ++i) {
-        if (c[i] == low) masked |= 1u << i;
-        if (p.score == SCORE_SOFTMAX) {
-            c[i] = c[i] == low ? 0.0 : exp(c[i] - m);
-            z += c[i];
-        } else {
-            c[i] = 1.0 / (1.0 + exp(-c[i]));
-        }
+        const double e = exp(softmax ? c[i] - m : -c[i]);
+        z += e;
+        c[i] = softmax ? e : 1.0 / (1.0 + e);
     }
-    z = p.score == SCORE_SOFTMAX ? warp_sum(z) : 1.0;
-#pragma unroll 1
+    const double inverse = softmax ? 1.0 / warp_sum(z) : 1.0;
+#pragma unroll TOGETHER
     for (int i = 0; i < V; ++i) {
         const int e = lane + 32 * i;
-        c[i] /= z;
+        c[i] *= inverse;
         if (p.bias != nullptr && e < p.E) c[i] += (double)p.bias[e];
         if (c[i] == low) masked |= 1u << i;
         // (without a bias the order is that of the logits, groups apart)
@@ -209,17 +224,20 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &p, long long row, do
         key[i] = masked >> i & 1 ? 0 : ordered(by);
     }
     if (p.groups > 1) {
+        const int size = p.E / p.groups, log_lanes = log_group_lanes(p.groups);
         __syncwarp();
-#pragma unroll 1
+#pragma unroll TOGETHER
         for (int i = 0; i < V; ++i) {
             const int e = lane + 32 * i;
             if (e < p.E) scratch[at_scratch(e)] = masked >> i & 1 ? low : c[i];
         }
         __syncwarp();
-        bool sure = true;
-        const unsigned keep = best_groups<double>(p, scratch, 0.0, sure);
-        const int log_lanes = log_group_lanes(p.groups);
-#pragma unroll 1
+        unsigned near;
+        double last, a, b;
+        largest_two<double>(p.groups, size, log_lanes, scratch, a, b);
+        if ((lane & ((1 << log_lanes) - 1)) != 0) a = low;
+        const unsigned keep = best_groups<double>(p, a, b, 0.0, near, last);
+#pragma unroll TOGETHER
         for (int i = 0; i < V; ++i) {
             const int e = lane + 32 * i;
             if (e >= p.E || !(keep >> (e / size << log_lanes) & 1)) key[i] = 0;
@@ -229,7 +247,7 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &p, long long row, do
     for (int j = 0; j < p.top; ++j) {
         uint64_t k = 0;
         int at = 0;
-#pragma unroll 1
+#pragma unroll TOGETHER
         for (int i = 0; i < V; ++i)
             if (key[i] > k) {
                 k = key[i];
@@ -238,7 +256,9 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &p, long long row, do
         const uint64_t best = warp_max(k);
         if (best == 0) break;
         const int e = (int)__reduce_min_sync(ALL, k == best ? (unsigned)(lane + 32 * at) : 0xffffffffu);
-        if (lane == e % 32) key[e / 32] = 0;
+#pragma unroll TOGETHER
+        for (int i = 0; i < V; ++i)
+            if (lane + 32 * i == e) key[i] = 0;
         if (lane == j) mine = e;
     }
     return mine;
@@ -251,12 +271,63 @@ struct Candidate {
 };
 constexpr int SCRATCH = 32 * sizeof(Candidate);      // bytes of a warp's, before its choices
 
+// What follows decides in FP64 where FP32 cannot.  It is seldom run, and then with
+// nothing of it in the instruction caches, of which every 128 bytes come from afar: so
+// it looks at the candidates alone, one per lane, in few instructions.  (All choices
+// of a token in FP64: 16 us.)
+
+// Expert e's choice; of the softmax with the sum of exact_sum.
+__device__ __noinline__ double exact_choice(const RouteArgs &p, long long row, int e, float m, double sum)
+{
+    const double x = (double)load_any(p.logits, row + e, p.type);
+    const bool softmax = p.score == SCORE_SOFTMAX;
+    const double y = exp(softmax ? x - (double)m : -x);
+    const double s = softmax ? y / sum : 1.0 / (1.0 + y);
+    return p.bias != nullptr ? s + (double)p.bias[e] : s;
+}
+
+__device__ __noinline__ double exact_sum(const RouteArgs &p, long long row, float m)
+{
+    double z = 0.0;
+#pragma unroll 1
+    for (int e = threadIdx.x & 31; e < p.E; e += 32) z += exp((double)load_any(p.logits, row + e, p.type) - (double)m);
+    return warp_sum(z);
+}
+
+// The groups once more: candidates (n <= 32, their group's first lane in `home`) of the
+// groups that are `near`; `keep` gets the best of these by their exact values.
+__device__ __noinline__ unsigned exact_groups(const RouteArgs &p, unsigned keep, unsigned near, bool on, int home, double choice)
+{
+    const int lane = threadIdx.x & 31;
+    uint64_t value = 0;                              // at a group's first lane
+    for (unsigned left = near; left != 0; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        uint64_t key = on && home == g ? ordered(choice) : 0;
+        const uint64_t a = warp_max(key);
+        const unsigned with = __ballot_sync(ALL, key == a);
+        if (lane == __ffs(with) - 1) key = 0;
+        const uint64_t b = p.group_sum == 2 ? warp_max(key) : 0;
+        auto of = [](uint64_t k) { return __longlong_as_double((long long)(k >> 63 ? k ^ 0x8000000000000000ull : ~k)); };
+        if (lane == g) value = ordered(b != 0 ? of(a) + of(b) : of(a));
+    }
+    int rank = 0;
+    for (unsigned left = near; left != 0; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        const uint64_t other = __shfl_sync(ALL, value, g);
+        rank += other > value || (other == value && g < lane);
+    }
+    const int places = __popc(keep & near);
+    return (keep & ~near) | __ballot_sync(ALL, (near >> lane & 1) && rank < places);
+}
+
 // What a warp keeps from token to token.
 template <int V>
 struct Experts {
     float bias[V];                                   // of this lane's, 0 without
     float most;                                      // the largest magnitude among all biases
-    uint8_t bit[V];                                  // of their groups' in best_groups
+    int size, rows;                                  // of a group: experts, and how many places of every lane (0: not whole ones)
+    int log_lanes;                                   // (0 with whole places: group g's home is lane g)
+    uint8_t home[V];                                 // of their groups
 };
 
 // The experts of a token, lane j's the j'th (-1: none), and lane j's weight, from
@@ -274,7 +345,7 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
     bool nan = false;
-    float key[V];                                    // -inf where masked
+    float key[V], by_group[V];                       // what experts and groups go by; -inf where masked
     bool sure = true;
     float tol = 0.0f;
     if (by_score) {
@@ -313,14 +384,14 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
             if (l[i] == minus_inf()) s[i] = minus_inf();
             nan = nan || s[i] != s[i];
             key[i] = biased || s[i] == minus_inf() ? s[i] : l[i];
-            if (grouped && lane + 32 * i < p.E) choices[at_scratch(lane + 32 * i)] = s[i];
+            by_group[i] = s[i];
         }
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             key[i] = l[i];
             nan = nan || l[i] != l[i];
-            if (grouped && lane + 32 * i < p.E) choices[at_scratch(lane + 32 * i)] = l[i];
+            by_group[i] = l[i];
         }
         if (softmax && !p.normalise) m = warp_max(m == m ? m : minus_inf());
     }
@@ -336,12 +407,68 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
         weight = 0.0f;
         return -1;
     }
+    Candidate *buffer = reinterpret_cast<Candidate *>(scratch);
     if (grouped) {
-        __syncwarp();
-        const unsigned keep = best_groups<float>(p, choices, 2.0f * tol, sure);
+        if (of.rows == 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (lane + 32 * i < p.E) choices[at_scratch(lane + 32 * i)] = by_group[i];
+            __syncwarp();
+        }
+        unsigned near;
+        float last, a = minus_inf(), b = minus_inf();
+        if (of.rows > 0) {
+            // Groups of whole places of every lane: from the registers, group after group.
+            float a1 = minus_inf(), b1 = minus_inf();
+            int g = 0, left = of.rows;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float v = by_group[i], less = fminf(v, a1);
+                a1 = fmaxf(v, a1);
+                b1 = fmaxf(less, b1);
+                if (--left > 0) continue;
+                const float top = warp_max(a1);
+                const bool is = lane == __ffs(__ballot_sync(ALL, a1 == top)) - 1;
+                const float next = p.group_sum == 2 ? warp_max(is ? b1 : a1) : minus_inf();
+                if (lane == g) {
+                    a = top;
+                    b = next;
+                }
+                ++g;
+                left = of.rows;
+                a1 = b1 = minus_inf();
+            }
+        } else {
+            largest_two<float>(p.groups, of.size, of.log_lanes, choices, a, b);
+            if ((lane & ((1 << of.log_lanes) - 1)) != 0) a = minus_inf();
+        }
+        unsigned keep = best_groups<float>(p, a, b, 2.0f * tol, near, last);
+        if (near != 0) {
+            // what of the groups' largest may be in their values
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float least = __shfl_sync(ALL, last, of.home[i]) - tol;
+                const int e = lane + 32 * i;
+                const bool in = e < p.E && (near >> of.home[i] & 1) && by_group[i] >= least && by_group[i] > minus_inf();
+                const unsigned all = __ballot_sync(ALL, in);
+                const int at = n + __popc(all & ((1u << lane) - 1));
+                if (in && at < 32) buffer[at] = {__int_as_float(of.home[i]), e};
+                n += __popc(all);
+            }
+            if (n <= 32) {
+                __syncwarp();
+                const Candidate c = buffer[max(min(lane, n - 1), 0)];
+                const double sum = softmax ? exact_sum(p, row, m) : 1.0;
+                keep = exact_groups(p, keep, near, lane < n, __float_as_int(c.key), exact_choice(p, row, c.expert, m, sum));
+                __syncwarp();
+            } else {
+                sure = false;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (!(keep >> of.bit[i] & 1)) key[i] = minus_inf();
+            if (!(keep >> of.home[i] & 1)) key[i] = minus_inf();
     }
 
     // The bound: the wanted number of lanes have a key that is not below it.
@@ -356,14 +483,14 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
         if (is) k = minus_inf();
     }
     if (biased) bound -= 1.01f * tol;
-    Candidate *buffer = reinterpret_cast<Candidate *>(scratch);
+    bound = fmaxf(bound, -0x1.fffffep127f);          // (not what is masked)
     int n = 0;
+    const unsigned below = (1u << lane) - 1;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const bool in = key[i] >= bound && key[i] > minus_inf();
-        const unsigned all = __ballot_sync(ALL, in);
-        const int at = n + __popc(all & ((1u << lane) - 1));
-        if (in && at < 32) buffer[at] = {key[i], lane + 32 * i};
+        const unsigned all = __ballot_sync(ALL, key[i] >= bound);
+        // (where they are more than 32 the buffer is not read)
+        if (key[i] >= bound) buffer[(n + __popc(all & below)) & 31] = {key[i], lane + 32 * i};
         n += __popc(all);
     }
     int mine = -1;
@@ -392,7 +519,20 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
             if (lane > 0 && lane < n && (lane <= p.top || before == last) && !(before - c.key > tol))
                 wrong = load_any(p.logits, row + expert, p.type) != load_any(p.logits, row + c.expert, p.type) ||
                         p.bias[expert] != p.bias[c.expert];
-            sure = sure && !__any_sync(ALL, wrong);
+            if (__any_sync(ALL, wrong) && sure) {
+                const double sum = softmax ? exact_sum(p, row, m) : 1.0;
+                const double exact = exact_choice(p, row, max(c.expert, 0), m, sum);
+                rank = 0;
+                for (int j = 0; j < n; ++j) {
+                    const double other = __shfl_sync(ALL, exact, j);
+                    const int of_other = __shfl_sync(ALL, c.expert, j);
+                    rank += other > exact || (other == exact && of_other < c.expert);
+                }
+                __syncwarp();
+                if (lane < n) buffer[rank] = c;
+                __syncwarp();
+                if (lane < min(n, p.top)) mine = buffer[lane].expert;
+            }
         }
     } else {
         int last = -1;
@@ -544,14 +684,16 @@ __global__ void __launch_bounds__(NT) route_kernel(const RouteArgs p, int scratc
     chunk_of(p.T, gridDim.x, blockIdx.x, from, to);
     Experts<V> of;
     of.most = 0.0f;
-    const int log_lanes = log_group_lanes(p.groups);
+    of.size = p.E / p.groups;
+    of.rows = of.size % 32 == 0 ? of.size / 32 : 0;
+    of.log_lanes = of.rows > 0 ? 0 : log_group_lanes(p.groups);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = lane + 32 * i;
         of.bias[i] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.0f;
         // (a bias of -inf masks its expert; behind the last, the logits do)
         if (of.bias[i] != minus_inf()) of.most = of.bias[i] == of.bias[i] ? fmaxf(of.most, fabsf(of.bias[i])) : -minus_inf();
-        of.bit[i] = (uint8_t)(min(e, p.E - 1) / (p.E / p.groups) << log_lanes);
+        of.home[i] = (uint8_t)(min(e, p.E - 1) / of.size << of.log_lanes);
     }
     of.most = warp_max(of.most);
     float l[V], next[V];
@@ -637,7 +779,7 @@ __global__ void __launch_bounds__(SORT_THREADS)
         if (part < parts)
             for (int e = tid - part * E; e < E; e += SORT_THREADS) {
                 int all = 0, lower = 0;
-#pragma unroll 16
+#pragma unroll 32
                 for (int c = part; c < (int)gridDim.x; c += parts) {
                     const int n = counts[(long long)c * E + e];
                     all += n;
