@@ -31,33 +31,95 @@ __device__ __forceinline__ float half_value(uint16_t b, bool bf16)
     return bf16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
 }
 
-// Eight columns in FP32, those from cnt on zero and not read.
-template <int TYPE>
-__device__ __forceinline__ void load8(const void *x, long long i, int cnt, float (&v)[8])
+// The larger, or smaller, of two; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b)
 {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Eight columns as they are stored; those from cnt on are zero and not read.
+template <int TYPE> struct Raw8 {
+    uint32_t u[TYPE == 2 ? 8 : 4];
+};
+
+template <int TYPE>
+__device__ __forceinline__ Raw8<TYPE> load8(const void *x, long long i, int cnt)
+{
+    Raw8<TYPE> r;
     if (TYPE == 2) {
         const float *src = static_cast<const float *>(x) + i;
         if (cnt == 8) {
-            const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            const uint4 a = reinterpret_cast<const uint4 *>(src)[0], b = reinterpret_cast<const uint4 *>(src)[1];
+            r.u[0] = a.x, r.u[1] = a.y, r.u[2] = a.z, r.u[3] = a.w;
+            r.u[TYPE == 2 ? 4 : 0] = b.x, r.u[TYPE == 2 ? 5 : 0] = b.y, r.u[TYPE == 2 ? 6 : 0] = b.z, r.u[TYPE == 2 ? 7 : 0] = b.w;
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = j < cnt ? src[j] : 0.0f;
+            for (int j = 0; j < 8; ++j) r.u[j % (TYPE == 2 ? 8 : 4)] = j < cnt ? __float_as_uint(src[j]) : 0u;
         }
-        return;
+        return r;
     }
     const uint16_t *src = static_cast<const uint16_t *>(x) + i;
-    uint32_t u[4] = {};
     if (cnt == 8) {
         const uint4 w = *reinterpret_cast<const uint4 *>(src);
-        u[0] = w.x, u[1] = w.y, u[2] = w.z, u[3] = w.w;
+        r.u[0] = w.x, r.u[1] = w.y, r.u[2] = w.z, r.u[3] = w.w;
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < cnt) u[j / 2] |= (uint32_t)src[j] << (16 * (j & 1));
-    }
+        for (int j = 0; j < 4; ++j) r.u[j] = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = half_value((uint16_t)(u[j / 2] >> (16 * (j & 1))), TYPE == 1);
+        for (int j = 0; j < 8; ++j)
+            if (j < cnt) r.u[j / 2] |= (uint32_t)src[j] << (16 * (j & 1));
+    }
+    return r;
+}
+
+// Columns 2 j and 2 j + 1 in FP32.
+template <int TYPE>
+__device__ __forceinline__ float2 pair(const Raw8<TYPE> &r, int j)
+{
+    if (TYPE == 2) return make_float2(__uint_as_float(r.u[(2 * j) % (TYPE == 2 ? 8 : 4)]), __uint_as_float(r.u[(2 * j + 1) % (TYPE == 2 ? 8 : 4)]));
+    if (TYPE == 1) return make_float2(__uint_as_float(r.u[j] << 16), __uint_as_float(r.u[j] & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&r.u[j]));
+}
+
+// The range of the eight columns and 0 (not ZERO: hi the largest magnitude), NaN where
+// there is one; of 16-bit columns two at a time.
+template <int TYPE, bool ZERO>
+__device__ __forceinline__ void range8(const Raw8<TYPE> &r, float &lo, float &hi)
+{
+    lo = hi = 0.0f;
+    if constexpr (TYPE == 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float v = __uint_as_float(r.u[j]);
+            if (ZERO) lo = min_nan(lo, v);
+            hi = max_nan(hi, ZERO ? v : fabsf(v));
+        }
+    } else {
+        using T2 = std::conditional_t<TYPE == 1, __nv_bfloat162, __half2>;
+        auto two = [](uint32_t u) { return *reinterpret_cast<const T2 *>(&u); };
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = ZERO ? r.u[j] : r.u[j] & 0x7fff7fffu;
+        const T2 top = __hmax2_nan(__hmax2_nan(two(u[0]), two(u[1])), __hmax2_nan(two(u[2]), two(u[3])));
+        Raw8<TYPE> f;
+        f.u[0] = *reinterpret_cast<const uint32_t *>(&top);
+        const float2 t = pair<TYPE>(f, 0);
+        hi = max_nan(hi, max_nan(t.x, t.y));
+        if (ZERO) {
+            const T2 low = __hmin2_nan(__hmin2_nan(two(u[0]), two(u[1])), __hmin2_nan(two(u[2]), two(u[3])));
+            f.u[0] = *reinterpret_cast<const uint32_t *>(&low);
+            const float2 b = pair<TYPE>(f, 0);
+            lo = min_nan(lo, min_nan(b.x, b.y));
+        }
+    }
 }
 
 template <int TYPE>
@@ -92,20 +154,6 @@ __device__ __forceinline__ void store8(void *x, long long i, int cnt, const floa
 // Bit of column j's code in its word of eight: columns 0, 2, 4, 6 in the lower
 // half, 1, 3, 5, 7 in the upper, so that one mask takes a pair of neighbours.
 __device__ __forceinline__ constexpr int code_bit(int j) { return 16 * (j & 1) + 4 * (j >> 1); }
-
-// The larger, or smaller, of two; NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float min_nan(float a, float b)
-{
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 
 // A scale in FP32 to its type: to nearest even; beyond the type's largest value
 // that value.
@@ -142,11 +190,11 @@ __global__ void __launch_bounds__(THREADS) w4_quantize_kernel(const W4Convert p,
     const int k0 = blockIdx.y * COLS, k = k0 + lane * 8;
     const int cnt = min(max(p.w.K - k, 0), 8), lanes = p.w.group / 8;   // lanes per group of columns
     const bool bf16 = p.stype == 1;
-    float v[ROWS][8];
+    Raw8<TYPE> raw[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const int n = n0 + warp * ROWS + r;
-        load8<TYPE>(p.X, ((long long)g * p.w.N + n) * p.ldx + k, n < p.w.N ? cnt : 0, v[r]);
+        raw[r] = load8<TYPE>(p.X, ((long long)g * p.w.N + n) * p.ldx + k, n < p.w.N ? cnt : 0);
     }
     // where this lane's codes end (those of columns that do not exist are 0)
     uint32_t keep = 0;
@@ -157,12 +205,7 @@ __global__ void __launch_bounds__(THREADS) w4_quantize_kernel(const W4Convert p,
     float lo[ROWS], hi[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        lo[r] = hi[r] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (ZERO) lo[r] = min_nan(lo[r], v[r][j]);
-            hi[r] = max_nan(hi[r], ZERO ? v[r][j] : fabsf(v[r][j]));
-        }
+        range8<TYPE, ZERO>(raw[r], lo[r], hi[r]);
         for (int d = 1; d < lanes; d <<= 1) {
             hi[r] = max_nan(hi[r], __shfl_xor_sync(ALL, hi[r], d));
             if (ZERO) lo[r] = min_nan(lo[r], __shfl_xor_sync(ALL, lo[r], d));
@@ -201,19 +244,30 @@ __global__ void __launch_bounds__(THREADS) w4_quantize_kernel(const W4Convert p,
         const bool bad = bits == 0x7fffu;
         const float s = half_value((uint16_t)bits, bf16);
         const bool tiny = s < TINY;
-        const float scale = tiny ? s * LARGER : s;
-        if (__any_sync(ALL, tiny)) {                 // seldom: all of these rows' numbers are made larger
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[r][j] = tiny ? v[r][j] * LARGER : v[r][j];
-        }
         // 2^23 + 2^22 takes the units' place: the sum is rounded to a whole number,
         // ties to even, and its lowest bits are that number's.
         constexpr float UNITS = 12582912.0f;
         uint32_t word = 0;
+        // Without a zero point a quotient is at most 7 and a scale's rounding, which needs no
+        // bound, unless the scale's type has no digits left or the scale was too large.
+        const bool plain = !ZERO && s >= (bf16 ? TINY : 0x1p-14f) && s < (bf16 ? 0x1p126f : 65504.0f);
+        if (__all_sync(ALL, plain || bad)) {
+            const float2 inv = make_float2(inverse, inverse), less = make_float2(-s, -s), units = make_float2(UNITS, UNITS);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float q = fminf(fmaxf(quotient(v[r][j], scale, inverse), -z), 15.0f - z) + UNITS;
-            word += __float_as_uint(q) << code_bit(j);
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = pair<TYPE>(raw[r], j), q = __fmul2_rn(x, inv);
+                const float2 u = __fadd2_rn(__ffma2_rn(__ffma2_rn(q, less, x), inv, q), units);
+                word += __float_as_uint(u.x) << code_bit(2 * j);
+                word += __float_as_uint(u.y) << code_bit(2 * j + 1);
+            }
+        } else {
+            const float larger = tiny ? LARGER : 1.0f, scale = s * larger;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 x = pair<TYPE>(raw[r], j / 2);
+                const float q = quotient((j & 1 ? x.y : x.x) * larger, scale, inverse);
+                word += __float_as_uint(fminf(fmaxf(q, -z), 15.0f - z) + UNITS) << code_bit(j);
+            }
         }
         // less the units, plus the zero point, in every code's place
         uint32_t places = 0;
