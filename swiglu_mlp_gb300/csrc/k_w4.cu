@@ -16,13 +16,14 @@
 // are scaled in FP32 as a whole, so that no product with a scale is ever rounded to
 // 16 bits.
 //
-// A CTA has one chunk of at most eight rows of A; its four warps are teams of
+// w4_kernel: a CTA has one chunk of at most eight rows of A; its four warps are teams of
 // `team` along K, and each team has 64 rows of W.  A team's warps take steps of 256
 // columns in turn.  Each warp has a ring of its own that TMA fills: a lane asks
 // for a step's codes (64 rows of 128 bytes), scales, zero points and columns of A
 // with an instruction or four each, which leaves the issue slots to the decoding;
 // cp.async by all lanes, with its addresses and edges, took as many instructions
-// again.  A team's sums are added at the end, in order.
+// again.  A team's sums are added at the end, in order.  w4_many_kernel, for more
+// rows or where there are too few rows of W, stands below it.
 #include <algorithm>
 #include <type_traits>
 
@@ -114,16 +115,156 @@ __host__ __device__ constexpr int shared_bytes(int per, bool zero, int tokens)
 }
 static_assert(WARPS * STAGES * 8 + 8 <= 256, "barriers and the abort flag");
 
-// PER: a scale's columns in units of 32.  `tokens`: rows of A of a chunk, 1, 2, 4 or
-// 8.  `team`: a power of two.
-//
 // Of a row's 128 bytes TMA puts 16-byte piece c to place c ^ (row % 8), the row being that
 // of shared memory.  Lane (quad, t) computes with two neighbouring rows of each 16, a
 // Gate and its Up, as rows quad and quad + 8 of the instruction; which, is chosen so
 // that reads of 4, 8 or 16 bytes a lane meet no bank twice: rows 2 pi and 2 pi + 1, pi
 // the quad with its lower bits swapped, the odd one first in quads 4 to 7.  Word j of
 // the eight that lane t has of a row is columns 32 PER (j / PER) + 8 PER t + 8 (j % PER)
-// .. + 7: the words of a place in all four lanes of a row share a scale.
+// .. + 7 (PER: a scale's columns in units of 32): the words of a place in all four
+// lanes of a row share a scale.
+struct Lane {
+    int pi, odd, t;
+    int swap0, swap1, row_at0, row_at1;              // of the first and second row
+    uint32_t units, order;                           // (order: of the rows' scales)
+};
+
+template <bool BF16>
+__device__ __forceinline__ Lane lane_of()
+{
+    Lane l;
+    const int lane = threadIdx.x & 31, quad = lane >> 2;
+    l.t = lane & 3;
+    l.pi = (quad & 4) | (quad & 1) << 1 | (quad >> 1 & 1);
+    l.odd = quad >> 2;
+    l.swap0 = (2 * l.pi + l.odd) & 7;
+    l.swap1 = (2 * l.pi + 1 - l.odd) & 7;
+    l.row_at0 = (2 * l.pi + l.odd) * (STEP / 2);
+    l.row_at1 = (2 * l.pi + 1 - l.odd) * (STEP / 2);
+    asm volatile("mov.b32 %0, %1;" : "=r"(l.units) : "n"(UNITS<BF16>));
+    l.order = l.odd ? 0x1032u : 0x3210u;
+    return l;
+}
+
+// acc += the products of a step: codes and params as TMA left them; rows of A in lines
+// of 128 bytes (64 columns) of shared memory, `lines` for each 64 columns, this lane's of
+// NT rows of A 8 apart from x_line on; MR pieces of 16 rows of W, from `piece` of the
+// slot's on.  whole: the second half has columns too.
+template <bool BF16, int PER, bool ZERO, int MR, int NT>
+__device__ __forceinline__ void multiply(const Lane &l, const unsigned char *shared, const unsigned char *codes,
+                                         const unsigned char *params, int x_line, int lines, bool whole,
+                                         int piece, float (&acc)[MR][NT][4])
+{
+    const uint32_t *scale = reinterpret_cast<const uint32_t *>(params) + piece * 8 + l.pi;
+    const uint16_t *zero = reinterpret_cast<const uint16_t *>(params + scales_bytes(PER)) + piece * 8 + l.pi;
+    const uint32_t scale0 = l.odd ? 0x3244u : 0x1044u, scale1 = l.odd ? 0x1044u : 0x3244u;
+    const int t = l.t;
+    float part[MR][NT][4];
+    uint32_t z0[MR], z1[MR];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        if (half == 1 && !whole) break;
+        uint32_t w[2 * MR][4];                       // both rows of each 16
+#pragma unroll
+        for (int r = 0; r < 2 * MR; ++r) {
+            const unsigned char *at = codes + (r % 2 ? l.row_at1 : l.row_at0) + (piece + r / 2) * 16 * (STEP / 2);
+            const int swap = r % 2 ? l.swap1 : l.swap0;
+            if (PER == 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(at + ((4 * half + t) ^ swap) * 16);
+                w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+            } else if (PER == 2) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(at + ((4 * half + 2 * h + (t >> 1)) ^ swap) * 16 + (t & 1) * 8);
+                    w[r][2 * h] = v.x, w[r][2 * h + 1] = v.y;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[r][j] = *reinterpret_cast<const uint32_t *>(at + ((4 * half + j) ^ swap) * 16 + t * 4);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // columns in units of 8: block of 64, piece of it
+            const int c = (4 * half + j) / PER * (4 * PER) + PER * t + j % PER;
+            uint4 x[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int line = (c >> 3) * lines + x_line + 8 * n;
+                x[n] = *reinterpret_cast<const uint4 *>(shared + line * 128 + ((c ^ line) & 7) * 16);
+            }
+            const int b = (4 * half + j) / PER;      // the scale's place among the step's
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                if (j % PER == 0) {
+                    z0[m] = z1[m] = UNITS<BF16> + 0x00080008u;
+                    if (ZERO) {
+                        const uint32_t z = __byte_perm(zero[(b * MT + m) * 8], 0, l.odd ? 0x4401 : 0x4410);
+                        z0[m] = UNITS<BF16> + (z & 15u) * 0x00010001u;
+                        z1[m] = UNITS<BF16> + (z >> 8 & 15u) * 0x00010001u;
+                    }
+                }
+                const uint32_t w0 = w[2 * m][j], w1 = w[2 * m + 1][j];
+                uint32_t f[8];                       // the fragments of two instructions
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f[2 * i] = decode<BF16>(w0, i, l.units, z0[m]);
+                    f[2 * i + 1] = decode<BF16>(w1, i, l.units, z1[m]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (j % PER == 0)
+                        mma16816<BF16, true>(part[m][n], f[0], f[1], f[2], f[3], x[n].x, x[n].y);
+                    else
+                        mma16816<BF16, false>(part[m][n], f[0], f[1], f[2], f[3], x[n].x, x[n].y);
+                    mma16816<BF16, false>(part[m][n], f[4], f[5], f[6], f[7], x[n].z, x[n].w);
+                }
+                if (j % PER == PER - 1) {
+                    float2 s;
+                    if (BF16)                        // (a bfloat16 is the upper half of its FP32)
+                        s = make_float2(__uint_as_float(__byte_perm(scale[(b * MT + m) * 8], 0, scale0)),
+                                        __uint_as_float(__byte_perm(scale[(b * MT + m) * 8], 0, scale1)));
+                    else
+                        s = scale_pair<BF16>(__byte_perm(scale[(b * MT + m) * 8], 0, l.order));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        acc[m][n][0] = fmaf(s.x, part[m][n][0], acc[m][n][0]);
+                        acc[m][n][1] = fmaf(s.x, part[m][n][1], acc[m][n][1]);
+                        acc[m][n][2] = fmaf(s.y, part[m][n][2], acc[m][n][2]);
+                        acc[m][n][3] = fmaf(s.y, part[m][n][3], acc[m][n][3]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Columns n, n + 1 of a row of A.
+__device__ __forceinline__ void store_pair(const W4Args &p, int row, int n, float x, float y)
+{
+    if (n >= p.w.N) return;
+    const long long o = row * p.ldc;
+    x *= p.alpha;
+    y *= p.alpha;
+    if (p.swiglu) {
+        store_out(p.C, o + n / 2, silu_f32(x) * y, p.out_kind);
+        return;
+    }
+    if (p.beta != 0.0f) x += p.beta * load_out(p.C, o + n, p.out_kind);
+    store_out(p.C, o + n, x, p.out_kind);
+    if (n + 1 < p.w.N) {
+        if (p.beta != 0.0f) y += p.beta * load_out(p.C, o + n + 1, p.out_kind);
+        store_out(p.C, o + n + 1, y, p.out_kind);
+    }
+}
+
+// Rows 2 pi and 2 pi + 1 of what a lane has of 16 rows of W, for row h of A.
+__device__ __forceinline__ float2 rows_of(const Lane &l, const float (&c)[4], int h)
+{
+    return l.odd ? make_float2(c[2 + h], c[h]) : make_float2(c[h], c[2 + h]);
+}
+
+// `tokens`: rows of A of a chunk, 1, 2, 4 or 8.  `team`: a power of two.
 template <bool BF16, int PER, bool ZERO>
 __global__ void __launch_bounds__(32 * WARPS, 3)
     w4_kernel(const __grid_constant__ W4Maps maps, const W4Args p, int tiles, int tokens, int team, int *err)
@@ -131,7 +272,7 @@ __global__ void __launch_bounds__(32 * WARPS, 3)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) unsigned char shared[];
     constexpr int BLOCKS = STEP / (32 * PER), PARAMS = params_pitch(PER, ZERO);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wk = warp & (team - 1), quad = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wk = warp & (team - 1), quad = lane >> 2;
     const int of_a = a_bytes(tokens);
     unsigned char *const codes = shared + warp * STAGES * CODES;
     unsigned char *const a = shared + WARPS * STAGES * CODES + warp * STAGES * of_a;
@@ -168,16 +309,10 @@ __global__ void __launch_bounds__(32 * WARPS, 3)
     for (int i = 0; i < STAGES; ++i)
         if (wk + i * team < steps) load(wk + i * team, i);
 
-    const int pi = (quad & 4) | (quad & 1) << 1 | (quad >> 1 & 1), odd = quad >> 2;
-    uint32_t units;
-    asm volatile("mov.b32 %0, %1;" : "=r"(units) : "n"(UNITS<BF16>));
-    const uint32_t order = odd ? 0x1032u : 0x3210u;  // of the rows' scales
-    const int swap0 = (2 * pi + odd) & 7, swap1 = (2 * pi + 1 - odd) & 7;
-    const uint32_t scale0 = odd ? 0x3244u : 0x1044u, scale1 = odd ? 0x1044u : 0x3244u;
-    const int row_at0 = (2 * pi + odd) * (STEP / 2), row_at1 = (2 * pi + 1 - odd) * (STEP / 2);
+    const Lane l = lane_of<BF16>();
     // (lanes of rows of A that do not exist compute with another, for nothing)
-    const int token = min(quad, tokens - 1);
-    float acc[MT][4] = {};
+    const int x_line = (int)(a - shared) / 128 + min(quad, tokens - 1);
+    float acc[MT][1][4] = {};
     bool stopped = false;
     int step = wk, slot = 0;
     uint32_t parity = 0;
@@ -186,76 +321,8 @@ __global__ void __launch_bounds__(32 * WARPS, 3)
             stopped = true;
             break;
         }
-        const unsigned char *row = codes + slot * CODES, *par = params + slot * PARAMS;
-        const int x_line = ((int)(a - shared) + slot * of_a) / 128 + token;      // in shared memory
-        const uint32_t *scale = reinterpret_cast<const uint32_t *>(par) + pi;
-        const uint16_t *zero = reinterpret_cast<const uint16_t *>(par + scales_bytes(PER)) + pi;
-        float part[MT][4];
-        uint32_t z0[MT], z1[MT];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (half == 1 && step * STEP + STEP / 2 >= p.w.K) break;
-            uint32_t w[2 * MT][4];                   // both rows of each 16
-#pragma unroll
-            for (int r = 0; r < 2 * MT; ++r) {
-                const unsigned char *at = row + (r % 2 ? row_at1 : row_at0) + r / 2 * 16 * (STEP / 2);
-                const int swap = r % 2 ? swap1 : swap0;
-                if (PER == 4) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(at + ((4 * half + t) ^ swap) * 16);
-                    w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
-                } else if (PER == 2) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(at + ((4 * half + 2 * h + (t >> 1)) ^ swap) * 16 + (t & 1) * 8);
-                        w[r][2 * h] = v.x, w[r][2 * h + 1] = v.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) w[r][j] = *reinterpret_cast<const uint32_t *>(at + ((4 * half + j) ^ swap) * 16 + t * 4);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // columns in units of 8: block of 64, piece of it
-                const int c = (4 * half + j) / PER * (4 * PER) + PER * t + j % PER, line = (c >> 3) * tokens + x_line;
-                const uint4 x = *reinterpret_cast<const uint4 *>(shared + line * 128 + ((c ^ line) & 7) * 16);
-                const int b = (4 * half + j) / PER;  // the scale's place among the step's
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if (j % PER == 0) {
-                        z0[m] = z1[m] = UNITS<BF16> + 0x00080008u;
-                        if (ZERO) {
-                            const uint32_t z = __byte_perm(zero[(b * MT + m) * 8], 0, odd ? 0x4401 : 0x4410);
-                            z0[m] = UNITS<BF16> + (z & 15u) * 0x00010001u;
-                            z1[m] = UNITS<BF16> + (z >> 8 & 15u) * 0x00010001u;
-                        }
-                    }
-                    const uint32_t w0 = w[2 * m][j], w1 = w[2 * m + 1][j];
-                    auto two = [&](int h, uint32_t b0, uint32_t b1, auto f) {
-                        mma16816<BF16, decltype(f)::value>(
-                            part[m], decode<BF16>(w0, h, units, z0[m]), decode<BF16>(w1, h, units, z1[m]),
-                            decode<BF16>(w0, h + 1, units, z0[m]), decode<BF16>(w1, h + 1, units, z1[m]), b0, b1);
-                    };
-                    if (j % PER == 0)
-                        two(0, x.x, x.y, std::true_type{});
-                    else
-                        two(0, x.x, x.y, std::false_type{});
-                    two(2, x.z, x.w, std::false_type{});
-                    if (j % PER == PER - 1) {
-                        float2 s;
-                        if (BF16)                    // (a bfloat16 is the upper half of its FP32)
-                            s = make_float2(__uint_as_float(__byte_perm(scale[(b * MT + m) * 8], 0, scale0)),
-                                            __uint_as_float(__byte_perm(scale[(b * MT + m) * 8], 0, scale1)));
-                        else
-                            s = scale_pair<BF16>(__byte_perm(scale[(b * MT + m) * 8], 0, order));
-                        acc[m][0] = fmaf(s.x, part[m][0], acc[m][0]);
-                        acc[m][1] = fmaf(s.x, part[m][1], acc[m][1]);
-                        acc[m][2] = fmaf(s.y, part[m][2], acc[m][2]);
-                        acc[m][3] = fmaf(s.y, part[m][3], acc[m][3]);
-                    }
-                }
-            }
-        }
+        multiply<BF16, PER, ZERO, MT, 1>(l, shared, codes + slot * CODES, params + slot * PARAMS, x_line + slot * of_a / 128, tokens,
+                                     step * STEP + STEP / 2 < p.w.K, 0, acc);
         __syncwarp();
         if (step + STAGES * team < steps) load(step + STAGES * team, slot);
         slot = slot + 1 == STAGES ? 0 : slot + 1;
@@ -267,33 +334,15 @@ __global__ void __launch_bounds__(32 * WARPS, 3)
             slot = slot + 1 == STAGES ? 0 : slot + 1;
             parity ^= slot == 0;
         }
-
-    auto store = [&](int row, int n, float x, float y) {             // columns n, n + 1 of a row of A
-        if (n >= p.w.N) return;
-        const long long o = row * p.ldc;
-        x *= p.alpha;
-        y *= p.alpha;
-        if (p.swiglu) {
-            store_out(p.C, o + n / 2, silu_f32(x) * y, p.out_kind);
-            return;
-        }
-        if (p.beta != 0.0f) x += p.beta * load_out(p.C, o + n, p.out_kind);
-        store_out(p.C, o + n, x, p.out_kind);
-        if (n + 1 < p.w.N) {
-            if (p.beta != 0.0f) y += p.beta * load_out(p.C, o + n + 1, p.out_kind);
-            store_out(p.C, o + n + 1, y, p.out_kind);
-        }
-    };
-    // Rows 2 pi and 2 pi + 1 for rows 2 t + h of A.
-    auto first = [&](int m, int h) { return odd ? acc[m][2 + h] : acc[m][h]; };
-    auto second = [&](int m, int h) { return odd ? acc[m][h] : acc[m][2 + h]; };
     if (team == 1) {
         if (stopped) return;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (2 * t + h < rows) store(row0 + 2 * t + h, n0 + m * 16 + 2 * pi, first(m, h), second(m, h));
+            for (int h = 0; h < 2; ++h) {
+                const float2 v = rows_of(l, acc[m][0], h);
+                if (2 * l.t + h < rows) store_pair(p, row0 + 2 * l.t + h, n0 + m * 16 + 2 * l.pi, v.x, v.y);
+            }
         return;
     }
     // [warp][row of A][row of W]
@@ -304,9 +353,8 @@ __global__ void __launch_bounds__(32 * WARPS, 3)
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (2 * t + h < rows)
-                *reinterpret_cast<float2 *>(sums + (warp * tokens + 2 * t + h) * SUMS + m * 16 + 2 * pi) =
-                    make_float2(first(m, h), second(m, h));
+            if (2 * l.t + h < rows)
+                *reinterpret_cast<float2 *>(sums + (warp * tokens + 2 * l.t + h) * SUMS + m * 16 + 2 * l.pi) = rows_of(l, acc[m][0], h);
     __syncthreads();
     const float *of_team = sums + (warp & ~(team - 1)) * tokens * SUMS;
     for (int o = wk * 32 + lane; o < rows * (ROWS / 2); o += team * 32) {
@@ -317,8 +365,139 @@ __global__ void __launch_bounds__(32 * WARPS, 3)
             x += v.x;
             y += v.y;
         }
-        store(row0 + row, n0 + 2 * pair, x, y);
+        store_pair(p, row0 + row, n0 + 2 * pair, x, y);
     }
+}
+
+// ------------------------------------------------------------ more rows of A
+
+// Chunks of 8, 16 or 32 rows of A, NT = 1, 2 or 4 tiles of 8.  A code decoded is used NT
+// times, and from NT = 2 on the mma.sync instructions bound it: one takes 17 cycles of
+// its quarter of an SM, as measured (32 rows, 14336 x 4096: 13.4 us on all SMs).  Rows
+// of A are as much to read as codes then, so four warps of 32 rows of W share them: a
+// CTA has 128 rows of W and a range of the steps, a fifth warp feeds its ring, two CTAs
+// fill an SM, and the CTAs of a cluster that have a tile's ranges add their sums
+// through shared memory, in order.  (One CTA of 256 rows for each SM: 41 us, since only
+// 15 clusters of eight of that size are resident, and 35.9 with clusters of four; this
+// 20.4; chunks of eight rows of the other kernel 31.4.)
+constexpr int MANY_BOXES = 2, MANY_ROWS = MANY_BOXES * ROWS;
+constexpr int MANY_MT = MANY_ROWS / 16 / WARPS;
+constexpr int MANY_THREADS = 32 * (WARPS + 1);
+constexpr int MANY_STAGES = 3;
+constexpr int MANY_SUMS = MANY_ROWS + 2;             // floats of a row of A's sums, padded
+constexpr int MOST_RANGES = 8;
+
+__host__ __device__ constexpr int many_stage(int per, bool zero, int nt)
+{
+    return MANY_BOXES * (CODES + params_pitch(per, zero)) + a_bytes(8 * nt);
+}
+__host__ __device__ constexpr int many_shared(int per, bool zero, int nt) { return MANY_STAGES * many_stage(per, zero, nt) + 256; }
+static_assert(2 * (many_shared(1, true, 4) + 1024) <= 233472, "two CTAs on an SM");
+static_assert(MANY_SUMS * 32 * 4 <= MANY_STAGES * MANY_BOXES * CODES, "the sums take the ring's place");
+
+__device__ __forceinline__ float2 load_cluster(uint32_t at)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+template <bool BF16, int PER, bool ZERO, int NT>
+__global__ void __launch_bounds__(MANY_THREADS, 2)
+    w4_many_kernel(const __grid_constant__ W4Maps maps, const W4Args p, int tiles, int ranges, int *err)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ __align__(1024) unsigned char shared[];
+    constexpr int BLOCKS = STEP / (32 * PER), PARAMS = params_pitch(PER, ZERO), TOKENS_MANY = 8 * NT;
+    constexpr int A = MANY_STAGES * MANY_BOXES * CODES, P = A + MANY_STAGES * a_bytes(TOKENS_MANY), B = P + MANY_STAGES * MANY_BOXES * PARAMS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t full = smem_u32(shared) + B, empty = full + 8 * MANY_STAGES;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(shared + B + 16 * MANY_STAGES);
+    // (a cluster's CTAs, the ranges of a tile, follow one another)
+    const int range = blockIdx.x % ranges, unit = blockIdx.x / ranges, chunk = unit / tiles, tile = unit - chunk * tiles;
+    const int n0 = tile * MANY_ROWS, boxes = min(MANY_BOXES, (p.w.N - n0 + ROWS - 1) / ROWS), used = boxes * (WARPS / MANY_BOXES);
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < MANY_STAGES; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, used);
+        }
+        fence_barrier_init();
+        *abort_flag = 0;
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int g, row0, rows;
+    if (!find_chunk(p.groups, TOKENS_MANY, chunk, err, g, row0, rows)) return;   // (the whole cluster)
+
+    const int steps = (p.w.K + STEP - 1) / STEP, first = (int)((long long)steps * range / ranges);
+    const int count = (int)((long long)steps * (range + 1) / ranges) - first;
+    float acc[MANY_MT][NT][4] = {};
+    const Lane l = lane_of<BF16>();
+    if (warp == WARPS) {
+        if (lane == 0) {
+            int i = 0;
+            for (; i < count; ++i) {
+                const int slot = i % MANY_STAGES, step = first + i;
+                const uint32_t bar = full + 8 * slot;
+                if (i >= MANY_STAGES && !wait_bounded(empty + 8 * slot, (uint32_t)((i / MANY_STAGES) - 1) & 1u, abort_flag, err)) break;
+                mbar_arrive_expect_tx(bar, boxes * (CODES + params_bytes(PER, ZERO)) + a_bytes(TOKENS_MANY));
+                for (int w = 0; w < boxes; ++w) {
+                    const uint32_t to = smem_u32(shared) + P + (slot * MANY_BOXES + w) * PARAMS;
+                    tma_load_3d_cta(smem_u32(shared) + (slot * MANY_BOXES + w) * CODES, &maps.q, bar, step * (STEP / 2), n0 + w * ROWS, g);
+                    tma_load_3d_cta(to, &maps.s, bar, n0 + w * ROWS, step * BLOCKS, g);
+                    if (ZERO) tma_load_3d_cta(to + scales_bytes(PER), &maps.z, bar, n0 + w * ROWS, step * BLOCKS, g);
+                }
+                for (int c = 0; c < 4; ++c)
+                    tma_load_2d(smem_u32(shared) + A + slot * a_bytes(TOKENS_MANY) + c * TOKENS_MANY * 128, &maps.a, bar, step * STEP + c * 64, row0);
+            }
+            // (all that is on its way lands before the sums take its place, after a wait that ran out too)
+            for (int j = max(i - MANY_STAGES, 0); j < i; ++j)
+                wait_bounded(full + 8 * (j % MANY_STAGES), (uint32_t)(j / MANY_STAGES) & 1u, abort_flag, err, false, DRAIN_LIMIT_NS);
+        }
+    } else if (warp < used) {
+        const int box = warp / (WARPS / MANY_BOXES);
+        for (int i = 0; i < count; ++i) {
+            const int slot = i % MANY_STAGES;
+            if (!__all_sync(0xffffffffu, wait_bounded(full + 8 * slot, (uint32_t)(i / MANY_STAGES) & 1u, abort_flag, err))) break;
+            multiply<BF16, PER, ZERO, MANY_MT, NT>(l, shared, shared + (slot * MANY_BOXES + box) * CODES, shared + P + (slot * MANY_BOXES + box) * PARAMS,
+                                          (A + slot * a_bytes(TOKENS_MANY)) / 128 + (lane >> 2), TOKENS_MANY,
+                                          (first + i) * STEP + STEP / 2 < p.w.K, warp * MANY_MT % MT, acc);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * slot);
+        }
+    }
+    // Sums: [row of A][row of W], in the ring's place.
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(shared);
+    if (warp < used) {
+#pragma unroll
+        for (int m = 0; m < MANY_MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<float2 *>(sums + (8 * n + 2 * l.t + h) * MANY_SUMS + (warp * MANY_MT + m) * 16 + 2 * l.pi) =
+                        rows_of(l, acc[m][n], h);
+    }
+    if (ranges > 1) cluster_sync_all();
+    else __syncthreads();
+    // A share of the pairs of rows of W for each CTA of the cluster.
+    const int pairs = MANY_ROWS / 2 / ranges, from = range * pairs;
+    if (!*abort_flag)
+        for (int o = threadIdx.x; o < rows * pairs; o += MANY_THREADS) {
+            const int row = o / pairs, pair = from + o - row * pairs;
+            if (n0 + 2 * pair >= p.w.N) continue;
+            const uint32_t at = smem_u32(sums + row * MANY_SUMS + 2 * pair);
+            float x = 0.0f, y = 0.0f;
+            for (int r = 0; r < ranges; ++r) {
+                const float2 v = ranges > 1 ? load_cluster(mapa_shared(at, r)) : *reinterpret_cast<const float2 *>(sums + row * MANY_SUMS + 2 * pair);
+                x += v.x;
+                y += v.y;
+            }
+            store_pair(p, row0 + row, n0 + 2 * pair, x, y);
+        }
+    if (ranges > 1) cluster_sync_all();              // no CTA leaves while its sums are read
 }
 
 // An upper bound of the chunks over all groups, and with offsets one more, whose
@@ -329,13 +508,35 @@ long long chunks_of(const Groups &g, int tokens)
     return g.offsets == nullptr ? (g.M + tokens - 1) / tokens : g.M / tokens + std::min(g.G, g.M) + 1;
 }
 
-// Rows of A per chunk: of groups four times their mean, since another chunk reads and
-// decodes the weights again (64 rows of 64 experts: 25.6 us with chunks of 1, 21.2
-// with 2, 19.2 with 4, 19.8 with 8).
-int chunk_rows(const Groups &g)
+struct Shape {
+    int tokens;                                      // rows of A of a chunk
+    bool many;                                       // of w4_many_kernel
+};
+
+// (times in us, bfloat16, group 128 with zero points)
+Shape shape_of(const W4Args &p, int sms)
 {
+    const Groups &g = p.groups;
+    const int steps = (p.w.K + STEP - 1) / STEP;
+    const long long items = (p.w.N + ROWS - 1ll) / ROWS;
+    // Groups: chunks of four times their mean, since another chunk reads and decodes the
+    // weights again (64 rows of 64 experts: 25.6 with chunks of 1, 21.2 with 2, 19.2 with
+    // 4, 19.8 with 8).  More than eight rows from a mean of 16 on, where the fuller
+    // instructions outweigh the emptier chunks (16 experts of 4096 x 1024: means of 8
+    // 24.1 and 19.3, 16 26.7 and 28.8, 32 38.7 and 46.3).
+    if (g.offsets != nullptr && g.M >= 16ll * g.G) return {32, true};
     const int want = g.offsets == nullptr ? g.M : (int)std::min<long long>(g.M, (4ll * g.M + g.G - 1) / g.G);
-    return want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : TOKENS;
+    // More than eight rows (4096 x 14336, 32 rows: 19.6 and 30.5; 4096 x 4096, 16 rows: 8.3
+    // and 9.7), unless there is too little to do for a cluster's barriers (1024 x 2048, 32
+    // rows: 6.0 and 4.9; 8192 x 1024, 16 rows: 6.4 and 4.9, 32 rows: 7.9 and 8.0).
+    if (g.offsets == nullptr && want > TOKENS && (steps > 8 || (want + TOKENS - 1) / TOKENS * items * steps > 12 * sms))
+        return {want <= 16 ? 16 : 32, true};
+    // Up to eight, where teams of four do not fill the GPU and a warp would take more
+    // than four steps in turn: a cluster has up to 32 warps for a tile (one row, 4096 x
+    // 14336: 14.9 and 19.6; 2048 x 8192: 7.8 and 11.8; but 14336 x 4096 13.4 and 11.3, 1024
+    // x 2048 4.5 and 4.6).
+    if (steps > 4 * WARPS && (g.offsets == nullptr ? 1 : std::min(g.G, g.M)) * items < sms) return {TOKENS, true};
+    return {want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : TOKENS, false};
 }
 
 template <bool BF16, int PER, bool ZERO>
@@ -371,18 +572,60 @@ cudaError_t launch(const W4Args &p, const W4Maps &maps, int tokens, int sms, int
     return cudaLaunchKernelEx(&cfg, kernel, maps, p, tiles, tokens, team, err);
 }
 
-template <bool BF16, int PER>
-cudaError_t launch_zero(const W4Args &p, const W4Maps &maps, int tokens, int sms, int *err, cudaStream_t s)
+template <bool BF16, int PER, bool ZERO, int NT>
+cudaError_t launch_many(const W4Args &p, const W4Maps &maps, int sms, int *err, cudaStream_t s)
 {
-    return p.w.Z != nullptr ? launch<BF16, PER, true>(p, maps, tokens, sms, err, s) : launch<BF16, PER, false>(p, maps, tokens, sms, err, s);
+    // As many ranges of the steps as the SMs have places for CTAs, two each.
+    const int steps = (p.w.K + STEP - 1) / STEP, tiles = (p.w.N + MANY_ROWS - 1) / MANY_ROWS;
+    const long long chunks = chunks_of(p.groups, 8 * NT);
+    const long long units = (p.groups.offsets ? std::min<long long>(p.groups.M / (8 * NT) + std::min(p.groups.G, p.groups.M), chunks) : chunks) * tiles;
+    int ranges = 1;
+    while (ranges < MOST_RANGES && 2 * ranges <= steps && ranges * units <= sms) ranges *= 2;
+    auto kernel = w4_many_kernel<BF16, PER, ZERO, NT>;
+    static DeviceOnce once;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (once.needed(dev)) {
+        if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, many_shared(PER, ZERO, NT))) return e;
+        once.mark(dev);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(chunks * tiles * ranges));
+    cfg.blockDim = dim3(MANY_THREADS);
+    cfg.dynamicSmemBytes = many_shared(PER, ZERO, NT);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ranges;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p, tiles, ranges, err);
+}
+
+template <bool BF16, int PER, bool ZERO>
+cudaError_t launch_any(const W4Args &p, const W4Maps &maps, Shape shape, int sms, int *err, cudaStream_t s)
+{
+    return !shape.many               ? launch<BF16, PER, ZERO>(p, maps, shape.tokens, sms, err, s)
+           : shape.tokens == TOKENS ? launch_many<BF16, PER, ZERO, 1>(p, maps, sms, err, s)
+           : shape.tokens == 16     ? launch_many<BF16, PER, ZERO, 2>(p, maps, sms, err, s)
+                                    : launch_many<BF16, PER, ZERO, 4>(p, maps, sms, err, s);
+}
+
+template <bool BF16, int PER>
+cudaError_t launch_zero(const W4Args &p, const W4Maps &maps, Shape shape, int sms, int *err, cudaStream_t s)
+{
+    return p.w.Z != nullptr ? launch_any<BF16, PER, true>(p, maps, shape, sms, err, s) : launch_any<BF16, PER, false>(p, maps, shape, sms, err, s);
 }
 
 template <bool BF16>
-cudaError_t launch_group(const W4Args &p, const W4Maps &maps, int tokens, int sms, int *err, cudaStream_t s)
+cudaError_t launch_group(const W4Args &p, const W4Maps &maps, Shape shape, int sms, int *err, cudaStream_t s)
 {
-    return p.w.group == 32   ? launch_zero<BF16, 1>(p, maps, tokens, sms, err, s)
-           : p.w.group == 64 ? launch_zero<BF16, 2>(p, maps, tokens, sms, err, s)
-                             : launch_zero<BF16, 4>(p, maps, tokens, sms, err, s);
+    return p.w.group == 32   ? launch_zero<BF16, 1>(p, maps, shape, sms, err, s)
+           : p.w.group == 64 ? launch_zero<BF16, 2>(p, maps, shape, sms, err, s)
+                             : launch_zero<BF16, 4>(p, maps, shape, sms, err, s);
 }
 
 }  // namespace
@@ -392,7 +635,7 @@ bool w4_fits(const W4Args &p) { return chunks_of(p.groups, 1) * ((p.w.N + 31ll) 
 cudaError_t launch_w4(const W4Args &p, int sms, int *err, cudaStream_t s, bool &mapped)
 {
     W4Maps maps{};
-    const int tokens = chunk_rows(p.groups);
+    const Shape shape = shape_of(p, sms);
     mapped = true;
     if (p.w.K > 0) {
         const uint64_t N = p.w.N, G = p.groups.G, blocks = p.w.blocks(), row = p.w.row_bytes(), lds = p.w.lds;
@@ -401,14 +644,14 @@ cudaError_t launch_w4(const W4Args &p, int sms, int *err, cudaStream_t s, bool &
         const uint32_t qb[] = {STEP / 2, ROWS, 1}, sb[] = {ROWS, per_step, 1};
         const uint64_t sd[] = {lds, blocks, G}, ss[] = {lds * 2, G > 1 ? lds * 2 * blocks : lds * 2}, zs[] = {lds, G > 1 ? lds * blocks : lds};
         const uint64_t ad[] = {(uint64_t)p.w.K, (uint64_t)p.groups.M}, as[] = {(uint64_t)p.lda * 2};
-        const uint32_t ab[] = {64, (uint32_t)tokens};
+        const uint32_t ab[] = {64, (uint32_t)shape.tokens};
         mapped = encode_tiled(&maps.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.w.Q, qd, qs, qb, 128) &&
                  encode_tiled(&maps.s, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, p.w.S, sd, ss, sb, 0) &&
                  (p.w.Z == nullptr || encode_tiled(&maps.z, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.w.Z, sd, zs, sb, 0)) &&
                  encode_tiled(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, p.A, ad, as, ab, 128);
         if (!mapped) return cudaErrorInvalidValue;
     }
-    return p.bf16 ? launch_group<true>(p, maps, tokens, sms, err, s) : launch_group<false>(p, maps, tokens, sms, err, s);
+    return p.bf16 ? launch_group<true>(p, maps, shape, sms, err, s) : launch_group<false>(p, maps, shape, sms, err, s);
 }
 
 }  // namespace swg

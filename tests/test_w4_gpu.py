@@ -186,6 +186,32 @@ def test_ragged_groups(rows, stype):
     run_gemm(rows, 72, 160, 32, False, stype, "f32", seed=len(rows) + 1, before=3, after=2)
 
 
+@pytest.mark.parametrize("K", [2049, 2300, 4096, 9000])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("M", [1, 8, 16, 40])
+def test_long_rows(K, group, zero, M):
+    run_gemm([M], 200, K, group, zero, "bf16" if zero else "f16", "f32", seed=K, dense=True)
+
+
+@pytest.mark.parametrize("N", [1, 2, 31, 63, 64, 65, 96, 127, 128, 129, 1000])
+@pytest.mark.parametrize("M", [9, 15, 17, 31, 32, 33, 70])
+def test_many_rows_and_columns(M, N):
+    run_gemm([M], N, 2100, 64, True, "f16", seed=M, dense=True, alpha=0.5, beta=1.0)
+
+
+@pytest.mark.parametrize("rows", [[16], [60, 0, 7, 1, 0, 33], [0, 0, 0, 70], [32, 64, 31], [17] * 20])
+@pytest.mark.parametrize("N,K,group,zero", [(72, 100, 32, True), (130, 700, 64, False), (8, 2100, 128, True)])
+@pytest.mark.parametrize("stype", ["bf16", "f16"])
+def test_ragged_groups_of_many_rows(rows, N, K, group, zero, stype):
+    run_gemm(rows, N, K, group, zero, stype, seed=N, before=3, after=2)
+
+
+@pytest.mark.parametrize("rows,N,K", [([40], 100, 2100), ([12], 64, 4000), ([30, 0, 40], 70, 600), ([2], 20, 4500)])
+def test_swiglu_of_many_rows(rows, N, K):
+    test_swiglu(rows, N, K, 64, True, "bf16")
+
+
 @pytest.mark.parametrize("alpha,beta", [(0.5, 0.0), (1.0, 1.0), (-2.0, 0.25), (0.0, 1.0)])
 @pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
 def test_alpha_beta(alpha, beta, out):
@@ -259,12 +285,20 @@ def test_wrong_offsets_are_clamped_and_reported():
         assert swg.get_device_error() == 1 and swg.get_device_error() == 0
         want, tol = product(f64(A), w, np.array(clamped), 1.0, 0.0, np.full((6, 40), 3.0), "f32")
         close(C, want, tol, str(off))
+    A = torch.randn((60, 64), generator=gen(1)).bfloat16()       # chunks of 32 rows
+    for off, clamped in (([0, 40, 2, 60], [0, 40, 40, 60]), ([-3, 20, 33, 90], [0, 20, 33, 60]), ([0, 70, 1, 2], [0, 60, 60, 60])):
+        C = torch.full((60, 40), 3.0, device="cuda")
+        swg.gemm_w4_into(C, A.cuda(), *W, 32, offsets=torch.tensor(off, dtype=torch.int32, device="cuda"))
+        assert swg.get_device_error() == 1 and swg.get_device_error() == 0
+        want, tol = product(f64(A), w, np.array(clamped), 1.0, 0.0, np.full((60, 40), 3.0), "f32")
+        close(C, want, tol, str(off))
 
 
 def test_same_bits_again_and_on_another_stream():
-    a = run_gemm([5, 9], 300, 1000, 64, True, "bf16", seed=8)
-    b = run_gemm([5, 9], 300, 1000, 64, True, "bf16", seed=8, stream=torch.cuda.Stream())
-    assert torch.equal(a, b)
+    for rows, K in (([5, 9], 1000), ([5], 9000), ([40], 2100)):
+        a = run_gemm(rows, 300, K, 64, True, "bf16", seed=8)
+        b = run_gemm(rows, 300, K, 64, True, "bf16", seed=8, stream=torch.cuda.Stream())
+        assert torch.equal(a, b)
 
 
 def test_beyond_32_bits():
