@@ -330,6 +330,27 @@ struct Experts {
     uint8_t home[V];                                 // of their groups
 };
 
+template <int V>
+__device__ __forceinline__ Experts<V> experts_of(const RouteArgs &p)
+{
+    const int lane = threadIdx.x & 31;
+    Experts<V> of;
+    of.most = 0.0f;
+    of.size = p.E / p.groups;
+    of.rows = of.size % 32 == 0 ? of.size / 32 : 0;
+    of.log_lanes = of.rows > 0 ? 0 : log_group_lanes(p.groups);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        of.bias[i] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.0f;
+        // (a bias of -inf masks its expert; behind the last, the logits do)
+        if (of.bias[i] != minus_inf()) of.most = of.bias[i] == of.bias[i] ? fmaxf(of.most, fabsf(of.bias[i])) : -minus_inf();
+        of.home[i] = (uint8_t)(min(e, p.E - 1) / of.size << of.log_lanes);
+    }
+    of.most = warp_max(of.most);
+    return of;
+}
+
 // The experts of a token, lane j's the j'th (-1: none), and lane j's weight, from
 // logits l (lane l's those of experts l, l + 32, ..; -inf behind the last).
 template <int V>
@@ -667,7 +688,7 @@ __device__ __forceinline__ void chunk_of(int T, int n, int c, int &from, int &to
 }
 
 template <int V, int NT>
-__global__ void __launch_bounds__(NT) route_kernel(const RouteArgs p, int scratch_bytes, int32_t *counts)
+__global__ void __launch_bounds__(NT) route_kernel(const __grid_constant__ RouteArgs p, int scratch_bytes, int32_t *counts)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -682,20 +703,7 @@ __global__ void __launch_bounds__(NT) route_kernel(const RouteArgs p, int scratc
     }
     int from, to;
     chunk_of(p.T, gridDim.x, blockIdx.x, from, to);
-    Experts<V> of;
-    of.most = 0.0f;
-    of.size = p.E / p.groups;
-    of.rows = of.size % 32 == 0 ? of.size / 32 : 0;
-    of.log_lanes = of.rows > 0 ? 0 : log_group_lanes(p.groups);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane + 32 * i;
-        of.bias[i] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.0f;
-        // (a bias of -inf masks its expert; behind the last, the logits do)
-        if (of.bias[i] != minus_inf()) of.most = of.bias[i] == of.bias[i] ? fmaxf(of.most, fabsf(of.bias[i])) : -minus_inf();
-        of.home[i] = (uint8_t)(min(e, p.E - 1) / of.size << of.log_lanes);
-    }
-    of.most = warp_max(of.most);
+    const Experts<V> of = experts_of<V>(p);
     float l[V], next[V];
     auto load = [&](int t) {
         const long long row = t * p.ld + lane;
@@ -731,6 +739,420 @@ __global__ void __launch_bounds__(NT) route_kernel(const RouteArgs p, int scratc
         return;
     }
     rank_slots<NT>(p.experts, 0, p.T * p.top, p.T * p.top, p.E, p.plan, count, count + p.E, count + 2 * p.E);
+}
+
+// ----------------------------------------------------- four tokens of a warp
+
+// For up to 256 experts, eight of them a token: eight lanes, a team, have a token.  A
+// token's instructions are then mostly those of its logits, 4 W a lane, four
+// neighbouring ones of every 32 (W pieces); what goes over lanes, and each
+// instruction of it, serves four tokens.  Steps as in choose: groups from
+// registers by halving (lane q has piece q's two largest at the end), a bound from the
+// largest of sixteenths of the experts, and a ranking of what passes.  What
+// FP32 cannot decide, the warp does together, one token after the other.
+constexpr int TEAM_THREADS = 512, TEAM_TOP = 8;
+constexpr int TEAM_BUFFER = 33;                      // 32 candidates, padded
+
+__host__ __device__ constexpr int keys_pitch(int w) { return 4 * w + 4; }           // floats of a lane
+__host__ __device__ constexpr int team_bytes(int w) { return 32 * keys_pitch(w) * 4 + 2 * 4 * TEAM_BUFFER * 8; }   // of a warp
+static_assert(SCRATCH + 8 * (256 + 8) <= 32 * keys_pitch(8) * 4 && SCRATCH + 8 * (32 + 1) <= 32 * keys_pitch(1) * 4, "a token's choices");
+
+template <class F>
+__device__ __forceinline__ float over_team(float v, F f)
+{
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) v = f(v, __shfl_xor_sync(ALL, v, d));
+    return v;
+}
+__device__ __forceinline__ float team_max(float v) { return over_team(v, [](float a, float b) { return fmaxf(a, b); }); }
+__device__ __forceinline__ float team_sum(float v) { return over_team(v, [](float a, float b) { return a + b; }); }
+
+__device__ __forceinline__ void merge_two(float &a, float &b, float a2, float b2)
+{
+    b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+    a = fmaxf(a, a2);
+}
+
+// Four neighbouring logits.
+__device__ __forceinline__ void load_four(const void *x, long long i, int type, float *v)
+{
+    if (type == 2) {
+        const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        return;
+    }
+    const uint2 a = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(x) + i);
+    float2 lo, hi;
+    if (type == 1) {
+        lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&a.x));
+        hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&a.y));
+    } else {
+        lo = __half22float2(*reinterpret_cast<const __half2 *>(&a.x));
+        hi = __half22float2(*reinterpret_cast<const __half2 *>(&a.y));
+    }
+    v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
+}
+
+// A whole warp's way, for what is left: many equal choices, biases of +inf.
+template <int V>
+__device__ __noinline__ int choose_alone(const RouteArgs &p, long long row, unsigned char *scratch, float *weight)
+{
+    const int lane = threadIdx.x & 31;
+    const Experts<V> of = experts_of<V>(p);
+    float l[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < p.E ? load_any(p.logits, row + lane + 32 * i, p.type) : minus_inf();
+    return choose<V>(p, row, l, of, scratch, *weight);
+}
+
+// Groups whose values are nearer than FP32 tells (bits of `near`, and of `keep` the
+// best so far, at their first pieces): the best, or nothing when more than 32 experts
+// matter for that.  `last`: at lane g the smallest choice in group g's value.  The choices as
+// route_team_kernel forms them.
+__device__ __noinline__ bool settle_groups(const RouteArgs &p, long long row, unsigned &keep, unsigned near, float last, float m,
+                                           float largest, float tol, int rows, uint64_t *buffer)
+{
+    const int lane = threadIdx.x & 31;
+    const bool softmax = p.score == SCORE_SOFTMAX;
+    int n = 0;
+#pragma unroll 1
+    for (int i = 0; 32 * i < p.E; ++i) {
+        const int home = i & ~(rows - 1), e = lane + 32 * i;
+        const float least = __shfl_sync(ALL, last, home) - tol;
+        if (!(near >> home & 1)) continue;
+        const float x = load_any(p.logits, row + e, p.type);
+        float s = softmax ? __expf(x - m) * largest : __fdividef(1.0f, 1.0f + __expf(-x));
+        if (p.bias != nullptr) s += p.bias[e];
+        const bool in = x > minus_inf() && s >= least && s > minus_inf();
+        const unsigned all = __ballot_sync(ALL, in);
+        const int at = n + __popc(all & ((1u << lane) - 1));
+        if (in && at < 32) buffer[at] = (uint64_t)home << 32 | (uint32_t)e;
+        n += __popc(all);
+    }
+    if (n == 0 || n > 32) return false;
+    __syncwarp();
+    const uint64_t c = buffer[min(lane, n - 1)];
+    const double sum = softmax ? exact_sum(p, row, m) : 1.0;
+    keep = exact_groups(p, keep, near, lane < n, (int)(c >> 32), exact_choice(p, row, (int)(uint32_t)c, m, sum));
+    __syncwarp();
+    return true;
+}
+
+// The order of n <= 32 ranked candidates once more, by their exact choices.
+__device__ __noinline__ void settle_order(const RouteArgs &p, long long row, int n, float m, uint64_t *sorted)
+{
+    const int lane = threadIdx.x & 31;
+    const double sum = p.score == SCORE_SOFTMAX ? exact_sum(p, row, m) : 1.0;
+    const uint64_t c = sorted[min(lane, n - 1)];
+    const int expert = (int)~(uint32_t)c;
+    const double exact = exact_choice(p, row, expert, m, sum);
+    int rank = 0;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+        const double other = __shfl_sync(ALL, exact, j);
+        const int of_other = __shfl_sync(ALL, expert, j);
+        rank += other > exact || (other == exact && of_other < expert);
+    }
+    __syncwarp();
+    if (lane < n) sorted[rank] = c;
+    __syncwarp();
+}
+
+template <int W>
+__global__ void __launch_bounds__(TEAM_THREADS) route_team_kernel(const __grid_constant__ RouteArgs p, int32_t *counts)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    extern __shared__ __align__(16) unsigned char shared[];
+    constexpr int WARPS = TEAM_THREADS / 32, N = 4 * W;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, team = lane >> 3, q = lane & 7;
+    unsigned char *const scratch = shared + warp * team_bytes(W);
+    float *const keys = reinterpret_cast<float *>(scratch) + lane * keys_pitch(W);
+    uint64_t *const buffers = reinterpret_cast<uint64_t *>(scratch + 32 * keys_pitch(W) * 4);
+    uint64_t *const buffer = buffers + team * TEAM_BUFFER, *const sorted = buffer + 4 * TEAM_BUFFER;
+    float *const biases = reinterpret_cast<float *>(shared + WARPS * team_bytes(W));
+    int *const count = reinterpret_cast<int *>(biases + 32 * W);
+    const bool planned = p.plan.offsets != nullptr, biased = p.bias != nullptr, grouped = p.groups > 1;
+    const bool by_score = biased || (grouped && p.group_sum == 2), softmax = p.score == SCORE_SOFTMAX;
+    if (planned)
+        for (int e = tid; e < 2 * p.E; e += TEAM_THREADS) count[e] = 0;
+    for (int e = tid; e < 32 * W; e += TEAM_THREADS) biases[e] = biased && e < p.E ? p.bias[e] : 0.0f;
+    __syncthreads();
+    float most = 0.0f;                               // as in experts_of
+    for (int i = 0; i < W; ++i) {
+        const float b = biases[lane + 32 * i];
+        if (b != minus_inf()) most = b == b ? fmaxf(most, fabsf(b)) : -minus_inf();
+    }
+    most = warp_max(most);
+    int from, to;
+    chunk_of(p.T, gridDim.x, blockIdx.x, from, to);
+    const unsigned mates = 0xffu << (8 * team);
+    const int rows = grouped ? p.E / p.groups / 32 : 1;              // pieces of a group, a power of two
+#pragma unroll 1
+    for (int first = from + 4 * warp; first < to; first += 4 * WARPS) {
+        const int t = min(first + team, to - 1);
+        const bool real = first + team < to;
+        const long long row = t * p.ld;
+        float l[N], v[N];                            // logits; what groups, then experts go by
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if (32 * i + 4 * q < p.E) {
+                load_four(p.logits, row + 32 * i + 4 * q, p.type, l + 4 * i);
+            } else {
+                l[4 * i] = l[4 * i + 1] = l[4 * i + 2] = l[4 * i + 3] = minus_inf();
+            }
+        }
+        float m = l[0], tol = 0.0f, largest = 1.0f, z = 1.0f;
+        bool nan = false, sure = true;
+#pragma unroll
+        for (int j = 1; j < N; ++j) m = fmaxf(m, l[j]);
+        m = team_max(m == m ? m : minus_inf());
+        if (by_score) {
+            // (scores and the bound of their error as in choose; the sum has as many additions)
+            if (softmax) {
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    v[j] = __expf(l[j] - m);
+                    sum[j % 4] += v[j];
+                }
+                largest = __fdividef(1.0f, team_sum((sum[0] + sum[1]) + (sum[2] + sum[3])));
+#pragma unroll
+                for (int j = 0; j < N; ++j) v[j] *= largest;
+                tol = largest * 0x1.8p-18f;
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j) v[j] = __fdividef(1.0f, 1.0f + __expf(-l[j]));
+                largest = m < -80.0f ? 0.0f : __fdividef(1.0f, 1.0f + __expf(-m));
+                tol = largest * (12.0f + 2.4f * fmaxf(-m, 0.0f)) * 0x1p-23f;
+            }
+            tol += 0x1p-22f * (largest + most) + 0x1p-120f;
+            sure = tol < 1.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float4 b = *reinterpret_cast<const float4 *>(biases + 32 * i + 4 * q);
+                v[4 * i] += b.x;
+                v[4 * i + 1] += b.y;
+                v[4 * i + 2] += b.z;
+                v[4 * i + 3] += b.w;
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (l[j] == minus_inf()) v[j] = minus_inf();
+                nan = nan || v[j] != v[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                v[j] = l[j];
+                nan = nan || l[j] != l[j];
+            }
+        }
+        if (softmax && !p.normalise) {
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < N; ++j) sum[j % 4] += expf(l[j] - m);
+            z = team_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        }
+        // (a NaN, for softmax +inf as well; a padding token, without a logit)
+        nan = (__ballot_sync(ALL, nan || (softmax && m == -minus_inf())) & mates) != 0;
+        const bool usual = real && !nan && m > minus_inf();
+
+        if (grouped) {
+            float a[W], b[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float h0 = fmaxf(v[4 * i], v[4 * i + 1]), h1 = fmaxf(v[4 * i + 2], v[4 * i + 3]);
+                const float l0 = fminf(v[4 * i], v[4 * i + 1]), l1 = fminf(v[4 * i + 2], v[4 * i + 3]);
+                a[i] = fmaxf(h0, h1);
+                b[i] = fmaxf(fminf(h0, h1), fmaxf(l0, l1));
+            }
+#pragma unroll
+            for (int d = W / 2; d > 0; d >>= 1)      // a half of the pieces for each half of the lanes
+#pragma unroll
+                for (int i = 0; i < d; ++i) {
+                    const bool up = q & d;
+                    const float a2 = __shfl_xor_sync(ALL, up ? a[i] : a[i + d], d), b2 = __shfl_xor_sync(ALL, up ? b[i] : b[i + d], d);
+                    a[i] = up ? a[i + d] : a[i];
+                    b[i] = up ? b[i + d] : b[i];
+                    merge_two(a[i], b[i], a2, b2);
+                }
+#pragma unroll
+            for (int d = W; d < 8; d <<= 1) merge_two(a[0], b[0], __shfl_xor_sync(ALL, a[0], d), __shfl_xor_sync(ALL, b[0], d));
+            for (int d = 1; d < rows; d <<= 1) merge_two(a[0], b[0], __shfl_xor_sync(ALL, a[0], d), __shfl_xor_sync(ALL, b[0], d));
+            // lane q: piece q % W's group, whose home is the lane of its first piece
+            const bool both = p.group_sum == 2 && b[0] > minus_inf();
+            const float value = both ? a[0] + b[0] : a[0], last = both ? b[0] : a[0];
+            const bool is = q < W && (q & (rows - 1)) == 0 && a[0] > minus_inf();
+            const uint32_t own = is ? ordered(value) : 0;
+            int rank = 0;
+#pragma unroll
+            for (int d = 1; d < 8; ++d) {
+                const uint32_t other = __shfl_sync(ALL, own, q + d, 8);
+                rank += other > own || (other == own && q + d >= 8);
+            }
+            const unsigned kept = __ballot_sync(ALL, is && rank < p.top_groups);
+            const unsigned worst = __ballot_sync(ALL, is && rank == p.top_groups - 1) & mates;
+            const unsigned next = __ballot_sync(ALL, is && rank == p.top_groups) & mates;
+            const float w = __shfl_sync(ALL, value, __ffs(worst | 1u << 31) - 1), r = __shfl_sync(ALL, value, __ffs(next | 1u << 31) - 1);
+            const float tol2 = 2.0f * tol;
+            const bool close = by_score && usual && sure && next != 0 && !(w - r > tol2);
+            const unsigned near = __ballot_sync(ALL, close && is && (rank < p.top_groups ? value - r <= tol2 : w - value <= tol2));
+            unsigned keep = kept >> (8 * team) & 0xffu;
+            if (near != 0) {
+#pragma unroll 1
+                for (int f = 0; f < 4; ++f) {
+                    const unsigned of = near >> (8 * f) & 0xffu;
+                    if (of == 0) continue;
+                    unsigned found = kept >> (8 * f) & 0xffu;
+                    const bool done = settle_groups(p, __shfl_sync(ALL, row, 8 * f), found, of, __shfl_sync(ALL, last, 8 * f + q),
+                                                    __shfl_sync(ALL, m, 8 * f), __shfl_sync(ALL, largest, 8 * f),
+                                                    __shfl_sync(ALL, tol, 8 * f), rows, buffers);
+                    if (team == f) {
+                        keep = found;
+                        sure = sure && done;
+                    }
+                }
+            }
+            for (int d = 1; d < rows; d <<= 1) keep |= keep << d;    // all pieces of a group
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (!biased) v[j] = l[j];
+                if (!(keep >> (j / 4) & 1)) v[j] = minus_inf();
+            }
+        }
+
+        // The bound: of the team's 16 parts, two of each lane, as many have a value
+        // that is not below it as are wanted.
+        float h0 = fmaxf(v[0], v[1]), h1 = fmaxf(v[2], v[3]);
+#pragma unroll
+        for (int i = 1; i < W; ++i) {
+            h0 = fmaxf(h0, fmaxf(v[4 * i], v[4 * i + 1]));
+            h1 = fmaxf(h1, fmaxf(v[4 * i + 2], v[4 * i + 3]));
+        }
+        int above0 = h1 > h0, above1 = h0 > h1;
+#pragma unroll
+        for (int d = 1; d < 8; ++d) {
+            const float o0 = __shfl_sync(ALL, h0, q + d, 8), o1 = __shfl_sync(ALL, h1, q + d, 8);
+            above0 += (o0 > h0) + (o1 > h0);
+            above1 += (o0 > h1) + (o1 > h1);
+        }
+        const int want = p.top + biased;             // (with a bias the next best has to be looked at too)
+        float bound = over_team(fminf(above0 < want ? h0 : -minus_inf(), above1 < want ? h1 : -minus_inf()),
+                                [](float x, float y) { return fminf(x, y); });
+        if (biased) bound -= 1.01f * tol;
+        bound = fmaxf(bound, -0x1.fffffep127f);      // (not what is masked)
+        unsigned pass = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) pass |= v[j] >= bound ? 1u << j : 0u;
+#pragma unroll
+        for (int i = 0; i < W; ++i) *reinterpret_cast<float4 *>(keys + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        if (!usual) pass = 0;
+        const int mine_pass = __popc(pass);
+        int at = mine_pass;
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) {
+            const int o = __shfl_up_sync(ALL, at, d, 8);
+            if (q >= d) at += o;
+        }
+        int n = __shfl_sync(ALL, at, 7, 8);
+        at -= mine_pass;
+        if (n > 32) {
+            sure = false;
+            pass = 0;
+            n = 0;
+        }
+        // candidates: their keys' order above, the complement of the expert below
+        for (; pass != 0; pass &= pass - 1, ++at) {
+            const int j = __ffs(pass) - 1;
+            buffer[at] = (uint64_t)ordered(keys[j]) << 32 | (uint32_t)~(32 * (j >> 2) + 4 * q + (j & 3));
+        }
+        __syncwarp();
+        const int longest = (int)__reduce_max_sync(ALL, (unsigned)n);
+        for (int base = 0; base < longest; base += 16) {
+            const uint64_t c0 = base + q < n ? buffer[base + q] : ~0ull, c1 = base + q + 8 < n ? buffer[base + q + 8] : ~0ull;
+            int rank0 = 0, rank1 = 0;
+            for (int j = 0; j < longest; ++j) {
+                const uint64_t other = j < n ? buffer[j] : 0;
+                rank0 += other > c0;
+                rank1 += other > c1;
+            }
+            if (base + q < n) sorted[rank0] = c0;
+            if (base + q + 8 < n) sorted[rank1] = c1;
+        }
+        __syncwarp();
+        if (biased) {
+            // Neighbours nearer than the error, and not the same logit and bias: as in choose.
+            bool wrong = false;
+            const uint32_t edge = p.top - 1 < n ? (uint32_t)(sorted[p.top - 1] >> 32) : 0;
+            for (int r = q + 1; r < n; r += 8) {
+                const uint64_t one = sorted[r - 1], two = sorted[r];
+                const uint32_t k1 = (uint32_t)(one >> 32), k2 = (uint32_t)(two >> 32);
+                if ((r <= p.top || k1 == edge) && !(value_of(k1) - value_of(k2) > tol)) {
+                    const int e1 = (int)~(uint32_t)one, e2 = (int)~(uint32_t)two;
+                    wrong = wrong || load_any(p.logits, row + e1, p.type) != load_any(p.logits, row + e2, p.type) || biases[e1] != biases[e2];
+                }
+            }
+            const unsigned any = __ballot_sync(ALL, wrong && sure);
+            if (any != 0) {
+#pragma unroll 1
+                for (int f = 0; f < 4; ++f)
+                    if (any >> (8 * f) & 0xffu)
+                        settle_order(p, __shfl_sync(ALL, row, 8 * f), __shfl_sync(ALL, n, 8 * f), __shfl_sync(ALL, m, 8 * f),
+                                     buffers + (4 + f) * TEAM_BUFFER);
+            }
+        }
+        int mine = q < min(n, p.top) ? (int)~(uint32_t)sorted[q] : -1;
+
+        // Weights, as in choose.
+        const bool on = mine >= 0;
+        const float x = on ? load_any(p.logits, row + mine, p.type) : minus_inf();
+        float weight;
+        if (!p.normalise) {
+            const float s = softmax ? __fdividef(expf(x - m), z) : __fdividef(1.0f, 1.0f + expf(-x));
+            weight = on ? p.scale * s : 0.0f;
+        } else {
+            const float top = team_max(x);
+            float s = 0.0f;
+            if (on) s = softmax || top < -40.0f ? expf(x - top) : __fdividef(1.0f, 1.0f + expf(-x));
+            const float sum = team_sum(s);
+            weight = on ? p.scale * __fdividef(s, sum) : 0.0f;
+        }
+        if (nan) {
+            mine = q < p.top ? q : -1;
+            weight = __int_as_float(0x7fffffff);
+        }
+        const unsigned left = __ballot_sync(ALL, usual && !sure);
+        if (left != 0) {
+#pragma unroll 1
+            for (int f = 0; f < 4; ++f) {
+                if (!(left >> (8 * f) & 0xffu)) continue;
+                float w;
+                __syncwarp();
+                const int e = choose_alone<W>(p, __shfl_sync(ALL, row, 8 * f), scratch, &w);
+                __syncwarp();
+                const int e8 = __shfl_sync(ALL, e, q);
+                const float w8 = __shfl_sync(ALL, w, q);
+                if (team == f) {
+                    mine = e8;
+                    weight = w8;
+                }
+            }
+        }
+        if (real && q < p.top) {
+            p.experts[(long long)t * p.top + q] = mine;
+            p.weights[(long long)t * p.top + q] = weight;
+            if (planned && mine >= 0) atomicAdd(&count[mine], 1);
+        }
+        __syncwarp();
+    }
+    if (!planned) return;
+    __syncthreads();
+    if (gridDim.x > 1) {
+        for (int e = tid; e < p.E; e += TEAM_THREADS) counts[(long long)blockIdx.x * p.E + e] = count[e];
+        return;
+    }
+    rank_slots<TEAM_THREADS>(p.experts, 0, p.T * p.top, p.T * p.top, p.E, p.plan, count, count + p.E, count + 2 * p.E);
 }
 
 __global__ void __launch_bounds__(SORT_THREADS)
@@ -912,6 +1334,23 @@ cudaError_t route_form(const RouteArgs &p, int ctas, int32_t *counts, cudaStream
     return go(route_kernel<V, NT>, once, ctas, NT, shared, s, p, scratch, counts);
 }
 
+template <int W>
+cudaError_t team_form(const RouteArgs &p, int ctas, int32_t *counts, cudaStream_t s)
+{
+    const size_t shared = TEAM_THREADS / 32 * (size_t)team_bytes(W) + 128 * W + (p.plan.offsets ? 4 * sort_ints(p.E, TEAM_THREADS / 32) : 0);
+    static DeviceOnce once;
+    return go(route_team_kernel<W>, once, ctas, TEAM_THREADS, shared, s, p, counts);
+}
+
+// Whether route_team_kernel takes them: its logits come four at a time.
+bool for_teams(const RouteArgs &p)
+{
+    const int rows = p.E / p.groups / 32;            // pieces of a group
+    return p.E <= 256 && p.top <= TEAM_TOP && p.E % 4 == 0 && p.ld % 4 == 0 &&
+           reinterpret_cast<uintptr_t>(p.logits) % (p.type == 2 ? 16 : 8) == 0 &&
+           (p.groups == 1 || (p.E / p.groups % 32 == 0 && (rows & (rows - 1)) == 0));
+}
+
 int values_per_lane(int E) { return (E + 31) / 32; }
 
 }  // namespace
@@ -928,6 +1367,10 @@ cudaError_t launch_route(const RouteArgs &p, int chunks, int32_t *counts, cudaSt
 {
     const int v = values_per_lane(p.E);
     const int ctas = p.plan.offsets ? chunks : 0;
+    if (for_teams(p)) {
+        const int n = ctas ? ctas : (p.T + TEAM_THREADS / 8 - 1) / (TEAM_THREADS / 8);
+        return v <= 1 ? team_form<1>(p, n, counts, s) : v <= 2 ? team_form<2>(p, n, counts, s) : v <= 4 ? team_form<4>(p, n, counts, s) : team_form<8>(p, n, counts, s);
+    }
 #define FORM(V, NT) return route_form<V, NT>(p, ctas ? ctas : (p.T + NT / 32 - 1) / (NT / 32), counts, s)
     if (ctas) {
         if (v <= 1) FORM(1, 1024);
