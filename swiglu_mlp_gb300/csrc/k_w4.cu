@@ -5,7 +5,8 @@
 // For few rows the weights' bytes are what the operator cannot do without; the
 // kernel streams them once, and what bounds it is the decoding: seven shifts and masks
 // for eight codes, on a pipe that takes one every two cycles (4096 x 14336: 3.7 us of
-// it, 4.5 of memory).  The rows of
+// it, 4.5 of memory, 9.6 in all; 28672 x 4096: 17.3, 3.6 TB/s; 64 rows of 64 experts, 2432 x
+// 896: 17.4, of which 6.7 memory).  The rows of
 // W are the 16 rows of an mma.sync m16n8k16 (FP32 accumulators), up to eight rows
 // of A its columns: at one row of A 7/8 of the instruction's work is for nothing,
 // but it is free, and the rows of W arrive in fragments as they lie in memory:
@@ -17,9 +18,10 @@
 // 16 bits.
 //
 // w4_kernel: a CTA has one chunk of at most eight rows of A; its four warps are teams of
-// `team` along K, and each team has 64 rows of W.  A team's warps take steps of 256
+// `team` along K, and each team has 32 rows of W (64: a third fewer warps fit, 20.3 us
+// instead of 17.4 for the experts above).  A team's warps take steps of 256
 // columns in turn.  Each warp has a ring of its own that TMA fills: a lane asks
-// for a step's codes (64 rows of 128 bytes), scales, zero points and columns of A
+// for a step's codes (32 rows of 128 bytes), scales, zero points and columns of A
 // with an instruction or four each, which leaves the issue slots to the decoding;
 // cp.async by all lanes, with its addresses and edges, took as many instructions
 // again.  A team's sums are added at the end, in order.  w4_many_kernel, for more
@@ -39,13 +41,14 @@ namespace swg {
 namespace {
 
 constexpr int WARPS = 4;
-constexpr int MT = 4;                    // tiles of 16 rows of W per warp
+constexpr int MT = 2;                    // tiles of 16 rows of W per warp
 constexpr int ROWS = 16 * MT;
 constexpr int TOKENS = 8;                // rows of A per chunk
 constexpr int STEP = 256;                // columns per warp and step
 constexpr int CODES = ROWS * STEP / 2;   // bytes of a step
 constexpr int SUMS = ROWS + 2;           // floats of a row of A's sums, padded
 constexpr int STAGES = 2;
+constexpr int SM_SHARED = 233472, CTA_SHARED = 232448;   // bytes of an SM (1024 of each CTA are the system's), most of a CTA
 
 // d = a b (FIRST) or d += a b, a 16 x 16 (row fragments), b 16 x 8.
 template <bool BF16, bool FIRST>
@@ -105,13 +108,14 @@ struct W4Maps {
 
 // Shared memory: rings of codes, of A, of scales and zero points, barriers; then the
 // teams' sums in its place.
-__host__ __device__ constexpr int scales_bytes(int per) { return STEP / (32 * per) * ROWS * 2; }
-__host__ __device__ constexpr int params_bytes(int per, bool zero) { return scales_bytes(per) * (zero ? 3 : 2) / 2; }
-__host__ __device__ constexpr int params_pitch(int per, bool zero) { return (params_bytes(per, zero) + 127) / 128 * 128; }  // (TMA's rule)
+// (of a box of `rows` rows of W)
+__host__ __device__ constexpr int scales_bytes(int per, int rows) { return STEP / (32 * per) * rows * 2; }
+__host__ __device__ constexpr int params_bytes(int per, bool zero, int rows) { return scales_bytes(per, rows) * (zero ? 3 : 2) / 2; }
+__host__ __device__ constexpr int params_pitch(int per, bool zero, int rows) { return (params_bytes(per, zero, rows) + 127) / 128 * 128; }  // (TMA's rule)
 __host__ __device__ constexpr int a_bytes(int tokens) { return STEP * 2 * tokens; }
 __host__ __device__ constexpr int shared_bytes(int per, bool zero, int tokens)
 {
-    return WARPS * STAGES * (CODES + a_bytes(tokens) + params_pitch(per, zero)) + 256;
+    return WARPS * STAGES * (CODES + a_bytes(tokens) + params_pitch(per, zero, ROWS)) + 256;
 }
 static_assert(WARPS * STAGES * 8 + 8 <= 256, "barriers and the abort flag");
 
@@ -148,25 +152,25 @@ __device__ __forceinline__ Lane lane_of()
 
 // acc += the products of a step: codes and params as TMA left them; rows of A in lines
 // of 128 bytes (64 columns) of shared memory, `lines` for each 64 columns, this lane's of
-// NT rows of A 8 apart from x_line on; MR pieces of 16 rows of W, from `piece` of the
-// slot's on.  whole: the second half has columns too.
-template <bool BF16, int PER, bool ZERO, int MR, int NT>
+// NT rows of A 8 apart from x_line on; MT pieces of 16 rows of W, from `piece` of the
+// slot's box of BOX rows on.  whole: the second half has columns too.
+template <bool BF16, int PER, bool ZERO, int BOX, int NT>
 __device__ __forceinline__ void multiply(const Lane &l, const unsigned char *shared, const unsigned char *codes,
                                          const unsigned char *params, int x_line, int lines, bool whole,
-                                         int piece, float (&acc)[MR][NT][4])
+                                         int piece, float (&acc)[MT][NT][4])
 {
     const uint32_t *scale = reinterpret_cast<const uint32_t *>(params) + piece * 8 + l.pi;
-    const uint16_t *zero = reinterpret_cast<const uint16_t *>(params + scales_bytes(PER)) + piece * 8 + l.pi;
+    const uint16_t *zero = reinterpret_cast<const uint16_t *>(params + scales_bytes(PER, BOX)) + piece * 8 + l.pi;
     const uint32_t scale0 = l.odd ? 0x3244u : 0x1044u, scale1 = l.odd ? 0x1044u : 0x3244u;
     const int t = l.t;
-    float part[MR][NT][4];
-    uint32_t z0[MR], z1[MR];
+    float part[MT][NT][4];
+    uint32_t z0[MT], z1[MT];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         if (half == 1 && !whole) break;
-        uint32_t w[2 * MR][4];                       // both rows of each 16
+        uint32_t w[2 * MT][4];                       // both rows of each 16
 #pragma unroll
-        for (int r = 0; r < 2 * MR; ++r) {
+        for (int r = 0; r < 2 * MT; ++r) {
             const unsigned char *at = codes + (r % 2 ? l.row_at1 : l.row_at0) + (piece + r / 2) * 16 * (STEP / 2);
             const int swap = r % 2 ? l.swap1 : l.swap0;
             if (PER == 4) {
@@ -195,11 +199,11 @@ __device__ __forceinline__ void multiply(const Lane &l, const unsigned char *sha
             }
             const int b = (4 * half + j) / PER;      // the scale's place among the step's
 #pragma unroll
-            for (int m = 0; m < MR; ++m) {
+            for (int m = 0; m < MT; ++m) {
                 if (j % PER == 0) {
                     z0[m] = z1[m] = UNITS<BF16> + 0x00080008u;
                     if (ZERO) {
-                        const uint32_t z = __byte_perm(zero[(b * MT + m) * 8], 0, l.odd ? 0x4401 : 0x4410);
+                        const uint32_t z = __byte_perm(zero[(b * (BOX / 16) + m) * 8], 0, l.odd ? 0x4401 : 0x4410);
                         z0[m] = UNITS<BF16> + (z & 15u) * 0x00010001u;
                         z1[m] = UNITS<BF16> + (z >> 8 & 15u) * 0x00010001u;
                     }
@@ -222,10 +226,10 @@ __device__ __forceinline__ void multiply(const Lane &l, const unsigned char *sha
                 if (j % PER == PER - 1) {
                     float2 s;
                     if (BF16)                        // (a bfloat16 is the upper half of its FP32)
-                        s = make_float2(__uint_as_float(__byte_perm(scale[(b * MT + m) * 8], 0, scale0)),
-                                        __uint_as_float(__byte_perm(scale[(b * MT + m) * 8], 0, scale1)));
+                        s = make_float2(__uint_as_float(__byte_perm(scale[(b * (BOX / 16) + m) * 8], 0, scale0)),
+                                        __uint_as_float(__byte_perm(scale[(b * (BOX / 16) + m) * 8], 0, scale1)));
                     else
-                        s = scale_pair<BF16>(__byte_perm(scale[(b * MT + m) * 8], 0, l.order));
+                        s = scale_pair<BF16>(__byte_perm(scale[(b * (BOX / 16) + m) * 8], 0, l.order));
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         acc[m][n][0] = fmaf(s.x, part[m][n][0], acc[m][n][0]);
@@ -266,12 +270,12 @@ __device__ __forceinline__ float2 rows_of(const Lane &l, const float (&c)[4], in
 
 // `tokens`: rows of A of a chunk, 1, 2, 4 or 8.  `team`: a power of two.
 template <bool BF16, int PER, bool ZERO>
-__global__ void __launch_bounds__(32 * WARPS, 3)
+__global__ void __launch_bounds__(32 * WARPS, 4)
     w4_kernel(const __grid_constant__ W4Maps maps, const W4Args p, int tiles, int tokens, int team, int *err)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) unsigned char shared[];
-    constexpr int BLOCKS = STEP / (32 * PER), PARAMS = params_pitch(PER, ZERO);
+    constexpr int BLOCKS = STEP / (32 * PER), PARAMS = params_pitch(PER, ZERO, ROWS);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wk = warp & (team - 1), quad = lane >> 2;
     const int of_a = a_bytes(tokens);
     unsigned char *const codes = shared + warp * STAGES * CODES;
@@ -298,10 +302,10 @@ __global__ void __launch_bounds__(32 * WARPS, 3)
         const uint32_t bar = bars + 8 * slot;
         if (lane == 0) {
             const uint32_t to = smem_u32(params) + slot * PARAMS;
-            mbar_arrive_expect_tx(bar, CODES + params_bytes(PER, ZERO) + a_bytes(tokens));
+            mbar_arrive_expect_tx(bar, CODES + params_bytes(PER, ZERO, ROWS) + a_bytes(tokens));
             tma_load_3d_cta(smem_u32(codes) + slot * CODES, &maps.q, bar, step * (STEP / 2), n0, g);
             tma_load_3d_cta(to, &maps.s, bar, n0, step * BLOCKS, g);
-            if (ZERO) tma_load_3d_cta(to + scales_bytes(PER), &maps.z, bar, n0, step * BLOCKS, g);
+            if (ZERO) tma_load_3d_cta(to + scales_bytes(PER, ROWS), &maps.z, bar, n0, step * BLOCKS, g);
         }
         if (lane < 4) tma_load_2d(smem_u32(a) + slot * of_a + lane * tokens * 128, &maps.a, bar, step * STEP + lane * 64, row0);
     };
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(32 * WARPS, 3)
             stopped = true;
             break;
         }
-        multiply<BF16, PER, ZERO, MT, 1>(l, shared, codes + slot * CODES, params + slot * PARAMS, x_line + slot * of_a / 128, tokens,
+        multiply<BF16, PER, ZERO, ROWS, 1>(l, shared, codes + slot * CODES, params + slot * PARAMS, x_line + slot * of_a / 128, tokens,
                                      step * STEP + STEP / 2 < p.w.K, 0, acc);
         __syncwarp();
         if (step + STAGES * team < steps) load(step + STAGES * team, slot);
@@ -380,8 +384,8 @@ __global__ void __launch_bounds__(32 * WARPS, 3)
 // through shared memory, in order.  (One CTA of 256 rows for each SM: 41 us, since only
 // 15 clusters of eight of that size are resident, and 35.9 with clusters of four; this
 // 20.4; chunks of eight rows of the other kernel 31.4.)
-constexpr int MANY_BOXES = 2, MANY_ROWS = MANY_BOXES * ROWS;
-constexpr int MANY_MT = MANY_ROWS / 16 / WARPS;
+constexpr int MANY_ROWS = WARPS * ROWS, MANY_BOX = 64, MANY_BOXES = MANY_ROWS / MANY_BOX;
+constexpr int MANY_CODES = MANY_BOX * STEP / 2;
 constexpr int MANY_THREADS = 32 * (WARPS + 1);
 constexpr int MANY_STAGES = 3;
 constexpr int MANY_SUMS = MANY_ROWS + 2;             // floats of a row of A's sums, padded
@@ -389,11 +393,11 @@ constexpr int MOST_RANGES = 8;
 
 __host__ __device__ constexpr int many_stage(int per, bool zero, int nt)
 {
-    return MANY_BOXES * (CODES + params_pitch(per, zero)) + a_bytes(8 * nt);
+    return MANY_BOXES * (MANY_CODES + params_pitch(per, zero, MANY_BOX)) + a_bytes(8 * nt);
 }
 __host__ __device__ constexpr int many_shared(int per, bool zero, int nt) { return MANY_STAGES * many_stage(per, zero, nt) + 256; }
-static_assert(2 * (many_shared(1, true, 4) + 1024) <= 233472, "two CTAs on an SM");
-static_assert(MANY_SUMS * 32 * 4 <= MANY_STAGES * MANY_BOXES * CODES, "the sums take the ring's place");
+static_assert(2 * (many_shared(1, true, 4) + 1024) <= SM_SHARED, "two CTAs on an SM");
+static_assert(MANY_SUMS * 32 * 4 <= MANY_STAGES * MANY_BOXES * MANY_CODES, "the sums take the ring's place");
 
 __device__ __forceinline__ float2 load_cluster(uint32_t at)
 {
@@ -408,14 +412,14 @@ __global__ void __launch_bounds__(MANY_THREADS, 2)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) unsigned char shared[];
-    constexpr int BLOCKS = STEP / (32 * PER), PARAMS = params_pitch(PER, ZERO), TOKENS_MANY = 8 * NT;
-    constexpr int A = MANY_STAGES * MANY_BOXES * CODES, P = A + MANY_STAGES * a_bytes(TOKENS_MANY), B = P + MANY_STAGES * MANY_BOXES * PARAMS;
+    constexpr int BLOCKS = STEP / (32 * PER), PARAMS = params_pitch(PER, ZERO, MANY_BOX), TOKENS_MANY = 8 * NT;
+    constexpr int A = MANY_STAGES * MANY_BOXES * MANY_CODES, P = A + MANY_STAGES * a_bytes(TOKENS_MANY), B = P + MANY_STAGES * MANY_BOXES * PARAMS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t full = smem_u32(shared) + B, empty = full + 8 * MANY_STAGES;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(shared + B + 16 * MANY_STAGES);
     // (a cluster's CTAs, the ranges of a tile, follow one another)
     const int range = blockIdx.x % ranges, unit = blockIdx.x / ranges, chunk = unit / tiles, tile = unit - chunk * tiles;
-    const int n0 = tile * MANY_ROWS, boxes = min(MANY_BOXES, (p.w.N - n0 + ROWS - 1) / ROWS), used = boxes * (WARPS / MANY_BOXES);
+    const int n0 = tile * MANY_ROWS, boxes = min(MANY_BOXES, (p.w.N - n0 + MANY_BOX - 1) / MANY_BOX), used = boxes * (WARPS / MANY_BOXES);
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int i = 0; i < MANY_STAGES; ++i) {
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 2)
 
     const int steps = (p.w.K + STEP - 1) / STEP, first = (int)((long long)steps * range / ranges);
     const int count = (int)((long long)steps * (range + 1) / ranges) - first;
-    float acc[MANY_MT][NT][4] = {};
+    float acc[MT][NT][4] = {};
     const Lane l = lane_of<BF16>();
     if (warp == WARPS) {
         if (lane == 0) {
@@ -441,12 +445,12 @@ __global__ void __launch_bounds__(MANY_THREADS, 2)
                 const int slot = i % MANY_STAGES, step = first + i;
                 const uint32_t bar = full + 8 * slot;
                 if (i >= MANY_STAGES && !wait_bounded(empty + 8 * slot, (uint32_t)((i / MANY_STAGES) - 1) & 1u, abort_flag, err)) break;
-                mbar_arrive_expect_tx(bar, boxes * (CODES + params_bytes(PER, ZERO)) + a_bytes(TOKENS_MANY));
+                mbar_arrive_expect_tx(bar, boxes * (MANY_CODES + params_bytes(PER, ZERO, MANY_BOX)) + a_bytes(TOKENS_MANY));
                 for (int w = 0; w < boxes; ++w) {
                     const uint32_t to = smem_u32(shared) + P + (slot * MANY_BOXES + w) * PARAMS;
-                    tma_load_3d_cta(smem_u32(shared) + (slot * MANY_BOXES + w) * CODES, &maps.q, bar, step * (STEP / 2), n0 + w * ROWS, g);
-                    tma_load_3d_cta(to, &maps.s, bar, n0 + w * ROWS, step * BLOCKS, g);
-                    if (ZERO) tma_load_3d_cta(to + scales_bytes(PER), &maps.z, bar, n0 + w * ROWS, step * BLOCKS, g);
+                    tma_load_3d_cta(smem_u32(shared) + (slot * MANY_BOXES + w) * MANY_CODES, &maps.q, bar, step * (STEP / 2), n0 + w * MANY_BOX, g);
+                    tma_load_3d_cta(to, &maps.s, bar, n0 + w * MANY_BOX, step * BLOCKS, g);
+                    if (ZERO) tma_load_3d_cta(to + scales_bytes(PER, MANY_BOX), &maps.z, bar, n0 + w * MANY_BOX, step * BLOCKS, g);
                 }
                 for (int c = 0; c < 4; ++c)
                     tma_load_2d(smem_u32(shared) + A + slot * a_bytes(TOKENS_MANY) + c * TOKENS_MANY * 128, &maps.a, bar, step * STEP + c * 64, row0);
@@ -455,14 +459,15 @@ __global__ void __launch_bounds__(MANY_THREADS, 2)
             for (int j = max(i - MANY_STAGES, 0); j < i; ++j)
                 wait_bounded(full + 8 * (j % MANY_STAGES), (uint32_t)(j / MANY_STAGES) & 1u, abort_flag, err, false, DRAIN_LIMIT_NS);
         }
+        __syncwarp();
     } else if (warp < used) {
         const int box = warp / (WARPS / MANY_BOXES);
         for (int i = 0; i < count; ++i) {
             const int slot = i % MANY_STAGES;
             if (!__all_sync(0xffffffffu, wait_bounded(full + 8 * slot, (uint32_t)(i / MANY_STAGES) & 1u, abort_flag, err))) break;
-            multiply<BF16, PER, ZERO, MANY_MT, NT>(l, shared, shared + (slot * MANY_BOXES + box) * CODES, shared + P + (slot * MANY_BOXES + box) * PARAMS,
-                                          (A + slot * a_bytes(TOKENS_MANY)) / 128 + (lane >> 2), TOKENS_MANY,
-                                          (first + i) * STEP + STEP / 2 < p.w.K, warp * MANY_MT % MT, acc);
+            multiply<BF16, PER, ZERO, MANY_BOX, NT>(l, shared, shared + (slot * MANY_BOXES + box) * MANY_CODES,
+                                                    shared + P + (slot * MANY_BOXES + box) * PARAMS, (A + slot * a_bytes(TOKENS_MANY)) / 128 + (lane >> 2), TOKENS_MANY,
+                                                    (first + i) * STEP + STEP / 2 < p.w.K, warp * MT % (MANY_BOX / 16), acc);
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + 8 * slot);
         }
@@ -472,12 +477,12 @@ __global__ void __launch_bounds__(MANY_THREADS, 2)
     float *sums = reinterpret_cast<float *>(shared);
     if (warp < used) {
 #pragma unroll
-        for (int m = 0; m < MANY_MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<float2 *>(sums + (8 * n + 2 * l.t + h) * MANY_SUMS + (warp * MANY_MT + m) * 16 + 2 * l.pi) =
+                    *reinterpret_cast<float2 *>(sums + (8 * n + 2 * l.t + h) * MANY_SUMS + (warp * MT + m) * 16 + 2 * l.pi) =
                         rows_of(l, acc[m][n], h);
     }
     if (ranges > 1) cluster_sync_all();
@@ -526,43 +531,48 @@ Shape shape_of(const W4Args &p, int sms)
     // 24.1 and 19.3, 16 26.7 and 28.8, 32 38.7 and 46.3).
     if (g.offsets != nullptr && g.M >= 16ll * g.G) return {32, true};
     const int want = g.offsets == nullptr ? g.M : (int)std::min<long long>(g.M, (4ll * g.M + g.G - 1) / g.G);
-    // More than eight rows (4096 x 14336, 32 rows: 19.6 and 30.5; 4096 x 4096, 16 rows: 8.3
-    // and 9.7), unless there is too little to do for a cluster's barriers (1024 x 2048, 32
-    // rows: 6.0 and 4.9; 8192 x 1024, 16 rows: 6.4 and 4.9, 32 rows: 7.9 and 8.0).
-    if (g.offsets == nullptr && want > TOKENS && (steps > 8 || (want + TOKENS - 1) / TOKENS * items * steps > 12 * sms))
+    // More than eight rows (4096 x 14336, 32 rows: 19.6 and 36.1; 14336 x 4096, 9 rows: 15.5
+    // and 19.1), unless there is too little to do for a cluster's barriers (4096 x 4096, 16
+    // rows: 8.5 and 7.4; 8192 x 1024, 16 rows: 5.7 both).
+    if (g.offsets == nullptr && want > TOKENS && (steps >= 24 || (want + TOKENS - 1) / TOKENS * items * steps > 28ll * sms))
         return {want <= 16 ? 16 : 32, true};
-    // Up to eight, where teams of four do not fill the GPU and a warp would take more
-    // than four steps in turn: a cluster has up to 32 warps for a tile (one row, 4096 x
-    // 14336: 14.9 and 19.6; 2048 x 8192: 7.8 and 11.8; but 14336 x 4096 13.4 and 11.3, 1024
-    // x 2048 4.5 and 4.6).
-    if (steps > 4 * WARPS && (g.offsets == nullptr ? 1 : std::min(g.G, g.M)) * items < sms) return {TOKENS, true};
+    // Up to eight, where rows are long and teams of four do not fill the GPU: a cluster has
+    // up to 32 warps for a tile (one row, 1024 x 8192: 6.4 and 9.2; 2048 x 8192: 7.9 and 9.2;
+    // 4096 x 14336: 14.9 and 15.2; but 4096 x 6144 8.3 and 7.4).
+    if (steps > 24 && (g.offsets == nullptr ? 1 : std::min(g.G, g.M)) * items < sms) return {TOKENS, true};
     return {want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : TOKENS, false};
 }
 
 template <bool BF16, int PER, bool ZERO>
 cudaError_t launch(const W4Args &p, const W4Maps &maps, int tokens, int sms, int *err, cudaStream_t s)
 {
-    // As small teams as leave 12 warps for each SM, as many as are resident: one row,
-    // 4096 x 14336, 10.8 us with teams of 4 and 21.2 without; 64 rows of 64 experts, 896 x
-    // 2432, 19.2 without and 23.9 with.
+    // As small teams as leave 16 warps for each SM, as many as are resident (8 experts of
+    // 4096 x 4096, 8 rows: 16.0, and 20.0 with 12 warps).
     const int steps = (p.w.K + STEP - 1) / STEP;
     const long long items = (p.groups.offsets ? std::min(p.groups.G, p.groups.M) : chunks_of(p.groups, tokens)) * ((p.w.N + ROWS - 1ll) / ROWS);
     int team = 1;
-    while (team < WARPS && team < steps && items * team < 12ll * sms) team *= 2;
+    while (team < WARPS && team < steps && items * team < 16ll * sms) team *= 2;
     const size_t sums = (size_t)WARPS * tokens * SUMS * 4;
     auto kernel = w4_kernel<BF16, PER, ZERO>;
     static DeviceOnce once;
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     if (once.needed(dev)) {
-        if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared_bytes(PER, ZERO, TOKENS))) return e;
+        if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CTA_SHARED)) return e;
         once.mark(dev);
     }
     const int per_cta = ROWS * (WARPS / team), tiles = (p.w.N + per_cta - 1) / per_cta;
+    const long long ctas = chunks_of(p.groups, tokens) * tiles;
+    size_t room = std::max((size_t)shared_bytes(PER, ZERO, tokens), sums);
+    // CTAs that are resident at once are spread evenly: no more of them fit an SM than its
+    // share (one row, 14336 x 4096: 448 CTAs, 10.1 and 11.9 when some SMs have four and some
+    // two; 4096 x 4096: 5.6 and 6.4).  Of groups it is not known how many have work.
+    const long long share = (ctas + sms - 1) / sms;
+    if (p.groups.offsets == nullptr && share < 8) room = std::max(room, std::min<size_t>(SM_SHARED / (share + 1) - 1024 + 128, CTA_SHARED));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(chunks_of(p.groups, tokens) * tiles));
+    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(32 * WARPS);
-    cfg.dynamicSmemBytes = std::max((size_t)shared_bytes(PER, ZERO, tokens), sums);
+    cfg.dynamicSmemBytes = room;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -641,7 +651,7 @@ cudaError_t launch_w4(const W4Args &p, int sms, int *err, cudaStream_t s, bool &
         const uint64_t N = p.w.N, G = p.groups.G, blocks = p.w.blocks(), row = p.w.row_bytes(), lds = p.w.lds;
         const uint32_t per_step = STEP / p.w.group;
         const uint64_t qd[] = {row, N, G}, qs[] = {row, G > 1 ? row * N : row};
-        const uint32_t qb[] = {STEP / 2, ROWS, 1}, sb[] = {ROWS, per_step, 1};
+        const uint32_t box = shape.many ? MANY_BOX : ROWS, qb[] = {STEP / 2, box, 1}, sb[] = {box, per_step, 1};
         const uint64_t sd[] = {lds, blocks, G}, ss[] = {lds * 2, G > 1 ? lds * 2 * blocks : lds * 2}, zs[] = {lds, G > 1 ? lds * blocks : lds};
         const uint64_t ad[] = {(uint64_t)p.w.K, (uint64_t)p.groups.M}, as[] = {(uint64_t)p.lda * 2};
         const uint32_t ab[] = {64, (uint32_t)shape.tokens};
