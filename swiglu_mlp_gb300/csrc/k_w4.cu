@@ -525,12 +525,12 @@ Shape shape_of(const W4Args &p, int sms)
     const int steps = (p.w.K + STEP - 1) / STEP;
     const long long items = (p.w.N + ROWS - 1ll) / ROWS;
     // Groups: chunks of four times their mean, since another chunk reads and decodes the
-    // weights again (64 rows of 64 experts: 25.6 with chunks of 1, 21.2 with 2, 19.2 with
-    // 4, 19.8 with 8).  More than eight rows from a mean of 16 on, where the fuller
+    // weights again (64 rows of 64 experts: 21.5 with chunks of 1, 17.9 with 2, 17.4 with
+    // 4 and 8), of few rows of as many (4 rows, 8 experts of 8192 x 2048: 10.5 with 2, 7.7).  More than eight rows from a mean of 16 on, where the fuller
     // instructions outweigh the emptier chunks (16 experts of 4096 x 1024: means of 8
     // 24.1 and 19.3, 16 26.7 and 28.8, 32 38.7 and 46.3).
     if (g.offsets != nullptr && g.M >= 16ll * g.G) return {32, true};
-    const int want = g.offsets == nullptr ? g.M : (int)std::min<long long>(g.M, (4ll * g.M + g.G - 1) / g.G);
+    const int want = g.offsets == nullptr || g.M <= TOKENS ? g.M : (int)std::min<long long>(g.M, (4ll * g.M + g.G - 1) / g.G);
     // More than eight rows (4096 x 14336, 32 rows: 19.6 and 36.1; 14336 x 4096, 9 rows: 15.5
     // and 19.1), unless there is too little to do for a cluster's barriers (4096 x 4096, 16
     // rows: 8.5 and 7.4; 8192 x 1024, 16 rows: 5.7 both).
