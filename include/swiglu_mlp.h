@@ -476,7 +476,9 @@ SWG_API int swiglu_mx4(int format, const void *A, const void *SA, const void *W,
  * (T x top).  T * top, R and D are at most 2^31 - 1024, the experts at most
  * SWG_MAX_EXPERTS, top at most SWG_MAX_TOP, else SWG_ERR_UNSUPPORTED.
  * X, rows, out and their gradients share one swg_type (but for FP32 rows, see
- * expert_combine); they are 16-byte aligned, row strides multiples of 16 bytes.  Logits need only their type's alignment.
+ * expert_combine); they are 16-byte aligned, row strides multiples of 16 bytes.  Logits
+ * need only their type's alignment (four logits at a multiple of their size are read
+ * faster: rows of a multiple of four, up to 256 experts and 8 of them a token).
  * None of the outputs may overlap an input, but out of expert_combine, which is
  * read for beta != 0.
  */
@@ -547,8 +549,9 @@ SWG_API int expert_route_grad(int score, int64_t T, int64_t E, int64_t top, cons
 /*
  * expert_dispatch — rows[position[t][j],:] = X[t,:] for every slot with a row: X
  * T x D, rows R x D.  Other rows keep their values.  Positions beyond [0, R) have no
- * row; those other than -1 are reported (device error word).  Its gradient is
- * expert_combine without weights.
+ * row; those other than -1 are reported (device error word).  The positions have to
+ * differ (as expert_sort's do): a row of several slots gets pieces of any of theirs.
+ * Its gradient is expert_combine without weights.
  */
 SWG_API int expert_dispatch(int64_t T, int64_t R, int64_t D, int64_t top, const void *X, int64_t ldx,
                             int type, const int32_t *position, void *rows, int64_t ldr, void *stream);
@@ -568,8 +571,8 @@ SWG_API int expert_combine(int64_t T, int64_t R, int64_t D, int64_t top, const v
  *   d_rows[position[t][j],:] = weights[t][j] * d_out[t,:]      (other rows keep theirs)
  *   d_weights[t][j] = <rows[position[t][j],:], d_out[t,:]>     (0 without a row)
  * weights NULL: ones.  d_weights NULL: not computed, and rows is not read.  The
- * positions have to differ (as expert_sort's do): a row of several slots gets the
- * gradient of one of them.
+ * positions have to differ (as expert_sort's do): a row of several slots gets pieces of
+ * any of their gradients.
  */
 SWG_API int expert_combine_grad(int64_t T, int64_t R, int64_t D, int64_t top, const void *d_out,
                                 int64_t ldd, const void *rows, int64_t ldr, int type,
@@ -614,7 +617,8 @@ SWG_API int w4_dequantize(int64_t G, int64_t N, int64_t K, const void *Q, const 
  * gemm_w4 — C[i,:] = alpha * A[i,:] * W_g^T + beta * C[i,:] for the rows i of every
  * group g (offsets, G: as for gemm_grouped; NULL and 1: dense), FP32 accumulation.
  *   A, S   of swg_type `type` (16 bits).   C   of ctype.
- * Meant for few rows of each expert; for many, w4_dequantize and gemm_grouped.
+ * Meant for few rows of each expert: up to about 32 it is faster than the product with
+ * 16-bit weights, beyond them w4_dequantize and gemm or gemm_grouped are.
  */
 SWG_API int gemm_w4(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, const void *A, int64_t lda,
                     const void *Q, const void *S, const void *Z, int64_t lds, int64_t group,

@@ -4,9 +4,9 @@
 //
 // For few rows the weights' bytes are what the operator cannot do without; the
 // kernel streams them once, and what bounds it is the decoding: seven shifts and masks
-// for eight codes, on a pipe that takes one every two cycles (4096 x 14336: 3.7 us of
-// it, 4.5 of memory, 9.6 in all; 28672 x 4096: 17.3, 3.6 TB/s; 64 rows of 64 experts, 2432 x
-// 896: 17.4, of which 6.7 memory).  The rows of
+// for eight codes, on a pipe that takes one every two cycles (a row through 14336 rows of
+// 4096: 3.7 us of it, 4.5 of memory, 9.6 in all; 28672 x 4096: 17.3, 3.6 TB/s; 64 rows of 64
+// experts, 2432 x 896: 17.4, of which 6.7 memory).  The rows of
 // W are the 16 rows of an mma.sync m16n8k16 (FP32 accumulators), up to eight rows
 // of A its columns: at one row of A 7/8 of the instruction's work is for nothing,
 // but it is free, and the rows of W arrive in fragments as they lie in memory:
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(32 * WARPS, 4)
 
 // Chunks of 8, 16 or 32 rows of A, NT = 1, 2 or 4 tiles of 8.  A code decoded is used NT
 // times, and from NT = 2 on the mma.sync instructions bound it: one takes 17 cycles of
-// its quarter of an SM, as measured (32 rows, 14336 x 4096: 13.4 us on all SMs).  Rows
+// its quarter of an SM, as measured (32 rows, 4096 x 14336: 13.4 us on all SMs).  Rows
 // of A are as much to read as codes then, so four warps of 32 rows of W share them: a
 // CTA has 128 rows of W and a range of the steps, a fifth warp feeds its ring, two CTAs
 // fill an SM, and the CTAs of a cluster that have a tile's ranges add their sums
@@ -585,7 +585,8 @@ cudaError_t launch(const W4Args &p, const W4Maps &maps, int tokens, int sms, int
 template <bool BF16, int PER, bool ZERO, int NT>
 cudaError_t launch_many(const W4Args &p, const W4Maps &maps, int sms, int *err, cudaStream_t s)
 {
-    // As many ranges of the steps as the SMs have places for CTAs, two each.
+    // As many ranges of the steps as the SMs have places for CTAs, two each (in us, with 1, 2,
+    // 4 and 8: 32 rows, 14336 x 4096 33.4, 23.2, 26.8, 33.1; 4096 x 14336 65, 36.5, 28.5, 19.7).
     const int steps = (p.w.K + STEP - 1) / STEP, tiles = (p.w.N + MANY_ROWS - 1) / MANY_ROWS;
     const long long chunks = chunks_of(p.groups, 8 * NT);
     const long long units = (p.groups.offsets ? std::min<long long>(p.groups.M / (8 * NT) + std::min(p.groups.G, p.groups.M), chunks) : chunks) * tiles;

@@ -6,6 +6,10 @@
 // has eight columns, a word of codes; a warp 256 columns of four rows; a CTA 32
 // rows, whose scales (which lie side by side for the rows of a group of columns)
 // pass through shared memory, so that they are stored 64 bytes at a time.
+//
+// 14336 x 4096 bfloat16, groups of 128: 43 us there and 24.5 back, 3.4 and 6.0 TB/s.  On the
+// way there instructions bound it (the range, the quotient and its correction); FP32 pairs in
+// one instruction and ranges in 16 bits took it from 62.
 #include <type_traits>
 
 #include <cuda_bf16.h>
