@@ -564,21 +564,26 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
             }
         }
     } else {
+        // One after the other.
         int last = -1;
         float before = 0.0f;
-        for (int j = 0; sure; ++j) {                 // one after the other, as far as that
+        for (int j = 0; sure && j < p.top; ++j) {
             float now;
             const int e = take_best<V>(key, now);
             if (e < 0) break;
-            const bool apart = !biased || j == 0 || before - now > tol;
-            if (!apart) {
-                const float x = load_any(p.logits, row + e, p.type), y = load_any(p.logits, row + last, p.type);
-                sure = x == y && p.bias[e] == p.bias[last];
-            }
-            if (j >= p.top && apart) break;
-            if (j < p.top && lane == j) mine = e;
+            if (biased && j > 0 && !(before - now > tol))
+                sure = load_any(p.logits, row + e, p.type) == load_any(p.logits, row + last, p.type) && p.bias[e] == p.bias[last];
+            if (lane == j) mine = e;
             before = now;
             last = e;
+        }
+        if (biased && sure && last >= 0) {           // what is left and not apart from the last has to be the same too
+            const float x = load_any(p.logits, row + last, p.type), y = p.bias[last];
+            bool wrong = false;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                wrong = wrong || (key[i] > minus_inf() && !(before - key[i] > tol) && (l[i] != x || of.bias[i] != y));
+            sure = !__any_sync(ALL, wrong);
         }
     }
     if (!sure) mine = choose_exactly<V>(p, row, reinterpret_cast<double *>(scratch + SCRATCH));

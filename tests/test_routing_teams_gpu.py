@@ -120,3 +120,21 @@ def test_equal_choices_beyond_a_teams_room():
         l[[0, 2, 3, 9]] = 0.25
         run_route(l, 8, bias=torch.zeros(E), groups=groups, top_groups=max(groups // 2, 1), group_sum=2)
         run_route(l, 8)
+
+
+@pytest.mark.parametrize("E", [64, 66, 256, 257, 1000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_one_of_many_equal_choices_is_apart(E, score):
+    """... by less than FP32 shows: one that is better comes first, one that is worse
+    is passed over."""
+    l = torch.zeros(9, E)
+    l[4] = logits_of(1, E, "f32", E)
+    for at, by in ((E - 2, 1e-9), (3, 1e-9), (3, -1e-9), (0, -1e-9), (7, -1e-10), (8, 1e-10)):
+        bias = torch.zeros(E)
+        bias[at] = by
+        run_route(l, 8, bias=bias, score=score)
+        if E % 64 == 0:
+            run_route(l, 8, bias=bias, score=score, groups=2, top_groups=1, group_sum=2)
+    bias = torch.zeros(E)
+    bias[::2] = -INF
+    run_route(l, 8, bias=bias, score=score)
