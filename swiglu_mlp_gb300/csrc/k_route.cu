@@ -14,7 +14,7 @@
 //
 // route_team_kernel, up to 256 experts and eight of them: the same by eight lanes for
 // each token.  Instructions bound it, 478 a token against 1412 (16384 tokens, eight of
-// 256 experts by four of eight groups, with the plan: 29 us, 10 of them sorting, against
+// 256 experts by four of eight groups, with the plan: 30 us, 10 of them sorting, against
 // 44; 8192 tokens, two of 16 experts, with the gradient: 12.0 against 14.9; 64 tokens of
 // 64 experts, one CTA: 4.7 against 5.3).  The logits themselves take 2.5 us.
 //

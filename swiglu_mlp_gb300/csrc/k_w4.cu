@@ -5,8 +5,8 @@
 // For few rows the weights' bytes are what the operator cannot do without; the
 // kernel streams them once, and what bounds it is the decoding: seven shifts and masks
 // for eight codes, on a pipe that takes one every two cycles (a row through 14336 rows of
-// 4096: 3.7 us of it, 4.5 of memory, 9.6 in all; 28672 x 4096: 17.3, 3.6 TB/s; 64 rows of 64
-// experts, 2432 x 896: 17.4, of which 6.7 memory).  The rows of
+// 4096: 3.7 us of it, 4.5 of memory, 9.3 in all; 28672 x 4096: 17.3, 3.6 TB/s; 64 rows of 64
+// experts, 2432 x 896: 17.3, of which 6.7 memory).  The rows of
 // W are the 16 rows of an mma.sync m16n8k16 (FP32 accumulators), up to eight rows
 // of A its columns: at one row of A 7/8 of the instruction's work is for nothing,
 // but it is free, and the rows of W arrive in fragments as they lie in memory:
@@ -113,9 +113,10 @@ __host__ __device__ constexpr int scales_bytes(int per, int rows) { return STEP 
 __host__ __device__ constexpr int params_bytes(int per, bool zero, int rows) { return scales_bytes(per, rows) * (zero ? 3 : 2) / 2; }
 __host__ __device__ constexpr int params_pitch(int per, bool zero, int rows) { return (params_bytes(per, zero, rows) + 127) / 128 * 128; }  // (TMA's rule)
 __host__ __device__ constexpr int a_bytes(int tokens) { return STEP * 2 * tokens; }
+__host__ __device__ constexpr int a_pitch(int tokens) { return tokens == 1 ? 1024 : a_bytes(tokens); }   // (whole times 1024)
 __host__ __device__ constexpr int shared_bytes(int per, bool zero, int tokens)
 {
-    return WARPS * STAGES * (CODES + a_bytes(tokens) + params_pitch(per, zero, ROWS)) + 256;
+    return WARPS * STAGES * (CODES + a_pitch(tokens) + params_pitch(per, zero, ROWS)) + 256;
 }
 static_assert(WARPS * STAGES * 8 + 8 <= 256, "barriers and the abort flag");
 
@@ -129,40 +130,48 @@ static_assert(WARPS * STAGES * 8 + 8 <= 256, "barriers and the abort flag");
 // lanes of a row share a scale.
 struct Lane {
     int pi, odd, t;
-    int swap0, swap1, row_at0, row_at1;              // of the first and second row
+    int w0, w1;                                      // where the first and second row's first word is in a box
+    int x[8];                                        // ... and the columns of A of the eight words in a step of them
     uint32_t units, order;                           // (order: of the rows' scales)
 };
 
-template <bool BF16>
-__device__ __forceinline__ Lane lane_of()
+// `row` of A, whose lines are `lines` apart from one 64 columns to the next.  (Steps
+// of A begin at multiples of eight lines: all of this is the same for each.)
+template <bool BF16, int PER>
+__device__ __forceinline__ Lane lane_of(int row, int lines)
 {
     Lane l;
     const int lane = threadIdx.x & 31, quad = lane >> 2;
     l.t = lane & 3;
     l.pi = (quad & 4) | (quad & 1) << 1 | (quad >> 1 & 1);
     l.odd = quad >> 2;
-    l.swap0 = (2 * l.pi + l.odd) & 7;
-    l.swap1 = (2 * l.pi + 1 - l.odd) & 7;
-    l.row_at0 = (2 * l.pi + l.odd) * (STEP / 2);
-    l.row_at1 = (2 * l.pi + 1 - l.odd) * (STEP / 2);
+    const int row0 = 2 * l.pi + l.odd, row1 = 2 * l.pi + 1 - l.odd;
+    const int piece = PER == 4 ? l.t : PER == 2 ? l.t >> 1 : 0, within = PER == 4 ? 0 : PER == 2 ? (l.t & 1) * 8 : l.t * 4;
+    l.w0 = row0 * (STEP / 2) + ((piece ^ row0) & 7) * 16 + within;
+    l.w1 = row1 * (STEP / 2) + ((piece ^ row1) & 7) * 16 + within;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int c = i / PER * (4 * PER) + PER * l.t + i % PER;     // columns in units of 8: block of 64, piece of it
+        const int line = (c >> 3) * lines + row;
+        l.x[i] = line * 128 + ((c ^ line) & 7) * 16;
+    }
     asm volatile("mov.b32 %0, %1;" : "=r"(l.units) : "n"(UNITS<BF16>));
     l.order = l.odd ? 0x1032u : 0x3210u;
     return l;
 }
 
-// acc += the products of a step: codes and params as TMA left them; rows of A in lines
-// of 128 bytes (64 columns) of shared memory, `lines` for each 64 columns, this lane's of
-// NT rows of A 8 apart from x_line on; MT pieces of 16 rows of W, from `piece` of the
+// acc += the products of a step: codes and params as TMA left them, and rows of A in
+// lines of 128 bytes, at these offsets of shared memory (codes 128, A 1024 bytes
+// aligned); NT tiles of eight rows of A; MT pieces of 16 rows of W, from `piece` of the
 // slot's box of BOX rows on.  whole: the second half has columns too.
 template <bool BF16, int PER, bool ZERO, int BOX, int NT>
-__device__ __forceinline__ void multiply(const Lane &l, const unsigned char *shared, const unsigned char *codes,
-                                         const unsigned char *params, int x_line, int lines, bool whole,
+__device__ __forceinline__ void multiply(const Lane &l, const unsigned char *shared, int codes, int params, int a, bool whole,
                                          int piece, float (&acc)[MT][NT][4])
 {
-    const uint32_t *scale = reinterpret_cast<const uint32_t *>(params) + piece * 8 + l.pi;
-    const uint16_t *zero = reinterpret_cast<const uint16_t *>(params + scales_bytes(PER, BOX)) + piece * 8 + l.pi;
+    const uint32_t *scale = reinterpret_cast<const uint32_t *>(shared + params) + piece * 8 + l.pi;
+    const uint16_t *zero = reinterpret_cast<const uint16_t *>(shared + params + scales_bytes(PER, BOX)) + piece * 8 + l.pi;
     const uint32_t scale0 = l.odd ? 0x3244u : 0x1044u, scale1 = l.odd ? 0x1044u : 0x3244u;
-    const int t = l.t;
+    const int w0 = codes + piece * 16 * (STEP / 2) + l.w0, w1 = codes + piece * 16 * (STEP / 2) + l.w1;
     float part[MT][NT][4];
     uint32_t z0[MT], z1[MT];
 #pragma unroll
@@ -171,32 +180,28 @@ __device__ __forceinline__ void multiply(const Lane &l, const unsigned char *sha
         uint32_t w[2 * MT][4];                       // both rows of each 16
 #pragma unroll
         for (int r = 0; r < 2 * MT; ++r) {
-            const unsigned char *at = codes + (r % 2 ? l.row_at1 : l.row_at0) + (piece + r / 2) * 16 * (STEP / 2);
-            const int swap = r % 2 ? l.swap1 : l.swap0;
+            // (a 16-byte piece further is one bit of the address turned over)
+            const unsigned char *const at = shared + r / 2 * 16 * (STEP / 2);
+            const int w_at = r % 2 ? w1 : w0;
             if (PER == 4) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(at + ((4 * half + t) ^ swap) * 16);
+                const uint4 v = *reinterpret_cast<const uint4 *>(at + (w_at ^ (half * 64)));
                 w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
             } else if (PER == 2) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(at + ((4 * half + 2 * h + (t >> 1)) ^ swap) * 16 + (t & 1) * 8);
+                    const uint2 v = *reinterpret_cast<const uint2 *>(at + (w_at ^ (half * 64 + h * 32)));
                     w[r][2 * h] = v.x, w[r][2 * h + 1] = v.y;
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[r][j] = *reinterpret_cast<const uint32_t *>(at + ((4 * half + j) ^ swap) * 16 + t * 4);
+                for (int j = 0; j < 4; ++j) w[r][j] = *reinterpret_cast<const uint32_t *>(at + (w_at ^ (half * 64 + j * 16)));
             }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            // columns in units of 8: block of 64, piece of it
-            const int c = (4 * half + j) / PER * (4 * PER) + PER * t + j % PER;
             uint4 x[NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int line = (c >> 3) * lines + x_line + 8 * n;
-                x[n] = *reinterpret_cast<const uint4 *>(shared + line * 128 + ((c ^ line) & 7) * 16);
-            }
+            for (int n = 0; n < NT; ++n) x[n] = *reinterpret_cast<const uint4 *>(shared + n * 1024 + (a + l.x[4 * half + j]));
             const int b = (4 * half + j) / PER;      // the scale's place among the step's
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -277,10 +282,9 @@ __global__ void __launch_bounds__(32 * WARPS, 4)
     extern __shared__ __align__(1024) unsigned char shared[];
     constexpr int BLOCKS = STEP / (32 * PER), PARAMS = params_pitch(PER, ZERO, ROWS);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wk = warp & (team - 1), quad = lane >> 2;
-    const int of_a = a_bytes(tokens);
-    unsigned char *const codes = shared + warp * STAGES * CODES;
-    unsigned char *const a = shared + WARPS * STAGES * CODES + warp * STAGES * of_a;
-    unsigned char *const params = shared + WARPS * STAGES * (CODES + of_a) + warp * STAGES * PARAMS;
+    const int of_a = a_pitch(tokens);
+    const int codes = warp * STAGES * CODES, a = WARPS * STAGES * CODES + warp * STAGES * of_a;
+    const int params = WARPS * STAGES * (CODES + of_a) + warp * STAGES * PARAMS;
     unsigned char *const at_bars = shared + WARPS * STAGES * (CODES + of_a + PARAMS);
     const uint32_t bars = smem_u32(at_bars) + warp * STAGES * 8;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(at_bars + WARPS * STAGES * 8);
@@ -301,21 +305,20 @@ __global__ void __launch_bounds__(32 * WARPS, 4)
     auto load = [&](int step, int slot) {            // by the first four lanes
         const uint32_t bar = bars + 8 * slot;
         if (lane == 0) {
-            const uint32_t to = smem_u32(params) + slot * PARAMS;
+            const uint32_t to = smem_u32(shared) + params + slot * PARAMS;
             mbar_arrive_expect_tx(bar, CODES + params_bytes(PER, ZERO, ROWS) + a_bytes(tokens));
-            tma_load_3d_cta(smem_u32(codes) + slot * CODES, &maps.q, bar, step * (STEP / 2), n0, g);
+            tma_load_3d_cta(smem_u32(shared) + codes + slot * CODES, &maps.q, bar, step * (STEP / 2), n0, g);
             tma_load_3d_cta(to, &maps.s, bar, n0, step * BLOCKS, g);
             if (ZERO) tma_load_3d_cta(to + scales_bytes(PER, ROWS), &maps.z, bar, n0, step * BLOCKS, g);
         }
-        if (lane < 4) tma_load_2d(smem_u32(a) + slot * of_a + lane * tokens * 128, &maps.a, bar, step * STEP + lane * 64, row0);
+        if (lane < 4) tma_load_2d(smem_u32(shared) + a + slot * of_a + lane * tokens * 128, &maps.a, bar, step * STEP + lane * 64, row0);
     };
 #pragma unroll 1
     for (int i = 0; i < STAGES; ++i)
         if (wk + i * team < steps) load(wk + i * team, i);
 
-    const Lane l = lane_of<BF16>();
     // (lanes of rows of A that do not exist compute with another, for nothing)
-    const int x_line = (int)(a - shared) / 128 + min(quad, tokens - 1);
+    const Lane l = lane_of<BF16, PER>(min(quad, tokens - 1), tokens);
     float acc[MT][1][4] = {};
     bool stopped = false;
     int step = wk, slot = 0;
@@ -325,8 +328,8 @@ __global__ void __launch_bounds__(32 * WARPS, 4)
             stopped = true;
             break;
         }
-        multiply<BF16, PER, ZERO, ROWS, 1>(l, shared, codes + slot * CODES, params + slot * PARAMS, x_line + slot * of_a / 128, tokens,
-                                     step * STEP + STEP / 2 < p.w.K, 0, acc);
+        multiply<BF16, PER, ZERO, ROWS, 1>(l, shared, codes + slot * CODES, params + slot * PARAMS, a + slot * of_a,
+                                           step * STEP + STEP / 2 < p.w.K, 0, acc);
         __syncwarp();
         if (step + STAGES * team < steps) load(step + STAGES * team, slot);
         slot = slot + 1 == STAGES ? 0 : slot + 1;
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(32 * WARPS, 4)
 // fill an SM, and the CTAs of a cluster that have a tile's ranges add their sums
 // through shared memory, in order.  (One CTA of 256 rows for each SM: 41 us, since only
 // 15 clusters of eight of that size are resident, and 35.9 with clusters of four; this
-// 20.4; chunks of eight rows of the other kernel 31.4.)
+// 19.7; chunks of eight rows of the other kernel 31.4.)
 constexpr int MANY_ROWS = WARPS * ROWS, MANY_BOX = 64, MANY_BOXES = MANY_ROWS / MANY_BOX;
 constexpr int MANY_CODES = MANY_BOX * STEP / 2;
 constexpr int MANY_THREADS = 32 * (WARPS + 1);
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 2)
     const int steps = (p.w.K + STEP - 1) / STEP, first = (int)((long long)steps * range / ranges);
     const int count = (int)((long long)steps * (range + 1) / ranges) - first;
     float acc[MT][NT][4] = {};
-    const Lane l = lane_of<BF16>();
+    const Lane l = lane_of<BF16, PER>(lane >> 2, TOKENS_MANY);
     if (warp == WARPS) {
         if (lane == 0) {
             int i = 0;
@@ -465,9 +468,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 2)
         for (int i = 0; i < count; ++i) {
             const int slot = i % MANY_STAGES;
             if (!__all_sync(0xffffffffu, wait_bounded(full + 8 * slot, (uint32_t)(i / MANY_STAGES) & 1u, abort_flag, err))) break;
-            multiply<BF16, PER, ZERO, MANY_BOX, NT>(l, shared, shared + (slot * MANY_BOXES + box) * MANY_CODES,
-                                                    shared + P + (slot * MANY_BOXES + box) * PARAMS, (A + slot * a_bytes(TOKENS_MANY)) / 128 + (lane >> 2), TOKENS_MANY,
-                                                    (first + i) * STEP + STEP / 2 < p.w.K, warp * MT % (MANY_BOX / 16), acc);
+            multiply<BF16, PER, ZERO, MANY_BOX, NT>(l, shared, (slot * MANY_BOXES + box) * MANY_CODES, P + (slot * MANY_BOXES + box) * PARAMS,
+                                                    A + slot * a_bytes(TOKENS_MANY), (first + i) * STEP + STEP / 2 < p.w.K,
+                                                    warp * MT % (MANY_BOX / 16), acc);
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + 8 * slot);
         }
@@ -524,13 +527,14 @@ Shape shape_of(const W4Args &p, int sms)
     const Groups &g = p.groups;
     const int steps = (p.w.K + STEP - 1) / STEP;
     const long long items = (p.w.N + ROWS - 1ll) / ROWS;
-    // Groups: chunks of four times their mean, since another chunk reads and decodes the
-    // weights again (64 rows of 64 experts: 21.5 with chunks of 1, 17.9 with 2, 17.4 with
-    // 4 and 8), of few rows of as many (4 rows, 8 experts of 8192 x 2048: 10.5 with 2, 7.7).  More than eight rows from a mean of 16 on, where the fuller
-    // instructions outweigh the emptier chunks (16 experts of 4096 x 1024: means of 8
-    // 24.1 and 19.3, 16 26.7 and 28.8, 32 38.7 and 46.3).
+    // Groups: chunks of four times their mean and four rows at least, since another chunk
+    // reads and decodes the weights again (64 rows of 64 experts: 21.5 with chunks of 1, 17.9
+    // with 2, 17.4 with 4 and 8; 4 rows, 8 experts of 8192 x 2048: 10.5 with 2, 7.7 with 4; 8
+    // rows, 16 experts of 4096 x 1024: 7.4 with 2, 8.0 with 4, 9.2 with 8).  More than eight
+    // rows from a mean of 16 on, where the fuller instructions outweigh the emptier chunks (16
+    // experts of 4096 x 1024: means of 8 24.1 and 19.3, 16 26.7 and 28.8, 32 38.7 and 46.3).
     if (g.offsets != nullptr && g.M >= 16ll * g.G) return {32, true};
-    const int want = g.offsets == nullptr || g.M <= TOKENS ? g.M : (int)std::min<long long>(g.M, (4ll * g.M + g.G - 1) / g.G);
+    const int want = g.offsets == nullptr ? g.M : (int)std::min<long long>(g.M, std::max(4ll, (4ll * g.M + g.G - 1) / g.G));
     // More than eight rows (4096 x 14336, 32 rows: 19.6 and 36.1; 14336 x 4096, 9 rows: 15.5
     // and 19.1), unless there is too little to do for a cluster's barriers (4096 x 4096, 16
     // rows: 8.5 and 7.4; 8192 x 1024, 16 rows: 5.7 both).
