@@ -89,20 +89,6 @@ __device__ __forceinline__ void tc_mma_f4_pair(uint32_t d_tmem, uint64_t adesc, 
             : "memory");
 }
 
-// True in one lane of the (converged) warp, the same one every time.  The
-// warps that issue MMAs stay converged and elect a lane only around the
-// tcgen05 instructions, so that descriptors and loop state are uniform.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t one;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(one));
-    return one != 0;
-}
-
 // wait_bounded by every lane of a converged warp.
 __device__ __forceinline__ bool wait_bounded_warp(uint32_t bar, uint32_t parity,
                                                   volatile int *abort_flag, int *err)

@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(32 * WARPS, 4)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) unsigned char shared[];
     constexpr int BLOCKS = STEP / (32 * PER), PARAMS = params_pitch(PER, ZERO, ROWS);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wk = warp & (team - 1), quad = lane >> 2;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);     // (known to be the same in all lanes)
+    const int wk = warp & (team - 1), quad = lane >> 2;
     const int of_a = a_pitch(tokens);
     const int codes = warp * STAGES * CODES, a = WARPS * STAGES * CODES + warp * STAGES * of_a;
     const int params = WARPS * STAGES * (CODES + of_a) + warp * STAGES * PARAMS;
@@ -302,16 +303,17 @@ __global__ void __launch_bounds__(32 * WARPS, 4)
     if (!find_chunk(p.groups, tokens, chunk, err, g, row0, rows)) return;
 
     const int steps = n0 < p.w.N ? (p.w.K + STEP - 1) / STEP : 0;
-    auto load = [&](int step, int slot) {            // by the first four lanes
-        const uint32_t bar = bars + 8 * slot;
-        if (lane == 0) {
-            const uint32_t to = smem_u32(shared) + params + slot * PARAMS;
+    auto load = [&](int step, int slot) {            // by one lane
+        if (elect_one()) {
+            const uint32_t bar = bars + 8 * slot, to = smem_u32(shared) + params + slot * PARAMS;
             mbar_arrive_expect_tx(bar, CODES + params_bytes(PER, ZERO, ROWS) + a_bytes(tokens));
             tma_load_3d_cta(smem_u32(shared) + codes + slot * CODES, &maps.q, bar, step * (STEP / 2), n0, g);
             tma_load_3d_cta(to, &maps.s, bar, n0, step * BLOCKS, g);
             if (ZERO) tma_load_3d_cta(to + scales_bytes(PER, ROWS), &maps.z, bar, n0, step * BLOCKS, g);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                tma_load_2d(smem_u32(shared) + a + slot * of_a + c * tokens * 128, &maps.a, bar, step * STEP + c * 64, row0);
         }
-        if (lane < 4) tma_load_2d(smem_u32(shared) + a + slot * of_a + lane * tokens * 128, &maps.a, bar, step * STEP + lane * 64, row0);
     };
 #pragma unroll 1
     for (int i = 0; i < STAGES; ++i)

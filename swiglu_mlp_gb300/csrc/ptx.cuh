@@ -400,6 +400,20 @@ __device__ __forceinline__ void st_dsmem_v4(uint32_t cluster_addr, uint32_t a, u
                  : "memory");
 }
 
+// True in one lane of the (converged) warp, the same one every time.  The
+// warps that issue MMAs stay converged and elect a lane only around the
+// tcgen05 instructions, so that descriptors and loop state are uniform.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 // Every thread of every CTA in the cluster arrives, then waits for all.
 __device__ __forceinline__ void cluster_sync_all()
 {
