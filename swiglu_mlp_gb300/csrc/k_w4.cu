@@ -5,8 +5,8 @@
 // For few rows the weights' bytes are what the operator cannot do without; the
 // kernel streams them once, and what bounds it is the decoding: seven shifts and masks
 // for eight codes, on a pipe that takes one every two cycles (a row through 14336 rows of
-// 4096: 3.7 us of it, 4.5 of memory, 9.3 in all; 28672 x 4096: 17.3, 3.6 TB/s; 64 rows of 64
-// experts, 2432 x 896: 17.3, of which 6.7 memory).  The rows of
+// 4096: 3.7 us of it, 4.5 of memory, 8.9 in all; 28672 x 4096: 16.0, 3.9 TB/s; 64 rows of 64
+// experts, 2432 x 896: 15.8, of which 6.7 memory).  The rows of
 // W are the 16 rows of an mma.sync m16n8k16 (FP32 accumulators), up to eight rows
 // of A its columns: at one row of A 7/8 of the instruction's work is for nothing,
 // but it is free, and the rows of W arrive in fragments as they lie in memory:
@@ -20,9 +20,10 @@
 // w4_kernel: a CTA has one chunk of at most eight rows of A; its four warps are teams of
 // `team` along K, and each team has 32 rows of W (64: a third fewer warps fit, 20.3 us
 // instead of 17.4 for the experts above).  A team's warps take steps of 256
-// columns in turn.  Each warp has a ring of its own that TMA fills: a lane asks
-// for a step's codes (32 rows of 128 bytes), scales, zero points and columns of A
-// with an instruction or four each, which leaves the issue slots to the decoding;
+// columns in turn.  Each warp has a ring of its own that TMA fills: an elected lane asks
+// for a step's codes (32 rows of 128 bytes), scales, zero points and columns of A, all from
+// values that the warp shares (addresses of its lanes' own took a loop over the lanes, a
+// seventh of all instructions), which leaves the issue slots to the decoding;
 // cp.async by all lanes, with its addresses and edges, took as many instructions
 // again.  A team's sums are added at the end, in order.  w4_many_kernel, for more
 // rows or where there are too few rows of W, stands below it.
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(32 * WARPS, 4)
 // fill an SM, and the CTAs of a cluster that have a tile's ranges add their sums
 // through shared memory, in order.  (One CTA of 256 rows for each SM: 41 us, since only
 // 15 clusters of eight of that size are resident, and 35.9 with clusters of four; this
-// 19.7; chunks of eight rows of the other kernel 31.4.)
+// 19.0; chunks of eight rows of the other kernel 29.9.)
 constexpr int MANY_ROWS = WARPS * ROWS, MANY_BOX = 64, MANY_BOXES = MANY_ROWS / MANY_BOX;
 constexpr int MANY_CODES = MANY_BOX * STEP / 2;
 constexpr int MANY_THREADS = 32 * (WARPS + 1);
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 2)
     extern __shared__ __align__(1024) unsigned char shared[];
     constexpr int BLOCKS = STEP / (32 * PER), PARAMS = params_pitch(PER, ZERO, MANY_BOX), TOKENS_MANY = 8 * NT;
     constexpr int A = MANY_STAGES * MANY_BOXES * MANY_CODES, P = A + MANY_STAGES * a_bytes(TOKENS_MANY), B = P + MANY_STAGES * MANY_BOXES * PARAMS;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const uint32_t full = smem_u32(shared) + B, empty = full + 8 * MANY_STAGES;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(shared + B + 16 * MANY_STAGES);
     // (a cluster's CTAs, the ranges of a tile, follow one another)
@@ -444,12 +445,14 @@ __global__ void __launch_bounds__(MANY_THREADS, 2)
     float acc[MT][NT][4] = {};
     const Lane l = lane_of<BF16, PER>(lane >> 2, TOKENS_MANY);
     if (warp == WARPS) {
-        if (lane == 0) {
-            int i = 0;
-            for (; i < count; ++i) {
-                const int slot = i % MANY_STAGES, step = first + i;
-                const uint32_t bar = full + 8 * slot;
-                if (i >= MANY_STAGES && !wait_bounded(empty + 8 * slot, (uint32_t)((i / MANY_STAGES) - 1) & 1u, abort_flag, err)) break;
+        int i = 0;
+        for (; i < count; ++i) {
+            const int slot = i % MANY_STAGES, step = first + i;
+            const uint32_t bar = full + 8 * slot;
+            if (i >= MANY_STAGES &&
+                !__all_sync(0xffffffffu, wait_bounded(empty + 8 * slot, (uint32_t)((i / MANY_STAGES) - 1) & 1u, abort_flag, err)))
+                break;
+            if (elect_one()) {
                 mbar_arrive_expect_tx(bar, boxes * (MANY_CODES + params_bytes(PER, ZERO, MANY_BOX)) + a_bytes(TOKENS_MANY));
                 for (int w = 0; w < boxes; ++w) {
                     const uint32_t to = smem_u32(shared) + P + (slot * MANY_BOXES + w) * PARAMS;
@@ -460,10 +463,11 @@ __global__ void __launch_bounds__(MANY_THREADS, 2)
                 for (int c = 0; c < 4; ++c)
                     tma_load_2d(smem_u32(shared) + A + slot * a_bytes(TOKENS_MANY) + c * TOKENS_MANY * 128, &maps.a, bar, step * STEP + c * 64, row0);
             }
-            // (all that is on its way lands before the sums take its place, after a wait that ran out too)
-            for (int j = max(i - MANY_STAGES, 0); j < i; ++j)
-                wait_bounded(full + 8 * (j % MANY_STAGES), (uint32_t)(j / MANY_STAGES) & 1u, abort_flag, err, false, DRAIN_LIMIT_NS);
+            __syncwarp();
         }
+        // (all that is on its way lands before the sums take its place, after a wait that ran out too)
+        for (int j = max(i - MANY_STAGES, 0); j < i; ++j)
+            wait_bounded(full + 8 * (j % MANY_STAGES), (uint32_t)(j / MANY_STAGES) & 1u, abort_flag, err, false, DRAIN_LIMIT_NS);
         __syncwarp();
     } else if (warp < used) {
         const int box = warp / (WARPS / MANY_BOXES);
@@ -523,7 +527,9 @@ struct Shape {
     bool many;                                       // of w4_many_kernel
 };
 
-// (times in us, bfloat16, group 128 with zero points)
+// (Times in us, bfloat16, groups of 128 with zero points, each of the same build on both
+// sides; of groups and teams as they were when one lane asked for a step's codes and four for A,
+// which cost a tenth.)
 Shape shape_of(const W4Args &p, int sms)
 {
     const Groups &g = p.groups;
@@ -537,15 +543,15 @@ Shape shape_of(const W4Args &p, int sms)
     // experts of 4096 x 1024: means of 8 24.1 and 19.3, 16 26.7 and 28.8, 32 38.7 and 46.3).
     if (g.offsets != nullptr && g.M >= 16ll * g.G) return {32, true};
     const int want = g.offsets == nullptr ? g.M : (int)std::min<long long>(g.M, std::max(4ll, (4ll * g.M + g.G - 1) / g.G));
-    // More than eight rows (4096 x 14336, 32 rows: 19.6 and 36.1; 14336 x 4096, 9 rows: 15.5
-    // and 19.1), unless there is too little to do for a cluster's barriers (4096 x 4096, 16
-    // rows: 8.5 and 7.4; 8192 x 1024, 16 rows: 5.7 both).
-    if (g.offsets == nullptr && want > TOKENS && (steps >= 24 || (want + TOKENS - 1) / TOKENS * items * steps > 28ll * sms))
+    // More than eight rows (4096 x 14336, 32 rows: 19.0 and 29.2; 14336 x 4096, 9 rows: 14.9
+    // and 18.4), unless there is too little to do for a cluster's barriers (2048 x 8192, 16
+    // rows: 9.0 and 7.4; 8192 x 1024, 16 rows: 5.2 both).
+    if (g.offsets == nullptr && want > TOKENS && (want + TOKENS - 1) / TOKENS * items * steps > 28ll * sms)
         return {want <= 16 ? 16 : 32, true};
-    // Up to eight, where rows are long and teams of four do not fill the GPU: a cluster has
-    // up to 32 warps for a tile (one row, 1024 x 8192: 6.4 and 9.2; 2048 x 8192: 7.9 and 9.2;
-    // 4096 x 14336: 14.9 and 15.2; but 4096 x 6144 8.3 and 7.4).
-    if (steps > 24 && (g.offsets == nullptr ? 1 : std::min(g.G, g.M)) * items < sms) return {TOKENS, true};
+    // Up to eight, where rows are long and few: a cluster has up to 32 warps for a tile, a
+    // team four (one row, 1024 x 8192: 5.7 and 7.4; 2048 x 8192: 7.4 both; but 4096 x 14336
+    // 14.2 and 12.2).
+    if (steps > 24 && (g.offsets == nullptr ? 1 : std::min(g.G, g.M)) * items * 2 < sms) return {TOKENS, true};
     return {want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : TOKENS, false};
 }
 

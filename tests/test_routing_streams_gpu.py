@@ -60,7 +60,7 @@ def test_threads_with_plans(shared):
         assert swg.get_device_error(stream) == 0
 
 
-@pytest.mark.parametrize("M,N,K", [(5, 300, 704), (5, 200, 8200), (40, 200, 6200), (12, 300, 904)])
+@pytest.mark.parametrize("M,N,K", [(5, 300, 704), (5, 200, 8200), (40, 200, 6200), (12, 300, 904), (16, 2100, 8704)])
 def test_products_in_two_graphs_at_once(M, N, K):
     """Each form of the product captured, and replayed beside another with new rows."""
     W, w = weight(1, N, K, 64, True, "bf16", 3)

@@ -200,6 +200,13 @@ def test_many_rows_and_columns(M, N):
     run_gemm([M], N, 2100, 64, True, "f16", seed=M, dense=True, alpha=0.5, beta=1.0)
 
 
+@pytest.mark.parametrize("M,N,K,group", [(9, 2100, 9000, 32), (16, 2303, 8200, 128), (31, 1100, 8200, 64), (32, 1057, 9001, 32),
+                                         (40, 1000, 9000, 128), (70, 520, 8500, 64)])
+@pytest.mark.parametrize("zero,stype", [(False, "bf16"), (True, "f16")])
+def test_many_rows_of_large_weights(M, N, K, group, zero, stype):
+    run_gemm([M], N, K, group, zero, stype, "f32", seed=N, dense=True)
+
+
 @pytest.mark.parametrize("rows", [[16], [60, 0, 7, 1, 0, 33], [0, 0, 0, 70], [32, 64, 31], [17] * 20])
 @pytest.mark.parametrize("N,K,group,zero", [(72, 100, 32, True), (130, 700, 64, False), (8, 2100, 128, True)])
 @pytest.mark.parametrize("stype", ["bf16", "f16"])
