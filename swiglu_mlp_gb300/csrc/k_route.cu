@@ -581,8 +581,11 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
             const float x = load_any(p.logits, row + last, p.type), y = p.bias[last];
             bool wrong = false;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                wrong = wrong || (key[i] > minus_inf() && !(before - key[i] > tol) && (l[i] != x || of.bias[i] != y));
+            for (int i = 0; i < V; ++i) {
+                const int e = lane + 32 * i;         // (read again: this is seldom run)
+                if (key[i] > minus_inf() && !(before - key[i] > tol))
+                    wrong = wrong || load_any(p.logits, row + e, p.type) != x || p.bias[e] != y;
+            }
             sure = !__any_sync(ALL, wrong);
         }
     }
