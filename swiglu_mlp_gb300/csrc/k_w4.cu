@@ -540,7 +540,7 @@ Shape shape_of(const W4Args &p, int sms)
     // with 2, 17.4 with 4 and 8; 4 rows, 8 experts of 8192 x 2048: 10.5 with 2, 7.7 with 4; 8
     // rows, 16 experts of 4096 x 1024: 7.4 with 2, 8.0 with 4, 9.2 with 8).  More than eight
     // rows from a mean of 16 on, where the fuller instructions outweigh the emptier chunks (16
-    // experts of 4096 x 1024: means of 8 24.1 and 19.3, 16 26.7 and 28.8, 32 38.7 and 46.3).
+    // experts of 4096 x 1024: means of 8 23.6 and 17.5, 16 26.3 and 27.0, 32 37.7 and 44.7).
     if (g.offsets != nullptr && g.M >= 16ll * g.G) return {32, true};
     const int want = g.offsets == nullptr ? g.M : (int)std::min<long long>(g.M, std::max(4ll, (4ll * g.M + g.G - 1) / g.G));
     // More than eight rows (4096 x 14336, 32 rows: 19.0 and 29.2; 14336 x 4096, 9 rows: 14.9
@@ -601,7 +601,9 @@ cudaError_t launch_many(const W4Args &p, const W4Maps &maps, int sms, int *err, 
     // 4 and 8: 32 rows, 14336 x 4096 33.4, 23.2, 26.8, 33.1; 4096 x 14336 65, 36.5, 28.5, 19.7).
     const int steps = (p.w.K + STEP - 1) / STEP, tiles = (p.w.N + MANY_ROWS - 1) / MANY_ROWS;
     const long long chunks = chunks_of(p.groups, 8 * NT);
-    const long long units = (p.groups.offsets ? std::min<long long>(p.groups.M / (8 * NT) + std::min(p.groups.G, p.groups.M), chunks) : chunks) * tiles;
+    // (of groups half a chunk more for each than their rows fill: 64 rows of 4 experts of 4096 x
+    // 4096 21.4 in two ranges, 30.4 in one)
+    const long long units = (p.groups.offsets ? p.groups.M / (8 * NT) + (std::min(p.groups.G, p.groups.M) + 1) / 2 : chunks) * tiles;
     int ranges = 1;
     while (ranges < MOST_RANGES && 2 * ranges <= steps && ranges * units <= sms) ranges *= 2;
     auto kernel = w4_many_kernel<BF16, PER, ZERO, NT>;
