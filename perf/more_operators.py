@@ -224,8 +224,7 @@ def prepare(case, seed):
         s["experts"] = torch.empty((T, top), dtype=torch.int32, device="cuda")
         s["weights"] = torch.empty((T, top), dtype=torch.float32, device="cuda")
         s["plan"] = room_for_plan(T, E, top)
-        s["rows"], s["Y"] = (torch.zeros((T * top, d), dtype=t, device="cuda") for d in (D, H))
-        s["Z"] = torch.zeros((T * top, D), dtype=torch.float32, device="cuda")   # summed before it is rounded
+        s["rows"], s["Y"], s["Z"] = (torch.zeros((T * top, d), dtype=t, device="cuda") for d in (D, H, D))
         s["out"] = torch.zeros((T, D), dtype=t, device="cuda")
     return s
 
