@@ -28,6 +28,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "chunks.h"
 #include "groups.cuh"
 #include "launch.h"
 #include "routing.h"
@@ -639,8 +640,8 @@ __device__ void rank_slots(const int32_t *experts, int lo, int hi, int slots, in
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ranking = rank_warps(E, NT / 32);
     int *sums = room, *start = room + 64;            // start[w][e]: the next place of warp w's slots of e
-    const int per = ((hi - lo + ranking - 1) / ranking + 31) & ~31;
-    const int from = min(lo + warp * per, hi), to = warp < ranking ? min(from + per, hi) : from;
+    int from, to;
+    slots_of_warp(lo, hi, ranking, warp, from, to);
     // (the first slots of each lane, which are all there are of most chunks, are asked for once)
     const int early = from + lane < to ? experts[from + lane] : -1;
     for (int i = tid; i < ranking * E; i += NT) start[i] = 0;
@@ -692,7 +693,9 @@ __device__ void rank_slots(const int32_t *experts, int lo, int hi, int slots, in
         if (slot < to) plan.position[slot] = place;
         if (on) plan.source[place] = slot;
     }
-    for (int r = carried + blockIdx.x * NT + tid; r < slots; r += gridDim.x * NT) plan.source[r] = -1;
+    int64_t first, step;
+    behind_rows(carried, blockIdx.x, gridDim.x, NT, tid, first, step);
+    for (int64_t r = first; r < slots; r += step) plan.source[r] = -1;
 }
 
 // The tokens of chunk c of n.
