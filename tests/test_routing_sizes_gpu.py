@@ -1,4 +1,4 @@
-"""Plans of as many slots as the entry points accept."""
+"""Tokens and slots as many as the entry points accept."""
 import pytest
 import torch
 
@@ -44,3 +44,22 @@ def test_sort_of_the_most_slots(none):
     assert offsets.tolist() == [0, half, half, rows]
     assert counts_up(source, 0, rows) and counts_up(position.view(-1), 0, rows)
     assert bool((source[rows:] == -1).all()) and bool((position.view(-1)[rows:] == -1).all())
+
+
+@pytest.mark.parametrize("E", [4, 3])                    # four tokens of a warp, and one
+def test_route_of_the_most_tokens(E):
+    """Token t's best expert is t % E, but for the last one, which has none."""
+    room(60)
+    T = MOST
+    logits = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+    for e in range(E):
+        logits[e::E, e] = 1.0
+    logits[T - 1] = -float("inf")
+    experts = torch.full((T, 1), 77, dtype=torch.int32, device="cuda")
+    weights = torch.full((T, 1), 7.0, device="cuda")
+    swg.expert_route_into(experts, weights, logits)
+    assert swg.get_device_error() == 0
+    for e in range(E):
+        assert bool((experts[e:T - 1:E] == e).all())
+    assert experts[-1].item() == -1 and weights[-1].item() == 0
+    assert bool((weights[:-1] == 1).all())

@@ -1,5 +1,5 @@
-"""How the kernels of a plan share out its slots (csrc/chunks.h), compiled for the host, up
-to the largest sizes that the entry points accept."""
+"""How the router's kernels share out tokens and slots (csrc/chunks.h), compiled for the
+host, up to the largest sizes that the entry points accept."""
 import ctypes
 import os
 import subprocess
@@ -12,11 +12,12 @@ from swiglu_mlp_gb300 import build as swg_build
 MOST = 2 ** 31 - 1024                                    # slots
 SOURCE = r"""
 #include "chunks.h"
+extern "C" void chunk_of(int T, int n, int c, int *out) { swg::chunk_of(T, n, c, out[0], out[1]); }
 extern "C" void slots_of_warp(int lo, int hi, int ranking, int warp, int *out)
 {
     swg::slots_of_warp(lo, hi, ranking, warp, out[0], out[1]);
 }
-extern "C" void behind_rows(int rows, int cta, int ctas, int threads, int tid, int64_t *out)
+extern "C" void behind_rows(int rows, int cta, int ctas, int threads, int tid, uint32_t *out)
 {
     swg::behind_rows(rows, cta, ctas, threads, tid, out[0], out[1]);
 }
@@ -62,9 +63,23 @@ def test_places_behind_the_last_row(host, ctas, threads, slots):
         met = np.zeros(slots - rows, int)
         for cta in range(ctas):
             for tid in range(threads) if ctas == 1 else (0, 1, threads - 1):
-                first, by = two(host.behind_rows, rows, cta, ctas, threads, tid, kind=ctypes.c_int64)
+                first, by = two(host.behind_rows, rows, cta, ctas, threads, tid, kind=ctypes.c_uint32)
                 assert by == step and first == rows + cta * threads + tid
                 met[first - rows::by] += 1
         assert (met <= 1).all()
         if ctas == 1:
             assert (met == 1).all()
+
+
+@pytest.mark.parametrize("T", [0, 1, 7, 8, 9, 63, 64, 65, 5003, 2 ** 30, 1908874354, MOST - 7, MOST])
+@pytest.mark.parametrize("per", [8, 64, None])
+def test_chunks_share_the_tokens(host, T, per):
+    """A CTA for every 8 or 64 tokens, or 152 of a plan."""
+    n = 152 if per is None else max(-(-T // per), 1)
+    for first, last in ((0, min(n, 300)), (max(n - 300, 0), n)):
+        at = min(first * -(-T // n), T)
+        for c in range(first, last):
+            a, b = two(host.chunk_of, T, n, c)
+            assert a == at and a <= b <= T and b - a <= -(-T // n)
+            at = b
+    assert at == T
