@@ -221,11 +221,11 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &p, long long row, do
         z += e;
         c[i] = softmax ? e : 1.0 / (1.0 + e);
     }
-    const double inverse = softmax ? 1.0 / warp_sum(z) : 1.0;
+    const double sum = softmax ? warp_sum(z) : 1.0;
 #pragma unroll TOGETHER
     for (int i = 0; i < V; ++i) {
         const int e = lane + 32 * i;
-        c[i] *= inverse;
+        if (softmax) c[i] /= sum;                    // (as in exact_choice: both round alike)
         if (p.bias != nullptr && e < p.E) c[i] += (double)p.bias[e];
         if (c[i] == low) masked |= 1u << i;
         // (without a bias the order is that of the logits, groups apart)
