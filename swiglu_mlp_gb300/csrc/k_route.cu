@@ -95,6 +95,16 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k)
     return (uint64_t)hi << 32 | lo;
 }
 
+// The sigmoid of x times e^-shift, shift 0 or from x up to 0: by the exponential of -|x|, so that
+// no divisor passes 2 and scores keep their digits as far down as FP32 goes, and with a
+// shift beyond that.  1 - sigmoid(x) is sigmoid(-x).  (FAST: the division that is off by 2 units.)
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float x, float shift = 0.0f)
+{
+    const float a = x < 0.0f ? expf(x - shift) : 1.0f, b = 1.0f + expf(-fabsf(x));
+    return FAST ? __fdividef(a, b) : a / b;
+}
+
 // The largest over the warp (of no NaN).
 __device__ __forceinline__ float warp_max(float m)
 {
@@ -593,7 +603,7 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
     if (!sure) mine = choose_exactly<V>(p, row, reinterpret_cast<double *>(scratch + SCRATCH));
 
     // Weights: scores of the chosen, from their logits.  (The fast division is off by 2
-    // units; its divisors are far from where it ends.)
+    // units; its divisors are far from 2^126, where it ends.)
     const bool on = mine >= 0;
     const float x = on ? load_any(p.logits, row + mine, p.type) : minus_inf();
     float s;
@@ -604,18 +614,15 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
             for (int i = 0; i < V; ++i) z += expf(l[i] - m);
             s = __fdividef(expf(x - m), warp_sum(z));
         } else {
-            s = __fdividef(1.0f, 1.0f + expf(-x));
+            s = sigmoid<true>(x);
         }
         weight = on ? p.scale * s : 0.0f;
     } else {
         // What the scores have in common cancels: the chosen experts' own
-        // softmax; of sigmoids too where all are so small that 1 + e^x is 1,
-        // and their sum may be 0 in FP32.
+        // softmax; of sigmoids too the exponential of the largest below 0, where their
+        // sum might be 0 in FP32.
         const float top = warp_max(x);
-        if (softmax || top < -40.0f)
-            s = on ? expf(x - top) : 0.0f;
-        else
-            s = on ? __fdividef(1.0f, 1.0f + expf(-x)) : 0.0f;
+        s = !on ? 0.0f : softmax ? expf(x - top) : sigmoid<true>(x, fminf(top, 0.0f));
         const float sum = warp_sum(s);
         weight = on ? p.scale * __fdividef(s, sum) : 0.0f;
     }
@@ -1123,12 +1130,12 @@ __global__ void __launch_bounds__(TEAM_THREADS, 1) route_team_kernel(const __gri
         const float x = on ? load_any(p.logits, row + mine, p.type) : minus_inf();
         float weight;
         if (!p.normalise) {
-            const float s = softmax ? __fdividef(expf(x - m), z) : __fdividef(1.0f, 1.0f + expf(-x));
+            const float s = softmax ? __fdividef(expf(x - m), z) : sigmoid<true>(x);
             weight = on ? p.scale * s : 0.0f;
         } else {
             const float top = team_max(x);
             float s = 0.0f;
-            if (on) s = softmax || top < -40.0f ? expf(x - top) : __fdividef(1.0f, 1.0f + expf(-x));
+            if (on) s = softmax ? expf(x - top) : sigmoid<true>(x, fminf(top, 0.0f));
             const float sum = team_sum(s);
             weight = on ? p.scale * __fdividef(s, sum) : 0.0f;
         }
@@ -1262,15 +1269,14 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradArgs p, 
     if (p.normalise) {
         const float top = warp_max(x);
         float s = 0.0f;
-        if (on) s = softmax || top < -40.0f ? expf(x - top) : 1.0f / (1.0f + expf(-x));
+        if (on) s = softmax ? expf(x - top) : sigmoid<false>(x, fminf(top, 0.0f));
         const float all = warp_sum(s);
         const float share = on ? s / all : 0.0f;
         const float mean = warp_sum(share * d);
         g = on ? share * (d - mean) : 0.0f;
-        if (!softmax && on) g *= 1.0f / (1.0f + expf(x));
+        if (!softmax && on) g *= sigmoid<false>(-x);
     } else if (!softmax) {
-        const float s = 1.0f / (1.0f + expf(-x));
-        g = on ? d * s * (1.0f / (1.0f + expf(x))) : 0.0f;
+        g = on ? d * sigmoid<false>(x) * sigmoid<false>(-x) : 0.0f;
     }
     if (full) {
         m = minus_inf();

@@ -5,6 +5,7 @@ import torch
 
 import routing_plain as plain
 import swiglu_mlp_gb300 as swg
+from experts_plain import f64
 from test_routing_gpu import INF
 
 pytestmark = pytest.mark.gpu
@@ -41,3 +42,48 @@ def test_every_way_has_the_same_order(E, apart):
     assert bool((all_of_them[:, 0] == E - 2).all())
     assert bool((few == 3).any(1).all()) and bool((few == 5).any(1).all())
     assert torch.equal(few, all_of_them[:, 1:])
+
+
+SMALL = [-39.0, -86.0, -87.3, -87.4, -88.0, -88.7, -88.8, -90.0, -95.0, -100.0, -102.0, -103.0]
+
+
+@pytest.mark.parametrize("E", [16, 15])                  # four tokens of a warp, and one
+@pytest.mark.parametrize("normalise", [False, True])
+def test_weights_of_small_sigmoids(E, normalise):
+    """Sigmoids below FP32's smallest normal number, and beside others from which they are far."""
+    l = torch.full((3, E), -INF)
+    l[:, :12] = torch.tensor(SMALL)
+    l[1, 0] = -INF
+    l[2, 0] = 3.0
+    scale = 2.0 ** 20
+    weights = torch.empty((3, 8), device="cuda")
+    for first in (0, 4):
+        x = l.clone()
+        x[:, 1:1 + first] = -INF
+        experts = torch.empty((3, 8), dtype=torch.int32, device="cuda")
+        swg.expert_route_into(experts, weights, x.cuda(), swg.SIGMOID, normalise=normalise, scale=scale)
+        assert swg.get_device_error() == 0
+        want, w = plain.route(f64(x), None, 8, "sigmoid", normalise=normalise, scale=scale)
+        assert np.array_equal(experts.cpu().numpy(), want)
+        if normalise:
+            tol = plain.route_bound(f64(x), w, 8) - 1e-37 + scale * 2.0 ** -149     # (a share may be subnormal)
+        else:
+            # exponential and division 2 units each, half a one of 1 + e^x; the product is exact
+            tol = 5 * 2.0 ** -23 * w + scale * 5 * 2.0 ** -149
+        got = f64(weights)
+        assert (np.abs(got - w) <= tol).all(), f"{got[np.abs(got - w) > tol]} {w[np.abs(got - w) > tol]}"
+
+
+def test_gradients_of_small_sigmoids():
+    x = torch.tensor([[*SMALL, *(-v for v in SMALL)]]).reshape(6, 4)
+    experts = torch.arange(4, dtype=torch.int32).repeat(6, 1).cuda()
+    dw = torch.linspace(-2, 3, 24).reshape(6, 4)
+    d = torch.empty((6, 4), device="cuda")
+    scale = 2.0 ** 20
+    swg.expert_route_grad_into(d, dw.cuda(), x.cuda(), experts, swg.SIGMOID, normalise=False, scale=scale)
+    assert swg.get_device_error() == 0
+    e = np.exp(-np.abs(f64(x)))
+    want = scale * f64(dw) * e / (1 + e) ** 2
+    # both scores: exponential 2 units, two halves; three products, half a one each
+    tol = 7.5 * 2.0 ** -23 * np.abs(want) + scale * np.abs(f64(dw)) * 5 * 2.0 ** -149
+    assert (np.abs(f64(d) - want) <= tol).all()
