@@ -389,12 +389,19 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
     bool sure = true;
     float tol = 0.0f;
     if (by_score) {
-        // Scores by the fast exponential, which is off by at most 2 + 1.2 |x| units,
-        // and division (2 units).  Softmax: x = l - m, and |x| e^x is at most 0.4: 3 units
-        // of the largest score for the exponential, as much for the sum's terms, 8 for
-        // its 15 additions in a tree, 1 more: two choices, 2^-18 of it and a half.
-        // Sigmoid: s (1 - s) (2 + 1.2 |x|) + 2 s, of the largest score 6 units, where all
-        // logits are negative 1.2 |m| more.
+        // Scores by the fast exponential, which is off by at most 2 + 1.2 |x| units (2^-23 of
+        // its value), and division (2 units).  tol bounds by how much the difference of two
+        // choices is off.
+        // Softmax: x = l - m, whose rounding is half a unit of e^x for each of |x|.  What the
+        // sum and its inverse are off by is common to all scores and takes that part of a
+        // difference, which is at most the largest score.  The terms' errors, 2 + 1.7 |x|
+        // weighted by e^x, are at most 9.3 units of the sum of 1024 (one term 0, the others
+        // all near -5.2), its 15 additions in a tree 7.5, the inverse 2.  Each score's own
+        // e^x, (2 + 1.7 |x|) e^x <= 2 units of the largest, and its product, a half: of two
+        // choices 5.  In all 24 units of the largest score; twice that is taken.
+        // Sigmoid: s (1 - s) (2 + 1.2 |x|) + 2.5 s is at most 3.6 units of the largest score
+        // where that is a half or more, and 4.5 + 1.2 |m| where all logits are negative: twice
+        // that, of two choices, is at most the 12 + 2.4 |m| that are taken.
         m = warp_max(m == m ? m : minus_inf());
         float s[V];
         float largest;
@@ -415,7 +422,8 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
             largest = m < -80.0f ? 0.0f : __fdividef(1.0f, 1.0f + __expf(-m));
             tol = largest * (12.0f + 2.4f * fmaxf(-m, 0.0f)) * 0x1p-23f;
         }
-        // (2^-120: scores that FP32 has no digits left for)
+        // Choices are rounded to FP32 (2^-23 of both; of the values of two groups, which are
+        // compared with 2 tol, 2^-21), and 2^-120 stands for scores that FP32 has no digits for.
         tol += 0x1p-22f * (largest + of.most) + 0x1p-120f;
         sure = tol < 1.0f;                           // (not with a bias of +inf, or of NaN)
 #pragma unroll

@@ -6,7 +6,7 @@ import torch
 import routing_plain as plain
 import swiglu_mlp_gb300 as swg
 from experts_plain import f64
-from test_routing_gpu import INF
+from test_routing_gpu import INF, run_route
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,26 @@ def test_gradients_of_small_sigmoids():
     # both scores: exponential 2 units, two halves; three products, half a one each
     tol = 7.5 * 2.0 ** -23 * np.abs(want) + scale * np.abs(f64(dw)) * 5 * 2.0 ** -149
     assert (np.abs(f64(d) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("E", [256, 1024])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_one_score_above_many_equal_ones(E, groups):
+    """All logits but one are the same, so that what their exponentials are off by does not
+    cancel in their sum, and biases bring the choices of six within a unit of FP32 of the one's:
+    the error of the sum moves a difference of choices by more than is between them."""
+    met = 0
+    for low in np.linspace(-7.0, -3.0, 25).astype(np.float32):
+        l = torch.full((1, E), float(low))
+        l[0, E // 2] = 0.0
+        s = plain.scores(f64(l), "softmax")[0]
+        for j in (-2, -1, 0, 1, 2):
+            bias = torch.full((E,), -1.0)
+            bias[1:7] = 0.25 + torch.arange(6) * 2.0 ** -25
+            bias[E // 2] = float(np.float32(0.25 + 2.0 ** -24 + s[1] - s[E // 2])) + j * 2.0 ** -26
+            c = np.sort(s + f64(bias))[-7:]
+            if np.diff(c).min() < 1e-14:
+                continue
+            met += 1
+            run_route(l, 4, bias=bias, groups=groups, top_groups=max(groups // 2, 1), group_sum=2)
+    assert met > 100
