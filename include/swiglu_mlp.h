@@ -549,7 +549,8 @@ SWG_API int expert_route_grad(int score, int64_t T, int64_t E, int64_t top, cons
 /*
  * expert_dispatch — rows[position[t][j],:] = X[t,:] for every slot with a row: X
  * T x D, rows R x D.  Other rows keep their values.  Positions beyond [0, R) have no
- * row; those other than -1 are reported (device error word).  The positions have to
+ * row; those other than -1 are reported (device error word), also where there are no
+ * rows or no columns to move.  The positions have to
  * differ (as expert_sort's do): a row of several slots gets pieces of any of theirs.
  * Its gradient is expert_combine without weights.
  */

@@ -224,9 +224,12 @@ int expert_dispatch(int64_t T, int64_t R, int64_t D, int64_t top, const void *X,
     int bytes;
     swg::RowsArgs p{};
     if (int rc = rows_args(T, R, D, top, type, position, nullptr, bytes, p)) return rc;
-    if (T == 0 || R == 0 || D == 0) return SWG_OK;
-    if (int rc = check_rows(X, ldx, D, bytes)) return rc;
-    if (int rc = check_rows(rows, ldr, D, bytes)) return rc;
+    if (T == 0) return SWG_OK;
+    if (R == 0) p.D = 0;                             // only positions to look at
+    if (p.D > 0) {
+        if (int rc = check_rows(X, ldx, D, bytes)) return rc;
+        if (int rc = check_rows(rows, ldr, D, bytes)) return rc;
+    }
     p.X = X;
     p.ldx = ldx;
     p.rows = rows;
@@ -244,10 +247,12 @@ int expert_combine(int64_t T, int64_t R, int64_t D, int64_t top, const void *row
     swg::RowsArgs p{};
     if (!type_bytes(otype, obytes) || (otype != type && type != SWG_TYPE_F32)) return SWG_ERR_UNSUPPORTED;
     if (int rc = rows_args(T, R, D, top, type, position, weights, bytes, p)) return rc;
-    if (T == 0 || D == 0) return SWG_OK;
-    if (R > 0)
-        if (int rc = check_rows(rows, ldr, D, bytes)) return rc;
-    if (int rc = check_rows(out, ldo, D, obytes)) return rc;
+    if (T == 0) return SWG_OK;
+    if (D > 0) {
+        if (R > 0)
+            if (int rc = check_rows(rows, ldr, D, bytes)) return rc;
+        if (int rc = check_rows(out, ldo, D, obytes)) return rc;
+    }
     p.rows = const_cast<void *>(rows);
     p.ldr = ldr;
     p.out = out;
@@ -268,7 +273,6 @@ int expert_combine_grad(int64_t T, int64_t R, int64_t D, int64_t top, const void
     if (int rc = rows_args(T, R, D, top, type, position, weights, bytes, p)) return rc;
     if (T == 0) return SWG_OK;
     if (!aligned4({d_weights})) return SWG_ERR_MISALIGNED;
-    if (D == 0 && d_weights == nullptr) return SWG_OK;
     if (D > 0) {
         if (int rc = check_rows(d_out, ldd, D, bytes)) return rc;
         if (R > 0 && d_weights != nullptr)
