@@ -2,16 +2,18 @@
 // token's rows, and that sum's gradients.
 //
 // All of them stream rows in 16-byte pieces and are bound by memory.  They go by
-// tokens, not by rows: what belongs to the token (its row, its sum, its gradient)
-// is read or written once and stays in registers while its slots pass by.  Sums
-// are in FP32, in the order of the slots.
+// tokens, not by rows: what belongs to the token (its row, its sum) is read or written
+// once and stays in registers while its slots pass by.  The sum's gradient has a product
+// for each slot as well, and reads its row again for every four slots, out of the caches.
+// Sums are in FP32, in the order of the slots.
 //
 // 8192 tokens of 4096 bfloat16 columns to two experts each: dispatch 31.3 us, 6.4 TB/s, 0.95
-// of a copy.  5003 tokens of 2051 binary16 columns, four experts each: combine 24.5 us and
-// its gradient 31.9, 4.2 and 5.8 TB/s (rows of 4112 bytes begin anywhere in a line, and the
-// reads that a sum waits for are all that its warp has in flight; spans handed out to resident
-// warps, with the next positions asked for ahead, were no faster).  32 tokens of 4096, eight
-// experts each: 2.7 us, one launch.
+// of a copy; the sum 41 us, 4.9 TB/s, its gradient 59, 5.7.  To eight each: 94, 91 and 171 us,
+// 6.4, 6.6 and 6.7 TB/s.  5003 tokens of 2051 binary16 columns, four experts each: the sum
+// 23.0 us and its gradient 31.8, 4.5 and 5.8 TB/s (rows of 4112 bytes begin anywhere in a line).
+// The reads that a sum waits for are all that its warp has in flight, which shows with few
+// slots; spans handed out to resident warps, with the next positions asked for ahead, were no
+// faster.  32 tokens of 4096, eight experts each: 2.7 us, one launch.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -261,8 +263,8 @@ __global__ void __launch_bounds__(32 * WARPS, 4) combine_kernel(const RowsArgs p
     }
 }
 
-// A CTA per token, its warps side by side along the row, U pieces per lane and round.
-template <int TYPE, int U>
+// A CTA per token, its warps side by side along the row, a piece per lane and round.
+template <int TYPE>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const RowsArgs p, int *err)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -276,47 +278,34 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RowsArgs p, int
     float mine = 0.0f;                               // lane j: slot j's product
     for (int j = 0; j < p.top; j += BATCH) {
         float dot[BATCH] = {};
-        for (long long col = (warp * 32 + lane) * PIECE<TYPE>; __any_sync(ALL, col < p.D); col += U * step) {
-            uint4 d[U], x[BATCH][U];
-            int cnt[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                cnt[u] = columns<TYPE>(p.D, col + u * step);
-                d[u] = load_piece<TYPE>(p.X, t * p.ldx + col + u * step, cnt[u], t + 1 < p.T);
-            }
+        for (long long col = (warp * 32 + lane) * PIECE<TYPE>; __any_sync(ALL, col < p.D); col += step) {
+            const int cnt = columns<TYPE>(p.D, col);
+            uint4 d = load_piece<TYPE>(p.X, t * p.ldx + col, cnt, t + 1 < p.T), x[BATCH];
 #pragma unroll
             for (int b = 0; b < BATCH; ++b) {
                 const int r = __shfl_sync(ALL, at, (j + b) & 31);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (products && j + b < p.top && r >= 0)
-                        x[b][u] = load_piece<TYPE>(p.rows, r * p.ldr + col + u * step, cnt[u], r + 1 < p.R);
+                if (products && j + b < p.top && r >= 0) x[b] = load_piece<TYPE>(p.rows, r * p.ldr + col, cnt, r + 1 < p.R);
             }
+            if (__any_sync(ALL, cnt % PIECE<TYPE> != 0)) {           // (the end of a row)
+                clear_behind<TYPE>(d, cnt);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (__any_sync(ALL, cnt[u] % PIECE<TYPE> != 0)) {    // (the end of a row)
-                    clear_behind<TYPE>(d[u], cnt[u]);
-#pragma unroll
-                    for (int b = 0; b < BATCH; ++b) clear_behind<TYPE>(x[b][u], cnt[u]);
-                }
+                for (int b = 0; b < BATCH; ++b) clear_behind<TYPE>(x[b], cnt);
+            }
 #pragma unroll
             for (int b = 0; b < BATCH; ++b) {
                 const int r = __shfl_sync(ALL, at, (j + b) & 31);
                 const float f = __shfl_sync(ALL, w, (j + b) & 31);
                 if (j + b >= p.top || r < 0) continue;
+                float dv[PIECE<TYPE>], v[PIECE<TYPE>];
+                to_floats<TYPE>(d, dv);
+                if (products) {
+                    to_floats<TYPE>(x[b], v);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float dv[PIECE<TYPE>], v[PIECE<TYPE>];
-                    to_floats<TYPE>(d[u], dv);
-                    if (products) {
-                        to_floats<TYPE>(x[b][u], v);
-#pragma unroll
-                        for (int i = 0; i < PIECE<TYPE>; ++i) dot[b] = fmaf(dv[i], v[i], dot[b]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < PIECE<TYPE>; ++i) v[i] = f * dv[i];
-                    store_piece<TYPE>(p.out, r * p.ldo + col + u * step, cnt[u], from_floats<TYPE>(v));
+                    for (int i = 0; i < PIECE<TYPE>; ++i) dot[b] = fmaf(dv[i], v[i], dot[b]);
                 }
+#pragma unroll
+                for (int i = 0; i < PIECE<TYPE>; ++i) v[i] = f * dv[i];
+                store_piece<TYPE>(p.out, r * p.ldo + col, cnt, from_floats<TYPE>(v));
             }
         }
         if (!products) continue;
@@ -404,7 +393,7 @@ cudaError_t combine_grad(const RowsArgs &p, int *err, cudaStream_t s)
             warps = w;
         }
     }
-    return go(combine_grad_kernel<TYPE, 1>, p.T, 32 * warps, s, p, err);
+    return go(combine_grad_kernel<TYPE>, p.T, 32 * warps, s, p, err);
 }
 
 }  // namespace
