@@ -629,7 +629,8 @@ SWG_API int gemm_w4(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, con
 /*
  * swiglu_w4 — Y[i,:] = SiLU(alpha A[i,:] W1_g^T) (.) (alpha A[i,:] W2_g^T), M x N of
  * `type`.  W has 2N rows for each group: row 2n = W1's n'th (Gate), row 2n + 1 = W2's
- * (Up); lds >= 2N.
+ * (Up); lds >= 2N.  Y is rounded to 16 bits, as gemm_w4 takes its A: a layer of both rounds
+ * its hidden values once, each by up to 2^-8 (bfloat16) or 2^-11 (binary16).
  */
 SWG_API int swiglu_w4(int64_t G, int64_t M, int64_t N, int64_t K, float alpha, const void *A, int64_t lda,
                       const void *Q, const void *S, const void *Z, int64_t lds, int64_t group,

@@ -13,10 +13,12 @@
 // the rounding of the exponential.
 //
 // route_team_kernel, up to 256 experts and eight of them: the same by eight lanes for
-// each token.  Instructions bound it, 478 a token against 1412 (16384 tokens, eight of
-// 256 experts by four of eight groups, with the plan: 30 us, 10 of them sorting, against
-// 44; 8192 tokens, two of 16 experts, with the gradient: 12.0 against 14.9; 64 tokens of
-// 64 experts, one CTA: 4.7 against 5.3).  The logits themselves take 2.5 us.
+// each token, 480 instructions a token against 1412 (16384 tokens, eight of
+// 256 experts by four of eight groups, with the plan: 29.6 us, 10 of them sorting, against
+// 44; 8192 tokens, two of 16 experts, with the gradient: 11.8 against 14.9; 4 tokens, six of
+// 64 experts, one CTA: 4.8 against 5.3).  The logits themselves take 2.5 us.  Instructions
+// and their latencies bound it: the 16 warps that their registers leave room for fill 42% of
+// the issue slots, and a CTA's 108 tokens are one full round of 64 and one of 44.
 //
 // Sorting is counting: every chunk of tokens counts its experts in shared memory,
 // and the second kernel adds up the chunks before its own and ranks its slots

@@ -3,17 +3,21 @@
 // expert.
 //
 // For few rows the weights' bytes are what the operator cannot do without; the
-// kernel streams them once, and what bounds it is the decoding: seven shifts and masks
+// kernel streams them once.  Decoding is most of its instructions: seven shifts and masks
 // for eight codes, on a pipe that takes one every two cycles (a row through 14336 rows of
 // 4096: 3.7 us of it, 4.5 of memory, 8.9 in all; 28672 x 4096: 16.0, 3.9 TB/s; 64 rows of 64
-// experts, 2432 x 896: 15.8, of which 6.7 memory).  The rows of
+// experts, 2432 x 896: 15.8, of which 6.7 memory).  No pipe is full: a warp waits for its
+// step, reads it, decodes and multiplies in turn, and the 12 to 16 warps that the shared
+// memory of an SM has room for fill 47 and 56% of its issue slots and 42 and 45% of that pipe
+// (the first and the last of these).  The rows of
 // W are the 16 rows of an mma.sync m16n8k16 (FP32 accumulators), up to eight rows
 // of A its columns: at one row of A 7/8 of the instruction's work is for nothing,
 // but it is free, and the rows of W arrive in fragments as they lie in memory:
 // codes become 16-bit numbers in registers, by one mask per two codes and one
 // subtraction of the zero point, exactly.  (The tcgen05 instructions take their
 // operands from shared or tensor memory, 128 rows of them: the decoded weights would
-// pass through it once more, four times their size.)  Sums of a group of columns
+// pass through it once more, four times their size.  Decoding into tensor memory, which
+// takes registers directly, has not been tried.)  Sums of a group of columns
 // are scaled in FP32 as a whole, so that no product with a scale is ever rounded to
 // 16 bits.
 //
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(32 * WARPS, 4)
 // fill an SM, and the CTAs of a cluster that have a tile's ranges add their sums
 // through shared memory, in order.  (One CTA of 256 rows for each SM: 41 us, since only
 // 15 clusters of eight of that size are resident, and 35.9 with clusters of four; this
-// 19.0; chunks of eight rows of the other kernel 29.9.)
+// 19.0; chunks of eight rows of the other kernel 29.3.)
 constexpr int MANY_ROWS = WARPS * ROWS, MANY_BOX = 64, MANY_BOXES = MANY_ROWS / MANY_BOX;
 constexpr int MANY_CODES = MANY_BOX * STEP / 2;
 constexpr int MANY_THREADS = 32 * (WARPS + 1);
@@ -528,29 +532,29 @@ struct Shape {
 };
 
 // (Times in us, bfloat16, groups of 128 with zero points, each of the same build on both
-// sides; of groups and teams as they were when one lane asked for a step's codes and four for A,
-// which cost a tenth.)
+// sides.)
 Shape shape_of(const W4Args &p, int sms)
 {
     const Groups &g = p.groups;
     const int steps = (p.w.K + STEP - 1) / STEP;
     const long long items = (p.w.N + ROWS - 1ll) / ROWS;
     // Groups: chunks of four times their mean and four rows at least, since another chunk
-    // reads and decodes the weights again (64 rows of 64 experts: 21.5 with chunks of 1, 17.9
-    // with 2, 17.4 with 4 and 8; 4 rows, 8 experts of 8192 x 2048: 10.5 with 2, 7.7 with 4; 8
-    // rows, 16 experts of 4096 x 1024: 7.4 with 2, 8.0 with 4, 9.2 with 8).  More than eight
-    // rows from a mean of 16 on, where the fuller instructions outweigh the emptier chunks (16
-    // experts of 4096 x 1024: means of 8 23.6 and 17.5, 16 26.3 and 27.0, 32 37.7 and 44.7).
+    // reads and decodes the weights again (64 rows of 64 experts of 2432 x 896, scales of 32
+    // columns: 21.9 with chunks of 1, 18.5 with 2, 18.3 with 4, 18.9 with 8; 4 rows, 8 experts of
+    // 8192 x 2048: 9.1 with 2, 6.8 with 4, 8.6 with 8; 8 rows, 16 experts of 4096 x 1024: 6.7 with
+    // 2, 7.5 with 4, 8.2 with 8).  More than eight rows from a mean of 16 on, where the fuller
+    // instructions outweigh the emptier chunks (16 experts of 4096 x 1024: means of 8 23.7 and
+    // 17.4, 12 24.8 and 22.3, 16 26.3 and 27.0, 32 37.8 and 44.8).
     if (g.offsets != nullptr && g.M >= 16ll * g.G) return {32, true};
     const int want = g.offsets == nullptr ? g.M : (int)std::min<long long>(g.M, std::max(4ll, (4ll * g.M + g.G - 1) / g.G));
-    // More than eight rows (4096 x 14336, 32 rows: 19.0 and 29.2; 14336 x 4096, 9 rows: 14.9
-    // and 18.4), unless there is too little to do for a cluster's barriers (2048 x 8192, 16
-    // rows: 9.0 and 7.4; 8192 x 1024, 16 rows: 5.2 both).
+    // More than eight rows (4096 x 14336, 32 rows: 19.0 and 29.3; 14336 x 4096, 9 rows: 15.0
+    // and 15.9), unless there is too little to do for a cluster's barriers (2048 x 8192, 16
+    // rows: 9.0 and 7.4; 8192 x 1024, 16 rows: 6.3 and 5.1).
     if (g.offsets == nullptr && want > TOKENS && (want + TOKENS - 1) / TOKENS * items * steps > 28ll * sms)
         return {want <= 16 ? 16 : 32, true};
     // Up to eight, where rows are long and few: a cluster has up to 32 warps for a tile, a
-    // team four (one row, 1024 x 8192: 5.7 and 7.4; 2048 x 8192: 7.4 both; but 4096 x 14336
-    // 14.2 and 12.2).
+    // team four (one row, 1024 x 8192: 5.7 and 7.5; 2048 x 8192: 7.4 and 7.5; but 4096 x 14336
+    // 14.1 and 12.3).
     if (steps > 24 && (g.offsets == nullptr ? 1 : std::min(g.G, g.M)) * items * 2 < sms) return {TOKENS, true};
     return {want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : TOKENS, false};
 }
@@ -559,7 +563,7 @@ template <bool BF16, int PER, bool ZERO>
 cudaError_t launch(const W4Args &p, const W4Maps &maps, int tokens, int sms, int *err, cudaStream_t s)
 {
     // As small teams as leave 16 warps for each SM, as many as are resident (8 experts of
-    // 4096 x 4096, 8 rows: 16.0, and 20.0 with 12 warps).
+    // 4096 x 4096, 8 rows: 13.9, and 17.7 with 12 warps).
     const int steps = (p.w.K + STEP - 1) / STEP;
     const long long items = (p.groups.offsets ? std::min(p.groups.G, p.groups.M) : chunks_of(p.groups, tokens)) * ((p.w.N + ROWS - 1ll) / ROWS);
     int team = 1;
@@ -577,8 +581,8 @@ cudaError_t launch(const W4Args &p, const W4Maps &maps, int tokens, int sms, int
     const long long ctas = chunks_of(p.groups, tokens) * tiles;
     size_t room = std::max((size_t)shared_bytes(PER, ZERO, tokens), sums);
     // CTAs that are resident at once are spread evenly: no more of them fit an SM than its
-    // share (one row, 14336 x 4096: 448 CTAs, 10.1 and 11.9 when some SMs have four and some
-    // two; 4096 x 4096: 5.6 and 6.4).  Of groups it is not known how many have work.
+    // share (one row, 14336 x 4096: 448 CTAs, 9.5 and 11.8 when some SMs have four and some
+    // two; 4096 x 4096: 4.8 and 5.4).  Of groups it is not known how many have work.
     const long long share = (ctas + sms - 1) / sms;
     if (p.groups.offsets == nullptr && share < 8) room = std::max(room, std::min<size_t>(SM_SHARED / (share + 1) - 1024 + 128, CTA_SHARED));
     cudaLaunchConfig_t cfg = {};
@@ -598,11 +602,11 @@ template <bool BF16, int PER, bool ZERO, int NT>
 cudaError_t launch_many(const W4Args &p, const W4Maps &maps, int sms, int *err, cudaStream_t s)
 {
     // As many ranges of the steps as the SMs have places for CTAs, two each (in us, with 1, 2,
-    // 4 and 8: 32 rows, 14336 x 4096 33.4, 23.2, 26.8, 33.1; 4096 x 14336 65, 36.5, 28.5, 19.7).
+    // 4 and 8: 32 rows, 14336 x 4096 32.3, 22.6, 26.2, 32.6; 4096 x 14336 61.8, 34.7, 27.6, 19.0).
     const int steps = (p.w.K + STEP - 1) / STEP, tiles = (p.w.N + MANY_ROWS - 1) / MANY_ROWS;
     const long long chunks = chunks_of(p.groups, 8 * NT);
     // (of groups half a chunk more for each than their rows fill: 64 rows of 4 experts of 4096 x
-    // 4096 21.4 in two ranges, 30.4 in one)
+    // 4096 21.5 in two ranges, 30.5 in one, 25.2 in four)
     const long long units = (p.groups.offsets ? p.groups.M / (8 * NT) + (std::min(p.groups.G, p.groups.M) + 1) / 2 : chunks) * tiles;
     int ranges = 1;
     while (ranges < MOST_RANGES && 2 * ranges <= steps && ranges * units <= sms) ranges *= 2;

@@ -39,8 +39,9 @@ struct RouteArgs {
 // a workspace of chunks x E ints.
 int plan_chunks(int T, int top, bool route, int sms);
 cudaError_t launch_route(const RouteArgs &p, int chunks, int32_t *counts, cudaStream_t s);
-// The second kernel of more than one chunk, after launch_route, or the whole of
-// expert_sort (counted: the workspace holds the chunks' counts already).
+// The plan of T x top experts.  More than one chunk: `counts` holds how many slots of each
+// chunk go to each expert, from launch_route or launch_count with as many chunks.  One chunk:
+// counted here, `counts` is not used.  err: where wrong experts are reported, or nullptr.
 cudaError_t launch_sort(int T, int E, int top, const int32_t *experts, const Plan &plan, int chunks,
                         int32_t *counts, int *err, cudaStream_t s);
 cudaError_t launch_count(int T, int E, int top, const int32_t *experts, int chunks, int32_t *counts,
