@@ -571,6 +571,7 @@ SWG_API int expert_combine(int64_t T, int64_t R, int64_t D, int64_t top, const v
  * expert_combine_grad — the gradients of that:
  *   d_rows[position[t][j],:] = weights[t][j] * d_out[t,:]      (other rows keep theirs)
  *   d_weights[t][j] = <rows[position[t][j],:], d_out[t,:]>     (0 without a row)
+ * d_out and d_rows are of the rows' type: FP32 for FP32 rows, whatever type their sum had.
  * weights NULL: ones.  d_weights NULL: not computed, and rows is not read.  The
  * positions have to differ (as expert_sort's do): a row of several slots gets pieces of
  * any of their gradients.

@@ -949,8 +949,8 @@ def expert_combine_into(out, rows, position, weights=None, beta=0.0, stream=None
 
 def expert_combine_grad_into(d_rows, d_weights, d_out, rows, position, weights=None, stream=None):
     """d_rows[position[t, j]] <- weights[t, j] * d_out[t] and d_weights[t, j] <-
-    <rows[position[t, j]], d_out[t]> (d_weights None: neither computed, and rows
-    may be None)."""
+    <rows[position[t, j]], d_out[t]> (d_weights None: not computed, and rows may be
+    None).  All of the rows' type: of float32 rows summed into 16 bits d_out is float32."""
     w = "expert_combine_grad_into"
     torch = _torch or _fast()
     lib = _bound
