@@ -629,8 +629,8 @@ __device__ __forceinline__ int choose(const RouteArgs &p, long long row, const f
         weight = on ? p.scale * s : 0.0f;
     } else {
         // What the scores have in common cancels: the chosen experts' own
-        // softmax; of sigmoids too the exponential of the largest below 0, where their
-        // sum might be 0 in FP32.
+        // softmax; of sigmoids the exponential of the largest logit where that is below 0, or
+        // their sum might be 0 in FP32.
         const float top = warp_max(x);
         s = !on ? 0.0f : softmax ? expf(x - top) : sigmoid<true>(x, fminf(top, 0.0f));
         const float sum = warp_sum(s);
